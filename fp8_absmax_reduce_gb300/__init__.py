@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import math
 import os
 
 import torch
@@ -21,7 +22,7 @@ from . import build as _build_mod
 E4M3, E5M2 = 0, 1
 BF16, F32 = 0, 1
 NN, NT, TN = 0, 1, 2
-STATUS_NONFINITE, STATUS_TIMEOUT = 0x1, 0x2
+STATUS_NONFINITE, STATUS_TIMEOUT, STATUS_BAD_TARGET = 0x1, 0x2, 0x4
 
 _LIB_PATH = _build_mod.LIB
 
@@ -77,6 +78,19 @@ def _load() -> ctypes.CDLL:
     L.fp8q_selftest_bounded_wait.argtypes = [i64, vp]
     L.fp8q_selftest_gemm_wait_limit.argtypes = [i32, i64, i64, i64, vp, i32, i64, vp, i32, i64, vp, vp, i32, vp, vp,
                                                 vp, i32, i64, i64, vp]
+    rope_p = ctypes.POINTER(FP8QRope)
+    L.rope_fwd.argtypes = [vp, i32, i64, i32, i32, rope_p, vp, vp, vp]
+    L.rope_bwd.argtypes = L.rope_fwd.argtypes
+    L.layernorm_fwd.argtypes = [vp, i32, vp, vp, i64, i64, f32, vp, vp, vp, vp]
+    L.layernorm_bwd_workspace_size.restype = sz
+    L.layernorm_bwd_workspace_size.argtypes = [i64, i64]
+    L.layernorm_bwd.argtypes = [vp, vp, i32, vp, vp, vp, vp, i64, i64, vp, vp, vp, vp, sz, vp]
+    for name in ("linear_cross_entropy_fwd", "linear_cross_entropy_bwd"):
+        size = getattr(L, name + "_workspace_size")
+        size.restype = sz
+        size.argtypes = [i64, i64, i64]
+    L.linear_cross_entropy_fwd.argtypes = [vp, vp, vp, i64, i64, i64, i64, vp, vp, vp, sz, vp]
+    L.linear_cross_entropy_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, i32, vp, sz, vp]
     L.fp8q_trace_start.argtypes = [i32]
     L.fp8q_trace_read.argtypes = [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int), i32]
     L.fp8q_kernel_name.restype = ctypes.c_char_p
@@ -119,6 +133,12 @@ class FP8QBlockHostIO(ctypes.Structure):
     """Mirror of ``fp8q_block_host_io`` in include/fp8q.h."""
     _fields_ = [(n, ctypes.c_void_p) for n in ("x", "g1", "W_qkv", "W_o", "att", "g", "W_gu", "W_d", "dY", "dQKV",
                                                "y", "dX", "d_att", "dW_qkv", "dW_o", "dg1", "dW_gu", "dW_d", "dg")]
+
+
+class FP8QRope(ctypes.Structure):
+    """Mirror of ``fp8q_rope`` in include/fp8q.h."""
+    _fields_ = [("head_dim", ctypes.c_int), ("rot_dim", ctypes.c_int), ("n_axes", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("inv_freq", ctypes.c_double * 128), ("axis", ctypes.c_uint8 * 128)]
 
 
 class FP8QBlock(ctypes.Structure):
@@ -347,6 +367,197 @@ def attention_bwd(qkv: torch.Tensor, att: torch.Tensor, lse: torch.Tensor, d_att
 
 
 # ---------------------------------------------------------------------------
+def _need(name: str, t, shape, *dtypes):
+    """A tensor argument of a given shape (None: any size in that place) and one of the given types,
+    dense, on the current CUDA device (the library launches there)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
+    if t.dim() != len(shape) or any(want is not None and have != want for have, want in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple('any' if s is None else s for s in shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _out(name: str, t, shape, dtype, like):
+    return torch.empty(shape, dtype=dtype, device=like.device) if t is None else _need(name, t, shape, dtype)
+
+
+@dataclasses.dataclass(frozen=True)
+class Rope:
+    """The plan of rotary positions (see fp8q_rope in include/fp8q.h): each pair's frequency
+    (radians per position) and axis.  Make one with :meth:`make` and keep it."""
+    head_dim: int
+    rot_dim: int
+    n_axes: int
+    interleaved: bool
+    inv_freq: tuple
+    axis: tuple
+    _struct: FP8QRope = dataclasses.field(repr=False, compare=False)
+
+    @staticmethod
+    def make(head_dim: int = 128, rot_dim: int | None = None, base: float = 10000.0, sections=None,
+             interleaved: bool = False, inv_freq=None, axis=None) -> "Rope":
+        """rot_dim: the rotated columns of a head (default: all).  inv_freq: rot_dim / 2 frequencies
+        (default base^(-2i / rot_dim)).  sections: pairs per axis, one after the other (default: one
+        axis); axis: the axis of each pair instead, in any order."""
+        rot_dim = head_dim if rot_dim is None else rot_dim
+        if not (8 <= head_dim <= 256) or head_dim % 8:
+            raise ValueError(f"head_dim {head_dim}: a multiple of 8 from 8 to 256")
+        if not (2 <= rot_dim <= head_dim) or rot_dim % 2:
+            raise ValueError(f"rot_dim {rot_dim}: even, from 2 to head_dim")
+        half = rot_dim // 2
+        if sections is not None and axis is not None:
+            raise ValueError("give sections or axis, not both")
+        if axis is None:
+            sections = [half] if sections is None else [int(n) for n in sections]
+            if any(n < 0 for n in sections):
+                raise ValueError("sections must not be negative")
+            axis = [a for a, n in enumerate(sections) for _ in range(n)]
+            n_axes = len(sections)
+        else:
+            axis = [int(a) for a in axis]
+            n_axes = max(axis, default=0) + 1
+        freq = [base ** (-2.0 * i / rot_dim) for i in range(half)] if inv_freq is None else [float(f) for f in inv_freq]
+        if len(axis) != half or len(freq) != half:
+            raise ValueError(f"{len(axis)} axes and {len(freq)} frequencies for {half} pairs")
+        if min(axis) < 0 or not 1 <= n_axes <= 255:
+            raise ValueError("axes from 0 to 254")
+        if not all(math.isfinite(f) for f in freq):
+            raise ValueError("frequencies must be finite")
+        s = FP8QRope(head_dim=head_dim, rot_dim=rot_dim, n_axes=n_axes, interleaved=int(bool(interleaved)))
+        s.inv_freq[:half] = freq
+        s.axis[:half] = axis
+        return Rope(head_dim, rot_dim, n_axes, bool(interleaved), tuple(freq), tuple(axis), s)
+
+
+def _rope_call(name, qkv, pos, rope, n_heads, n_kv_heads, out, stream):
+    _need("qkv", qkv, (None, (n_heads + 2 * n_kv_heads) * rope.head_dim), torch.bfloat16, torch.float32)
+    T = qkv.shape[0]
+    _need("pos", pos, (T,) if rope.n_axes == 1 and pos.dim() == 1 else (rope.n_axes, T), torch.int32)
+    out = _out("out", out, qkv.shape, qkv.dtype, qkv)
+    _check(name, getattr(lib, name)(_ptr(qkv), _dtype_code(qkv), T, n_heads, n_kv_heads, ctypes.byref(rope._struct),
+                                    _ptr(pos), _ptr(out), _stream(stream)))
+    return out
+
+
+def rope_fwd(qkv: torch.Tensor, pos: torch.Tensor, rope: Rope, n_heads: int, n_kv_heads: int, out=None, stream=None):
+    """Rotary positions of qkv [T, (n_heads + 2 n_kv_heads) head_dim] (bf16 or fp32, the layout
+    attention_fwd reads): q and k heads rotated, v heads copied.  pos: [n_axes, T] int32, or [T] with
+    one axis.  out=qkv works in place.  n_kv_heads=0 rotates every head."""
+    return _rope_call("rope_fwd", qkv, pos, rope, n_heads, n_kv_heads, out, stream)
+
+
+def rope_bwd(d_out: torch.Tensor, pos: torch.Tensor, rope: Rope, n_heads: int, n_kv_heads: int, dqkv=None, stream=None):
+    """Gradient of rope_fwd at its input, for the gradient d_out at its output (attention_bwd's dqkv):
+    the rotation by the negative angles.  dqkv=d_out works in place."""
+    return _rope_call("rope_bwd", d_out, pos, rope, n_heads, n_kv_heads, dqkv, stream)
+
+
+def layernorm_fwd(x: torch.Tensor, g: torch.Tensor, b: torch.Tensor | None = None, eps: float = 1e-5, y=None,
+                  mean=None, rstd=None, stream=None):
+    """Layer norm of x [T,d] with gain g and bias b [d] (all bf16 or all fp32).
+    Returns (y [T,d], mean [T] fp32, rstd [T] fp32)."""
+    _need("x", x, (None, None), torch.bfloat16, torch.float32)
+    T, d = x.shape
+    _need("g", g, (d,), x.dtype)
+    if b is not None:
+        _need("b", b, (d,), x.dtype)
+    y = _out("y", y, (T, d), x.dtype, x)
+    mean = _out("mean", mean, (T,), torch.float32, x)
+    rstd = _out("rstd", rstd, (T,), torch.float32, x)
+    _check("layernorm_fwd", lib.layernorm_fwd(_ptr(x), _dtype_code(x), _ptr(g), _ptr(b), T, d, eps, _ptr(y), _ptr(mean),
+                                              _ptr(rstd), _stream(stream)))
+    return y, mean, rstd
+
+
+def layernorm_bwd_workspace_size(T: int, d: int) -> int:
+    return lib.layernorm_bwd_workspace_size(T, d)
+
+
+def layernorm_bwd(dY: torch.Tensor, x: torch.Tensor, g: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                  dres: torch.Tensor | None = None, dX=None, dg=None, db=None, ws=None, stream=None):
+    """Layer norm backward: dY, x (and dres, the residual branch's gradient, added to dX) [T,d], g [d],
+    the forward's mean and rstd [T].  Returns (dX [T,d], dg [d] fp32, db [d] fp32)."""
+    _need("x", x, (None, None), torch.bfloat16, torch.float32)
+    T, d = x.shape
+    _need("dY", dY, (T, d), x.dtype)
+    _need("g", g, (d,), x.dtype)
+    _need("mean", mean, (T,), torch.float32)
+    _need("rstd", rstd, (T,), torch.float32)
+    if dres is not None:
+        _need("dres", dres, (T, d), x.dtype)
+    dX = _out("dX", dX, (T, d), x.dtype, x)
+    dg = _out("dg", dg, (d,), torch.float32, x)
+    db = _out("db", db, (d,), torch.float32, x)
+    nb = lib.layernorm_bwd_workspace_size(T, d)
+    w = _ws(nb, x.device, ws)
+    _check("layernorm_bwd", lib.layernorm_bwd(_ptr(dY), _ptr(x), _dtype_code(x), _ptr(g), _ptr(mean), _ptr(rstd),
+                                              _ptr(dres), T, d, _ptr(dX), _ptr(dg), _ptr(db), _ptr(w), nb,
+                                              _stream(stream)))
+    return dX, dg, db
+
+
+def linear_cross_entropy_fwd_workspace_size(T: int, d: int, V: int) -> int:
+    return lib.linear_cross_entropy_fwd_workspace_size(T, d, V)
+
+
+def linear_cross_entropy_bwd_workspace_size(T: int, d: int, V: int) -> int:
+    return lib.linear_cross_entropy_bwd_workspace_size(T, d, V)
+
+
+def _ce_args(x, W, targets):
+    _need("x", x, (None, None), torch.bfloat16)
+    T, d = x.shape
+    _need("W", W, (None, d), torch.bfloat16)
+    _need("targets", targets, (T,), torch.int64)
+    return T, d, W.shape[0]
+
+
+def linear_cross_entropy_fwd(x: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
+                             loss=None, lse=None, ws=None, stream=None):
+    """Softmax cross entropy of the head z = x W^T, logits never kept: x [T,d] bf16, W [V,d] bf16,
+    targets [T] int64.  Returns (loss [T] fp32, 0 for ignored tokens; lse [T] fp32)."""
+    T, d, V = _ce_args(x, W, targets)
+    loss = _out("loss", loss, (T,), torch.float32, x)
+    lse = _out("lse", lse, (T,), torch.float32, x)
+    nb = lib.linear_cross_entropy_fwd_workspace_size(T, d, V)
+    w = _ws(nb, x.device, ws)
+    _check("linear_cross_entropy_fwd",
+           lib.linear_cross_entropy_fwd(_ptr(x), _ptr(W), _ptr(targets), T, d, V, ignore_index, _ptr(loss), _ptr(lse),
+                                        _ptr(w), nb, _stream(stream)))
+    return loss, lse
+
+
+def linear_cross_entropy_bwd(x: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                             dloss: torch.Tensor, ignore_index: int = -100, dX=None, dW=None,
+                             dw_dtype=torch.float32, ws=None, stream=None):
+    """Gradients of linear_cross_entropy_fwd for dloss [T] fp32, the gradient at each token's loss (a
+    mean: 1 / the number of tokens that count).  Returns (dX [T,d] bf16, dW [V,d] of dw_dtype, fp32 or
+    bf16; a given dW decides its own type)."""
+    T, d, V = _ce_args(x, W, targets)
+    _need("lse", lse, (T,), torch.float32)
+    _need("dloss", dloss, (T,), torch.float32)
+    dX = _out("dX", dX, (T, d), torch.bfloat16, x)
+    if dW is None:
+        if dw_dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"dw_dtype {dw_dtype}: bfloat16 or float32")
+        dW = torch.empty((V, d), dtype=dw_dtype, device=x.device)
+    else:
+        _need("dW", dW, (V, d), torch.bfloat16, torch.float32)
+    nb = lib.linear_cross_entropy_bwd_workspace_size(T, d, V)
+    w = _ws(nb, x.device, ws)
+    _check("linear_cross_entropy_bwd",
+           lib.linear_cross_entropy_bwd(_ptr(x), _ptr(W), _ptr(targets), _ptr(lse), _ptr(dloss), T, d, V, ignore_index,
+                                        _ptr(dX), _ptr(dW), _dtype_code(dW), _ptr(w), nb, _stream(stream)))
+    return dX, dW
+
+
+# ---------------------------------------------------------------------------
 @dataclasses.dataclass
 class MlpBuffers:
     """Caller-owned device buffers of one MLP block (see fp8q_mlp in include/fp8q.h)."""
@@ -483,7 +694,7 @@ def _steps_args(b0, b1, host, io_type):
 
 
 def get_status(clear: bool = False) -> int:
-    """Device status bits (STATUS_NONFINITE, STATUS_TIMEOUT); synchronize the stream first."""
+    """Device status bits (STATUS_NONFINITE, STATUS_TIMEOUT, STATUS_BAD_TARGET); synchronize the stream first."""
     v = lib.fp8q_get_status(int(clear))
     if v < 0:
         raise Fp8qError("fp8q_get_status failed")

@@ -4,6 +4,7 @@
 #include "fp8q.h"
 #include "fp8q_internal.h"
 
+#include <cmath>
 #include <mutex>
 #include <vector>
 
@@ -26,7 +27,7 @@ enum Kind {
   kKGemmGateUp, kKGemmDown, kKGemmDownDgrad, kKGemmDownWgrad, kKGemmGateUpDgrad, kKGemmGateUpWgrad, kKGemm,
   kKGemmQkv, kKGemmOResidual, kKGemmODgrad, kKGemmOWgrad, kKGemmQkvDgrad, kKGemmQkvWgrad,
   kKGemmGateUpRecompute, kKRmsnormBf16, kKAttnFwd, kKAttnBwdDelta, kKAttnBwdDkdv, kKAttnBwdDq,
-  kKMxQuant, kKPrologueStats, kKPrologueCast,
+  kKMxQuant, kKPrologueStats, kKPrologueCast, kKLayernormFwd, kKLayernormBwd, kKRope, kKCeFwd, kKCeBwd,
   kKCount
 };
 const char* const kKindNames[kKCount] = {
@@ -35,7 +36,7 @@ const char* const kKindNames[kKCount] = {
     "gemm_down_wgrad", "gemm_gate_up_dgrad", "gemm_gate_up_wgrad", "gemm",
     "gemm_qkv", "gemm_o_residual", "gemm_o_dgrad", "gemm_o_wgrad", "gemm_qkv_dgrad", "gemm_qkv_wgrad",
     "gemm_gate_up_recompute", "rmsnorm_bf16", "attn_fwd", "attn_bwd_delta", "attn_bwd_dkdv", "attn_bwd_dq",
-    "mx_quant", "prologue_stats", "prologue_cast"};
+    "mx_quant", "prologue_stats", "prologue_cast", "layernorm_fwd", "layernorm_bwd", "rope", "ce_fwd", "ce_bwd"};
 
 struct Trace {
   bool on = false;
@@ -1411,6 +1412,148 @@ int attention_bwd(const void* qkv, const void* att, const float* lse, const void
                                                   lse2, c.L));
   FP8Q_STEP(kKAttnBwdDkdv, launch_attn_bwd_dkdv(q16, do16, T, S, n_heads, n_kv_heads, delta, lse2, dq16, c.L));
   FP8Q_STEP(kKAttnBwdDq, launch_attn_bwd_dq(q16, do16, T, S, n_heads, n_kv_heads, delta, lse2, dq16, c.L));
+  return finish(c);
+}
+
+// ---------------------------------------------------------------------------
+// Layer norm
+// ---------------------------------------------------------------------------
+namespace {
+inline bool al4(const void* p) { return p && ((uintptr_t)p & 3u) == 0; }
+inline bool al8(const void* p) { return p && ((uintptr_t)p & 7u) == 0; }
+
+int validate_layernorm(fp8q_dtype dtype, int64_t T, int64_t d) {
+  if (dtype != FP8Q_BF16 && dtype != FP8Q_F32) return FP8Q_ERR_INVALID_ARG;
+  if (T < 1 || T > ((int64_t)1 << 28) || d < 1 || d > 16384) return FP8Q_ERR_INVALID_ARG;
+  return FP8Q_OK;
+}
+}  // namespace
+
+int layernorm_fwd(const void* x, fp8q_dtype dtype, const void* g, const void* b, int64_t T, int64_t d, float eps,
+                  void* y, float* mean, float* rstd, fp8q_stream stream) {
+  int e = validate_layernorm(dtype, T, d);
+  if (e) return e;
+  if (!al16(x) || !al16(g) || (b && !al16(b)) || !al16(y) || !al4(mean) || !al4(rstd)) return FP8Q_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || std::isinf(eps)) return FP8Q_ERR_INVALID_ARG;
+  Ctx c;
+  if ((e = make_ctx(&c, stream))) return e;
+  FP8Q_STEP(kKLayernormFwd, launch_layernorm_fwd(x, dtype == FP8Q_F32, g, b, T, (int)d, eps, y, mean, rstd, c.L));
+  return finish(c);
+}
+
+size_t layernorm_bwd_workspace_size(int64_t T, int64_t d) {
+  if (T < 1 || d < 1) return 0;
+  return round256((size_t)layernorm_bwd_blocks(T, (int)d) * 2 * (size_t)d * 4);
+}
+
+int layernorm_bwd(const void* dY, const void* x, fp8q_dtype dtype, const void* g, const float* mean, const float* rstd,
+                  const void* dres, int64_t T, int64_t d, void* dX, float* dg, float* db, void* ws, size_t ws_bytes,
+                  fp8q_stream stream) {
+  int e = validate_layernorm(dtype, T, d);
+  if (e) return e;
+  if (!al16(dY) || !al16(x) || !al16(g) || (dres && !al16(dres)) || !al16(dX)) return FP8Q_ERR_INVALID_ARG;
+  if (!al4(mean) || !al4(rstd) || !al4(dg) || (db && !al4(db))) return FP8Q_ERR_INVALID_ARG;
+  if ((e = check_ws(ws, ws_bytes, layernorm_bwd_workspace_size(T, d)))) return e;
+  Ctx c;
+  if ((e = make_ctx(&c, stream))) return e;
+  FP8Q_STEP(kKLayernormBwd, launch_layernorm_bwd(dY, x, dtype == FP8Q_F32, g, mean, rstd, dres, T, (int)d, dX, dg, db,
+                                                 static_cast<float*>(ws), c.L));
+  return finish(c);
+}
+
+// ---------------------------------------------------------------------------
+// Rotary positions
+// ---------------------------------------------------------------------------
+namespace {
+int rope_run(const void* qkv, fp8q_dtype dtype, int64_t T, int n_heads, int n_kv_heads, const fp8q_rope* r,
+             const int32_t* pos, int inverse, void* out, fp8q_stream stream) {
+  if (!r || (dtype != FP8Q_BF16 && dtype != FP8Q_F32)) return FP8Q_ERR_INVALID_ARG;
+  if (r->head_dim < 8 || r->head_dim > 256 || r->head_dim % 8) return FP8Q_ERR_UNSUPPORTED;
+  if (r->rot_dim < 2 || r->rot_dim > r->head_dim || r->rot_dim % 2) return FP8Q_ERR_INVALID_ARG;
+  if (r->n_axes < 1 || r->n_axes > 255) return FP8Q_ERR_INVALID_ARG;
+  if (T < 1 || T > ((int64_t)1 << 28) || n_heads < 1 || n_heads > 1024 || n_kv_heads < 0 || n_kv_heads > 1024)
+    return FP8Q_ERR_INVALID_ARG;
+  if (!al16(qkv) || !al16(out) || !al4(pos)) return FP8Q_ERR_INVALID_ARG;
+  const uint64_t bytes = (uint64_t)T * (uint64_t)(n_heads + 2 * n_kv_heads) * (uint64_t)r->head_dim *
+                         (dtype == FP8Q_F32 ? 4u : 2u);
+  const uintptr_t a = (uintptr_t)qkv, o = (uintptr_t)out;
+  if (a != o && a < o + bytes && o < a + bytes) return FP8Q_ERR_INVALID_ARG;
+  RopePlan p{};
+  p.dh = r->head_dim;
+  p.rot = r->rot_dim;
+  p.interleaved = r->interleaved != 0;
+  for (int i = 0; i < r->rot_dim / 2; ++i) {
+    const double f = r->inv_freq[i] / 6.283185307179586476925;
+    if (!std::isfinite(f) || r->axis[i] >= r->n_axes) return FP8Q_ERR_INVALID_ARG;
+    // the fraction of a turn per position in 0.64 fixed point (frac < 1 - 2^-54, so it fits)
+    p.turn[i] = (uint64_t)std::ldexp(f - std::floor(f), 64);
+    p.axis[i] = r->axis[i];
+  }
+  Ctx c;
+  int e = make_ctx(&c, stream);
+  if (e) return e;
+  FP8Q_STEP(kKRope, launch_rope(qkv, dtype == FP8Q_F32, p, pos, T, n_heads, n_kv_heads, inverse, out, c.L));
+  return finish(c);
+}
+}  // namespace
+
+int rope_fwd(const void* qkv, fp8q_dtype dtype, int64_t T, int n_heads, int n_kv_heads, const fp8q_rope* rope,
+             const int32_t* pos, void* out, fp8q_stream stream) {
+  return rope_run(qkv, dtype, T, n_heads, n_kv_heads, rope, pos, 0, out, stream);
+}
+int rope_bwd(const void* d_out, fp8q_dtype dtype, int64_t T, int n_heads, int n_kv_heads, const fp8q_rope* rope,
+             const int32_t* pos, void* dqkv, fp8q_stream stream) {
+  return rope_run(d_out, dtype, T, n_heads, n_kv_heads, rope, pos, 1, dqkv, stream);
+}
+
+// ---------------------------------------------------------------------------
+// The language model head's cross entropy
+// ---------------------------------------------------------------------------
+namespace {
+int validate_ce(const void* x, const void* W, const int64_t* targets, int64_t T, int64_t d, int64_t V) {
+  if (T < 1 || T > ((int64_t)1 << 24) || V < 1 || V > ((int64_t)1 << 24)) return FP8Q_ERR_INVALID_ARG;
+  if (d < 8 || d > 65536 || d % 8) return FP8Q_ERR_INVALID_ARG;
+  if (!al16(x) || !al16(W) || !al8(targets)) return FP8Q_ERR_INVALID_ARG;
+  return FP8Q_OK;
+}
+bool ce_sizes_ok(int64_t T, int64_t d, int64_t V) {
+  return T >= 1 && T <= ((int64_t)1 << 24) && V >= 1 && V <= ((int64_t)1 << 24) && d >= 8 && d <= 65536 && d % 8 == 0;
+}
+}  // namespace
+
+size_t linear_cross_entropy_fwd_workspace_size(int64_t T, int64_t d, int64_t V) {
+  return ce_sizes_ok(T, d, V) ? round256(ce_workspace_bytes(T, d, V, 0)) : 0;
+}
+size_t linear_cross_entropy_bwd_workspace_size(int64_t T, int64_t d, int64_t V) {
+  return ce_sizes_ok(T, d, V) ? round256(ce_workspace_bytes(T, d, V, 1)) : 0;
+}
+
+int linear_cross_entropy_fwd(const void* x, const void* W, const int64_t* targets, int64_t T, int64_t d, int64_t V,
+                             int64_t ignore_index, float* loss, float* lse, void* ws, size_t ws_bytes,
+                             fp8q_stream stream) {
+  int e = validate_ce(x, W, targets, T, d, V);
+  if (e) return e;
+  if (!al4(loss) || !al4(lse)) return FP8Q_ERR_INVALID_ARG;
+  if ((e = check_ws(ws, ws_bytes, linear_cross_entropy_fwd_workspace_size(T, d, V)))) return e;
+  Ctx c;
+  if ((e = make_ctx(&c, stream))) return e;
+  FP8Q_STEP(kKCeFwd, launch_ce_fwd((const uint16_t*)x, (const uint16_t*)W, targets, T, (int)d, V, ignore_index, loss,
+                                   lse, ws, c.L));
+  return finish(c);
+}
+
+int linear_cross_entropy_bwd(const void* x, const void* W, const int64_t* targets, const float* lse,
+                             const float* dloss, int64_t T, int64_t d, int64_t V, int64_t ignore_index, void* dX,
+                             void* dW, fp8q_dtype dw_dtype, void* ws, size_t ws_bytes, fp8q_stream stream) {
+  int e = validate_ce(x, W, targets, T, d, V);
+  if (e) return e;
+  if (!al4(lse) || !al4(dloss) || !al16(dX) || !al16(dW)) return FP8Q_ERR_INVALID_ARG;
+  if (dw_dtype != FP8Q_BF16 && dw_dtype != FP8Q_F32) return FP8Q_ERR_INVALID_ARG;
+  if ((e = check_ws(ws, ws_bytes, linear_cross_entropy_bwd_workspace_size(T, d, V)))) return e;
+  Ctx c;
+  if ((e = make_ctx(&c, stream))) return e;
+  FP8Q_STEP(kKCeBwd, launch_ce_bwd((const uint16_t*)x, (const uint16_t*)W, targets, lse, dloss, T, (int)d, V,
+                                   ignore_index, (uint16_t*)dX, dW, dw_dtype == FP8Q_F32, ws, c.L));
   return finish(c);
 }
 

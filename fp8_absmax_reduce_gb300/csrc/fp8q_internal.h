@@ -75,6 +75,34 @@ cudaError_t launch_attn_bwd_dkdv(const uint16_t* qkv, const uint16_t* datt, int6
 cudaError_t launch_attn_bwd_dq(const uint16_t* qkv, const uint16_t* datt, int64_t T, int S, int Hq, int Hkv,
                                const float* delta, const float* lse2, uint16_t* dqkv, const Launch& L);
 
+// Layer norm of x [T, d] (bf16, or fp32 with f32 != 0; g, b, y alike; b may be null).
+cudaError_t launch_layernorm_fwd(const void* x, int f32, const void* g, const void* b, int64_t T, int d, float eps,
+                                 void* y, float* mean, float* rstd, const Launch& L);
+// Backward: dX (dres may be null), dg and db (db may be null); part: layernorm_bwd_blocks(T, d) x 2 d floats.
+constexpr int kLnRows = 64;
+int layernorm_bwd_blocks(int64_t T, int d);
+cudaError_t launch_layernorm_bwd(const void* dY, const void* x, int f32, const void* g, const float* mean,
+                                 const float* rstd, const void* dres, int64_t T, int d, void* dX, float* dg, float* db,
+                                 float* part, const Launch& L);
+
+// Rotary positions: pair i of a rotated head turns by pos[axis[i]] turn[i] 2^-64 turns.
+constexpr int kRopePairs = 128;
+struct RopePlan {
+  int dh, rot, interleaved;
+  uint64_t turn[kRopePairs];
+  uint8_t axis[kRopePairs];
+};
+cudaError_t launch_rope(const void* in, int f32, const RopePlan& plan, const int32_t* pos, int64_t T, int n_heads,
+                        int n_kv_heads, int inverse, void* out, const Launch& L);
+
+// Softmax cross entropy of the linear head z = x W^T (x [T, d], W [V, d] bf16).
+size_t ce_workspace_bytes(int64_t T, int64_t d, int64_t V, int bwd);
+cudaError_t launch_ce_fwd(const uint16_t* x, const uint16_t* W, const int64_t* targets, int64_t T, int d, int64_t V,
+                          int64_t ignore, float* loss, float* lse, void* ws, const Launch& L);
+cudaError_t launch_ce_bwd(const uint16_t* x, const uint16_t* W, const int64_t* targets, const float* lse,
+                          const float* dloss, int64_t T, int d, int64_t V, int64_t ignore, uint16_t* dX, void* dW,
+                          int dw_f32, void* ws, const Launch& L);
+
 // Diagnostics: a bounded wait that is made to run out (see fp8q_selftest_bounded_wait).
 cudaError_t launch_selftest_bounded_wait(uint64_t limit_ns, const Launch& L);
 

@@ -77,6 +77,7 @@ typedef void* fp8q_stream; /* cudaStream_t */
 /* Device status bits returned by fp8q_get_status. */
 #define FP8Q_STATUS_NONFINITE 0x1u
 #define FP8Q_STATUS_TIMEOUT 0x2u
+#define FP8Q_STATUS_BAD_TARGET 0x4u /* linear_cross_entropy_*: a target outside [0, V) that is not ignore_index */
 
 /* ------------------------------------------------------------------------ */
 /* Per-tensor absmax quantization (LLMQ §1 dynamic tensor-level scaling;    */
@@ -496,6 +497,89 @@ FP8Q_API size_t attention_bwd_workspace_size(int64_t T, int n_heads);
 FP8Q_API int attention_bwd(const void* qkv, const void* att, const float* lse, const void* d_att, int64_t T,
                            int64_t seq_len, int n_heads, int n_kv_heads, int head_dim, void* dqkv, void* ws,
                            size_t ws_bytes, fp8q_stream stream);
+
+/* ------------------------------------------------------------------------ */
+/* Rotary positions, between the QKV projection and the attention core.     */
+/* ------------------------------------------------------------------------ */
+/* Pair i (0 <= i < rot_dim / 2) of a rotated head turns by the angle pos[axis[i]][t] inv_freq[i]
+ * (radians): (a, b) -> (a cos - b sin, b cos + a sin).  The pair's elements are columns i and
+ * i + rot_dim / 2 of the head or, with interleaved != 0, columns 2i and 2i + 1; columns from
+ * rot_dim on are copied.  Several axes (text: one; video: time, height, width) give each pair the
+ * position of its own axis.  The angle is exact modulo one turn to |pos| 2^-65 + |angle| 2^-53
+ * turns, whatever the position; sine and cosine are fp32, the rotation fp32, rounded once.
+ * The structure is host memory and is read during the call only. */
+typedef struct fp8q_rope {
+  int head_dim;         /* a multiple of 8, 8 <= head_dim <= 256 */
+  int rot_dim;          /* even, 2 <= rot_dim <= head_dim */
+  int n_axes;           /* rows of pos, 1 .. 255 */
+  int interleaved;
+  double inv_freq[128]; /* [rot_dim / 2], finite */
+  uint8_t axis[128];    /* [rot_dim / 2], each < n_axes */
+} fp8q_rope;
+/* qkv [T, (n_heads + 2 n_kv_heads) head_dim] (bf16 or fp32), row t = [q heads | k heads | v heads]
+ * as attention_fwd reads it; pos [n_axes, T] int32 (any value, negative ones too).  The q and k heads
+ * are rotated, the v heads copied; out has qkv's layout and may be qkv itself (in place), but must not
+ * overlap it otherwise.  n_kv_heads = 0 rotates all n_heads heads (a tensor of q or of k alone).
+ * rope_bwd is the gradient: the same rotation by the negative angles of d_out.
+ * Requirements: 1 <= T <= 2^28, 1 <= n_heads <= 1024, 0 <= n_kv_heads <= 1024; qkv and out 16-byte,
+ * pos 4-byte aligned; head_dim outside its range is FP8Q_ERR_UNSUPPORTED.  No workspace. */
+FP8Q_API int rope_fwd(const void* qkv, fp8q_dtype dtype, int64_t T, int n_heads, int n_kv_heads,
+                      const fp8q_rope* rope, const int32_t* pos, void* out, fp8q_stream stream);
+FP8Q_API int rope_bwd(const void* d_out, fp8q_dtype dtype, int64_t T, int n_heads, int n_kv_heads,
+                      const fp8q_rope* rope, const int32_t* pos, void* dqkv, fp8q_stream stream);
+
+/* ------------------------------------------------------------------------ */
+/* Layer norm, beside the RMSNorm entry points, for models that use it.     */
+/* ------------------------------------------------------------------------ */
+/* x [T,d], g [d], b [d] (all bf16 or all fp32; b may be NULL) -> y [T,d] of the same type,
+ * mean [T] and rstd [T] fp32 (kept for the backward):
+ *   mean = (1/d) sum x, rstd = 1 / sqrt((1/d) sum (x - mean)^2 + eps), y = (x - mean) rstd g + b.
+ * A row of equal values has variance 0 (rstd = eps^-1/2; eps = 0 then gives Inf and NaN).
+ * y may be x itself.
+ * Backward: dY [T,d], x, g and the forward's mean and rstd, dres [T,d] optional (the residual branch's
+ * gradient, as rmsnorm_bwd's dY) -> dX [T,d], dg [d] fp32 and, unless db is NULL, db [d] fp32:
+ *   xh = (x - mean) rstd, u = dY g, dX = rstd (u - mean_j(u) - xh mean_j(u xh)) (+ dres),
+ *   dg = sum_t dY xh, db = sum_t dY.
+ * dX may be dY, x or dres itself.  Sums are fp32 in a fixed order, so results repeat bit for bit.
+ * Requirements: 1 <= T <= 2^28, 1 <= d <= 16384, eps finite and >= 0; [T,d] tensors, g and b 16-byte,
+ * mean, rstd, dg and db 4-byte aligned.  Workspace (backward): layernorm_bwd_workspace_size(T, d)
+ * bytes, 256-byte aligned. */
+FP8Q_API int layernorm_fwd(const void* x, fp8q_dtype dtype, const void* g, const void* b, int64_t T, int64_t d,
+                           float eps, void* y, float* mean, float* rstd, fp8q_stream stream);
+FP8Q_API size_t layernorm_bwd_workspace_size(int64_t T, int64_t d);
+FP8Q_API int layernorm_bwd(const void* dY, const void* x, fp8q_dtype dtype, const void* g, const float* mean,
+                           const float* rstd, const void* dres, int64_t T, int64_t d, void* dX, float* dg, float* db,
+                           void* ws, size_t ws_bytes, fp8q_stream stream);
+
+/* ------------------------------------------------------------------------ */
+/* Softmax cross entropy of the language model head, without its logits     */
+/* (LLMQ §3: chunked logits).                                               */
+/* ------------------------------------------------------------------------ */
+/* x [T,d] bf16 (the last hidden states), W [V,d] bf16 (one row per vocabulary entry, as a tied
+ * embedding has them), targets [T] int64.  With z = x W^T in fp32 (never stored in full):
+ *   lse [T] fp32:  lse_t = log sum_v e^{z_tv};
+ *   loss [T] fp32: lse_t - z_{t,y} for the target y; 0 where targets[t] == ignore_index.
+ * A target outside [0, V) that is not ignore_index sets FP8Q_STATUS_BAD_TARGET and is ignored.
+ * Backward: lse as the forward wrote it, dloss [T] fp32 the gradient at each token's loss (a mean:
+ * 1 / the number of tokens that count; entries of ignored tokens are not used) ->
+ *   G = dloss_t (e^{z - lse_t} - 1[v = y]), 0 in the rows of ignored tokens;
+ *   dX [T,d] bf16 = G W, dW [V,d] (bf16 or fp32) = G^T x, both overwritten in full.
+ * The logits are computed again in pieces of the vocabulary; G is rounded to bf16 relative to
+ * max |dloss| as the tensor cores' operand (the sums are fp32), so an fp32 dW carries that rounding
+ * (2^-9 of the terms of its sums).  Rows of x of ignored tokens may hold anything, NaN too, without
+ * reaching dX or dW.  Deterministic.
+ * Requirements: 1 <= T, V <= 2^24, d a multiple of 8, 8 <= d <= 65536; x, W, dX, dW 16-byte, targets
+ * 8-byte, loss, lse, dloss 4-byte aligned; outputs must not overlap inputs.  Workspaces: the
+ * matching *_workspace_size(T, d, V) bytes (0 for sizes outside the limits), 256-byte aligned. */
+FP8Q_API size_t linear_cross_entropy_fwd_workspace_size(int64_t T, int64_t d, int64_t V);
+FP8Q_API int linear_cross_entropy_fwd(const void* x, const void* W, const int64_t* targets, int64_t T, int64_t d,
+                                      int64_t V, int64_t ignore_index, float* loss, float* lse, void* ws,
+                                      size_t ws_bytes, fp8q_stream stream);
+FP8Q_API size_t linear_cross_entropy_bwd_workspace_size(int64_t T, int64_t d, int64_t V);
+FP8Q_API int linear_cross_entropy_bwd(const void* x, const void* W, const int64_t* targets, const float* lse,
+                                      const float* dloss, int64_t T, int64_t d, int64_t V, int64_t ignore_index,
+                                      void* dX, void* dW, fp8q_dtype dw_dtype, void* ws, size_t ws_bytes,
+                                      fp8q_stream stream);
 
 /* ------------------------------------------------------------------------ */
 /* Status and introspection                                                 */

@@ -1,0 +1,239 @@
+"""The head's cross entropy on the GPU against its 64-bit definition, element by element.
+
+Tolerances.  A logit is an fp32 tensor-core sum of d exact products in steps of at least 16 terms, each step within
+2^-23 of the partial sums, which are at most S = sum |x w|: e_z = (d / 16 + 32) 2^-23 S, with S the row's largest.
+The row's sum of exponentials has fewer than 100 roundings on any path and exponentials within 2^-21:
+lse is within e_z + 1e-5 + 2^-24 |lse|, and a target's loss within twice e_z + the same.
+Backward: p = e^(z - lse) is within e_z + 2^-21 (|z - lse| + 4) of itself; G is rounded to bf16, half a step 2^-8; the products
+are fp32 sums in steps of 16 terms of |G W| (vocabulary) or |G x| (tokens); the result is rounded to its type.  So
+an element is within 2^-8 sum|G w| + (n / 16 + 32) 2^-23 sum|G w| + e_p sum p|dloss w| + half a step.  The bound is
+a worst case.  A rounding's RMS is 0.41 of the largest (uniform in the step, the step against the value averaged over
+an octave), so with one dominant term the two roundings of 2^-8 give an RMS of sqrt(2) 0.41 / 2 = 0.29 of the bound,
+and less with many terms: below 0.35 where the sums have 16 terms or more."""
+
+import pytest
+import torch
+
+import fp8_absmax_reduce_gb300 as fq
+from tests import _head_ref as ref
+from tests.test_gpu_guard import Guarded
+
+pytestmark = pytest.mark.gpu
+
+IGN = -100
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+SHAPES = [(1, 8, 1), (1, 16, 2), (2, 8, 300), (3, 64, 7), (127, 72, 129), (128, 128, 256), (129, 136, 257), (300, 512, 1000), (64, 256, 20001),
+          (257, 2048, 8200), (1000, 264, 5003), (513, 128, 16385), (2, 4096, 1001)]
+
+
+def make(T, d, V, seed=0, lean=8.0, ignored=0.2, scale=0.05):
+    g = torch.Generator(device="cuda").manual_seed(seed + T + 7 * d + 13 * V)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    W = (n(V, d) * scale).bfloat16()
+    t = torch.randint(0, V, (T,), generator=g, device="cuda")
+    x = n(T, d)
+    x = (x + lean * torch.rand(T, 1, generator=g, device="cuda") * W[t].float() / (scale * d ** 0.5)).bfloat16()
+    t[torch.rand(T, generator=g, device="cuda") < ignored] = IGN
+    dl = torch.randn(T, generator=g, device="cuda") / T
+    return x, W, t, dl
+
+
+def e_z(x, W):
+    S = (x.double().abs() @ W.double().abs().t()).max(1).values
+    return (x.shape[1] / 16 + 32) * 2.0 ** -23 * S
+
+
+def check_fwd(x, W, t, loss, lse):
+    wl, we = ref.cross_entropy(x.double(), W.double(), t, IGN)
+    tol = e_z(x, W) + 1e-5 + 2.0 ** -24 * we.abs()
+    err = (lse.double() - we).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    err = (loss.double() - wl).abs()
+    assert bool((err <= 2 * tol + 2.0 ** -24 * wl.abs()).all()), float((err / tol).max())
+    assert bool((loss[t == IGN] == 0).all())
+
+
+def check_bwd(x, W, t, dl, dX, dW):
+    xd, Wd = x.double(), W.double()
+    G = ref.cross_entropy_grad(xd, Wd, t, dl.double(), IGN)
+    z = xd @ Wd.t()
+    lse = torch.logsumexp(z, 1, keepdim=True)
+    p = torch.exp(z - lse) * torch.where(t == IGN, 0.0, dl.double().abs())[:, None]
+    ep = p * (2 * e_z(x, W)[:, None] + 2.0 ** -21 * ((z - lse).abs() + 4))
+    for got, want, a, other, n in ((dX, G @ Wd, G.abs(), Wd.abs(), W.shape[0]), (dW, G.t() @ xd, G.abs().t(), xd.abs(), x.shape[0])):
+        e = ep if got is dX else ep.t()
+        bound = ((2.0 ** -8 + (n / 16 + 32) * 2.0 ** -23) * (a @ other) + e @ other + HALF[got.dtype] * want.abs()) * (1 + 2.0 ** -7) + 1e-30
+        err = (got.double() - want).abs()
+        assert bool((err <= bound).all()), float((err / bound).max())
+        if n >= 16:
+            assert float((err / bound).square().mean().sqrt()) < 0.35
+    assert bool((dX[t == IGN] == 0).all())
+
+
+@pytest.mark.parametrize("T,d,V", SHAPES)
+def test_forward_and_backward(T, d, V):
+    x, W, t, dl = make(T, d, V)
+    fq.get_status(clear=True)
+    loss, lse = fq.linear_cross_entropy_fwd(x, W, t)
+    check_fwd(x, W, t, loss, lse)
+    for dt in (torch.float32, torch.bfloat16):
+        dX, dW = fq.linear_cross_entropy_bwd(x, W, t, lse, dl, dw_dtype=dt)
+        assert dW.dtype == dt
+        check_bwd(x, W, t, dl, dX, dW)
+    torch.cuda.synchronize()
+    assert fq.get_status() == 0
+
+
+def test_mean_of_one_weight():
+    x, W, t, _ = make(700, 256, 3000, lean=20.0)
+    dl = torch.full((700,), 1.0 / float((t != IGN).sum()), device="cuda")
+    loss, lse = fq.linear_cross_entropy_fwd(x, W, t)
+    check_bwd(x, W, t, dl, *fq.linear_cross_entropy_bwd(x, W, t, lse, dl))
+
+
+def test_sharp_rows_and_wide_logits():
+    """Logits of hundreds: rows whose probabilities are 0 and 1, far from the largest logit on both sides."""
+    x, W, t, dl = make(200, 128, 1500, lean=0.0, scale=4.0)
+    x[50:] *= 8
+    loss, lse = fq.linear_cross_entropy_fwd(x, W, t)
+    check_fwd(x, W, t, loss, lse)
+    assert bool(torch.isfinite(lse).all())
+    # the gradient bound holds where the logits' own error stays small: the rows of moderate logits
+    check_bwd(x[:50], W, t[:50], dl[:50], *fq.linear_cross_entropy_bwd(x[:50], W, t[:50], lse[:50], dl[:50]))
+
+
+def test_every_token_ignored():
+    x, W, t, dl = make(130, 64, 500, ignored=2.0)
+    loss, lse = fq.linear_cross_entropy_fwd(x, W, t)
+    check_fwd(x, W, t, loss, lse)
+    dX, dW = fq.linear_cross_entropy_bwd(x, W, t, lse, dl)
+    assert bool((loss == 0).all()) and bool((dX == 0).all()) and bool((dW == 0).all())
+
+
+def test_zero_weights():
+    x, W, t, dl = make(64, 64, 300)
+    _, lse = fq.linear_cross_entropy_fwd(x, W, t)
+    dX, dW = fq.linear_cross_entropy_bwd(x, W, t, lse, torch.zeros_like(dl))
+    assert bool((dX == 0).all()) and bool((dW == 0).all())
+
+
+def test_padded_rows_may_hold_anything():
+    """Ignored tokens with NaN and Inf in x and in dloss: nothing of it leaves their rows."""
+    x, W, t, dl = make(300, 128, 2000)
+    t[7:40] = IGN
+    xb, dlb = x.clone(), dl.clone()
+    xb[7:40:2], xb[8:40:2] = float("nan"), float("inf")
+    dlb[7:40] = float("nan")
+    loss, lse = fq.linear_cross_entropy_fwd(xb, W, t)
+    assert bool((loss[7:40] == 0).all())
+    l0, e0 = fq.linear_cross_entropy_fwd(x, W, t)
+    assert torch.equal(loss, l0) and torch.equal(lse[:7], e0[:7]) and torch.equal(lse[40:], e0[40:])
+    a = fq.linear_cross_entropy_bwd(xb, W, t, lse, dlb)
+    b = fq.linear_cross_entropy_bwd(x, W, t, e0, dl)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_non_finite_token_reaches_its_own_loss_only():
+    x, W, t, dl = make(300, 128, 2000, ignored=0.0)
+    l0, _ = fq.linear_cross_entropy_fwd(x, W, t)
+    x[9, 3] = float("nan")
+    loss, lse = fq.linear_cross_entropy_fwd(x, W, t)
+    assert bool(torch.isnan(loss[9])) and bool(torch.isnan(lse[9]))
+    loss[9] = l0[9]
+    assert torch.equal(loss, l0)
+
+
+def test_bad_targets_are_recorded_and_ignored():
+    x, W, t, dl = make(100, 64, 500, ignored=0.0)
+    good = t.clone()
+    good[[3, 4, 5]] = IGN
+    bad = t.clone()
+    bad[3], bad[4], bad[5] = 500, -1, 2 ** 40
+    fq.get_status(clear=True)
+    a = fq.linear_cross_entropy_fwd(x, W, bad)
+    torch.cuda.synchronize()
+    assert fq.get_status(clear=True) == fq.STATUS_BAD_TARGET
+    b = fq.linear_cross_entropy_fwd(x, W, good)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ga = fq.linear_cross_entropy_bwd(x, W, bad, a[1], dl)
+    torch.cuda.synchronize()
+    assert fq.get_status(clear=True) == fq.STATUS_BAD_TARGET
+    gb = fq.linear_cross_entropy_bwd(x, W, good, a[1], dl)
+    assert torch.equal(ga[0], gb[0]) and torch.equal(ga[1], gb[1])
+    # another ignore_index, inside the vocabulary: class 7 does not count
+    t[10] = 7
+    torch.cuda.synchronize()
+    assert fq.get_status(clear=True) == 0
+    assert float(fq.linear_cross_entropy_fwd(x, W, t, ignore_index=7)[0][10]) == 0.0
+
+
+def test_guard_bands_repeats_and_second_stream():
+    T, d, V = 259, 136, 8321
+    x, W, t, dl = make(T, d, V)
+    loss, lse = fq.linear_cross_entropy_fwd(x, W, t)
+    for dt in (torch.float32, torch.bfloat16):
+        gl, ge, gx, gw = Guarded((T,), torch.float32), Guarded((T,), torch.float32), Guarded((T, d), torch.bfloat16), Guarded((V, d), dt)
+        fq.linear_cross_entropy_fwd(x, W, t, loss=gl.t, lse=ge.t)
+        fq.linear_cross_entropy_bwd(x, W, t, ge.t, dl, dX=gx.t, dW=gw.t)
+        torch.cuda.synchronize()
+        assert all(v.intact() for v in (gl, ge, gx, gw))
+        assert torch.equal(gl.t, loss) and torch.equal(ge.t, lse)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            again = fq.linear_cross_entropy_bwd(x, W, t, lse, dl, dw_dtype=dt)
+        s.synchronize()
+        assert torch.equal(again[0], gx.t) and torch.equal(again[1], gw.t)
+
+
+def test_workspace_bytes_past_the_need_are_left_alone():
+    T, d, V = 130, 72, 9001
+    x, W, t, dl = make(T, d, V)
+    for size, run in ((fq.linear_cross_entropy_fwd_workspace_size(T, d, V), lambda w: fq.linear_cross_entropy_fwd(x, W, t, ws=w)),
+                      (fq.linear_cross_entropy_bwd_workspace_size(T, d, V),
+                       lambda w: fq.linear_cross_entropy_bwd(x, W, t, torch.zeros(T, device="cuda"), dl, ws=w))):
+        ws = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        run(ws)
+        torch.cuda.synchronize()
+        assert bool((ws[size:] == 0xA5).all())
+
+
+def test_dw_past_32_bit_offsets():
+    """V d above 2^31: the last pieces' rows of dW and the logits against a head of those rows."""
+    T, d, V = 3, 16384, 140000
+    x, W, t, dl = make(T, d, 8)
+    W = torch.zeros(V, d, dtype=torch.bfloat16, device="cuda")
+    W[-5:] = (torch.randn(5, d, device="cuda") * 0.02).bfloat16()
+    t[:] = torch.tensor([V - 1, V - 3, 0], device="cuda")
+    loss, lse = fq.linear_cross_entropy_fwd(x, W, t)
+    z = x.double() @ W[-5:].double().t()
+    want = torch.logsumexp(torch.cat([z, torch.full((T, 1), float(torch.log(torch.tensor(V - 5.0))), device="cuda").double()], 1), 1)
+    assert bool(((lse.double() - want).abs() <= e_z(x, W[-5:]) + 1e-5 + 2.0 ** -24 * want.abs()).all())
+    dX, dW = fq.linear_cross_entropy_bwd(x, W, t, lse, dl, dw_dtype=torch.bfloat16)
+    p = torch.exp(z - want[:, None])
+    p[0, 4] -= 1
+    p[1, 2] -= 1
+    G = p * dl.double()[:, None]
+    err = (dW[-5:].double() - G.t() @ x.double()).abs()
+    assert bool((err <= 2.0 ** -7 * (G.abs().t() @ x.double().abs())).all())
+
+
+def test_refusals():
+    x, W, t, dl = make(16, 64, 100)
+    lse = torch.zeros(16, device="cuda")
+    for call in (lambda: fq.linear_cross_entropy_fwd(x, W[:, :32], t), lambda: fq.linear_cross_entropy_fwd(x, W.t(), t),
+                 lambda: fq.linear_cross_entropy_fwd(x, W, t[:8]), lambda: fq.linear_cross_entropy_bwd(x, W, t, lse[:8], dl),
+                 lambda: fq.linear_cross_entropy_bwd(x, W, t, lse, dl, dW=torch.empty(100, 32, device="cuda")),
+                 lambda: fq.linear_cross_entropy_fwd(x, W, t.cpu()),
+                 lambda: fq.linear_cross_entropy_fwd(x, W, t, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: fq.linear_cross_entropy_fwd(x.float(), W, t), lambda: fq.linear_cross_entropy_fwd(x, W, t.int()),
+                 lambda: fq.linear_cross_entropy_bwd(x, W, t, lse.double(), dl),
+                 lambda: fq.linear_cross_entropy_bwd(x, W, t, lse, dl, dw_dtype=torch.float16)):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(fq.Fp8qError):
+        fq.linear_cross_entropy_fwd(x[:, :60].contiguous(), W[:, :60].contiguous(), t)
+    with pytest.raises(fq.Fp8qError):
+        fq.linear_cross_entropy_fwd(x[:0], W, t[:0])
