@@ -61,88 +61,100 @@ __device__ __forceinline__ float ln_warp_sum(float v) {
 
 // ---------------------------------------------------------------------------
 // Forward: W warps hold a row in registers, NP pieces a lane (piece k of lane l of warp w is piece
-// (k W + w) 32 + l of the row); a block of max(W, 8) warps has 8 / W rows.  Each warp takes the mean and the sum of squares about
-// it of its own elements, in two passes over its registers; the warps' (mean, M2) pairs are then
-// joined with the parallel-variance formula M2 = M2_a + M2_b + delta^2 n_a n_b / n, so a row costs one
-// block barrier and nothing cancels.
+// (k W + w) 32 + l of the row); a block of max(W, 8) warps has 8 / W rows at a time and walks the rows with the
+// grid's stride, the next row's pieces in flight while the current one is computed and written.  Each
+// warp takes the mean and the sum of squares about it of its own elements, in two passes over its registers; the
+// warps' (mean, M2) pairs are then joined with the parallel-variance formula
+// M2 = M2_a + M2_b + delta^2 n_a n_b / n, so a row costs one block barrier and nothing cancels.
 // ---------------------------------------------------------------------------
+constexpr int ln_fwd_threads(int W) { return W < 8 ? 256 : 32 * W; }
+// Resident blocks per SM: 1024 threads of 64 registers, or 512 of 128 where fp32 pieces fill more.
+constexpr int ln_fwd_per_sm(int F32, int VEC, int W) {
+  return (F32 && VEC == 8 ? 512 : 1024) / ln_fwd_threads(W) > 0 ? (F32 && VEC == 8 ? 512 : 1024) / ln_fwd_threads(W) : 1;
+}
+
 template <int F32, int VEC, int NP, int W>
-__global__ void __launch_bounds__(W < 8 ? 256 : 32 * W) k_layernorm_fwd(const void* __restrict__ x, const void* __restrict__ g,
-                                                       const void* __restrict__ b, int64_t T, int d, float eps, void* y,
-                                                       float* __restrict__ mean, float* __restrict__ rstd) {
+__global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(F32, VEC, W))
+    k_layernorm_fwd(const void* x, const void* __restrict__ g, const void* __restrict__ b, int64_t T, int d, float eps,
+                    void* y, float* __restrict__ mean, float* __restrict__ rstd) {
   constexpr int kRows = W < 8 ? 8 / W : 1;
-  __shared__ float sm[kRows][W], sv[kRows][W];
+  __shared__ float sm[2][kRows][W], sv[2][kRows][W];
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W, r = (threadIdx.x >> 5) / W;
-  const int64_t row = (int64_t)blockIdx.x * kRows + r;
-  const bool live = row < T;
-  const int64_t base = row * d;
   const int pieces = d / VEC;
-  Piece<F32, VEC> px[NP];
-  float s = 0.0f;
+  // elements of a warp: full groups of 32 pieces, and what the last one holds
+  auto count = [&](int w) {
+    int n = 0;
 #pragma unroll
-  for (int k = 0; k < NP; ++k) {
-    const int i = (k * W + warp) * 32 + lane;
-    if (live && i < pieces) px[k].load(x, base + (int64_t)i * VEC);
-  }
+    for (int k = 0; k < NP; ++k) n += min(32, max(0, pieces - (k * W + w) * 32));
+    return n * VEC;
+  };
+  const int n_own = count(warp);
+  const float inv_own = n_own ? 1.0f / (float)n_own : 0.0f;
+  Piece<F32, VEC> px[NP], nx[NP];
+  auto load = [&](Piece<F32, VEC>(&p)[NP], int64_t row) {
 #pragma unroll
-  for (int k = 0; k < NP; ++k) {
-    const int i = (k * W + warp) * 32 + lane;
-    if (live && i < pieces)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) s += px[k].at(e);
-  }
-  // this warp's element count: full groups of 32 pieces, and what the last one holds
-  int n_own = 0;
-#pragma unroll
-  for (int k = 0; k < NP; ++k) n_own += min(32, max(0, pieces - (k * W + warp) * 32));
-  n_own *= VEC;
-  float mu = n_own ? ln_warp_sum(s) / (float)n_own : 0.0f;
-  float m2 = 0.0f;
-#pragma unroll
-  for (int k = 0; k < NP; ++k) {
-    const int i = (k * W + warp) * 32 + lane;
-    if (live && i < pieces)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float c = px[k].at(e) - mu;
-        m2 += c * c;
-      }
-  }
-  m2 = ln_warp_sum(m2);
-  if (W > 1) {
-    if (lane == 0) { sm[r][warp] = mu; sv[r][warp] = m2; }
-    __syncthreads();
-    float n = 0.0f;
-    mu = 0.0f;
-    m2 = 0.0f;
-    for (int w = 0; w < W; ++w) {
-      int nw = 0;
-#pragma unroll
-      for (int k = 0; k < NP; ++k) nw += min(32, max(0, pieces - (k * W + w) * 32));
-      if (nw == 0) break;
-      const float nf = (float)(nw * VEC), tot = n + nf, delta = sm[r][w] - mu, share = nf / tot;
-      mu += delta * share;
-      m2 += sv[r][w] + delta * delta * n * share;
-      n = tot;
+    for (int k = 0; k < NP; ++k) {
+      const int i = (k * W + warp) * 32 + lane;
+      if (row < T && i < pieces) p[k].load(x, row * d + (int64_t)i * VEC);
     }
-  }
-  if (!live) return;
-  const float rs = 1.0f / sqrtf(m2 / (float)d + eps);
-  if (warp == 0 && lane == 0) {
-    mean[row] = mu;
-    rstd[row] = rs;
-  }
+  };
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t row = (int64_t)blockIdx.x * kRows + r;
+  load(nx, row);
+  int par = 0;
+  for (int64_t first = (int64_t)blockIdx.x * kRows; first < T; first += step, row += step, par ^= 1) {
 #pragma unroll
-  for (int k = 0; k < NP; ++k) {
-    const int i = (k * W + warp) * 32 + lane;
-    if (i < pieces) {
-      Piece<F32, VEC> pg, pb;
-      pg.load(g, (int64_t)i * VEC);
-      if (b) pb.load(b, (int64_t)i * VEC);
-      float v[VEC];
+    for (int k = 0; k < NP; ++k) px[k] = nx[k];
+    load(nx, row + step);
+    float s = 0.0f;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[e] = (px[k].at(e) - mu) * rs * pg.at(e) + (b ? pb.at(e) : 0.0f);
-      Piece<F32, VEC>::store(y, base + (int64_t)i * VEC, v);
+    for (int k = 0; k < NP; ++k)
+      if ((k * W + warp) * 32 + lane < pieces)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s += px[k].at(e);
+    float mu = ln_warp_sum(s) * inv_own;
+    float m2 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NP; ++k)
+      if ((k * W + warp) * 32 + lane < pieces)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float c = px[k].at(e) - mu;
+          m2 += c * c;
+        }
+    m2 = ln_warp_sum(m2);
+    if (W > 1) {
+      if (lane == 0) { sm[par][r][warp] = mu; sv[par][r][warp] = m2; }
+      __syncthreads();
+      float n = (float)count(0);
+      mu = sm[par][r][0];
+      m2 = sv[par][r][0];
+#pragma unroll
+      for (int w = 1; w < W; ++w) {
+        const float nf = (float)count(w), tot = n + nf, delta = sm[par][r][w] - mu, share = __fdividef(nf, tot);
+        mu += delta * share;
+        m2 += sv[par][r][w] + delta * delta * n * share;
+        n = tot;
+      }
+    }
+    if (row >= T) continue;
+    const float rs = 1.0f / sqrtf(m2 / (float)d + eps);
+    if (warp == 0 && lane == 0) {
+      mean[row] = mu;
+      rstd[row] = rs;
+    }
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int i = (k * W + warp) * 32 + lane;
+      if (i < pieces) {
+        Piece<F32, VEC> pg, pb;
+        pg.load(g, (int64_t)i * VEC);
+        if (b) pb.load(b, (int64_t)i * VEC);
+        float v[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] = (px[k].at(e) - mu) * rs * pg.at(e) + (b ? pb.at(e) : 0.0f);
+        Piece<F32, VEC>::store(y, row * d + (int64_t)i * VEC, v);
+      }
     }
   }
 }
@@ -345,7 +357,8 @@ template <int F32, int VEC, int NP, int W>
 cudaError_t fwd_go(const void* x, const void* g, const void* b, int64_t T, int d, float eps, void* y, float* mean,
                    float* rstd, const Launch& L) {
   constexpr int rows = W < 8 ? 8 / W : 1;
-  k_layernorm_fwd<F32, VEC, NP, W><<<(unsigned)((T + rows - 1) / rows), W < 8 ? 256 : 32 * W, 0, L.stream>>>(
+  const int64_t need = (T + rows - 1) / rows, wave = (int64_t)L.num_sms * ln_fwd_per_sm(F32, VEC, W);
+  k_layernorm_fwd<F32, VEC, NP, W><<<(unsigned)(need < wave ? need : wave), ln_fwd_threads(W), 0, L.stream>>>(
       x, g, b, T, d, eps, y, mean, rstd);
   return launched(L);
 }

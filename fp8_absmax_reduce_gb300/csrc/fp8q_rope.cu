@@ -63,7 +63,7 @@ struct Vec8 {
   }
 };
 
-constexpr int kRopeThreads = 256, kRopeHeads = 4;  // threads of a block; heads a thread has in flight
+constexpr int kRopeThreads = 128, kRopeHeads = 4;  // threads of a block; heads a thread has in flight
 
 // rot_dim a multiple of 16.  A token has `units` * `slots` threads: thread (u, s) turns pairs 8u .. 8u+7
 // of heads s, s + slots, ...; then the token's threads copy what is not rotated.
@@ -79,14 +79,8 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_vec(const void* in, const
   const int slot = r / units, u = r - slot * units;
   const int64_t base = t * heads * p.dh;
   const int c0 = INTER ? 16 * u : 8 * u, c1 = INTER ? c0 + 8 : c0 + (p.rot >> 1);
-  float s[8], c[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int i = 8 * u + k;
-    rope_sincos(pos[(int64_t)p.axis[i] * T + t], p.turn[i], sign, s[k], c[k]);
-  }
-  for (int h0 = slot; h0 < rot_heads; h0 += kRopeHeads * slots) {
-    Vec8<F32> a[kRopeHeads], b[kRopeHeads];
+  Vec8<F32> a[kRopeHeads], b[kRopeHeads];
+  auto load = [&](int h0) {
 #pragma unroll
     for (int q = 0; q < kRopeHeads; ++q) {
       const int h = h0 + q * slots;
@@ -95,6 +89,16 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_vec(const void* in, const
         b[q].load(in, base + h * p.dh + c1);
       }
     }
+  };
+  load(slot);  // in flight while the angles are computed
+  float s[8], c[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int i = 8 * u + k;
+    rope_sincos(pos[(int64_t)p.axis[i] * T + t], p.turn[i], sign, s[k], c[k]);
+  }
+  for (int h0 = slot; h0 < rot_heads; h0 += kRopeHeads * slots) {
+    if (h0 != slot) load(h0);
 #pragma unroll
     for (int q = 0; q < kRopeHeads; ++q) {
       const int h = h0 + q * slots;
