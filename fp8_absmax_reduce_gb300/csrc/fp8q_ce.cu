@@ -2,142 +2,516 @@
 //
 //   z = x W^T,  lse_t = log sum_v e^{z_tv},  loss_t = lse_t - z_{t,y_t} (0 for an ignored token);
 //   G = dloss_t (e^{z - lse_t} - 1[v = y_t]) (0 for an ignored token),  dX = G W,  dW = G^T x.
-// The vocabulary is walked in pieces; the backward computes each piece's logits again.  G is kept in
-// bf16, the tensor cores' operand type, as G / s with s = max_t |dloss_t|: a mean's one weight for
-// all tokens then leaves no rounding of its own in G's large entries (p - 1 near -1).  s joins the
-// products in fp32.  An ignored token's row of x is replaced by zero before dW = G^T x, so that a
-// padded row may hold anything (0 times a NaN would reach every row of dW).
+// The forward is one product whose epilogue keeps, of each 128-column piece of a row, the maximum and
+// the sum of exponentials below it; a second kernel joins them.  The backward walks the vocabulary
+// in pieces: the piece's logits again, turned into G in the epilogue, then its share of dX and its rows
+// of dW.  All products are bf16 on the tensor cores with fp32 sums, and bound by them.
+//
+// G is kept in bf16, the tensor cores' operand type, as G / s with s = max_t |dloss_t|: a mean's
+// one weight for all tokens then leaves no rounding of its own in G's large entries (p - 1 near -1).
+// s joins the products in fp32.  An ignored token's row of x is replaced by zero before dW = G^T x, so
+// that a padded row may hold anything (0 times a NaN would reach every row of dW).
 #include "fp8q_common.cuh"
 #include "fp8q_internal.h"
+
+#include <atomic>
+#include <mutex>
 
 namespace fp8q {
 
 namespace {
 
-// A target outside [0, V) that is not ignore_index is a mistake of the caller: recorded, and ignored.
-__device__ __forceinline__ int64_t ce_target(int64_t y, int64_t V, int64_t ignore, unsigned* status) {
-  if (y == ignore) return -1;
-  if (y < 0 || y >= V) {
-    atomicOr(status, kStatusBadTarget);
-    return -1;
-  }
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ce_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-__device__ __forceinline__ float ce_warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  return v;
-}
-__device__ __forceinline__ float ce_warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
+// ---------------------------------------------------------------------------
+// The product: two SMs per 256 x 256 tile (tcgen05.mma cta_group::2), persistent, warp-specialised.
+//
+// A pair of CTAs (a cluster of two) computes C[256, 256] += A[256, K] B[256, K]^T in steps of 64 of K: each
+// CTA loads its 128 rows of A and its 128 columns of B (32 KB a stage, where one SM with a
+// 128 x 256 tile would load 48 KB for the same work: the operand bytes that reach an SM are what
+// bounds the 128 x 256 kernel of the block's products), the even CTA issues the MMAs for both, and
+// each CTA's tensor memory receives its 128 rows.  Two accumulators (2 x 256 columns) let a tile's
+// epilogue run under the next tile's MMAs.
+//   warp 0      TMA producer of its CTA; both signal the even CTA's full barrier;
+//   warp 1      the even CTA's MMA issuer; its commits free the stage, and hand over the
+//               accumulator, in both CTAs;
+//   warp 2      tensor memory;
+//   warps 4-11  epilogue: warp w reads lanes 32 (w % 4) .., columns 128 (w / 4 - 1) ...
+// Every wait is bounded.  On expiry a CTA records the time-out and stops; its copies in flight, which
+// signal the other CTA, get kCopyDrainNs to land; the pair meets at a cluster barrier and frees its tensor memory.
+// ---------------------------------------------------------------------------
+constexpr int PM = 256, PN = 256, PK = 64;
+constexpr int kHalfTile = 128 * 128;  // bytes: 128 rows (or columns) x 64 bf16
+constexpr int kPairStage = 2 * kHalfTile;
+constexpr int kPairStages = 6;
+constexpr int kPairThreads = 384;
+constexpr int kPairStaging = 4096;  // per epilogue warp
+constexpr int kPairStagingOffset = kPairStages * kPairStage;
+constexpr int kPairBarOffset = kPairStagingOffset + 8 * kPairStaging;
+constexpr int kPairSmem = kPairBarOffset + 256 + 1024;
+static_assert(kPairSmem <= 232448, "shared memory per CTA");
+constexpr uint64_t kCopyDrainNs = 5000000ull;  // far beyond any copy in flight
 
-// One warp per row: joins a piece's logits into the running maximum, sum and target logit.
-__global__ void __launch_bounds__(256) k_ce_piece(const float* z, int64_t ldz, int64_t T, int v0, int n,
-                                                  const int64_t* targets, int64_t V, int64_t ignore, float* run_m,
-                                                  float* run_s, float* run_y, float* loss, float* lse, int last,
-                                                  unsigned* status) {
-  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (t >= T) return;
-  const float* row = z + t * ldz;
-  float m = -INFINITY;
-  for (int j = lane; j < n; j += 32) m = fmaxf(m, row[j]);
-  m = ce_warp_max(m);
-  float s = 0.0f;
-  for (int j = lane; j < n; j += 32) s += expf(row[j] - m);
-  s = ce_warp_sum(s);
-  if (lane == 0) {
-    const int64_t y = ce_target(targets[t], V, ignore, status);
-    float zy = v0 ? run_y[t] : 0.0f;
-    if (y >= v0 && y < v0 + n) zy = row[y - v0];
-    if (v0) {
-      const float m0 = run_m[t], mm = fmaxf(m0, m);
-      s = run_s[t] * expf(m0 - mm) + s * expf(m - mm);
-      m = mm;
-    }
-    run_m[t] = m;
-    run_s[t] = s;
-    run_y[t] = zy;
-    if (last) {
-      const float l = m + logf(s);
-      lse[t] = l;
-      loss[t] = y >= 0 ? l - zy : 0.0f;
+enum PairMode {
+  kPairLse = 0,   // per row and 128 columns: log2-domain maximum and sum; the target's logit
+  kPairGrad = 1,  // G / s as bf16
+  kPairDx = 2,    // dX: fp32 store, fp32 add or bf16 of the joined sum
+  kPairDw = 3,    // dW: bf16 or fp32
+};
+enum PairOut { kOutF32Store = 0, kOutF32Add = 1, kOutBf16 = 2, kOutBf16Join = 3 };
+
+struct PairArgs {
+  int M, N, K;
+  int m_tiles, n_tiles, num_tiles, k_blocks, group;
+  uint32_t idesc;
+  int out;                  // PairOut
+  const float* scale;       // kPairDx (bf16 outputs), kPairDw: s
+  float* acc;               // kOutBf16Join: the sum so far [M, N]
+  int v0;                   // kPairGrad: the piece's first column
+  const int64_t* targets;   // kPairLse
+  float2* part;             // kPairLse: [2 n_tiles][M] (maximum log2e, sum)
+  float* zy;                // kPairLse: [M] the target's logit
+  const int2* row_y;        // kPairGrad: [M] {target or -1, -}
+  const float2* row_w;      // kPairGrad: [M] {lse log2e, dloss / s}
+  unsigned* status;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A 2D tile into this CTA's shared memory; the bytes are counted on `bar`, a barrier of either CTA.
+__device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* tm, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+      "[%2];" ::"r"(smem_addr(dst)),
+      "l"(tm), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on the barrier at this offset in the CTAs of `mask` once the MMAs issued so far are done.
+__device__ __forceinline__ void pair_commit(uint64_t* bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_addr(bar)),
+      "h"(mask)
+      : "memory");
+}
+__device__ __forceinline__ void remote_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The wait of a barrier that the other CTA (or its MMAs) arrives on: acquire at cluster scope.
+__device__ __forceinline__ bool pair_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (pair_try(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (pair_try(bar, parity)) return true;
+    if ((it & 15) == 0) {
+      if (*abort) return false;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
     }
   }
 }
 
-// s = max |dloss| over the tokens that count (1 where that is 0 or not finite); scale = {s, 1}.
-__global__ void __launch_bounds__(1024) k_ce_scale(const float* dloss, const int64_t* targets, int64_t T, int64_t V,
-                                                   int64_t ignore, float* scale, unsigned* status) {
+__device__ __forceinline__ void out_store_2d(const CUtensorMap* tm, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(tm), "r"(src), "r"(x),
+               "r"(y)
+               : "memory");
+}
+// fp32 addition in global memory.  Each element is added to once per launch, so the order is fixed.
+__device__ __forceinline__ void out_add_2d(const CUtensorMap* tm, uint32_t src, int x, int y) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(tm),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void out_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// A warp's 32 x 32 block of a tile on its way out: staged in the layout of the tensor map's swizzle
+// (64 bytes for bf16, 128 for fp32) and stored by lane 0.  bf16 blocks alternate between the buffer's halves.
+struct PairStager {
+  uint32_t buf;
+  int lane, flip = 0;
+  __device__ __forceinline__ PairStager(uint32_t b, int l) : buf(b), lane(l) {}
+  __device__ __forceinline__ void bf16(const CUtensorMap* tm, const float (&v)[32], int x, int y) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    __syncwarp();
+    const uint32_t b = buf + 2048 * flip;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      sts_v4(b + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), pack_bf16x2(v[8 * q], v[8 * q + 1]),
+             pack_bf16x2(v[8 * q + 2], v[8 * q + 3]), pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
+             pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+      out_store_2d(tm, b, x, y);
+      out_commit();
+    }
+    flip ^= 1;
+  }
+  __device__ __forceinline__ void f32(const CUtensorMap* tm, const float (&v)[32], int x, int y, bool add) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      sts_v4(buf + lane * 128 + ((q ^ (lane & 7)) << 4), __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+             __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+      if (add) out_add_2d(tm, buf, x, y);
+      else out_store_2d(tm, buf, x, y);
+      out_commit();
+    }
+  }
+};
+
+// Tile -> (M tile, N tile) in groups of p.group M tiles: all N tiles of a group, M fastest inside it.
+__device__ __forceinline__ void pair_coords(int tile, const PairArgs& p, int& mb, int& nb) {
+  const int span = p.group * p.n_tiles, grp = tile / span, first = grp * p.group;
+  const int gm = min(p.group, p.m_tiles - first), local = tile - grp * span;
+  mb = first + local % gm;
+  nb = local / gm;
+}
+
+template <int A_MN, int B_MN, int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    k_ce_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+              const __grid_constant__ CUtensorMap tmC, const PairArgs p) {
+  extern __shared__ uint8_t pair_smem[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pair_smem) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairBarOffset);
+  uint64_t* empty = full + kPairStages;
+  uint64_t* tfull = empty + kPairStages;  // [2]
+  uint64_t* tempty = tfull + 2;           // [2]
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int first = (int)(blockIdx.x >> 1), step = (int)(gridDim.x >> 1);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int a = 0; a < 2; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], 16); }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    if (MODE != kPairLse) tma_prefetch_desc(&tmC);
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers exist, both have their tensor memory
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer ----------------
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = first; tile < p.num_tiles && ok; tile += step) {
+        int mb, nb;
+        pair_coords(tile, p, mb, nb);
+        const int m0 = mb * PM + 128 * rank, n0 = nb * PN + 128 * rank;
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          if (!pair_wait(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
+          uint8_t* sA = smem + stage * kPairStage;
+          uint8_t* sB = sA + kHalfTile;
+          const uint32_t bar = map_to_rank(smem_addr(&full[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kPairStage);
+          const int k0 = kb * PK;
+          if (A_MN) {  // two 64-element-wide boxes of 64 rows of K
+            pair_load_2d(sA, &tmA, bar, m0, k0);
+            pair_load_2d(sA + kHalfTile / 2, &tmA, bar, m0 + 64, k0);
+          } else {
+            pair_load_2d(sA, &tmA, bar, k0, m0);
+          }
+          if (B_MN) {
+            pair_load_2d(sB, &tmB, bar, n0, k0);
+            pair_load_2d(sB + kHalfTile / 2, &tmB, bar, n0 + 64, k0);
+          } else {
+            pair_load_2d(sB, &tmB, bar, k0, n0);
+          }
+          if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok) {
+        atomicOr(p.status, kStatusTimeout);
+        *abort_flag = 1;
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < kCopyDrainNs) {}
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ---------------- MMA issuer ----------------
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int tile = first; tile < p.num_tiles && ok; tile += step) {
+        if (!pair_wait(&tempty[acc], acc_phase ^ 1u, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(acc * PN);
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          if (!pair_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sA = smem_addr(smem + stage * kPairStage), sB = sA + kHalfTile;
+#pragma unroll
+          for (int kk = 0; kk < PK / 16; ++kk) {
+            // K-major: 32 bytes further inside the 128-byte swizzle row; MN-major: 16 rows of K further,
+            // the second 64-element block of MN 8 KB on
+            const uint64_t ad = A_MN ? smem_desc_sw128(sA + kk * 2048, kHalfTile / 2, 1024) : smem_desc_sw128(sA + kk * 32, 16, 1024);
+            const uint64_t bd = B_MN ? smem_desc_sw128(sB + kk * 2048, kHalfTile / 2, 1024) : smem_desc_sw128(sB + kk * 32, 16, 1024);
+            pair_mma(d, ad, bd, p.idesc, (kb | kk) != 0 ? 1u : 0u);
+          }
+          pair_commit(&empty[stage], 3);
+          if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        pair_commit(&tfull[acc], 3);
+        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+      }
+      if (!ok) {
+        atomicOr(p.status, kStatusTimeout);
+        *abort_flag = 1;
+      }
+      // every MMA issued is done before tensor memory is released
+      pair_commit(drain, 1);
+      int dummy = 0;
+      pair_wait(drain, 0, &dummy);
+    }
+  } else if (warp >= 4) {
+    // ---------------- epilogue ----------------
+    const int sub = warp & 3, half = (warp - 4) >> 2;
+    PairStager out(smem_addr(smem + kPairStagingOffset + (warp - 4) * kPairStaging), lane);
+    const uint32_t tempty0 = map_to_rank(smem_addr(tempty), 0);
+    const float alpha = (MODE == kPairDx || MODE == kPairDw) ? *p.scale : 1.0f;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int tile = first; tile < p.num_tiles; tile += step) {
+      int mb, nb;
+      pair_coords(tile, p, mb, nb);
+      const int row0 = mb * PM + 128 * rank + sub * 32, row = row0 + lane;
+      const bool row_ok = row < p.M, warp_ok = row0 < p.M;
+      const int col0 = nb * PN + 128 * half;
+      int y = -1;              // kPairLse, kPairGrad: the target
+      float lse2 = 0.0f, w = 0.0f;
+      if (MODE == kPairLse && row_ok) {
+        const int64_t t = p.targets[row];
+        if (t >= 0 && t < p.N) y = (int)t;
+      }
+      if (MODE == kPairGrad && row_ok) {
+        y = p.row_y[row].x;
+        const float2 rw = p.row_w[row];
+        lse2 = rw.x;
+        w = rw.y;
+      }
+      int full_ok = 0;
+      if (lane == 0) full_ok = pair_wait(&tfull[acc], acc_phase, abort_flag) ? 1 : 0;
+      if (!__shfl_sync(0xFFFFFFFFu, full_ok, 0)) {
+        atomicOr(p.status, kStatusTimeout);
+        *abort_flag = 1;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t tbase = tmem_base + (uint32_t)(acc * PN + 128 * half) + ((uint32_t)(sub * 32) << 16);
+      float m2 = -INFINITY, s = 0.0f;  // kPairLse: the largest logit in log2 units, sum of 2^(z2 - m2)
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        const int col = col0 + c * 32, ncol = min(32, p.N - col);
+        if (!warp_ok || ncol <= 0) break;
+        __syncwarp();
+        uint32_t a[32];
+        tmem_ld32(tbase + c * 32, a);
+        if (MODE == kPairLse) {
+          if (ncol < 32)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j >= ncol) a[j] = 0xFF800000u;
+          if ((unsigned)(y - col) < 32u) {
+            float zy = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (y - col == j) zy = __uint_as_float(a[j]);
+            p.zy[row] = zy;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(a[j]));
+          const float cm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kLog2e;
+          const float mn = fmaxf(m2, cm);
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[j & 3] += ce_exp2(fmaf(__uint_as_float(a[j]), kLog2e, -mn));
+          s = s * ce_exp2(m2 - mn) + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+          m2 = mn;
+        } else {
+          float v[32];
+          if (MODE == kPairGrad) {
+            const int yc = y - p.v0 - col;
+            const bool keep = y >= 0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              float q = ce_exp2(fmaf(__uint_as_float(a[j]), kLog2e, -lse2));
+              if (j == yc) q -= 1.0f;
+              v[j] = keep ? w * q : 0.0f;
+            }
+            out.bf16(&tmC, v, col, row0);
+          } else if (MODE == kPairDx && p.out == kOutBf16Join) {
+            const float* old = p.acc + (int64_t)row * p.N + col;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (row_ok && 4 * q < ncol) o = *reinterpret_cast<const float4*>(old + 4 * q);
+              v[4 * q] = alpha * (__uint_as_float(a[4 * q]) + o.x);
+              v[4 * q + 1] = alpha * (__uint_as_float(a[4 * q + 1]) + o.y);
+              v[4 * q + 2] = alpha * (__uint_as_float(a[4 * q + 2]) + o.z);
+              v[4 * q + 3] = alpha * (__uint_as_float(a[4 * q + 3]) + o.w);
+            }
+            out.bf16(&tmC, v, col, row0);
+          } else if (p.out == kOutBf16) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = alpha * __uint_as_float(a[j]);
+            out.bf16(&tmC, v, col, row0);
+          } else {
+            const float f = MODE == kPairDw ? alpha : 1.0f;  // dX's sum is scaled when it is complete
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = f * __uint_as_float(a[j]);
+            out.f32(&tmC, v, col, row0, p.out == kOutF32Add);
+          }
+        }
+      }
+      if (MODE == kPairLse && row_ok && col0 < p.N) p.part[(int64_t)(2 * nb + half) * p.M + row] = make_float2(m2, s);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) remote_arrive(tempty0 + 8 * acc);
+      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+    }
+    if (MODE != kPairLse && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  cluster_sync_all();  // neither CTA's memory or barriers are in use by the other any more
+  tc_fence_after();
+  if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// The small kernels around it
+// ---------------------------------------------------------------------------
+// Joins the pieces of a row: 32 rows a block, warp w takes pieces w, w + 8, ..., lane = row; then the
+// warps' pairs.  lse = ln 2 (m2 + log2 s).  A target outside [0, V) that is not ignore_index is a mistake of
+// the caller: recorded, and ignored.
+__global__ void __launch_bounds__(256) k_ce_finish(const float2* __restrict__ part, int pieces, int64_t T,
+                                                   const int64_t* __restrict__ targets, int64_t V, int64_t ignore,
+                                                   const float* __restrict__ zy, float* __restrict__ loss,
+                                                   float* __restrict__ lse, unsigned* status) {
+  __shared__ float2 sh[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * 32 + lane;
+  float m = -INFINITY, s = 0.0f;
+  bool any = false;
+  auto join = [&](float2 q) {
+    if (!any) { m = q.x; s = q.y; any = true; return; }
+    const float mn = fmaxf(m, q.x);
+    s = s * ce_exp2(m - mn) + q.y * ce_exp2(q.x - mn);
+    m = mn;
+  };
+  if (t < T)
+#pragma unroll 4
+    for (int i = warp; i < pieces; i += 8) join(part[(int64_t)i * T + t]);
+  sh[warp][lane] = make_float2(m, s);
+  __syncthreads();
+  if (warp != 0 || t >= T) return;
+  for (int w = 1; w < 8 && w < pieces; ++w) join(sh[w][lane]);
+  const float l = kLn2 * (m + log2f(s));
+  lse[t] = l;
+  const int64_t y = targets[t];
+  const bool in = y >= 0 && y < V;
+  if (y != ignore && !in) atomicOr(status, kStatusBadTarget);
+  loss[t] = y != ignore && in ? l - zy[t] : 0.0f;
+}
+
+// s = max |dloss| over the tokens that count (1 where that is 0 or not finite).
+__global__ void __launch_bounds__(1024) k_ce_scale(const float* __restrict__ dloss, const int64_t* __restrict__ targets,
+                                                   int64_t T, int64_t V, int64_t ignore, float* scale, unsigned* status) {
   __shared__ uint32_t red[32];
   uint32_t m = 0;
-  for (int64_t t = threadIdx.x; t < T; t += blockDim.x)
-    if (ce_target(targets[t], V, ignore, status) >= 0) m = max(m, abs_bits(dloss[t]));
+  for (int64_t t = threadIdx.x; t < T; t += blockDim.x) {
+    const int64_t y = targets[t];
+    if (y == ignore) continue;
+    if (y < 0 || y >= V) atomicOr(status, kStatusBadTarget);
+    else m = max(m, abs_bits(dloss[t]));
+  }
   m = block_max_u32(m, red);
-  if (threadIdx.x == 0) {
-    scale[0] = (m == 0 || m >= 0x7F800000u) ? 1.0f : __uint_as_float(m);
-    scale[1] = 1.0f;
-  }
+  if (threadIdx.x == 0) *scale = (m == 0 || m >= 0x7F800000u) ? 1.0f : __uint_as_float(m);
 }
 
-// x with the rows of ignored tokens zeroed.
-__global__ void __launch_bounds__(256) k_ce_mask_x(const uint16_t* x, const int64_t* targets, int64_t T, int d, int64_t V,
-                                                   int64_t ignore, uint16_t* xz) {
-  const int64_t n8 = T * d / 8;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n8; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t y = targets[i * 8 / d];
+// Per token: its target (-1 where it is ignored), {lse log2e, dloss / s}, and x with ignored rows zeroed.
+__global__ void __launch_bounds__(256) k_ce_rows(const uint16_t* __restrict__ x, const int64_t* __restrict__ targets,
+                                                 const float* __restrict__ lse, const float* __restrict__ dloss, int64_t T,
+                                                 int d, int64_t V, int64_t ignore, const float* __restrict__ scale,
+                                                 int2* __restrict__ row_y, float2* __restrict__ row_w,
+                                                 uint16_t* __restrict__ xz) {
+  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+    const int64_t y = targets[t];
     const bool keep = y != ignore && y >= 0 && y < V;
-    st_v4(xz + 8 * i, keep ? ld_v4(x + 8 * i) : make_uint4(0, 0, 0, 0));
+    if (threadIdx.x == 0) {
+      row_y[t] = make_int2(keep ? (int)y : -1, 0);
+      row_w[t] = make_float2(lse[t] * kLog2e, keep ? dloss[t] / *scale : 0.0f);
+    }
+    const uint16_t* src = x + t * d;
+    uint16_t* dst = xz + t * d;
+    for (int j = 8 * threadIdx.x; j < d; j += 8 * blockDim.x) st_v4(dst + j, keep ? ld_v4(src + j) : make_uint4(0, 0, 0, 0));
   }
-}
-
-__global__ void __launch_bounds__(256) k_ce_grad(const float* z, int64_t ldz, int64_t T, int v0, int n,
-                                                 const int64_t* targets, int64_t V, int64_t ignore, const float* lse,
-                                                 const float* dloss, const float* scale, uint16_t* G, int64_t ldg) {
-  const int64_t t = blockIdx.x;
-  const int64_t y = targets[t];
-  const bool keep = y != ignore && y >= 0 && y < V;
-  const float w = keep ? dloss[t] / scale[0] : 0.0f, l = lse[t];
-  for (int j = threadIdx.x; j < n; j += blockDim.x) {
-    float p = expf(z[t * ldz + j] - l);
-    if (v0 + j == y) p -= 1.0f;
-    reinterpret_cast<__nv_bfloat16*>(G)[t * ldg + j] = __float2bfloat16_rn(keep ? w * p : 0.0f);
-  }
-}
-
-__global__ void __launch_bounds__(256) k_ce_join(float* acc, const float* part, int64_t n, int first, uint16_t* out) {
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const float v = first ? part[i] : acc[i] + part[i];
-    acc[i] = v;
-    if (out) reinterpret_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
-  }
-}
-
-constexpr int64_t kPiece = 8192;
-
-GemmProblem ce_gemm(int a_mn, int b_mn, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
-                    int64_t ldb, int64_t b_cols, int out_f32, void* C, int64_t ldc) {
-  GemmProblem g{};
-  g.op16 = 1;
-  g.a_mn = a_mn;
-  g.b_mn = b_mn;
-  g.M = (int)M;
-  g.N = (int)N;
-  g.K = (int)K;
-  g.A = static_cast<const uint8_t*>(A);
-  g.lda = lda;
-  g.B = static_cast<const uint8_t*>(B);
-  g.ldb = ldb;
-  g.b_cols = b_cols;
-  g.epi = kEpiStore;
-  g.out_f32 = out_f32;
-  g.C = C;
-  g.ldc = ldc;
-  return g;
 }
 
 cudaError_t launched(const Launch& L) {
@@ -145,8 +519,112 @@ cudaError_t launched(const Launch& L) {
   return cudaGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encode_fn() {
+  static EncodeFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(ptr);
+  });
+  return fn;
+}
+bool make_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int es, int box_cols, int box_rows,
+              CUtensorMapSwizzle sw) {
+  EncodeFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(ld * es)};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+  const cuuint32_t one[2] = {1, 1};
+  return enc(m, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
+             dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// op(A) [M, K] op(B) [N, K]^T: a K-major operand is stored [M or N, K], an MN-major one [K, M or N].
+struct PairProblem {
+  int64_t M, N, K;
+  const void* A;
+  int64_t lda;
+  const void* B;
+  int64_t ldb;
+  void* C;
+  int64_t ldc;
+};
+
+// The M tiles of a rasterisation group: every one of them while A fits in L2 beside the streamed B, one
+// (N fastest) while B does instead, else 2048 rows.
+int pair_group(const PairProblem& q, int m_tiles) {
+  constexpr int64_t kResident = 48ll << 20;
+  const int64_t a = 2 * q.M * q.K, b = 2 * q.N * q.K;
+  if (a <= b && a <= kResident) return m_tiles;
+  if (b < a && b <= kResident) return 1;
+  return 2048 / PM;
+}
+
+template <int A_MN, int B_MN, int MODE>
+cudaError_t launch_pair(const PairProblem& q, PairArgs a, const Launch& L) {
+  a.M = (int)q.M;
+  a.N = (int)q.N;
+  a.K = (int)q.K;
+  a.m_tiles = (a.M + PM - 1) / PM;
+  a.n_tiles = (a.N + PN - 1) / PN;
+  a.k_blocks = (a.K + PK - 1) / PK;
+  if ((int64_t)a.m_tiles * a.n_tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  a.num_tiles = a.m_tiles * a.n_tiles;
+  a.group = pair_group(q, a.m_tiles);
+  // fp32 sums, bf16 operands and their majors, N / 8 and M / 16 of the pair's tile
+  a.idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
+            ((uint32_t)(PN >> 3) << 17) | ((uint32_t)(PM >> 4) << 24);
+  a.status = L.status;
+  CUtensorMap ta, tb, tc;
+  bool ok = A_MN ? make_map(&ta, q.A, q.M, q.K, q.lda, 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)
+                 : make_map(&ta, q.A, q.K, q.M, q.lda, 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+  ok = ok && (B_MN ? make_map(&tb, q.B, q.N, q.K, q.ldb, 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)
+                   : make_map(&tb, q.B, q.K, q.N, q.ldb, 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B));
+  tc = ta;
+  if (MODE != kPairLse) {
+    const bool f32 = MODE != kPairGrad && (a.out == kOutF32Store || a.out == kOutF32Add);
+    ok = ok && make_map(&tc, q.C, q.N, q.M, q.ldc, f32 ? 4 : 2, 32, 32,
+                        f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  static std::atomic<uint64_t> configured{0};  // a bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!(configured.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(k_ce_gemm<A_MN, B_MN, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(1ull << dev);
+  }
+  const int pairs = L.num_sms / 2 < a.num_tiles ? L.num_sms / 2 : a.num_tiles;
+  k_ce_gemm<A_MN, B_MN, MODE><<<2 * pairs, kPairThreads, kPairSmem, L.stream>>>(ta, tb, tc, a);
+  return launched(L);
+}
+
+// Columns of a backward piece: G of all tokens in about 256 MB, in whole tiles, the pieces alike.
+int64_t ce_piece(int64_t T, int64_t V) {
+  constexpr int64_t kPieceBytes = 256ll << 20;
+  int64_t most = kPieceBytes / (2 * T) / PN * PN;
+  if (most < 4 * PN) most = 4 * PN;
+  const int64_t n = (V + most - 1) / most;
+  return ((V + n - 1) / n + PN - 1) / PN * PN;
+}
+
 struct CeWs {
-  float *z, *m, *s, *y, *part, *acc, *scale;
+  float2 *part, *row_w;
+  float *zy, *acc, *scale;
+  int2* row_y;
   uint16_t *G, *xz;
 };
 size_t ce_layout(int64_t T, int64_t d, int64_t V, bool bwd, uint8_t* base, CeWs* w) {
@@ -156,19 +634,18 @@ size_t ce_layout(int64_t T, int64_t d, int64_t V, bool bwd, uint8_t* base, CeWs*
     off += ((size_t)bytes + 255) & ~size_t(255);
     return p;
   };
-  const int64_t ld = V < kPiece ? (V + 7) / 8 * 8 : kPiece;
   CeWs t{};
-  t.z = (float*)take(T * ld * 4);
   if (bwd) {
-    t.G = (uint16_t*)take(T * ld * 2);
+    const int64_t piece = ce_piece(T, V);
+    t.G = (uint16_t*)take(T * piece * 2);
     t.xz = (uint16_t*)take(T * d * 2);
-    t.part = (float*)take(T * d * 4);
-    t.acc = (float*)take(T * d * 4);
-    t.scale = (float*)take(8);
+    if (piece < V) t.acc = (float*)take(T * d * 4);
+    t.row_y = (int2*)take(T * 8);
+    t.row_w = (float2*)take(T * 8);
+    t.scale = (float*)take(4);
   } else {
-    t.m = (float*)take(T * 4);
-    t.s = (float*)take(T * 4);
-    t.y = (float*)take(T * 4);
+    t.part = (float2*)take(2 * ((V + PN - 1) / PN) * T * 8);
+    t.zy = (float*)take(T * 4);
   }
   if (w) *w = t;
   return off;
@@ -182,17 +659,15 @@ cudaError_t launch_ce_fwd(const uint16_t* x, const uint16_t* W, const int64_t* t
                           int64_t ignore, float* loss, float* lse, void* ws, const Launch& L) {
   CeWs w;
   ce_layout(T, d, V, false, static_cast<uint8_t*>(ws), &w);
-  const int64_t ld = V < kPiece ? (V + 7) / 8 * 8 : kPiece;
-  int P = 0;
-  for (int64_t v0 = 0; v0 < V; v0 += kPiece) {
-    const int n = (int)(V - v0 < kPiece ? V - v0 : kPiece);
-    cudaError_t e = launch_gemm(ce_gemm(0, 0, T, n, d, x, d, W + v0 * d, d, n, 1, w.z, ld), &P, L);
-    if (e != cudaSuccess) return e;
-    k_ce_piece<<<(unsigned)((T + 7) / 8), 256, 0, L.stream>>>(w.z, ld, T, (int)v0, n, targets, V, ignore, w.m, w.s, w.y,
-                                                              loss, lse, v0 + n == V, L.status);
-    if ((e = launched(L)) != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  PairArgs a{};
+  a.targets = targets;
+  a.part = w.part;
+  a.zy = w.zy;
+  cudaError_t e = launch_pair<0, 0, kPairLse>(PairProblem{T, V, d, x, d, W, d, nullptr, 0}, a, L);
+  if (e != cudaSuccess) return e;
+  const int pieces = (int)((V + 127) / 128);
+  k_ce_finish<<<(unsigned)((T + 31) / 32), 256, 0, L.stream>>>(w.part, pieces, T, targets, V, ignore, w.zy, loss, lse, L.status);
+  return launched(L);
 }
 
 cudaError_t launch_ce_bwd(const uint16_t* x, const uint16_t* W, const int64_t* targets, const float* lse,
@@ -200,31 +675,36 @@ cudaError_t launch_ce_bwd(const uint16_t* x, const uint16_t* W, const int64_t* t
                           int dw_f32, void* ws, const Launch& L) {
   CeWs w;
   ce_layout(T, d, V, true, static_cast<uint8_t*>(ws), &w);
-  const int64_t ld = V < kPiece ? (V + 7) / 8 * 8 : kPiece;
-  int P = 0;
+  const int64_t piece = ce_piece(T, V);
   cudaError_t e;
   k_ce_scale<<<1, 1024, 0, L.stream>>>(dloss, targets, T, V, ignore, w.scale, L.status);
   if ((e = launched(L)) != cudaSuccess) return e;
-  k_ce_mask_x<<<L.num_sms * 4, 256, 0, L.stream>>>(x, targets, T, d, V, ignore, w.xz);
+  k_ce_rows<<<(unsigned)(T < 8 * L.num_sms ? T : 8 * L.num_sms), 256, 0, L.stream>>>(x, targets, lse, dloss, T, d, V, ignore,
+                                                                                 w.scale, w.row_y, w.row_w, w.xz);
   if ((e = launched(L)) != cudaSuccess) return e;
-  for (int64_t v0 = 0; v0 < V; v0 += kPiece) {
-    const int n = (int)(V - v0 < kPiece ? V - v0 : kPiece);
-    if ((e = launch_gemm(ce_gemm(0, 0, T, n, d, x, d, W + v0 * d, d, n, 1, w.z, ld), &P, L)) != cudaSuccess) return e;
-    k_ce_grad<<<(unsigned)T, 256, 0, L.stream>>>(w.z, ld, T, (int)v0, n, targets, V, ignore, lse, dloss, w.scale, w.G, ld);
-    if ((e = launched(L)) != cudaSuccess) return e;
-    // dX += s G W[piece]
-    GemmProblem gx = ce_gemm(0, 1, T, d, n, w.G, ld, W + v0 * d, d, d, 1, w.part, d);
-    gx.sinvA = w.scale;
-    gx.sinvB = w.scale + 1;
-    if ((e = launch_gemm(gx, &P, L)) != cudaSuccess) return e;
-    k_ce_join<<<L.num_sms * 4, 256, 0, L.stream>>>(w.acc, w.part, T * d, v0 == 0, v0 + n == V ? dX : nullptr);
-    if ((e = launched(L)) != cudaSuccess) return e;
-    // dW[piece] = s G^T x
+  for (int64_t v0 = 0; v0 < V; v0 += piece) {
+    const int64_t n = V - v0 < piece ? V - v0 : piece;
+    const bool first = v0 == 0, last = v0 + n == V;
+    PairArgs a{};
+    a.v0 = (int)v0;
+    a.row_y = w.row_y;
+    a.row_w = w.row_w;
+    e = launch_pair<0, 0, kPairGrad>(PairProblem{T, n, d, x, d, W + v0 * d, d, w.G, piece}, a, L);
+    if (e != cudaSuccess) return e;
+    // dX (+)= G W[piece]
+    PairArgs ax{};
+    ax.scale = w.scale;
+    ax.acc = w.acc;
+    ax.out = first ? (last ? kOutBf16 : kOutF32Store) : (last ? kOutBf16Join : kOutF32Add);
+    e = launch_pair<0, 1, kPairDx>(PairProblem{T, d, n, w.G, piece, W + v0 * d, d, last ? (void*)dX : (void*)w.acc, d}, ax, L);
+    if (e != cudaSuccess) return e;
+    // dW[piece] = G^T x
+    PairArgs aw{};
+    aw.scale = w.scale;
+    aw.out = dw_f32 ? kOutF32Store : kOutBf16;
     void* dst = dw_f32 ? (void*)(static_cast<float*>(dW) + v0 * d) : (void*)(static_cast<uint16_t*>(dW) + v0 * d);
-    GemmProblem gw = ce_gemm(1, 1, n, d, T, w.G, ld, w.xz, d, d, dw_f32, dst, d);
-    gw.sinvA = w.scale;
-    gw.sinvB = w.scale + 1;
-    if ((e = launch_gemm(gw, &P, L)) != cudaSuccess) return e;
+    e = launch_pair<1, 1, kPairDw>(PairProblem{n, d, T, w.G, piece, w.xz, d, dst, d}, aw, L);
+    if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }

@@ -13,7 +13,6 @@ namespace fp8q {
 
 constexpr unsigned kStatusNonfinite = 0x1u;
 constexpr unsigned kStatusTimeout = 0x2u;
-constexpr unsigned kStatusBadTarget = 0x4u;
 
 // --------------------------------------------------------------------------
 // Numerics

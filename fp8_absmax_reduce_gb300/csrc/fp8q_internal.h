@@ -95,6 +95,7 @@ cudaError_t launch_rope(const void* in, int f32, const RopePlan& plan, const int
                         int n_kv_heads, int inverse, void* out, const Launch& L);
 
 // Softmax cross entropy of the linear head z = x W^T (x [T, d], W [V, d] bf16).
+constexpr unsigned kStatusBadTarget = 0x4u;
 size_t ce_workspace_bytes(int64_t T, int64_t d, int64_t V, int bwd);
 cudaError_t launch_ce_fwd(const uint16_t* x, const uint16_t* W, const int64_t* targets, int64_t T, int d, int64_t V,
                           int64_t ignore, float* loss, float* lse, void* ws, const Launch& L);
