@@ -178,8 +178,10 @@ def _ptr(t):
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    # the raw handle: a torch.cuda.Stream object costs 3 us to make, as long as a small kernel runs
+    if stream is None:
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _check(name: str, rc: int):
@@ -370,21 +372,35 @@ def attention_bwd(qkv: torch.Tensor, att: torch.Tensor, lse: torch.Tensor, d_att
 def _need(name: str, t, shape, *dtypes):
     """A tensor argument of a given shape (None: any size in that place) and one of the given types,
     dense, on the current CUDA device (the library launches there)."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_cuda and t.is_contiguous()
+            and t.get_device() == torch._C._cuda_getDevice()
+            and (t.shape == shape or (None in shape and t.dim() == len(shape)
+                                      and all(want is None or have == want for have, want in zip(t.shape, shape))))):
+        return t
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
-    if t.dim() != len(shape) or any(want is not None and have != want for have, want in zip(t.shape, shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple('any' if s is None else s for s in shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple('any' if s is None else s for s in shape)}")
 
 
 def _out(name: str, t, shape, dtype, like):
     return torch.empty(shape, dtype=dtype, device=like.device) if t is None else _need(name, t, shape, dtype)
+
+
+def _scratch(nbytes: int, like, ws):
+    """The workspace's address and bytes: the caller's, or a new one."""
+    if ws is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    elif not (ws.is_cuda and ws.is_contiguous() and ws.get_device() == like.get_device()):
+        raise ValueError("the workspace must be a contiguous tensor on the inputs' device")
+    elif ws.numel() * ws.element_size() < nbytes:
+        raise ValueError("workspace too small")
+    return ws
 
 
 @dataclasses.dataclass(frozen=True)
@@ -440,8 +456,8 @@ def _rope_call(name, qkv, pos, rope, n_heads, n_kv_heads, out, stream):
     T = qkv.shape[0]
     _need("pos", pos, (T,) if rope.n_axes == 1 and pos.dim() == 1 else (rope.n_axes, T), torch.int32)
     out = _out("out", out, qkv.shape, qkv.dtype, qkv)
-    _check(name, getattr(lib, name)(_ptr(qkv), _dtype_code(qkv), T, n_heads, n_kv_heads, ctypes.byref(rope._struct),
-                                    _ptr(pos), _ptr(out), _stream(stream)))
+    _check(name, getattr(lib, name)(qkv.data_ptr(), _dtype_code(qkv), T, n_heads, n_kv_heads, ctypes.byref(rope._struct),
+                                    pos.data_ptr(), out.data_ptr(), _stream(stream)))
     return out
 
 
@@ -470,8 +486,8 @@ def layernorm_fwd(x: torch.Tensor, g: torch.Tensor, b: torch.Tensor | None = Non
     y = _out("y", y, (T, d), x.dtype, x)
     mean = _out("mean", mean, (T,), torch.float32, x)
     rstd = _out("rstd", rstd, (T,), torch.float32, x)
-    _check("layernorm_fwd", lib.layernorm_fwd(_ptr(x), _dtype_code(x), _ptr(g), _ptr(b), T, d, eps, _ptr(y), _ptr(mean),
-                                              _ptr(rstd), _stream(stream)))
+    _check("layernorm_fwd", lib.layernorm_fwd(x.data_ptr(), _dtype_code(x), g.data_ptr(), None if b is None else b.data_ptr(), T, d, eps, y.data_ptr(), mean.data_ptr(),
+                                              rstd.data_ptr(), _stream(stream)))
     return y, mean, rstd
 
 
@@ -495,9 +511,9 @@ def layernorm_bwd(dY: torch.Tensor, x: torch.Tensor, g: torch.Tensor, mean: torc
     dg = _out("dg", dg, (d,), torch.float32, x)
     db = _out("db", db, (d,), torch.float32, x)
     nb = lib.layernorm_bwd_workspace_size(T, d)
-    w = _ws(nb, x.device, ws)
-    _check("layernorm_bwd", lib.layernorm_bwd(_ptr(dY), _ptr(x), _dtype_code(x), _ptr(g), _ptr(mean), _ptr(rstd),
-                                              _ptr(dres), T, d, _ptr(dX), _ptr(dg), _ptr(db), _ptr(w), nb,
+    w = _scratch(nb, x, ws)
+    _check("layernorm_bwd", lib.layernorm_bwd(dY.data_ptr(), x.data_ptr(), _dtype_code(x), g.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                              None if dres is None else dres.data_ptr(), T, d, dX.data_ptr(), dg.data_ptr(), db.data_ptr(), w.data_ptr(), nb,
                                               _stream(stream)))
     return dX, dg, db
 
@@ -526,10 +542,10 @@ def linear_cross_entropy_fwd(x: torch.Tensor, W: torch.Tensor, targets: torch.Te
     loss = _out("loss", loss, (T,), torch.float32, x)
     lse = _out("lse", lse, (T,), torch.float32, x)
     nb = lib.linear_cross_entropy_fwd_workspace_size(T, d, V)
-    w = _ws(nb, x.device, ws)
+    w = _scratch(nb, x, ws)
     _check("linear_cross_entropy_fwd",
-           lib.linear_cross_entropy_fwd(_ptr(x), _ptr(W), _ptr(targets), T, d, V, ignore_index, _ptr(loss), _ptr(lse),
-                                        _ptr(w), nb, _stream(stream)))
+           lib.linear_cross_entropy_fwd(x.data_ptr(), W.data_ptr(), targets.data_ptr(), T, d, V, ignore_index, loss.data_ptr(), lse.data_ptr(),
+                                        w.data_ptr(), nb, _stream(stream)))
     return loss, lse
 
 
@@ -550,10 +566,10 @@ def linear_cross_entropy_bwd(x: torch.Tensor, W: torch.Tensor, targets: torch.Te
     else:
         _need("dW", dW, (V, d), torch.bfloat16, torch.float32)
     nb = lib.linear_cross_entropy_bwd_workspace_size(T, d, V)
-    w = _ws(nb, x.device, ws)
+    w = _scratch(nb, x, ws)
     _check("linear_cross_entropy_bwd",
-           lib.linear_cross_entropy_bwd(_ptr(x), _ptr(W), _ptr(targets), _ptr(lse), _ptr(dloss), T, d, V, ignore_index,
-                                        _ptr(dX), _ptr(dW), _dtype_code(dW), _ptr(w), nb, _stream(stream)))
+           lib.linear_cross_entropy_bwd(x.data_ptr(), W.data_ptr(), targets.data_ptr(), lse.data_ptr(), dloss.data_ptr(), T, d, V, ignore_index,
+                                        dX.data_ptr(), dW.data_ptr(), _dtype_code(dW), w.data_ptr(), nb, _stream(stream)))
     return dX, dW
 
 

@@ -69,10 +69,12 @@ enum PairOut { kOutF32Store = 0, kOutF32Add = 1, kOutBf16 = 2, kOutBf16Join = 3 
 
 struct PairArgs {
   int M, N, K;
-  int m_tiles, n_tiles, num_tiles, k_blocks, group;
+  int m_tiles, n_tiles, k_blocks, group;
+  int splits, split_blocks;  // parts of K, and the blocks of 64 in each (the last may have fewer)
+  int num_tiles;             // m_tiles n_tiles splits
   uint32_t idesc;
-  int out;                  // PairOut
-  const float* scale;       // kPairDx (bf16 outputs), kPairDw: s
+  int out;                  // PairOut; with splits > 1 fp32, split i at rows i 256 m_tiles of C
+  const float* scale;       // s, or null: the sum as it is
   float* acc;               // kOutBf16Join: the sum so far [M, N]
   int v0;                   // kPairGrad: the piece's first column
   const int64_t* targets;   // kPairLse
@@ -203,12 +205,18 @@ struct PairStager {
   }
 };
 
-// Tile -> (M tile, N tile) in groups of p.group M tiles: all N tiles of a group, M fastest inside it.
-__device__ __forceinline__ void pair_coords(int tile, const PairArgs& p, int& mb, int& nb) {
+// Tile -> (part of K, M tile, N tile): a part's tiles in groups of p.group M tiles, all N tiles of a group,
+// M fastest inside it.  Its blocks of K are [k0, k1).
+__device__ __forceinline__ int pair_coords(int tile, const PairArgs& p, int& mb, int& nb, int& k0, int& k1) {
+  const int each = p.m_tiles * p.n_tiles, part = tile / each;
+  tile -= part * each;
+  k0 = part * p.split_blocks;
+  k1 = min(k0 + p.split_blocks, p.k_blocks);
   const int span = p.group * p.n_tiles, grp = tile / span, first = grp * p.group;
   const int gm = min(p.group, p.m_tiles - first), local = tile - grp * span;
   mb = first + local % gm;
   nb = local / gm;
+  return part;
 }
 
 template <int A_MN, int B_MN, int MODE>
@@ -256,10 +264,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int tile = first; tile < p.num_tiles && ok; tile += step) {
-        int mb, nb;
-        pair_coords(tile, p, mb, nb);
+        int mb, nb, kb0, kb1;
+        pair_coords(tile, p, mb, nb, kb0, kb1);
         const int m0 = mb * PM + 128 * rank, n0 = nb * PN + 128 * rank;
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!pair_wait(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
           uint8_t* sA = smem + stage * kPairStage;
           uint8_t* sB = sA + kHalfTile;
@@ -298,7 +306,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (!pair_wait(&tempty[acc], acc_phase ^ 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(acc * PN);
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
+        int mb, nb, kb0, kb1;
+        pair_coords(tile, p, mb, nb, kb0, kb1);
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!pair_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
           tc_fence_after();
           const uint32_t sA = smem_addr(smem + stage * kPairStage), sB = sA + kHalfTile;
@@ -308,7 +318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             // the second 64-element block of MN 8 KB on
             const uint64_t ad = A_MN ? smem_desc_sw128(sA + kk * 2048, kHalfTile / 2, 1024) : smem_desc_sw128(sA + kk * 32, 16, 1024);
             const uint64_t bd = B_MN ? smem_desc_sw128(sB + kk * 2048, kHalfTile / 2, 1024) : smem_desc_sw128(sB + kk * 32, 16, 1024);
-            pair_mma(d, ad, bd, p.idesc, (kb | kk) != 0 ? 1u : 0u);
+            pair_mma(d, ad, bd, p.idesc, (kb - kb0) | kk ? 1u : 0u);
           }
           pair_commit(&empty[stage], 3);
           if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
@@ -331,12 +341,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int sub = warp & 3, half = (warp - 4) >> 2;
     PairStager out(smem_addr(smem + kPairStagingOffset + (warp - 4) * kPairStaging), lane);
     const uint32_t tempty0 = map_to_rank(smem_addr(tempty), 0);
-    const float alpha = (MODE == kPairDx || MODE == kPairDw) ? *p.scale : 1.0f;
+    const float alpha = p.scale ? *p.scale : 1.0f;
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int tile = first; tile < p.num_tiles; tile += step) {
-      int mb, nb;
-      pair_coords(tile, p, mb, nb);
+      int mb, nb, kb0, kb1;
+      const int split_row = pair_coords(tile, p, mb, nb, kb0, kb1) * p.m_tiles * PM;
       const int row0 = mb * PM + 128 * rank + sub * 32, row = row0 + lane;
       const bool row_ok = row < p.M, warp_ok = row0 < p.M;
       const int col0 = nb * PN + 128 * half;
@@ -420,10 +430,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             for (int j = 0; j < 32; ++j) v[j] = alpha * __uint_as_float(a[j]);
             out.bf16(&tmC, v, col, row0);
           } else {
-            const float f = MODE == kPairDw ? alpha : 1.0f;  // dX's sum is scaled when it is complete
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = f * __uint_as_float(a[j]);
-            out.f32(&tmC, v, col, row0, p.out == kOutF32Add);
+            for (int j = 0; j < 32; ++j) v[j] = alpha * __uint_as_float(a[j]);
+            out.f32(&tmC, v, col, split_row + row0, p.out == kOutF32Add);
           }
         }
       }
@@ -447,37 +456,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // ---------------------------------------------------------------------------
 // The small kernels around it
 // ---------------------------------------------------------------------------
-// Joins the pieces of a row: 32 rows a block, warp w takes pieces w, w + 8, ..., lane = row; then the
-// warps' pairs.  lse = ln 2 (m2 + log2 s).  A target outside [0, V) that is not ignore_index is a mistake of
-// the caller: recorded, and ignored.
-__global__ void __launch_bounds__(256) k_ce_finish(const float2* __restrict__ part, int pieces, int64_t T,
-                                                   const int64_t* __restrict__ targets, int64_t V, int64_t ignore,
-                                                   const float* __restrict__ zy, float* __restrict__ loss,
-                                                   float* __restrict__ lse, unsigned* status) {
-  __shared__ float2 sh[8][32];
+// Joins the pieces of a row: 32 rows a block, lane = row, warp w takes pieces w, w + 32, ... four at a
+// time; then the warps' pairs.  lse = ln 2 (m2 + log2 s).  A target outside [0, V) that is not ignore_index is a
+// mistake of the caller: recorded, and ignored.
+__device__ __forceinline__ float2 ce_join2(float2 a, float2 b) {
+  // a pair that holds nothing is (-inf, 0); both may be
+  const float m = fmaxf(a.x, b.x);
+  if (m == -INFINITY) return make_float2(m, a.y + b.y);
+  return make_float2(m, a.y * ce_exp2(a.x - m) + b.y * ce_exp2(b.x - m));
+}
+__global__ void __launch_bounds__(1024) k_ce_finish(const float2* __restrict__ part, int pieces, int64_t T,
+                                                    const int64_t* __restrict__ targets, int64_t V, int64_t ignore,
+                                                    const float* __restrict__ zy, float* __restrict__ loss,
+                                                    float* __restrict__ lse, unsigned* status) {
+  __shared__ float2 sh[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * 32 + lane;
-  float m = -INFINITY, s = 0.0f;
-  bool any = false;
-  auto join = [&](float2 q) {
-    if (!any) { m = q.x; s = q.y; any = true; return; }
-    const float mn = fmaxf(m, q.x);
-    s = s * ce_exp2(m - mn) + q.y * ce_exp2(q.x - mn);
-    m = mn;
-  };
+  const float2 none = make_float2(-INFINITY, 0.0f);
+  float2 r = none;
   if (t < T)
-#pragma unroll 4
-    for (int i = warp; i < pieces; i += 8) join(part[(int64_t)i * T + t]);
-  sh[warp][lane] = make_float2(m, s);
+    for (int i = warp; i < pieces; i += 128) {
+      float2 q[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) q[k] = i + 32 * k < pieces ? part[(int64_t)(i + 32 * k) * T + t] : none;
+      r = ce_join2(r, ce_join2(ce_join2(q[0], q[1]), ce_join2(q[2], q[3])));
+    }
+  sh[warp][lane] = r;
   __syncthreads();
-  if (warp != 0 || t >= T) return;
-  for (int w = 1; w < 8 && w < pieces; ++w) join(sh[w][lane]);
-  const float l = kLn2 * (m + log2f(s));
-  lse[t] = l;
-  const int64_t y = targets[t];
+  // warp w joins row w of the block: a butterfly over the 32 warps' pairs
+  r = sh[lane][warp];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float2 q = make_float2(__shfl_xor_sync(0xFFFFFFFFu, r.x, o), __shfl_xor_sync(0xFFFFFFFFu, r.y, o));
+    r = (lane & o) ? ce_join2(q, r) : ce_join2(r, q);
+  }
+  const int64_t row = (int64_t)blockIdx.x * 32 + warp;
+  if (lane != 0 || row >= T) return;
+  const float l = kLn2 * (r.x + log2f(r.y));
+  lse[row] = l;
+  const int64_t y = targets[row];
   const bool in = y >= 0 && y < V;
   if (y != ignore && !in) atomicOr(status, kStatusBadTarget);
-  loss[t] = y != ignore && in ? l - zy[t] : 0.0f;
+  loss[row] = y != ignore && in ? l - zy[row] : 0.0f;
 }
 
 // s = max |dloss| over the tokens that count (1 where that is 0 or not finite).
@@ -511,6 +531,25 @@ __global__ void __launch_bounds__(256) k_ce_rows(const uint16_t* __restrict__ x,
     const uint16_t* src = x + t * d;
     uint16_t* dst = xz + t * d;
     for (int j = 8 * threadIdx.x; j < d; j += 8 * blockDim.x) st_v4(dst + j, keep ? ld_v4(src + j) : make_uint4(0, 0, 0, 0));
+  }
+}
+
+// out = s (sum of the parts of K), part i at rows i `rows_pad` of part; N a multiple of 8.
+__global__ void __launch_bounds__(256) k_ce_join(const float* __restrict__ part, int splits, int64_t rows_pad, int64_t M,
+                                                 int N, const float* __restrict__ scale, void* out, int f32) {
+  const int64_t n4 = M * N / 4, stride = rows_pad * N / 4;
+  const float alpha = *scale;
+  const float4* p = reinterpret_cast<const float4*>(part);
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n4; i += (int64_t)gridDim.x * blockDim.x) {
+    float4 s = p[i];
+#pragma unroll 4
+    for (int k = 1; k < splits; ++k) {
+      const float4 q = p[k * stride + i];
+      s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
+    }
+    s.x *= alpha; s.y *= alpha; s.z *= alpha; s.w *= alpha;
+    if (f32) reinterpret_cast<float4*>(out)[i] = s;
+    else reinterpret_cast<uint2*>(out)[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
   }
 }
 
@@ -571,16 +610,40 @@ int pair_group(const PairProblem& q, int m_tiles) {
   return 2048 / PM;
 }
 
+// Parts of K for a product with few tiles.  A block of 64 of K takes a pair about 0.33 us (25 TFLOP/s), a
+// tile's fill and epilogue about 2 us, and joining the parts a launch (3 us) and a read and a write of each
+// part at about 6 TB/s; the tiles run in waves of one per pair.  E.g. T = 1003, d = 2048, V = 50257: dX has 32 tiles
+// for 76 pairs, 245 us in one part.
+constexpr int kPlanPairs = 76;
+int pair_splits(int64_t M, int64_t N, int64_t K) {
+  const int64_t m_pad = (M + PM - 1) / PM * PM, tiles = m_pad / PM * ((N + PN - 1) / PN), kb = (K + PK - 1) / PK;
+  if (tiles >= 4 * kPlanPairs) return 1;
+  int best = 1;
+  double least = 0.0;
+  for (int s = 1; s <= 32 && s <= kb; ++s) {
+    const int64_t each = (kb + s - 1) / s;
+    if ((kb + each - 1) / each != s) continue;  // fewer parts hold the same blocks
+    if (s > 1 && s * m_pad * N * 4 > (256ll << 20)) break;
+    const double waves = (double)((tiles * s + kPlanPairs - 1) / kPlanPairs);
+    const double us = waves * (0.33 * (double)each + 2.0) + (s > 1 ? 3.0 + (double)(s * M * N) * 8.0 / 6e6 : 0.0);
+    if (s == 1 || us < least) { best = s; least = us; }
+  }
+  return best;
+}
+
 template <int A_MN, int B_MN, int MODE>
-cudaError_t launch_pair(const PairProblem& q, PairArgs a, const Launch& L) {
+cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Launch& L) {
   a.M = (int)q.M;
   a.N = (int)q.N;
   a.K = (int)q.K;
   a.m_tiles = (a.M + PM - 1) / PM;
   a.n_tiles = (a.N + PN - 1) / PN;
   a.k_blocks = (a.K + PK - 1) / PK;
-  if ((int64_t)a.m_tiles * a.n_tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  a.num_tiles = a.m_tiles * a.n_tiles;
+  if ((int64_t)a.m_tiles * a.n_tiles * splits > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  // a shorter last piece of the vocabulary may need fewer parts; the others then get nothing added
+  a.split_blocks = (a.k_blocks + splits - 1) / splits;
+  a.splits = (a.k_blocks + a.split_blocks - 1) / a.split_blocks;
+  a.num_tiles = a.m_tiles * a.n_tiles * a.splits;
   a.group = pair_group(q, a.m_tiles);
   // fp32 sums, bf16 operands and their majors, N / 8 and M / 16 of the pair's tile
   a.idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
@@ -594,7 +657,7 @@ cudaError_t launch_pair(const PairProblem& q, PairArgs a, const Launch& L) {
   tc = ta;
   if (MODE != kPairLse) {
     const bool f32 = MODE != kPairGrad && (a.out == kOutF32Store || a.out == kOutF32Add);
-    ok = ok && make_map(&tc, q.C, q.N, q.M, q.ldc, f32 ? 4 : 2, 32, 32,
+    ok = ok && make_map(&tc, q.C, q.N, splits > 1 ? (int64_t)splits * a.m_tiles * PM : q.M, q.ldc, f32 ? 4 : 2, 32, 32,
                         f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
   }
   if (!ok) return cudaErrorInvalidValue;
@@ -621,9 +684,23 @@ int64_t ce_piece(int64_t T, int64_t V) {
   return ((V + n - 1) / n + PN - 1) / PN * PN;
 }
 
+// The backward's plan: the piece, and the parts of K of its two products.
+struct CePlan {
+  int64_t piece;
+  int dx_splits, dw_splits;
+};
+CePlan ce_plan(int64_t T, int64_t d, int64_t V) {
+  CePlan p{};
+  p.piece = ce_piece(T, V);
+  const int64_t n = p.piece < V ? p.piece : V;
+  p.dx_splits = pair_splits(T, d, n);
+  p.dw_splits = pair_splits(n, d, T);
+  return p;
+}
+
 struct CeWs {
   float2 *part, *row_w;
-  float *zy, *acc, *scale;
+  float *zy, *acc, *dw_part, *scale;
   int2* row_y;
   uint16_t *G, *xz;
 };
@@ -636,10 +713,13 @@ size_t ce_layout(int64_t T, int64_t d, int64_t V, bool bwd, uint8_t* base, CeWs*
   };
   CeWs t{};
   if (bwd) {
-    const int64_t piece = ce_piece(T, V);
-    t.G = (uint16_t*)take(T * piece * 2);
+    const CePlan p = ce_plan(T, d, V);
+    t.G = (uint16_t*)take(T * p.piece * 2);
     t.xz = (uint16_t*)take(T * d * 2);
-    if (piece < V) t.acc = (float*)take(T * d * 4);
+    const int64_t m_pad = (T + PM - 1) / PM * PM;
+    if (p.dx_splits > 1) t.acc = (float*)take(p.dx_splits * m_pad * d * 4);
+    else if (p.piece < V) t.acc = (float*)take(T * d * 4);
+    if (p.dw_splits > 1) t.dw_part = (float*)take(p.dw_splits * p.piece * d * 4);
     t.row_y = (int2*)take(T * 8);
     t.row_w = (float2*)take(T * 8);
     t.scale = (float*)take(4);
@@ -663,10 +743,11 @@ cudaError_t launch_ce_fwd(const uint16_t* x, const uint16_t* W, const int64_t* t
   a.targets = targets;
   a.part = w.part;
   a.zy = w.zy;
-  cudaError_t e = launch_pair<0, 0, kPairLse>(PairProblem{T, V, d, x, d, W, d, nullptr, 0}, a, L);
+  cudaError_t e = launch_pair<0, 0, kPairLse>(PairProblem{T, V, d, x, d, W, d, nullptr, 0}, 1, a, L);
   if (e != cudaSuccess) return e;
   const int pieces = (int)((V + 127) / 128);
-  k_ce_finish<<<(unsigned)((T + 31) / 32), 256, 0, L.stream>>>(w.part, pieces, T, targets, V, ignore, w.zy, loss, lse, L.status);
+  k_ce_finish<<<(unsigned)((T + 31) / 32), 1024, 0, L.stream>>>(w.part, pieces, T, targets, V, ignore, w.zy, loss, lse,
+                                                               L.status);
   return launched(L);
 }
 
@@ -675,7 +756,9 @@ cudaError_t launch_ce_bwd(const uint16_t* x, const uint16_t* W, const int64_t* t
                           int dw_f32, void* ws, const Launch& L) {
   CeWs w;
   ce_layout(T, d, V, true, static_cast<uint8_t*>(ws), &w);
-  const int64_t piece = ce_piece(T, V);
+  const CePlan plan = ce_plan(T, d, V);
+  const int64_t piece = plan.piece;
+  const int join_blocks = 4 * L.num_sms;
   cudaError_t e;
   k_ce_scale<<<1, 1024, 0, L.stream>>>(dloss, targets, T, V, ignore, w.scale, L.status);
   if ((e = launched(L)) != cudaSuccess) return e;
@@ -689,22 +772,33 @@ cudaError_t launch_ce_bwd(const uint16_t* x, const uint16_t* W, const int64_t* t
     a.v0 = (int)v0;
     a.row_y = w.row_y;
     a.row_w = w.row_w;
-    e = launch_pair<0, 0, kPairGrad>(PairProblem{T, n, d, x, d, W + v0 * d, d, w.G, piece}, a, L);
+    e = launch_pair<0, 0, kPairGrad>(PairProblem{T, n, d, x, d, W + v0 * d, d, w.G, piece}, 1, a, L);
     if (e != cudaSuccess) return e;
-    // dX (+)= G W[piece]
+    // dX (+)= G W[piece]: the sum so far stays in fp32 (its parts of K apart), s joins it at the end
     PairArgs ax{};
-    ax.scale = w.scale;
+    const int xs = plan.dx_splits;
     ax.acc = w.acc;
-    ax.out = first ? (last ? kOutBf16 : kOutF32Store) : (last ? kOutBf16Join : kOutF32Add);
-    e = launch_pair<0, 1, kPairDx>(PairProblem{T, d, n, w.G, piece, W + v0 * d, d, last ? (void*)dX : (void*)w.acc, d}, ax, L);
+    ax.out = xs > 1 || !last ? (first ? kOutF32Store : kOutF32Add) : (first ? kOutBf16 : kOutBf16Join);
+    if (xs == 1 && last) ax.scale = w.scale;
+    void* to = xs > 1 || !last ? (void*)w.acc : (void*)dX;
+    e = launch_pair<0, 1, kPairDx>(PairProblem{T, d, n, w.G, piece, W + v0 * d, d, to, d}, xs, ax, L);
     if (e != cudaSuccess) return e;
-    // dW[piece] = G^T x
+    if (xs > 1 && last) {
+      k_ce_join<<<join_blocks, 256, 0, L.stream>>>(w.acc, xs, (T + PM - 1) / PM * PM, T, d, w.scale, dX, 0);
+      if ((e = launched(L)) != cudaSuccess) return e;
+    }
+    // dW[piece] = s G^T x
     PairArgs aw{};
-    aw.scale = w.scale;
-    aw.out = dw_f32 ? kOutF32Store : kOutBf16;
+    const int wsp = plan.dw_splits;
+    if (wsp == 1) aw.scale = w.scale;
+    aw.out = wsp > 1 || dw_f32 ? kOutF32Store : kOutBf16;
     void* dst = dw_f32 ? (void*)(static_cast<float*>(dW) + v0 * d) : (void*)(static_cast<uint16_t*>(dW) + v0 * d);
-    e = launch_pair<1, 1, kPairDw>(PairProblem{n, d, T, w.G, piece, w.xz, d, dst, d}, aw, L);
+    e = launch_pair<1, 1, kPairDw>(PairProblem{n, d, T, w.G, piece, w.xz, d, wsp > 1 ? (void*)w.dw_part : dst, d}, wsp, aw, L);
     if (e != cudaSuccess) return e;
+    if (wsp > 1) {
+      k_ce_join<<<join_blocks, 256, 0, L.stream>>>(w.dw_part, wsp, (n + PM - 1) / PM * PM, n, d, w.scale, dst, dw_f32);
+      if ((e = launched(L)) != cudaSuccess) return e;
+    }
   }
   return cudaSuccess;
 }

@@ -218,6 +218,27 @@ def test_dw_past_32_bit_offsets():
     assert bool((err <= 2.0 ** -7 * (G.abs().t() @ x.double().abs())).all())
 
 
+@pytest.mark.parametrize("T,d,V", [(16500, 16, 26000), (40000, 8, 4500), (5000, 64, 30500), (1, 64, 100003), (4100, 24, 300)])
+def test_many_pieces_and_parts(T, d, V):
+    """Several pieces of the vocabulary (the last one short), products of few tiles cut along K (a last piece
+    with fewer parts), against the definition on sampled rows of dX and dW."""
+    x, W, t, dl = make(T, d, V)
+    loss, lse = fq.linear_cross_entropy_fwd(x, W, t)
+    dX, dW = fq.linear_cross_entropy_bwd(x, W, t, lse, dl)
+    rows = sorted({r for r in (0, 1, T // 2, T - 2, T - 1) if 0 <= r < T})
+    check_fwd(x[rows], W, t[rows], loss[rows], lse[rows])
+    G = ref.cross_entropy_grad(x[rows].double(), W.double(), t[rows], dl[rows].double(), IGN)
+    bound = (2.0 ** -8 * (1 + 2.0 ** -4) + (V / 16 + 32) * 2.0 ** -23) * (G.abs() @ W.double().abs()) + 2.0 ** -8 * (G @ W.double()).abs() + 1e-9
+    assert bool(((dX[rows].double() - G @ W.double()).abs() <= bound).all())
+    want, mag = torch.zeros(V, d, dtype=torch.float64, device="cuda"), torch.zeros(V, d, dtype=torch.float64, device="cuda")
+    for i in range(0, T, 4096):
+        s = slice(i, i + 4096)
+        G = ref.cross_entropy_grad(x[s].double(), W.double(), t[s], dl[s].double(), IGN)
+        want += G.t() @ x[s].double()
+        mag += G.abs().t() @ x[s].double().abs()
+    assert bool(((dW.double() - want).abs() <= (2.0 ** -8 * (1 + 2.0 ** -4) + (T / 16 + 32) * 2.0 ** -23) * mag + 1e-9).all())
+
+
 def test_refusals():
     x, W, t, dl = make(16, 64, 100)
     lse = torch.zeros(16, device="cuda")
