@@ -167,7 +167,9 @@ def load_library() -> ctypes.CDLL:
 
 class _LazyLib:
     def __getattr__(self, name):
-        return getattr(load_library(), name)
+        f = getattr(load_library(), name)
+        setattr(self, name, f)  # found directly from the second use on
+        return f
 
 
 lib = _LazyLib()
@@ -369,38 +371,75 @@ def attention_bwd(qkv: torch.Tensor, att: torch.Tensor, lse: torch.Tensor, d_att
 
 
 # ---------------------------------------------------------------------------
-def _need(name: str, t, shape, *dtypes):
-    """A tensor argument of a given shape (None: any size in that place) and one of the given types,
-    dense, on the current CUDA device (the library launches there)."""
-    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_cuda and t.is_contiguous()
-            and t.get_device() == torch._C._cuda_getDevice()
-            and (t.shape == shape or (None in shape and t.dim() == len(shape)
-                                      and all(want is None or have == want for have, want in zip(t.shape, shape))))):
-        return t
+# The operators below run in a few microseconds on small inputs, so what their binding does on the host
+# counts: the checks are one short function, and pointers and the stream go to ctypes as integers.
+_REAL = (torch.bfloat16, torch.float32)
+
+
+def _fits(t, dtype, shape) -> bool:
+    """Whether t is a dense tensor of this type and shape on the current CUDA device (the library
+    launches there)."""
+    try:
+        return (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
+                and t.get_device() == torch._C._cuda_getDevice())
+    except AttributeError:
+        return False
+
+
+def _refuse(name: str, t, dtype, shape):
+    """The reason why _fits is false, raised."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple('any' if s is None else s for s in shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, not {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _out(name: str, t, shape, dtype, like):
-    return torch.empty(shape, dtype=dtype, device=like.device) if t is None else _need(name, t, shape, dtype)
+def _need(name: str, t, dtype, shape):
+    if not _fits(t, dtype, shape):
+        _refuse(name, t, dtype, shape)
 
 
-def _scratch(nbytes: int, like, ws):
-    """The workspace's address and bytes: the caller's, or a new one."""
+def _matrix(name: str, t, types=_REAL):
+    """A [rows, columns] argument of one of the types; its shape and type decide the others'."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in types:
+        raise TypeError(f"{name} has dtype {t.dtype}, not {' or '.join(str(d) for d in types)}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not [rows, columns]")
+    if not t.is_contiguous() or t.get_device() != torch._C._cuda_getDevice():
+        _refuse(name, t, t.dtype, t.shape)
+    return t.shape
+
+
+def _out(name: str, t, dtype, shape, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not _fits(t, dtype, shape):
+        _refuse(name, t, dtype, shape)
+    return t
+
+
+def _scratch(nbytes: int, device, ws):
+    """The caller's workspace, or a new one."""
     if ws is None:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    elif not (ws.is_cuda and ws.is_contiguous() and ws.get_device() == like.get_device()):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not (ws.is_cuda and ws.is_contiguous() and ws.device == device):
         raise ValueError("the workspace must be a contiguous tensor on the inputs' device")
-    elif ws.numel() * ws.element_size() < nbytes:
+    if ws.nbytes < nbytes:
         raise ValueError("workspace too small")
     return ws
+
+
+def _raw_stream(stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 @dataclasses.dataclass(frozen=True)
@@ -413,7 +452,7 @@ class Rope:
     interleaved: bool
     inv_freq: tuple
     axis: tuple
-    _struct: FP8QRope = dataclasses.field(repr=False, compare=False)
+    _ref: object = dataclasses.field(repr=False, compare=False)  # ctypes reference to the FP8QRope
 
     @staticmethod
     def make(head_dim: int = 128, rot_dim: int | None = None, base: float = 10000.0, sections=None,
@@ -448,16 +487,21 @@ class Rope:
         s = FP8QRope(head_dim=head_dim, rot_dim=rot_dim, n_axes=n_axes, interleaved=int(bool(interleaved)))
         s.inv_freq[:half] = freq
         s.axis[:half] = axis
-        return Rope(head_dim, rot_dim, n_axes, bool(interleaved), tuple(freq), tuple(axis), s)
+        return Rope(head_dim, rot_dim, n_axes, bool(interleaved), tuple(freq), tuple(axis), ctypes.byref(s))
 
 
-def _rope_call(name, qkv, pos, rope, n_heads, n_kv_heads, out, stream):
-    _need("qkv", qkv, (None, (n_heads + 2 * n_kv_heads) * rope.head_dim), torch.bfloat16, torch.float32)
-    T = qkv.shape[0]
-    _need("pos", pos, (T,) if rope.n_axes == 1 and pos.dim() == 1 else (rope.n_axes, T), torch.int32)
-    out = _out("out", out, qkv.shape, qkv.dtype, qkv)
-    _check(name, getattr(lib, name)(qkv.data_ptr(), _dtype_code(qkv), T, n_heads, n_kv_heads, ctypes.byref(rope._struct),
-                                    pos.data_ptr(), out.data_ptr(), _stream(stream)))
+def _rope_call(name, fn, qkv, pos, rope, n_heads, n_kv_heads, out, stream):
+    T, width = _matrix("qkv", qkv)
+    dtype = qkv.dtype
+    if width != (n_heads + 2 * n_kv_heads) * rope.head_dim:
+        raise ValueError(f"qkv has {width} columns, not ({n_heads} + 2 * {n_kv_heads}) heads of {rope.head_dim}")
+    _need("pos", pos, torch.int32, (T,) if rope.n_axes == 1 and pos.dim() == 1 else (rope.n_axes, T))
+    if out is None:
+        out = torch.empty_like(qkv)
+    elif out is not qkv:
+        _need("out", out, dtype, (T, width))
+    _check(name, fn(qkv.data_ptr(), BF16 if dtype is torch.bfloat16 else F32, T, n_heads, n_kv_heads, rope._ref,
+                    pos.data_ptr(), out.data_ptr(), _raw_stream(stream)))
     return out
 
 
@@ -465,29 +509,30 @@ def rope_fwd(qkv: torch.Tensor, pos: torch.Tensor, rope: Rope, n_heads: int, n_k
     """Rotary positions of qkv [T, (n_heads + 2 n_kv_heads) head_dim] (bf16 or fp32, the layout
     attention_fwd reads): q and k heads rotated, v heads copied.  pos: [n_axes, T] int32, or [T] with
     one axis.  out=qkv works in place.  n_kv_heads=0 rotates every head."""
-    return _rope_call("rope_fwd", qkv, pos, rope, n_heads, n_kv_heads, out, stream)
+    return _rope_call("rope_fwd", lib.rope_fwd, qkv, pos, rope, n_heads, n_kv_heads, out, stream)
 
 
 def rope_bwd(d_out: torch.Tensor, pos: torch.Tensor, rope: Rope, n_heads: int, n_kv_heads: int, dqkv=None, stream=None):
     """Gradient of rope_fwd at its input, for the gradient d_out at its output (attention_bwd's dqkv):
     the rotation by the negative angles.  dqkv=d_out works in place."""
-    return _rope_call("rope_bwd", d_out, pos, rope, n_heads, n_kv_heads, dqkv, stream)
+    return _rope_call("rope_bwd", lib.rope_bwd, d_out, pos, rope, n_heads, n_kv_heads, dqkv, stream)
 
 
 def layernorm_fwd(x: torch.Tensor, g: torch.Tensor, b: torch.Tensor | None = None, eps: float = 1e-5, y=None,
                   mean=None, rstd=None, stream=None):
     """Layer norm of x [T,d] with gain g and bias b [d] (all bf16 or all fp32).
     Returns (y [T,d], mean [T] fp32, rstd [T] fp32)."""
-    _need("x", x, (None, None), torch.bfloat16, torch.float32)
-    T, d = x.shape
-    _need("g", g, (d,), x.dtype)
+    T, d = shape = _matrix("x", x)
+    dtype, dev = x.dtype, x.device
+    _need("g", g, dtype, (d,))
     if b is not None:
-        _need("b", b, (d,), x.dtype)
-    y = _out("y", y, (T, d), x.dtype, x)
-    mean = _out("mean", mean, (T,), torch.float32, x)
-    rstd = _out("rstd", rstd, (T,), torch.float32, x)
-    _check("layernorm_fwd", lib.layernorm_fwd(x.data_ptr(), _dtype_code(x), g.data_ptr(), None if b is None else b.data_ptr(), T, d, eps, y.data_ptr(), mean.data_ptr(),
-                                              rstd.data_ptr(), _stream(stream)))
+        _need("b", b, dtype, (d,))
+    y = torch.empty_like(x) if y is None else _out("y", y, dtype, shape, dev)
+    mean = _out("mean", mean, torch.float32, (T,), dev)
+    rstd = _out("rstd", rstd, torch.float32, (T,), dev)
+    _check("layernorm_fwd", lib.layernorm_fwd(x.data_ptr(), BF16 if dtype is torch.bfloat16 else F32, g.data_ptr(),
+                                              None if b is None else b.data_ptr(), T, d, eps, y.data_ptr(),
+                                              mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream)))
     return y, mean, rstd
 
 
@@ -499,22 +544,23 @@ def layernorm_bwd(dY: torch.Tensor, x: torch.Tensor, g: torch.Tensor, mean: torc
                   dres: torch.Tensor | None = None, dX=None, dg=None, db=None, ws=None, stream=None):
     """Layer norm backward: dY, x (and dres, the residual branch's gradient, added to dX) [T,d], g [d],
     the forward's mean and rstd [T].  Returns (dX [T,d], dg [d] fp32, db [d] fp32)."""
-    _need("x", x, (None, None), torch.bfloat16, torch.float32)
-    T, d = x.shape
-    _need("dY", dY, (T, d), x.dtype)
-    _need("g", g, (d,), x.dtype)
-    _need("mean", mean, (T,), torch.float32)
-    _need("rstd", rstd, (T,), torch.float32)
+    T, d = shape = _matrix("x", x)
+    dtype, dev = x.dtype, x.device
+    _need("dY", dY, dtype, shape)
+    _need("g", g, dtype, (d,))
+    _need("mean", mean, torch.float32, (T,))
+    _need("rstd", rstd, torch.float32, (T,))
     if dres is not None:
-        _need("dres", dres, (T, d), x.dtype)
-    dX = _out("dX", dX, (T, d), x.dtype, x)
-    dg = _out("dg", dg, (d,), torch.float32, x)
-    db = _out("db", db, (d,), torch.float32, x)
+        _need("dres", dres, dtype, shape)
+    dX = torch.empty_like(x) if dX is None else _out("dX", dX, dtype, shape, dev)
+    dg = _out("dg", dg, torch.float32, (d,), dev)
+    db = _out("db", db, torch.float32, (d,), dev)
     nb = lib.layernorm_bwd_workspace_size(T, d)
-    w = _scratch(nb, x, ws)
-    _check("layernorm_bwd", lib.layernorm_bwd(dY.data_ptr(), x.data_ptr(), _dtype_code(x), g.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-                                              None if dres is None else dres.data_ptr(), T, d, dX.data_ptr(), dg.data_ptr(), db.data_ptr(), w.data_ptr(), nb,
-                                              _stream(stream)))
+    w = _scratch(nb, dev, ws)
+    _check("layernorm_bwd", lib.layernorm_bwd(dY.data_ptr(), x.data_ptr(), BF16 if dtype is torch.bfloat16 else F32,
+                                              g.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                              None if dres is None else dres.data_ptr(), T, d, dX.data_ptr(),
+                                              dg.data_ptr(), db.data_ptr(), w.data_ptr(), nb, _raw_stream(stream)))
     return dX, dg, db
 
 
@@ -526,26 +572,31 @@ def linear_cross_entropy_bwd_workspace_size(T: int, d: int, V: int) -> int:
     return lib.linear_cross_entropy_bwd_workspace_size(T, d, V)
 
 
-def _ce_args(x, W, targets):
-    _need("x", x, (None, None), torch.bfloat16)
-    T, d = x.shape
-    _need("W", W, (None, d), torch.bfloat16)
-    _need("targets", targets, (T,), torch.int64)
-    return T, d, W.shape[0]
+_HEAD = (torch.bfloat16,)
+
+
+def _ce_sizes(x, W, targets):
+    T, d = _matrix("x", x, _HEAD)
+    V, dw = _matrix("W", W, _HEAD)
+    if dw != d:
+        raise ValueError(f"W has {dw} columns, x has {d}")
+    _need("targets", targets, torch.int64, (T,))
+    return T, d, V
 
 
 def linear_cross_entropy_fwd(x: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
                              loss=None, lse=None, ws=None, stream=None):
     """Softmax cross entropy of the head z = x W^T, logits never kept: x [T,d] bf16, W [V,d] bf16,
     targets [T] int64.  Returns (loss [T] fp32, 0 for ignored tokens; lse [T] fp32)."""
-    T, d, V = _ce_args(x, W, targets)
-    loss = _out("loss", loss, (T,), torch.float32, x)
-    lse = _out("lse", lse, (T,), torch.float32, x)
+    T, d, V = _ce_sizes(x, W, targets)
+    dev = x.device
+    loss = _out("loss", loss, torch.float32, (T,), dev)
+    lse = _out("lse", lse, torch.float32, (T,), dev)
     nb = lib.linear_cross_entropy_fwd_workspace_size(T, d, V)
-    w = _scratch(nb, x, ws)
+    w = _scratch(nb, dev, ws)
     _check("linear_cross_entropy_fwd",
-           lib.linear_cross_entropy_fwd(x.data_ptr(), W.data_ptr(), targets.data_ptr(), T, d, V, ignore_index, loss.data_ptr(), lse.data_ptr(),
-                                        w.data_ptr(), nb, _stream(stream)))
+           lib.linear_cross_entropy_fwd(x.data_ptr(), W.data_ptr(), targets.data_ptr(), T, d, V, ignore_index,
+                                        loss.data_ptr(), lse.data_ptr(), w.data_ptr(), nb, _raw_stream(stream)))
     return loss, lse
 
 
@@ -555,21 +606,24 @@ def linear_cross_entropy_bwd(x: torch.Tensor, W: torch.Tensor, targets: torch.Te
     """Gradients of linear_cross_entropy_fwd for dloss [T] fp32, the gradient at each token's loss (a
     mean: 1 / the number of tokens that count).  Returns (dX [T,d] bf16, dW [V,d] of dw_dtype, fp32 or
     bf16; a given dW decides its own type)."""
-    T, d, V = _ce_args(x, W, targets)
-    _need("lse", lse, (T,), torch.float32)
-    _need("dloss", dloss, (T,), torch.float32)
-    dX = _out("dX", dX, (T, d), torch.bfloat16, x)
+    T, d, V = _ce_sizes(x, W, targets)
+    dev = x.device
+    _need("lse", lse, torch.float32, (T,))
+    _need("dloss", dloss, torch.float32, (T,))
+    dX = torch.empty_like(x) if dX is None else _out("dX", dX, torch.bfloat16, (T, d), dev)
     if dW is None:
-        if dw_dtype not in (torch.bfloat16, torch.float32):
+        if dw_dtype not in _REAL:
             raise TypeError(f"dw_dtype {dw_dtype}: bfloat16 or float32")
-        dW = torch.empty((V, d), dtype=dw_dtype, device=x.device)
+        dW = torch.empty((V, d), dtype=dw_dtype, device=dev)
     else:
-        _need("dW", dW, (V, d), torch.bfloat16, torch.float32)
+        _need("dW", dW, torch.bfloat16 if dW.dtype is torch.bfloat16 else torch.float32, (V, d))
     nb = lib.linear_cross_entropy_bwd_workspace_size(T, d, V)
-    w = _scratch(nb, x, ws)
+    w = _scratch(nb, dev, ws)
     _check("linear_cross_entropy_bwd",
-           lib.linear_cross_entropy_bwd(x.data_ptr(), W.data_ptr(), targets.data_ptr(), lse.data_ptr(), dloss.data_ptr(), T, d, V, ignore_index,
-                                        dX.data_ptr(), dW.data_ptr(), _dtype_code(dW), w.data_ptr(), nb, _stream(stream)))
+           lib.linear_cross_entropy_bwd(x.data_ptr(), W.data_ptr(), targets.data_ptr(), lse.data_ptr(),
+                                        dloss.data_ptr(), T, d, V, ignore_index, dX.data_ptr(), dW.data_ptr(),
+                                        BF16 if dW.dtype is torch.bfloat16 else F32, w.data_ptr(), nb,
+                                        _raw_stream(stream)))
     return dX, dW
 
 

@@ -44,19 +44,34 @@ __device__ __forceinline__ float ce_exp2(float x) {
 //               accumulator, in both CTAs;
 //   warp 2      tensor memory;
 //   warps 4-11  epilogue: warp w reads lanes 32 (w % 4) .., columns 128 (w / 4 - 1) ...
+// Up to 128 tokens the operands trade places (kTok*): the 256 rows of a pair's tile are rows of W (of W^T for
+// dX) and its NT = 32, 64 or 128 columns the tokens, so that the tensor cores do not work on padding (256 rows
+// for 24 tokens: 10.6 us of MMAs a tile at d = 2048 against 12 us for its operands from HBM) and W streams
+// at HBM's rate.  The softmax statistics then run down the tile's lanes: each warp turns its 32 x 32 blocks
+// in shared memory and keeps a running pair for each token over all its tiles.
+//
 // Every wait is bounded.  On expiry a CTA records the time-out and stops; its copies in flight, which
 // signal the other CTA, get kCopyDrainNs to land; the pair meets at a cluster barrier and frees its tensor memory.
 // ---------------------------------------------------------------------------
 constexpr int PM = 256, PN = 256, PK = 64;
 constexpr int kHalfTile = 128 * 128;  // bytes: 128 rows (or columns) x 64 bf16
-constexpr int kPairStage = 2 * kHalfTile;
-constexpr int kPairStages = 6;
 constexpr int kPairThreads = 384;
 constexpr int kPairStaging = 4096;  // per epilogue warp
-constexpr int kPairStagingOffset = kPairStages * kPairStage;
-constexpr int kPairBarOffset = kPairStagingOffset + 8 * kPairStaging;
-constexpr int kPairSmem = kPairBarOffset + 256 + 1024;
-static_assert(kPairSmem <= 232448, "shared memory per CTA");
+constexpr int kTokMax = 128;        // tokens up to which the operands trade places
+
+// The shared memory of a CTA for tiles of NT columns.
+template <int NT>
+struct PairPlan {
+  static constexpr int kB = NT / 2 * 128;  // bytes of its share of B in a stage
+  static constexpr int kStage = kHalfTile + kB;
+  static constexpr int kStages = NT == 256 ? 6 : NT == 128 ? 7 : NT == 64 ? 9 : 10;
+  static constexpr int kStagingOffset = kStages * kStage;
+  static constexpr int kTokOffset = kStagingOffset + 8 * kPairStaging;
+  static constexpr int kBarOffset = kTokOffset + (NT < 256 ? NT * 16 : 0);
+  static constexpr int kSmem = kBarOffset + 256 + 1024;
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+  static_assert(kStage % 1024 == 0, "swizzle atoms");
+};
 constexpr uint64_t kCopyDrainNs = 5000000ull;  // far beyond any copy in flight
 
 enum PairMode {
@@ -64,6 +79,9 @@ enum PairMode {
   kPairGrad = 1,  // G / s as bf16
   kPairDx = 2,    // dX: fp32 store, fp32 add or bf16 of the joined sum
   kPairDw = 3,    // dW: bf16 or fp32
+  kTokLse = 4,    // the same three with the tokens as columns: statistics of each warp's rows of W
+  kTokGrad = 5,   //   G / s, stored by token
+  kTokDx = 6,     //   dX's sum in fp32, by token, the parts of K apart
 };
 enum PairOut { kOutF32Store = 0, kOutF32Add = 1, kOutBf16 = 2, kOutBf16Join = 3 };
 
@@ -77,11 +95,11 @@ struct PairArgs {
   const float* scale;       // s, or null: the sum as it is
   float* acc;               // kOutBf16Join: the sum so far [M, N]
   int v0;                   // kPairGrad: the piece's first column
-  const int64_t* targets;   // kPairLse
-  float2* part;             // kPairLse: [2 n_tiles][M] (maximum log2e, sum)
-  float* zy;                // kPairLse: [M] the target's logit
-  const int2* row_y;        // kPairGrad: [M] {target or -1, -}
-  const float2* row_w;      // kPairGrad: [M] {lse log2e, dloss / s}
+  const int64_t* targets;   // kPairLse, kTokLse
+  int V;                    // kPairLse, kTokLse
+  float2* part;             // (maximum log2e, sum) pairs: kPairLse [2 n_tiles][M], kTokLse [4 CTAs][N]
+  float* zy;                // kPairLse, kTokLse: each token's target logit
+  const float4* rows;       // kPairGrad, kTokGrad: each token's {lse log2e, dloss / s, target or -1 (int bits), 0}
   unsigned* status;
 };
 
@@ -219,15 +237,18 @@ __device__ __forceinline__ int pair_coords(int tile, const PairArgs& p, int& mb,
   return part;
 }
 
-template <int A_MN, int B_MN, int MODE>
+template <int A_MN, int B_MN, int MODE, int NT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_ce_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmC, const PairArgs p) {
+  using PL = PairPlan<NT>;
+  constexpr bool kTok = NT < 256;
+  static_assert(kTok == (MODE >= kTokLse) && !(kTok && B_MN), "the tokens are a K-major operand");
   extern __shared__ uint8_t pair_smem[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pair_smem) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairBarOffset);
-  uint64_t* empty = full + kPairStages;
-  uint64_t* tfull = empty + kPairStages;  // [2]
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + PL::kBarOffset);
+  uint64_t* empty = full + PL::kStages;
+  uint64_t* tfull = empty + PL::kStages;  // [2]
   uint64_t* tempty = tfull + 2;           // [2]
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -237,15 +258,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int rank = (int)cluster_rank();
   const int first = (int)(blockIdx.x >> 1), step = (int)(gridDim.x >> 1);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kPairStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int s = 0; s < PL::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
     for (int a = 0; a < 2; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], 16); }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
-    if (MODE != kPairLse) tma_prefetch_desc(&tmC);
+    if (MODE != kPairLse && MODE != kTokLse && MODE != kTokDx) tma_prefetch_desc(&tmC);
   }
+  // kTokGrad: the tokens' rows (kTokLse: their targets) where every lane can read them
+  float4* tok = reinterpret_cast<float4*>(smem + PL::kTokOffset);
+  if (MODE == kTokGrad && threadIdx.x < NT)
+    tok[threadIdx.x] = (int)threadIdx.x < p.N ? p.rows[threadIdx.x] : make_float4(0.0f, 0.0f, __int_as_float(-1), 0.0f);
   if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)), "r"(512)
                  : "memory");
@@ -266,13 +291,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       for (int tile = first; tile < p.num_tiles && ok; tile += step) {
         int mb, nb, kb0, kb1;
         pair_coords(tile, p, mb, nb, kb0, kb1);
-        const int m0 = mb * PM + 128 * rank, n0 = nb * PN + 128 * rank;
+        const int m0 = mb * PM + 128 * rank, n0 = nb * NT + NT / 2 * rank;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!pair_wait(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
-          uint8_t* sA = smem + stage * kPairStage;
+          uint8_t* sA = smem + stage * PL::kStage;
           uint8_t* sB = sA + kHalfTile;
           const uint32_t bar = map_to_rank(smem_addr(&full[stage]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kPairStage);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * PL::kStage);
           const int k0 = kb * PK;
           if (A_MN) {  // two 64-element-wide boxes of 64 rows of K
             pair_load_2d(sA, &tmA, bar, m0, k0);
@@ -286,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           } else {
             pair_load_2d(sB, &tmB, bar, k0, n0);
           }
-          if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
+          if (++stage == PL::kStages) { stage = 0; phase ^= 1u; }
         }
       }
       if (!ok) {
@@ -305,13 +330,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       for (int tile = first; tile < p.num_tiles && ok; tile += step) {
         if (!pair_wait(&tempty[acc], acc_phase ^ 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(acc * PN);
+        const uint32_t d = tmem_base + (uint32_t)(acc * NT);
         int mb, nb, kb0, kb1;
         pair_coords(tile, p, mb, nb, kb0, kb1);
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!pair_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sA = smem_addr(smem + stage * kPairStage), sB = sA + kHalfTile;
+          const uint32_t sA = smem_addr(smem + stage * PL::kStage), sB = sA + kHalfTile;
 #pragma unroll
           for (int kk = 0; kk < PK / 16; ++kk) {
             // K-major: 32 bytes further inside the 128-byte swizzle row; MN-major: 16 rows of K further,
@@ -321,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             pair_mma(d, ad, bd, p.idesc, (kb - kb0) | kk ? 1u : 0u);
           }
           pair_commit(&empty[stage], 3);
-          if (++stage == kPairStages) { stage = 0; phase ^= 1u; }
+          if (++stage == PL::kStages) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
         pair_commit(&tfull[acc], 3);
@@ -339,9 +364,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else if (warp >= 4) {
     // ---------------- epilogue ----------------
     const int sub = warp & 3, half = (warp - 4) >> 2;
-    PairStager out(smem_addr(smem + kPairStagingOffset + (warp - 4) * kPairStaging), lane);
+    PairStager out(smem_addr(smem + PL::kStagingOffset + (warp - 4) * kPairStaging), lane);
     const uint32_t tempty0 = map_to_rank(smem_addr(tempty), 0);
     const float alpha = p.scale ? *p.scale : 1.0f;
+    // kTok*: warpgroup `half` takes the 32-token blocks half, half + 2, ...; lane = token after the turn
+    constexpr int kBlocks = NT >= 64 ? NT / 64 : 1;
+    float tm[kBlocks], ts[kBlocks];
+    int ty[kBlocks];
+    if (MODE == kTokLse)
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i) {
+        const int t = 32 * (half + 2 * i) + lane;
+        tm[i] = -INFINITY;
+        ts[i] = 0.0f;
+        const int64_t y = t < p.N ? p.targets[t] : -1;
+        ty[i] = y >= 0 && y < p.V ? (int)y : -1;
+      }
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int tile = first; tile < p.num_tiles; tile += step) {
@@ -349,18 +387,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int split_row = pair_coords(tile, p, mb, nb, kb0, kb1) * p.m_tiles * PM;
       const int row0 = mb * PM + 128 * rank + sub * 32, row = row0 + lane;
       const bool row_ok = row < p.M, warp_ok = row0 < p.M;
-      const int col0 = nb * PN + 128 * half;
+      const int col0 = nb * NT + 128 * half;
       int y = -1;              // kPairLse, kPairGrad: the target
       float lse2 = 0.0f, w = 0.0f;
       if (MODE == kPairLse && row_ok) {
         const int64_t t = p.targets[row];
-        if (t >= 0 && t < p.N) y = (int)t;
+        if (t >= 0 && t < p.V) y = (int)t;
       }
       if (MODE == kPairGrad && row_ok) {
-        y = p.row_y[row].x;
-        const float2 rw = p.row_w[row];
-        lse2 = rw.x;
-        w = rw.y;
+        const float4 r = p.rows[row];
+        lse2 = r.x;
+        w = r.y;
+        y = __float_as_int(r.z);
       }
       int full_ok = 0;
       if (lane == 0) full_ok = pair_wait(&tfull[acc], acc_phase, abort_flag) ? 1 : 0;
@@ -370,6 +408,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         break;
       }
       tc_fence_after();
+      if (kTok) {
+        const uint32_t tbase = tmem_base + (uint32_t)(acc * NT) + ((uint32_t)(sub * 32) << 16);
+        const uint32_t stage = out.buf;
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+          const int c = half + 2 * i;
+          if (32 * c >= NT || 32 * c >= p.N || !warp_ok) continue;
+          __syncwarp();
+          uint32_t a[32];
+          tmem_ld32(tbase + c * 32, a);  // lane: row of W, register: token
+          if (MODE == kTokLse) {
+            // element (row r, token j) at word 32 r + (r ^ j): rows and columns are both free of bank conflicts
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(stage + 4 * (32 * lane + (lane ^ j))), "r"(row_ok ? a[j] : 0xFF800000u) : "memory");
+            __syncwarp();
+#pragma unroll
+            for (int r = 0; r < 32; ++r)
+              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(a[r]) : "r"(stage + 4 * (32 * r + (r ^ lane))) : "memory");
+            if ((unsigned)(ty[i] - row0) < 32u) {
+              float zy;
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(zy) : "r"(stage + 4 * (32 * (ty[i] - row0) + ((ty[i] - row0) ^ lane))) : "memory");
+              p.zy[32 * c + lane] = zy;
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int r = 0; r < 32; ++r) mx[r & 3] = fmaxf(mx[r & 3], __uint_as_float(a[r]));
+            const float mn = fmaxf(tm[i], fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kLog2e);
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int r = 0; r < 32; ++r) sum[r & 3] += ce_exp2(fmaf(__uint_as_float(a[r]), kLog2e, -mn));
+            ts[i] = ts[i] * ce_exp2(tm[i] - mn) + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+            tm[i] = mn;
+          } else if (MODE == kTokGrad) {
+            // G by token: 32 tokens x 32 rows of W, 64 bytes a token
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float4 r = tok[32 * c + j];
+              const int ry = __float_as_int(r.z);
+              float q = ce_exp2(fmaf(__uint_as_float(a[j]), kLog2e, -r.x));
+              if (ry == p.v0 + row) q -= 1.0f;
+              const __nv_bfloat16 g = __float2bfloat16_rn(ry >= 0 ? r.y * q : 0.0f);
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + 64 * j + 2 * lane), "h"(__bfloat16_as_ushort(g)) : "memory");
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              out_store_2d(&tmC, stage, row0, 32 * c);
+              out_commit();
+            }
+          } else if (row_ok) {
+            float* dst = p.acc + ((int64_t)(split_row / PM / p.m_tiles) * p.N + 32 * c) * p.M + row;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (32 * c + j < p.N) {
+                float* q = dst + (int64_t)j * p.M;
+                *q = p.out == kOutF32Add ? *q + __uint_as_float(a[j]) : __uint_as_float(a[j]);
+              }
+          }
+        }
+      } else {
       const uint32_t tbase = tmem_base + (uint32_t)(acc * PN + 128 * half) + ((uint32_t)(sub * 32) << 16);
       float m2 = -INFINITY, s = 0.0f;  // kPairLse: the largest logit in log2 units, sum of 2^(z2 - m2)
 #pragma unroll 1
@@ -437,12 +538,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
       }
       if (MODE == kPairLse && row_ok && col0 < p.N) p.part[(int64_t)(2 * nb + half) * p.M + row] = make_float2(m2, s);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) remote_arrive(tempty0 + 8 * acc);
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
-    if (MODE != kPairLse && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (MODE == kTokLse)
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i) {
+        const int t = 32 * (half + 2 * i) + lane;
+        if (t < p.N && 32 * (half + 2 * i) < NT) p.part[(int64_t)(4 * blockIdx.x + sub) * p.N + t] = make_float2(tm[i], ts[i]);
+      }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   tc_fence_before();
@@ -515,18 +623,16 @@ __global__ void __launch_bounds__(1024) k_ce_scale(const float* __restrict__ dlo
   if (threadIdx.x == 0) *scale = (m == 0 || m >= 0x7F800000u) ? 1.0f : __uint_as_float(m);
 }
 
-// Per token: its target (-1 where it is ignored), {lse log2e, dloss / s}, and x with ignored rows zeroed.
+// Per token: {lse log2e, dloss / s, its target or -1 where it is ignored}, and x with ignored rows zeroed.
 __global__ void __launch_bounds__(256) k_ce_rows(const uint16_t* __restrict__ x, const int64_t* __restrict__ targets,
                                                  const float* __restrict__ lse, const float* __restrict__ dloss, int64_t T,
                                                  int d, int64_t V, int64_t ignore, const float* __restrict__ scale,
-                                                 int2* __restrict__ row_y, float2* __restrict__ row_w,
-                                                 uint16_t* __restrict__ xz) {
+                                                 float4* __restrict__ rows, uint16_t* __restrict__ xz) {
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
     const int64_t y = targets[t];
     const bool keep = y != ignore && y >= 0 && y < V;
     if (threadIdx.x == 0) {
-      row_y[t] = make_int2(keep ? (int)y : -1, 0);
-      row_w[t] = make_float2(lse[t] * kLog2e, keep ? dloss[t] / *scale : 0.0f);
+      rows[t] = make_float4(lse[t] * kLog2e, keep ? dloss[t] / *scale : 0.0f, __int_as_float(keep ? (int)y : -1), 0.0f);
     }
     const uint16_t* src = x + t * d;
     uint16_t* dst = xz + t * d;
@@ -610,11 +716,16 @@ int pair_group(const PairProblem& q, int m_tiles) {
   return 2048 / PM;
 }
 
+constexpr int kPlanPairs = 76;
+int pair_grid(const Launch& L, int64_t tiles) {
+  const int most = L.num_sms / 2 < kPlanPairs ? L.num_sms / 2 : kPlanPairs;
+  return tiles < most ? (int)tiles : most;
+}
+
 // Parts of K for a product with few tiles.  A block of 64 of K takes a pair about 0.33 us (25 TFLOP/s), a
 // tile's fill and epilogue about 2 us, and joining the parts a launch (3 us) and a read and a write of each
 // part at about 6 TB/s; the tiles run in waves of one per pair.  E.g. T = 1003, d = 2048, V = 50257: dX has 32 tiles
 // for 76 pairs, 245 us in one part.
-constexpr int kPlanPairs = 76;
 int pair_splits(int64_t M, int64_t N, int64_t K) {
   const int64_t m_pad = (M + PM - 1) / PM * PM, tiles = m_pad / PM * ((N + PN - 1) / PN), kb = (K + PK - 1) / PK;
   if (tiles >= 4 * kPlanPairs) return 1;
@@ -631,31 +742,34 @@ int pair_splits(int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
-template <int A_MN, int B_MN, int MODE>
+template <int A_MN, int B_MN, int MODE, int NT = 256>
 cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Launch& L) {
+  constexpr bool kTok = NT < 256;
   a.M = (int)q.M;
   a.N = (int)q.N;
   a.K = (int)q.K;
   a.m_tiles = (a.M + PM - 1) / PM;
-  a.n_tiles = (a.N + PN - 1) / PN;
+  a.n_tiles = (a.N + NT - 1) / NT;
   a.k_blocks = (a.K + PK - 1) / PK;
   if ((int64_t)a.m_tiles * a.n_tiles * splits > 0x7FFFFFFF) return cudaErrorInvalidValue;
   // a shorter last piece of the vocabulary may need fewer parts; the others then get nothing added
   a.split_blocks = (a.k_blocks + splits - 1) / splits;
   a.splits = (a.k_blocks + a.split_blocks - 1) / a.split_blocks;
   a.num_tiles = a.m_tiles * a.n_tiles * a.splits;
-  a.group = pair_group(q, a.m_tiles);
+  a.group = kTok ? a.m_tiles : pair_group(q, a.m_tiles);
   // fp32 sums, bf16 operands and their majors, N / 8 and M / 16 of the pair's tile
   a.idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
-            ((uint32_t)(PN >> 3) << 17) | ((uint32_t)(PM >> 4) << 24);
+            ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(PM >> 4) << 24);
   a.status = L.status;
   CUtensorMap ta, tb, tc;
   bool ok = A_MN ? make_map(&ta, q.A, q.M, q.K, q.lda, 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)
                  : make_map(&ta, q.A, q.K, q.M, q.lda, 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
   ok = ok && (B_MN ? make_map(&tb, q.B, q.N, q.K, q.ldb, 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)
-                   : make_map(&tb, q.B, q.K, q.N, q.ldb, 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B));
+                   : make_map(&tb, q.B, q.K, q.N, q.ldb, 2, 64, NT / 2, CU_TENSOR_MAP_SWIZZLE_128B));
   tc = ta;
-  if (MODE != kPairLse) {
+  if (MODE == kTokGrad) {  // by token: [N, M]
+    ok = ok && make_map(&tc, q.C, q.M, q.N, q.ldc, 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE);
+  } else if (!kTok && MODE != kPairLse) {
     const bool f32 = MODE != kPairGrad && (a.out == kOutF32Store || a.out == kOutF32Add);
     ok = ok && make_map(&tc, q.C, q.N, splits > 1 ? (int64_t)splits * a.m_tiles * PM : q.M, q.ldc, f32 ? 4 : 2, 32, 32,
                         f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
@@ -666,12 +780,12 @@ cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Laun
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!(configured.load() >> dev & 1)) {
-    e = cudaFuncSetAttribute(k_ce_gemm<A_MN, B_MN, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+    e = cudaFuncSetAttribute(k_ce_gemm<A_MN, B_MN, MODE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, PairPlan<NT>::kSmem);
     if (e != cudaSuccess) return e;
     configured.fetch_or(1ull << dev);
   }
-  const int pairs = L.num_sms / 2 < a.num_tiles ? L.num_sms / 2 : a.num_tiles;
-  k_ce_gemm<A_MN, B_MN, MODE><<<2 * pairs, kPairThreads, kPairSmem, L.stream>>>(ta, tb, tc, a);
+  const int pairs = pair_grid(L, a.num_tiles);
+  k_ce_gemm<A_MN, B_MN, MODE, NT><<<2 * pairs, kPairThreads, PairPlan<NT>::kSmem, L.stream>>>(ta, tb, tc, a);
   return launched(L);
 }
 
@@ -693,15 +807,15 @@ CePlan ce_plan(int64_t T, int64_t d, int64_t V) {
   CePlan p{};
   p.piece = ce_piece(T, V);
   const int64_t n = p.piece < V ? p.piece : V;
-  p.dx_splits = pair_splits(T, d, n);
+  p.dx_splits = T <= kTokMax ? pair_splits(d, T, n) : pair_splits(T, d, n);
   p.dw_splits = pair_splits(n, d, T);
   return p;
 }
 
 struct CeWs {
-  float2 *part, *row_w;
+  float2* part;
+  float4* rows;
   float *zy, *acc, *dw_part, *scale;
-  int2* row_y;
   uint16_t *G, *xz;
 };
 size_t ce_layout(int64_t T, int64_t d, int64_t V, bool bwd, uint8_t* base, CeWs* w) {
@@ -717,14 +831,14 @@ size_t ce_layout(int64_t T, int64_t d, int64_t V, bool bwd, uint8_t* base, CeWs*
     t.G = (uint16_t*)take(T * p.piece * 2);
     t.xz = (uint16_t*)take(T * d * 2);
     const int64_t m_pad = (T + PM - 1) / PM * PM;
-    if (p.dx_splits > 1) t.acc = (float*)take(p.dx_splits * m_pad * d * 4);
+    if (T <= kTokMax) t.acc = (float*)take(p.dx_splits * T * d * 4);
+    else if (p.dx_splits > 1) t.acc = (float*)take(p.dx_splits * m_pad * d * 4);
     else if (p.piece < V) t.acc = (float*)take(T * d * 4);
     if (p.dw_splits > 1) t.dw_part = (float*)take(p.dw_splits * p.piece * d * 4);
-    t.row_y = (int2*)take(T * 8);
-    t.row_w = (float2*)take(T * 8);
+    t.rows = (float4*)take(T * 16);
     t.scale = (float*)take(4);
   } else {
-    t.part = (float2*)take(2 * ((V + PN - 1) / PN) * T * 8);
+    t.part = (float2*)take(T <= kTokMax ? 8 * kPlanPairs * T * 8 : 2 * ((V + PN - 1) / PN) * T * 8);
     t.zy = (float*)take(T * 4);
   }
   if (w) *w = t;
@@ -741,11 +855,21 @@ cudaError_t launch_ce_fwd(const uint16_t* x, const uint16_t* W, const int64_t* t
   ce_layout(T, d, V, false, static_cast<uint8_t*>(ws), &w);
   PairArgs a{};
   a.targets = targets;
+  a.V = (int)V;
   a.part = w.part;
   a.zy = w.zy;
-  cudaError_t e = launch_pair<0, 0, kPairLse>(PairProblem{T, V, d, x, d, W, d, nullptr, 0}, 1, a, L);
+  cudaError_t e;
+  int pieces;
+  if (T <= kTokMax) {
+    const PairProblem q{V, T, d, W, d, x, d, nullptr, 0};
+    e = T <= 32 ? launch_pair<0, 0, kTokLse, 32>(q, 1, a, L)
+        : T <= 64 ? launch_pair<0, 0, kTokLse, 64>(q, 1, a, L) : launch_pair<0, 0, kTokLse, 128>(q, 1, a, L);
+    pieces = 8 * pair_grid(L, (V + PM - 1) / PM);
+  } else {
+    e = launch_pair<0, 0, kPairLse>(PairProblem{T, V, d, x, d, W, d, nullptr, 0}, 1, a, L);
+    pieces = (int)((V + 127) / 128);
+  }
   if (e != cudaSuccess) return e;
-  const int pieces = (int)((V + 127) / 128);
   k_ce_finish<<<(unsigned)((T + 31) / 32), 1024, 0, L.stream>>>(w.part, pieces, T, targets, V, ignore, w.zy, loss, lse,
                                                                L.status);
   return launched(L);
@@ -763,28 +887,39 @@ cudaError_t launch_ce_bwd(const uint16_t* x, const uint16_t* W, const int64_t* t
   k_ce_scale<<<1, 1024, 0, L.stream>>>(dloss, targets, T, V, ignore, w.scale, L.status);
   if ((e = launched(L)) != cudaSuccess) return e;
   k_ce_rows<<<(unsigned)(T < 8 * L.num_sms ? T : 8 * L.num_sms), 256, 0, L.stream>>>(x, targets, lse, dloss, T, d, V, ignore,
-                                                                                 w.scale, w.row_y, w.row_w, w.xz);
+                                                                                 w.scale, w.rows, w.xz);
   if ((e = launched(L)) != cudaSuccess) return e;
   for (int64_t v0 = 0; v0 < V; v0 += piece) {
     const int64_t n = V - v0 < piece ? V - v0 : piece;
     const bool first = v0 == 0, last = v0 + n == V;
-    PairArgs a{};
+    PairArgs a{}, ax{};
     a.v0 = (int)v0;
-    a.row_y = w.row_y;
-    a.row_w = w.row_w;
-    e = launch_pair<0, 0, kPairGrad>(PairProblem{T, n, d, x, d, W + v0 * d, d, w.G, piece}, 1, a, L);
-    if (e != cudaSuccess) return e;
-    // dX (+)= G W[piece]: the sum so far stays in fp32 (its parts of K apart), s joins it at the end
-    PairArgs ax{};
-    const int xs = plan.dx_splits;
+    a.rows = w.rows;
     ax.acc = w.acc;
-    ax.out = xs > 1 || !last ? (first ? kOutF32Store : kOutF32Add) : (first ? kOutBf16 : kOutBf16Join);
-    if (xs == 1 && last) ax.scale = w.scale;
-    void* to = xs > 1 || !last ? (void*)w.acc : (void*)dX;
-    e = launch_pair<0, 1, kPairDx>(PairProblem{T, d, n, w.G, piece, W + v0 * d, d, to, d}, xs, ax, L);
-    if (e != cudaSuccess) return e;
-    if (xs > 1 && last) {
-      k_ce_join<<<join_blocks, 256, 0, L.stream>>>(w.acc, xs, (T + PM - 1) / PM * PM, T, d, w.scale, dX, 0);
+    const int xs = plan.dx_splits;
+    if (T <= kTokMax) {
+      const PairProblem q{n, T, d, W + v0 * d, d, x, d, w.G, piece};
+      const PairProblem qx{d, T, n, W + v0 * d, d, w.G, piece, nullptr, 0};
+      ax.out = first ? kOutF32Store : kOutF32Add;
+      e = T <= 32 ? launch_pair<0, 0, kTokGrad, 32>(q, 1, a, L)
+          : T <= 64 ? launch_pair<0, 0, kTokGrad, 64>(q, 1, a, L) : launch_pair<0, 0, kTokGrad, 128>(q, 1, a, L);
+      if (e != cudaSuccess) return e;
+      e = T <= 32 ? launch_pair<1, 0, kTokDx, 32>(qx, xs, ax, L)
+          : T <= 64 ? launch_pair<1, 0, kTokDx, 64>(qx, xs, ax, L) : launch_pair<1, 0, kTokDx, 128>(qx, xs, ax, L);
+      if (e != cudaSuccess) return e;
+    } else {
+      e = launch_pair<0, 0, kPairGrad>(PairProblem{T, n, d, x, d, W + v0 * d, d, w.G, piece}, 1, a, L);
+      if (e != cudaSuccess) return e;
+      // dX (+)= G W[piece]: the sum so far stays in fp32 (its parts of K apart), s joins it at the end
+      ax.out = xs > 1 || !last ? (first ? kOutF32Store : kOutF32Add) : (first ? kOutBf16 : kOutBf16Join);
+      if (xs == 1 && last) ax.scale = w.scale;
+      void* to = xs > 1 || !last ? (void*)w.acc : (void*)dX;
+      e = launch_pair<0, 1, kPairDx>(PairProblem{T, d, n, w.G, piece, W + v0 * d, d, to, d}, xs, ax, L);
+      if (e != cudaSuccess) return e;
+    }
+    if (last && (xs > 1 || T <= kTokMax)) {
+      const int64_t pad = T <= kTokMax ? T : (T + PM - 1) / PM * PM;
+      k_ce_join<<<join_blocks, 256, 0, L.stream>>>(w.acc, xs, pad, T, d, w.scale, dX, 0);
       if ((e = launched(L)) != cudaSuccess) return e;
     }
     // dW[piece] = s G^T x
