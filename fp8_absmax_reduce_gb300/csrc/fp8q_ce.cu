@@ -43,7 +43,11 @@ __device__ __forceinline__ float ce_exp2(float x) {
 //   warp 1      the even CTA's MMA issuer; its commits free the stage, and hand over the
 //               accumulator, in both CTAs;
 //   warp 2      tensor memory;
-//   warps 4-11  epilogue: warp w reads lanes 32 (w % 4) .., columns 128 (w / 4 - 1) ...
+//   warps 3-10  epilogue: warp w reads lanes 32 (w % 4) ..; the first four take columns 0-127, the others 128-255.
+// The tensor cores' fp32 sums drop what falls below the sum's last place at each step, so a logit's error grows
+// with the steps; the loss's logits are therefore summed over K in parts of 1024 that the epilogue adds in
+// registers (the accumulators change hands after each part; measured at T = 4096, d = 3584, V = 50257: the loss's error
+// 2.7e-6 -> 0.7e-6 of its norm, 868 -> 888 us).
 // Up to 128 tokens the operands trade places (kTok*): the 256 rows of a pair's tile are rows of W (of W^T for
 // dX) and its NT = 32, 64 or 128 columns the tokens, so that the tensor cores do not work on padding (256 rows
 // for 24 tokens: 10.6 us of MMAs a tile at d = 2048 against 12 us for its operands from HBM) and W streams
@@ -55,35 +59,38 @@ __device__ __forceinline__ float ce_exp2(float x) {
 // ---------------------------------------------------------------------------
 constexpr int PM = 256, PN = 256, PK = 64;
 constexpr int kHalfTile = 128 * 128;  // bytes: 128 rows (or columns) x 64 bf16
-constexpr int kPairThreads = 384;
-constexpr int kPairStaging = 4096;  // per epilogue warp
-constexpr int kTokMax = 128;        // tokens up to which the operands trade places
-
-// The shared memory of a CTA for tiles of NT columns.
-template <int NT>
-struct PairPlan {
-  static constexpr int kB = NT / 2 * 128;  // bytes of its share of B in a stage
-  static constexpr int kStage = kHalfTile + kB;
-  static constexpr int kStages = NT == 256 ? 6 : NT == 128 ? 7 : NT == 64 ? 9 : 10;
-  static constexpr int kStagingOffset = kStages * kStage;
-  static constexpr int kTokOffset = kStagingOffset + 8 * kPairStaging;
-  static constexpr int kBarOffset = kTokOffset + (NT < 256 ? NT * 16 : 0);
-  static constexpr int kSmem = kBarOffset + 256 + 1024;
-  static_assert(kSmem <= 232448, "shared memory per CTA");
-  static_assert(kStage % 1024 == 0, "swizzle atoms");
-};
-constexpr uint64_t kCopyDrainNs = 5000000ull;  // far beyond any copy in flight
+constexpr int kEpiWarp = 3;           // the first of the 8 epilogue warps
+constexpr int kPairThreads = 32 * (kEpiWarp + 8);
+constexpr int kTokMax = 128;  // tokens up to which the operands trade places
+constexpr int kSegBlocks = 16; // K of a partial sum of the logits, in blocks of 64
 
 enum PairMode {
   kPairLse = 0,   // per row and 128 columns: log2-domain maximum and sum; the target's logit
   kPairGrad = 1,  // G / s as bf16
   kPairDx = 2,    // dX: fp32 store, fp32 add or bf16 of the joined sum
   kPairDw = 3,    // dW: bf16 or fp32
-  kTokLse = 4,    // the same three with the tokens as columns: statistics of each warp's rows of W
+  kTokLse = 4,    // the same three with the tokens as columns: statistics of a CTA's rows of W
   kTokGrad = 5,   //   G / s, stored by token
   kTokDx = 6,     //   dX's sum in fp32, by token, the parts of K apart
 };
 enum PairOut { kOutF32Store = 0, kOutF32Add = 1, kOutBf16 = 2, kOutBf16Join = 3 };
+
+// The shared memory of a CTA for tiles of NT columns.  dW's products are short where there are few
+// tokens, and bound by its stores: it trades a stage for staging buffers of two blocks of 4 KB a warp.
+template <int MODE, int NT>
+struct PairPlan {
+  static constexpr int kB = NT / 2 * 128;  // bytes of its share of B in a stage
+  static constexpr int kStage = kHalfTile + kB;
+  static constexpr int kStages = MODE == kPairDw ? 5 : NT == 256 ? 6 : NT == 128 ? 7 : NT == 64 ? 9 : 10;
+  static constexpr int kStaging = MODE == kPairDw ? 8192 : 4096;  // per epilogue warp
+  static constexpr int kStagingOffset = kStages * kStage;
+  static constexpr int kTokOffset = kStagingOffset + 8 * kStaging;
+  static constexpr int kBarOffset = kTokOffset + (NT < 256 ? NT * 16 : 0);
+  static constexpr int kSmem = kBarOffset + 256 + 1024;
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+  static_assert(kStage % 1024 == 0, "swizzle atoms");
+};
+constexpr uint64_t kCopyDrainNs = 5000000ull;  // far beyond any copy in flight
 
 struct PairArgs {
   int M, N, K;
@@ -97,7 +104,7 @@ struct PairArgs {
   int v0;                   // kPairGrad: the piece's first column
   const int64_t* targets;   // kPairLse, kTokLse
   int V;                    // kPairLse, kTokLse
-  float2* part;             // (maximum log2e, sum) pairs: kPairLse [2 n_tiles][M], kTokLse [4 CTAs][N]
+  float2* part;             // (maximum log2e, sum) pairs: kPairLse [2 n_tiles][M], kTokLse [CTAs][N]
   float* zy;                // kPairLse, kTokLse: each token's target logit
   const float4* rows;       // kPairGrad, kTokGrad: each token's {lse log2e, dloss / s, target or -1 (int bits), 0}
   unsigned* status;
@@ -183,45 +190,98 @@ __device__ __forceinline__ void sts_v4(uint32_t addr, uint32_t a, uint32_t b, ui
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// A warp's 32 x 32 block of a tile on its way out: staged in the layout of the tensor map's swizzle
-// (64 bytes for bf16, 128 for fp32) and stored by lane 0.  bf16 blocks alternate between the buffer's halves.
+// A warp's block of a tile on its way out: staged in the layout of the tensor map's swizzle and stored by
+// lane 0, the blocks taking the warp's BYTES of staging in turn.  Rows of 64 bytes: 32 bf16; of 128: 64 bf16 or 32 fp32.
+template <int BYTES>
 struct PairStager {
   uint32_t buf;
-  int lane, flip = 0;
+  int lane, turn = 0;
   __device__ __forceinline__ PairStager(uint32_t b, int l) : buf(b), lane(l) {}
-  __device__ __forceinline__ void bf16(const CUtensorMap* tm, const float (&v)[32], int x, int y) {
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+  template <int BLOCK>
+  __device__ __forceinline__ uint32_t acquire() {
+    constexpr int n = BYTES / BLOCK;
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(n - 1) : "memory");
     __syncwarp();
-    const uint32_t b = buf + 2048 * flip;
+    const uint32_t b = buf + BLOCK * turn;
+    turn = turn + 1 == n ? 0 : turn + 1;
+    return b;
+  }
+  __device__ __forceinline__ void publish(const CUtensorMap* tm, uint32_t b, int x, int y, bool add = false) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+      if (add) out_add_2d(tm, b, x, y);
+      else out_store_2d(tm, b, x, y);
+      out_commit();
+    }
+  }
+  __device__ __forceinline__ void bf16(const CUtensorMap* tm, const float (&v)[32], int x, int y) {
+    const uint32_t b = acquire<2048>();
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       sts_v4(b + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), pack_bf16x2(v[8 * q], v[8 * q + 1]),
              pack_bf16x2(v[8 * q + 2], v[8 * q + 3]), pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
              pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane == 0) {
-      out_store_2d(tm, b, x, y);
-      out_commit();
-    }
-    flip ^= 1;
+    publish(tm, b, x, y);
   }
-  __device__ __forceinline__ void f32(const CUtensorMap* tm, const float (&v)[32], int x, int y, bool add) {
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    __syncwarp();
+  __device__ __forceinline__ void bf16_wide(const CUtensorMap* tm, const uint32_t (&a)[32], const uint32_t (&c)[32],
+                                            float f, int x, int y) {
+    const uint32_t b = acquire<4096>();
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int j = 8 * (q & 3) + 2 * k;
+        w[k] = pack_bf16x2(f * __uint_as_float(q < 4 ? a[j] : c[j]), f * __uint_as_float(q < 4 ? a[j + 1] : c[j + 1]));
+      }
+      sts_v4(b + lane * 128 + ((q ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+    }
+    publish(tm, b, x, y);
+  }
+  __device__ __forceinline__ void f32(const CUtensorMap* tm, const uint32_t (&a)[32], float f, int x, int y, bool add) {
+    const uint32_t b = acquire<4096>();
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-      sts_v4(buf + lane * 128 + ((q ^ (lane & 7)) << 4), __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-             __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane == 0) {
-      if (add) out_add_2d(tm, buf, x, y);
-      else out_store_2d(tm, buf, x, y);
-      out_commit();
-    }
+      sts_v4(b + lane * 128 + ((q ^ (lane & 7)) << 4), __float_as_uint(f * __uint_as_float(a[4 * q])),
+             __float_as_uint(f * __uint_as_float(a[4 * q + 1])), __float_as_uint(f * __uint_as_float(a[4 * q + 2])),
+             __float_as_uint(f * __uint_as_float(a[4 * q + 3])));
+    publish(tm, b, x, y, add);
   }
 };
+
+// (maximum, sum) of logits in log2 units, brought together; a pair that holds nothing is (-inf, 0).
+__device__ __forceinline__ float2 ce_join2(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  if (m == -INFINITY) return make_float2(m, a.y + b.y);
+  return make_float2(m, a.y * ce_exp2(a.x - m) + b.y * ce_exp2(b.x - m));
+}
+// 16 columns of this thread's tensor-memory lane, added to z.
+__device__ __forceinline__ void ce_tmem_add16(uint32_t taddr, float* z) {
+  uint32_t a[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]),
+        "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int j = 0; j < 16; ++j) z[j] += __uint_as_float(a[j]);
+}
+
+// The pair of N logits.
+template <int N>
+__device__ __forceinline__ float2 ce_pair(const float (&z)[N]) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int j = 0; j < N; ++j) mx[j & 3] = fmaxf(mx[j & 3], z[j]);
+  const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kLog2e;
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < N; ++j) sum[j & 3] += ce_exp2(fmaf(z[j], kLog2e, -m));
+  return make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+}
 
 // Tile -> (part of K, M tile, N tile): a part's tiles in groups of p.group M tiles, all N tiles of a group,
 // M fastest inside it.  Its blocks of K are [k0, k1).
@@ -241,7 +301,8 @@ template <int A_MN, int B_MN, int MODE, int NT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_ce_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmC, const PairArgs p) {
-  using PL = PairPlan<NT>;
+  using PL = PairPlan<MODE, NT>;
+  constexpr bool kSeg = MODE == kPairLse || MODE == kTokLse;  // the sum over K comes in parts
   constexpr bool kTok = NT < 256;
   static_assert(kTok == (MODE >= kTokLse) && !(kTok && B_MN), "the tokens are a K-major operand");
   extern __shared__ uint8_t pair_smem[];
@@ -328,29 +389,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int tile = first; tile < p.num_tiles && ok; tile += step) {
-        if (!pair_wait(&tempty[acc], acc_phase ^ 1u, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(acc * NT);
         int mb, nb, kb0, kb1;
         pair_coords(tile, p, mb, nb, kb0, kb1);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!pair_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
+        for (int kb = kb0; kb < kb1 && ok;) {
+          const int begin = kb, end = kSeg ? min(kb + kSegBlocks, kb1) : kb1;
+          if (!pair_wait(&tempty[acc], acc_phase ^ 1u, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sA = smem_addr(smem + stage * PL::kStage), sB = sA + kHalfTile;
+          const uint32_t d = tmem_base + (uint32_t)(acc * NT);
+          for (; kb < end; ++kb) {
+            if (!pair_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sA = smem_addr(smem + stage * PL::kStage), sB = sA + kHalfTile;
 #pragma unroll
-          for (int kk = 0; kk < PK / 16; ++kk) {
-            // K-major: 32 bytes further inside the 128-byte swizzle row; MN-major: 16 rows of K further,
-            // the second 64-element block of MN 8 KB on
-            const uint64_t ad = A_MN ? smem_desc_sw128(sA + kk * 2048, kHalfTile / 2, 1024) : smem_desc_sw128(sA + kk * 32, 16, 1024);
-            const uint64_t bd = B_MN ? smem_desc_sw128(sB + kk * 2048, kHalfTile / 2, 1024) : smem_desc_sw128(sB + kk * 32, 16, 1024);
-            pair_mma(d, ad, bd, p.idesc, (kb - kb0) | kk ? 1u : 0u);
+            for (int kk = 0; kk < PK / 16; ++kk) {
+              // K-major: 32 bytes further inside the 128-byte swizzle row; MN-major: 16 rows of K further,
+              // the second 64-element block of MN 8 KB on
+              const uint64_t ad = A_MN ? smem_desc_sw128(sA + kk * 2048, kHalfTile / 2, 1024) : smem_desc_sw128(sA + kk * 32, 16, 1024);
+              const uint64_t bd = B_MN ? smem_desc_sw128(sB + kk * 2048, kHalfTile / 2, 1024) : smem_desc_sw128(sB + kk * 32, 16, 1024);
+              pair_mma(d, ad, bd, p.idesc, (kb - begin) | kk ? 1u : 0u);
+            }
+            pair_commit(&empty[stage], 3);
+            if (++stage == PL::kStages) { stage = 0; phase ^= 1u; }
           }
-          pair_commit(&empty[stage], 3);
-          if (++stage == PL::kStages) { stage = 0; phase ^= 1u; }
+          if (!ok) break;
+          pair_commit(&tfull[acc], 3);
+          if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
         }
-        if (!ok) break;
-        pair_commit(&tfull[acc], 3);
-        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
       if (!ok) {
         atomicOr(p.status, kStatusTimeout);
@@ -361,195 +425,244 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int dummy = 0;
       pair_wait(drain, 0, &dummy);
     }
-  } else if (warp >= 4) {
+  } else if (warp >= kEpiWarp) {
     // ---------------- epilogue ----------------
-    const int sub = warp & 3, half = (warp - 4) >> 2;
-    PairStager out(smem_addr(smem + PL::kStagingOffset + (warp - 4) * kPairStaging), lane);
+    const int sub = warp & 3, half = (warp - kEpiWarp) >> 2;
+    PairStager<PL::kStaging> out(smem_addr(smem + PL::kStagingOffset + (warp - kEpiWarp) * PL::kStaging), lane);
     const uint32_t tempty0 = map_to_rank(smem_addr(tempty), 0);
     const float alpha = p.scale ? *p.scale : 1.0f;
     // kTok*: warpgroup `half` takes the 32-token blocks half, half + 2, ...; lane = token after the turn
     constexpr int kBlocks = NT >= 64 ? NT / 64 : 1;
-    float tm[kBlocks], ts[kBlocks];
+    float2 tp[kBlocks];
     int ty[kBlocks];
     if (MODE == kTokLse)
 #pragma unroll
       for (int i = 0; i < kBlocks; ++i) {
         const int t = 32 * (half + 2 * i) + lane;
-        tm[i] = -INFINITY;
-        ts[i] = 0.0f;
+        tp[i] = make_float2(-INFINITY, 0.0f);
         const int64_t y = t < p.N ? p.targets[t] : -1;
         ty[i] = y >= 0 && y < p.V ? (int)y : -1;
       }
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int tile = first; tile < p.num_tiles; tile += step) {
-      int mb, nb, kb0, kb1;
-      const int split_row = pair_coords(tile, p, mb, nb, kb0, kb1) * p.m_tiles * PM;
-      const int row0 = mb * PM + 128 * rank + sub * 32, row = row0 + lane;
-      const bool row_ok = row < p.M, warp_ok = row0 < p.M;
-      const int col0 = nb * NT + 128 * half;
-      int y = -1;              // kPairLse, kPairGrad: the target
-      float lse2 = 0.0f, w = 0.0f;
-      if (MODE == kPairLse && row_ok) {
-        const int64_t t = p.targets[row];
-        if (t >= 0 && t < p.V) y = (int)t;
-      }
-      if (MODE == kPairGrad && row_ok) {
-        const float4 r = p.rows[row];
-        lse2 = r.x;
-        w = r.y;
-        y = __float_as_int(r.z);
-      }
-      int full_ok = 0;
-      if (lane == 0) full_ok = pair_wait(&tfull[acc], acc_phase, abort_flag) ? 1 : 0;
-      if (!__shfl_sync(0xFFFFFFFFu, full_ok, 0)) {
+    // lane 0 waits for the accumulator and the warp follows its result (what comes is warp-collective)
+    auto take = [&]() -> bool {
+      int ok = 0;
+      if (lane == 0) ok = pair_wait(&tfull[acc], acc_phase, abort_flag) ? 1 : 0;
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      if (!ok) {
         atomicOr(p.status, kStatusTimeout);
         *abort_flag = 1;
-        break;
       }
       tc_fence_after();
-      if (kTok) {
-        const uint32_t tbase = tmem_base + (uint32_t)(acc * NT) + ((uint32_t)(sub * 32) << 16);
-        const uint32_t stage = out.buf;
-#pragma unroll
-        for (int i = 0; i < kBlocks; ++i) {
-          const int c = half + 2 * i;
-          if (32 * c >= NT || 32 * c >= p.N || !warp_ok) continue;
-          __syncwarp();
-          uint32_t a[32];
-          tmem_ld32(tbase + c * 32, a);  // lane: row of W, register: token
-          if (MODE == kTokLse) {
-            // element (row r, token j) at word 32 r + (r ^ j): rows and columns are both free of bank conflicts
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(stage + 4 * (32 * lane + (lane ^ j))), "r"(row_ok ? a[j] : 0xFF800000u) : "memory");
-            __syncwarp();
-#pragma unroll
-            for (int r = 0; r < 32; ++r)
-              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(a[r]) : "r"(stage + 4 * (32 * r + (r ^ lane))) : "memory");
-            if ((unsigned)(ty[i] - row0) < 32u) {
-              float zy;
-              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(zy) : "r"(stage + 4 * (32 * (ty[i] - row0) + ((ty[i] - row0) ^ lane))) : "memory");
-              p.zy[32 * c + lane] = zy;
-            }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int r = 0; r < 32; ++r) mx[r & 3] = fmaxf(mx[r & 3], __uint_as_float(a[r]));
-            const float mn = fmaxf(tm[i], fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kLog2e);
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int r = 0; r < 32; ++r) sum[r & 3] += ce_exp2(fmaf(__uint_as_float(a[r]), kLog2e, -mn));
-            ts[i] = ts[i] * ce_exp2(tm[i] - mn) + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
-            tm[i] = mn;
-          } else if (MODE == kTokGrad) {
-            // G by token: 32 tokens x 32 rows of W, 64 bytes a token
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float4 r = tok[32 * c + j];
-              const int ry = __float_as_int(r.z);
-              float q = ce_exp2(fmaf(__uint_as_float(a[j]), kLog2e, -r.x));
-              if (ry == p.v0 + row) q -= 1.0f;
-              const __nv_bfloat16 g = __float2bfloat16_rn(ry >= 0 ? r.y * q : 0.0f);
-              asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + 64 * j + 2 * lane), "h"(__bfloat16_as_ushort(g)) : "memory");
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-              out_store_2d(&tmC, stage, row0, 32 * c);
-              out_commit();
-            }
-          } else if (row_ok) {
-            float* dst = p.acc + ((int64_t)(split_row / PM / p.m_tiles) * p.N + 32 * c) * p.M + row;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (32 * c + j < p.N) {
-                float* q = dst + (int64_t)j * p.M;
-                *q = p.out == kOutF32Add ? *q + __uint_as_float(a[j]) : __uint_as_float(a[j]);
-              }
-          }
-        }
-      } else {
-      const uint32_t tbase = tmem_base + (uint32_t)(acc * PN + 128 * half) + ((uint32_t)(sub * 32) << 16);
-      float m2 = -INFINITY, s = 0.0f;  // kPairLse: the largest logit in log2 units, sum of 2^(z2 - m2)
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        const int col = col0 + c * 32, ncol = min(32, p.N - col);
-        if (!warp_ok || ncol <= 0) break;
-        __syncwarp();
-        uint32_t a[32];
-        tmem_ld32(tbase + c * 32, a);
-        if (MODE == kPairLse) {
-          if (ncol < 32)
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j >= ncol) a[j] = 0xFF800000u;
-          if ((unsigned)(y - col) < 32u) {
-            float zy = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (y - col == j) zy = __uint_as_float(a[j]);
-            p.zy[row] = zy;
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(a[j]));
-          const float cm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kLog2e;
-          const float mn = fmaxf(m2, cm);
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int j = 0; j < 32; ++j) sum[j & 3] += ce_exp2(fmaf(__uint_as_float(a[j]), kLog2e, -mn));
-          s = s * ce_exp2(m2 - mn) + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
-          m2 = mn;
-        } else {
-          float v[32];
-          if (MODE == kPairGrad) {
-            const int yc = y - p.v0 - col;
-            const bool keep = y >= 0;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              float q = ce_exp2(fmaf(__uint_as_float(a[j]), kLog2e, -lse2));
-              if (j == yc) q -= 1.0f;
-              v[j] = keep ? w * q : 0.0f;
-            }
-            out.bf16(&tmC, v, col, row0);
-          } else if (MODE == kPairDx && p.out == kOutBf16Join) {
-            const float* old = p.acc + (int64_t)row * p.N + col;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (row_ok && 4 * q < ncol) o = *reinterpret_cast<const float4*>(old + 4 * q);
-              v[4 * q] = alpha * (__uint_as_float(a[4 * q]) + o.x);
-              v[4 * q + 1] = alpha * (__uint_as_float(a[4 * q + 1]) + o.y);
-              v[4 * q + 2] = alpha * (__uint_as_float(a[4 * q + 2]) + o.z);
-              v[4 * q + 3] = alpha * (__uint_as_float(a[4 * q + 3]) + o.w);
-            }
-            out.bf16(&tmC, v, col, row0);
-          } else if (p.out == kOutBf16) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = alpha * __uint_as_float(a[j]);
-            out.bf16(&tmC, v, col, row0);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = alpha * __uint_as_float(a[j]);
-            out.f32(&tmC, v, col, split_row + row0, p.out == kOutF32Add);
-          }
-        }
-      }
-      if (MODE == kPairLse && row_ok && col0 < p.N) p.part[(int64_t)(2 * nb + half) * p.M + row] = make_float2(m2, s);
-      }
+      return ok != 0;
+    };
+    auto release = [&]() {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) remote_arrive(tempty0 + 8 * acc);
       if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
-    }
-    if (MODE == kTokLse)
+    };
+    for (int tile = first; tile < p.num_tiles; tile += step) {
+      int mb, nb, kb0, kb1;
+      const int part = pair_coords(tile, p, mb, nb, kb0, kb1);
+      const int row0 = mb * PM + 128 * rank + sub * 32, row = row0 + lane;
+      const bool row_ok = row < p.M, warp_ok = row0 < p.M;
+      const uint32_t lanes = tmem_base + ((uint32_t)(sub * 32) << 16);
+      if constexpr (MODE == kPairLse) {
+        const int col0 = nb * NT + 128 * half;
+        int y = -1;
+        if (row_ok) {
+          const int64_t t = p.targets[row];
+          if (t >= 0 && t < p.V) y = (int)t;
+        }
+        float z[128];
 #pragma unroll
-      for (int i = 0; i < kBlocks; ++i) {
-        const int t = 32 * (half + 2 * i) + lane;
-        if (t < p.N && 32 * (half + 2 * i) < NT) p.part[(int64_t)(4 * blockIdx.x + sub) * p.N + t] = make_float2(tm[i], ts[i]);
+        for (int j = 0; j < 128; ++j) z[j] = 0.0f;
+        bool ok = true;
+#pragma unroll 1
+        for (int kb = kb0; kb < kb1; kb += kSegBlocks) {
+          if (!(ok = take())) break;
+          if (warp_ok)
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              ce_tmem_add16(lanes + (uint32_t)(acc * NT + 128 * half + 16 * c), z + 16 * c);
+          release();
+        }
+        if (!ok) break;
+        if (row_ok && col0 < p.N) {
+          if ((unsigned)(y - col0) < 128u) {
+            float zy = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 128; ++j)
+              if (y - col0 == j) zy = z[j];
+            p.zy[row] = zy;
+          }
+          if (col0 + 128 > p.N)
+#pragma unroll
+            for (int j = 0; j < 128; ++j)
+              if (col0 + j >= p.N) z[j] = -INFINITY;
+          p.part[(int64_t)(2 * nb + half) * p.M + row] = ce_pair(z);
+        }
+        __syncwarp();
+      } else if constexpr (MODE == kTokLse) {
+        float z[kBlocks][32];
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z[i][j] = 0.0f;
+        bool ok = true;
+#pragma unroll 1
+        for (int kb = kb0; kb < kb1; kb += kSegBlocks) {
+          if (!(ok = take())) break;
+#pragma unroll
+          for (int i = 0; i < kBlocks; ++i) {
+            const int c = half + 2 * i;
+            if (32 * c >= NT || !warp_ok) continue;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)  // lane: row of W, register: token
+              ce_tmem_add16(lanes + (uint32_t)(acc * NT + 32 * c + 16 * q), z[i] + 16 * q);
+          }
+          release();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+          const int c = half + 2 * i;
+          if (32 * c >= NT || 32 * c >= p.N || !warp_ok) continue;
+          // element (row r, token j) at word 32 r + (r ^ j): rows and columns are both free of bank conflicts
+          const uint32_t stage = out.buf;
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage + 4 * (32 * lane + (lane ^ j))), "f"(row_ok ? z[i][j] : -INFINITY)
+                         : "memory");
+          __syncwarp();
+#pragma unroll
+          for (int r = 0; r < 32; ++r)
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(z[i][r]) : "r"(stage + 4 * (32 * r + (r ^ lane))) : "memory");
+          const int at = ty[i] - row0;
+          if ((unsigned)at < 32u) {
+            float zy;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(zy) : "r"(stage + 4 * (32 * at + (at ^ lane))) : "memory");
+            p.zy[32 * c + lane] = zy;
+          }
+          tp[i] = ce_join2(tp[i], ce_pair(z[i]));
+        }
+      } else {
+        float4 rw = make_float4(0.0f, 0.0f, __int_as_float(-1), 0.0f);  // kPairGrad
+        if (MODE == kPairGrad && row_ok) rw = p.rows[row];
+        if (!take()) break;
+        if constexpr (kTok) {
+#pragma unroll
+          for (int i = 0; i < kBlocks; ++i) {
+            const int c = half + 2 * i;
+            if (32 * c >= NT || 32 * c >= p.N || !warp_ok) continue;
+            __syncwarp();
+            uint32_t a[32];
+            tmem_ld32(lanes + (uint32_t)(acc * NT + 32 * c), a);  // lane: row of W (column of dX), register: token
+            if (MODE == kTokGrad) {
+              // G by token: 32 tokens x 32 rows of W, 64 bytes a token
+              const uint32_t b = out.template acquire<2048>();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float4 r = tok[32 * c + j];
+                const int ry = __float_as_int(r.z);
+                float q = ce_exp2(fmaf(__uint_as_float(a[j]), kLog2e, -r.x));
+                if (ry == p.v0 + row) q -= 1.0f;
+                const __nv_bfloat16 g = __float2bfloat16_rn(ry >= 0 ? r.y * q : 0.0f);
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(b + 64 * j + 2 * lane), "h"(__bfloat16_as_ushort(g)) : "memory");
+              }
+              out.publish(&tmC, b, row0, 32 * c);
+            } else if (row_ok) {
+              float* dst = p.acc + ((int64_t)part * p.N + 32 * c) * p.M + row;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (32 * c + j < p.N) {
+                  float* q = dst + (int64_t)j * p.M;
+                  *q = p.out == kOutF32Add ? *q + __uint_as_float(a[j]) : __uint_as_float(a[j]);
+                }
+            }
+          }
+        } else {
+          const int col0 = nb * NT + 128 * half;
+          const int row_c = part * p.m_tiles * PM + row0;  // of C, whose parts of K lie one after another
+          const uint32_t cols = lanes + (uint32_t)(acc * NT + 128 * half);
+          if (MODE == kPairDw && p.out == kOutBf16) {
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              const int col = col0 + c * 64;
+              if (!warp_ok || col >= p.N) break;
+              __syncwarp();
+              uint32_t a[32], b[32];
+              tmem_ld32x2(cols + c * 64, cols + c * 64 + 32, a, b);
+              out.bf16_wide(&tmC, a, b, alpha, col, row_c);
+            }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const int col = col0 + c * 32;
+              if (!warp_ok || col >= p.N) break;
+              __syncwarp();
+              uint32_t a[32];
+              tmem_ld32(cols + c * 32, a);
+              float v[32];
+              if (MODE == kPairGrad) {
+                const int y = __float_as_int(rw.z), yc = y - p.v0 - col;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  float q = ce_exp2(fmaf(__uint_as_float(a[j]), kLog2e, -rw.x));
+                  if (j == yc) q -= 1.0f;
+                  v[j] = y >= 0 ? rw.y * q : 0.0f;
+                }
+                out.bf16(&tmC, v, col, row0);
+              } else if (MODE == kPairDx && p.out == kOutBf16Join) {
+                const float* old = p.acc + (int64_t)row * p.N + col;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                  if (row_ok && col + 4 * q < p.N) o = *reinterpret_cast<const float4*>(old + 4 * q);
+                  v[4 * q] = alpha * (__uint_as_float(a[4 * q]) + o.x);
+                  v[4 * q + 1] = alpha * (__uint_as_float(a[4 * q + 1]) + o.y);
+                  v[4 * q + 2] = alpha * (__uint_as_float(a[4 * q + 2]) + o.z);
+                  v[4 * q + 3] = alpha * (__uint_as_float(a[4 * q + 3]) + o.w);
+                }
+                out.bf16(&tmC, v, col, row0);
+              } else if (MODE == kPairDx && p.out == kOutBf16) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = alpha * __uint_as_float(a[j]);
+                out.bf16(&tmC, v, col, row0);
+              } else {
+                out.f32(&tmC, a, alpha, col, row_c, p.out == kOutF32Add);
+              }
+            }
+          }
+        }
+        release();
       }
+    }
+    if (MODE == kTokLse) {
+      // the four warps that share a warpgroup's tokens bring their pairs together (the abort path has partial
+      // ones: its results are incomplete anyway)
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i)
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(out.buf + 8 * (32 * i + lane)), "f"(tp[i].x), "f"(tp[i].y) : "memory");
+      if (half == 0) asm volatile("bar.sync 1, 128;" ::: "memory");
+      else asm volatile("bar.sync 2, 128;" ::: "memory");
+      if (sub == 0)
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+          const int c = half + 2 * i, t = 32 * c + lane;
+          float2 r = make_float2(-INFINITY, 0.0f);
+          for (int k = 0; k < 4; ++k) {
+            float2 q;
+            const uint32_t at = smem_addr(smem + PL::kStagingOffset + (4 * half + k) * PL::kStaging) + 8 * (32 * i + lane);
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(q.x), "=f"(q.y) : "r"(at) : "memory");
+            r = ce_join2(r, q);
+          }
+          if (32 * c < NT && t < p.N) p.part[(int64_t)blockIdx.x * p.N + t] = r;
+        }
+    }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
@@ -567,12 +680,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // Joins the pieces of a row: 32 rows a block, lane = row, warp w takes pieces w, w + 32, ... four at a
 // time; then the warps' pairs.  lse = ln 2 (m2 + log2 s).  A target outside [0, V) that is not ignore_index is a
 // mistake of the caller: recorded, and ignored.
-__device__ __forceinline__ float2 ce_join2(float2 a, float2 b) {
-  // a pair that holds nothing is (-inf, 0); both may be
-  const float m = fmaxf(a.x, b.x);
-  if (m == -INFINITY) return make_float2(m, a.y + b.y);
-  return make_float2(m, a.y * ce_exp2(a.x - m) + b.y * ce_exp2(b.x - m));
-}
 __global__ void __launch_bounds__(1024) k_ce_finish(const float2* __restrict__ part, int pieces, int64_t T,
                                                     const int64_t* __restrict__ targets, int64_t V, int64_t ignore,
                                                     const float* __restrict__ zy, float* __restrict__ loss,
@@ -608,32 +715,51 @@ __global__ void __launch_bounds__(1024) k_ce_finish(const float2* __restrict__ p
   loss[row] = y != ignore && in ? l - zy[row] : 0.0f;
 }
 
-// s = max |dloss| over the tokens that count (1 where that is 0 or not finite).
+// The largest |dloss| over the tokens that count (1 where that is 0 or not finite), valid in every thread.
+__device__ __forceinline__ float ce_block_scale(const float* __restrict__ dloss, const int64_t* __restrict__ targets,
+                                                int64_t T, int64_t V, int64_t ignore, unsigned* status, uint32_t* red) {
+  uint32_t m = 0;
+  bool bad = false;
+#pragma unroll 8
+  for (int64_t t = threadIdx.x; t < T; t += blockDim.x) {
+    const int64_t y = targets[t];
+    const uint32_t v = abs_bits(dloss[t]);
+    const bool in = y >= 0 && y < V;
+    if (y != ignore && in) m = max(m, v);
+    bad |= y != ignore && !in;
+  }
+  if (bad) atomicOr(status, kStatusBadTarget);
+  m = block_max_u32(m, red);
+  return (m == 0 || m >= 0x7F800000u) ? 1.0f : __uint_as_float(m);
+}
 __global__ void __launch_bounds__(1024) k_ce_scale(const float* __restrict__ dloss, const int64_t* __restrict__ targets,
                                                    int64_t T, int64_t V, int64_t ignore, float* scale, unsigned* status) {
   __shared__ uint32_t red[32];
-  uint32_t m = 0;
-  for (int64_t t = threadIdx.x; t < T; t += blockDim.x) {
-    const int64_t y = targets[t];
-    if (y == ignore) continue;
-    if (y < 0 || y >= V) atomicOr(status, kStatusBadTarget);
-    else m = max(m, abs_bits(dloss[t]));
-  }
-  m = block_max_u32(m, red);
-  if (threadIdx.x == 0) *scale = (m == 0 || m >= 0x7F800000u) ? 1.0f : __uint_as_float(m);
+  const float s = ce_block_scale(dloss, targets, T, V, ignore, status, red);
+  if (threadIdx.x == 0) *scale = s;
 }
 
 // Per token: {lse log2e, dloss / s, its target or -1 where it is ignored}, and x with ignored rows zeroed.
+// OWN: every block finds s itself (up to kCeOwnScale tokens, which saves a launch), and block 0 stores it.
+constexpr int64_t kCeOwnScale = 2048;
+template <int OWN>
 __global__ void __launch_bounds__(256) k_ce_rows(const uint16_t* __restrict__ x, const int64_t* __restrict__ targets,
                                                  const float* __restrict__ lse, const float* __restrict__ dloss, int64_t T,
-                                                 int d, int64_t V, int64_t ignore, const float* __restrict__ scale,
-                                                 float4* __restrict__ rows, uint16_t* __restrict__ xz) {
+                                                 int d, int64_t V, int64_t ignore, float* scale,
+                                                 float4* __restrict__ rows, uint16_t* __restrict__ xz, unsigned* status) {
+  __shared__ uint32_t red[32];
+  float s;
+  if (OWN) {
+    s = ce_block_scale(dloss, targets, T, V, ignore, status, red);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *scale = s;
+  } else {
+    s = *scale;
+  }
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
     const int64_t y = targets[t];
     const bool keep = y != ignore && y >= 0 && y < V;
-    if (threadIdx.x == 0) {
-      rows[t] = make_float4(lse[t] * kLog2e, keep ? dloss[t] / *scale : 0.0f, __int_as_float(keep ? (int)y : -1), 0.0f);
-    }
+    if (threadIdx.x == 0)
+      rows[t] = make_float4(lse[t] * kLog2e, keep ? dloss[t] / s : 0.0f, __int_as_float(keep ? (int)y : -1), 0.0f);
     const uint16_t* src = x + t * d;
     uint16_t* dst = xz + t * d;
     for (int j = 8 * threadIdx.x; j < d; j += 8 * blockDim.x) st_v4(dst + j, keep ? ld_v4(src + j) : make_uint4(0, 0, 0, 0));
@@ -771,8 +897,9 @@ cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Laun
     ok = ok && make_map(&tc, q.C, q.M, q.N, q.ldc, 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE);
   } else if (!kTok && MODE != kPairLse) {
     const bool f32 = MODE != kPairGrad && (a.out == kOutF32Store || a.out == kOutF32Add);
-    ok = ok && make_map(&tc, q.C, q.N, splits > 1 ? (int64_t)splits * a.m_tiles * PM : q.M, q.ldc, f32 ? 4 : 2, 32, 32,
-                        f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+    const bool wide = MODE == kPairDw && !f32;  // rows of 128 bytes, as fp32's
+    ok = ok && make_map(&tc, q.C, q.N, splits > 1 ? (int64_t)splits * a.m_tiles * PM : q.M, q.ldc, f32 ? 4 : 2,
+                        wide ? 64 : 32, 32, f32 || wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
   }
   if (!ok) return cudaErrorInvalidValue;
   static std::atomic<uint64_t> configured{0};  // a bit per device
@@ -780,12 +907,12 @@ cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Laun
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!(configured.load() >> dev & 1)) {
-    e = cudaFuncSetAttribute(k_ce_gemm<A_MN, B_MN, MODE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, PairPlan<NT>::kSmem);
+    e = cudaFuncSetAttribute(k_ce_gemm<A_MN, B_MN, MODE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, PairPlan<MODE, NT>::kSmem);
     if (e != cudaSuccess) return e;
     configured.fetch_or(1ull << dev);
   }
   const int pairs = pair_grid(L, a.num_tiles);
-  k_ce_gemm<A_MN, B_MN, MODE, NT><<<2 * pairs, kPairThreads, PairPlan<NT>::kSmem, L.stream>>>(ta, tb, tc, a);
+  k_ce_gemm<A_MN, B_MN, MODE, NT><<<2 * pairs, kPairThreads, PairPlan<MODE, NT>::kSmem, L.stream>>>(ta, tb, tc, a);
   return launched(L);
 }
 
@@ -838,7 +965,7 @@ size_t ce_layout(int64_t T, int64_t d, int64_t V, bool bwd, uint8_t* base, CeWs*
     t.rows = (float4*)take(T * 16);
     t.scale = (float*)take(4);
   } else {
-    t.part = (float2*)take(T <= kTokMax ? 8 * kPlanPairs * T * 8 : 2 * ((V + PN - 1) / PN) * T * 8);
+    t.part = (float2*)take(T <= kTokMax ? 2 * kPlanPairs * T * 8 : 2 * ((V + PN - 1) / PN) * T * 8);
     t.zy = (float*)take(T * 4);
   }
   if (w) *w = t;
@@ -864,7 +991,7 @@ cudaError_t launch_ce_fwd(const uint16_t* x, const uint16_t* W, const int64_t* t
     const PairProblem q{V, T, d, W, d, x, d, nullptr, 0};
     e = T <= 32 ? launch_pair<0, 0, kTokLse, 32>(q, 1, a, L)
         : T <= 64 ? launch_pair<0, 0, kTokLse, 64>(q, 1, a, L) : launch_pair<0, 0, kTokLse, 128>(q, 1, a, L);
-    pieces = 8 * pair_grid(L, (V + PM - 1) / PM);
+    pieces = 2 * pair_grid(L, (V + PM - 1) / PM);
   } else {
     e = launch_pair<0, 0, kPairLse>(PairProblem{T, V, d, x, d, W, d, nullptr, 0}, 1, a, L);
     pieces = (int)((V + 127) / 128);
@@ -884,10 +1011,14 @@ cudaError_t launch_ce_bwd(const uint16_t* x, const uint16_t* W, const int64_t* t
   const int64_t piece = plan.piece;
   const int join_blocks = 4 * L.num_sms;
   cudaError_t e;
-  k_ce_scale<<<1, 1024, 0, L.stream>>>(dloss, targets, T, V, ignore, w.scale, L.status);
-  if ((e = launched(L)) != cudaSuccess) return e;
-  k_ce_rows<<<(unsigned)(T < 8 * L.num_sms ? T : 8 * L.num_sms), 256, 0, L.stream>>>(x, targets, lse, dloss, T, d, V, ignore,
-                                                                                 w.scale, w.rows, w.xz);
+  const unsigned row_blocks = (unsigned)(T < 8 * L.num_sms ? T : 8 * L.num_sms);
+  if (T <= kCeOwnScale) {
+    k_ce_rows<1><<<row_blocks, 256, 0, L.stream>>>(x, targets, lse, dloss, T, d, V, ignore, w.scale, w.rows, w.xz, L.status);
+  } else {
+    k_ce_scale<<<1, 1024, 0, L.stream>>>(dloss, targets, T, V, ignore, w.scale, L.status);
+    if ((e = launched(L)) != cudaSuccess) return e;
+    k_ce_rows<0><<<row_blocks, 256, 0, L.stream>>>(x, targets, lse, dloss, T, d, V, ignore, w.scale, w.rows, w.xz, L.status);
+  }
   if ((e = launched(L)) != cudaSuccess) return e;
   for (int64_t v0 = 0; v0 < V; v0 += piece) {
     const int64_t n = V - v0 < piece ? V - v0 : piece;
