@@ -32,26 +32,49 @@ struct Piece {
       w[0] = F32 ? static_cast<const uint32_t*>(p)[i] : (uint32_t)static_cast<const uint16_t*>(p)[i] << 16;
     }
   }
-  __device__ __forceinline__ float at(int k) const {
-    if constexpr (VEC == 8 && !F32) return (k & 1) ? bf16_hi(w[k >> 1]) : bf16_lo(w[k >> 1]);
-    else return __uint_as_float(w[k]);
+  // unit k: elements 2 k and 2 k + 1 of 8, or the element
+  __device__ __forceinline__ auto unit(int k) const {
+    if constexpr (VEC == 1) return __uint_as_float(w[0]);
+    else if constexpr (F32) return make_float2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+    else return make_float2(bf16_lo(w[k]), bf16_hi(w[k]));
   }
-  __device__ static void store(void* p, int64_t i, const float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-      if constexpr (F32) {
-        float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-        q[0] = make_float4(v[0], v[1], v[2], v[3]);
-        q[1] = make_float4(v[4], v[5], v[6], v[7]);
-      } else {
-        st_v4(static_cast<uint16_t*>(p) + i, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                       pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
-      }
+  __device__ __forceinline__ static void store(void* p, int64_t i, const float2 (&v)[4]) {
+    if constexpr (F32) {
+      float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+      q[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+      q[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
     } else {
-      if constexpr (F32) static_cast<float*>(p)[i] = v[0];
-      else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v[0]);
+      st_v4(static_cast<uint16_t*>(p) + i, make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                                     pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y)));
     }
   }
+  __device__ __forceinline__ static void store(void* p, int64_t i, const float (&v)[1]) {
+    if constexpr (F32) static_cast<float*>(p)[i] = v[0];
+    else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v[0]);
+  }
 };
+
+// A thread's arithmetic is on pairs of columns (packed fp32 instructions) where VEC = 8, else on floats.
+template <int VEC>
+struct Unit { using T = float2; static constexpr int kCount = 4; };
+template <>
+struct Unit<1> { using T = float; static constexpr int kCount = 1; };
+__device__ __forceinline__ float2 add(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float sum(float2 v) { return v.x + v.y; }
+__device__ __forceinline__ float sum(float v) { return v; }
+__device__ __forceinline__ void fill(float2& v, float f) { v = make_float2(f, f); }
+__device__ __forceinline__ void fill(float& v, float f) { v = f; }
+template <int VEC>
+__device__ __forceinline__ typename Unit<VEC>::T all(float f) {
+  typename Unit<VEC>::T v;
+  fill(v, f);
+  return v;
+}
 
 __device__ __forceinline__ float ln_warp_sum(float v) {
 #pragma unroll
@@ -68,15 +91,19 @@ __device__ __forceinline__ float ln_warp_sum(float v) {
 // M2 = M2_a + M2_b + delta^2 n_a n_b / n, so a row costs one block barrier and nothing cancels.
 // ---------------------------------------------------------------------------
 constexpr int ln_fwd_threads(int W) { return W < 8 ? 256 : 32 * W; }
-// Resident blocks per SM: 1024 threads of 64 registers, or 512 of 128 where fp32 pieces fill more.
+// Resident blocks per SM: 768 threads of 80 registers, or 512 of 128
+// for fp32 pieces of 8 (two rows of them: 64 registers a thread at 4 pieces).
 constexpr int ln_fwd_per_sm(int F32, int VEC, int W) {
-  return (F32 && VEC == 8 ? 512 : 1024) / ln_fwd_threads(W) > 0 ? (F32 && VEC == 8 ? 512 : 1024) / ln_fwd_threads(W) : 1;
+  const int n = (F32 && VEC == 8 ? 512 : 768) / ln_fwd_threads(W);
+  return n > 0 ? n : 1;
 }
 
 template <int F32, int VEC, int NP, int W>
 __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(F32, VEC, W))
     k_layernorm_fwd(const void* x, const void* __restrict__ g, const void* __restrict__ b, int64_t T, int d, float eps,
                     void* y, float* __restrict__ mean, float* __restrict__ rstd) {
+  using E = typename Unit<VEC>::T;
+  constexpr int kUnits = Unit<VEC>::kCount;
   constexpr int kRows = W < 8 ? 8 / W : 1;
   __shared__ float sm[2][kRows][W], sv[2][kRows][W];
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W, r = (threadIdx.x >> 5) / W;
@@ -106,23 +133,29 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(F32, VEC, W))
 #pragma unroll
     for (int k = 0; k < NP; ++k) px[k] = nx[k];
     load(nx, row + step);
-    float s = 0.0f;
+    // x about the warp's mean, in registers
+    E c[NP][kUnits];
+    E s = all<VEC>(0.0f);
 #pragma unroll
     for (int k = 0; k < NP; ++k)
       if ((k * W + warp) * 32 + lane < pieces)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) s += px[k].at(e);
-    float mu = ln_warp_sum(s) * inv_own;
-    float m2 = 0.0f;
-#pragma unroll
-    for (int k = 0; k < NP; ++k)
-      if ((k * W + warp) * 32 + lane < pieces)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float c = px[k].at(e) - mu;
-          m2 += c * c;
+        for (int e = 0; e < kUnits; ++e) {
+          c[k][e] = px[k].unit(e);
+          s = add(s, c[k][e]);
         }
-    m2 = ln_warp_sum(m2);
+    const float own_mu = ln_warp_sum(sum(s)) * inv_own;
+    float mu = own_mu;
+    E q = all<VEC>(0.0f);
+#pragma unroll
+    for (int k = 0; k < NP; ++k)
+      if ((k * W + warp) * 32 + lane < pieces)
+#pragma unroll
+        for (int e = 0; e < kUnits; ++e) {
+          c[k][e] = add(c[k][e], all<VEC>(-own_mu));
+          q = fma(c[k][e], c[k][e], q);
+        }
+    float m2 = ln_warp_sum(sum(q));
     if (W > 1) {
       if (lane == 0) { sm[par][r][warp] = mu; sv[par][r][warp] = m2; }
       __syncthreads();
@@ -150,9 +183,12 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(F32, VEC, W))
         Piece<F32, VEC> pg, pb;
         pg.load(g, (int64_t)i * VEC);
         if (b) pb.load(b, (int64_t)i * VEC);
-        float v[VEC];
+        E v[kUnits];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = (px[k].at(e) - mu) * rs * pg.at(e) + (b ? pb.at(e) : 0.0f);
+        for (int e = 0; e < kUnits; ++e) {
+          const E f = mul(pg.unit(e), all<VEC>(rs)), h = add(c[k][e], all<VEC>(own_mu - mu));
+          v[e] = b ? fma(h, f, pb.unit(e)) : mul(h, f);
+        }
         Piece<F32, VEC>::store(y, row * d + (int64_t)i * VEC, v);
       }
     }
@@ -174,25 +210,35 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(F32, VEC, W))
 constexpr int kLnSlotsMax = 8;
 constexpr int kLnThreads = 512;
 
+// Sums of two values over the warp: lanes 0-15 end with a's, lanes 16-31 with b's (5 exchanges for both).
+__device__ __forceinline__ float ln_warp_sum2(float a, float b, int lane) {
+  float v = (lane < 16 ? a : b) + __shfl_xor_sync(0xFFFFFFFFu, lane < 16 ? b : a, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
 template <int F32, int VEC, int NP, int RING>
 __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
     k_layernorm_bwd(const void* dY, const void* x, const void* __restrict__ g, const float* __restrict__ mean,
                     const float* __restrict__ rstd, const void* dres, int64_t T, int d, int rows, int S, void* dX,
                     float* __restrict__ part, unsigned* status) {
+  static_assert(RING == (VEC == 8), "the ring's pieces are vectors");
+  using E = typename Unit<VEC>::T;
+  constexpr int kUnits = Unit<VEC>::kCount;
   constexpr int ES = F32 ? 4 : 2;
-  constexpr bool kHold = RING || NP <= 8;
+  constexpr bool kHold = RING || NP <= 8;  // a thread's inputs stay in registers for their second use
+  constexpr bool kKeep = RING && NP <= 2;  // and so do u and xh
   extern __shared__ __align__(128) uint8_t ln_rows[];
   __shared__ uint64_t full[kLnSlotsMax];
-  __shared__ float red[2][2][32];
-  __shared__ int bad[2][32];
+  __shared__ float red[2][2][16];
   __shared__ volatile int give_up;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, nwarps = blockDim.x >> 5;
   const int pieces = d / VEC;
   const int64_t r0 = (int64_t)blockIdx.x * rows;
   const int nrows = (int)(T - r0 < rows ? T - r0 : rows);
   const uint32_t row_bytes = (uint32_t)d * ES, slot_bytes = row_bytes * (dres ? 3u : 2u);
-  auto issue = [&](int rr) {  // thread 0 only
-    const int s = rr % S;
+  auto issue = [&](int rr, int s) {  // thread 0 only
     uint8_t* slot = ln_rows + (size_t)s * slot_bytes;
     const int64_t off = (r0 + rr) * (int64_t)row_bytes;
     mbar_arrive_expect_tx(&full[s], slot_bytes);
@@ -208,13 +254,13 @@ __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
     }
     __syncthreads();
     if (t == 0)
-      for (int k = 0; k < S && k < nrows; ++k) issue(k);
+      for (int k = 0; k < S && k < nrows; ++k) issue(k, k);
   }
-  float ag[NP][VEC], ab[NP][VEC];
+  E ag[NP][kUnits], ab[NP][kUnits];
 #pragma unroll
   for (int k = 0; k < NP; ++k)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) ag[k][e] = ab[k][e] = 0.0f;
+    for (int e = 0; e < kUnits; ++e) ag[k][e] = ab[k][e] = all<VEC>(0.0f);
   Piece<F32, VEC> pg[NP];
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
@@ -224,7 +270,8 @@ __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
   const float inv_d = 1.0f / (float)d;
   float mu_next = mean[r0], rs_next = rstd[r0];
   bool aborted = false;
-  int rr = 0;
+  int rr = 0, s = 0;
+  uint32_t par = 0;
   for (; rr < nrows; ++rr) {
     const float mu = mu_next, rs = rs_next;
     if (rr + 1 < nrows) { mu_next = mean[r0 + rr + 1]; rs_next = rstd[r0 + rr + 1]; }
@@ -232,13 +279,13 @@ __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
     const uint8_t* slot = nullptr;
     bool ok = true;
     if (RING) {
-      const int s = rr % S;
-      ok = mbar_wait(&full[s], (uint32_t)(rr / S) & 1u, &give_up);
+      ok = mbar_wait(&full[s], par, &give_up);
       if (!ok) give_up = 1;
       slot = ln_rows + (size_t)s * slot_bytes;
     }
     Piece<F32, VEC> py[NP], px[NP], pr[NP];
-    float su = 0.0f, sx = 0.0f;
+    E u[kKeep ? NP : 1][kUnits], xh[kKeep ? NP : 1][kUnits];
+    E su_t = all<VEC>(0.0f), sx_t = all<VEC>(0.0f);
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
       const int i = k * (int)blockDim.x + t;
@@ -259,32 +306,30 @@ __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
     for (int k = 0; k < NP; ++k) {
       if (k * (int)blockDim.x + t >= pieces) continue;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float dy = py[k].at(e), xh = (px[k].at(e) - mu) * rs, u = dy * pg[k].at(e);
-        su += u;
-        sx += u * xh;
-        ag[k][e] += dy * xh;
-        ab[k][e] += dy;
+      for (int e = 0; e < kUnits; ++e) {
+        const E dy = py[k].unit(e), uu = mul(dy, pg[k].unit(e));
+        const E h = mul(add(px[k].unit(e), all<VEC>(-mu)), all<VEC>(rs));
+        su_t = add(su_t, uu);
+        sx_t = fma(uu, h, sx_t);
+        ag[k][e] = fma(dy, h, ag[k][e]);
+        ab[k][e] = add(ab[k][e], dy);
+        if (kKeep) { u[kKeep ? k : 0][e] = uu; xh[kKeep ? k : 0][e] = h; }
       }
     }
-    su = ln_warp_sum(su);
-    sx = ln_warp_sum(sx);
-    const int warp_bad = RING ? __any_sync(0xFFFFFFFFu, !ok) : 0;
-    if (lane == 0) {
-      red[rr & 1][0][warp] = su;
-      red[rr & 1][1][warp] = sx;
-      if (RING) bad[rr & 1][warp] = warp_bad;
-    }
-    __syncthreads();
-    su = ln_warp_sum(lane < nwarps ? red[rr & 1][0][lane] : 0.0f) * inv_d;
-    sx = ln_warp_sum(lane < nwarps ? red[rr & 1][1][lane] : 0.0f) * inv_d;
+    const float both = ln_warp_sum2(sum(su_t), sum(sx_t), lane);
+    if ((lane & 15) == 0) red[rr & 1][lane >> 4][warp] = both;
+    // the row's one barrier; a wait that expired anywhere in the block is seen by all after it
+    if (RING) aborted = __syncthreads_or(!ok);
+    else __syncthreads();
+    if (aborted) break;
+    float tot = (lane & 15) < nwarps ? red[rr & 1][lane >> 4][lane & 15] : 0.0f;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) tot += __shfl_xor_sync(0xFFFFFFFFu, tot, o);
+    const float su = __shfl_sync(0xFFFFFFFFu, tot, 0) * inv_d, sx = __shfl_sync(0xFFFFFFFFu, tot, 16) * inv_d;
     if (RING) {
-      if (__any_sync(0xFFFFFFFFu, lane < nwarps && bad[rr & 1][lane] != 0)) {
-        aborted = true;
-        break;
-      }
       // every thread has its values of row rr in registers: the slot takes row rr + S
-      if (t == 0 && rr + S < nrows) issue(rr + S);
+      if (t == 0 && rr + S < nrows) issue(rr + S, s);
+      if (++s == S) { s = 0; par ^= 1u; }
     }
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
@@ -297,12 +342,13 @@ __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
         pg[k].load(g, j);
         if (dres) pr[k].load(dres, base + j);
       }
-      float v[VEC];
+      E v[kUnits];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float xh = (px[k].at(e) - mu) * rs;
-        v[e] = rs * (py[k].at(e) * pg[k].at(e) - su - xh * sx);
-        if (dres) v[e] += pr[k].at(e);
+      for (int e = 0; e < kUnits; ++e) {
+        const E h = kKeep ? xh[kKeep ? k : 0][e] : mul(add(px[k].unit(e), all<VEC>(-mu)), all<VEC>(rs));
+        const E uu = kKeep ? u[kKeep ? k : 0][e] : mul(py[k].unit(e), pg[k].unit(e));
+        const E w = add(fma(h, all<VEC>(-sx), uu), all<VEC>(-su));
+        v[e] = dres ? fma(w, all<VEC>(rs), pr[k].unit(e)) : mul(w, all<VEC>(rs));
       }
       Piece<F32, VEC>::store(dX, base + j, v);
     }
@@ -311,6 +357,7 @@ __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
     if (t == 0) {
       atomicOr(status, kStatusTimeout);
       volatile int never = 0;
+      // rows rr .. rr + S - 1 may still have copies in flight into this block's ring
       for (int k = rr; k < rr + S && k < nrows; ++k) mbar_wait(&full[k % S], (uint32_t)(k / S) & 1u, &never);
     }
     return;
