@@ -83,31 +83,86 @@ __device__ __forceinline__ float ln_warp_sum(float v) {
 }
 
 // ---------------------------------------------------------------------------
+// Rows on their way in: bulk copies into a ring of slots in shared memory, completing on a slot's
+// mbarrier, so that the bytes in flight are set by the ring and not by registers.
+//
+// A bulk copy moves whole 16-byte units.  Where a row's bytes are no multiple of 16 (odd widths), the copy starts at
+// the unit that holds the first byte and the data lie `off & 15` bytes into their region; the last unit is
+// copied whole too, unless it would pass the tensor's end, whose last elements thread 0 then copies itself.
+// ---------------------------------------------------------------------------
+constexpr int kLnSlotsMax = 8;
+constexpr size_t kLnSmemBudget = 200 * 1024;  // per SM
+
+__host__ __device__ inline uint32_t ln_region(uint32_t bytes) {
+  return bytes % 16 == 0 ? bytes : (bytes + 15) / 16 * 16 + 16;
+}
+// The bytes of a copy of [off, off + bytes) of a tensor of `total` bytes.  EVEN: all are multiples of 16.
+template <bool EVEN>
+__device__ __forceinline__ uint32_t ln_copy_bytes(int64_t off, uint32_t bytes, int64_t total) {
+  if (EVEN) return bytes;
+  const int64_t begin = off & ~(int64_t)15, end = min((off + bytes + 15) & ~(int64_t)15, total & ~(int64_t)15);
+  return end > begin ? (uint32_t)(end - begin) : 0u;
+}
+template <bool EVEN>
+__device__ __forceinline__ void ln_copy(uint8_t* dst, const void* src, int64_t off, uint32_t bytes, uint32_t n,
+                                        uint64_t* bar) {
+  if (EVEN) {
+    bulk_load(dst, static_cast<const uint8_t*>(src) + off, n, bar);
+    return;
+  }
+  const uint8_t* from = static_cast<const uint8_t*>(src) + (off & ~(int64_t)15);
+  if (n) bulk_load(dst, from, n, bar);
+  const uint32_t mis = (uint32_t)(off & 15);
+  for (uint32_t k = n; k < mis + bytes; k += 2)
+    if (k >= mis) *reinterpret_cast<uint16_t*>(dst + k) = *reinterpret_cast<const uint16_t*>(from + k);
+}
+
+// ---------------------------------------------------------------------------
 // Forward: W warps hold a row in registers, NP pieces a lane (piece k of lane l of warp w is piece
-// (k W + w) 32 + l of the row); a block of max(W, 8) warps has 8 / W rows at a time and walks the rows with the
-// grid's stride, the next row's pieces in flight while the current one is computed and written.  Each
-// warp takes the mean and the sum of squares about it of its own elements, in two passes over its registers; the
-// warps' (mean, M2) pairs are then joined with the parallel-variance formula
-// M2 = M2_a + M2_b + delta^2 n_a n_b / n, so a row costs one block barrier and nothing cancels.
+// (k W + w) 32 + l of the row); a block of max(W, 8) warps takes kRows = 8 / W consecutive rows at a time (one
+// slot of the ring, one copy) and walks them with the grid's stride.  Each warp takes the mean and
+// the sum of squares about it of its own elements, in two passes over its registers; the warps' (mean, M2)
+// pairs are then joined, mean = sum n_w mean_w / d and M2 = sum (M2_w + n_w (mean_w - mean)^2), so a row
+// costs one block barrier and nothing cancels.
 // ---------------------------------------------------------------------------
 constexpr int ln_fwd_threads(int W) { return W < 8 ? 256 : 32 * W; }
-// Resident blocks per SM: 768 threads of 80 registers, or 512 of 128
-// for fp32 pieces of 8 (two rows of them: 64 registers a thread at 4 pieces).
+// Resident blocks per SM by registers: 512 threads of 128 for pieces of 8, 768 of 80 for single columns.  They hold a
+// thread's gain and bias too: read again for each row, those come from L2 (the ring leaves L1 too little), and
+// the rows wait for them (T = 16384, d = 5120: 70 us against LNFWD us).
 constexpr int ln_fwd_per_sm(int F32, int VEC, int W) {
-  const int n = (F32 && VEC == 8 ? 512 : 768) / ln_fwd_threads(W);
+  const int n = (VEC == 8 ? 512 : 768) / ln_fwd_threads(W);
   return n > 0 ? n : 1;
 }
 
 template <int F32, int VEC, int NP, int W>
 __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(F32, VEC, W))
     k_layernorm_fwd(const void* x, const void* __restrict__ g, const void* __restrict__ b, int64_t T, int d, float eps,
-                    void* y, float* __restrict__ mean, float* __restrict__ rstd) {
+                    int S, void* y, float* __restrict__ mean, float* __restrict__ rstd, unsigned* status) {
   using E = typename Unit<VEC>::T;
-  constexpr int kUnits = Unit<VEC>::kCount;
+  constexpr int kUnits = Unit<VEC>::kCount, ES = F32 ? 4 : 2;
   constexpr int kRows = W < 8 ? 8 / W : 1;
-  __shared__ float sm[2][kRows][W], sv[2][kRows][W];
+  extern __shared__ __align__(128) uint8_t ln_rows[];
+  __shared__ uint64_t full[kLnSlotsMax];
+  __shared__ float2 pairs[2][kRows][W];
+  __shared__ volatile int give_up;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W, r = (threadIdx.x >> 5) / W;
   const int pieces = d / VEC;
+  const uint32_t row_bytes = (uint32_t)d * ES, slot_bytes = ln_region(kRows * row_bytes);
+  const int64_t total = T * (int64_t)row_bytes, groups = (T + kRows - 1) / kRows;
+  auto issue = [&](int64_t group, int s) {  // thread 0 only
+    const int64_t first = group * kRows, off = first * row_bytes;
+    const uint32_t bytes = (uint32_t)min((int64_t)kRows, T - first) * row_bytes, n = ln_copy_bytes<VEC == 8>(off, bytes, total);
+    uint8_t* slot = ln_rows + (size_t)s * slot_bytes;
+    ln_copy<VEC == 8>(slot, x, off, bytes, n, &full[s]);
+    mbar_arrive_expect_tx(&full[s], n);
+  };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+    give_up = 0;
+    fence_mbar_init();
+    for (int s = 0; s < S && blockIdx.x + s * (int64_t)gridDim.x < groups; ++s) issue(blockIdx.x + s * (int64_t)gridDim.x, s);
+  }
+  __syncthreads();
   // elements of a warp: full groups of 32 pieces, and what the last one holds
   auto count = [&](int w) {
     int n = 0;
@@ -116,35 +171,45 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(F32, VEC, W))
     return n * VEC;
   };
   const int n_own = count(warp);
-  const float inv_own = n_own ? 1.0f / (float)n_own : 0.0f;
-  Piece<F32, VEC> px[NP], nx[NP];
-  auto load = [&](Piece<F32, VEC>(&p)[NP], int64_t row) {
+  const float inv_own = n_own ? 1.0f / (float)n_own : 0.0f, inv_d = 1.0f / (float)d;
+  const float lane_count = (float)count(lane & (W - 1)), lane_share = lane_count * inv_d;
+  Piece<F32, VEC> pg[NP], pb[NP];
 #pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      const int i = (k * W + warp) * 32 + lane;
-      if (row < T && i < pieces) p[k].load(x, row * d + (int64_t)i * VEC);
+  for (int k = 0; k < NP; ++k) {
+    const int i = (k * W + warp) * 32 + lane;
+    if (i < pieces) {
+      pg[k].load(g, (int64_t)i * VEC);
+      if (b) pb[k].load(b, (int64_t)i * VEC);
     }
-  };
-  const int64_t step = (int64_t)gridDim.x * kRows;
-  int64_t row = (int64_t)blockIdx.x * kRows + r;
-  load(nx, row);
-  int par = 0;
-  for (int64_t first = (int64_t)blockIdx.x * kRows; first < T; first += step, row += step, par ^= 1) {
-#pragma unroll
-    for (int k = 0; k < NP; ++k) px[k] = nx[k];
-    load(nx, row + step);
+  }
+  int s = 0, turn = 0;
+  uint32_t par = 0;
+  bool aborted = false;
+  int64_t group = blockIdx.x;
+  for (; group < groups; group += gridDim.x, turn ^= 1) {
+    const int64_t row = group * kRows + r;
+    bool ok = mbar_wait(&full[s], par, &give_up);
+    if (!ok) give_up = 1;
     // x about the warp's mean, in registers
     E c[NP][kUnits];
-    E s = all<VEC>(0.0f);
+    E sum_t = all<VEC>(0.0f);
+    if (ok && row < T) {
+      const uint8_t* slot = ln_rows + (size_t)s * slot_bytes + (VEC == 8 ? 0 : (int)((group * kRows * row_bytes) & 15));
 #pragma unroll
-    for (int k = 0; k < NP; ++k)
-      if ((k * W + warp) * 32 + lane < pieces)
+      for (int k = 0; k < NP; ++k) {
+        const int i = (k * W + warp) * 32 + lane;
+        if (i < pieces) {
+          Piece<F32, VEC> px;
+          px.load(slot, r * d + i * VEC);
 #pragma unroll
-        for (int e = 0; e < kUnits; ++e) {
-          c[k][e] = px[k].unit(e);
-          s = add(s, c[k][e]);
+          for (int e = 0; e < kUnits; ++e) {
+            c[k][e] = px.unit(e);
+            sum_t = add(sum_t, c[k][e]);
+          }
         }
-    const float own_mu = ln_warp_sum(sum(s)) * inv_own;
+      }
+    }
+    const float own_mu = ln_warp_sum(sum(sum_t)) * inv_own;
     float mu = own_mu;
     E q = all<VEC>(0.0f);
 #pragma unroll
@@ -156,22 +221,25 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(F32, VEC, W))
           q = fma(c[k][e], c[k][e], q);
         }
     float m2 = ln_warp_sum(sum(q));
+    if (W > 1 && lane == 0) pairs[turn][r][warp] = make_float2(mu, m2);
+    // the one barrier: the pairs are there, and every thread has its part of the slot, which takes the group S
+    // turns ahead; a wait that expired anywhere in the block is seen by all
+    aborted = __syncthreads_or(!ok);
+    if (aborted) break;
+    if (threadIdx.x == 0 && group + S * (int64_t)gridDim.x < groups) issue(group + S * (int64_t)gridDim.x, s);
+    if (++s == S) { s = 0; par ^= 1u; }
     if (W > 1) {
-      if (lane == 0) { sm[par][r][warp] = mu; sv[par][r][warp] = m2; }
-      __syncthreads();
-      float n = (float)count(0);
-      mu = sm[par][r][0];
-      m2 = sv[par][r][0];
+      const float2 of = pairs[turn][r][lane & (W - 1)];
+      mu = of.x * lane_share;
 #pragma unroll
-      for (int w = 1; w < W; ++w) {
-        const float nf = (float)count(w), tot = n + nf, delta = sm[par][r][w] - mu, share = __fdividef(nf, tot);
-        mu += delta * share;
-        m2 += sv[par][r][w] + delta * delta * n * share;
-        n = tot;
-      }
+      for (int o = W / 2; o > 0; o >>= 1) mu += __shfl_xor_sync(0xFFFFFFFFu, mu, o);
+      const float off = of.x - mu;
+      m2 = fmaf(off * off, lane_count, of.y);
+#pragma unroll
+      for (int o = W / 2; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xFFFFFFFFu, m2, o);
     }
     if (row >= T) continue;
-    const float rs = 1.0f / sqrtf(m2 / (float)d + eps);
+    const float rs = rsqrtf(fmaf(m2, inv_d, eps));
     if (warp == 0 && lane == 0) {
       mean[row] = mu;
       rstd[row] = rs;
@@ -180,17 +248,23 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(F32, VEC, W))
     for (int k = 0; k < NP; ++k) {
       const int i = (k * W + warp) * 32 + lane;
       if (i < pieces) {
-        Piece<F32, VEC> pg, pb;
-        pg.load(g, (int64_t)i * VEC);
-        if (b) pb.load(b, (int64_t)i * VEC);
         E v[kUnits];
 #pragma unroll
         for (int e = 0; e < kUnits; ++e) {
-          const E f = mul(pg.unit(e), all<VEC>(rs)), h = add(c[k][e], all<VEC>(own_mu - mu));
-          v[e] = b ? fma(h, f, pb.unit(e)) : mul(h, f);
+          const E f = mul(pg[k].unit(e), all<VEC>(rs)), h = add(c[k][e], all<VEC>(own_mu - mu));
+          v[e] = b ? fma(h, f, pb[k].unit(e)) : mul(h, f);
         }
         Piece<F32, VEC>::store(y, row * d + (int64_t)i * VEC, v);
       }
+    }
+  }
+  if (aborted && threadIdx.x == 0) {
+    atomicOr(status, kStatusTimeout);
+    volatile int never = 0;
+    // the copies still in flight: this turn's and those of the next S - 1 turns
+    for (int k = 0; k < S && group + k * (int64_t)gridDim.x < groups; ++k) {
+      mbar_wait(&full[s], par, &never);
+      if (++s == S) { s = 0; par ^= 1u; }
     }
   }
 }
@@ -200,14 +274,9 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(F32, VEC, W))
 // shares of dg and db it keeps in registers; k_layernorm_bwd_finish adds the blocks' partial rows.
 // A row needs one exchange between its warps, of the two sums in one barrier.
 //
-// RING (rows of a multiple of 16 bytes): x, dY and dres rows arrive in shared memory through bulk copies
-// up to S rows ahead, so the bytes in flight are set by the ring and not by registers.  Every wait is
-// bounded; on expiry all threads leave together after the row's barrier and thread 0 waits for the
-// copies in flight before the block exits.
-// Without RING (odd widths) a thread loads its elements itself, and again for the second use where it
-// has more than 8.
+// dY, x and dres rows come through the ring, up to S rows ahead.  Every wait is bounded; on expiry all
+// threads leave together after the row's barrier and thread 0 waits for the copies in flight before the block exits.
 // ---------------------------------------------------------------------------
-constexpr int kLnSlotsMax = 8;
 constexpr int kLnThreads = 512;
 
 // Sums of two values over the warp: lanes 0-15 end with a's, lanes 16-31 with b's (5 exchanges for both).
@@ -218,17 +287,15 @@ __device__ __forceinline__ float ln_warp_sum2(float a, float b, int lane) {
   return v;
 }
 
-template <int F32, int VEC, int NP, int RING>
+template <int F32, int VEC, int NP>
 __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
     k_layernorm_bwd(const void* dY, const void* x, const void* __restrict__ g, const float* __restrict__ mean,
                     const float* __restrict__ rstd, const void* dres, int64_t T, int d, int rows, int S, void* dX,
                     float* __restrict__ part, unsigned* status) {
-  static_assert(RING == (VEC == 8), "the ring's pieces are vectors");
   using E = typename Unit<VEC>::T;
   constexpr int kUnits = Unit<VEC>::kCount;
   constexpr int ES = F32 ? 4 : 2;
-  constexpr bool kHold = RING || NP <= 8;  // a thread's inputs stay in registers for their second use
-  constexpr bool kKeep = RING && NP <= 2;  // and so do u and xh
+  constexpr bool kKeep = NP * VEC <= 16;  // u and xh stay in registers for their second use, else the inputs
   extern __shared__ __align__(128) uint8_t ln_rows[];
   __shared__ uint64_t full[kLnSlotsMax];
   __shared__ float red[2][2][16];
@@ -237,25 +304,24 @@ __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
   const int pieces = d / VEC;
   const int64_t r0 = (int64_t)blockIdx.x * rows;
   const int nrows = (int)(T - r0 < rows ? T - r0 : rows);
-  const uint32_t row_bytes = (uint32_t)d * ES, slot_bytes = row_bytes * (dres ? 3u : 2u);
+  const uint32_t row_bytes = (uint32_t)d * ES, region = ln_region(row_bytes), slot_bytes = region * (dres ? 3u : 2u);
+  const int64_t total = T * (int64_t)row_bytes;
   auto issue = [&](int rr, int s) {  // thread 0 only
     uint8_t* slot = ln_rows + (size_t)s * slot_bytes;
     const int64_t off = (r0 + rr) * (int64_t)row_bytes;
-    mbar_arrive_expect_tx(&full[s], slot_bytes);
-    bulk_load(slot, static_cast<const uint8_t*>(dY) + off, row_bytes, &full[s]);
-    bulk_load(slot + row_bytes, static_cast<const uint8_t*>(x) + off, row_bytes, &full[s]);
-    if (dres) bulk_load(slot + 2 * row_bytes, static_cast<const uint8_t*>(dres) + off, row_bytes, &full[s]);
+    const uint32_t n = ln_copy_bytes<VEC == 8>(off, row_bytes, total);
+    ln_copy<VEC == 8>(slot, dY, off, row_bytes, n, &full[s]);
+    ln_copy<VEC == 8>(slot + region, x, off, row_bytes, n, &full[s]);
+    if (dres) ln_copy<VEC == 8>(slot + 2 * region, dres, off, row_bytes, n, &full[s]);
+    mbar_arrive_expect_tx(&full[s], n * (dres ? 3u : 2u));
   };
-  if (RING) {
-    if (t == 0) {
-      for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
-      give_up = 0;
-      fence_mbar_init();
-    }
-    __syncthreads();
-    if (t == 0)
-      for (int k = 0; k < S && k < nrows; ++k) issue(k, k);
+  if (t == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+    give_up = 0;
+    fence_mbar_init();
+    for (int k = 0; k < S && k < nrows; ++k) issue(k, k);
   }
+  __syncthreads();
   E ag[NP][kUnits], ab[NP][kUnits];
 #pragma unroll
   for (int k = 0; k < NP; ++k)
@@ -265,7 +331,7 @@ __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
     const int i = k * (int)blockDim.x + t;
-    if (kHold && i < pieces) pg[k].load(g, (int64_t)i * VEC);
+    if (i < pieces) pg[k].load(g, (int64_t)i * VEC);
   }
   const float inv_d = 1.0f / (float)d;
   float mu_next = mean[r0], rs_next = rstd[r0];
@@ -276,13 +342,9 @@ __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
     const float mu = mu_next, rs = rs_next;
     if (rr + 1 < nrows) { mu_next = mean[r0 + rr + 1]; rs_next = rstd[r0 + rr + 1]; }
     const int64_t base = (r0 + rr) * d;
-    const uint8_t* slot = nullptr;
-    bool ok = true;
-    if (RING) {
-      ok = mbar_wait(&full[s], par, &give_up);
-      if (!ok) give_up = 1;
-      slot = ln_rows + (size_t)s * slot_bytes;
-    }
+    const bool ok = mbar_wait(&full[s], par, &give_up);
+    if (!ok) give_up = 1;
+    const uint8_t* slot = ln_rows + (size_t)s * slot_bytes + (VEC == 8 ? 0 : (int)((base * ES) & 15));
     Piece<F32, VEC> py[NP], px[NP], pr[NP];
     E u[kKeep ? NP : 1][kUnits], xh[kKeep ? NP : 1][kUnits];
     E su_t = all<VEC>(0.0f), sx_t = all<VEC>(0.0f);
@@ -290,17 +352,10 @@ __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
     for (int k = 0; k < NP; ++k) {
       const int i = k * (int)blockDim.x + t;
       if (i >= pieces) continue;
-      const int64_t j = (int64_t)i * VEC;
-      if (RING) {
-        py[k].load(slot, j);
-        px[k].load(slot + row_bytes, j);
-        if (dres) pr[k].load(slot + 2 * row_bytes, j);
-      } else {
-        py[k].load(dY, base + j);
-        px[k].load(x, base + j);
-        if (kHold && dres) pr[k].load(dres, base + j);
-        if (!kHold) pg[k].load(g, j);
-      }
+      const int j = i * VEC;
+      py[k].load(slot, j);
+      px[k].load(slot + region, j);
+      if (dres) pr[k].load(slot + 2 * region, j);
     }
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
@@ -319,29 +374,20 @@ __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
     const float both = ln_warp_sum2(sum(su_t), sum(sx_t), lane);
     if ((lane & 15) == 0) red[rr & 1][lane >> 4][warp] = both;
     // the row's one barrier; a wait that expired anywhere in the block is seen by all after it
-    if (RING) aborted = __syncthreads_or(!ok);
-    else __syncthreads();
+    aborted = __syncthreads_or(!ok);
     if (aborted) break;
     float tot = (lane & 15) < nwarps ? red[rr & 1][lane >> 4][lane & 15] : 0.0f;
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) tot += __shfl_xor_sync(0xFFFFFFFFu, tot, o);
     const float su = __shfl_sync(0xFFFFFFFFu, tot, 0) * inv_d, sx = __shfl_sync(0xFFFFFFFFu, tot, 16) * inv_d;
-    if (RING) {
-      // every thread has its values of row rr in registers: the slot takes row rr + S
-      if (t == 0 && rr + S < nrows) issue(rr + S, s);
-      if (++s == S) { s = 0; par ^= 1u; }
-    }
+    // every thread has its values of row rr in registers: the slot takes row rr + S
+    if (t == 0 && rr + S < nrows) issue(rr + S, s);
+    if (++s == S) { s = 0; par ^= 1u; }
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
       const int i = k * (int)blockDim.x + t;
       if (i >= pieces) continue;
       const int64_t j = (int64_t)i * VEC;
-      if (!kHold) {
-        py[k].load(dY, base + j);
-        px[k].load(x, base + j);
-        pg[k].load(g, j);
-        if (dres) pr[k].load(dres, base + j);
-      }
       E v[kUnits];
 #pragma unroll
       for (int e = 0; e < kUnits; ++e) {
@@ -400,13 +446,27 @@ cudaError_t launched(const Launch& L) {
   return cudaGetLastError();
 }
 
+// Slots of a ring, at least one, within a block's share of the shared memory; fewer blocks per SM where that leaves
+// each fewer than three.
+int ring_slots(size_t slot, int* per_sm) {
+  while (*per_sm > 1 && kLnSmemBudget / *per_sm < 3 * slot) --*per_sm;
+  const int n = (int)(kLnSmemBudget / *per_sm / slot);
+  return n < kLnSlotsMax ? n : kLnSlotsMax;
+}
+
 template <int F32, int VEC, int NP, int W>
 cudaError_t fwd_go(const void* x, const void* g, const void* b, int64_t T, int d, float eps, void* y, float* mean,
                    float* rstd, const Launch& L) {
+  auto* k = k_layernorm_fwd<F32, VEC, NP, W>;
   constexpr int rows = W < 8 ? 8 / W : 1;
-  const int64_t need = (T + rows - 1) / rows, wave = (int64_t)L.num_sms * ln_fwd_per_sm(F32, VEC, W);
-  k_layernorm_fwd<F32, VEC, NP, W><<<(unsigned)(need < wave ? need : wave), ln_fwd_threads(W), 0, L.stream>>>(
-      x, g, b, T, d, eps, y, mean, rstd);
+  const size_t slot = ln_region((uint32_t)(rows * d * (F32 ? 4 : 2)));
+  int per_sm = ln_fwd_per_sm(F32, VEC, W);
+  const int S = ring_slots(slot, &per_sm);
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLnSmemBudget);
+  if (e != cudaSuccess) return e;
+  const int64_t need = (T + rows - 1) / rows, wave = (int64_t)L.num_sms * per_sm;
+  k<<<(unsigned)(need < wave ? need : wave), ln_fwd_threads(W), S * slot, L.stream>>>(x, g, b, T, d, eps, S, y, mean,
+                                                                                      rstd, L.status);
   return launched(L);
 }
 
@@ -443,54 +503,39 @@ cudaError_t fwd_t(const void* x, const void* g, const void* b, int64_t T, int d,
 
 // The backward's launch shape.  d is a multiple of 8: a thread has 1, 2 or 4 pieces of 8 columns (d up to
 // 4096, 8192, 16384); otherwise 4, 8, 16 or 32 single columns.
-struct BwdShape {
-  int np, threads, per_sm, S;
-};
-constexpr size_t kLnSmemBudget = 200 * 1024;  // per SM
-BwdShape bwd_shape(int d, int f32, bool dres) {
-  BwdShape s{};
-  const bool ring = d % 8 == 0;
-  const int pieces = ring ? d / 8 : d;
-  s.np = ring ? 1 : 4;
-  while (pieces > kLnThreads * s.np) s.np *= 2;
-  s.threads = ((pieces + s.np - 1) / s.np + 31) / 32 * 32;
-  if (s.threads < 64 && !ring) s.threads = 64;
-  s.per_sm = s.np * (ring ? 8 : 1) <= 8 ? 2 : 1;
-  if (ring) {
-    const size_t slot = (size_t)d * (f32 ? 4 : 2) * (dres ? 3 : 2);
-    if (2 * 3 * slot > kLnSmemBudget) s.per_sm = 1;
-    s.S = (int)(kLnSmemBudget / s.per_sm / slot);
-    if (s.S > kLnSlotsMax) s.S = kLnSlotsMax;
-  }
-  return s;
-}
-
-template <int F32, int VEC, int NP, int RING>
-cudaError_t bwd_go(const BwdShape& s, const void* dY, const void* x, const void* g, const float* mean, const float* rstd,
-                   const void* dres, int64_t T, int d, void* dX, float* part, int nblk, int rows, const Launch& L) {
-  auto* k = k_layernorm_bwd<F32, VEC, NP, RING>;
-  size_t smem = 0;
-  if (RING) {
-    smem = (size_t)s.S * d * (F32 ? 4 : 2) * (dres ? 3 : 2);
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLnSmemBudget);
-    if (e != cudaSuccess) return e;
-  }
-  k<<<nblk, s.threads, smem, L.stream>>>(dY, x, g, mean, rstd, dres, T, d, rows, s.S, dX, part, L.status);
+template <int F32, int VEC, int NP>
+cudaError_t bwd_go(const void* dY, const void* x, const void* g, const float* mean, const float* rstd, const void* dres,
+                   int64_t T, int d, void* dX, float* part, int* nblk, const Launch& L) {
+  auto* k = k_layernorm_bwd<F32, VEC, NP>;
+  const int threads = ((d / VEC + NP - 1) / NP + 31) / 32 * 32;
+  const size_t slot = (size_t)ln_region((uint32_t)(d * (F32 ? 4 : 2))) * (dres ? 3 : 2);
+  int per_sm = NP * VEC <= 8 ? 2 : 1;
+  const int S = ring_slots(slot, &per_sm);
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLnSmemBudget);
+  if (e != cudaSuccess) return e;
+  // one wave of resident blocks, each with a run of consecutive rows; the workspace holds kLnMaxBlocks partial rows
+  int64_t most = (int64_t)L.num_sms * per_sm;
+  if (most > kLnMaxBlocks) most = kLnMaxBlocks;
+  const int rows = (int)((T + most - 1) / most);
+  *nblk = (int)((T + rows - 1) / rows);
+  k<<<*nblk, threads, S * slot, L.stream>>>(dY, x, g, mean, rstd, dres, T, d, rows, S, dX, part, L.status);
   return launched(L);
 }
 
 template <int F32>
-cudaError_t bwd_t(const BwdShape& s, const void* dY, const void* x, const void* g, const float* mean, const float* rstd,
-                  const void* dres, int64_t T, int d, void* dX, float* part, int nblk, int rows, const Launch& L) {
+cudaError_t bwd_t(const void* dY, const void* x, const void* g, const float* mean, const float* rstd, const void* dres,
+                  int64_t T, int d, void* dX, float* part, int* nblk, const Launch& L) {
+#define FP8Q_LN_BWD(VEC, NP) return bwd_go<F32, VEC, NP>(dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, L)
   if (d % 8 == 0) {
-    if (s.np == 1) return bwd_go<F32, 8, 1, 1>(s, dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, rows, L);
-    if (s.np == 2) return bwd_go<F32, 8, 2, 1>(s, dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, rows, L);
-    return bwd_go<F32, 8, 4, 1>(s, dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, rows, L);
+    if (d <= 8 * kLnThreads) FP8Q_LN_BWD(8, 1);
+    if (d <= 16 * kLnThreads) FP8Q_LN_BWD(8, 2);
+    FP8Q_LN_BWD(8, 4);
   }
-  if (s.np == 4) return bwd_go<F32, 1, 4, 0>(s, dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, rows, L);
-  if (s.np == 8) return bwd_go<F32, 1, 8, 0>(s, dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, rows, L);
-  if (s.np == 16) return bwd_go<F32, 1, 16, 0>(s, dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, rows, L);
-  return bwd_go<F32, 1, 32, 0>(s, dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, rows, L);
+  if (d <= 4 * kLnThreads) FP8Q_LN_BWD(1, 4);
+  if (d <= 8 * kLnThreads) FP8Q_LN_BWD(1, 8);
+  if (d <= 16 * kLnThreads) FP8Q_LN_BWD(1, 16);
+  FP8Q_LN_BWD(1, 32);
+#undef FP8Q_LN_BWD
 }
 
 }  // namespace
@@ -500,18 +545,12 @@ cudaError_t launch_layernorm_fwd(const void* x, int f32, const void* g, const vo
   return f32 ? fwd_t<1>(x, g, b, T, d, eps, y, mean, rstd, L) : fwd_t<0>(x, g, b, T, d, eps, y, mean, rstd, L);
 }
 
-// One wave of resident blocks, each with a run of consecutive rows.  The workspace holds kLnMaxBlocks
-// partial rows (or T, where that is less): no more blocks than that run.
 cudaError_t launch_layernorm_bwd(const void* dY, const void* x, int f32, const void* g, const float* mean,
                                  const float* rstd, const void* dres, int64_t T, int d, void* dX, float* dg, float* db,
                                  float* part, const Launch& L) {
-  const BwdShape s = bwd_shape(d, f32, dres != nullptr);
-  int64_t most = (int64_t)L.num_sms * s.per_sm;
-  if (most > kLnMaxBlocks) most = kLnMaxBlocks;
-  const int rows = (int)((T + most - 1) / most);
-  const int nblk = (int)((T + rows - 1) / rows);
-  cudaError_t e = f32 ? bwd_t<1>(s, dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, rows, L)
-                      : bwd_t<0>(s, dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, rows, L);
+  int nblk = 0;
+  cudaError_t e = f32 ? bwd_t<1>(dY, x, g, mean, rstd, dres, T, d, dX, part, &nblk, L)
+                      : bwd_t<0>(dY, x, g, mean, rstd, dres, T, d, dX, part, &nblk, L);
   if (e != cudaSuccess) return e;
   k_layernorm_bwd_finish<<<(2 * d + 31) / 32, 1024, 0, L.stream>>>(part, nblk, d, dg, db);
   return launched(L);
