@@ -82,6 +82,14 @@ __device__ __forceinline__ float ln_warp_sum(float v) {
   return v;
 }
 
+// Sums of two values over the warp: lanes 0-15 end with a's, lanes 16-31 with b's (5 exchanges for both).
+__device__ __forceinline__ float ln_warp_sum2(float a, float b, int lane) {
+  float v = (lane < 16 ? a : b) + __shfl_xor_sync(0xFFFFFFFFu, lane < 16 ? b : a, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
 // ---------------------------------------------------------------------------
 // Rows on their way in: bulk copies into a ring of slots in shared memory, completing on a slot's
 // mbarrier, so that the bytes in flight are set by the ring and not by registers.
@@ -118,34 +126,47 @@ __device__ __forceinline__ void ln_copy(uint8_t* dst, const void* src, int64_t o
 }
 
 // ---------------------------------------------------------------------------
-// Forward: W warps hold a row in registers, NP pieces a lane (piece k of lane l of warp w is piece
-// (k W + w) 32 + l of the row); a block of max(W, 8) warps takes kRows = 8 / W consecutive rows at a time (one
-// slot of the ring, one copy) and walks them with the grid's stride.  Each warp takes the mean and
-// the sum of squares about it of its own elements, in two passes over its registers; the warps' (mean, M2)
-// pairs are then joined, mean = sum n_w mean_w / d and M2 = sum (M2_w + n_w (mean_w - mean)^2), so a row
-// costs one block barrier and nothing cancels.
+// Forward: W warps hold RT rows at once in registers, NP pieces of each row a lane (piece k of lane l of warp w
+// is piece (k W + w) 32 + l); a block of max(W, 8) warps takes kRows consecutive rows at a time (one slot of the
+// ring, one copy) and walks them with the grid's stride.  Each warp takes the mean and the sum of
+// squares about it of its own elements, in two passes over its registers; the warps' (mean, M2) pairs are then joined,
+// mean = sum n_w mean_w / d and M2 = sum (M2_w + n_w (mean_w - mean)^2), so a row costs one block barrier and
+// nothing cancels.  bf16 rows go two at a time (RT = 2): what bounds them is instructions, and the
+// second row shares the unpacking of gain and bias and the exchanges (T = 16384, d = 5120: 66 -> LNFWD us).
 // ---------------------------------------------------------------------------
 constexpr int ln_fwd_threads(int W) { return W < 8 ? 256 : 32 * W; }
 // Resident blocks per SM by registers: 512 threads of 128 for pieces of 8, 768 of 80 for single columns.  They hold a
-// thread's gain and bias too: read again for each row, those come from L2 (the ring leaves L1 too little), and
-// the rows wait for them (T = 16384, d = 5120: 70 us against LNFWD us).
-constexpr int ln_fwd_per_sm(int F32, int VEC, int W) {
+// thread's gain and bias too: read again for each row, those come from L2 (the ring leaves L1 too little).
+constexpr int ln_fwd_per_sm(int VEC, int W) {
   const int n = (VEC == 8 ? 512 : 768) / ln_fwd_threads(W);
   return n > 0 ? n : 1;
 }
 
-template <int F32, int VEC, int NP, int W>
-__global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(F32, VEC, W))
+// Sums of RT values over the warp, valid in every lane.
+template <int RT>
+__device__ __forceinline__ void ln_warp_sums(float (&v)[RT], int lane) {
+  if constexpr (RT == 1) {
+    v[0] = ln_warp_sum(v[0]);
+  } else {
+    const float t = ln_warp_sum2(v[0], v[1], lane);
+    v[0] = __shfl_sync(0xFFFFFFFFu, t, 0);
+    v[1] = __shfl_sync(0xFFFFFFFFu, t, 16);
+  }
+}
+
+template <int F32, int VEC, int NP, int W, int RT>
+__global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(VEC, W))
     k_layernorm_fwd(const void* x, const void* __restrict__ g, const void* __restrict__ b, int64_t T, int d, float eps,
                     int S, void* y, float* __restrict__ mean, float* __restrict__ rstd, unsigned* status) {
   using E = typename Unit<VEC>::T;
   constexpr int kUnits = Unit<VEC>::kCount, ES = F32 ? 4 : 2;
-  constexpr int kRows = W < 8 ? 8 / W : 1;
+  constexpr int kRows = W < 8 ? RT * (8 / W) : RT;
+  static_assert(RT == 1 || W <= 16, "two rows join in the warp's halves");
   extern __shared__ __align__(128) uint8_t ln_rows[];
   __shared__ uint64_t full[kLnSlotsMax];
   __shared__ float2 pairs[2][kRows][W];
   __shared__ volatile int give_up;
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W, r = (threadIdx.x >> 5) / W;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W, r = (threadIdx.x >> 5) / W * RT;  // r: its first row
   const int pieces = d / VEC;
   const uint32_t row_bytes = (uint32_t)d * ES, slot_bytes = ln_region(kRows * row_bytes);
   const int64_t total = T * (int64_t)row_bytes, groups = (T + kRows - 1) / kRows;
@@ -188,40 +209,49 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(F32, VEC, W))
   int64_t group = blockIdx.x;
   for (; group < groups; group += gridDim.x, turn ^= 1) {
     const int64_t row = group * kRows + r;
-    bool ok = mbar_wait(&full[s], par, &give_up);
+    const bool ok = mbar_wait(&full[s], par, &give_up);
     if (!ok) give_up = 1;
-    // x about the warp's mean, in registers
-    E c[NP][kUnits];
-    E sum_t = all<VEC>(0.0f);
-    if (ok && row < T) {
-      const uint8_t* slot = ln_rows + (size_t)s * slot_bytes + (VEC == 8 ? 0 : (int)((group * kRows * row_bytes) & 15));
+    // x about the warp's mean, in registers.  A row past the end (or given up) holds what the slot held: it is not written
+    E c[RT][NP][kUnits];
+    float own_mu[RT], mu[RT], m2[RT];
+    const uint8_t* slot = ln_rows + (size_t)s * slot_bytes + (VEC == 8 ? 0 : (int)((group * kRows * row_bytes) & 15));
+#pragma unroll
+    for (int q = 0; q < RT; ++q) {
+      E sum_t = all<VEC>(0.0f);
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
         const int i = (k * W + warp) * 32 + lane;
         if (i < pieces) {
           Piece<F32, VEC> px;
-          px.load(slot, r * d + i * VEC);
+          px.load(slot, (r + q) * d + i * VEC);
 #pragma unroll
           for (int e = 0; e < kUnits; ++e) {
-            c[k][e] = px.unit(e);
-            sum_t = add(sum_t, c[k][e]);
+            c[q][k][e] = px.unit(e);
+            sum_t = add(sum_t, c[q][k][e]);
           }
         }
       }
+      own_mu[q] = sum(sum_t);
     }
-    const float own_mu = ln_warp_sum(sum(sum_t)) * inv_own;
-    float mu = own_mu;
-    E q = all<VEC>(0.0f);
+    ln_warp_sums<RT>(own_mu, lane);
 #pragma unroll
-    for (int k = 0; k < NP; ++k)
-      if ((k * W + warp) * 32 + lane < pieces)
+    for (int q = 0; q < RT; ++q) {
+      mu[q] = own_mu[q] = own_mu[q] * inv_own;
+      E sq = all<VEC>(0.0f);
 #pragma unroll
-        for (int e = 0; e < kUnits; ++e) {
-          c[k][e] = add(c[k][e], all<VEC>(-own_mu));
-          q = fma(c[k][e], c[k][e], q);
-        }
-    float m2 = ln_warp_sum(sum(q));
-    if (W > 1 && lane == 0) pairs[turn][r][warp] = make_float2(mu, m2);
+      for (int k = 0; k < NP; ++k)
+        if ((k * W + warp) * 32 + lane < pieces)
+#pragma unroll
+          for (int e = 0; e < kUnits; ++e) {
+            c[q][k][e] = add(c[q][k][e], all<VEC>(-own_mu[q]));
+            sq = fma(c[q][k][e], c[q][k][e], sq);
+          }
+      m2[q] = sum(sq);
+    }
+    ln_warp_sums<RT>(m2, lane);
+    if (W > 1 && lane == 0)
+#pragma unroll
+      for (int q = 0; q < RT; ++q) pairs[turn][r + q][warp] = make_float2(mu[q], m2[q]);
     // the one barrier: the pairs are there, and every thread has its part of the slot, which takes the group S
     // turns ahead; a wait that expired anywhere in the block is seen by all
     aborted = __syncthreads_or(!ok);
@@ -229,32 +259,48 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(F32, VEC, W))
     if (threadIdx.x == 0 && group + S * (int64_t)gridDim.x < groups) issue(group + S * (int64_t)gridDim.x, s);
     if (++s == S) { s = 0; par ^= 1u; }
     if (W > 1) {
-      const float2 of = pairs[turn][r][lane & (W - 1)];
-      mu = of.x * lane_share;
+      // lanes 0-15 join the first row's pairs, 16-31 the second's
+      const float2 of = pairs[turn][r + (RT == 2 ? lane >> 4 : 0)][lane & (W - 1)];
+      float m = of.x * lane_share;
 #pragma unroll
-      for (int o = W / 2; o > 0; o >>= 1) mu += __shfl_xor_sync(0xFFFFFFFFu, mu, o);
-      const float off = of.x - mu;
-      m2 = fmaf(off * off, lane_count, of.y);
+      for (int o = W / 2; o > 0; o >>= 1) m += __shfl_xor_sync(0xFFFFFFFFu, m, o);
+      const float off = of.x - m;
+      float v = fmaf(off * off, lane_count, of.y);
 #pragma unroll
-      for (int o = W / 2; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xFFFFFFFFu, m2, o);
+      for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+#pragma unroll
+      for (int q = 0; q < RT; ++q) {
+        mu[q] = RT == 1 ? m : __shfl_sync(0xFFFFFFFFu, m, 16 * q);
+        m2[q] = RT == 1 ? v : __shfl_sync(0xFFFFFFFFu, v, 16 * q);
+      }
     }
-    if (row >= T) continue;
-    const float rs = rsqrtf(fmaf(m2, inv_d, eps));
-    if (warp == 0 && lane == 0) {
-      mean[row] = mu;
-      rstd[row] = rs;
+    float rs[RT], shift[RT];
+#pragma unroll
+    for (int q = 0; q < RT; ++q) {
+      rs[q] = rsqrtf(fmaf(m2[q], inv_d, eps));
+      shift[q] = own_mu[q] - mu[q];
+      if (warp == 0 && lane == 0 && row + q < T) {
+        mean[row + q] = mu[q];
+        rstd[row + q] = rs[q];
+      }
     }
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
       const int i = (k * W + warp) * 32 + lane;
       if (i < pieces) {
-        E v[kUnits];
+        E gu[kUnits], bu[kUnits];
 #pragma unroll
         for (int e = 0; e < kUnits; ++e) {
-          const E f = mul(pg[k].unit(e), all<VEC>(rs)), h = add(c[k][e], all<VEC>(own_mu - mu));
-          v[e] = b ? fma(h, f, pb[k].unit(e)) : mul(h, f);
+          gu[e] = pg[k].unit(e);
+          bu[e] = b ? pb[k].unit(e) : all<VEC>(0.0f);
         }
-        Piece<F32, VEC>::store(y, row * d + (int64_t)i * VEC, v);
+#pragma unroll
+        for (int q = 0; q < RT; ++q) {
+          E v[kUnits];
+#pragma unroll
+          for (int e = 0; e < kUnits; ++e) v[e] = fma(add(c[q][k][e], all<VEC>(shift[q])), mul(gu[e], all<VEC>(rs[q])), bu[e]);
+          if (row + q < T) Piece<F32, VEC>::store(y, (row + q) * d + (int64_t)i * VEC, v);
+        }
       }
     }
   }
@@ -278,14 +324,6 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(F32, VEC, W))
 // threads leave together after the row's barrier and thread 0 waits for the copies in flight before the block exits.
 // ---------------------------------------------------------------------------
 constexpr int kLnThreads = 512;
-
-// Sums of two values over the warp: lanes 0-15 end with a's, lanes 16-31 with b's (5 exchanges for both).
-__device__ __forceinline__ float ln_warp_sum2(float a, float b, int lane) {
-  float v = (lane < 16 ? a : b) + __shfl_xor_sync(0xFFFFFFFFu, lane < 16 ? b : a, 16);
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
 
 template <int F32, int VEC, int NP>
 __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
@@ -457,10 +495,10 @@ int ring_slots(size_t slot, int* per_sm) {
 template <int F32, int VEC, int NP, int W>
 cudaError_t fwd_go(const void* x, const void* g, const void* b, int64_t T, int d, float eps, void* y, float* mean,
                    float* rstd, const Launch& L) {
-  auto* k = k_layernorm_fwd<F32, VEC, NP, W>;
-  constexpr int rows = W < 8 ? 8 / W : 1;
+  constexpr int RT = VEC == 8 && !F32 && NP <= 3 ? 2 : 1, rows = W < 8 ? RT * (8 / W) : RT;
+  auto* k = k_layernorm_fwd<F32, VEC, NP, W, RT>;
   const size_t slot = ln_region((uint32_t)(rows * d * (F32 ? 4 : 2)));
-  int per_sm = ln_fwd_per_sm(F32, VEC, W);
+  int per_sm = ln_fwd_per_sm(VEC, W);
   const int S = ring_slots(slot, &per_sm);
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLnSmemBudget);
   if (e != cudaSuccess) return e;
@@ -470,25 +508,36 @@ cudaError_t fwd_go(const void* x, const void* g, const void* b, int64_t T, int d
   return launched(L);
 }
 
-// The fewest warps (a power of two) whose lanes hold the row: up to 4 pieces of 8 columns or 16 single
-// columns a lane.  More than one warp is taken only past half of what it holds, so a lane then has 3 or 4
-// pieces of 8 (up to 16 single columns).
+// The fewest warps (a power of two) whose lanes hold the row: in fp32 up to 4 pieces of 8 columns a lane, in bf16
+// up to 3 (two rows of 4 do not fit in the registers: T = 16384, d = 4096 takes 70 us so, one such row at a time 51, and
+// LN4096 with twice the warps), in odd widths up to 16 single columns.
 template <int F32>
 cudaError_t fwd_t(const void* x, const void* g, const void* b, int64_t T, int d, float eps, void* y, float* mean,
                   float* rstd, const Launch& L) {
 #define FP8Q_LN_FWD(VEC, NP, W) return fwd_go<F32, VEC, NP, W>(x, g, b, T, d, eps, y, mean, rstd, L)
+  constexpr int kCols = 256;  // of a warp's lanes with a piece each
   if (d % 8 == 0) {
-    if (d <= 256) FP8Q_LN_FWD(8, 1, 1);
-    if (d <= 512) FP8Q_LN_FWD(8, 2, 1);
-    if (d <= 768) FP8Q_LN_FWD(8, 3, 1);
-    if (d <= 1024) FP8Q_LN_FWD(8, 4, 1);
-    if (d <= 1536) FP8Q_LN_FWD(8, 3, 2);
-    if (d <= 2048) FP8Q_LN_FWD(8, 4, 2);
-    if (d <= 4096 - 1024) FP8Q_LN_FWD(8, 3, 4);
-    if (d <= 4096) FP8Q_LN_FWD(8, 4, 4);
-    if (d <= 6144) FP8Q_LN_FWD(8, 3, 8);
-    if (d <= 8192) FP8Q_LN_FWD(8, 4, 8);
-    if (d <= 12288) FP8Q_LN_FWD(8, 3, 16);
+    if (d <= kCols) FP8Q_LN_FWD(8, 1, 1);
+    if (d <= 2 * kCols) FP8Q_LN_FWD(8, 2, 1);
+    if (d <= 3 * kCols) FP8Q_LN_FWD(8, 3, 1);
+    if constexpr (F32) {
+      if (d <= 4 * kCols) FP8Q_LN_FWD(8, 4, 1);
+      if (d <= 6 * kCols) FP8Q_LN_FWD(8, 3, 2);
+      if (d <= 8 * kCols) FP8Q_LN_FWD(8, 4, 2);
+      if (d <= 12 * kCols) FP8Q_LN_FWD(8, 3, 4);
+      if (d <= 16 * kCols) FP8Q_LN_FWD(8, 4, 4);
+      if (d <= 24 * kCols) FP8Q_LN_FWD(8, 3, 8);
+      if (d <= 32 * kCols) FP8Q_LN_FWD(8, 4, 8);
+    } else {
+      if (d <= 4 * kCols) FP8Q_LN_FWD(8, 2, 2);
+      if (d <= 6 * kCols) FP8Q_LN_FWD(8, 3, 2);
+      if (d <= 8 * kCols) FP8Q_LN_FWD(8, 2, 4);
+      if (d <= 12 * kCols) FP8Q_LN_FWD(8, 3, 4);
+      if (d <= 16 * kCols) FP8Q_LN_FWD(8, 2, 8);
+      if (d <= 24 * kCols) FP8Q_LN_FWD(8, 3, 8);
+      if (d <= 32 * kCols) FP8Q_LN_FWD(8, 2, 16);
+    }
+    if (d <= 48 * kCols) FP8Q_LN_FWD(8, 3, 16);
     FP8Q_LN_FWD(8, 4, 16);
   }
   if (d <= 128) FP8Q_LN_FWD(1, 4, 1);
