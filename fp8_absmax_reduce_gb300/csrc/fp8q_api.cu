@@ -1442,8 +1442,8 @@ int layernorm_fwd(const void* x, fp8q_dtype dtype, const void* g, const void* b,
 }
 
 size_t layernorm_bwd_workspace_size(int64_t T, int64_t d) {
-  if (T < 1 || d < 1) return 0;
-  return round256((size_t)(T < kLnMaxBlocks ? T : kLnMaxBlocks) * 2 * (size_t)d * 4);
+  if (T < 1 || d < 1 || d > 16384) return 0;
+  return round256((size_t)layernorm_bwd_blocks(T, (int)d) * 2 * (size_t)d * 4);
 }
 
 int layernorm_bwd(const void* dY, const void* x, fp8q_dtype dtype, const void* g, const float* mean, const float* rstd,

@@ -78,8 +78,8 @@ cudaError_t launch_attn_bwd_dq(const uint16_t* qkv, const uint16_t* datt, int64_
 // Layer norm of x [T, d] (bf16, or fp32 with f32 != 0; g, b, y alike; b may be null).
 cudaError_t launch_layernorm_fwd(const void* x, int f32, const void* g, const void* b, int64_t T, int d, float eps,
                                  void* y, float* mean, float* rstd, const Launch& L);
-// Backward: dX (dres may be null), dg and db (db may be null); part: min(T, kLnMaxBlocks) x 2 d floats.
-constexpr int kLnMaxBlocks = 512;
+// Backward: dX (dres may be null), dg and db (db may be null); part: layernorm_bwd_blocks(T, d) x 2 d floats.
+int layernorm_bwd_blocks(int64_t T, int d);
 cudaError_t launch_layernorm_bwd(const void* dY, const void* x, int f32, const void* g, const float* mean,
                                  const float* rstd, const void* dres, int64_t T, int d, void* dX, float* dg, float* db,
                                  float* part, const Launch& L);

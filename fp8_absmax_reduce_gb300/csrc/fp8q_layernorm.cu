@@ -132,13 +132,13 @@ __device__ __forceinline__ void ln_copy(uint8_t* dst, const void* src, int64_t o
 // squares about it of its own elements, in two passes over its registers; the warps' (mean, M2) pairs are then joined,
 // mean = sum n_w mean_w / d and M2 = sum (M2_w + n_w (mean_w - mean)^2), so a row costs one block barrier and
 // nothing cancels.  bf16 rows go two at a time (RT = 2): what bounds them is instructions, and the
-// second row shares the unpacking of gain and bias and the exchanges (T = 16384, d = 5120: 66 -> LNFWD us).
+// second row shares the unpacking of gain and bias and the exchanges (T = 16384, d = 5120: 66 -> 60 us).
 // ---------------------------------------------------------------------------
 constexpr int ln_fwd_threads(int W) { return W < 8 ? 256 : 32 * W; }
 // Resident blocks per SM by registers: 512 threads of 128 for pieces of 8, 768 of 80 for single columns.  They hold a
 // thread's gain and bias too: read again for each row, those come from L2 (the ring leaves L1 too little).
 constexpr int ln_fwd_per_sm(int VEC, int W) {
-  const int n = (VEC == 8 ? 512 : 768) / ln_fwd_threads(W);
+  const int n = (VEC == 8 ? (W == 10 ? 640 : 512) : 768) / ln_fwd_threads(W);
   return n > 0 ? n : 1;
 }
 
@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(VEC, W))
   constexpr int kUnits = Unit<VEC>::kCount, ES = F32 ? 4 : 2;
   constexpr int kRows = W < 8 ? RT * (8 / W) : RT;
   static_assert(RT == 1 || W <= 16, "two rows join in the warp's halves");
+  constexpr int kJoin = W <= 1 ? 1 : W <= 2 ? 2 : W <= 4 ? 4 : W <= 8 ? 8 : W <= 16 ? 16 : 32;  // lanes that join W pairs
   extern __shared__ __align__(128) uint8_t ln_rows[];
   __shared__ uint64_t full[kLnSlotsMax];
   __shared__ float2 pairs[2][kRows][W];
@@ -193,7 +194,8 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(VEC, W))
   };
   const int n_own = count(warp);
   const float inv_own = n_own ? 1.0f / (float)n_own : 0.0f, inv_d = 1.0f / (float)d;
-  const float lane_count = (float)count(lane & (W - 1)), lane_share = lane_count * inv_d;
+  const int of_warp = lane & (kJoin - 1);
+  const float lane_count = of_warp < W ? (float)count(of_warp) : 0.0f, lane_share = lane_count * inv_d;
   Piece<F32, VEC> pg[NP], pb[NP];
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
@@ -260,14 +262,15 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(VEC, W))
     if (++s == S) { s = 0; par ^= 1u; }
     if (W > 1) {
       // lanes 0-15 join the first row's pairs, 16-31 the second's
-      const float2 of = pairs[turn][r + (RT == 2 ? lane >> 4 : 0)][lane & (W - 1)];
+      float2 of = make_float2(0.0f, 0.0f);
+      if (of_warp < W) of = pairs[turn][r + (RT == 2 ? lane >> 4 : 0)][of_warp];
       float m = of.x * lane_share;
 #pragma unroll
-      for (int o = W / 2; o > 0; o >>= 1) m += __shfl_xor_sync(0xFFFFFFFFu, m, o);
+      for (int o = kJoin / 2; o > 0; o >>= 1) m += __shfl_xor_sync(0xFFFFFFFFu, m, o);
       const float off = of.x - m;
       float v = fmaf(off * off, lane_count, of.y);
 #pragma unroll
-      for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+      for (int o = kJoin / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
 #pragma unroll
       for (int q = 0; q < RT; ++q) {
         mu[q] = RT == 1 ? m : __shfl_sync(0xFFFFFFFFu, m, 16 * q);
@@ -325,8 +328,8 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(VEC, W))
 // ---------------------------------------------------------------------------
 constexpr int kLnThreads = 512;
 
-template <int F32, int VEC, int NP>
-__global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
+template <int F32, int VEC, int NP, int STRIDE>
+__global__ void __launch_bounds__(STRIDE > 0 && STRIDE < kLnThreads ? STRIDE : kLnThreads, (NP * VEC <= 8 ? 1024 : 512) / (STRIDE > 0 ? STRIDE : kLnThreads))
     k_layernorm_bwd(const void* dY, const void* x, const void* __restrict__ g, const float* __restrict__ mean,
                     const float* __restrict__ rstd, const void* dres, int64_t T, int d, int rows, int S, void* dX,
                     float* __restrict__ part, unsigned* status) {
@@ -340,6 +343,7 @@ __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
   __shared__ volatile int give_up;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, nwarps = blockDim.x >> 5;
   const int pieces = d / VEC;
+  const int stride = STRIDE ? STRIDE : (int)blockDim.x;  // a constant lets single columns use immediate offsets
   const int64_t r0 = (int64_t)blockIdx.x * rows;
   const int nrows = (int)(T - r0 < rows ? T - r0 : rows);
   const uint32_t row_bytes = (uint32_t)d * ES, region = ln_region(row_bytes), slot_bytes = region * (dres ? 3u : 2u);
@@ -368,7 +372,7 @@ __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
   Piece<F32, VEC> pg[NP];
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
-    const int i = k * (int)blockDim.x + t;
+    const int i = k * stride + t;
     if (i < pieces) pg[k].load(g, (int64_t)i * VEC);
   }
   const float inv_d = 1.0f / (float)d;
@@ -388,7 +392,7 @@ __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
     E su_t = all<VEC>(0.0f), sx_t = all<VEC>(0.0f);
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      const int i = k * (int)blockDim.x + t;
+      const int i = k * stride + t;
       if (i >= pieces) continue;
       const int j = i * VEC;
       py[k].load(slot, j);
@@ -397,7 +401,7 @@ __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
     }
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      if (k * (int)blockDim.x + t >= pieces) continue;
+      if (k * stride + t >= pieces) continue;
 #pragma unroll
       for (int e = 0; e < kUnits; ++e) {
         const E dy = py[k].unit(e), uu = mul(dy, pg[k].unit(e));
@@ -423,7 +427,7 @@ __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
     if (++s == S) { s = 0; par ^= 1u; }
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      const int i = k * (int)blockDim.x + t;
+      const int i = k * stride + t;
       if (i >= pieces) continue;
       const int64_t j = (int64_t)i * VEC;
       E v[kUnits];
@@ -449,7 +453,7 @@ __global__ void __launch_bounds__(kLnThreads, NP * VEC <= 8 ? 2 : 1)
   float* pgp = part + (int64_t)blockIdx.x * 2 * d;
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
-    const int i = k * (int)blockDim.x + t;
+    const int i = k * stride + t;
     if (i >= pieces) continue;
     Piece<1, VEC>::store(pgp, (int64_t)i * VEC, ag[k]);
     Piece<1, VEC>::store(pgp + d, (int64_t)i * VEC, ab[k]);
@@ -464,8 +468,13 @@ __global__ void __launch_bounds__(1024) k_layernorm_bwd_finish(const float* __re
   const int j = blockIdx.x * 32 + tx;
   float s = 0.0f;
   if (j < 2 * d)
-#pragma unroll 4
-    for (int k = ty; k < nblk; k += 32) s += part[(int64_t)k * 2 * d + j];
+    for (int k = ty; k < nblk; k += 32 * 8) {
+      float v[8];  // 8 loads in flight
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = k + 32 * q < nblk ? part[(int64_t)(k + 32 * q) * 2 * d + j] : 0.0f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s += v[q];
+    }
   sum[ty][tx] = s;
   __syncthreads();
 #pragma unroll
@@ -510,7 +519,7 @@ cudaError_t fwd_go(const void* x, const void* g, const void* b, int64_t T, int d
 
 // The fewest warps (a power of two) whose lanes hold the row: in fp32 up to 4 pieces of 8 columns a lane, in bf16
 // up to 3 (two rows of 4 do not fit in the registers: T = 16384, d = 4096 takes 70 us so, one such row at a time 51, and
-// LN4096 with twice the warps), in odd widths up to 16 single columns.
+// 42 with twice the warps), in odd widths up to 16 single columns.
 template <int F32>
 cudaError_t fwd_t(const void* x, const void* g, const void* b, int64_t T, int d, float eps, void* y, float* mean,
                   float* rstd, const Launch& L) {
@@ -534,6 +543,7 @@ cudaError_t fwd_t(const void* x, const void* g, const void* b, int64_t T, int d,
       if (d <= 8 * kCols) FP8Q_LN_FWD(8, 2, 4);
       if (d <= 12 * kCols) FP8Q_LN_FWD(8, 3, 4);
       if (d <= 16 * kCols) FP8Q_LN_FWD(8, 2, 8);
+      if (d <= 20 * kCols) FP8Q_LN_FWD(8, 2, 10);
       if (d <= 24 * kCols) FP8Q_LN_FWD(8, 3, 8);
       if (d <= 32 * kCols) FP8Q_LN_FWD(8, 2, 16);
     }
@@ -551,43 +561,72 @@ cudaError_t fwd_t(const void* x, const void* g, const void* b, int64_t T, int d,
 }
 
 // The backward's launch shape.  d is a multiple of 8: a thread has 1, 2 or 4 pieces of 8 columns (d up to
-// 4096, 8192, 16384); otherwise 4, 8, 16 or 32 single columns.
-template <int F32, int VEC, int NP>
+// 4096, 8192, 16384).  Otherwise 1 to 32 single columns, of 128 threads up to d = 1024 and of 512 above.
+constexpr int kLnNarrow = 128;
+constexpr int bwd_np(int d) {
+  const int pieces = d % 8 == 0 ? d / 8 : d, threads = d % 8 == 0 || d > 8 * kLnNarrow ? kLnThreads : kLnNarrow;
+  int np = 1;
+  while (pieces > np * threads) np *= 2;
+  return np;
+}
+constexpr int bwd_threads(int d) {
+  if (d % 8 != 0) return d > 8 * kLnNarrow ? kLnThreads : kLnNarrow;
+  return ((d / 8 + bwd_np(d) - 1) / bwd_np(d) + 31) / 32 * 32;
+}
+// Resident blocks per SM: 1024 threads of 64 registers (up to 16 narrow blocks: a row is a chain of
+// dependent steps of about 0.8 us, so narrow rows need many blocks at work; T = 16384, d = 304: 15 us with 16), or
+// 512 of 128.
+constexpr int bwd_per_sm(int d) {
+  if (bwd_np(d) * (d % 8 == 0 ? 8 : 1) > 8) return 1;
+  const int n = 1024 / bwd_threads(d);
+  return n < 16 ? n : 16;
+}
+constexpr int kLnPlanSms = 152;
+
+template <int F32, int VEC, int NP, int STRIDE>
 cudaError_t bwd_go(const void* dY, const void* x, const void* g, const float* mean, const float* rstd, const void* dres,
                    int64_t T, int d, void* dX, float* part, int* nblk, const Launch& L) {
-  auto* k = k_layernorm_bwd<F32, VEC, NP>;
-  const int threads = ((d / VEC + NP - 1) / NP + 31) / 32 * 32;
+  auto* k = k_layernorm_bwd<F32, VEC, NP, STRIDE>;
   const size_t slot = (size_t)ln_region((uint32_t)(d * (F32 ? 4 : 2))) * (dres ? 3 : 2);
-  int per_sm = NP * VEC <= 8 ? 2 : 1;
+  int per_sm = bwd_per_sm(d);
   const int S = ring_slots(slot, &per_sm);
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLnSmemBudget);
   if (e != cudaSuccess) return e;
-  // one wave of resident blocks, each with a run of consecutive rows; the workspace holds kLnMaxBlocks partial rows
-  int64_t most = (int64_t)L.num_sms * per_sm;
-  if (most > kLnMaxBlocks) most = kLnMaxBlocks;
+  // one wave of resident blocks, each with a run of consecutive rows (at most layernorm_bwd_blocks of them)
+  const int64_t most = (int64_t)(L.num_sms < kLnPlanSms ? L.num_sms : kLnPlanSms) * per_sm;
   const int rows = (int)((T + most - 1) / most);
   *nblk = (int)((T + rows - 1) / rows);
-  k<<<*nblk, threads, S * slot, L.stream>>>(dY, x, g, mean, rstd, dres, T, d, rows, S, dX, part, L.status);
+  k<<<*nblk, bwd_threads(d), S * slot, L.stream>>>(dY, x, g, mean, rstd, dres, T, d, rows, S, dX, part, L.status);
   return launched(L);
 }
 
 template <int F32>
 cudaError_t bwd_t(const void* dY, const void* x, const void* g, const float* mean, const float* rstd, const void* dres,
                   int64_t T, int d, void* dX, float* part, int* nblk, const Launch& L) {
-#define FP8Q_LN_BWD(VEC, NP) return bwd_go<F32, VEC, NP>(dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, L)
+#define FP8Q_LN_BWD(VEC, NP, STRIDE) \
+  return bwd_go<F32, VEC, NP, STRIDE>(dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, L)
   if (d % 8 == 0) {
-    if (d <= 8 * kLnThreads) FP8Q_LN_BWD(8, 1);
-    if (d <= 16 * kLnThreads) FP8Q_LN_BWD(8, 2);
-    FP8Q_LN_BWD(8, 4);
+    if (d <= 8 * kLnThreads) FP8Q_LN_BWD(8, 1, 0);
+    if (d <= 16 * kLnThreads) FP8Q_LN_BWD(8, 2, 0);
+    FP8Q_LN_BWD(8, 4, 0);
   }
-  if (d <= 4 * kLnThreads) FP8Q_LN_BWD(1, 4);
-  if (d <= 8 * kLnThreads) FP8Q_LN_BWD(1, 8);
-  if (d <= 16 * kLnThreads) FP8Q_LN_BWD(1, 16);
-  FP8Q_LN_BWD(1, 32);
+  if (d <= kLnNarrow) FP8Q_LN_BWD(1, 1, kLnNarrow);
+  if (d <= 2 * kLnNarrow) FP8Q_LN_BWD(1, 2, kLnNarrow);
+  if (d <= 4 * kLnNarrow) FP8Q_LN_BWD(1, 4, kLnNarrow);
+  if (d <= 8 * kLnNarrow) FP8Q_LN_BWD(1, 8, kLnNarrow);
+  if (d <= 4 * kLnThreads) FP8Q_LN_BWD(1, 4, kLnThreads);
+  if (d <= 8 * kLnThreads) FP8Q_LN_BWD(1, 8, kLnThreads);
+  if (d <= 16 * kLnThreads) FP8Q_LN_BWD(1, 16, kLnThreads);
+  FP8Q_LN_BWD(1, 32, kLnThreads);
 #undef FP8Q_LN_BWD
 }
 
 }  // namespace
+
+int layernorm_bwd_blocks(int64_t T, int d) {
+  const int64_t n = (int64_t)kLnPlanSms * bwd_per_sm(d);
+  return (int)(T < n ? T : n);
+}
 
 cudaError_t launch_layernorm_fwd(const void* x, int f32, const void* g, const void* b, int64_t T, int d, float eps,
                                  void* y, float* mean, float* rstd, const Launch& L) {
