@@ -376,22 +376,21 @@ def attention_bwd(qkv: torch.Tensor, att: torch.Tensor, lse: torch.Tensor, d_att
 _REAL = (torch.bfloat16, torch.float32)
 
 
-def _fits(t, dtype, shape) -> bool:
-    """Whether t is a dense tensor of this type and shape on the current CUDA device (the library
-    launches there)."""
+def _fits(t, dtype, shape, dev: int) -> bool:
+    """Whether t is a dense tensor of this type and shape on CUDA device dev, the current one (the
+    library launches there)."""
     try:
-        return (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
-                and t.get_device() == torch._C._cuda_getDevice())
+        return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
     except AttributeError:
         return False
 
 
-def _refuse(name: str, t, dtype, shape):
+def _refuse(name: str, t, dtype, shape, dev: int):
     """The reason why _fits is false, raised."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{dev}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, not {dtype}")
     if t.shape != shape:
@@ -399,47 +398,47 @@ def _refuse(name: str, t, dtype, shape):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _need(name: str, t, dtype, shape):
-    if not _fits(t, dtype, shape):
-        _refuse(name, t, dtype, shape)
+def _need(name: str, t, dtype, shape, dev: int):
+    if not _fits(t, dtype, shape, dev):
+        _refuse(name, t, dtype, shape, dev)
 
 
 def _matrix(name: str, t, types=_REAL):
-    """A [rows, columns] argument of one of the types; its shape and type decide the others'."""
+    """A [rows, columns] argument of one of the types; its shape and type decide the others'.  Returns
+    the shape and the current device's index, where it has to be."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in types:
         raise TypeError(f"{name} has dtype {t.dtype}, not {' or '.join(str(d) for d in types)}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not [rows, columns]")
-    if not t.is_contiguous() or t.get_device() != torch._C._cuda_getDevice():
-        _refuse(name, t, t.dtype, t.shape)
-    return t.shape
+    shape, dev = t.shape, torch._C._cuda_getDevice()
+    if len(shape) != 2:
+        raise ValueError(f"{name} has shape {tuple(shape)}, not [rows, columns]")
+    if t.get_device() != dev or not t.is_contiguous():
+        _refuse(name, t, t.dtype, shape, dev)
+    return shape, dev
 
 
-def _out(name: str, t, dtype, shape, device):
+def _out(name: str, t, dtype, shape, dev: int, device):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not _fits(t, dtype, shape):
-        _refuse(name, t, dtype, shape)
+    if not _fits(t, dtype, shape, dev):
+        _refuse(name, t, dtype, shape, dev)
     return t
 
 
-def _scratch(nbytes: int, device, ws):
+def _scratch(nbytes: int, dev: int, device, ws):
     """The caller's workspace, or a new one."""
     if ws is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if not (ws.is_cuda and ws.is_contiguous() and ws.device == device):
+    if ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("the workspace must be a contiguous tensor on the inputs' device")
     if ws.nbytes < nbytes:
         raise ValueError("workspace too small")
     return ws
 
 
-def _raw_stream(stream):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream
+def _raw_stream(stream, dev: int):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 @dataclasses.dataclass(frozen=True)
@@ -491,17 +490,17 @@ class Rope:
 
 
 def _rope_call(name, fn, qkv, pos, rope, n_heads, n_kv_heads, out, stream):
-    T, width = _matrix("qkv", qkv)
+    (T, width), dev = _matrix("qkv", qkv)
     dtype = qkv.dtype
     if width != (n_heads + 2 * n_kv_heads) * rope.head_dim:
         raise ValueError(f"qkv has {width} columns, not ({n_heads} + 2 * {n_kv_heads}) heads of {rope.head_dim}")
-    _need("pos", pos, torch.int32, (T,) if rope.n_axes == 1 and pos.dim() == 1 else (rope.n_axes, T))
+    _need("pos", pos, torch.int32, (T,) if rope.n_axes == 1 and pos.dim() == 1 else (rope.n_axes, T), dev)
     if out is None:
         out = torch.empty_like(qkv)
     elif out is not qkv:
-        _need("out", out, dtype, (T, width))
+        _need("out", out, dtype, (T, width), dev)
     _check(name, fn(qkv.data_ptr(), BF16 if dtype is torch.bfloat16 else F32, T, n_heads, n_kv_heads, rope._ref,
-                    pos.data_ptr(), out.data_ptr(), _raw_stream(stream)))
+                    pos.data_ptr(), out.data_ptr(), _raw_stream(stream, dev)))
     return out
 
 
@@ -522,17 +521,18 @@ def layernorm_fwd(x: torch.Tensor, g: torch.Tensor, b: torch.Tensor | None = Non
                   mean=None, rstd=None, stream=None):
     """Layer norm of x [T,d] with gain g and bias b [d] (all bf16 or all fp32).
     Returns (y [T,d], mean [T] fp32, rstd [T] fp32)."""
-    T, d = shape = _matrix("x", x)
-    dtype, dev = x.dtype, x.device
-    _need("g", g, dtype, (d,))
+    shape, dev = _matrix("x", x)
+    T, d = shape
+    dtype, device = x.dtype, x.device
+    _need("g", g, dtype, (d,), dev)
     if b is not None:
-        _need("b", b, dtype, (d,))
-    y = torch.empty_like(x) if y is None else _out("y", y, dtype, shape, dev)
-    mean = _out("mean", mean, torch.float32, (T,), dev)
-    rstd = _out("rstd", rstd, torch.float32, (T,), dev)
+        _need("b", b, dtype, (d,), dev)
+    y = torch.empty_like(x) if y is None else _out("y", y, dtype, shape, dev, device)
+    mean = _out("mean", mean, torch.float32, (T,), dev, device)
+    rstd = _out("rstd", rstd, torch.float32, (T,), dev, device)
     _check("layernorm_fwd", lib.layernorm_fwd(x.data_ptr(), BF16 if dtype is torch.bfloat16 else F32, g.data_ptr(),
                                               None if b is None else b.data_ptr(), T, d, eps, y.data_ptr(),
-                                              mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream)))
+                                              mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, dev)))
     return y, mean, rstd
 
 
@@ -544,23 +544,24 @@ def layernorm_bwd(dY: torch.Tensor, x: torch.Tensor, g: torch.Tensor, mean: torc
                   dres: torch.Tensor | None = None, dX=None, dg=None, db=None, ws=None, stream=None):
     """Layer norm backward: dY, x (and dres, the residual branch's gradient, added to dX) [T,d], g [d],
     the forward's mean and rstd [T].  Returns (dX [T,d], dg [d] fp32, db [d] fp32)."""
-    T, d = shape = _matrix("x", x)
-    dtype, dev = x.dtype, x.device
-    _need("dY", dY, dtype, shape)
-    _need("g", g, dtype, (d,))
-    _need("mean", mean, torch.float32, (T,))
-    _need("rstd", rstd, torch.float32, (T,))
+    shape, dev = _matrix("x", x)
+    T, d = shape
+    dtype, device = x.dtype, x.device
+    _need("dY", dY, dtype, shape, dev)
+    _need("g", g, dtype, (d,), dev)
+    _need("mean", mean, torch.float32, (T,), dev)
+    _need("rstd", rstd, torch.float32, (T,), dev)
     if dres is not None:
-        _need("dres", dres, dtype, shape)
-    dX = torch.empty_like(x) if dX is None else _out("dX", dX, dtype, shape, dev)
-    dg = _out("dg", dg, torch.float32, (d,), dev)
-    db = _out("db", db, torch.float32, (d,), dev)
+        _need("dres", dres, dtype, shape, dev)
+    dX = torch.empty_like(x) if dX is None else _out("dX", dX, dtype, shape, dev, device)
+    dg = _out("dg", dg, torch.float32, (d,), dev, device)
+    db = _out("db", db, torch.float32, (d,), dev, device)
     nb = lib.layernorm_bwd_workspace_size(T, d)
-    w = _scratch(nb, dev, ws)
+    w = _scratch(nb, dev, device, ws)
     _check("layernorm_bwd", lib.layernorm_bwd(dY.data_ptr(), x.data_ptr(), BF16 if dtype is torch.bfloat16 else F32,
                                               g.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
                                               None if dres is None else dres.data_ptr(), T, d, dX.data_ptr(),
-                                              dg.data_ptr(), db.data_ptr(), w.data_ptr(), nb, _raw_stream(stream)))
+                                              dg.data_ptr(), db.data_ptr(), w.data_ptr(), nb, _raw_stream(stream, dev)))
     return dX, dg, db
 
 
@@ -576,27 +577,27 @@ _HEAD = (torch.bfloat16,)
 
 
 def _ce_sizes(x, W, targets):
-    T, d = _matrix("x", x, _HEAD)
-    V, dw = _matrix("W", W, _HEAD)
+    (T, d), dev = _matrix("x", x, _HEAD)
+    (V, dw), _ = _matrix("W", W, _HEAD)
     if dw != d:
         raise ValueError(f"W has {dw} columns, x has {d}")
-    _need("targets", targets, torch.int64, (T,))
-    return T, d, V
+    _need("targets", targets, torch.int64, (T,), dev)
+    return T, d, V, dev
 
 
 def linear_cross_entropy_fwd(x: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
                              loss=None, lse=None, ws=None, stream=None):
     """Softmax cross entropy of the head z = x W^T, logits never kept: x [T,d] bf16, W [V,d] bf16,
     targets [T] int64.  Returns (loss [T] fp32, 0 for ignored tokens; lse [T] fp32)."""
-    T, d, V = _ce_sizes(x, W, targets)
-    dev = x.device
-    loss = _out("loss", loss, torch.float32, (T,), dev)
-    lse = _out("lse", lse, torch.float32, (T,), dev)
+    T, d, V, dev = _ce_sizes(x, W, targets)
+    device = x.device
+    loss = _out("loss", loss, torch.float32, (T,), dev, device)
+    lse = _out("lse", lse, torch.float32, (T,), dev, device)
     nb = lib.linear_cross_entropy_fwd_workspace_size(T, d, V)
-    w = _scratch(nb, dev, ws)
+    w = _scratch(nb, dev, device, ws)
     _check("linear_cross_entropy_fwd",
            lib.linear_cross_entropy_fwd(x.data_ptr(), W.data_ptr(), targets.data_ptr(), T, d, V, ignore_index,
-                                        loss.data_ptr(), lse.data_ptr(), w.data_ptr(), nb, _raw_stream(stream)))
+                                        loss.data_ptr(), lse.data_ptr(), w.data_ptr(), nb, _raw_stream(stream, dev)))
     return loss, lse
 
 
@@ -606,24 +607,24 @@ def linear_cross_entropy_bwd(x: torch.Tensor, W: torch.Tensor, targets: torch.Te
     """Gradients of linear_cross_entropy_fwd for dloss [T] fp32, the gradient at each token's loss (a
     mean: 1 / the number of tokens that count).  Returns (dX [T,d] bf16, dW [V,d] of dw_dtype, fp32 or
     bf16; a given dW decides its own type)."""
-    T, d, V = _ce_sizes(x, W, targets)
-    dev = x.device
-    _need("lse", lse, torch.float32, (T,))
-    _need("dloss", dloss, torch.float32, (T,))
-    dX = torch.empty_like(x) if dX is None else _out("dX", dX, torch.bfloat16, (T, d), dev)
+    T, d, V, dev = _ce_sizes(x, W, targets)
+    device = x.device
+    _need("lse", lse, torch.float32, (T,), dev)
+    _need("dloss", dloss, torch.float32, (T,), dev)
+    dX = torch.empty_like(x) if dX is None else _out("dX", dX, torch.bfloat16, (T, d), dev, device)
     if dW is None:
         if dw_dtype not in _REAL:
             raise TypeError(f"dw_dtype {dw_dtype}: bfloat16 or float32")
-        dW = torch.empty((V, d), dtype=dw_dtype, device=dev)
+        dW = torch.empty((V, d), dtype=dw_dtype, device=device)
     else:
-        _need("dW", dW, torch.bfloat16 if dW.dtype is torch.bfloat16 else torch.float32, (V, d))
+        _need("dW", dW, torch.bfloat16 if dW.dtype is torch.bfloat16 else torch.float32, (V, d), dev)
     nb = lib.linear_cross_entropy_bwd_workspace_size(T, d, V)
-    w = _scratch(nb, dev, ws)
+    w = _scratch(nb, dev, device, ws)
     _check("linear_cross_entropy_bwd",
            lib.linear_cross_entropy_bwd(x.data_ptr(), W.data_ptr(), targets.data_ptr(), lse.data_ptr(),
                                         dloss.data_ptr(), T, d, V, ignore_index, dX.data_ptr(), dW.data_ptr(),
                                         BF16 if dW.dtype is torch.bfloat16 else F32, w.data_ptr(), nb,
-                                        _raw_stream(stream)))
+                                        _raw_stream(stream, dev)))
     return dX, dW
 
 

@@ -1485,8 +1485,8 @@ int rope_run(const void* qkv, fp8q_dtype dtype, int64_t T, int n_heads, int n_kv
   for (int i = 0; i < r->rot_dim / 2; ++i) {
     const double f = r->inv_freq[i] / 6.283185307179586476925;
     if (!std::isfinite(f) || r->axis[i] >= r->n_axes) return FP8Q_ERR_INVALID_ARG;
-    // the fraction of a turn per position in 0.64 fixed point (frac < 1 - 2^-54, so it fits)
-    p.turn[i] = (uint64_t)std::ldexp(f - std::floor(f), 64);
+    // the fraction of a turn per position in 0.64 fixed point (at most 1 - 2^-53, so it fits)
+    p.turn[i] = (uint64_t)((f - std::floor(f)) * 18446744073709551616.0);
     p.axis[i] = r->axis[i];
   }
   Ctx c;

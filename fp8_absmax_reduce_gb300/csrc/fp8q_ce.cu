@@ -328,15 +328,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tma_prefetch_desc(&tmB);
     if (MODE != kPairLse && MODE != kTokLse && MODE != kTokDx) tma_prefetch_desc(&tmC);
   }
-  // kTokGrad: the tokens' rows (kTokLse: their targets) where every lane can read them
-  float4* tok = reinterpret_cast<float4*>(smem + PL::kTokOffset);
-  if (MODE == kTokGrad && threadIdx.x < NT)
-    tok[threadIdx.x] = (int)threadIdx.x < p.N ? p.rows[threadIdx.x] : make_float4(0.0f, 0.0f, __int_as_float(-1), 0.0f);
   if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  wait_for_previous();
+  start_dependents();
+  // kTokGrad: the tokens' rows (kTokLse: their targets) where every lane can read them
+  float4* tok = reinterpret_cast<float4*>(smem + PL::kTokOffset);
+  if (MODE == kTokGrad && threadIdx.x < NT)
+    tok[threadIdx.x] = (int)threadIdx.x < p.N ? p.rows[threadIdx.x] : make_float4(0.0f, 0.0f, __int_as_float(-1), 0.0f);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // both CTAs' barriers exist, both have their tensor memory
@@ -689,6 +691,8 @@ __global__ void __launch_bounds__(1024) k_ce_finish(const float2* __restrict__ p
   const int64_t t = (int64_t)blockIdx.x * 32 + lane;
   const float2 none = make_float2(-INFINITY, 0.0f);
   float2 r = none;
+  wait_for_previous();
+  start_dependents();
   if (t < T)
     for (int i = warp; i < pieces; i += 128) {
       float2 q[4];
@@ -735,6 +739,7 @@ __device__ __forceinline__ float ce_block_scale(const float* __restrict__ dloss,
 __global__ void __launch_bounds__(1024) k_ce_scale(const float* __restrict__ dloss, const int64_t* __restrict__ targets,
                                                    int64_t T, int64_t V, int64_t ignore, float* scale, unsigned* status) {
   __shared__ uint32_t red[32];
+  start_dependents();
   const float s = ce_block_scale(dloss, targets, T, V, ignore, status, red);
   if (threadIdx.x == 0) *scale = s;
 }
@@ -748,6 +753,8 @@ __global__ void __launch_bounds__(256) k_ce_rows(const uint16_t* __restrict__ x,
                                                  int d, int64_t V, int64_t ignore, float* scale,
                                                  float4* __restrict__ rows, uint16_t* __restrict__ xz, unsigned* status) {
   __shared__ uint32_t red[32];
+  if (!OWN) wait_for_previous();
+  start_dependents();
   float s;
   if (OWN) {
     s = ce_block_scale(dloss, targets, T, V, ignore, status, red);
@@ -769,6 +776,8 @@ __global__ void __launch_bounds__(256) k_ce_rows(const uint16_t* __restrict__ x,
 // out = s (sum of the parts of K), part i at rows i `rows_pad` of part; N a multiple of 8.
 __global__ void __launch_bounds__(256) k_ce_join(const float* __restrict__ part, int splits, int64_t rows_pad, int64_t M,
                                                  int N, const float* __restrict__ scale, void* out, int f32) {
+  wait_for_previous();
+  start_dependents();
   const int64_t n4 = M * N / 4, stride = rows_pad * N / 4;
   const float alpha = *scale;
   const float4* p = reinterpret_cast<const float4*>(part);
@@ -912,8 +921,15 @@ cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Laun
     configured.fetch_or(1ull << dev);
   }
   const int pairs = pair_grid(L, a.num_tiles);
-  k_ce_gemm<A_MN, B_MN, MODE, NT><<<2 * pairs, kPairThreads, PairPlan<MODE, NT>::kSmem, L.stream>>>(ta, tb, tc, a);
-  return launched(L);
+  if constexpr (MODE == kPairLse || MODE == kTokLse) {  // comes first in its call
+    k_ce_gemm<A_MN, B_MN, MODE, NT><<<2 * pairs, kPairThreads, PairPlan<MODE, NT>::kSmem, L.stream>>>(ta, tb, tc, a);
+    e = cudaGetLastError();
+  } else {
+    e = launch_dependent(k_ce_gemm<A_MN, B_MN, MODE, NT>, 2 * pairs, kPairThreads, PairPlan<MODE, NT>::kSmem, L.stream,
+                         ta, tb, tc, a);
+  }
+  if (L.launches) ++*L.launches;
+  return e;
 }
 
 // Columns of a backward piece: G of all tokens in about 256 MB, in whole tiles, the pieces alike.
@@ -997,9 +1013,10 @@ cudaError_t launch_ce_fwd(const uint16_t* x, const uint16_t* W, const int64_t* t
     pieces = (int)((V + 127) / 128);
   }
   if (e != cudaSuccess) return e;
-  k_ce_finish<<<(unsigned)((T + 31) / 32), 1024, 0, L.stream>>>(w.part, pieces, T, targets, V, ignore, w.zy, loss, lse,
-                                                               L.status);
-  return launched(L);
+  e = launch_dependent(k_ce_finish, (unsigned)((T + 31) / 32), 1024, 0, L.stream, w.part, pieces, T, targets, V, ignore,
+                       w.zy, loss, lse, L.status);
+  if (L.launches) ++*L.launches;
+  return e;
 }
 
 cudaError_t launch_ce_bwd(const uint16_t* x, const uint16_t* W, const int64_t* targets, const float* lse,
@@ -1017,7 +1034,8 @@ cudaError_t launch_ce_bwd(const uint16_t* x, const uint16_t* W, const int64_t* t
   } else {
     k_ce_scale<<<1, 1024, 0, L.stream>>>(dloss, targets, T, V, ignore, w.scale, L.status);
     if ((e = launched(L)) != cudaSuccess) return e;
-    k_ce_rows<0><<<row_blocks, 256, 0, L.stream>>>(x, targets, lse, dloss, T, d, V, ignore, w.scale, w.rows, w.xz, L.status);
+    e = launch_dependent(k_ce_rows<0>, row_blocks, 256, 0, L.stream, x, targets, lse, dloss, T, d, V, ignore, w.scale, w.rows, w.xz, L.status);
+    if (e != cudaSuccess) return e;
   }
   if ((e = launched(L)) != cudaSuccess) return e;
   for (int64_t v0 = 0; v0 < V; v0 += piece) {
@@ -1050,8 +1068,9 @@ cudaError_t launch_ce_bwd(const uint16_t* x, const uint16_t* W, const int64_t* t
     }
     if (last && (xs > 1 || T <= kTokMax)) {
       const int64_t pad = T <= kTokMax ? T : (T + PM - 1) / PM * PM;
-      k_ce_join<<<join_blocks, 256, 0, L.stream>>>(w.acc, xs, pad, T, d, w.scale, dX, 0);
-      if ((e = launched(L)) != cudaSuccess) return e;
+      e = launch_dependent(k_ce_join, join_blocks, 256, 0, L.stream, w.acc, xs, pad, T, d, w.scale, dX, 0);
+      if (e == cudaSuccess) e = launched(L);
+      if (e != cudaSuccess) return e;
     }
     // dW[piece] = s G^T x
     PairArgs aw{};
@@ -1062,8 +1081,9 @@ cudaError_t launch_ce_bwd(const uint16_t* x, const uint16_t* W, const int64_t* t
     e = launch_pair<1, 1, kPairDw>(PairProblem{n, d, T, w.G, piece, w.xz, d, wsp > 1 ? (void*)w.dw_part : dst, d}, wsp, aw, L);
     if (e != cudaSuccess) return e;
     if (wsp > 1) {
-      k_ce_join<<<join_blocks, 256, 0, L.stream>>>(w.dw_part, wsp, (n + PM - 1) / PM * PM, n, d, w.scale, dst, dw_f32);
-      if ((e = launched(L)) != cudaSuccess) return e;
+      e = launch_dependent(k_ce_join, join_blocks, 256, 0, L.stream, w.dw_part, wsp, (n + PM - 1) / PM * PM, n, d, w.scale, dst, dw_f32);
+      if (e == cudaSuccess) e = launched(L);
+      if (e != cudaSuccess) return e;
     }
   }
   return cudaSuccess;

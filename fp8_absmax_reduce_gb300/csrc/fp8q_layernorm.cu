@@ -10,6 +10,8 @@
 #include "fp8q_common.cuh"
 #include "fp8q_internal.h"
 
+#include <atomic>
+
 namespace fp8q {
 
 namespace {
@@ -341,6 +343,7 @@ __global__ void __launch_bounds__(STRIDE > 0 && STRIDE < kLnThreads ? STRIDE : k
   __shared__ uint64_t full[kLnSlotsMax];
   __shared__ float red[2][2][16];
   __shared__ volatile int give_up;
+  start_dependents();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, nwarps = blockDim.x >> 5;
   const int pieces = d / VEC;
   const int stride = STRIDE ? STRIDE : (int)blockDim.x;  // a constant lets single columns use immediate offsets
@@ -464,6 +467,7 @@ __global__ void __launch_bounds__(STRIDE > 0 && STRIDE < kLnThreads ? STRIDE : k
 __global__ void __launch_bounds__(1024) k_layernorm_bwd_finish(const float* __restrict__ part, int nblk, int d,
                                                                float* __restrict__ dg, float* __restrict__ db) {
   __shared__ float sum[32][33];
+  wait_for_previous();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int j = blockIdx.x * 32 + tx;
   float s = 0.0f;
@@ -493,6 +497,17 @@ cudaError_t launched(const Launch& L) {
   return cudaGetLastError();
 }
 
+// The kernel's shared memory limit, raised once per device.
+template <class Kernel>
+cudaError_t ring_limit(Kernel* k, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (done.load(std::memory_order_relaxed) >> (dev & 63) & 1)) return e;
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLnSmemBudget);
+  if (e == cudaSuccess) done.fetch_or(1ull << (dev & 63));
+  return e;
+}
+
 // Slots of a ring, at least one, within a block's share of the shared memory; fewer blocks per SM where that leaves
 // each fewer than three.
 int ring_slots(size_t slot, int* per_sm) {
@@ -509,7 +524,8 @@ cudaError_t fwd_go(const void* x, const void* g, const void* b, int64_t T, int d
   const size_t slot = ln_region((uint32_t)(rows * d * (F32 ? 4 : 2)));
   int per_sm = ln_fwd_per_sm(VEC, W);
   const int S = ring_slots(slot, &per_sm);
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLnSmemBudget);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = ring_limit(k, done);
   if (e != cudaSuccess) return e;
   const int64_t need = (T + rows - 1) / rows, wave = (int64_t)L.num_sms * per_sm;
   k<<<(unsigned)(need < wave ? need : wave), ln_fwd_threads(W), S * slot, L.stream>>>(x, g, b, T, d, eps, S, y, mean,
@@ -590,7 +606,8 @@ cudaError_t bwd_go(const void* dY, const void* x, const void* g, const float* me
   const size_t slot = (size_t)ln_region((uint32_t)(d * (F32 ? 4 : 2))) * (dres ? 3 : 2);
   int per_sm = bwd_per_sm(d);
   const int S = ring_slots(slot, &per_sm);
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLnSmemBudget);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = ring_limit(k, done);
   if (e != cudaSuccess) return e;
   // one wave of resident blocks, each with a run of consecutive rows (at most layernorm_bwd_blocks of them)
   const int64_t most = (int64_t)(L.num_sms < kLnPlanSms ? L.num_sms : kLnPlanSms) * per_sm;
@@ -640,8 +657,9 @@ cudaError_t launch_layernorm_bwd(const void* dY, const void* x, int f32, const v
   cudaError_t e = f32 ? bwd_t<1>(dY, x, g, mean, rstd, dres, T, d, dX, part, &nblk, L)
                       : bwd_t<0>(dY, x, g, mean, rstd, dres, T, d, dX, part, &nblk, L);
   if (e != cudaSuccess) return e;
-  k_layernorm_bwd_finish<<<(2 * d + 31) / 32, 1024, 0, L.stream>>>(part, nblk, d, dg, db);
-  return launched(L);
+  e = launch_dependent(k_layernorm_bwd_finish, (unsigned)((2 * d + 31) / 32), 1024, 0, L.stream, part, nblk, d, dg, db);
+  if (L.launches) ++*L.launches;
+  return e;
 }
 
 }  // namespace fp8q
