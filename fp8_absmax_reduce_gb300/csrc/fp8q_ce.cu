@@ -92,11 +92,24 @@ struct PairPlan {
 };
 constexpr uint64_t kCopyDrainNs = 5000000ull;  // far beyond any copy in flight
 
+// Division of n < 2^31 by a number known at the launch: n m >> s with m = ceil(2^s / d), s = 31 + ceil(log2 d).
+// (Roles walk short tiles in less time than a chain of integer divisions takes.)
+struct Divisor {
+  uint32_t d, m, s;
+};
+Divisor divisor(int d) {
+  uint32_t l = 0;
+  while ((1ull << l) < (uint64_t)d) ++l;
+  return Divisor{(uint32_t)d, (uint32_t)(((1ull << (31 + l)) + (uint32_t)d - 1) / (uint32_t)d), 31 + l};
+}
+__device__ __forceinline__ int divide(int n, const Divisor& d) { return (int)(((uint64_t)(uint32_t)n * d.m) >> d.s); }
+
 struct PairArgs {
   int M, N, K;
   int m_tiles, n_tiles, k_blocks, group;
   int splits, split_blocks;  // parts of K, and the blocks of 64 in each (the last may have fewer)
   int num_tiles;             // m_tiles n_tiles splits
+  Divisor by_part, by_span, by_group, by_last;  // tiles of a part, of a group; M tiles of a group, of the last group
   uint32_t idesc;
   int out;                  // PairOut; with splits > 1 fp32, split i at rows i 256 m_tiles of C
   const float* scale;       // s, or null: the sum as it is
@@ -286,14 +299,14 @@ __device__ __forceinline__ float2 ce_pair(const float (&z)[N]) {
 // Tile -> (part of K, M tile, N tile): a part's tiles in groups of p.group M tiles, all N tiles of a group,
 // M fastest inside it.  Its blocks of K are [k0, k1).
 __device__ __forceinline__ int pair_coords(int tile, const PairArgs& p, int& mb, int& nb, int& k0, int& k1) {
-  const int each = p.m_tiles * p.n_tiles, part = tile / each;
-  tile -= part * each;
+  const int part = divide(tile, p.by_part);
+  tile -= part * (int)p.by_part.d;
   k0 = part * p.split_blocks;
   k1 = min(k0 + p.split_blocks, p.k_blocks);
-  const int span = p.group * p.n_tiles, grp = tile / span, first = grp * p.group;
-  const int gm = min(p.group, p.m_tiles - first), local = tile - grp * span;
-  mb = first + local % gm;
-  nb = local / gm;
+  const int grp = divide(tile, p.by_span), first = grp * p.group, local = tile - grp * (int)p.by_span.d;
+  const bool full = first + p.group <= p.m_tiles;  // the last group may have fewer rows
+  nb = divide(local, full ? p.by_group : p.by_last);
+  mb = first + local - nb * (int)(full ? p.by_group.d : p.by_last.d);
   return part;
 }
 
@@ -892,6 +905,11 @@ cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Laun
   a.splits = (a.k_blocks + a.split_blocks - 1) / a.split_blocks;
   a.num_tiles = a.m_tiles * a.n_tiles * a.splits;
   a.group = kTok ? a.m_tiles : pair_group(q, a.m_tiles);
+  if (a.group > a.m_tiles) a.group = a.m_tiles;
+  a.by_part = divisor(a.m_tiles * a.n_tiles);
+  a.by_span = divisor(a.group * a.n_tiles);
+  a.by_group = divisor(a.group);
+  a.by_last = divisor(a.m_tiles % a.group ? a.m_tiles % a.group : a.group);
   // fp32 sums, bf16 operands and their majors, N / 8 and M / 16 of the pair's tile
   a.idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
             ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(PM >> 4) << 24);
