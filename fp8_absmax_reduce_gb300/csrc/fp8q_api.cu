@@ -1510,14 +1510,15 @@ int rope_bwd(const void* d_out, fp8q_dtype dtype, int64_t T, int n_heads, int n_
 // The language model head's cross entropy
 // ---------------------------------------------------------------------------
 namespace {
+bool ce_sizes_ok(int64_t T, int64_t d, int64_t V) {
+  if (T < 1 || T > ((int64_t)1 << 24) || V < 1 || V > ((int64_t)1 << 24)) return false;
+  if (d < 8 || d > 65536 || d % 8) return false;
+  return ((T + 255) / 256) * ((V + 255) / 256) < ((int64_t)1 << 31);  // tiles of the logits
+}
 int validate_ce(const void* x, const void* W, const int64_t* targets, int64_t T, int64_t d, int64_t V) {
-  if (T < 1 || T > ((int64_t)1 << 24) || V < 1 || V > ((int64_t)1 << 24)) return FP8Q_ERR_INVALID_ARG;
-  if (d < 8 || d > 65536 || d % 8) return FP8Q_ERR_INVALID_ARG;
+  if (!ce_sizes_ok(T, d, V)) return FP8Q_ERR_INVALID_ARG;
   if (!al16(x) || !al16(W) || !al8(targets)) return FP8Q_ERR_INVALID_ARG;
   return FP8Q_OK;
-}
-bool ce_sizes_ok(int64_t T, int64_t d, int64_t V) {
-  return T >= 1 && T <= ((int64_t)1 << 24) && V >= 1 && V <= ((int64_t)1 << 24) && d >= 8 && d <= 65536 && d % 8 == 0;
 }
 }  // namespace
 

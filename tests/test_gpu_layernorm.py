@@ -120,6 +120,26 @@ def test_in_place_guard_bands_and_repeats(T, d, dtype):
     assert torch.equal(gy.t, y) and torch.equal(gx.t, dX) and torch.equal(gg.t, dg) and torch.equal(gb.t, db)
 
 
+@pytest.mark.parametrize("d", [8192, 8191])
+def test_offsets_past_32_bits(d):
+    """More than 2^31 elements: the last rows' results are those of the same rows alone."""
+    T = 2 ** 31 // d + 600
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    t = make(40, d, torch.bfloat16, seed=4)
+    x[-40:] = t["x"]
+    y, mean, rstd = fq.layernorm_fwd(x, t["g"], t["b"])
+    y2, m2, r2 = fq.layernorm_fwd(t["x"], t["g"], t["b"])
+    assert torch.equal(y[-40:], y2) and torch.equal(mean[-40:], m2) and torch.equal(rstd[-40:], r2)
+    assert torch.equal(y[5], t["b"])
+    y.zero_()
+    y[-40:] = t["dY"]
+    dX, dg, db = fq.layernorm_bwd(y, x, t["g"], mean, rstd)
+    w = fq.layernorm_bwd(t["dY"], t["x"], t["g"], m2, r2)
+    assert torch.equal(dX[-40:], w[0]) and bool((dX[:100] == 0).all())
+    for got, want in ((dg, w[1]), (db, w[2])):  # other blocks, so another order of the same 40 terms
+        assert float((got - want).abs().max()) <= 40 * 2.0 ** -23 * float(want.abs().max()) + 40 * 2.0 ** -23
+
+
 def test_refusals():
     t = make(8, 64, torch.bfloat16)
     m = torch.zeros(8, device="cuda")

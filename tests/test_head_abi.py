@@ -91,6 +91,7 @@ def test_cross_entropy_refuses(fq):
                 dict(d=0), dict(d=60), dict(d=65544), dict(lse=ODD)):
         assert fwd(**bad) == INVALID and bwd(**bad) == INVALID, bad
     assert fwd(loss=None) == INVALID
+    assert fwd(T=1 << 24, V=1 << 24) == INVALID and fq.linear_cross_entropy_fwd_workspace_size(1 << 24, 64, 1 << 24) == 0
     for bad in (dict(dl=ODD), dict(dX=ODD), dict(dW=None), dict(dt=2)):
         assert bwd(**bad) == INVALID, bad
     for f, n in ((fwd, nf), (bwd, nb)):
