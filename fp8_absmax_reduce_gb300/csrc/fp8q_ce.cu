@@ -12,6 +12,7 @@
 // s joins the products in fp32.  An ignored token's row of x is replaced by zero before dW = G^T x, so
 // that a padded row may hold anything (0 times a NaN would reach every row of dW).
 #include "fp8q_common.cuh"
+#include "fp8q_head.cuh"
 #include "fp8q_internal.h"
 
 #include <atomic>
@@ -49,10 +50,11 @@ __device__ __forceinline__ float ce_exp2(float x) {
 // registers (the accumulators change hands after each part; measured at T = 4096, d = 3584, V = 50257: the loss's error
 // 2.7e-6 -> 0.7e-6 of its norm, 868 -> 888 us).
 // Up to 128 tokens the operands trade places (kTok*): the 256 rows of a pair's tile are rows of W (of W^T for
-// dX) and its NT = 32, 64 or 128 columns the tokens, so that the tensor cores do not work on padding (256 rows
-// for 24 tokens: 10.6 us of MMAs a tile at d = 2048 against 12 us for its operands from HBM) and W streams
-// at HBM's rate.  The softmax statistics then run down the tile's lanes: each warp turns its 32 x 32 blocks
-// in shared memory and keeps a running pair for each token over all its tiles.
+// dX) and its NT = 32, 64 or 128 columns the tokens, so that W streams at HBM's rate and the tensor cores do not
+// work on padding.  The softmax statistics then run down the tile's lanes: each warp turns its 32 x 32 blocks
+// in shared memory and keeps a running pair for each token over all its tiles.  Measured against the
+// padded tiles (d = 2048, V = 32000): forward 42 against 54 us for one token, 42 / 46 for 24, 45 / 46 for 100;
+// backward 90 / 112, 89 / 94, 97 / 100.
 //
 // Every wait is bounded.  On expiry a CTA records the time-out and stops; its copies in flight, which
 // signal the other CTA, get kCopyDrainNs to land; the pair meets at a cluster barrier and frees its tensor memory.
@@ -347,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         pair_coords(tile, p, mb, nb, kb0, kb1);
         const int m0 = mb * PM + 128 * rank, n0 = nb * NT + NT / 2 * rank;
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
+          if (!mbar_wait_held(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
           uint8_t* sA = smem + stage * PL::kStage;
           uint8_t* sB = sA + kHalfTile;
           const uint32_t bar = map_to_rank(smem_addr(&full[stage]), 0);
@@ -386,11 +388,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         pair_coords(tile, p, mb, nb, kb0, kb1);
         for (int kb = kb0; kb < kb1 && ok;) {
           const int begin = kb, end = kSeg ? min(kb + kSegBlocks, kb1) : kb1;
-          if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag)) { ok = false; break; }
+          if (!mbar_wait_held(&tempty[acc], acc_phase ^ 1u, abort_flag)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d = tmem_base + (uint32_t)(acc * NT);
           for (; kb < end; ++kb) {
-            if (!mbar_wait(&full[stage], phase, abort_flag)) { ok = false; break; }
+            if (!mbar_wait_held(&full[stage], phase, abort_flag)) { ok = false; break; }
             tc_fence_after();
             const uint32_t sA = smem_addr(smem + stage * PL::kStage), sB = sA + kHalfTile;
 #pragma unroll
@@ -416,7 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       // every MMA issued is done before tensor memory is released
       pair_commit(drain, 1);
       int dummy = 0;
-      mbar_wait(drain, 0, &dummy);
+      mbar_wait_held(drain, 0, &dummy);
     }
   } else if (warp >= kEpiWarp) {
     // ---------------- epilogue ----------------
@@ -441,7 +443,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // lane 0 waits for the accumulator and the warp follows its result (what comes is warp-collective)
     auto take = [&]() -> bool {
       int ok = 0;
-      if (lane == 0) ok = mbar_wait(&tfull[acc], acc_phase, abort_flag) ? 1 : 0;
+      if (lane == 0) ok = mbar_wait_held(&tfull[acc], acc_phase, abort_flag) ? 1 : 0;
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       if (!ok) {
         atomicOr(p.status, kStatusTimeout);

@@ -24,29 +24,6 @@ struct Launch {
 // device (resolved once per device).  Returns 0 on success.
 int device_status_and_sms(unsigned** status, int* num_sms);
 
-// A launch whose blocks may become resident as soon as every block of the kernel before it on the stream has called
-// start_dependents() or exited; they call wait_for_previous(), which returns once that kernel is
-// complete and its writes are visible, before they touch global memory.  What it hides: the launch, and the
-// block's own preparation (barriers, tensor memory, descriptors), about 3 us between two short kernels.
-template <class... P, class... A>
-cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3(grid);
-  c.blockDim = dim3((unsigned)threads);
-  c.dynamicSmemBytes = smem;
-  c.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = &at;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
-}
-#ifdef __CUDACC__
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void start_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-#endif
-
 // Per-tensor absmax quantization: pass 1 writes *P partials, pass 2 casts.
 // absmax_partial_blocks: the number of partials pass 1 writes for n elements (its grid size;
 // never more than kMaxPartials).

@@ -8,6 +8,7 @@
 // E[x^2] - mean^2, which would cancel for rows whose mean is large.  Bound by memory: every tensor
 // is read or written once.
 #include "fp8q_common.cuh"
+#include "fp8q_head.cuh"
 #include "fp8q_internal.h"
 
 #include <atomic>
