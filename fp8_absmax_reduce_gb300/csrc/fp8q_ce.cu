@@ -639,6 +639,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (MODE == kTokLse) {
       // the four warps that share a warpgroup's tokens bring their pairs together (the abort path has partial
       // ones: its results are incomplete anyway)
+      __syncwarp();  // every lane has read its last block
 #pragma unroll
       for (int i = 0; i < kBlocks; ++i)
         asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(out.buf + 8 * (32 * i + lane)), "f"(tp[i].x), "f"(tp[i].y) : "memory");
@@ -835,13 +836,14 @@ struct PairProblem {
 };
 
 // The M tiles of a rasterisation group: every one of them while A fits in L2 beside the streamed B, one
-// (N fastest) while B does instead, else 2048 rows.
+// (N fastest) while B does instead, else 4096 rows (the forward at T = 8192, d = 3584, V = 32000, back to back: 1146 us with
+// 1024 rows, 1094 with 2048, 1068 with 4096, 1082 with 8192; the backward 3484, 3398, 3398, 3540).
 int pair_group(const PairProblem& q, int m_tiles) {
   constexpr int64_t kResident = 48ll << 20;
   const int64_t a = 2 * q.M * q.K, b = 2 * q.N * q.K;
   if (a <= b && a <= kResident) return m_tiles;
   if (b < a && b <= kResident) return 1;
-  return 2048 / PM;
+  return 4096 / PM;
 }
 
 constexpr int kPlanPairs = 76;
