@@ -9,7 +9,12 @@
 //
 // G is kept in bf16, the tensor cores' operand type, as G / s with s = max_t |dloss_t|: a mean's
 // one weight for all tokens then leaves no rounding of its own in G's large entries (p - 1 near -1).
-// s joins the products in fp32.  An ignored token's row of x is replaced by zero before dW = G^T x, so
+// s joins the products in fp32.  With few tokens (up to kTwoParts, where the products wait for memory) nothing
+// averages the rounding of a token's largest entry, so G is kept there as two bf16 parts, the value and what its rounding
+// lost, 2 Tp rows in all (Tp = T in whole blocks of 32): dX adds the two parts' products, dW runs over both with x twice
+// (T = 2, d = 4080, V = 1686: dW's error 3.5e-3 of its norm with one part, as the plain fp32 form's 2.2e-3 with two;
+// d = 2048, V = 32000: 89 -> 90 us for 24 tokens, 89 -> 95 for 60, but 97 -> 111 for 100).  An ignored
+// token's row of x is replaced by zero before dW = G^T x, so
 // that a padded row may hold anything (0 times a NaN would reach every row of dW).
 #include "fp8q_common.cuh"
 #include "fp8q_head.cuh"
@@ -64,6 +69,7 @@ constexpr int kHalfTile = 128 * 128;  // bytes: 128 rows (or columns) x 64 bf16
 constexpr int kEpiWarp = 3;           // the first of the 8 epilogue warps
 constexpr int kPairThreads = 32 * (kEpiWarp + 8);
 constexpr int kTokMax = 128;  // tokens up to which the operands trade places
+constexpr int kTwoParts = 64; // tokens up to which the backward keeps G in two parts
 constexpr int kSegBlocks = 16; // K of a partial sum of the logits, in blocks of 64
 
 enum PairMode {
@@ -72,8 +78,8 @@ enum PairMode {
   kPairDx = 2,    // dX: fp32 store, fp32 add or bf16 of the joined sum
   kPairDw = 3,    // dW: bf16 or fp32
   kTokLse = 4,    // the same three with the tokens as columns: statistics of a CTA's rows of W
-  kTokGrad = 5,   //   G / s, stored by token
-  kTokDx = 6,     //   dX's sum in fp32, by token, the parts of K apart
+  kTokGrad = 5,   //   G / s in two parts, stored by token
+  kTokDx = 6,     //   dX's sum in fp32, by token, the parts of K and of G apart
 };
 enum PairOut { kOutF32Store = 0, kOutF32Add = 1, kOutBf16 = 2, kOutBf16Join = 3 };
 
@@ -87,7 +93,7 @@ struct PairPlan {
   static constexpr int kStaging = MODE == kPairDw ? 8192 : 4096;  // per epilogue warp
   static constexpr int kStagingOffset = kStages * kStage;
   static constexpr int kTokOffset = kStagingOffset + 8 * kStaging;
-  static constexpr int kBarOffset = kTokOffset + (NT < 256 ? NT * 16 : 0);
+  static constexpr int kBarOffset = kTokOffset + (MODE == kTokGrad ? NT * 16 : 0);
   static constexpr int kSmem = kBarOffset + 256 + 1024;
   static_assert(kSmem <= 232448, "shared memory per CTA");
   static_assert(kStage % 1024 == 0, "swizzle atoms");
@@ -116,7 +122,8 @@ struct PairArgs {
   int out;                  // PairOut; with splits > 1 fp32, split i at rows i 256 m_tiles of C
   const float* scale;       // s, or null: the sum as it is
   float* acc;               // kOutBf16Join: the sum so far [M, N]
-  int v0;                   // kPairGrad: the piece's first column
+  int v0;                   // kPairGrad, kTokGrad: the piece's first column
+  int rows_lo;              // kTokGrad: the first row of G's second part, or 0: it has one
   const int64_t* targets;   // kPairLse, kTokLse
   int V;                    // kPairLse, kTokLse
   float2* part;             // (maximum log2e, sum) pairs: kPairLse [2 n_tiles][M], kTokLse [CTAs][N]
@@ -296,8 +303,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               const __grid_constant__ CUtensorMap tmC, const PairArgs p) {
   using PL = PairPlan<MODE, NT>;
   constexpr bool kSeg = MODE == kPairLse || MODE == kTokLse;  // the sum over K comes in parts
-  constexpr bool kTok = NT < 256;
-  static_assert(kTok == (MODE >= kTokLse) && !(kTok && B_MN), "the tokens are a K-major operand");
+  constexpr bool kTok = MODE >= kTokLse;
+  static_assert(!(kTok && B_MN), "the tokens are a K-major operand");
   extern __shared__ uint8_t pair_smem[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pair_smem) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + PL::kBarOffset);
@@ -549,7 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (MODE == kPairGrad && row_ok) rw = p.rows[row];
         if (!take()) break;
         if constexpr (kTok) {
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < kBlocks; ++i) {
             const int c = half + 2 * i;
             if (32 * c >= NT || 32 * c >= p.N || !warp_ok) continue;
@@ -557,18 +564,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             uint32_t a[32];
             tmem_ld32(lanes + (uint32_t)(acc * NT + 32 * c), a);  // lane: row of W (column of dX), register: token
             if (MODE == kTokGrad) {
-              // G by token: 32 tokens x 32 rows of W, 64 bytes a token
-              const uint32_t b = out.template acquire<2048>();
+              // G by token: 32 tokens x 32 rows of W, 64 bytes a token, and as much for what the rounding lost
+              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+              __syncwarp();
+              const uint32_t hi = out.buf, lo = out.buf + 2048;
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
                 const float4 r = tok[32 * c + j];
                 const int ry = __float_as_int(r.z);
                 float q = ce_exp2(fmaf(__uint_as_float(a[j]), kLog2e, -r.x));
                 if (ry == p.v0 + row) q -= 1.0f;
-                const __nv_bfloat16 g = __float2bfloat16_rn(ry >= 0 ? r.y * q : 0.0f);
-                asm volatile("st.shared.u16 [%0], %1;" ::"r"(b + 64 * j + 2 * lane), "h"(__bfloat16_as_ushort(g)) : "memory");
+                q = ry >= 0 ? r.y * q : 0.0f;
+                const __nv_bfloat16 g = __float2bfloat16_rn(q), e = __float2bfloat16_rn(q - __bfloat162float(g));
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(hi + 64 * j + 2 * lane), "h"(__bfloat16_as_ushort(g)) : "memory");
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(lo + 64 * j + 2 * lane), "h"(__bfloat16_as_ushort(e)) : "memory");
               }
-              out.publish(&tmC, b, row0, 32 * c);
+              out.publish(&tmC, hi, row0, 32 * c);
+              if (p.rows_lo) out.publish(&tmC, lo, row0, p.rows_lo + 32 * c);
             } else if (row_ok) {
               float* dst = p.acc + ((int64_t)part * p.N + 32 * c) * p.M + row;
 #pragma unroll
@@ -745,7 +757,8 @@ template <int OWN>
 __global__ void __launch_bounds__(256) k_ce_rows(const uint16_t* __restrict__ x, const int64_t* __restrict__ targets,
                                                  const float* __restrict__ lse, const float* __restrict__ dloss, int64_t T,
                                                  int d, int64_t V, int64_t ignore, float* scale,
-                                                 float4* __restrict__ rows, uint16_t* __restrict__ xz, unsigned* status) {
+                                                 float4* __restrict__ rows, uint16_t* __restrict__ xz, int64_t pad, int copies,
+                                                 unsigned* status) {
   __shared__ uint32_t red[32];
   if (!OWN) wait_for_previous();
   start_dependents();
@@ -756,14 +769,16 @@ __global__ void __launch_bounds__(256) k_ce_rows(const uint16_t* __restrict__ x,
   } else {
     s = *scale;
   }
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    const int64_t y = targets[t];
+  // rows T .. pad - 1 are zero; `copies` copies of the pad rows
+  for (int64_t t = blockIdx.x; t < pad; t += gridDim.x) {
+    const int64_t y = t < T ? targets[t] : ignore;
     const bool keep = y != ignore && y >= 0 && y < V;
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0 && t < T)
       rows[t] = make_float4(lse[t] * kLog2e, keep ? dloss[t] / s : 0.0f, __int_as_float(keep ? (int)y : -1), 0.0f);
-    const uint16_t* src = x + t * d;
-    uint16_t* dst = xz + t * d;
-    for (int j = 8 * threadIdx.x; j < d; j += 8 * blockDim.x) st_v4(dst + j, keep ? ld_v4(src + j) : make_uint4(0, 0, 0, 0));
+    for (int j = 8 * threadIdx.x; j < d; j += 8 * blockDim.x) {
+      const uint4 v = keep ? ld_v4(x + t * d + j) : make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < copies; ++c) st_v4(xz + (c * pad + t) * d + j, v);
+    }
   }
 }
 
@@ -874,7 +889,7 @@ int pair_splits(int64_t M, int64_t N, int64_t K) {
 
 template <int A_MN, int B_MN, int MODE, int NT = 256>
 cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Launch& L) {
-  constexpr bool kTok = NT < 256;
+  constexpr bool kTok = MODE >= kTokLse;
   a.M = (int)q.M;
   a.N = (int)q.N;
   a.K = (int)q.K;
@@ -902,8 +917,8 @@ cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Laun
   ok = ok && (B_MN ? make_map(&tb, q.B, q.N, q.K, q.ldb, 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)
                    : make_map(&tb, q.B, q.K, q.N, q.ldb, 2, 64, NT / 2, CU_TENSOR_MAP_SWIZZLE_128B));
   tc = ta;
-  if (MODE == kTokGrad) {  // by token: [N, M]
-    ok = ok && make_map(&tc, q.C, q.M, q.N, q.ldc, 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE);
+  if (MODE == kTokGrad) {  // by token: [2 Tp, M] or [N, M]
+    ok = ok && make_map(&tc, q.C, q.M, a.rows_lo ? 2 * a.rows_lo : q.N, q.ldc, 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE);
   } else if (!kTok && MODE != kPairLse) {
     const bool f32 = MODE != kPairGrad && (a.out == kOutF32Store || a.out == kOutF32Add);
     const bool wide = MODE == kPairDw && !f32;  // rows of 128 bytes, as fp32's
@@ -946,12 +961,14 @@ struct CePlan {
   int64_t piece;
   int dx_splits, dw_splits;
 };
+// Rows of G: its two parts of whole blocks of 32 tokens, or T.
+int64_t ce_g_rows(int64_t T) { return T <= kTwoParts ? 2 * ((T + 31) / 32 * 32) : T; }
 CePlan ce_plan(int64_t T, int64_t d, int64_t V) {
   CePlan p{};
   p.piece = ce_piece(T, V);
   const int64_t n = p.piece < V ? p.piece : V;
-  p.dx_splits = T <= kTokMax ? pair_splits(d, T, n) : pair_splits(T, d, n);
-  p.dw_splits = pair_splits(n, d, T);
+  p.dx_splits = T <= kTokMax ? pair_splits(d, ce_g_rows(T), n) : pair_splits(T, d, n);
+  p.dw_splits = pair_splits(n, d, ce_g_rows(T));
   return p;
 }
 
@@ -971,10 +988,11 @@ size_t ce_layout(int64_t T, int64_t d, int64_t V, bool bwd, uint8_t* base, CeWs*
   CeWs t{};
   if (bwd) {
     const CePlan p = ce_plan(T, d, V);
-    t.G = (uint16_t*)take(T * p.piece * 2);
-    t.xz = (uint16_t*)take(T * d * 2);
+    const int64_t g_rows = ce_g_rows(T);
+    t.G = (uint16_t*)take(g_rows * p.piece * 2);
+    t.xz = (uint16_t*)take(g_rows * d * 2);
     const int64_t m_pad = (T + PM - 1) / PM * PM;
-    if (T <= kTokMax) t.acc = (float*)take(p.dx_splits * T * d * 4);
+    if (T <= kTokMax) t.acc = (float*)take(p.dx_splits * g_rows * d * 4);
     else if (p.dx_splits > 1) t.acc = (float*)take(p.dx_splits * m_pad * d * 4);
     else if (p.piece < V) t.acc = (float*)take(T * d * 4);
     if (p.dw_splits > 1) t.dw_part = (float*)take(p.dw_splits * p.piece * d * 4);
@@ -1028,13 +1046,18 @@ cudaError_t launch_ce_bwd(const uint16_t* x, const uint16_t* W, const int64_t* t
   const int64_t piece = plan.piece;
   const int join_blocks = 4 * L.num_sms;
   cudaError_t e;
-  const unsigned row_blocks = (unsigned)(T < 8 * L.num_sms ? T : 8 * L.num_sms);
+  const int64_t g_rows = ce_g_rows(T);
+  const int copies = T <= kTwoParts ? 2 : 1;
+  const int64_t pad = g_rows / copies;
+  const unsigned row_blocks = (unsigned)(pad < 8 * L.num_sms ? pad : 8 * L.num_sms);
   if (T <= kCeOwnScale) {
-    k_ce_rows<1><<<row_blocks, 256, 0, L.stream>>>(x, targets, lse, dloss, T, d, V, ignore, w.scale, w.rows, w.xz, L.status);
+    k_ce_rows<1><<<row_blocks, 256, 0, L.stream>>>(x, targets, lse, dloss, T, d, V, ignore, w.scale, w.rows, w.xz, pad, copies,
+                                                   L.status);
   } else {
     k_ce_scale<<<1, 1024, 0, L.stream>>>(dloss, targets, T, V, ignore, w.scale, L.status);
     if ((e = launched(L)) != cudaSuccess) return e;
-    e = launch_dependent(k_ce_rows<0>, row_blocks, 256, 0, L.stream, x, targets, lse, dloss, T, d, V, ignore, w.scale, w.rows, w.xz, L.status);
+    e = launch_dependent(k_ce_rows<0>, row_blocks, 256, 0, L.stream, x, targets, lse, dloss, T, d, V, ignore, w.scale, w.rows,
+                         w.xz, pad, copies, L.status);
     if (e != cudaSuccess) return e;
   }
   if ((e = launched(L)) != cudaSuccess) return e;
@@ -1048,13 +1071,13 @@ cudaError_t launch_ce_bwd(const uint16_t* x, const uint16_t* W, const int64_t* t
     const int xs = plan.dx_splits;
     if (T <= kTokMax) {
       const PairProblem q{n, T, d, W + v0 * d, d, x, d, w.G, piece};
-      const PairProblem qx{d, T, n, W + v0 * d, d, w.G, piece, nullptr, 0};
+      const PairProblem qx{d, g_rows, n, W + v0 * d, d, w.G, piece, nullptr, 0};
+      a.rows_lo = copies == 2 ? (int)pad : 0;
       ax.out = first ? kOutF32Store : kOutF32Add;
       e = T <= 32 ? launch_pair<0, 0, kTokGrad, 32>(q, 1, a, L)
           : T <= 64 ? launch_pair<0, 0, kTokGrad, 64>(q, 1, a, L) : launch_pair<0, 0, kTokGrad, 128>(q, 1, a, L);
       if (e != cudaSuccess) return e;
-      e = T <= 32 ? launch_pair<1, 0, kTokDx, 32>(qx, xs, ax, L)
-          : T <= 64 ? launch_pair<1, 0, kTokDx, 64>(qx, xs, ax, L) : launch_pair<1, 0, kTokDx, 128>(qx, xs, ax, L);
+      e = T <= 32 ? launch_pair<1, 0, kTokDx, 64>(qx, xs, ax, L) : launch_pair<1, 0, kTokDx, 128>(qx, xs, ax, L);
       if (e != cudaSuccess) return e;
     } else {
       e = launch_pair<0, 0, kPairGrad>(PairProblem{T, n, d, x, d, W + v0 * d, d, w.G, piece}, 1, a, L);
@@ -1067,8 +1090,9 @@ cudaError_t launch_ce_bwd(const uint16_t* x, const uint16_t* W, const int64_t* t
       if (e != cudaSuccess) return e;
     }
     if (last && (xs > 1 || T <= kTokMax)) {
-      const int64_t pad = T <= kTokMax ? T : (T + PM - 1) / PM * PM;
-      e = launch_dependent(k_ce_join, join_blocks, 256, 0, L.stream, w.acc, xs, pad, T, d, w.scale, dX, 0);
+      const bool few = T <= kTokMax;
+      e = launch_dependent(k_ce_join, join_blocks, 256, 0, L.stream, w.acc, few ? copies * xs : xs,
+                           few ? pad : (T + PM - 1) / PM * PM, T, d, w.scale, dX, 0);
       if (e == cudaSuccess) e = launched(L);
       if (e != cudaSuccess) return e;
     }
@@ -1078,7 +1102,7 @@ cudaError_t launch_ce_bwd(const uint16_t* x, const uint16_t* W, const int64_t* t
     if (wsp == 1) aw.scale = w.scale;
     aw.out = wsp > 1 || dw_f32 ? kOutF32Store : kOutBf16;
     void* dst = dw_f32 ? (void*)(static_cast<float*>(dW) + v0 * d) : (void*)(static_cast<uint16_t*>(dW) + v0 * d);
-    e = launch_pair<1, 1, kPairDw>(PairProblem{n, d, T, w.G, piece, w.xz, d, wsp > 1 ? (void*)w.dw_part : dst, d}, wsp, aw, L);
+    e = launch_pair<1, 1, kPairDw>(PairProblem{n, d, g_rows, w.G, piece, w.xz, d, wsp > 1 ? (void*)w.dw_part : dst, d}, wsp, aw, L);
     if (e != cudaSuccess) return e;
     if (wsp > 1) {
       e = launch_dependent(k_ce_join, join_blocks, 256, 0, L.stream, w.dw_part, wsp, (n + PM - 1) / PM * PM, n, d, w.scale, dst, dw_f32);

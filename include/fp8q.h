@@ -566,7 +566,7 @@ FP8Q_API int layernorm_bwd(const void* dY, const void* x, fp8q_dtype dtype, cons
  *   dX [T,d] bf16 = G W, dW [V,d] (bf16 or fp32) = G^T x, both overwritten in full.
  * The logits are computed again in pieces of the vocabulary; G is rounded to bf16 relative to
  * max |dloss| as the tensor cores' operand (the sums are fp32), so an fp32 dW carries that rounding
- * (2^-8 of the terms of its sums at most).  Rows of x of ignored tokens may hold anything, NaN too, without
+ * (2^-8 of the terms of its sums at most; up to 64 tokens G is kept in two parts, 2^-16).  Rows of x of ignored tokens may hold anything, NaN too, without
  * reaching dX or dW.  Deterministic.
  * Requirements: 1 <= T, V <= 2^24 with fewer than 2^31 tiles of 256 x 256 logits, d a multiple of 8,
  * 8 <= d <= 65536; x, W, dX, dW 16-byte, targets

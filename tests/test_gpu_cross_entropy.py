@@ -22,7 +22,7 @@ pytestmark = pytest.mark.gpu
 
 IGN = -100
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
-SHAPES = [(1, 8, 1), (1, 16, 2), (2, 8, 300), (3, 64, 7), (127, 72, 129), (128, 128, 256), (129, 136, 257), (300, 512, 1000), (64, 256, 20001),
+SHAPES = [(1, 8, 1), (1, 16, 2), (2, 8, 300), (3, 64, 7), (127, 72, 129), (128, 128, 256), (129, 136, 257), (300, 512, 1000), (64, 256, 20001), (65, 128, 900), (33, 72, 5000),
           (257, 2048, 8200), (1000, 264, 5003), (513, 128, 16385), (2, 4096, 1001)]
 
 
@@ -89,6 +89,22 @@ def test_mean_of_one_weight():
     dl = torch.full((700,), 1.0 / float((t != IGN).sum()), device="cuda")
     loss, lse = fq.linear_cross_entropy_fwd(x, W, t)
     check_bwd(x, W, t, dl, *fq.linear_cross_entropy_bwd(x, W, t, lse, dl))
+
+
+@pytest.mark.parametrize("T", [1, 2, 33, 64])
+def test_few_tokens_lose_nothing_to_the_gradient_at_the_logits(T):
+    """Up to 64 tokens G is kept in two bf16 parts: 2^-16 of the terms, so fp32 gradients show fp32-like errors."""
+    x, W, t, dl = make(T, 512, 3001, lean=20.0, ignored=0.0)
+    loss, lse = fq.linear_cross_entropy_fwd(x, W, t)
+    dX, dW = fq.linear_cross_entropy_bwd(x, W, t, lse, dl)
+    xd, Wd = x.double(), W.double()
+    G = ref.cross_entropy_grad(xd, Wd, t, dl.double(), IGN)
+    z = xd @ Wd.t()
+    gap = (z - torch.logsumexp(z, 1, keepdim=True)).abs()
+    ep = (G.abs() + (t[:, None] == torch.arange(3001, device="cuda")) * dl.double().abs()[:, None]) * (2 * e_z(x, W)[:, None] + 2.0 ** -21 * (gap + 4))
+    terms = G.abs() * (2.0 ** -16 + (3001 / 16 + 64) * 2.0 ** -23) + ep
+    assert bool(((dW.double() - G.t() @ xd).abs() <= terms.t() @ xd.abs() + 1e-30).all())
+    assert bool(((dX.double() - G @ Wd).abs() <= (terms @ Wd.abs() + 2.0 ** -8 * (G @ Wd).abs()) * (1 + 2.0 ** -7)).all())
 
 
 def test_sharp_rows_and_wide_logits():
