@@ -329,10 +329,12 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(VEC, W))
 // dY, x and dres rows come through the ring, up to S rows ahead.  Every wait is bounded; on expiry all
 // threads leave together after the row's barrier and thread 0 waits for the copies in flight before the block exits.
 // ---------------------------------------------------------------------------
-constexpr int kLnThreads = 512;
+constexpr int kLnThreads = 512, kLnWide = 1024;
+// The threads of a block at most.
+constexpr int ln_bwd_most(int np, int stride) { return stride ? stride : np == 1 ? kLnWide : kLnThreads; }
 
 template <int F32, int VEC, int NP, int STRIDE>
-__global__ void __launch_bounds__(STRIDE > 0 && STRIDE < kLnThreads ? STRIDE : kLnThreads, (NP * VEC <= 8 ? 1024 : 512) / (STRIDE > 0 ? STRIDE : kLnThreads))
+__global__ void __launch_bounds__(ln_bwd_most(NP, STRIDE), (NP * VEC <= 8 ? kLnWide : kLnThreads) / ln_bwd_most(NP, STRIDE))
     k_layernorm_bwd(const void* dY, const void* x, const void* __restrict__ g, const float* __restrict__ mean,
                     const float* __restrict__ rstd, const void* dres, int64_t T, int d, int rows, int S, void* dX,
                     float* __restrict__ part, unsigned* status) {
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__(STRIDE > 0 && STRIDE < kLnThreads ? STRIDE : k
   constexpr bool kKeep = NP * VEC <= 16;  // u and xh stay in registers for their second use, else the inputs
   extern __shared__ __align__(128) uint8_t ln_rows[];
   __shared__ uint64_t full[kLnSlotsMax];
-  __shared__ float red[2][2][16];
+  __shared__ float red[2][2][32];
   __shared__ volatile int give_up;
   start_dependents();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, nwarps = blockDim.x >> 5;
@@ -423,6 +425,7 @@ __global__ void __launch_bounds__(STRIDE > 0 && STRIDE < kLnThreads ? STRIDE : k
     aborted = __syncthreads_or(!ok);
     if (aborted) break;
     float tot = (lane & 15) < nwarps ? red[rr & 1][lane >> 4][lane & 15] : 0.0f;
+    if ((lane & 15) + 16 < nwarps) tot += red[rr & 1][lane >> 4][(lane & 15) + 16];
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) tot += __shfl_xor_sync(0xFFFFFFFFu, tot, o);
     const float su = __shfl_sync(0xFFFFFFFFu, tot, 0) * inv_d, sx = __shfl_sync(0xFFFFFFFFu, tot, 16) * inv_d;
@@ -577,13 +580,16 @@ cudaError_t fwd_t(const void* x, const void* g, const void* b, int64_t T, int d,
 #undef FP8Q_LN_FWD
 }
 
-// The backward's launch shape.  d is a multiple of 8: a thread has 1, 2 or 4 pieces of 8 columns (d up to
-// 4096, 8192, 16384).  Otherwise 1 to 32 single columns, of 128 threads up to d = 1024 and of 512 above.
+// The backward's launch shape.  d is a multiple of 8: a thread has one piece of 8 columns up to d = 8192 (two above
+// 4096, in half the threads, leave half the warps to cover a row's chain of dependent steps: T = 8192, d = 5120 in bf16
+// with dres takes 83 us so and 74 with one), else 4.  Otherwise 1 to 32 single columns, of 128 threads up to d = 1024 and
+// of 512 above.
 constexpr int kLnNarrow = 128;
 constexpr int bwd_np(int d) {
-  const int pieces = d % 8 == 0 ? d / 8 : d, threads = d % 8 == 0 || d > 8 * kLnNarrow ? kLnThreads : kLnNarrow;
+  if (d % 8 == 0) return d <= 8 * kLnWide ? 1 : 4;
+  const int threads = d > 8 * kLnNarrow ? kLnThreads : kLnNarrow;
   int np = 1;
-  while (pieces > np * threads) np *= 2;
+  while (d > np * threads) np *= 2;
   return np;
 }
 constexpr int bwd_threads(int d) {
@@ -624,8 +630,7 @@ cudaError_t bwd_t(const void* dY, const void* x, const void* g, const float* mea
 #define FP8Q_LN_BWD(VEC, NP, STRIDE) \
   return bwd_go<F32, VEC, NP, STRIDE>(dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, L)
   if (d % 8 == 0) {
-    if (d <= 8 * kLnThreads) FP8Q_LN_BWD(8, 1, 0);
-    if (d <= 16 * kLnThreads) FP8Q_LN_BWD(8, 2, 0);
+    if (d <= 8 * kLnWide) FP8Q_LN_BWD(8, 1, 0);
     FP8Q_LN_BWD(8, 4, 0);
   }
   if (d <= kLnNarrow) FP8Q_LN_BWD(1, 1, kLnNarrow);

@@ -22,7 +22,7 @@ pytestmark = pytest.mark.gpu
 C = 1e-5
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
 SHAPES = [(1, 1), (3, 2), (5, 8), (37, 16), (1, 2048), (2, 5120), (129, 257), (300, 1000), (65, 1409), (77, 4096), (33, 8192),
-          (9, 10007), (17, 16384), (5000, 72), (1031, 3584)]
+          (9, 10007), (17, 16384), (5000, 72), (1031, 3584), (401, 4104), (613, 5552)]
 
 
 def make(T, d, dtype, seed=0, offset=0.5):
