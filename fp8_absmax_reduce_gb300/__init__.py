@@ -451,7 +451,27 @@ class Rope:
     interleaved: bool
     inv_freq: tuple
     axis: tuple
-    _ref: object = dataclasses.field(repr=False, compare=False)  # ctypes reference to the FP8QRope
+    _ref: object = dataclasses.field(init=False, repr=False, compare=False)  # ctypes reference to the FP8QRope
+
+    def __post_init__(self):
+        half = self.rot_dim // 2
+        if not (8 <= self.head_dim <= 256) or self.head_dim % 8:
+            raise ValueError(f"head_dim {self.head_dim}: a multiple of 8 from 8 to 256")
+        if not (2 <= self.rot_dim <= self.head_dim) or self.rot_dim % 2:
+            raise ValueError(f"rot_dim {self.rot_dim}: even, from 2 to head_dim")
+        if len(self.axis) != half or len(self.inv_freq) != half:
+            raise ValueError(f"{len(self.axis)} axes and {len(self.inv_freq)} frequencies for {half} pairs")
+        if not 1 <= self.n_axes <= 255 or not all(0 <= a < self.n_axes for a in self.axis):
+            raise ValueError("axes from 0 to 254")
+        if not all(math.isfinite(f) for f in self.inv_freq):
+            raise ValueError("frequencies must be finite")
+        s = FP8QRope(head_dim=self.head_dim, rot_dim=self.rot_dim, n_axes=self.n_axes, interleaved=int(self.interleaved))
+        s.inv_freq[:half] = self.inv_freq
+        s.axis[:half] = self.axis
+        object.__setattr__(self, "_ref", ctypes.byref(s))
+
+    def __reduce__(self):  # copies and pickles make their own structure
+        return Rope, (self.head_dim, self.rot_dim, self.n_axes, self.interleaved, self.inv_freq, self.axis)
 
     @staticmethod
     def make(head_dim: int = 128, rot_dim: int | None = None, base: float = 10000.0, sections=None,
@@ -460,10 +480,6 @@ class Rope:
         (default base^(-2i / rot_dim)).  sections: pairs per axis, one after the other (default: one
         axis); axis: the axis of each pair instead, in any order."""
         rot_dim = head_dim if rot_dim is None else rot_dim
-        if not (8 <= head_dim <= 256) or head_dim % 8:
-            raise ValueError(f"head_dim {head_dim}: a multiple of 8 from 8 to 256")
-        if not (2 <= rot_dim <= head_dim) or rot_dim % 2:
-            raise ValueError(f"rot_dim {rot_dim}: even, from 2 to head_dim")
         half = rot_dim // 2
         if sections is not None and axis is not None:
             raise ValueError("give sections or axis, not both")
@@ -477,16 +493,7 @@ class Rope:
             axis = [int(a) for a in axis]
             n_axes = max(axis, default=0) + 1
         freq = [base ** (-2.0 * i / rot_dim) for i in range(half)] if inv_freq is None else [float(f) for f in inv_freq]
-        if len(axis) != half or len(freq) != half:
-            raise ValueError(f"{len(axis)} axes and {len(freq)} frequencies for {half} pairs")
-        if min(axis) < 0 or not 1 <= n_axes <= 255:
-            raise ValueError("axes from 0 to 254")
-        if not all(math.isfinite(f) for f in freq):
-            raise ValueError("frequencies must be finite")
-        s = FP8QRope(head_dim=head_dim, rot_dim=rot_dim, n_axes=n_axes, interleaved=int(bool(interleaved)))
-        s.inv_freq[:half] = freq
-        s.axis[:half] = axis
-        return Rope(head_dim, rot_dim, n_axes, bool(interleaved), tuple(freq), tuple(axis), ctypes.byref(s))
+        return Rope(head_dim, rot_dim, n_axes, bool(interleaved), tuple(freq), tuple(axis))
 
 
 def _rope_call(name, fn, qkv, pos, rope, n_heads, n_kv_heads, out, stream):
@@ -494,7 +501,7 @@ def _rope_call(name, fn, qkv, pos, rope, n_heads, n_kv_heads, out, stream):
     dtype = qkv.dtype
     if width != (n_heads + 2 * n_kv_heads) * rope.head_dim:
         raise ValueError(f"qkv has {width} columns, not ({n_heads} + 2 * {n_kv_heads}) heads of {rope.head_dim}")
-    _need("pos", pos, torch.int32, (T,) if rope.n_axes == 1 and pos.dim() == 1 else (rope.n_axes, T), dev)
+    _need("pos", pos, torch.int32, (T,) if rope.n_axes == 1 and getattr(pos, "ndim", 0) == 1 else (rope.n_axes, T), dev)
     if out is None:
         out = torch.empty_like(qkv)
     elif out is not qkv:
@@ -617,7 +624,7 @@ def linear_cross_entropy_bwd(x: torch.Tensor, W: torch.Tensor, targets: torch.Te
             raise TypeError(f"dw_dtype {dw_dtype}: bfloat16 or float32")
         dW = torch.empty((V, d), dtype=dw_dtype, device=device)
     else:
-        _need("dW", dW, torch.bfloat16 if dW.dtype is torch.bfloat16 else torch.float32, (V, d), dev)
+        _need("dW", dW, torch.bfloat16 if getattr(dW, "dtype", None) is torch.bfloat16 else torch.float32, (V, d), dev)
     nb = lib.linear_cross_entropy_bwd_workspace_size(T, d, V)
     w = _scratch(nb, dev, device, ws)
     _check("linear_cross_entropy_bwd",

@@ -566,12 +566,12 @@ FP8Q_API int layernorm_bwd(const void* dY, const void* x, fp8q_dtype dtype, cons
  *   dX [T,d] bf16 = G W, dW [V,d] (bf16 or fp32) = G^T x, both overwritten in full.
  * The logits are computed again in pieces of the vocabulary; G is rounded to bf16 relative to
  * max |dloss| as the tensor cores' operand (the sums are fp32), so an fp32 dW carries that rounding
- * (2^-8 of the terms of its sums at most; up to 64 tokens G is kept in two parts, 2^-16).  Rows of x of ignored tokens may hold anything, NaN too, without
- * reaching dX or dW.  Deterministic.
+ * (2^-8 of the terms of its sums at most; up to 64 tokens G is kept in two parts, 2^-16).  Rows of x of
+ * ignored tokens may hold anything, NaN too, without reaching dX or dW.  Deterministic.
  * Requirements: 1 <= T, V <= 2^24 with fewer than 2^31 tiles of 256 x 256 logits, d a multiple of 8,
- * 8 <= d <= 65536; x, W, dX, dW 16-byte, targets
- * 8-byte, loss, lse, dloss 4-byte aligned; outputs must not overlap inputs.  Workspaces: the
- * matching *_workspace_size(T, d, V) bytes (0 for sizes outside the limits), 256-byte aligned. */
+ * 8 <= d <= 65536; x, W, dX, dW 16-byte, targets 8-byte, loss, lse, dloss 4-byte aligned; outputs must not
+ * overlap inputs.  Workspaces: the matching *_workspace_size(T, d, V) bytes (0 for sizes outside the limits),
+ * 256-byte aligned. */
 FP8Q_API size_t linear_cross_entropy_fwd_workspace_size(int64_t T, int64_t d, int64_t V);
 FP8Q_API int linear_cross_entropy_fwd(const void* x, const void* W, const int64_t* targets, int64_t T, int64_t d,
                                       int64_t V, int64_t ignore_index, float* loss, float* lse, void* ws,

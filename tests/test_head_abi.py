@@ -1,8 +1,11 @@
 """Refusals of layer norm, rotary positions and the head's cross entropy, without a GPU: the C entry
 points return the documented codes before they touch the device, and the Python entry points raise."""
 
+import copy
 import ctypes
+import dataclasses
 import os
+import pickle
 import shutil
 import subprocess
 
@@ -75,6 +78,18 @@ def test_rope_plan_refuses(fq):
             fq.Rope.make(**bad)
     r = fq.Rope.make(sections=[16, 24, 24])
     assert r.n_axes == 3 and r.axis[15:17] == (0, 1) and r.inv_freq[0] == 1.0 and r == fq.Rope.make(sections=[16, 24, 24])
+
+
+def test_a_changed_or_copied_rope_plan_is_its_own(fq):
+    r = fq.Rope.make(head_dim=64, sections=[16, 16])
+    for c in (copy.deepcopy(r), pickle.loads(pickle.dumps(r))):
+        assert c == r and c._ref._obj is not r._ref._obj and list(c._ref._obj.axis) == list(r._ref._obj.axis)
+    wide = dataclasses.replace(r, head_dim=128)
+    assert (wide._ref._obj.head_dim, wide._ref._obj.rot_dim, r._ref._obj.head_dim) == (128, 64, 64)
+    with pytest.raises(ValueError):
+        dataclasses.replace(r, head_dim=32)
+    with pytest.raises(ValueError):
+        dataclasses.replace(r, n_axes=1)
 
 
 def test_cross_entropy_refuses(fq):
