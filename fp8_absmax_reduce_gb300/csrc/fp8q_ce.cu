@@ -123,6 +123,7 @@ struct PairArgs {
   const float* scale;       // s, or null: the sum as it is
   float* acc;               // kOutBf16Join: the sum so far [M, N]
   int v0;                   // kPairGrad, kTokGrad: the piece's first column
+  int half_rows;            // rows of A in each CTA's half of a tile: 128, or fewer (kTokLse: tok_half_rows)
   int rows_lo;              // kTokGrad: the first row of G's second part, or 0: it has one
   const int64_t* targets;   // kPairLse, kTokLse
   int V;                    // kPairLse, kTokLse
@@ -318,6 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
   const int first = (int)(blockIdx.x >> 1), step = (int)(gridDim.x >> 1);
+  const int half_rows = MODE == kTokLse ? p.half_rows : 128;
   if (threadIdx.x == 0) {
     for (int s = 0; s < PL::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
     for (int a = 0; a < 2; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], 16); }
@@ -354,13 +356,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       for (int tile = first; tile < p.num_tiles && ok; tile += step) {
         int mb, nb, kb0, kb1;
         pair_coords(tile, p, mb, nb, kb0, kb1);
-        const int m0 = mb * PM + 128 * rank, n0 = nb * NT + NT / 2 * rank;
+        const int m0 = (2 * mb + rank) * half_rows, n0 = nb * NT + NT / 2 * rank;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait_held(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
           uint8_t* sA = smem + stage * PL::kStage;
           uint8_t* sB = sA + kHalfTile;
           const uint32_t bar = map_to_rank(smem_addr(&full[stage]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * PL::kStage);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (half_rows * 128 + PL::kB));
           const int k0 = kb * PK;
           if (A_MN) {  // two 64-element-wide boxes of 64 rows of K
             pair_load_2d(sA, &tmA, bar, m0, k0);
@@ -468,8 +470,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     for (int tile = first; tile < p.num_tiles; tile += step) {
       int mb, nb, kb0, kb1;
       const int part = pair_coords(tile, p, mb, nb, kb0, kb1);
-      const int row0 = mb * PM + 128 * rank + sub * 32, row = row0 + lane;
-      const bool row_ok = row < p.M, warp_ok = row0 < p.M;
+      const int row0 = (2 * mb + rank) * half_rows + sub * 32, row = row0 + lane;
+      const bool row_ok = row < p.M && sub * 32 + lane < half_rows, warp_ok = row0 < p.M && sub * 32 < half_rows;
       const uint32_t lanes = tmem_base + ((uint32_t)(sub * 32) << 16);
       if constexpr (MODE == kPairLse) {
         const int col0 = nb * NT + 128 * half;
@@ -544,7 +546,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           for (int r = 0; r < 32; ++r)
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(z[i][r]) : "r"(stage + 4 * (32 * r + (r ^ lane))) : "memory");
           const int at = ty[i] - row0;
-          if ((unsigned)at < 32u) {
+          if ((unsigned)at < 32u && sub * 32 + at < half_rows) {
             float zy;
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(zy) : "r"(stage + 4 * (32 * at + (at ^ lane))) : "memory");
             p.zy[32 * c + lane] = zy;
@@ -887,13 +889,24 @@ int pair_splits(int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
+// Rows of W in each half of a tile of the forward of few tokens, a multiple of 8 up to 128: as many tiles as the pairs take
+// in the waves of full ones, so that all pairs stream for the same time (T = 24 and 120, d = 4096, V = 100000, 391 full
+// tiles: 153 -> 143 and 158 -> 148 us; nothing is gained where one wave holds them, nor in the backward's logits, which
+// write G).  The MMAs work on 128 rows all the same: what the stage held beyond makes sums that are not read back.
+int tok_half_rows(int64_t V, const Launch& L) {
+  const int64_t pairs = pair_grid(L, 0x7FFFFFFF), waves = ((V + PM - 1) / PM + pairs - 1) / pairs;
+  if (waves == 1) return PM / 2;
+  return (int)(((V + 2 * pairs * waves - 1) / (2 * pairs * waves) + 7) / 8 * 8);
+}
+
 template <int A_MN, int B_MN, int MODE, int NT = 256>
 cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Launch& L) {
   constexpr bool kTok = MODE >= kTokLse;
   a.M = (int)q.M;
   a.N = (int)q.N;
   a.K = (int)q.K;
-  a.m_tiles = (a.M + PM - 1) / PM;
+  a.half_rows = MODE == kTokLse ? tok_half_rows(q.M, L) : PM / 2;
+  a.m_tiles = (int)((q.M + 2 * a.half_rows - 1) / (2 * a.half_rows));
   a.n_tiles = (a.N + NT - 1) / NT;
   a.k_blocks = (a.K + PK - 1) / PK;
   if ((int64_t)a.m_tiles * a.n_tiles * splits > 0x7FFFFFFF) return cudaErrorInvalidValue;
@@ -913,7 +926,7 @@ cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Laun
   a.status = L.status;
   CUtensorMap ta, tb, tc;
   bool ok = A_MN ? make_map(&ta, q.A, q.M, q.K, q.lda, 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)
-                 : make_map(&ta, q.A, q.K, q.M, q.lda, 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+                 : make_map(&ta, q.A, q.K, q.M, q.lda, 2, 64, a.half_rows, CU_TENSOR_MAP_SWIZZLE_128B);
   ok = ok && (B_MN ? make_map(&tb, q.B, q.N, q.K, q.ldb, 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)
                    : make_map(&tb, q.B, q.K, q.N, q.ldb, 2, 64, NT / 2, CU_TENSOR_MAP_SWIZZLE_128B));
   tc = ta;
@@ -1025,7 +1038,8 @@ cudaError_t launch_ce_fwd(const uint16_t* x, const uint16_t* W, const int64_t* t
     const PairProblem q{V, T, d, W, d, x, d, nullptr, 0};
     e = T <= 32 ? launch_pair<0, 0, kTokLse, 32>(q, 1, a, L)
         : T <= 64 ? launch_pair<0, 0, kTokLse, 64>(q, 1, a, L) : launch_pair<0, 0, kTokLse, 128>(q, 1, a, L);
-    pieces = 2 * pair_grid(L, (V + PM - 1) / PM);
+    const int half = tok_half_rows(V, L);
+    pieces = 2 * pair_grid(L, (V + 2 * half - 1) / (2 * half));
   } else {
     e = launch_pair<0, 0, kPairLse>(PairProblem{T, V, d, x, d, W, d, nullptr, 0}, 1, a, L);
     pieces = (int)((V + 127) / 128);

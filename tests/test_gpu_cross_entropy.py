@@ -22,7 +22,7 @@ pytestmark = pytest.mark.gpu
 
 IGN = -100
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
-SHAPES = [(1, 8, 1), (1, 16, 2), (2, 8, 300), (3, 64, 7), (127, 72, 129), (128, 128, 256), (129, 136, 257), (300, 512, 1000), (64, 256, 20001), (65, 128, 900), (33, 72, 5000),
+SHAPES = [(1, 8, 1), (1, 16, 2), (2, 8, 300), (3, 64, 7), (127, 72, 129), (128, 128, 256), (129, 136, 257), (300, 512, 1000), (64, 256, 20001), (65, 128, 900), (33, 72, 5000), (24, 64, 25000), (127, 64, 39001),
           (257, 2048, 8200), (1000, 264, 5003), (513, 128, 16385), (2, 4096, 1001)]
 
 
@@ -68,6 +68,18 @@ def check_bwd(x, W, t, dl, dX, dW):
         if n >= 16:
             assert float((err / bound).square().mean().sqrt()) < 0.35
     assert bool((dX[t == IGN] == 0).all())
+
+
+@pytest.mark.parametrize("T", [30, 60, 128])
+@pytest.mark.parametrize("V", [20001, 25000, 39001, 19456])
+def test_few_tokens_find_their_targets_at_every_tile_edge(T, V):
+    x, W, _, _ = make(T, 16, V)
+    edges = torch.cat([torch.arange(e, V, 8) for e in (0, 7)])
+    for i in range(0, edges.numel(), 16 * T):  # every 16th run of T edges
+        t = edges[i:i + T].cuda()
+        t = torch.cat([t, t.new_full((T - t.numel(),), V - 1)])
+        loss, lse = fq.linear_cross_entropy_fwd(x, W, t, IGN)
+        check_fwd(x, W, t, loss, lse)
 
 
 @pytest.mark.parametrize("T,d,V", SHAPES)
