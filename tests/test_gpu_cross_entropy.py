@@ -22,7 +22,7 @@ pytestmark = pytest.mark.gpu
 
 IGN = -100
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
-SHAPES = [(1, 8, 1), (1, 16, 2), (2, 8, 300), (3, 64, 7), (127, 72, 129), (128, 128, 256), (129, 136, 257), (300, 512, 1000), (64, 256, 20001), (65, 128, 900), (33, 72, 5000), (24, 64, 25000), (127, 64, 39001),
+SHAPES = [(1, 8, 1), (1, 16, 2), (2, 8, 300), (3, 64, 7), (127, 72, 129), (128, 128, 256), (129, 136, 257), (300, 512, 1000), (64, 256, 20001), (65, 128, 900), (33, 72, 5000), (24, 64, 25000), (127, 64, 39001), (300, 64, 9000), (257, 72, 21013), (512, 64, 32000),
           (257, 2048, 8200), (1000, 264, 5003), (513, 128, 16385), (2, 4096, 1001)]
 
 
