@@ -322,8 +322,8 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(VEC, W))
 }
 
 // ---------------------------------------------------------------------------
-// Backward: a block owns a run of consecutive rows, a thread the same NP pieces of every row, whose
-// shares of dg and db it keeps in registers; k_layernorm_bwd_finish adds the blocks' partial rows.
+// Backward of the other rows (odd widths, wider ones): a block owns a run of consecutive rows, a thread the same NP pieces
+// of every row, whose shares of dg and db it keeps in registers; k_layernorm_bwd_finish adds the blocks' partial rows.
 // A row needs one exchange between its warps, of the two sums in one barrier.
 //
 // dY, x and dres rows come through the ring, up to S rows ahead.  Every wait is bounded; on expiry all
@@ -467,63 +467,82 @@ __global__ void __launch_bounds__(ln_bwd_most(NP, STRIDE), (NP * VEC <= 8 ? kLnW
   }
 }
 
-// Narrow bf16 rows (d a multiple of 8 up to 1024): a warp owns a run of rows, a lane NP pieces of each (piece k of lane l
-// is piece 32 k + l).  A lane copies its own pieces of the next D - 1 rows into its own part of shared memory meanwhile, so
-// nothing but the two sums crosses the warp and no row waits for a barrier; the warps' shares of dg and db are added
-// in shared memory at the end, which leaves the second launch 152 to 608 rows instead of up to 2432.  Against a row to a
-// block, with dres: T = 16384, d = 1024: 36 -> 29 us; d = 768: 33 -> 23; T = 32768, d = 512: 42 -> 30; T = 65536, d = 256:
-// 45 -> 33.  fp32 rows have half the copies in flight in the same memory and are slower so (T = 16384, d = 512: 38 -> 44).
-template <int NP>
-struct NarrowPlan {
-  static constexpr int kWarps = NP >= 3 ? 12 : 8;
-  static constexpr int kPerSm = NP == 1 ? 4 : NP == 2 ? 2 : 1;  // 64, 128, 168, 168 registers
-  static constexpr int kDepth = NP <= 2 ? 4 : NP == 3 ? 3 : 2;
+// Backward of rows of whole 16-byte vectors, up to 8192 bf16 or 4096 fp32 columns: W warps own a run of consecutive rows, a
+// lane NP vectors of each (vector k of lane l of warp w is vector (k W + w) 32 + l).  A lane copies its own vectors of the
+// next D - 1 rows into its own part of shared memory meanwhile, so a row waits for no one's copies but its own, and only the
+// two sums cross the W warps (one barrier among them).  An SM's 16 warps hold 16 / W rows at once; their shares of
+// dg and db are added in shared memory at the end, so that the second launch reads one row an SM (four for the narrowest).
+// Against one block a row with a ring of bulk copies (as below), with dres: bf16 T = 8192, d = 3584: 48 -> 45 us; d = 5120:
+// 72 -> 62; T = 16384, d = 1024: 36 -> 29; T = 65536, d = 256: 45 -> 32; fp32 T = 16384, d = 512: 38 -> 28; T = 4096,
+// d = 4096: 56 -> 49; T = 1000, d = 1024: 13 -> 7.  Bound by memory: 0.80 of the measured copy rate at 8192 x 5120.
+template <int NP, int W>
+struct RunPlan {
+  static constexpr int kPerSm = NP == 1 ? 4 : 1;
+  static constexpr int kWarps = NP == 1 ? 8 : 16 / W * W;
+  static constexpr int kDepth = 4;
+  static constexpr int kBytes = kWarps * kDepth * 3 * NP * 512;
+};
+// One vector of 16 bytes: 8 bf16 or 4 fp32 columns, taken in pairs.
+template <int F32>
+struct Vec16 {
+  static constexpr int kUnits = F32 ? 2 : 4, kCols = 2 * kUnits;
+  uint4 w;
+  __device__ __forceinline__ void load(const void* p) { w = *static_cast<const uint4*>(p); }
+  __device__ __forceinline__ float2 unit(int e) const {
+    if constexpr (F32) return e == 0 ? make_float2(__uint_as_float(w.x), __uint_as_float(w.y)) : make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+    const uint32_t v = e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w;
+    return make_float2(bf16_lo(v), bf16_hi(v));
+  }
+  __device__ __forceinline__ static void store(void* p, const float2 (&v)[kUnits]) {
+    if constexpr (F32) *static_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    else st_v4(static_cast<uint16_t*>(p), make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                                    pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y)));
+  }
 };
 
-template <int NP>
-__global__ void __launch_bounds__(32 * NarrowPlan<NP>::kWarps, NarrowPlan<NP>::kPerSm)
-    k_layernorm_bwd_narrow(const void* dY, const void* x, const void* __restrict__ g, const float* __restrict__ mean,
-                           const float* __restrict__ rstd, const void* dres, int64_t T, int d, int run, void* dX,
-                           float* __restrict__ part) {
-  using P = Piece<0, 8>;
-  constexpr int kWarps = NarrowPlan<NP>::kWarps, D = NarrowPlan<NP>::kDepth;
+template <int F32, int NP, int W>
+__global__ void __launch_bounds__(32 * RunPlan<NP, W>::kWarps, RunPlan<NP, W>::kPerSm)
+    k_layernorm_bwd_runs(const uint8_t* dY, const uint8_t* x, const uint8_t* __restrict__ g, const float* __restrict__ mean,
+                         const float* __restrict__ rstd, const uint8_t* dres, int64_t T, int d, int run, uint8_t* dX,
+                         float* __restrict__ part) {
+  using P = Vec16<F32>;
+  constexpr int kWarps = RunPlan<NP, W>::kWarps, D = RunPlan<NP, W>::kDepth, kUnits = P::kUnits;
   extern __shared__ __align__(128) uint8_t ln_rows[];  // [warps][D][3][NP][32] pieces
+  __shared__ float red[2][kWarps][2];
   start_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pieces = d / 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pieces = d / P::kCols;
+  const int group = warp / W, first = warp % W * 32 + lane;
   uint8_t* own = ln_rows + (warp * D * 3 * NP * 32 + lane) * 16;
-  float2 ag[NP][4], ab[NP][4];
+  float2 ag[NP][kUnits], ab[NP][kUnits];
   P pg[NP];
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) ag[k][e] = ab[k][e] = all<8>(0.0f);
-    if (32 * k + lane < pieces) pg[k].load(g, 8 * (32 * k + lane));
+    for (int e = 0; e < kUnits; ++e) ag[k][e] = ab[k][e] = all<8>(0.0f);
+    if (32 * W * k + first < pieces) pg[k].load(g + 16 * (32 * W * k + first));
   }
-  const int64_t r0 = ((int64_t)blockIdx.x * kWarps + warp) * run;
+  const int64_t r0 = ((int64_t)blockIdx.x * (kWarps / W) + group) * run, row_bytes = (int64_t)pieces * 16;
   const int n = (int)(T - r0 < run ? (T > r0 ? T - r0 : 0) : run);
   auto fetch = [&](int i, int slot) {
     if (i < n) {
-      const int64_t row = r0 + i;
 #pragma unroll
       for (int w = 0; w < 3; ++w) {
-        const void* src = w == 0 ? dY : w == 1 ? x : dres;
+        const uint8_t* src = w == 0 ? dY : w == 1 ? x : dres;
         if (!src) continue;
 #pragma unroll
-        for (int k = 0; k < NP; ++k) {
-          const int i = 32 * k + lane;
-          if (i >= pieces) continue;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(own + ((slot * 3 + w) * NP + k) * 512)),
-                       "l"(static_cast<const uint16_t*>(src) + row * d + 8 * i)
-                       : "memory");
-        }
+        for (int k = 0; k < NP; ++k)
+          if (32 * W * k + first < pieces)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(own + ((slot * 3 + w) * NP + k) * 512)),
+                         "l"(src + (r0 + i) * row_bytes + 16 * (32 * W * k + first))
+                         : "memory");
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   auto take = [&](int slot, int w, int k) {
-    P r;
-    r.load(own + ((slot * 3 + w) * NP + k) * 512, 0);
-    return r;
+    P v;
+    v.load(own + ((slot * 3 + w) * NP + k) * 512);
+    return v;
   };
   const float inv_d = 1.0f / (float)d;
 #pragma unroll
@@ -531,8 +550,7 @@ __global__ void __launch_bounds__(32 * NarrowPlan<NP>::kWarps, NarrowPlan<NP>::k
   float mus = 0.0f, rss = 0.0f;  // lane l's: of row l of the 32 at hand
   int slot = 0;
   for (int i = 0; i < n; ++i) {
-    const int64_t row = r0 + i;
-    if ((i & 31) == 0 && i + lane < n) { mus = mean[row + lane]; rss = rstd[row + lane]; }
+    if ((i & 31) == 0 && i + lane < n) { mus = mean[r0 + i + lane]; rss = rstd[r0 + i + lane]; }
     const float mu = __shfl_sync(0xFFFFFFFFu, mus, i & 31), rs = __shfl_sync(0xFFFFFFFFu, rss, i & 31);
     fetch(i + D - 1, slot == 0 ? D - 1 : slot - 1);
     asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
@@ -540,11 +558,11 @@ __global__ void __launch_bounds__(32 * NarrowPlan<NP>::kWarps, NarrowPlan<NP>::k
     float2 su_t = all<8>(0.0f), sx_t = all<8>(0.0f);
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      if (32 * k + lane >= pieces) continue;
+      if (32 * W * k + first >= pieces) continue;
       py[k] = take(slot, 0, k);
       px[k] = take(slot, 1, k);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < kUnits; ++e) {
         const float2 dy = py[k].unit(e), u = mul(dy, pg[k].unit(e));
         const float2 h = mul(add(px[k].unit(e), all<8>(-mu)), all<8>(rs));
         su_t = add(su_t, u);
@@ -554,37 +572,54 @@ __global__ void __launch_bounds__(32 * NarrowPlan<NP>::kWarps, NarrowPlan<NP>::k
       }
     }
     const float both = ln_warp_sum2(sum(su_t), sum(sx_t), lane) * inv_d;
-    const float su = __shfl_sync(0xFFFFFFFFu, both, 0), sx = __shfl_sync(0xFFFFFFFFu, both, 16);
+    float su, sx;
+    if (W == 1) {
+      su = __shfl_sync(0xFFFFFFFFu, both, 0);
+      sx = __shfl_sync(0xFFFFFFFFu, both, 16);
+    } else {  // the next row's pairs take the other buffer, so one barrier a row is enough
+      if ((lane & 15) == 0) red[i & 1][warp][lane >> 4] = both;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * W) : "memory");
+      su = sx = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        su += red[i & 1][group * W + w][0];
+        sx += red[i & 1][group * W + w][1];
+      }
+    }
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      const int i = 32 * k + lane;
-      if (i >= pieces) continue;
+      if (32 * W * k + first >= pieces) continue;
       P pr;
       if (dres) pr = take(slot, 2, k);
-      float2 v[4];
+      float2 v[kUnits];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < kUnits; ++e) {
         const float2 h = mul(add(px[k].unit(e), all<8>(-mu)), all<8>(rs)), u = mul(py[k].unit(e), pg[k].unit(e));
         const float2 w = add(fma(h, all<8>(-sx), u), all<8>(-su));
         v[e] = dres ? fma(w, all<8>(rs), pr.unit(e)) : mul(w, all<8>(rs));
       }
-      P::store(dX, row * d + 8 * i, v);
+      P::store(dX + (r0 + i) * row_bytes + 16 * (32 * W * k + first), v);
     }
     slot = slot + 1 == D ? 0 : slot + 1;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-  float* rows = reinterpret_cast<float*>(ln_rows);  // [warps][d]
+  float* rows = reinterpret_cast<float*>(ln_rows);  // [groups][d]
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < NP; ++k)
-      if (32 * k + lane < pieces) Piece<1, 8>::store(rows, (int64_t)warp * d + 8 * (32 * k + lane), which ? ab[k] : ag[k]);
+      if (32 * W * k + first < pieces)
+#pragma unroll
+        for (int e = 0; e < kUnits; e += 2) {
+          const float2 a = which ? ab[k][e] : ag[k][e], b = which ? ab[k][e + 1] : ag[k][e + 1];
+          *reinterpret_cast<float4*>(rows + group * d + P::kCols * (32 * W * k + first) + 2 * e) = make_float4(a.x, a.y, b.x, b.y);
+        }
     __syncthreads();
     for (int j = threadIdx.x; j < d; j += 32 * kWarps) {
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += rows[w * d + j];
+      for (int w = 0; w < kWarps / W; ++w) v += rows[w * d + j];
       part[((int64_t)blockIdx.x * 2 + which) * d + j] = v;
     }
   }
@@ -703,10 +738,8 @@ cudaError_t fwd_t(const void* x, const void* g, const void* b, int64_t T, int d,
 #undef FP8Q_LN_FWD
 }
 
-// The backward's launch shape.  d is a multiple of 8: a thread has one piece of 8 columns up to d = 8192 (two above
-// 4096, in half the threads, leave half the warps to cover a row's chain of dependent steps: T = 8192, d = 5120 in bf16
-// with dres takes 83 us so and 74 with one), else 4.  Otherwise 1 to 32 single columns, of 128 threads up to d = 1024 and
-// of 512 above.
+// The launch shape of a block a row.  d is a multiple of 8: a thread has one piece of 8 columns up to d = 8192, else 4.
+// Otherwise 1 to 32 single columns, of 128 threads up to d = 1024 and of 512 above.
 constexpr int kLnNarrow = 128;
 constexpr int bwd_np(int d) {
   if (d % 8 == 0) return d <= 8 * kLnWide ? 1 : 4;
@@ -747,21 +780,23 @@ cudaError_t bwd_go(const void* dY, const void* x, const void* g, const float* me
   return launched(L);
 }
 
-template <int NP>
-cudaError_t narrow_go(const void* dY, const void* x, const void* g, const float* mean, const float* rstd, const void* dres,
-                      int64_t T, int d, void* dX, float* part, int* nblk, const Launch& L) {
-  using N = NarrowPlan<NP>;
-  auto* k = k_layernorm_bwd_narrow<NP>;
+template <int F32, int NP, int W>
+cudaError_t runs_go(const void* dY, const void* x, const void* g, const float* mean, const float* rstd, const void* dres,
+                    int64_t T, int d, void* dX, float* part, int* nblk, const Launch& L) {
+  using R = RunPlan<NP, W>;
+  static_assert(R::kBytes * R::kPerSm <= (int)kLnSmemBudget, "shared memory per SM");
+  auto* k = k_layernorm_bwd_runs<F32, NP, W>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = ring_limit(k, done);
   if (e != cudaSuccess) return e;
-  // a wave of resident blocks, each warp with a run of consecutive rows
-  const int64_t warps = (int64_t)(L.num_sms < kLnPlanSms ? L.num_sms : kLnPlanSms) * N::kPerSm * N::kWarps;
-  const int run = (int)((T + warps - 1) / warps), block_rows = run * N::kWarps;
+  // a wave of resident blocks, each group of warps with a run of consecutive rows
+  constexpr int kGroups = R::kWarps / W;
+  const int64_t groups = (int64_t)(L.num_sms < kLnPlanSms ? L.num_sms : kLnPlanSms) * R::kPerSm * kGroups;
+  const int run = (int)((T + groups - 1) / groups), block_rows = run * kGroups;
   *nblk = (int)((T + block_rows - 1) / block_rows);
-  constexpr size_t smem = (size_t)N::kWarps * N::kDepth * 3 * NP * 512;
-  static_assert(smem * N::kPerSm <= kLnSmemBudget, "shared memory per SM");
-  k<<<*nblk, 32 * N::kWarps, smem, L.stream>>>(dY, x, g, mean, rstd, dres, T, d, run, dX, part);
+  auto bytes = [](const void* p) { return static_cast<const uint8_t*>(p); };
+  k<<<*nblk, 32 * R::kWarps, R::kBytes, L.stream>>>(bytes(dY), bytes(x), bytes(g), mean, rstd, bytes(dres), T, d, run,
+                                                    static_cast<uint8_t*>(dX), part);
   return launched(L);
 }
 
@@ -771,13 +806,24 @@ cudaError_t bwd_t(const void* dY, const void* x, const void* g, const float* mea
 #define FP8Q_LN_BWD(VEC, NP, STRIDE) \
   return bwd_go<F32, VEC, NP, STRIDE>(dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, L)
   if (d % 8 == 0) {
-    if constexpr (!F32) {
-      if (d <= 256) return narrow_go<1>(dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, L);
-      if (d <= 512) return narrow_go<2>(dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, L);
-      if (d <= 768) return narrow_go<3>(dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, L);
-      if (d <= 1024) return narrow_go<4>(dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, L);
+#define FP8Q_LN_RUNS(NP, W) return runs_go<F32, NP, W>(dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, L)
+    constexpr int kCols = F32 ? 256 : 512;  // of a warp
+    if (2 * d <= kCols) FP8Q_LN_RUNS(1, 1);
+    if (d <= kCols) FP8Q_LN_RUNS(2, 1);
+    if (d <= 2 * kCols) FP8Q_LN_RUNS(2, 2);
+    if (d <= 3 * kCols) FP8Q_LN_RUNS(2, 3);
+    if (d <= 4 * kCols) FP8Q_LN_RUNS(2, 4);
+    if (d <= 5 * kCols) FP8Q_LN_RUNS(2, 5);
+    if (d <= 6 * kCols) FP8Q_LN_RUNS(2, 6);
+    if (d <= 7 * kCols) FP8Q_LN_RUNS(2, 7);
+    if (d <= 8 * kCols) FP8Q_LN_RUNS(2, 8);
+    if (d <= 10 * kCols) FP8Q_LN_RUNS(2, 10);
+    if (d <= 12 * kCols) FP8Q_LN_RUNS(2, 12);
+    if (d <= 16 * kCols) FP8Q_LN_RUNS(2, 16);
+#undef FP8Q_LN_RUNS
+    if constexpr (F32) {
+      if (d <= 8 * kLnWide) FP8Q_LN_BWD(8, 1, 0);
     }
-    if (d <= 8 * kLnWide) FP8Q_LN_BWD(8, 1, 0);
     FP8Q_LN_BWD(8, 4, 0);
   }
   if (d <= kLnNarrow) FP8Q_LN_BWD(1, 1, kLnNarrow);

@@ -23,7 +23,8 @@ C = 1e-5
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
 SHAPES = [(1, 1), (3, 2), (5, 8), (37, 16), (1, 2048), (2, 5120), (129, 257), (300, 1000), (65, 1409), (77, 4096), (33, 8192),
           (9, 10007), (17, 16384), (5000, 72), (1031, 3584), (401, 4104), (613, 5552),
-          (60001, 776), (20000, 520), (80000, 264), (160000, 24), (3000, 1024), (2500, 768), (5, 512)]
+          (60001, 776), (20000, 520), (80000, 264), (160000, 24), (3000, 1024), (2500, 768), (5, 512), (700, 1408),
+          (333, 2560), (333, 2816), (200, 1280), (200, 1792), (450, 2048), (5000, 4096), (10100, 3584)]
 
 
 def make(T, d, dtype, seed=0, offset=0.5):
@@ -101,7 +102,7 @@ def test_non_finite_rows_stay_in_their_rows():
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("T,d", [(50, 2048), (31, 1409), (700, 1000), (9000, 200), (45, 768), (300, 512)])
+@pytest.mark.parametrize("T,d", [(50, 2048), (31, 1409), (700, 1000), (401, 5120), (600, 3584), (9000, 200), (45, 768), (300, 512)])
 def test_in_place_guard_bands_and_repeats(T, d, dtype):
     t = make(T, d, dtype, seed=7)
     y, mean, rstd = fq.layernorm_fwd(t["x"], t["g"], t["b"])
