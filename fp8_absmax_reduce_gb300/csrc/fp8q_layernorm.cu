@@ -625,26 +625,30 @@ __global__ void __launch_bounds__(32 * RunPlan<NP, W>::kWarps, RunPlan<NP, W>::k
   }
 }
 
-// Column sums of the blocks' partial rows part [nblk][2 d]: 32 columns a block, 32 row groups, then a tree.
-__global__ void __launch_bounds__(1024) k_layernorm_bwd_finish(const float* __restrict__ part, int nblk, int d,
-                                                               float* __restrict__ dg, float* __restrict__ db) {
-  __shared__ float sum[32][33];
+// Column sums of the blocks' partial rows part [nblk][2 d]: 16 columns a block, 16 row groups, then a tree.  A block is small
+// enough to become resident beside the kernel before it (against 1024 threads: T = 8192, d = 5120 in bf16 62 -> 60 us,
+// T = 4096, d = 256 7.4 -> 6.8).
+constexpr int kFinishCols = 16, kFinishThreads = 256;
+__global__ void __launch_bounds__(kFinishThreads) k_layernorm_bwd_finish(const float* __restrict__ part, int nblk, int d,
+                                                                         float* __restrict__ dg, float* __restrict__ db) {
+  constexpr int kGroups = kFinishThreads / kFinishCols;
+  __shared__ float sum[kGroups][kFinishCols + 1];
   wait_for_previous();
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int j = blockIdx.x * 32 + tx;
+  const int tx = threadIdx.x % kFinishCols, ty = threadIdx.x / kFinishCols;
+  const int j = blockIdx.x * kFinishCols + tx;
   float s = 0.0f;
   if (j < 2 * d)
-    for (int k = ty; k < nblk; k += 32 * 8) {
-      float v[8];  // 8 loads in flight
+    for (int k = ty; k < nblk; k += kGroups * 10) {
+      float v[10];  // 10 loads in flight
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = k + 32 * q < nblk ? part[(int64_t)(k + 32 * q) * 2 * d + j] : 0.0f;
+      for (int q = 0; q < 10; ++q) v[q] = k + kGroups * q < nblk ? part[(int64_t)(k + kGroups * q) * 2 * d + j] : 0.0f;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) s += v[q];
+      for (int q = 0; q < 10; ++q) s += v[q];
     }
   sum[ty][tx] = s;
   __syncthreads();
 #pragma unroll
-  for (int w = 16; w > 0; w >>= 1) {
+  for (int w = kGroups / 2; w > 0; w >>= 1) {
     if (ty < w) sum[ty][tx] += sum[ty + w][tx];
     __syncthreads();
   }
@@ -856,7 +860,7 @@ cudaError_t launch_layernorm_bwd(const void* dY, const void* x, int f32, const v
   cudaError_t e = f32 ? bwd_t<1>(dY, x, g, mean, rstd, dres, T, d, dX, part, &nblk, L)
                       : bwd_t<0>(dY, x, g, mean, rstd, dres, T, d, dX, part, &nblk, L);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(k_layernorm_bwd_finish, (unsigned)((2 * d + 31) / 32), 1024, 0, L.stream, part, nblk, d, dg, db);
+  e = launch_dependent(k_layernorm_bwd_finish, (unsigned)((2 * d + kFinishCols - 1) / kFinishCols), kFinishThreads, 0, L.stream, part, nblk, d, dg, db);
   if (L.launches) ++*L.launches;
   return e;
 }
