@@ -130,14 +130,14 @@ __device__ __forceinline__ void ln_copy(uint8_t* dst, const void* src, int64_t o
 
 // ---------------------------------------------------------------------------
 // Forward: W warps hold RT rows at once in registers, NP pieces of each row a lane (piece k of lane l of warp w
-// is piece (k W + w) 32 + l); a block of max(W, 8) warps takes kRows consecutive rows at a time (one slot of the
+// is piece (k W + w) 32 + l); a block of 8 warps (W where that is no divisor of 8) takes kRows consecutive rows at a time (one slot of the
 // ring, one copy) and walks them with the grid's stride.  Each warp takes the mean and the sum of
 // squares about it of its own elements, in two passes over its registers; the warps' (mean, M2) pairs are then joined,
 // mean = sum n_w mean_w / d and M2 = sum (M2_w + n_w (mean_w - mean)^2), so a row costs one block barrier and
 // nothing cancels.  bf16 rows go two at a time (RT = 2): what bounds them is instructions, and the
 // second row shares the unpacking of gain and bias and the exchanges (T = 16384, d = 5120: 66 -> 60 us).
 // ---------------------------------------------------------------------------
-constexpr int ln_fwd_threads(int W) { return W < 8 ? 256 : 32 * W; }
+constexpr int ln_fwd_threads(int W) { return 8 % W == 0 ? 256 : 32 * W; }
 // Resident blocks per SM by registers: 512 threads of 128 for pieces of 8, 768 of 80 for single columns.  They hold a
 // thread's gain and bias too: read again for each row, those come from L2 (the ring leaves L1 too little).
 constexpr int ln_fwd_per_sm(int VEC, int W) {
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(VEC, W))
                     int S, void* y, float* __restrict__ mean, float* __restrict__ rstd, unsigned* status) {
   using E = typename Unit<VEC>::T;
   constexpr int kUnits = Unit<VEC>::kCount, ES = F32 ? 4 : 2;
-  constexpr int kRows = W < 8 ? RT * (8 / W) : RT;
+  constexpr int kRows = 8 % W == 0 ? RT * (8 / W) : RT;
   static_assert(RT == 1 || W <= 16, "two rows join in the warp's halves");
   constexpr int kJoin = W <= 1 ? 1 : W <= 2 ? 2 : W <= 4 ? 4 : W <= 8 ? 8 : W <= 16 ? 16 : 32;  // lanes that join W pairs
   extern __shared__ __align__(128) uint8_t ln_rows[];
@@ -685,7 +685,7 @@ int ring_slots(size_t slot, int* per_sm) {
 template <int F32, int VEC, int NP, int W>
 cudaError_t fwd_go(const void* x, const void* g, const void* b, int64_t T, int d, float eps, void* y, float* mean,
                    float* rstd, const Launch& L) {
-  constexpr int RT = VEC == 8 && !F32 && NP <= 3 ? 2 : 1, rows = W < 8 ? RT * (8 / W) : RT;
+  constexpr int RT = VEC == 8 && !F32 && NP <= 3 ? 2 : 1, rows = 8 % W == 0 ? RT * (8 / W) : RT;
   auto* k = k_layernorm_fwd<F32, VEC, NP, W, RT>;
   const size_t slot = ln_region((uint32_t)(rows * d * (F32 ? 4 : 2)));
   int per_sm = ln_fwd_per_sm(VEC, W);
@@ -701,7 +701,8 @@ cudaError_t fwd_go(const void* x, const void* g, const void* b, int64_t T, int d
 
 // The fewest warps (a power of two) whose lanes hold the row: in fp32 up to 4 pieces of 8 columns a lane, in bf16
 // up to 3 (two rows of 4 do not fit in the registers: T = 16384, d = 4096 takes 70 us so, one such row at a time 51, and
-// 42 with twice the warps), in odd widths up to 16 single columns.
+// 42 with twice the warps), in odd widths up to 16 single columns.  In bf16 five or ten warps where they fit the row better
+// (T = 16384, d = 2560: 36 us with four, 30 with five).
 template <int F32>
 cudaError_t fwd_t(const void* x, const void* g, const void* b, int64_t T, int d, float eps, void* y, float* mean,
                   float* rstd, const Launch& L) {
@@ -723,6 +724,7 @@ cudaError_t fwd_t(const void* x, const void* g, const void* b, int64_t T, int d,
       if (d <= 4 * kCols) FP8Q_LN_FWD(8, 2, 2);
       if (d <= 6 * kCols) FP8Q_LN_FWD(8, 3, 2);
       if (d <= 8 * kCols) FP8Q_LN_FWD(8, 2, 4);
+      if (d <= 10 * kCols) FP8Q_LN_FWD(8, 2, 5);
       if (d <= 12 * kCols) FP8Q_LN_FWD(8, 3, 4);
       if (d <= 16 * kCols) FP8Q_LN_FWD(8, 2, 8);
       if (d <= 20 * kCols) FP8Q_LN_FWD(8, 2, 10);

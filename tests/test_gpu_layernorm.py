@@ -24,7 +24,7 @@ HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
 SHAPES = [(1, 1), (3, 2), (5, 8), (37, 16), (1, 2048), (2, 5120), (129, 257), (300, 1000), (65, 1409), (77, 4096), (33, 8192),
           (9, 10007), (17, 16384), (5000, 72), (1031, 3584), (401, 4104), (613, 5552),
           (60001, 776), (20000, 520), (80000, 264), (160000, 24), (3000, 1024), (2500, 768), (5, 512), (700, 1408),
-          (333, 2560), (333, 2816), (200, 1280), (200, 1792), (450, 2048), (5000, 4096), (10100, 3584)]
+          (333, 2560), (333, 2816), (77, 2056), (200, 1280), (200, 1792), (450, 2048), (5000, 4096), (10100, 3584)]
 
 
 def make(T, d, dtype, seed=0, offset=0.5):
