@@ -129,19 +129,26 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_vec(const void* in, const
     }
   }
   if (in == out) return;
-  const int v_vecs = (heads - rot_heads) * p.dh / 8;  // the v heads, one run of the row
-#pragma unroll 2
-  for (int i = r; i < v_vecs; i += group) {
-    Vec8<F32> a;
-    a.load(in, base + (int64_t)rot_heads * p.dh + 8 * i);
-    a.store(out, base + (int64_t)rot_heads * p.dh + 8 * i);
-  }
-  const int tail = (p.dh - p.rot) / 8;  // the rotated heads' columns from rot on
-  for (int i = r; i < tail * rot_heads; i += group) {
-    const int h = i / tail, k = i - h * tail;
-    Vec8<F32> a;
-    a.load(in, base + h * p.dh + p.rot + 8 * k);
-    a.store(out, base + h * p.dh + p.rot + 8 * k);
+  // the rest: the v heads, one run of the row, and the rotated heads' columns from rot on; kCopies vectors in flight
+  constexpr int kCopies = F32 ? 4 : 8;
+  const int v_vecs = (heads - rot_heads) * p.dh / 8, tail = (p.dh - p.rot) / 8, all = v_vecs + tail * rot_heads;
+  for (int i0 = r; i0 < all; i0 += kCopies * group) {
+    Vec8<F32> v[kCopies];
+    int at[kCopies];
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q) {
+      const int i = i0 + q * group;
+      if (i < v_vecs) {
+        at[q] = rot_heads * p.dh + 8 * i;
+      } else if (i < all) {
+        const int h = (i - v_vecs) / tail;
+        at[q] = h * p.dh + p.rot + 8 * (i - v_vecs - h * tail);
+      }
+      if (i < all) v[q].load(in, base + at[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q)
+      if (i0 + q * group < all) v[q].store(out, base + at[q]);
   }
 }
 
