@@ -8,7 +8,8 @@
 //
 // Bound by memory: every element is read and written once (in place: the rotated heads alone).  A
 // thread keeps the sines and cosines of 8 pairs of one token in registers and applies them to its
-// share of the token's heads, two 16-byte vectors a head, four heads' loads in flight.
+// share of the token's heads, two vectors of 8 columns a head, four heads' loads in flight (fp32 two: with four, the registers
+// leave too few blocks; T = 2000, 56 heads of 128, 64 turned: 24 us so and 20 with two).
 #include "fp8q_common.cuh"
 #include "fp8q_internal.h"
 
@@ -63,7 +64,7 @@ struct Vec8 {
   }
 };
 
-constexpr int kRopeThreads = 128, kRopeHeads = 4;  // threads of a block; heads a thread has in flight
+constexpr int kRopeThreads = 128, kRopeShare = 8;  // threads of a block; heads of a thread, where tokens are many
 
 // rot_dim a multiple of 16.  A token has `units` * `slots` threads: thread (u, s) turns pairs 8u .. 8u+7
 // of heads s, s + slots, ...; then the token's threads copy what is not rotated.
@@ -72,6 +73,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_vec(const void* in, const
                                                            const int32_t* __restrict__ pos, int64_t T, int heads,
                                                            int rot_heads, int units, int slots, int tokens, float sign,
                                                            void* out) {
+  constexpr int kHeads = F32 ? 2 : 4;  // in flight
   const int group = units * slots;
   const int tok = threadIdx.x / group, r = threadIdx.x - tok * group;
   const int64_t t = (int64_t)blockIdx.x * tokens + tok;
@@ -79,10 +81,10 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_vec(const void* in, const
   const int slot = r / units, u = r - slot * units;
   const int64_t base = t * heads * p.dh;
   const int c0 = INTER ? 16 * u : 8 * u, c1 = INTER ? c0 + 8 : c0 + (p.rot >> 1);
-  Vec8<F32> a[kRopeHeads], b[kRopeHeads];
+  Vec8<F32> a[kHeads], b[kHeads];
   auto load = [&](int h0) {
 #pragma unroll
-    for (int q = 0; q < kRopeHeads; ++q) {
+    for (int q = 0; q < kHeads; ++q) {
       const int h = h0 + q * slots;
       if (h < rot_heads) {
         a[q].load(in, base + h * p.dh + c0);
@@ -97,10 +99,10 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_vec(const void* in, const
     const int i = 8 * u + k;
     rope_sincos(pos[(int64_t)p.axis[i] * T + t], p.turn[i], sign, s[k], c[k]);
   }
-  for (int h0 = slot; h0 < rot_heads; h0 += kRopeHeads * slots) {
+  for (int h0 = slot; h0 < rot_heads; h0 += kHeads * slots) {
     if (h0 != slot) load(h0);
 #pragma unroll
-    for (int q = 0; q < kRopeHeads; ++q) {
+    for (int q = 0; q < kHeads; ++q) {
       const int h = h0 + q * slots;
       if (h < rot_heads) {
         float x[8], y[8], xo[8], yo[8];
@@ -194,11 +196,11 @@ cudaError_t launch_rope(const void* in, int f32, const RopePlan& p, const int32_
   const int heads = n_heads + 2 * n_kv_heads, rot_heads = n_heads + n_kv_heads;
   const float sign = inverse ? -1.0f : 1.0f;
   if (p.rot % 16 == 0) {
-    // Threads per token: enough slots that each thread has at most 2 kRopeHeads heads and 16 vectors to copy (T = 16384, 24 heads
-    // of 96, 48 turned: 35 us with heads alone counted, 28 so), and for few tokens
-    // more (down to one head a thread), until the grid holds about 512 threads per SM.
+    // Threads per token: enough slots that each thread has at most kRopeShare heads and 16 vectors to copy (T = 16384, 24
+    // heads of 96, 48 turned: 35 us with heads alone counted, 28 so), and for few tokens more (down to one head a thread),
+    // until the grid holds about 512 threads per SM.
     const int units = p.rot / 16, most = kRopeThreads / units;
-    int64_t slots = (rot_heads + 2 * kRopeHeads - 1) / (2 * kRopeHeads);
+    int64_t slots = (rot_heads + kRopeShare - 1) / kRopeShare;
     const int copies = in == out ? 0 : (heads * p.dh - rot_heads * p.rot) / 8;
     if (slots * 16 * units < copies) slots = (copies + 16 * units - 1) / (16 * units);
     const int64_t fill = ((int64_t)L.num_sms * 512 + T * units - 1) / (T * units);
