@@ -727,6 +727,72 @@ __global__ void __launch_bounds__(1024) k_ce_finish(const float2* __restrict__ p
   loss[row] = y != ignore && in ? l - zy[row] : 0.0f;
 }
 
+// Few tokens and a small vocabulary: the logits themselves, [splits][T][V] in fp32, one part of K each (tok_logit_splits).
+__device__ __forceinline__ float ce_logit(const float* __restrict__ z, int splits, int64_t T, int64_t V, int64_t t, int64_t v) {
+  float sum = 0.0f;
+  for (int k = 0; k < splits; ++k) sum += z[(k * T + t) * V + v];
+  return sum;
+}
+// Forward: a block a token.
+__global__ void __launch_bounds__(1024) k_ce_logits_fwd(const float* __restrict__ z, int splits, int64_t T,
+                                                        const int64_t* __restrict__ targets, int64_t V, int64_t ignore,
+                                                        float* __restrict__ loss, float* __restrict__ lse, unsigned* status) {
+  __shared__ float2 sh[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = blockIdx.x;
+  wait_for_previous();
+  start_dependents();
+  float2 r = make_float2(-INFINITY, 0.0f);
+  for (int64_t v0 = threadIdx.x; v0 < V; v0 += 8 * 1024) {
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = v0 + 1024 * i < V ? ce_logit(z, splits, T, V, t, v0 + 1024 * i) : -INFINITY;
+    r = ce_join2(r, ce_pair(q));
+  }
+  auto join = [&]() {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float2 q = make_float2(__shfl_xor_sync(0xFFFFFFFFu, r.x, o), __shfl_xor_sync(0xFFFFFFFFu, r.y, o));
+      r = (lane & o) ? ce_join2(q, r) : ce_join2(r, q);
+    }
+  };
+  join();
+  if (lane == 0) sh[warp] = r;
+  __syncthreads();
+  if (warp != 0) return;
+  r = sh[lane];
+  join();
+  if (lane != 0) return;
+  const float l = kLn2 * (r.x + log2f(r.y));
+  lse[t] = l;
+  const int64_t y = targets[t];
+  const bool in = y >= 0 && y < V;
+  if (y != ignore && !in) atomicOr(status, kStatusBadTarget);
+  loss[t] = y != ignore && in ? l - ce_logit(z, splits, T, V, t, y) : 0.0f;
+}
+// Backward: G / s in `copies` parts (rows T .. pad - 1 zero), as kTokGrad stores it.
+__global__ void __launch_bounds__(256) k_ce_logits_grad(const float* __restrict__ z, int splits, int64_t T, int64_t V,
+                                                        const float4* __restrict__ rows, uint16_t* __restrict__ G,
+                                                        int64_t pitch, int64_t pad, int copies) {
+  wait_for_previous();
+  start_dependents();
+  const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
+  if (v >= V) return;
+  float q = 0.0f;
+  if (t < T) {
+    const float4 r = rows[t];
+    const int y = __float_as_int(r.z);
+    if (y >= 0) {
+      q = ce_exp2(fmaf(ce_logit(z, splits, T, V, t, v), kLog2e, -r.x));
+      if (y == v) q -= 1.0f;
+      q *= r.y;
+    }
+  }
+  const __nv_bfloat16 g = __float2bfloat16_rn(q);
+  G[t * pitch + v] = __bfloat16_as_ushort(g);
+  if (copies == 2) G[(pad + t) * pitch + v] = __bfloat16_as_ushort(__float2bfloat16_rn(q - __bfloat162float(g)));
+}
+
 // The largest |dloss| over the tokens that count (1 where that is 0 or not finite), valid in every thread.
 __device__ __forceinline__ float ce_block_scale(const float* __restrict__ dloss, const int64_t* __restrict__ targets,
                                                 int64_t T, int64_t V, int64_t ignore, unsigned* status, uint32_t* red) {
@@ -899,8 +965,28 @@ int tok_half_rows(int64_t V, const Launch& L) {
   return (int)(((V + 2 * pairs * waves - 1) / (2 * pairs * waves) + 7) / 8 * 8);
 }
 
+// Parts of K for the logits of few tokens, stored in fp32 and joined by another kernel; 0: in one launch (kTokLse, kTokGrad).
+// A block of 64 of K takes a pair 0.25 us whatever the tokens and rows (an MMA of 256 rows takes as long for 32 columns as for
+// 256), so where a small vocabulary has few tiles for the pairs, the pairs share K, in one wave.  Parts of at most 1024 of K
+// keep the forward's precision.  T = 5, d = 4656, V = 2476, forward 29 -> 21 us and backward 49 -> 39; T = 2, d = 4080, V = 1686
+// 27 -> 20 and 45 -> 33; T = 60, d = 3584, V = 4000 26 -> 22 and 49 -> 42 (in three waves T = 1, d = 5120, V = 9000 took 41 for 36).
+int tok_logit_splits(int64_t T, int64_t d, int64_t V) {
+  const int64_t tiles = (V + PM - 1) / PM, kb = (d + PK - 1) / PK;
+  if (T > kTokMax) return 0;
+  int best = 0;
+  double least = 0.25 * (double)kb - 2.0;  // one launch; the parts cost the backward a launch more
+  for (int64_t s = (kb + kSegBlocks - 1) / kSegBlocks; s <= kb && s <= 64 && tiles * s <= kPlanPairs; ++s) {
+    const int64_t each = (kb + s - 1) / s;
+    if (s < 2 || (kb + each - 1) / each != s) continue;
+    if (s * T * V * 4 > (32ll << 20)) break;
+    const double us = 0.25 * (double)each + 2.0 + (double)(s * T * V) * 8.0 / 3e6;
+    if (us < least) { best = (int)s; least = us; }
+  }
+  return best;
+}
+
 template <int A_MN, int B_MN, int MODE, int NT = 256>
-cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Launch& L) {
+cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Launch& L, bool dependent = true) {
   constexpr bool kTok = MODE >= kTokLse;
   a.M = (int)q.M;
   a.N = (int)q.N;
@@ -949,7 +1035,7 @@ cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Laun
     configured.fetch_or(1ull << dev);
   }
   const int pairs = pair_grid(L, a.num_tiles);
-  if constexpr (MODE == kPairLse || MODE == kTokLse) {  // comes first in its call
+  if (!dependent) {  // comes first in its call
     k_ce_gemm<A_MN, B_MN, MODE, NT><<<2 * pairs, kPairThreads, PairPlan<MODE, NT>::kSmem, L.stream>>>(ta, tb, tc, a);
     e = cudaGetLastError();
   } else {
@@ -973,6 +1059,7 @@ int64_t ce_piece(int64_t T, int64_t V) {
 struct CePlan {
   int64_t piece;
   int dx_splits, dw_splits;
+  int z_splits;  // of the logits' K, or 0
 };
 // Rows of G: its two parts of whole blocks of 32 tokens, or T.
 int64_t ce_g_rows(int64_t T) { return T <= kTwoParts ? 2 * ((T + 31) / 32 * 32) : T; }
@@ -982,13 +1069,14 @@ CePlan ce_plan(int64_t T, int64_t d, int64_t V) {
   const int64_t n = p.piece < V ? p.piece : V;
   p.dx_splits = T <= kTokMax ? pair_splits(d, ce_g_rows(T), n) : pair_splits(T, d, n);
   p.dw_splits = pair_splits(n, d, ce_g_rows(T));
+  p.z_splits = n == V ? tok_logit_splits(T, d, V) : 0;
   return p;
 }
 
 struct CeWs {
   float2* part;
   float4* rows;
-  float *zy, *acc, *dw_part, *scale;
+  float *zy, *acc, *dw_part, *scale, *z;
   uint16_t *G, *xz;
 };
 size_t ce_layout(int64_t T, int64_t d, int64_t V, bool bwd, uint8_t* base, CeWs* w) {
@@ -1011,12 +1099,27 @@ size_t ce_layout(int64_t T, int64_t d, int64_t V, bool bwd, uint8_t* base, CeWs*
     if (p.dw_splits > 1) t.dw_part = (float*)take(p.dw_splits * p.piece * d * 4);
     t.rows = (float4*)take(T * 16);
     t.scale = (float*)take(4);
+    if (p.z_splits) t.z = (float*)take(p.z_splits * T * V * 4);
+  } else if (const int z_splits = tok_logit_splits(T, d, V)) {
+    t.z = (float*)take(z_splits * T * V * 4);
   } else {
     t.part = (float2*)take(T <= kTokMax ? 2 * kPlanPairs * T * 8 : 2 * ((V + PN - 1) / PN) * T * 8);
     t.zy = (float*)take(T * 4);
   }
   if (w) *w = t;
   return off;
+}
+
+// The logits of few tokens, in parts of K.
+cudaError_t launch_tok_logits(const uint16_t* x, const uint16_t* W, int64_t T, int64_t d, int64_t V, int splits, float* z,
+                              const Launch& L, bool dependent) {
+  const PairProblem q{V, T, d, W, d, x, d, nullptr, 0};
+  PairArgs a{};
+  a.acc = z;
+  a.out = kOutF32Store;
+  return T <= 32   ? launch_pair<0, 0, kTokDx, 32>(q, splits, a, L, dependent)
+         : T <= 64 ? launch_pair<0, 0, kTokDx, 64>(q, splits, a, L, dependent)
+                   : launch_pair<0, 0, kTokDx, 128>(q, splits, a, L, dependent);
 }
 
 }  // namespace
@@ -1027,21 +1130,27 @@ cudaError_t launch_ce_fwd(const uint16_t* x, const uint16_t* W, const int64_t* t
                           int64_t ignore, float* loss, float* lse, void* ws, const Launch& L) {
   CeWs w;
   ce_layout(T, d, V, false, static_cast<uint8_t*>(ws), &w);
+  cudaError_t e;
+  if (const int splits = tok_logit_splits(T, d, V)) {
+    if ((e = launch_tok_logits(x, W, T, d, V, splits, w.z, L, false)) != cudaSuccess) return e;
+    e = launch_dependent(k_ce_logits_fwd, (unsigned)T, 1024, 0, L.stream, w.z, splits, T, targets, V, ignore, loss, lse, L.status);
+    if (L.launches) ++*L.launches;
+    return e;
+  }
   PairArgs a{};
   a.targets = targets;
   a.V = (int)V;
   a.part = w.part;
   a.zy = w.zy;
-  cudaError_t e;
   int pieces;
   if (T <= kTokMax) {
     const PairProblem q{V, T, d, W, d, x, d, nullptr, 0};
-    e = T <= 32 ? launch_pair<0, 0, kTokLse, 32>(q, 1, a, L)
-        : T <= 64 ? launch_pair<0, 0, kTokLse, 64>(q, 1, a, L) : launch_pair<0, 0, kTokLse, 128>(q, 1, a, L);
+    e = T <= 32 ? launch_pair<0, 0, kTokLse, 32>(q, 1, a, L, false)
+        : T <= 64 ? launch_pair<0, 0, kTokLse, 64>(q, 1, a, L, false) : launch_pair<0, 0, kTokLse, 128>(q, 1, a, L, false);
     const int half = tok_half_rows(V, L);
     pieces = 2 * pair_grid(L, (V + 2 * half - 1) / (2 * half));
   } else {
-    e = launch_pair<0, 0, kPairLse>(PairProblem{T, V, d, x, d, W, d, nullptr, 0}, 1, a, L);
+    e = launch_pair<0, 0, kPairLse>(PairProblem{T, V, d, x, d, W, d, nullptr, 0}, 1, a, L, false);
     pieces = (int)((V + 127) / 128);
   }
   if (e != cudaSuccess) return e;
@@ -1088,8 +1197,15 @@ cudaError_t launch_ce_bwd(const uint16_t* x, const uint16_t* W, const int64_t* t
       const PairProblem qx{d, g_rows, n, W + v0 * d, d, w.G, piece, nullptr, 0};
       a.rows_lo = copies == 2 ? (int)pad : 0;
       ax.out = first ? kOutF32Store : kOutF32Add;
-      e = T <= 32 ? launch_pair<0, 0, kTokGrad, 32>(q, 1, a, L)
-          : T <= 64 ? launch_pair<0, 0, kTokGrad, 64>(q, 1, a, L) : launch_pair<0, 0, kTokGrad, 128>(q, 1, a, L);
+      if (plan.z_splits) {
+        if ((e = launch_tok_logits(x, W, T, d, V, plan.z_splits, w.z, L, true)) != cudaSuccess) return e;
+        e = launch_dependent(k_ce_logits_grad, dim3((unsigned)((V + 255) / 256), (unsigned)pad), 256, 0, L.stream, w.z,
+                             plan.z_splits, T, V, w.rows, w.G, piece, pad, copies);
+        if (L.launches) ++*L.launches;
+      } else {
+        e = T <= 32   ? launch_pair<0, 0, kTokGrad, 32>(q, 1, a, L)
+            : T <= 64 ? launch_pair<0, 0, kTokGrad, 64>(q, 1, a, L) : launch_pair<0, 0, kTokGrad, 128>(q, 1, a, L);
+      }
       if (e != cudaSuccess) return e;
       e = T <= 32 ? launch_pair<1, 0, kTokDx, 64>(qx, xs, ax, L) : launch_pair<1, 0, kTokDx, 128>(qx, xs, ax, L);
       if (e != cudaSuccess) return e;

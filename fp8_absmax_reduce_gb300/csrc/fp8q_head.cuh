@@ -11,9 +11,9 @@ namespace fp8q {
 // complete and its writes are visible, before they touch global memory.  What it hides: the launch, and the
 // block's own preparation (barriers, tensor memory, descriptors), about 3 us between two short kernels.
 template <class... P, class... A>
-cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s, A... args) {
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3(grid);
+  c.gridDim = grid;
   c.blockDim = dim3((unsigned)threads);
   c.dynamicSmemBytes = smem;
   c.stream = s;

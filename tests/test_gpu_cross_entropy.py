@@ -286,3 +286,32 @@ def test_refusals():
         fq.linear_cross_entropy_fwd(x[:, :60].contiguous(), W[:, :60].contiguous(), t)
     with pytest.raises(fq.Fp8qError):
         fq.linear_cross_entropy_fwd(x[:0], W, t[:0])
+
+
+@pytest.mark.parametrize("T,d,V", [(1, 8192, 3000), (5, 4656, 2476), (33, 2048, 1000), (64, 1600, 301), (100, 2048, 257), (128, 4096, 700),
+                                   (3, 65536, 9)])
+def test_small_heads_of_few_tokens_whose_logits_come_in_parts(T, d, V):
+    x, W, t, dl = make(T, d, V, scale=0.02)
+    nan = t == IGN
+    xb, dlb = x.clone(), dl.clone()
+    xb[nan], dlb[nan] = float("nan"), float("nan")
+    nf, nb = fq.linear_cross_entropy_fwd_workspace_size(T, d, V), fq.linear_cross_entropy_bwd_workspace_size(T, d, V)
+    wf, wb = (torch.full((n + 4096,), 0xFF, dtype=torch.uint8, device="cuda") for n in (nf, nb))
+    gl, ge, gx = Guarded((T,), torch.float32), Guarded((T,), torch.float32), Guarded((T, d), torch.bfloat16)
+    fq.linear_cross_entropy_fwd(x, W, t, loss=gl.t, lse=ge.t, ws=wf)
+    check_fwd(x, W, t, gl.t, ge.t)
+    keep = ge.t.clone()
+    for dt in (torch.float32, torch.bfloat16):
+        gw = Guarded((V, d), dt)
+        fq.linear_cross_entropy_bwd(xb, W, t, keep, dlb, dX=gx.t, dW=gw.t, ws=wb)
+        torch.cuda.synchronize()
+        check_bwd(x, W, t, dl, gx.t, gw.t)
+        assert gw.intact()
+    assert all(v.intact() for v in (gl, ge, gx))
+    assert bool((wf[nf:] == 0xFF).all()) and bool((wb[nb:] == 0xFF).all())
+    bad = t.clone()
+    bad[0] = V
+    fq.get_status(clear=True)
+    again = fq.linear_cross_entropy_fwd(x, W, bad)
+    torch.cuda.synchronize()
+    assert fq.get_status(clear=True) == fq.STATUS_BAD_TARGET and float(again[0][0]) == 0.0 and torch.equal(again[1], keep)
