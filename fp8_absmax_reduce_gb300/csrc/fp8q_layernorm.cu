@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(ln_bwd_most(NP, STRIDE), (NP * VEC <= 8 ? kLnW
 // dg and db are added in shared memory at the end, so that the second launch reads one row an SM (four for the narrowest).
 // Against one block a row with a ring of bulk copies (as below), with dres: bf16 T = 8192, d = 3584: 48 -> 45 us; d = 5120:
 // 72 -> 62; T = 16384, d = 1024: 36 -> 29; T = 65536, d = 256: 45 -> 32; fp32 T = 16384, d = 512: 38 -> 28; T = 4096,
-// d = 4096: 56 -> 49; T = 1000, d = 1024: 13 -> 7.  Bound by memory: 0.80 of the measured copy rate at 8192 x 5120.
+// d = 4096: 56 -> 49; T = 1000, d = 1024: 13 -> 7.  Bound by memory: 0.84 of the measured copy rate at 8192 x 5120.
 template <int NP, int W>
 struct RunPlan {
   static constexpr int kPerSm = NP == 1 ? 4 : 1;
@@ -759,8 +759,7 @@ constexpr int bwd_threads(int d) {
   return ((d / 8 + bwd_np(d) - 1) / bwd_np(d) + 31) / 32 * 32;
 }
 // Resident blocks per SM: 1024 threads of 64 registers (up to 16 narrow blocks: a row is a chain of
-// dependent steps of about 0.8 us, so narrow rows need many blocks at work; T = 16384, d = 304: 15 us with 16), or
-// 512 of 128.
+// dependent steps of about 0.8 us, so narrow rows need many blocks at work), or 512 of 128.
 constexpr int bwd_per_sm(int d) {
   if (bwd_np(d) * (d % 8 == 0 ? 8 : 1) > 8) return 1;
   const int n = 1024 / bwd_threads(d);
