@@ -594,7 +594,7 @@ def _ce_sizes(x, W, targets):
 
 def linear_cross_entropy_fwd(x: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
                              loss=None, lse=None, ws=None, stream=None):
-    """Softmax cross entropy of the head z = x W^T, logits never kept: x [T,d] bf16, W [V,d] bf16,
+    """Softmax cross entropy of the head z = x W^T, its logits not returned or kept: x [T,d] bf16, W [V,d] bf16,
     targets [T] int64.  Returns (loss [T] fp32, 0 for ignored tokens; lse [T] fp32)."""
     T, d, V, dev = _ce_sizes(x, W, targets)
     device = x.device

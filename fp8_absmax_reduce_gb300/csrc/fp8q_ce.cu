@@ -6,6 +6,7 @@
 // the sum of exponentials below it; a second kernel joins them.  The backward walks the vocabulary
 // in pieces: the piece's logits again, turned into G in the epilogue, then its share of dX and its rows
 // of dW.  All products are bf16 on the tensor cores with fp32 sums, and bound by them.
+// (Up to 128 tokens with a small vocabulary, the logits do come to memory: in parts of K, see tok_logit_splits.)
 //
 // G is kept in bf16, the tensor cores' operand type, as G / s with s = max_t |dloss_t|: a mean's
 // one weight for all tokens then leaves no rounding of its own in G's large entries (p - 1 near -1).

@@ -556,7 +556,8 @@ FP8Q_API int layernorm_bwd(const void* dY, const void* x, fp8q_dtype dtype, cons
 /* (LLMQ §3: chunked logits).                                               */
 /* ------------------------------------------------------------------------ */
 /* x [T,d] bf16 (the last hidden states), W [V,d] bf16 (one row per vocabulary entry, as a tied
- * embedding has them), targets [T] int64.  With z = x W^T in fp32 (never stored in full):
+ * embedding has them), targets [T] int64.  With z = x W^T in fp32 (never stored in full, except up to 128 tokens with
+ * a vocabulary of a few thousand: at most 32 MB of the workspace then):
  *   lse [T] fp32:  lse_t = log sum_v e^{z_tv};
  *   loss [T] fp32: lse_t - z_{t,y} for the target y; 0 where targets[t] == ignore_index.
  * A target outside [0, V) that is not ignore_index sets FP8Q_STATUS_BAD_TARGET and is ignored.
