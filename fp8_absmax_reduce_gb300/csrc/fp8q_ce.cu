@@ -272,16 +272,18 @@ __device__ __forceinline__ void ce_tmem_add16(uint32_t taddr, float* z) {
   for (int j = 0; j < 16; ++j) z[j] += __uint_as_float(a[j]);
 }
 
-// The pair of N logits.
+// The pair of N logits.  Where all of them are -inf (masked columns; a mask of the type's lowest value gets there in
+// log2 units), their sum is 0: about a maximum of -inf it would be NaN, and reach the whole row.
 template <int N>
 __device__ __forceinline__ float2 ce_pair(const float (&z)[N]) {
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
   for (int j = 0; j < N; ++j) mx[j & 3] = fmaxf(mx[j & 3], z[j]);
   const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kLog2e;
+  const float about = m == -INFINITY ? 0.0f : m;
   float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int j = 0; j < N; ++j) sum[j & 3] += ce_exp2(fmaf(z[j], kLog2e, -m));
+  for (int j = 0; j < N; ++j) sum[j & 3] += ce_exp2(fmaf(z[j], kLog2e, -about));
   return make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
 }
 

@@ -561,6 +561,8 @@ FP8Q_API int layernorm_bwd(const void* dY, const void* x, fp8q_dtype dtype, cons
  *   lse [T] fp32:  lse_t = log sum_v e^{z_tv};
  *   loss [T] fp32: lse_t - z_{t,y} for the target y; 0 where targets[t] == ignore_index.
  * A target outside [0, V) that is not ignore_index sets FP8Q_STATUS_BAD_TARGET and is ignored.
+ * A logit of -Inf or below -2.3e38 (a vocabulary entry masked through its row of W) counts for nothing in
+ * lse, and its G is 0.
  * Backward: lse as the forward wrote it, dloss [T] fp32 the gradient at each token's loss (a mean:
  * 1 / the number of tokens that count; entries of ignored tokens are not used) ->
  *   G = dloss_t (e^{z - lse_t} - 1[v = y]), 0 in the rows of ignored tokens;

@@ -315,3 +315,26 @@ def test_small_heads_of_few_tokens_whose_logits_come_in_parts(T, d, V):
     again = fq.linear_cross_entropy_fwd(x, W, bad)
     torch.cuda.synchronize()
     assert fq.get_status(clear=True) == fq.STATUS_BAD_TARGET and float(again[0][0]) == 0.0 and torch.equal(again[1], keep)
+
+
+@pytest.mark.parametrize("mask", [float("-inf"), torch.finfo(torch.bfloat16).min])
+@pytest.mark.parametrize("T,d,V,lo,hi", [(1, 64, 25000, 1, 24999), (3, 4656, 2476, 128, 2400), (24, 64, 25000, 512, 20000),
+                                         (60, 64, 25000, 100, 24990), (100, 64, 25000, 512, 20000), (300, 64, 9000, 512, 7000),
+                                         (257, 2048, 8200, 1, 8200)])
+def test_masked_vocabulary_counts_for_nothing(T, d, V, lo, hi, mask):
+    """Columns lo .. hi - 1 masked through a constant feature, by -inf and by the type's lowest value: whole tiles hold nothing
+    else, and the loss and the gradients are those of the head without these rows."""
+    x, W, t, dl = make(T, d, V, ignored=0.1)
+    x[:, 0], W[:, 0] = 1.0, 0.0
+    t[t != IGN] %= lo
+    W[lo:hi] = 0.0
+    W[lo:hi, 0] = mask
+    kept = torch.cat([W[:lo], W[hi:]])
+    loss, lse = fq.linear_cross_entropy_fwd(x, W, t)
+    assert bool(torch.isfinite(lse).all())
+    check_fwd(x, kept, t, loss, lse)
+    dX, dW = fq.linear_cross_entropy_bwd(x, W, t, lse, dl)
+    assert bool((dW[lo:hi] == 0).all())
+    if mask == float("-inf"):
+        dX[:, 0] = 0.0  # 0 times -inf there, in the definition too
+    check_bwd(x, kept, t, dl, dX, torch.cat([dW[:lo], dW[hi:]]))
