@@ -70,6 +70,8 @@ __device__ __forceinline__ float mul(float a, float b) { return a * b; }
 __device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
 __device__ __forceinline__ float sum(float2 v) { return v.x + v.y; }
 __device__ __forceinline__ float sum(float v) { return v; }
+__device__ __forceinline__ float first_of(float2 v) { return v.x; }
+__device__ __forceinline__ float first_of(float v) { return v; }
 __device__ __forceinline__ void fill(float2& v, float f) { v = make_float2(f, f); }
 __device__ __forceinline__ void fill(float& v, float f) { v = f; }
 template <int VEC>
@@ -132,9 +134,16 @@ __device__ __forceinline__ void ln_copy(uint8_t* dst, const void* src, int64_t o
 // Forward: W warps hold RT rows at once in registers, NP pieces of each row a lane (piece k of lane l of warp w
 // is piece (k W + w) 32 + l); a block of 8 warps (W where that is no divisor of 8) takes kRows consecutive rows at a time (one slot of the
 // ring, one copy) and walks them with the grid's stride.  Each warp takes the mean and the sum of
-// squares about it of its own elements, in two passes over its registers; the warps' (mean, M2) pairs are then joined,
-// mean = sum n_w mean_w / d and M2 = sum (M2_w + n_w (mean_w - mean)^2), so a row costs one block barrier and
-// nothing cancels.  bf16 rows go two at a time (RT = 2): what bounds them is instructions, and the
+// squares about it of its own elements, in two passes over its registers; the warps' (mean, M2) pairs are then joined about
+// the first one's mean m_0, mean = m_0 + sum n_w (m_w - m_0) / d and M2 = sum (M2_w + n_w (m_w - mean)^2), so a row costs one
+// block barrier and nothing cancels.  A row of equal values has to end with M2 = 0, whatever the value: a mean one step off
+// would make a variance of (2^-24 x)^2, which passes eps from |x| = 5e4 on.  So where a warp's first element is as near to its
+// mean as the mean's own roundings (kNear), it is the centre.  In bf16 sums of equal values are exact (8 + 14 bits) and the
+// division's two roundings are left; other rows come that near only by a mean that is the element, or beside elements half as
+// large as the mean or more away from it (bf16 steps are 2^-8), whose deviation is 2^14 times the difference or more.  In
+// fp32 the sum has up to 32 roundings and other rows' elements are as near, so the second pass also adds up x - centre, which
+// corrects the mean and M2.  (T = 16384, d = 5120 61.4 -> 62.6 us cold, d = 2560 32.8 -> 34.4; fp32 8192 x 4096 equal.)
+// bf16 rows go two at a time (RT = 2): what bounds them is instructions, and the
 // second row shares the unpacking of gain and bias and the exchanges (T = 16384, d = 5120: 66 -> 60 us).
 // ---------------------------------------------------------------------------
 constexpr int ln_fwd_threads(int W) { return 8 % W == 0 ? 256 : 32 * W; }
@@ -164,6 +173,7 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(VEC, W))
   using E = typename Unit<VEC>::T;
   constexpr int kUnits = Unit<VEC>::kCount, ES = F32 ? 4 : 2;
   constexpr int kRows = 8 % W == 0 ? RT * (8 / W) : RT;
+  constexpr float kNear = F32 ? 0x1p-19f : 0x1p-22f;
   static_assert(RT == 1 || W <= 16, "two rows join in the warp's halves");
   constexpr int kJoin = W <= 1 ? 1 : W <= 2 ? 2 : W <= 4 ? 4 : W <= 8 ? 8 : W <= 16 ? 16 : 32;  // lanes that join W pairs
   extern __shared__ __align__(128) uint8_t ln_rows[];
@@ -195,8 +205,7 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(VEC, W))
     for (int k = 0; k < NP; ++k) n += min(32, max(0, pieces - (k * W + w) * 32));
     return n * VEC;
   };
-  const int n_own = count(warp);
-  const float inv_own = n_own ? 1.0f / (float)n_own : 0.0f, inv_d = 1.0f / (float)d;
+  const float inv_own = 1.0f / (float)count(warp), inv_d = 1.0f / (float)d;  // every warp has a piece
   const int of_warp = lane & (kJoin - 1);
   const float lane_count = of_warp < W ? (float)count(of_warp) : 0.0f, lane_share = lane_count * inv_d;
   Piece<F32, VEC> pg[NP], pb[NP];
@@ -241,8 +250,11 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(VEC, W))
     ln_warp_sums<RT>(own_mu, lane);
 #pragma unroll
     for (int q = 0; q < RT; ++q) {
-      mu[q] = own_mu[q] = own_mu[q] * inv_own;
-      E sq = all<VEC>(0.0f);
+      const float x0 = __shfl_sync(0xFFFFFFFFu, first_of(c[q][0][0]), 0);
+      own_mu[q] *= inv_own;
+      if (fabsf(x0 - own_mu[q]) < kNear * fabsf(own_mu[q])) own_mu[q] = x0;
+      mu[q] = own_mu[q];
+      E sq = all<VEC>(0.0f), off = all<VEC>(0.0f);
 #pragma unroll
       for (int k = 0; k < NP; ++k)
         if ((k * W + warp) * 32 + lane < pieces)
@@ -250,10 +262,18 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(VEC, W))
           for (int e = 0; e < kUnits; ++e) {
             c[q][k][e] = add(c[q][k][e], all<VEC>(-own_mu[q]));
             sq = fma(c[q][k][e], c[q][k][e], sq);
+            if (F32) off = add(off, c[q][k][e]);
           }
       m2[q] = sum(sq);
+      if (F32) {
+        const float both = ln_warp_sum2(m2[q], sum(off), lane);
+        const float s1 = __shfl_sync(0xFFFFFFFFu, both, 16), more = s1 * inv_own;
+        mu[q] += more;
+        m2[q] = fmaf(-s1, more, __shfl_sync(0xFFFFFFFFu, both, 0));
+        if (m2[q] < 0.0f) m2[q] = 0.0f;  // (a NaN stays)
+      }
     }
-    ln_warp_sums<RT>(m2, lane);
+    if (!F32) ln_warp_sums<RT>(m2, lane);
     if (W > 1 && lane == 0)
 #pragma unroll
       for (int q = 0; q < RT; ++q) pairs[turn][r + q][warp] = make_float2(mu[q], m2[q]);
@@ -266,14 +286,18 @@ __global__ void __launch_bounds__(ln_fwd_threads(W), ln_fwd_per_sm(VEC, W))
     if (W > 1) {
       // lanes 0-15 join the first row's pairs, 16-31 the second's
       float2 of = make_float2(0.0f, 0.0f);
-      if (of_warp < W) of = pairs[turn][r + (RT == 2 ? lane >> 4 : 0)][of_warp];
+      const auto& row_pairs = pairs[turn][r + (RT == 2 ? lane >> 4 : 0)];
+      const float m0 = row_pairs[0].x;
+      if (of_warp < W) of = row_pairs[of_warp];
+      of.x = of_warp < W ? of.x - m0 : 0.0f;
       float m = of.x * lane_share;
 #pragma unroll
       for (int o = kJoin / 2; o > 0; o >>= 1) m += __shfl_xor_sync(0xFFFFFFFFu, m, o);
-      const float off = of.x - m;
+      const float off = of_warp < W ? of.x - m : 0.0f;  // (lanes past W count for nothing, even where m m overflows)
       float v = fmaf(off * off, lane_count, of.y);
 #pragma unroll
       for (int o = kJoin / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+      m += m0;
 #pragma unroll
       for (int q = 0; q < RT; ++q) {
         mu[q] = RT == 1 ? m : __shfl_sync(0xFFFFFFFFu, m, 16 * q);

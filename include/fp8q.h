@@ -534,7 +534,8 @@ FP8Q_API int rope_bwd(const void* d_out, fp8q_dtype dtype, int64_t T, int n_head
 /* x [T,d], g [d], b [d] (all bf16 or all fp32; b may be NULL) -> y [T,d] of the same type,
  * mean [T] and rstd [T] fp32 (kept for the backward):
  *   mean = (1/d) sum x, rstd = 1 / sqrt((1/d) sum (x - mean)^2 + eps), y = (x - mean) rstd g + b.
- * A row of equal values has variance 0 (rstd = eps^-1/2; eps = 0 then gives Inf and NaN).
+ * A row of equal values has variance 0 (rstd = eps^-1/2; eps = 0 then gives Inf and NaN).  Sums are fp32: a row whose
+ * sum, or whose sum of squares about the mean, passes fp32's range may give 0, Inf or NaN.
  * y may be x itself.
  * Backward: dY [T,d], x, g and the forward's mean and rstd, dres [T,d] optional (the residual branch's
  * gradient, as rmsnorm_bwd's dY) -> dX [T,d], dg [d] fp32 and, unless db is NULL, db [d] fp32:

@@ -159,3 +159,36 @@ def test_refusals():
         fq.layernorm_fwd(t["x"][:0], t["g"])
     with pytest.raises(fq.Fp8qError):
         fq.layernorm_fwd(t["x"].view(-1)[1:65].view(1, 64), t["g"])  # two bytes off a 16-byte boundary
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [1, 7, 72, 257, 768, 1000, 1409, 2048, 2056, 2560, 3584, 4104, 5120, 5552, 8192, 10007, 16384])
+def test_rows_of_equal_values_have_variance_zero(d, dtype):
+    """Whatever the value (sums within fp32's range) and the width: mean is the value, y is the bias, and rstd is eps^-1/2 to
+    the reciprocal square root's 2 steps and the rounding of eps."""
+    values = torch.tensor([0.0, 3.0, 0.1, -1000.3, 1e4 / 3, 123456.7, 1e20, -1.37e20, 3e33, -1e-30, 2e-38]).to(dtype).cuda()
+    x = values[:, None].expand(-1, d).contiguous()
+    t = make(len(values), d, dtype)
+    for eps in (1e-5, 1e-12):
+        y, mean, rstd = fq.layernorm_fwd(x, t["g"], t["b"], eps=eps)
+        assert torch.equal(mean, values.float())
+        assert torch.equal(y, t["b"].expand(len(values), d))
+        assert float((rstd.double() * eps ** 0.5 - 1).abs().max()) <= 5 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("d", [72, 257, 1000, 2056, 5120, 10007])
+def test_fp32_rows_far_from_zero(d):
+    """Deviations of a hundred of the values' steps.  A warp's mean is rounded once, and so is the row's, so the mean is within
+    two roundings (and 1e-5 of that for its correction).  The row's variance takes the warps' means with an error of e_m at
+    most: 2 e_m sigma + e_m^2, so rstd is within e_m / sigma (1 + e_m / 2 sigma) beside the sums' own 1e-5.  y is off by the
+    mean's error and four roundings of its own."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    x = (torch.randn(64, 1, generator=g, device="cuda") * 1e4 + 3e4) * (1 + 1e-5 * torch.randn(64, d, generator=g, device="cuda"))
+    one = torch.ones(d, device="cuda")
+    y, mean, rstd = fq.layernorm_fwd(x, one, eps=1e-12)
+    wy, wm, wr = ref.layernorm(x.double(), one.double(), None, 1e-12)
+    em = 2.001 * 2.0 ** -24 * wm.abs()
+    assert bool(((mean.double() - wm).abs() <= em).all())
+    rel = 1e-5 + em * wr * (1 + em * wr)
+    assert bool(((rstd.double() - wr).abs() <= wr * rel).all())
+    assert bool(((y.double() - wy).abs() <= (em * wr)[:, None] + wy.abs() * (rel[:, None] + 2.0 ** -22)).all())
