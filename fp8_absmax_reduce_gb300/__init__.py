@@ -5,6 +5,10 @@ Every function here only marshals torch tensors (device memory, the current
 stream) into the C calls; all arithmetic runs in the library's CUDA kernels.
 There is no CPU fallback: without the built library, the first call raises.
 
+``stream=`` launches a call on that stream instead of the current one.  What the call allocates itself (its
+workspace, outputs that are not given) is then that stream's memory, so neither stream's allocator hands it out
+while the other still uses it; that the inputs are ready there, and the outputs waited for, is the caller's to order.
+
 Build the library with ``python -m fp8_absmax_reduce_gb300.build``.
 """
 
@@ -191,14 +195,37 @@ def _check(name: str, rc: int):
         raise Fp8qError(f"{name}: {lib.fp8q_status_string(rc).decode()} (status {rc})")
 
 
-def _ws(nbytes: int, device, ws=None):
+def _foreign(stream, dev: int) -> bool:
+    """Whether the call runs on another stream than the current one of CUDA device dev."""
+    return stream is not None and stream.cuda_stream != torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _empty(shape, dtype, device, stream):
+    """An output of a call on `stream`, for which the current stream may wait and which it may use too."""
+    if stream is None or not _foreign(stream, device.index):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _empty_ws(nbytes: int, device, stream):
+    """A workspace that is dropped when the call has been launched: memory of the stream it runs on."""
+    if stream is None or not _foreign(stream, device.index):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _ws(nbytes: int, device, ws=None, stream=None):
     if nbytes == 0:
         return None
     if ws is not None:
         if ws.numel() * ws.element_size() < nbytes:
             raise ValueError("workspace too small")
         return ws
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _empty_ws(nbytes, device, stream)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -219,10 +246,10 @@ def _dev(t: torch.Tensor):
 def fp8_quantize_absmax(x: torch.Tensor, fmt: int = E4M3, q=None, scal=None, ws=None, stream=None):
     """Per-tensor absmax quantization. Returns (codes uint8 like x, scal float32[3] = amax, scale, scale_inv)."""
     dev = _dev(x)
-    q = torch.empty(x.shape, dtype=torch.uint8, device=dev) if q is None else q
-    scal = torch.empty(3, dtype=torch.float32, device=dev) if scal is None else scal
+    q = _empty(x.shape, torch.uint8, dev, stream) if q is None else q
+    scal = _empty(3, torch.float32, dev, stream) if scal is None else scal
     nb = lib.fp8_quantize_absmax_workspace_size(x.numel())
-    w = _ws(nb, dev, ws)
+    w = _ws(nb, dev, ws, stream)
     _check("fp8_quantize_absmax", lib.fp8_quantize_absmax(_ptr(x), _dtype_code(x), x.numel(), fmt, _ptr(q),
                                                           _ptr(scal), _ptr(w), nb, _stream(stream)))
     return q, scal
@@ -241,7 +268,7 @@ def fp8_gemm_scaled(layout: int, A: torch.Tensor, fmtA: int, B: torch.Tensor, fm
     N = B.shape[0] if layout == NT else B.shape[1]
     lda, ldb = A.shape[1], B.shape[1]
     out_code = {torch.bfloat16: BF16, torch.float32: F32}[out_dtype]
-    C = torch.empty((M, N), dtype=out_dtype, device=dev) if C is None else C
+    C = _empty((M, N), out_dtype, dev, stream) if C is None else C
     ldr = residual.shape[1] if residual is not None else 0
     _check("fp8_gemm_scaled", lib.fp8_gemm_scaled(layout, M, N, K, _ptr(A), fmtA, lda, _ptr(B), fmtB, ldb,
                                                   _ptr(sinvA), _ptr(sinvB), _ptr(C), out_code, C.shape[1],
@@ -260,10 +287,10 @@ def mx_quantize(x: torch.Tensor, fmt: int = E4M3, rows: bool = True, cols: bool 
     GEMM contracting over C) and down each column (contracting over R), scales in the chunked layout."""
     dev = _dev(x)
     R, C = x.shape
-    r = (torch.empty((R, C), dtype=torch.uint8, device=dev),
-         torch.empty(mx_scale_bytes(R, C), dtype=torch.uint8, device=dev)) if rows else None
-    c = (torch.empty((R, C), dtype=torch.uint8, device=dev),
-         torch.empty(mx_scale_bytes(C, R), dtype=torch.uint8, device=dev)) if cols else None
+    r = (_empty((R, C), torch.uint8, dev, stream),
+         _empty(mx_scale_bytes(R, C), torch.uint8, dev, stream)) if rows else None
+    c = (_empty((R, C), torch.uint8, dev, stream),
+         _empty(mx_scale_bytes(C, R), torch.uint8, dev, stream)) if cols else None
     _check("mx_quantize", lib.mx_quantize(_ptr(x), _dtype_code(x), R, C, fmt, _ptr(r[0]) if r else None,
                                           _ptr(r[1]) if r else None, _ptr(c[0]) if c else None,
                                           _ptr(c[1]) if c else None, _stream(stream)))
@@ -282,7 +309,7 @@ def fp8_gemm_mx(layout: int, A: torch.Tensor, fmtA: int, sfA: torch.Tensor, B: t
         M, K = A.shape
     N = B.shape[0] if layout == NT else B.shape[1]
     out_code = {torch.bfloat16: BF16, torch.float32: F32}[out_dtype]
-    C = torch.empty((M, N), dtype=out_dtype, device=dev) if C is None else C
+    C = _empty((M, N), out_dtype, dev, stream) if C is None else C
     ldr = residual.shape[1] if residual is not None else 0
     _check("fp8_gemm_mx", lib.fp8_gemm_mx(layout, M, N, K, _ptr(A), fmtA, A.shape[1], _ptr(sfA), _ptr(B), fmtB,
                                           B.shape[1], _ptr(sfB), _ptr(C), out_code, C.shape[1], _ptr(residual), ldr,
@@ -295,11 +322,11 @@ def rmsnorm_quant(x: torch.Tensor, g: torch.Tensor, eps: float = 1e-6, q=None, s
     """RMSNorm + E4M3 quantization. Returns (codes [T,d], scal[3], rstd[T])."""
     dev = _dev(x)
     T, d = x.shape
-    q = torch.empty((T, d), dtype=torch.uint8, device=dev) if q is None else q
-    scal = torch.empty(3, dtype=torch.float32, device=dev) if scal is None else scal
-    rstd = torch.empty(T, dtype=torch.float32, device=dev) if rstd is None else rstd
+    q = _empty((T, d), torch.uint8, dev, stream) if q is None else q
+    scal = _empty(3, torch.float32, dev, stream) if scal is None else scal
+    rstd = _empty(T, torch.float32, dev, stream) if rstd is None else rstd
     nb = lib.rmsnorm_quant_workspace_size(T, d)
-    w = _ws(nb, dev, ws)
+    w = _ws(nb, dev, ws, stream)
     _check("rmsnorm_quant", lib.rmsnorm_quant(_ptr(x), _ptr(g), T, d, eps, _ptr(q), _ptr(scal), _ptr(rstd),
                                               _ptr(w), nb, _stream(stream)))
     return q, scal, rstd
@@ -308,10 +335,10 @@ def rmsnorm_quant(x: torch.Tensor, g: torch.Tensor, eps: float = 1e-6, q=None, s
 def _rmsnorm_bwd_call(name, dN, x, dY, g, rstd, dX, dg, ws, stream, *limit):
     dev = _dev(x)
     T, d = x.shape
-    dX = torch.empty((T, d), dtype=torch.bfloat16, device=dev) if dX is None else dX
-    dg = torch.empty(d, dtype=torch.float32, device=dev) if dg is None else dg
+    dX = _empty((T, d), torch.bfloat16, dev, stream) if dX is None else dX
+    dg = _empty(d, torch.float32, dev, stream) if dg is None else dg
     nb = lib.rmsnorm_bwd_workspace_size(T, d)
-    w = _ws(nb, dev, ws)
+    w = _ws(nb, dev, ws, stream)
     _check(name, getattr(lib, name)(_ptr(dN), _ptr(x), _ptr(dY), _ptr(g), _ptr(rstd), T, d, _ptr(dX), _ptr(dg),
                                     _ptr(w), nb, *limit, _stream(stream)))
     return dX, dg
@@ -336,10 +363,10 @@ def swiglu_quant(H: torch.Tensor, fmt: int = E4M3, q=None, scal=None, ws=None, s
     dev = _dev(H)
     T, f2 = H.shape
     f = f2 // 2
-    q = torch.empty((T, f), dtype=torch.uint8, device=dev) if q is None else q
-    scal = torch.empty(3, dtype=torch.float32, device=dev) if scal is None else scal
+    q = _empty((T, f), torch.uint8, dev, stream) if q is None else q
+    scal = _empty(3, torch.float32, dev, stream) if scal is None else scal
     nb = lib.swiglu_quant_workspace_size(T, f)
-    w = _ws(nb, dev, ws)
+    w = _ws(nb, dev, ws, stream)
     _check("swiglu_quant", lib.swiglu_quant(_ptr(H), T, f, fmt, _ptr(q), _ptr(scal), _ptr(w), nb, _stream(stream)))
     return q, scal
 
@@ -350,8 +377,8 @@ def attention_fwd(qkv: torch.Tensor, seq_len: int, n_heads: int, n_kv_heads: int
     Returns (att [T, n_heads 128] bf16, lse [n_heads, T] fp32)."""
     dev = _dev(qkv)
     T = qkv.shape[0]
-    att = torch.empty((T, n_heads * 128), dtype=torch.bfloat16, device=dev) if att is None else att
-    lse = torch.empty((n_heads, T), dtype=torch.float32, device=dev) if lse is None else lse
+    att = _empty((T, n_heads * 128), torch.bfloat16, dev, stream) if att is None else att
+    lse = _empty((n_heads, T), torch.float32, dev, stream) if lse is None else lse
     _check("attention_fwd", lib.attention_fwd(_ptr(qkv), T, seq_len, n_heads, n_kv_heads, 128, _ptr(att), _ptr(lse),
                                               _stream(stream)))
     return att, lse
@@ -362,9 +389,9 @@ def attention_bwd(qkv: torch.Tensor, att: torch.Tensor, lse: torch.Tensor, d_att
     """Input gradient dqkv [T, (n_heads + 2 n_kv_heads) 128] (bf16) of attention_fwd for d_att."""
     dev = _dev(qkv)
     T = qkv.shape[0]
-    dqkv = torch.empty_like(qkv) if dqkv is None else dqkv
+    dqkv = _empty(qkv.shape, qkv.dtype, dev, stream) if dqkv is None else dqkv
     nb = lib.attention_bwd_workspace_size(T, n_heads)
-    w = _ws(nb, dev, ws)
+    w = _ws(nb, dev, ws, stream)
     _check("attention_bwd", lib.attention_bwd(_ptr(qkv), _ptr(att), _ptr(lse), _ptr(d_att), T, seq_len, n_heads,
                                               n_kv_heads, 128, _ptr(dqkv), _ptr(w), nb, _stream(stream)))
     return dqkv
@@ -418,18 +445,18 @@ def _matrix(name: str, t, types=_REAL):
     return shape, dev
 
 
-def _out(name: str, t, dtype, shape, dev: int, device):
+def _out(name: str, t, dtype, shape, dev: int, device, stream):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device) if stream is None else _empty(shape, dtype, device, stream)
     if not _fits(t, dtype, shape, dev):
         _refuse(name, t, dtype, shape, dev)
     return t
 
 
-def _scratch(nbytes: int, dev: int, device, ws):
+def _scratch(nbytes: int, dev: int, device, ws, stream):
     """The caller's workspace, or a new one."""
     if ws is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return _empty_ws(nbytes, device, stream)
     if ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("the workspace must be a contiguous tensor on the inputs' device")
     if ws.nbytes < nbytes:
@@ -503,7 +530,7 @@ def _rope_call(name, fn, qkv, pos, rope, n_heads, n_kv_heads, out, stream):
         raise ValueError(f"qkv has {width} columns, not ({n_heads} + 2 * {n_kv_heads}) heads of {rope.head_dim}")
     _need("pos", pos, torch.int32, (T,) if rope.n_axes == 1 and getattr(pos, "ndim", 0) == 1 else (rope.n_axes, T), dev)
     if out is None:
-        out = torch.empty_like(qkv)
+        out = _empty((T, width), dtype, qkv.device, stream)
     elif out is not qkv:
         _need("out", out, dtype, (T, width), dev)
     _check(name, fn(qkv.data_ptr(), BF16 if dtype is torch.bfloat16 else F32, T, n_heads, n_kv_heads, rope._ref,
@@ -534,9 +561,9 @@ def layernorm_fwd(x: torch.Tensor, g: torch.Tensor, b: torch.Tensor | None = Non
     _need("g", g, dtype, (d,), dev)
     if b is not None:
         _need("b", b, dtype, (d,), dev)
-    y = torch.empty_like(x) if y is None else _out("y", y, dtype, shape, dev, device)
-    mean = _out("mean", mean, torch.float32, (T,), dev, device)
-    rstd = _out("rstd", rstd, torch.float32, (T,), dev, device)
+    y = _out("y", y, dtype, shape, dev, device, stream)
+    mean = _out("mean", mean, torch.float32, (T,), dev, device, stream)
+    rstd = _out("rstd", rstd, torch.float32, (T,), dev, device, stream)
     _check("layernorm_fwd", lib.layernorm_fwd(x.data_ptr(), BF16 if dtype is torch.bfloat16 else F32, g.data_ptr(),
                                               None if b is None else b.data_ptr(), T, d, eps, y.data_ptr(),
                                               mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, dev)))
@@ -560,11 +587,11 @@ def layernorm_bwd(dY: torch.Tensor, x: torch.Tensor, g: torch.Tensor, mean: torc
     _need("rstd", rstd, torch.float32, (T,), dev)
     if dres is not None:
         _need("dres", dres, dtype, shape, dev)
-    dX = torch.empty_like(x) if dX is None else _out("dX", dX, dtype, shape, dev, device)
-    dg = _out("dg", dg, torch.float32, (d,), dev, device)
-    db = _out("db", db, torch.float32, (d,), dev, device)
+    dX = _out("dX", dX, dtype, shape, dev, device, stream)
+    dg = _out("dg", dg, torch.float32, (d,), dev, device, stream)
+    db = _out("db", db, torch.float32, (d,), dev, device, stream)
     nb = lib.layernorm_bwd_workspace_size(T, d)
-    w = _scratch(nb, dev, device, ws)
+    w = _scratch(nb, dev, device, ws, stream)
     _check("layernorm_bwd", lib.layernorm_bwd(dY.data_ptr(), x.data_ptr(), BF16 if dtype is torch.bfloat16 else F32,
                                               g.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
                                               None if dres is None else dres.data_ptr(), T, d, dX.data_ptr(),
@@ -598,10 +625,10 @@ def linear_cross_entropy_fwd(x: torch.Tensor, W: torch.Tensor, targets: torch.Te
     targets [T] int64.  Returns (loss [T] fp32, 0 for ignored tokens; lse [T] fp32)."""
     T, d, V, dev = _ce_sizes(x, W, targets)
     device = x.device
-    loss = _out("loss", loss, torch.float32, (T,), dev, device)
-    lse = _out("lse", lse, torch.float32, (T,), dev, device)
+    loss = _out("loss", loss, torch.float32, (T,), dev, device, stream)
+    lse = _out("lse", lse, torch.float32, (T,), dev, device, stream)
     nb = lib.linear_cross_entropy_fwd_workspace_size(T, d, V)
-    w = _scratch(nb, dev, device, ws)
+    w = _scratch(nb, dev, device, ws, stream)
     _check("linear_cross_entropy_fwd",
            lib.linear_cross_entropy_fwd(x.data_ptr(), W.data_ptr(), targets.data_ptr(), T, d, V, ignore_index,
                                         loss.data_ptr(), lse.data_ptr(), w.data_ptr(), nb, _raw_stream(stream, dev)))
@@ -618,15 +645,15 @@ def linear_cross_entropy_bwd(x: torch.Tensor, W: torch.Tensor, targets: torch.Te
     device = x.device
     _need("lse", lse, torch.float32, (T,), dev)
     _need("dloss", dloss, torch.float32, (T,), dev)
-    dX = torch.empty_like(x) if dX is None else _out("dX", dX, torch.bfloat16, (T, d), dev, device)
+    dX = _out("dX", dX, torch.bfloat16, (T, d), dev, device, stream)
     if dW is None:
         if dw_dtype not in _REAL:
             raise TypeError(f"dw_dtype {dw_dtype}: bfloat16 or float32")
-        dW = torch.empty((V, d), dtype=dw_dtype, device=device)
+        dW = _empty((V, d), dw_dtype, device, stream)
     else:
         _need("dW", dW, torch.bfloat16 if getattr(dW, "dtype", None) is torch.bfloat16 else torch.float32, (V, d), dev)
     nb = lib.linear_cross_entropy_bwd_workspace_size(T, d, V)
-    w = _scratch(nb, dev, device, ws)
+    w = _scratch(nb, dev, device, ws, stream)
     _check("linear_cross_entropy_bwd",
            lib.linear_cross_entropy_bwd(x.data_ptr(), W.data_ptr(), targets.data_ptr(), lse.data_ptr(),
                                         dloss.data_ptr(), T, d, V, ignore_index, dX.data_ptr(), dW.data_ptr(),
@@ -912,7 +939,7 @@ def selftest_gemm_wait_limit(layout: int, A: torch.Tensor, fmtA: int, B: torch.T
         M, K = A.shape
     N = B.shape[0] if layout == NT else B.shape[1]
     out_code = {torch.bfloat16: BF16, torch.float32: F32}[out_dtype]
-    C = torch.empty((M, N), dtype=out_dtype, device=dev) if C is None else C
+    C = _empty((M, N), out_dtype, dev, stream) if C is None else C
     mx = sfA is not None
     _check("fp8q_selftest_gemm_wait_limit",
            lib.fp8q_selftest_gemm_wait_limit(layout, M, N, K, _ptr(A), fmtA, A.shape[1], _ptr(B), fmtB, B.shape[1],
