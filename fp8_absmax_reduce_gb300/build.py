@@ -22,7 +22,7 @@ OBJ_DIR = os.path.join(OUT_DIR, "obj")
 LIB = os.path.join(OUT_DIR, "libfp8q.so")
 SOURCES = ["fp8q_api.cu", "fp8q_quant.cu", "fp8q_gemm.cu", "fp8q_attn.cu", "fp8q_noalloc.cu", "fp8q_mx.cu",
            "fp8q_layernorm.cu", "fp8q_rope.cu", "fp8q_ce.cu"]
-HEADERS = ["fp8q_common.cuh", "fp8q_internal.h", "fp8q_head.cuh"]
+HEADERS = ["fp8q_common.cuh", "fp8q_internal.h", "fp8q_head.cuh", "fp8q_turn.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -3,6 +3,7 @@
 // MLP block.  Every call only enqueues kernels on the caller's stream.
 #include "fp8q.h"
 #include "fp8q_internal.h"
+#include "fp8q_turn.h"
 
 #include <cmath>
 #include <mutex>
@@ -1483,10 +1484,8 @@ int rope_run(const void* qkv, fp8q_dtype dtype, int64_t T, int n_heads, int n_kv
   p.rot = r->rot_dim;
   p.interleaved = r->interleaved != 0;
   for (int i = 0; i < r->rot_dim / 2; ++i) {
-    const double f = r->inv_freq[i] / 6.283185307179586476925;
-    if (!std::isfinite(f) || r->axis[i] >= r->n_axes) return FP8Q_ERR_INVALID_ARG;
-    // the fraction of a turn per position in 0.64 fixed point (at most 1 - 2^-53, so it fits)
-    p.turn[i] = (uint64_t)((f - std::floor(f)) * 18446744073709551616.0);
+    if (!std::isfinite(r->inv_freq[i]) || r->axis[i] >= r->n_axes) return FP8Q_ERR_INVALID_ARG;
+    p.turn[i] = rope_turn(r->inv_freq[i]);
     p.axis[i] = r->axis[i];
   }
   Ctx c;

@@ -3,8 +3,8 @@
 // Pair i of a rotated head turns by the angle pos[axis(i)] freq(i).  The angle is kept as a phase in
 // turns, a 64-bit fixed-point fraction: F = round(freq / (2 pi) 2^64) wraps modulo one turn, so
 // pos * F modulo 2^64 is the phase's fraction for any 32-bit position (negative ones too), off by at
-// most |pos| 2^-65 turns: no floating-point range reduction, and far positions lose nothing.  The
-// top 32 bits, as a signed number of half-turns, go to sincospif.
+// most |pos| 2^-65 turns: no floating-point range reduction, and far positions lose nothing.  As a
+// signed number of half-turns, rounded to fp32 from all 64 bits (small angles keep their digits), it goes to sincospif.
 //
 // Bound by memory: every element is read and written once (in place: the rotated heads alone).  A
 // thread keeps the sines and cosines of 8 pairs of one token in registers and applies them to its
@@ -19,7 +19,7 @@ namespace {
 
 __device__ __forceinline__ void rope_sincos(int32_t pos, uint64_t F, float sign, float& s, float& c) {
   const uint64_t phase = (uint64_t)(int64_t)pos * F;
-  const float half_turns = (float)(int32_t)(phase >> 32) * 4.656612873077392578125e-10f;  // 2^-31
+  const float half_turns = (float)(int64_t)phase * 0x1p-63f;
   sincospif(half_turns, &s, &c);
   s *= sign;
 }

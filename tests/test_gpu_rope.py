@@ -117,3 +117,22 @@ def test_refusals():
     buf = torch.zeros(8 * 192 + 8, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(fq.Fp8qError):  # overlapping, but not the same
         fq.rope_fwd(buf[:8 * 192].view(8, 192), pos, plan, 1, 1, out=buf[8:].view(8, 192))
+
+
+@pytest.mark.parametrize("rot", [16, 12])
+def test_small_angles_keep_their_digits(rot):
+    """Frequencies of both signs whose angles stay below a quarter turn, at near and far positions: cosine and sine of the angle
+    itself (the pair (1, 0) turned).  The angle: |pos| 2^-65 turns for the fixed point, |angle| 2^-51 for the division and the
+    reference's product, half a step of fp32; the sine 2 steps."""
+    freqs = [-1e-20, 4.7e-13, -4.7e-13, -3.1e-10, 1e-10, -1e-8 / 16, 3.1e-11, -2.3e-13][:rot // 2]
+    plan = fq.Rope.make(head_dim=16, rot_dim=rot, inv_freq=freqs)
+    pos = torch.tensor([2 ** 31 - 1, -2 ** 31, 1, -1, 12345, -999999, 0], dtype=torch.int32, device="cuda")
+    x = torch.zeros(7, 16, device="cuda")
+    x[:, :rot // 2] = 1.0
+    for sign, fn in ((1.0, fq.rope_fwd), (-1.0, fq.rope_bwd)):
+        out = fn(x, pos, plan, 1, 0).double()
+        ang = sign * pos.double()[:, None] * torch.tensor(freqs, dtype=torch.float64, device="cuda")
+        s, c = torch.sin(ang), torch.cos(ang)
+        e = ang.abs() * (2.0 ** -51 + 2.0 ** -24) + pos.double().abs()[:, None] * 2.0 ** -65 * 6.2832
+        assert bool(((out[:, rot // 2:rot] - s).abs() <= e + s.abs() * 2.0 ** -22).all())
+        assert bool(((out[:, :rot // 2] - c).abs() <= e * s.abs() + e * e + 2.0 ** -22).all())

@@ -4,6 +4,7 @@ points return the documented codes before they touch the device, and the Python 
 import copy
 import ctypes
 import dataclasses
+import fractions
 import os
 import pickle
 import shutil
@@ -135,3 +136,27 @@ def test_rope_struct_matches_the_header(fq, tmp_path):
     got = subprocess.run([str(tmp_path / "layout")], check=True, capture_output=True, text=True).stdout.split()
     r = fq.FP8QRope
     assert [int(v) for v in got] == [ctypes.sizeof(r), r.inv_freq.offset, r.axis.offset]
+
+
+def test_rope_frequencies_in_turns(tmp_path):
+    """The fixed-point fraction of a turn per position against exact arithmetic: half a unit of 2^-64, and the
+    division's and the constant's roundings, below 2^-52 of the turns (the fraction is taken without error)."""
+    cxx = shutil.which("g++")
+    if not cxx:
+        pytest.skip("g++ not available")
+    freqs = [s * f for s in (1.0, -1.0) for f in
+             (0.0, 1e-300, 1e-20, 3.1e-19, 4.7e-13, 1e-10, 3.1e-10, 1e-8, 3.1e-7, 1e-4, 0.1, 0.5, 1.0, 3.0, 6.283185307179586,
+              6.28318530717958, 7.0, 12345.678, 1e9, 2.0 ** 52 + 0.5)] + [10000.0 ** (-i / 64) for i in range(64)]
+    src = tmp_path / "turn.cpp"
+    src.write_text('#include "fp8q_turn.h"\n#include <cstdio>\n#include <cstdlib>\nint main(int n, char** v) { for (int i = 1; i < n; ++i) '
+                   'std::printf("%llu\\n", (unsigned long long)fp8q::rope_turn(std::strtod(v[i], nullptr))); }\n')
+    subprocess.run([cxx, "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover=undefined", "-I",
+                    os.path.join(ROOT, "fp8_absmax_reduce_gb300", "csrc"), str(src), "-o", str(tmp_path / "turn")], check=True)
+    got = subprocess.run([str(tmp_path / "turn"), *[f.hex() for f in freqs]], check=True, capture_output=True, text=True).stdout.split()
+    two_pi = fractions.Fraction("6.28318530717958647692528676655900576839433879875021164194988918461563281257")
+    one = fractions.Fraction(2) ** 64
+    for f, u in zip(freqs, got):
+        turns = fractions.Fraction(f) / two_pi
+        off = (int(u) - turns * one) % one
+        off = min(off, one - off)
+        assert off <= fractions.Fraction(1, 2) + abs(turns) * 2 ** 12, (f, float(off))
