@@ -1049,10 +1049,13 @@ cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Laun
   return e;
 }
 
-// Columns of a backward piece: G of all tokens in about 256 MB, in whole tiles, the pieces alike.
+// Rows of G: its two parts of whole blocks of 32 tokens, or T.
+int64_t ce_g_rows(int64_t T) { return T <= kTwoParts ? 2 * ((T + 31) / 32 * 32) : T; }
+// Columns of a backward piece: all rows of G in about 256 MB (more than 131072 of them: 1024 columns), in whole tiles, the
+// pieces alike.
 int64_t ce_piece(int64_t T, int64_t V) {
   constexpr int64_t kPieceBytes = 256ll << 20;
-  int64_t most = kPieceBytes / (2 * T) / PN * PN;
+  int64_t most = kPieceBytes / (2 * ce_g_rows(T)) / PN * PN;
   if (most < 4 * PN) most = 4 * PN;
   const int64_t n = (V + most - 1) / most;
   return ((V + n - 1) / n + PN - 1) / PN * PN;
@@ -1064,8 +1067,6 @@ struct CePlan {
   int dx_splits, dw_splits;
   int z_splits;  // of the logits' K, or 0
 };
-// Rows of G: its two parts of whole blocks of 32 tokens, or T.
-int64_t ce_g_rows(int64_t T) { return T <= kTwoParts ? 2 * ((T + 31) / 32 * 32) : T; }
 CePlan ce_plan(int64_t T, int64_t d, int64_t V) {
   CePlan p{};
   p.piece = ce_piece(T, V);

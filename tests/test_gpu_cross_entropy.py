@@ -338,3 +338,21 @@ def test_masked_vocabulary_counts_for_nothing(T, d, V, lo, hi, mask):
     if mask == float("-inf"):
         dX[:, 0] = 0.0  # 0 times -inf there, in the definition too
     check_bwd(x, kept, t, dl, dX, torch.cat([dW[:lo], dW[hi:]]))
+
+
+@pytest.mark.parametrize("T,d,V", [(1, 8, 4_200_003), (24, 16, 2_100_001), (33, 8, 2_100_003), (64, 24, 1_100_003), (65, 8, 2_100_001),
+                                   (128, 16, 1_100_003)])
+def test_few_tokens_over_several_pieces_of_the_vocabulary(T, d, V):
+    """Up to 128 tokens and more than 256 MB of G: the pieces' shares of dX add up, each piece writes its own rows of dW, and
+    targets lie in all of them."""
+    x, W, t, dl = make(T, d, V)
+    t[0] = V - 1
+    loss, lse = fq.linear_cross_entropy_fwd(x, W, t)
+    check_fwd(x, W, t, loss, lse)
+    for dt in (torch.float32, torch.bfloat16):
+        gx, gw = Guarded((T, d), torch.bfloat16), Guarded((V, d), dt)
+        fq.linear_cross_entropy_bwd(x, W, t, lse, dl, dX=gx.t, dW=gw.t)
+        assert fq.last_launch_count() > 6  # one piece: the tokens' rows, G, dX and its join, dW and its join
+        torch.cuda.synchronize()
+        assert gx.intact() and gw.intact()
+        check_bwd(x, W, t, dl, gx.t, gw.t)

@@ -160,3 +160,14 @@ def test_rope_frequencies_in_turns(tmp_path):
         off = (int(u) - turns * one) % one
         off = min(off, one - off)
         assert off <= fractions.Fraction(1, 2) + abs(turns) * 2 ** 12, (f, float(off))
+
+
+@pytest.mark.parametrize("T", [1, 2, 32, 33, 64, 65, 128, 129, 1000, 8192, 131072])
+def test_backward_pieces_of_any_vocabulary_fit_their_limit(fq, T):
+    """What a larger vocabulary adds to the backward's workspace stops at G's 256 MB (d = 8: the parts of dX, of dW and of the
+    logits are at most 32 Tp d, 32 MB and 256 MB), whatever the tokens."""
+    size = lambda V: fq.linear_cross_entropy_bwd_workspace_size(T, 8, V)
+    rows = 2 * ((T + 31) // 32 * 32) if T <= 64 else T
+    other = rows * 8 * (2 + 32 * 4) + T * 16 + (rows + 256) * 8 * 4 * 32 + 4096
+    for V in (1 << 20, 3_000_000, 5_000_001, (1 << 24) - 3, 1 << 24):
+        assert 0 < size(V) <= (256 << 20) + (256 << 20) + other, V
