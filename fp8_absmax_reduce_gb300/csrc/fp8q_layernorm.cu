@@ -140,7 +140,7 @@ __device__ __forceinline__ void ln_copy(uint8_t* dst, const void* src, int64_t o
 // would make a variance of (2^-24 x)^2, which passes eps from |x| = 5e4 on.  So where a warp's first element is as near to its
 // mean as the mean's own roundings (kNear), it is the centre.  In bf16 sums of equal values are exact (8 + 14 bits) and the
 // division's two roundings are left; other rows come that near only by a mean that is the element, or beside elements half as
-// large as the mean or more away from it (bf16 steps are 2^-8), whose deviation is 2^14 times the difference or more.  In
+// large as the mean or more away from it (bf16 steps are 2^-8), whose deviation is 2^13 times the difference or more.  In
 // fp32 the sum has up to 32 roundings and other rows' elements are as near, so the second pass also adds up x - centre, which
 // corrects the mean and M2.  (T = 16384, d = 5120 61.4 -> 62.6 us cold, d = 2560 32.8 -> 34.4; fp32 8192 x 4096 equal.)
 // bf16 rows go two at a time (RT = 2): what bounds them is instructions, and the
@@ -768,7 +768,8 @@ cudaError_t fwd_t(const void* x, const void* g, const void* b, int64_t T, int d,
 #undef FP8Q_LN_FWD
 }
 
-// The launch shape of a block a row.  d is a multiple of 8: a thread has one piece of 8 columns up to d = 8192, else 4.
+// The launch shape of a block a row.  d is a multiple of 8 (the widest, and fp32 above 4096): a thread has one piece of 8
+// columns up to d = 8192, else 4.
 // Otherwise 1 to 32 single columns, of 128 threads up to d = 1024 and of 512 above.
 constexpr int kLnNarrow = 128;
 constexpr int bwd_np(int d) {
@@ -790,6 +791,7 @@ constexpr int bwd_per_sm(int d) {
   return n < 16 ? n : 16;
 }
 constexpr int kLnPlanSms = 152;
+static_assert(bwd_per_sm(4104) == 1 && bwd_per_sm(8192) == 1, "fp32 widths that the bf16 runs' workspace holds too");
 
 template <int F32, int VEC, int NP, int STRIDE>
 cudaError_t bwd_go(const void* dY, const void* x, const void* g, const float* mean, const float* rstd, const void* dres,
@@ -808,6 +810,8 @@ cudaError_t bwd_go(const void* dY, const void* x, const void* g, const float* me
   k<<<*nblk, bwd_threads(d), S * slot, L.stream>>>(dY, x, g, mean, rstd, dres, T, d, rows, S, dX, part, L.status);
   return launched(L);
 }
+
+constexpr int kRunsNarrow = 256, kRunsMost = 8192;  // bf16 columns of a warp with one vector a lane; of 16 with two
 
 template <int F32, int NP, int W>
 cudaError_t runs_go(const void* dY, const void* x, const void* g, const float* mean, const float* rstd, const void* dres,
@@ -836,7 +840,8 @@ cudaError_t bwd_t(const void* dY, const void* x, const void* g, const float* mea
   return bwd_go<F32, VEC, NP, STRIDE>(dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, L)
   if (d % 8 == 0) {
 #define FP8Q_LN_RUNS(NP, W) return runs_go<F32, NP, W>(dY, x, g, mean, rstd, dres, T, d, dX, part, nblk, L)
-    constexpr int kCols = F32 ? 256 : 512;  // of a warp
+    constexpr int kCols = 2 * kRunsNarrow / (F32 ? 2 : 1);  // of a warp with two
+    static_assert(F32 || 16 * kCols == kRunsMost, "widths in runs");
     if (2 * d <= kCols) FP8Q_LN_RUNS(1, 1);
     if (d <= kCols) FP8Q_LN_RUNS(2, 1);
     if (d <= 2 * kCols) FP8Q_LN_RUNS(2, 2);
@@ -868,8 +873,11 @@ cudaError_t bwd_t(const void* dY, const void* x, const void* g, const float* mea
 
 }  // namespace
 
+// Blocks of the first launch at most, of either type: those of k_layernorm_bwd_runs for the widths that it takes in bf16
+// (in fp32 the wider ones of them have a block a row and an SM).
 int layernorm_bwd_blocks(int64_t T, int d) {
-  const int64_t n = (int64_t)kLnPlanSms * bwd_per_sm(d);
+  const bool runs = d % 8 == 0 && d <= kRunsMost;
+  const int64_t n = (int64_t)kLnPlanSms * (!runs ? bwd_per_sm(d) : d <= kRunsNarrow ? RunPlan<1, 1>::kPerSm : RunPlan<2, 1>::kPerSm);
   return (int)(T < n ? T : n);
 }
 

@@ -192,3 +192,17 @@ def test_fp32_rows_far_from_zero(d):
     rel = 1e-5 + em * wr * (1 + em * wr)
     assert bool(((rstd.double() - wr).abs() <= wr * rel).all())
     assert bool(((y.double() - wy).abs() <= (em * wr)[:, None] + wy.abs() * (rel[:, None] + 2.0 ** -22)).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,d", [(3, 8), (700, 8), (30000, 128), (30000, 136), (30000, 256), (30000, 264), (3000, 512), (3000, 520), (2000, 1024), (1000, 4096),
+                                 (1000, 4104), (500, 8192), (500, 8200), (400, 16384), (3000, 1000), (30000, 7), (5000, 1025), (1000, 4099)])
+def test_backward_stays_inside_its_workspace(T, d, dtype):
+    t = make(T, d, dtype)
+    _, mean, rstd = fq.layernorm_fwd(t["x"], t["g"], t["b"])
+    n = fq.layernorm_bwd_workspace_size(T, d)
+    ws = torch.full((n + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+    out = fq.layernorm_bwd(t["dY"], t["x"], t["g"], mean, rstd, dres=t["dres"], ws=ws)
+    torch.cuda.synchronize()
+    assert bool((ws[n:] == 0xFF).all())
+    check_bwd(t, mean, rstd, out, True)

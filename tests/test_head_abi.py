@@ -171,3 +171,13 @@ def test_backward_pieces_of_any_vocabulary_fit_their_limit(fq, T):
     other = rows * 8 * (2 + 32 * 4) + T * 16 + (rows + 256) * 8 * 4 * 32 + 4096
     for V in (1 << 20, 3_000_000, 5_000_001, (1 << 24) - 3, 1 << 24):
         assert 0 < size(V) <= (256 << 20) + (256 << 20) + other, V
+
+
+@pytest.mark.parametrize("d,rows", [(8, 4 * 152), (256, 4 * 152), (264, 152), (512, 152), (1024, 152), (4096, 152), (5120, 152), (8192, 152),
+                                    (8200, 152), (16384, 152)])
+def test_layernorm_workspace_is_what_the_widths_use(fq, d, rows):
+    """Partial rows of dg and db for one block an SM, four where rows are narrow (152 SMs), not for shapes that a width no
+    longer takes; fewer tokens need no more rows than tokens."""
+    pad = lambda n: (n + 255) // 256 * 256
+    assert fq.layernorm_bwd_workspace_size(100000, d) == pad(rows * 2 * d * 4)
+    assert fq.layernorm_bwd_workspace_size(5, d) == pad(5 * 2 * d * 4)
