@@ -51,10 +51,13 @@ __device__ __forceinline__ float ce_exp2(float x) {
 //               accumulator, in both CTAs;
 //   warp 2      tensor memory;
 //   warps 3-10  epilogue: warp w reads lanes 32 (w % 4) ..; the first four take columns 0-127, the others 128-255.
-// The tensor cores' fp32 sums drop what falls below the sum's last place at each step, so a logit's error grows
-// with the steps; the loss's logits are therefore summed over K in parts of 1024 that the epilogue adds in
-// registers (the accumulators change hands after each part; measured at T = 4096, d = 3584, V = 50257: the loss's error
-// 2.7e-6 -> 0.7e-6 of its norm, 868 -> 888 us).
+// The tensor cores' fp32 sums drop what falls below the sum's last place at each step of 16 of K, so a logit's error grows
+// with the steps (products of one sign, parts of 1024: 12 2^-23 of the logit on average); the loss's logits are therefore
+// summed over K in parts that the epilogue adds in registers, the accumulators changing hands after each.  Parts of 1024
+// with many tokens (T = 4096, d = 3584, V = 50257: the loss's error 2.7e-6 -> 0.7e-6 of its norm, 868 -> 888 us).  Up to 128
+// tokens nothing averages a token's error (T = 1, d = 2048, V = 32000: 6.3e-6 so), and the parts are of 128, 0.7 2^-23 of
+// the logit, with as many accumulators as tensor memory has room for, up to 8 (T = 24, d = 4096, V = 100000 141 -> 146 us,
+// T = 120 147 -> 155, d = 2048, V = 32000 38.9 -> 39.4, cold; parts of 64: 161, 179, 40.3; of 192: 144, 151, 39.1).
 // Up to 128 tokens the operands trade places (kTok*): the 256 rows of a pair's tile are rows of W (of W^T for
 // dX) and its NT = 32, 64 or 128 columns the tokens, so that W streams at HBM's rate and the tensor cores do not
 // work on padding.  The softmax statistics then run down the tile's lanes: each warp turns its 32 x 32 blocks
@@ -71,7 +74,10 @@ constexpr int kEpiWarp = 3;           // the first of the 8 epilogue warps
 constexpr int kPairThreads = 32 * (kEpiWarp + 8);
 constexpr int kTokMax = 128;  // tokens up to which the operands trade places
 constexpr int kTwoParts = 64; // tokens up to which the backward keeps G in two parts
-constexpr int kSegBlocks = 16; // K of a partial sum of the logits, in blocks of 64
+// K of a partial sum of the logits, in blocks of 64, and the accumulators that take turns: up to 128 tokens and above.
+constexpr int kSegTok = 2, kSegWide = 16;
+constexpr int acc_count(int NT) { return NT == 256 ? 2 : NT == 128 ? 4 : 8; }
+constexpr int kPartBlocks = 16; // K of a part of the logits that comes to memory, at most
 
 enum PairMode {
   kPairLse = 0,   // per row and 128 columns: log2-domain maximum and sum; the target's logit
@@ -81,6 +87,7 @@ enum PairMode {
   kTokLse = 4,    // the same three with the tokens as columns: statistics of a CTA's rows of W
   kTokGrad = 5,   //   G / s in two parts, stored by token
   kTokDx = 6,     //   dX's sum in fp32, by token, the parts of K and of G apart
+  kTokLogits = 7, // the logits of few tokens in fp32, by token, the parts of K apart
 };
 enum PairOut { kOutF32Store = 0, kOutF32Add = 1, kOutBf16 = 2, kOutBf16Join = 3 };
 
@@ -95,7 +102,8 @@ struct PairPlan {
   static constexpr int kStagingOffset = kStages * kStage;
   static constexpr int kTokOffset = kStagingOffset + 8 * kStaging;
   static constexpr int kBarOffset = kTokOffset + (MODE == kTokGrad ? NT * 16 : 0);
-  static constexpr int kSmem = kBarOffset + 256 + 1024;
+  static constexpr int kAcc = acc_count(NT);
+  static constexpr int kSmem = kBarOffset + 512 + 1024;
   static_assert(kSmem <= 232448, "shared memory per CTA");
   static_assert(kStage % 1024 == 0, "swizzle atoms");
 };
@@ -306,16 +314,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_ce_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmC, const PairArgs p) {
   using PL = PairPlan<MODE, NT>;
-  constexpr bool kSeg = MODE == kPairLse || MODE == kTokLse;  // the sum over K comes in parts
+  constexpr bool kSeg = MODE == kPairLse || MODE == kTokLse || MODE == kTokLogits;  // the sum over K comes in parts
   constexpr bool kTok = MODE >= kTokLse;
+  constexpr int kSegBlocks = kTok ? kSegTok : kSegWide;
   static_assert(!(kTok && B_MN), "the tokens are a K-major operand");
   extern __shared__ uint8_t pair_smem[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pair_smem) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + PL::kBarOffset);
   uint64_t* empty = full + PL::kStages;
-  uint64_t* tfull = empty + PL::kStages;  // [2]
-  uint64_t* tempty = tfull + 2;           // [2]
-  uint64_t* drain = tempty + 2;
+  uint64_t* tfull = empty + PL::kStages;  // [kAcc]
+  uint64_t* tempty = tfull + PL::kAcc;    // [kAcc]
+  uint64_t* drain = tempty + PL::kAcc;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -325,13 +334,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int half_rows = MODE == kTokLse ? p.half_rows : 128;
   if (threadIdx.x == 0) {
     for (int s = 0; s < PL::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
-    for (int a = 0; a < 2; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], 16); }
+    for (int a = 0; a < PL::kAcc; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], 16); }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
-    if (MODE != kPairLse && MODE != kTokLse && MODE != kTokDx) tma_prefetch_desc(&tmC);
+    if (MODE != kPairLse && MODE != kTokLse && MODE != kTokDx && MODE != kTokLogits) tma_prefetch_desc(&tmC);
   }
   if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)), "r"(512)
@@ -420,7 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
           if (!ok) break;
           pair_commit(&tfull[acc], 3);
-          if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+          if (++acc == PL::kAcc) { acc = 0; acc_phase ^= 1u; }
         }
       }
       if (!ok) {
@@ -468,7 +477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) remote_arrive(tempty0 + 8 * acc);
-      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+      if (++acc == PL::kAcc) { acc = 0; acc_phase ^= 1u; }
     };
     for (int tile = first; tile < p.num_tiles; tile += step) {
       int mb, nb, kb0, kb1;
@@ -512,7 +521,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           p.part[(int64_t)(2 * nb + half) * p.M + row] = ce_pair(z);
         }
         __syncwarp();
-      } else if constexpr (MODE == kTokLse) {
+      } else if constexpr (MODE == kTokLse || MODE == kTokLogits) {
         float z[kBlocks][32];
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i)
@@ -526,9 +535,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           for (int i = 0; i < kBlocks; ++i) {
             const int c = half + 2 * i;
             if (32 * c >= NT || !warp_ok) continue;
+            uint32_t a[32];  // lane: row of W, register: token
+            tmem_ld32(lanes + (uint32_t)(acc * NT + 32 * c), a);
 #pragma unroll
-            for (int q = 0; q < 2; ++q)  // lane: row of W, register: token
-              ce_tmem_add16(lanes + (uint32_t)(acc * NT + 32 * c + 16 * q), z[i] + 16 * q);
+            for (int j = 0; j < 32; ++j) z[i][j] += __uint_as_float(a[j]);
           }
           release();
         }
@@ -537,6 +547,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         for (int i = 0; i < kBlocks; ++i) {
           const int c = half + 2 * i;
           if (32 * c >= NT || 32 * c >= p.N || !warp_ok) continue;
+          if constexpr (MODE == kTokLogits) {
+            if (!row_ok) continue;
+            float* dst = p.acc + ((int64_t)part * p.N + 32 * c) * p.M + row;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (32 * c + j < p.N) dst[(int64_t)j * p.M] = z[i][j];
+            continue;
+          }
           // element (row r, token j) at word 32 r + (r ^ j): rows and columns are both free of bank conflicts
           const uint32_t stage = out.buf;
           __syncwarp();
@@ -970,15 +988,15 @@ int tok_half_rows(int64_t V, const Launch& L) {
 
 // Parts of K for the logits of few tokens, stored in fp32 and joined by another kernel; 0: in one launch (kTokLse, kTokGrad).
 // A block of 64 of K takes a pair 0.25 us whatever the tokens and rows (an MMA of 256 rows takes as long for 32 columns as for
-// 256), so where a small vocabulary has few tiles for the pairs, the pairs share K, in one wave.  Parts of at most 1024 of K
-// keep the forward's precision.  T = 5, d = 4656, V = 2476, forward 29 -> 21 us and backward 49 -> 39; T = 2, d = 4080, V = 1686
+// 256), so where a small vocabulary has few tiles for the pairs, the pairs share K, in one wave.  The parts are of at
+// most 1024 of K, each summed in parts of 128 as above.  T = 5, d = 4656, V = 2476, forward 29 -> 21 us and backward 49 -> 39; T = 2, d = 4080, V = 1686
 // 27 -> 20 and 45 -> 33; T = 60, d = 3584, V = 4000 26 -> 22 and 49 -> 42 (in three waves T = 1, d = 5120, V = 9000 took 41 for 36).
 int tok_logit_splits(int64_t T, int64_t d, int64_t V) {
   const int64_t tiles = (V + PM - 1) / PM, kb = (d + PK - 1) / PK;
   if (T > kTokMax) return 0;
   int best = 0;
   double least = 0.25 * (double)kb - 2.0;  // one launch; the parts cost the backward a launch more
-  for (int64_t s = (kb + kSegBlocks - 1) / kSegBlocks; s <= kb && s <= 64 && tiles * s <= kPlanPairs; ++s) {
+  for (int64_t s = (kb + kPartBlocks - 1) / kPartBlocks; s <= kb && s <= 64 && tiles * s <= kPlanPairs; ++s) {
     const int64_t each = (kb + s - 1) / s;
     if (s < 2 || (kb + each - 1) / each != s) continue;
     if (s * T * V * 4 > (32ll << 20)) break;
@@ -1120,10 +1138,9 @@ cudaError_t launch_tok_logits(const uint16_t* x, const uint16_t* W, int64_t T, i
   const PairProblem q{V, T, d, W, d, x, d, nullptr, 0};
   PairArgs a{};
   a.acc = z;
-  a.out = kOutF32Store;
-  return T <= 32   ? launch_pair<0, 0, kTokDx, 32>(q, splits, a, L, dependent)
-         : T <= 64 ? launch_pair<0, 0, kTokDx, 64>(q, splits, a, L, dependent)
-                   : launch_pair<0, 0, kTokDx, 128>(q, splits, a, L, dependent);
+  return T <= 32   ? launch_pair<0, 0, kTokLogits, 32>(q, splits, a, L, dependent)
+         : T <= 64 ? launch_pair<0, 0, kTokLogits, 64>(q, splits, a, L, dependent)
+                   : launch_pair<0, 0, kTokLogits, 128>(q, splits, a, L, dependent);
 }
 
 }  // namespace

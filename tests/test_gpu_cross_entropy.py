@@ -356,3 +356,21 @@ def test_few_tokens_over_several_pieces_of_the_vocabulary(T, d, V):
         torch.cuda.synchronize()
         assert gx.intact() and gw.intact()
         check_bwd(x, W, t, dl, gx.t, gw.t)
+
+
+@pytest.mark.parametrize("T,d,V", [(1, 1024, 25000), (30, 1024, 25000), (64, 1024, 25000), (128, 1024, 25000), (24, 2048, 32000), (30, 2048, 9000),
+                                   (100, 2048, 9000), (1, 4656, 2476)])
+def test_few_tokens_keep_the_precision_of_their_logits(T, d, V):
+    """One logit of about 70 whose products are all positive, the others 0: lse is that logit.  Sums that are cut at each step
+    lose up to 2^-23 of the partial sum a step, in parts of 128 (8 steps) (8 + 1) / 2 2^-23 of the logit; adding up P = d / 128
+    parts rounds to (P + 1) / 2 2^-24, and the way to log2 units and back is four roundings and two constants: 2 2^-23."""
+    g = torch.Generator(device="cuda").manual_seed(T + d + V)
+    u = lambda *s: torch.rand(*s, generator=g, device="cuda") + 0.1
+    x, W = u(T, d).bfloat16(), torch.zeros(V, d, dtype=torch.bfloat16, device="cuda")
+    W[V // 2] = (u(d) * (200.0 / d)).bfloat16()
+    _, lse = fq.linear_cross_entropy_fwd(x, W, torch.zeros(T, dtype=torch.int64, device="cuda"))
+    z = x.double() @ W[V // 2].double()
+    want = z + torch.log1p((V - 1) * torch.exp(-z))
+    assert float(z.min()) > 30.0
+    bound = 4.5 + (d / 128 + 1) / 4 + 2.0
+    assert float(((lse.double() - want) / want).abs().max()) <= bound * 2.0 ** -23
