@@ -266,6 +266,9 @@ __device__ __forceinline__ float2 ce_join2(float2 a, float2 b) {
   if (m == -INFINITY) return make_float2(m, a.y + b.y);
   return make_float2(m, a.y * ce_exp2(a.x - m) + b.y * ce_exp2(b.x - m));
 }
+// lse - zy of a row's pair, about the maximum in log2 units: where the target is the likeliest entry, that difference is
+// exact, while lse itself is rounded to 2^-24 of its size, which a small loss may not be far above.
+__device__ __forceinline__ float ce_loss(float2 r, float zy) { return kLn2 * (fmaf(-zy, kLog2e, r.x) + log2f(r.y)); }
 // 16 columns of this thread's tensor-memory lane, added to z.
 __device__ __forceinline__ void ce_tmem_add16(uint32_t taddr, float* z) {
   uint32_t a[16];
@@ -745,7 +748,7 @@ __global__ void __launch_bounds__(1024) k_ce_finish(const float2* __restrict__ p
   const int64_t y = targets[row];
   const bool in = y >= 0 && y < V;
   if (y != ignore && !in) atomicOr(status, kStatusBadTarget);
-  loss[row] = y != ignore && in ? l - zy[row] : 0.0f;
+  loss[row] = y != ignore && in ? ce_loss(r, zy[row]) : 0.0f;
 }
 
 // Few tokens and a small vocabulary: the logits themselves, [splits][T][V] in fp32, one part of K each (tok_logit_splits).
@@ -789,7 +792,7 @@ __global__ void __launch_bounds__(1024) k_ce_logits_fwd(const float* __restrict_
   const int64_t y = targets[t];
   const bool in = y >= 0 && y < V;
   if (y != ignore && !in) atomicOr(status, kStatusBadTarget);
-  loss[t] = y != ignore && in ? l - ce_logit(z, splits, T, V, t, y) : 0.0f;
+  loss[t] = y != ignore && in ? ce_loss(r, ce_logit(z, splits, T, V, t, y)) : 0.0f;
 }
 // Backward: G / s in `copies` parts (rows T .. pad - 1 zero), as kTokGrad stores it.
 __global__ void __launch_bounds__(256) k_ce_logits_grad(const float* __restrict__ z, int splits, int64_t T, int64_t V,

@@ -374,3 +374,22 @@ def test_few_tokens_keep_the_precision_of_their_logits(T, d, V):
     assert float(z.min()) > 30.0
     bound = 4.5 + (d / 128 + 1) / 4 + 2.0
     assert float(((lse.double() - want) / want).abs().max()) <= bound * 2.0 ** -23
+
+
+@pytest.mark.parametrize("T,V", [(1, 300), (24, 25000), (100, 25000), (300, 9000)])
+def test_small_losses_are_not_lost_in_lse(T, V):
+    """Logits of two exact values, the target's of 2048 and the others' of 2048 - gap: loss = log1p((V - 1) e^-gap), down to
+    2e-5, beside an lse whose step is 2.4e-4.  The target's term of the sum is within 2^-22, and the sum, a little above 1, has
+    fewer than 60 roundings on any path: 64 2^-24.  The other terms are within 2^-18 of themselves: an exponent of up to 31 in log2
+    units rounded to 2^-20, its constant's 2^-25 of that, the exponential's 2^-22, 60 roundings; log2 and the last product 2^-22."""
+    gaps = ((torch.log(torch.tensor(float(V))) + torch.linspace(1.0, 11.0, T)) * 8).round().cuda() / 8
+    x, W = torch.zeros(T, 8, device="cuda"), torch.zeros(V, 8, device="cuda")
+    x[:, 0], W[:, 0] = 2048.0, 1.0
+    x[:, 1], x[:, 2], W[:, 1:3] = -gaps.floor(), gaps.floor() - gaps, 1.0
+    W[5, 1:3] = 0.0
+    xb, Wb = x.bfloat16(), W.bfloat16()
+    assert torch.equal(xb.float(), x) and torch.equal(Wb.float(), W)
+    loss, _ = fq.linear_cross_entropy_fwd(xb, Wb, torch.full((T,), 5, dtype=torch.int64, device="cuda"))
+    want = torch.log1p((V - 1) * torch.exp(-gaps.double()))
+    err = (loss.double() - want).abs()
+    assert bool((err <= 64 * 2.0 ** -24 + want * 2.0 ** -18).all()), float((err - want * 2.0 ** -18).max())
