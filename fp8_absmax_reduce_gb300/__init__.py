@@ -95,6 +95,8 @@ def _load() -> ctypes.CDLL:
         size.argtypes = [i64, i64, i64]
     L.linear_cross_entropy_fwd.argtypes = [vp, vp, vp, i64, i64, i64, i64, vp, vp, vp, sz, vp]
     L.linear_cross_entropy_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, i32, vp, sz, vp]
+    L.fp8q_selftest_linear_cross_entropy_wait_limit.argtypes = [i32, vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, i32,
+                                                                vp, sz, i64, vp]
     L.fp8q_trace_start.argtypes = [i32]
     L.fp8q_trace_read.argtypes = [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int), i32]
     L.fp8q_kernel_name.restype = ctypes.c_char_p
@@ -952,3 +954,29 @@ def selftest_bounded_wait(limit_s: float = 0.02, stream=None):
     """Make the library's bounded wait run out on purpose (an mbarrier nothing arrives at);
     afterwards the device status carries STATUS_TIMEOUT.  Diagnostics only."""
     _check("fp8q_selftest_bounded_wait", lib.fp8q_selftest_bounded_wait(int(limit_s * 1e9), _stream(stream)))
+
+
+def selftest_linear_cross_entropy_wait_limit(x: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, limit_s: float,
+                                             lse=None, dloss=None, ignore_index: int = -100, dw_dtype=torch.float32,
+                                             stream=None):
+    """linear_cross_entropy_fwd, or with dloss (and the forward's lse) linear_cross_entropy_bwd, with the pipeline waits
+    of their products limited to limit_s (fp8q_selftest_linear_cross_entropy_wait_limit in include/fp8q.h).  Returns what
+    they return, incomplete on a time-out."""
+    T, d, V, dev = _ce_sizes(x, W, targets)
+    device, back = x.device, dloss is not None
+    lse = _out("lse", lse, torch.float32, (T,), dev, device, stream)
+    nb = (lib.linear_cross_entropy_bwd_workspace_size if back else lib.linear_cross_entropy_fwd_workspace_size)(T, d, V)
+    w = _empty_ws(nb, device, stream)
+    if back:
+        _need("dloss", dloss, torch.float32, (T,), dev)
+        out = _empty((T, d), torch.bfloat16, device, stream), _empty((V, d), dw_dtype, device, stream)
+        ptrs = dloss.data_ptr(), None, *(t.data_ptr() for t in out)
+    else:
+        out = _empty((T,), torch.float32, device, stream), lse
+        ptrs = None, out[0].data_ptr(), None, None
+    _check("fp8q_selftest_linear_cross_entropy_wait_limit",
+           lib.fp8q_selftest_linear_cross_entropy_wait_limit(int(back), x.data_ptr(), W.data_ptr(), targets.data_ptr(),
+                                                             ptrs[0], T, d, V, ignore_index, ptrs[1], lse.data_ptr(),
+                                                             ptrs[2], ptrs[3], BF16 if dw_dtype is torch.bfloat16 else F32,
+                                                             w.data_ptr(), nb, max(1, int(limit_s * 1e9)), _raw_stream(stream, dev)))
+    return out

@@ -1528,23 +1528,24 @@ size_t linear_cross_entropy_bwd_workspace_size(int64_t T, int64_t d, int64_t V) 
   return ce_sizes_ok(T, d, V) ? round256(ce_workspace_bytes(T, d, V, 1)) : 0;
 }
 
-int linear_cross_entropy_fwd(const void* x, const void* W, const int64_t* targets, int64_t T, int64_t d, int64_t V,
-                             int64_t ignore_index, float* loss, float* lse, void* ws, size_t ws_bytes,
-                             fp8q_stream stream) {
+namespace {
+int ce_fwd_run(const void* x, const void* W, const int64_t* targets, int64_t T, int64_t d, int64_t V, int64_t ignore_index,
+               float* loss, float* lse, void* ws, size_t ws_bytes, fp8q_stream stream, uint64_t wait_ns) {
   int e = validate_ce(x, W, targets, T, d, V);
   if (e) return e;
   if (!al4(loss) || !al4(lse)) return FP8Q_ERR_INVALID_ARG;
   if ((e = check_ws(ws, ws_bytes, linear_cross_entropy_fwd_workspace_size(T, d, V)))) return e;
   Ctx c;
   if ((e = make_ctx(&c, stream))) return e;
+  c.L.wait_ns = wait_ns;
   FP8Q_STEP(kKCeFwd, launch_ce_fwd((const uint16_t*)x, (const uint16_t*)W, targets, T, (int)d, V, ignore_index, loss,
                                    lse, ws, c.L));
   return finish(c);
 }
 
-int linear_cross_entropy_bwd(const void* x, const void* W, const int64_t* targets, const float* lse,
-                             const float* dloss, int64_t T, int64_t d, int64_t V, int64_t ignore_index, void* dX,
-                             void* dW, fp8q_dtype dw_dtype, void* ws, size_t ws_bytes, fp8q_stream stream) {
+int ce_bwd_run(const void* x, const void* W, const int64_t* targets, const float* lse, const float* dloss, int64_t T,
+               int64_t d, int64_t V, int64_t ignore_index, void* dX, void* dW, fp8q_dtype dw_dtype, void* ws,
+               size_t ws_bytes, fp8q_stream stream, uint64_t wait_ns) {
   int e = validate_ce(x, W, targets, T, d, V);
   if (e) return e;
   if (!al4(lse) || !al4(dloss) || !al16(dX) || !al16(dW)) return FP8Q_ERR_INVALID_ARG;
@@ -1552,9 +1553,34 @@ int linear_cross_entropy_bwd(const void* x, const void* W, const int64_t* target
   if ((e = check_ws(ws, ws_bytes, linear_cross_entropy_bwd_workspace_size(T, d, V)))) return e;
   Ctx c;
   if ((e = make_ctx(&c, stream))) return e;
+  c.L.wait_ns = wait_ns;
   FP8Q_STEP(kKCeBwd, launch_ce_bwd((const uint16_t*)x, (const uint16_t*)W, targets, lse, dloss, T, (int)d, V,
                                    ignore_index, (uint16_t*)dX, dW, dw_dtype == FP8Q_F32, ws, c.L));
   return finish(c);
+}
+}  // namespace
+
+int linear_cross_entropy_fwd(const void* x, const void* W, const int64_t* targets, int64_t T, int64_t d, int64_t V,
+                             int64_t ignore_index, float* loss, float* lse, void* ws, size_t ws_bytes,
+                             fp8q_stream stream) {
+  return ce_fwd_run(x, W, targets, T, d, V, ignore_index, loss, lse, ws, ws_bytes, stream, 0);
+}
+
+int linear_cross_entropy_bwd(const void* x, const void* W, const int64_t* targets, const float* lse,
+                             const float* dloss, int64_t T, int64_t d, int64_t V, int64_t ignore_index, void* dX,
+                             void* dW, fp8q_dtype dw_dtype, void* ws, size_t ws_bytes, fp8q_stream stream) {
+  return ce_bwd_run(x, W, targets, lse, dloss, T, d, V, ignore_index, dX, dW, dw_dtype, ws, ws_bytes, stream, 0);
+}
+
+int fp8q_selftest_linear_cross_entropy_wait_limit(int backward, const void* x, const void* W, const int64_t* targets,
+                                                  const float* dloss, int64_t T, int64_t d, int64_t V,
+                                                  int64_t ignore_index, float* loss, float* lse, void* dX, void* dW,
+                                                  fp8q_dtype dw_dtype, void* ws, size_t ws_bytes, int64_t limit_ns,
+                                                  fp8q_stream stream) {
+  if (limit_ns < 1 || limit_ns > 10000000000ll) return FP8Q_ERR_INVALID_ARG;
+  return backward ? ce_bwd_run(x, W, targets, lse, dloss, T, d, V, ignore_index, dX, dW, dw_dtype, ws, ws_bytes, stream,
+                               (uint64_t)limit_ns)
+                  : ce_fwd_run(x, W, targets, T, d, V, ignore_index, loss, lse, ws, ws_bytes, stream, (uint64_t)limit_ns);
 }
 
 // ---------------------------------------------------------------------------

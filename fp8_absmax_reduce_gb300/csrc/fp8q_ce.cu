@@ -65,7 +65,7 @@ __device__ __forceinline__ float ce_exp2(float x) {
 // padded tiles (d = 2048, V = 32000): forward 42 against 54 us for one token, 42 / 46 for 24, 45 / 46 for 100;
 // backward 90 / 112, 89 / 94, 97 / 100.
 //
-// Every wait is bounded.  On expiry a CTA records the time-out and stops; its copies in flight, which
+// Every wait is bounded.  On expiry a CTA records the time-out and stops; once all its roles have, its copies in flight, which
 // signal the other CTA, get kCopyDrainNs to land; the pair meets at a cluster barrier and frees its tensor memory.
 // ---------------------------------------------------------------------------
 constexpr int PM = 256, PN = 256, PK = 64;
@@ -140,6 +140,7 @@ struct PairArgs {
   float* zy;                // kPairLse, kTokLse: each token's target logit
   const float4* rows;       // kPairGrad, kTokGrad: each token's {lse log2e, dloss / s, target or -1 (int bits), 0}
   unsigned* status;
+  uint64_t wait_ns;         // the self-test's limit of every wait of the pipeline, or 0 (issued MMAs keep kWaitLimitNs)
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -312,7 +313,9 @@ __device__ __forceinline__ int pair_coords(int tile, const PairArgs& p, int& mb,
   return part;
 }
 
-template <int A_MN, int B_MN, int MODE, int NT>
+// SHORT: the self-test, whose waits poll, so that limits of nanoseconds are honoured (as a branch of one kernel: 741 -> 867 us
+// at T = 4096, d = 3584, V = 50257).
+template <int A_MN, int B_MN, int MODE, int NT, int SHORT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_ce_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmC, const PairArgs p) {
@@ -335,6 +338,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int rank = (int)cluster_rank();
   const int first = (int)(blockIdx.x >> 1), step = (int)(gridDim.x >> 1);
   const int half_rows = MODE == kTokLse ? p.half_rows : 128;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if constexpr (SHORT) return mbar_poll(bar, parity, abort_flag, p.wait_ns);
+    else return mbar_wait_held(bar, parity, abort_flag);
+  };
   if (threadIdx.x == 0) {
     for (int s = 0; s < PL::kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
     for (int a = 0; a < PL::kAcc; ++a) { mbar_init(&tfull[a], 1); mbar_init(&tempty[a], 16); }
@@ -373,7 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         pair_coords(tile, p, mb, nb, kb0, kb1);
         const int m0 = (2 * mb + rank) * half_rows, n0 = nb * NT + NT / 2 * rank;
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait_held(&empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
+          if (!wait(&empty[stage], phase ^ 1u)) { ok = false; break; }
           uint8_t* sA = smem + stage * PL::kStage;
           uint8_t* sB = sA + kHalfTile;
           const uint32_t bar = map_to_rank(smem_addr(&full[stage]), 0);
@@ -397,8 +404,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (!ok) {
         atomicOr(p.status, kStatusTimeout);
         *abort_flag = 1;
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < kCopyDrainNs) {}
       }
     }
   } else if (warp == 1) {
@@ -412,11 +417,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         pair_coords(tile, p, mb, nb, kb0, kb1);
         for (int kb = kb0; kb < kb1 && ok;) {
           const int begin = kb, end = kSeg ? min(kb + kSegBlocks, kb1) : kb1;
-          if (!mbar_wait_held(&tempty[acc], acc_phase ^ 1u, abort_flag)) { ok = false; break; }
+          if (!wait(&tempty[acc], acc_phase ^ 1u)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d = tmem_base + (uint32_t)(acc * NT);
           for (; kb < end; ++kb) {
-            if (!mbar_wait_held(&full[stage], phase, abort_flag)) { ok = false; break; }
+            if (!wait(&full[stage], phase)) { ok = false; break; }
             tc_fence_after();
             const uint32_t sA = smem_addr(smem + stage * PL::kStage), sB = sA + kHalfTile;
 #pragma unroll
@@ -467,7 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // lane 0 waits for the accumulator and the warp follows its result (what comes is warp-collective)
     auto take = [&]() -> bool {
       int ok = 0;
-      if (lane == 0) ok = mbar_wait_held(&tfull[acc], acc_phase, abort_flag) ? 1 : 0;
+      if (lane == 0) ok = wait(&tfull[acc], acc_phase) ? 1 : 0;
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       if (!ok) {
         atomicOr(p.status, kStatusTimeout);
@@ -703,6 +708,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   tc_fence_before();
   __syncwarp();
   __syncthreads();
+  // Where any role of the CTA gave up, copies may be in flight, its producer's among them though that finished: no one waits
+  // for their barriers any more.  (The other CTA's roles then run into their own limits, so both wait here.)
+  if (*abort_flag) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < kCopyDrainNs) {}
+    __syncwarp();
+  }
   cluster_sync_all();  // neither CTA's memory or barriers are in use by the other any more
   tc_fence_after();
   if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512) : "memory");
@@ -1009,6 +1021,31 @@ int tok_logit_splits(int64_t T, int64_t d, int64_t V) {
   return best;
 }
 
+template <int A_MN, int B_MN, int MODE, int NT, int SHORT>
+cudaError_t launch_pair_kernel(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc, const PairArgs& a,
+                               const Launch& L, bool dependent) {
+  auto* k = k_ce_gemm<A_MN, B_MN, MODE, NT, SHORT>;
+  constexpr int kSmem = PairPlan<MODE, NT>::kSmem;
+  static std::atomic<uint64_t> configured{0};  // a bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!(configured.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(1ull << dev);
+  }
+  const int pairs = pair_grid(L, a.num_tiles);
+  if (!dependent) {  // comes first in its call
+    k<<<2 * pairs, kPairThreads, kSmem, L.stream>>>(ta, tb, tc, a);
+    e = cudaGetLastError();
+  } else {
+    e = launch_dependent(k, 2 * pairs, kPairThreads, kSmem, L.stream, ta, tb, tc, a);
+  }
+  if (L.launches) ++*L.launches;
+  return e;
+}
+
 template <int A_MN, int B_MN, int MODE, int NT = 256>
 cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Launch& L, bool dependent = true) {
   constexpr bool kTok = MODE >= kTokLse;
@@ -1034,6 +1071,7 @@ cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Laun
   a.idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) |
             ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(PM >> 4) << 24);
   a.status = L.status;
+  a.wait_ns = L.wait_ns;
   CUtensorMap ta, tb, tc;
   bool ok = A_MN ? make_map(&ta, q.A, q.M, q.K, q.lda, 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B)
                  : make_map(&ta, q.A, q.K, q.M, q.lda, 2, 64, a.half_rows, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -1049,25 +1087,8 @@ cudaError_t launch_pair(const PairProblem& q, int splits, PairArgs a, const Laun
                         wide ? 64 : 32, 32, f32 || wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
   }
   if (!ok) return cudaErrorInvalidValue;
-  static std::atomic<uint64_t> configured{0};  // a bit per device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (!(configured.load() >> dev & 1)) {
-    e = cudaFuncSetAttribute(k_ce_gemm<A_MN, B_MN, MODE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, PairPlan<MODE, NT>::kSmem);
-    if (e != cudaSuccess) return e;
-    configured.fetch_or(1ull << dev);
-  }
-  const int pairs = pair_grid(L, a.num_tiles);
-  if (!dependent) {  // comes first in its call
-    k_ce_gemm<A_MN, B_MN, MODE, NT><<<2 * pairs, kPairThreads, PairPlan<MODE, NT>::kSmem, L.stream>>>(ta, tb, tc, a);
-    e = cudaGetLastError();
-  } else {
-    e = launch_dependent(k_ce_gemm<A_MN, B_MN, MODE, NT>, 2 * pairs, kPairThreads, PairPlan<MODE, NT>::kSmem, L.stream,
-                         ta, tb, tc, a);
-  }
-  if (L.launches) ++*L.launches;
-  return e;
+  if (a.wait_ns) return launch_pair_kernel<A_MN, B_MN, MODE, NT, 1>(ta, tb, tc, a, L, dependent);
+  return launch_pair_kernel<A_MN, B_MN, MODE, NT, 0>(ta, tb, tc, a, L, dependent);
 }
 
 // Rows of G: its two parts of whole blocks of 32 tokens, or T.

@@ -18,6 +18,7 @@ struct Launch {
   unsigned* status;  // device status word (FP8Q_STATUS_* bits)
   int num_sms;
   int* launches;     // incremented once per kernel launch
+  uint64_t wait_ns = 0;  // limit of the pipeline waits in the head's products (0: the default)
 };
 
 // Device address of the library's status word and the SM count of the current

@@ -636,6 +636,19 @@ FP8Q_API int fp8q_selftest_rmsnorm_bwd_wait_limit(const float* dN, const void* x
                                                   void* ws, size_t ws_bytes, int64_t limit_ns,
                                                   fp8q_stream stream);
 
+/* Diagnostics for the abort sequence of the head's products (no page counterpart): linear_cross_entropy_fwd
+ * (backward == 0: x, W, targets -> loss, lse) or linear_cross_entropy_bwd (backward != 0: lse and dloss are read, dX
+ * and dW written), except that the waits of the products' pipelines poll and give up after limit_ns (1 ns ..
+ * 10 s) instead of 2 s.  With a limit of nanoseconds ordinary waits run out: the two CTAs of a tile record
+ * FP8Q_STATUS_TIMEOUT, stop issuing, wait for the MMAs and copies that they issued, free their tensor memory and
+ * exit; the outputs are then incomplete and the context stays usable.  Returns FP8Q_OK once enqueued
+ * (synchronous errors as the entry points). */
+FP8Q_API int fp8q_selftest_linear_cross_entropy_wait_limit(int backward, const void* x, const void* W,
+                                                           const int64_t* targets, const float* dloss, int64_t T,
+                                                           int64_t d, int64_t V, int64_t ignore_index, float* loss,
+                                                           float* lse, void* dX, void* dW, fp8q_dtype dw_dtype, void* ws,
+                                                           size_t ws_bytes, int64_t limit_ns, fp8q_stream stream);
+
 /* Kernel-level timing for benchmarks.  While tracing is on for the calling
  * host thread, each kernel step the library enqueues is bracketed by two CUDA
  * events recorded on the stream it is launched on (host-side CUDA objects; no

@@ -111,3 +111,32 @@ def test_gemm_wait_limit_is_validated():
     s = torch.ones(2, dtype=torch.float32, device="cuda")
     with pytest.raises(fq.Fp8qError):
         fq.selftest_gemm_wait_limit(fq.NN, A, 0, A, 0, 1e-7, sinvA=s[0:1], sinvB=s[1:2])
+
+
+@pytest.mark.parametrize("T,d,V", [(24, 2048, 32000), (100, 1024, 25000), (5, 4656, 2476), (1000, 2048, 9000), (300, 512, 1000)])
+@pytest.mark.parametrize("backward", [False, True])
+def test_head_products_abort_sequence_on_short_waits(T, d, V, backward):
+    """The products of the head's cross entropy on pairs of SMs, with their waits limited to a nanosecond: both CTAs of a tile
+    give up with copies in flight that signal the other, wait for them, and meet at the end.  The same call afterwards gives
+    what it gave before."""
+    g = torch.Generator(device="cuda").manual_seed(T + V)
+    x = torch.randn(T, d, generator=g, device="cuda").bfloat16()
+    W = (0.02 * torch.randn(V, d, generator=g, device="cuda")).bfloat16()
+    t = torch.randint(0, V, (T,), generator=g, device="cuda")
+    dl = torch.full((T,), 1.0 / T, device="cuda")
+
+    def normal():
+        loss, lse = fq.linear_cross_entropy_fwd(x, W, t)
+        return (loss, lse, *(fq.linear_cross_entropy_bwd(x, W, t, lse, dl) if backward else ()))
+
+    fq.get_status(clear=True)
+    before = normal()
+    torch.cuda.synchronize()
+    assert fq.get_status() == 0
+    fq.selftest_linear_cross_entropy_wait_limit(x, W, t, 1e-9, **(dict(lse=before[1], dloss=dl) if backward else {}))
+    torch.cuda.synchronize()
+    assert fq.get_status(clear=True) & fq.STATUS_TIMEOUT
+    again = normal()
+    torch.cuda.synchronize()
+    assert fq.get_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(before, again))

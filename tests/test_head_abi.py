@@ -181,3 +181,16 @@ def test_layernorm_workspace_is_what_the_widths_use(fq, d, rows):
     pad = lambda n: (n + 255) // 256 * 256
     assert fq.layernorm_bwd_workspace_size(100000, d) == pad(rows * 2 * d * 4)
     assert fq.layernorm_bwd_workspace_size(5, d) == pad(5 * 2 * d * 4)
+
+
+def test_head_wait_limit_is_validated(fq):
+    T, d, V = 5, 64, 100
+    n = max(fq.linear_cross_entropy_fwd_workspace_size(T, d, V), fq.linear_cross_entropy_bwd_workspace_size(T, d, V))
+
+    def call(back, limit=1, x=FAKE, ws=FAKE, n=n):
+        return fq.lib.fp8q_selftest_linear_cross_entropy_wait_limit(back, x, FAKE, FAKE, FAKE, T, d, V, -100, FAKE, FAKE, FAKE,
+                                                                    FAKE, F32, ws, n, limit, None)
+    for back in (0, 1):
+        for bad in (dict(limit=10 ** 10 + 1), dict(limit=0), dict(limit=-5), dict(x=ODD)):
+            assert call(back, **bad) == INVALID, bad
+        assert call(back, ws=None) == WORKSPACE and call(back, n=16) == WORKSPACE
