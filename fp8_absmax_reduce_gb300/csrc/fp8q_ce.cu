@@ -63,7 +63,7 @@ __device__ __forceinline__ float ce_exp2(float x) {
 // work on padding.  The softmax statistics then run down the tile's lanes: each warp turns its 32 x 32 blocks
 // in shared memory and keeps a running pair for each token over all its tiles.  Measured against the
 // padded tiles (d = 2048, V = 32000): forward 42 against 54 us for one token, 42 / 46 for 24, 45 / 46 for 100;
-// backward 90 / 112, 89 / 94, 97 / 100.
+// backward 90 / 112, 89 / 94, 97 / 100 (when it was made; now 39, 39, 43 and 87, 89, 93).
 //
 // Every wait is bounded.  On expiry a CTA records the time-out and stops; once all its roles have, its copies in flight, which
 // signal the other CTA, get kCopyDrainNs to land; the pair meets at a cluster barrier and frees its tensor memory.
@@ -993,7 +993,7 @@ int pair_splits(int64_t M, int64_t N, int64_t K) {
 
 // Rows of W in each half of a tile of the forward of few tokens, a multiple of 8 up to 128: as many tiles as the pairs take
 // in the waves of full ones, so that all pairs stream for the same time (T = 24 and 120, d = 4096, V = 100000, 391 full
-// tiles: 153 -> 143 and 158 -> 148 us; nothing is gained where one wave holds them, nor in the backward's logits, which
+// tiles: 153 -> 143 and 158 -> 148 us, with K in parts of 1024; nothing is gained where one wave holds them, nor in the backward's logits, which
 // write G).  The MMAs work on 128 rows all the same: what the stage held beyond makes sums that are not read back.
 int tok_half_rows(int64_t V, const Launch& L) {
   const int64_t pairs = pair_grid(L, 0x7FFFFFFF), waves = ((V + PM - 1) / PM + pairs - 1) / pairs;

@@ -541,7 +541,8 @@ FP8Q_API int rope_bwd(const void* d_out, fp8q_dtype dtype, int64_t T, int n_head
  * gradient, as rmsnorm_bwd's dY) -> dX [T,d], dg [d] fp32 and, unless db is NULL, db [d] fp32:
  *   xh = (x - mean) rstd, u = dY g, dX = rstd (u - mean_j(u) - xh mean_j(u xh)) (+ dres),
  *   dg = sum_t dY xh, db = sum_t dY.
- * dX may be dY, x or dres itself.  Sums are fp32 in a fixed order, so results repeat bit for bit.
+ * dX may be dY, x or dres itself.  Sums are fp32 in a fixed order, so results repeat bit for bit; dg and db add runs of
+ * rows in sequence, T / 4864 of them where rows are narrow, T / 152 where they are widest, then the runs.
  * Requirements: 1 <= T <= 2^28, 1 <= d <= 16384, eps finite and >= 0; [T,d] tensors, g and b 16-byte,
  * mean, rstd, dg and db 4-byte aligned.  Workspace (backward): layernorm_bwd_workspace_size(T, d)
  * bytes, 256-byte aligned. */
@@ -569,8 +570,9 @@ FP8Q_API int layernorm_bwd(const void* dY, const void* x, fp8q_dtype dtype, cons
  *   G = dloss_t (e^{z - lse_t} - 1[v = y]), 0 in the rows of ignored tokens;
  *   dX [T,d] bf16 = G W, dW [V,d] (bf16 or fp32) = G^T x, both overwritten in full.
  * The logits are computed again in pieces of the vocabulary; G is rounded to bf16 relative to
- * max |dloss| as the tensor cores' operand (the sums are fp32), so an fp32 dW carries that rounding
- * (2^-8 of the terms of its sums at most; up to 64 tokens G is kept in two parts, 2^-16).  Rows of x of
+ * max |dloss| as the tensor cores' operand, so an fp32 dW carries that rounding
+ * (2^-8 of the terms of its sums at most; up to 64 tokens G is kept in two parts, 2^-16).  The sums are fp32, cut at each
+ * step of 16 terms: up to (T / 16 + 32) 2^-23 of the sum of the terms' magnitudes for dW, the same with V for dX.  Rows of x of
  * ignored tokens may hold anything, NaN too, without reaching dX or dW.  Deterministic.
  * Requirements: 1 <= T, V <= 2^24 with fewer than 2^31 tiles of 256 x 256 logits, d a multiple of 8,
  * 8 <= d <= 65536; x, W, dX, dW 16-byte, targets 8-byte, loss, lse, dloss 4-byte aligned; outputs must not
