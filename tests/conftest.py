@@ -21,6 +21,11 @@ def pytest_collection_modifyitems(config, items):
     except Exception:
         has_gpu = False
     if has_gpu:
+        # these calls pass fake pointers through every check and expect the missing device's error
+        skip = pytest.mark.skip(reason="only without a CUDA device: fake pointers reach it")
+        for it in items:
+            if it.path.name == "test_host_executor.py":
+                it.add_marker(skip)
         return
     skip = pytest.mark.skip(reason="no CUDA device")
     for it in items:
