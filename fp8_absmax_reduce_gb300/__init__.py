@@ -26,7 +26,7 @@ from . import build as _build_mod
 E4M3, E5M2 = 0, 1
 BF16, F32 = 0, 1
 NN, NT, TN = 0, 1, 2
-STATUS_NONFINITE, STATUS_TIMEOUT, STATUS_BAD_TARGET = 0x1, 0x2, 0x4
+STATUS_NONFINITE, STATUS_TIMEOUT, STATUS_BAD_TARGET, STATUS_BAD_CACHE = 0x1, 0x2, 0x4, 0x8
 
 _LIB_PATH = _build_mod.LIB
 
@@ -97,6 +97,12 @@ def _load() -> ctypes.CDLL:
     L.linear_cross_entropy_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, i32, vp, sz, vp]
     L.fp8q_selftest_linear_cross_entropy_wait_limit.argtypes = [i32, vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, i32,
                                                                 vp, sz, i64, vp]
+    cache_p = ctypes.POINTER(FP8QKvCache)
+    L.kv_cache_append.argtypes = [cache_p, vp, i64, i64, vp, vp, vp, i32, i64, i32, vp]
+    L.kv_cache_read.argtypes = [cache_p, vp, i64, i64, vp, vp, i64, vp, i32, vp]
+    L.attention_cached_workspace_size.restype = sz
+    L.attention_cached_workspace_size.argtypes = [cache_p, i64, i64, i32]
+    L.attention_cached.argtypes = [cache_p, vp, i64, i64, vp, vp, vp, i64, i32, vp, vp, vp, sz, vp]
     L.fp8q_trace_start.argtypes = [i32]
     L.fp8q_trace_read.argtypes = [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int), i32]
     L.fp8q_kernel_name.restype = ctypes.c_char_p
@@ -145,6 +151,13 @@ class FP8QRope(ctypes.Structure):
     """Mirror of ``fp8q_rope`` in include/fp8q.h."""
     _fields_ = [("head_dim", ctypes.c_int), ("rot_dim", ctypes.c_int), ("n_axes", ctypes.c_int),
                 ("interleaved", ctypes.c_int), ("inv_freq", ctypes.c_double * 128), ("axis", ctypes.c_uint8 * 128)]
+
+
+class FP8QKvCache(ctypes.Structure):
+    """Mirror of ``fp8q_kv_cache`` in include/fp8q.h."""
+    _fields_ = [("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("fmt", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
 class FP8QBlock(ctypes.Structure):
@@ -662,6 +675,143 @@ def linear_cross_entropy_bwd(x: torch.Tensor, W: torch.Tensor, targets: torch.Te
                                         BF16 if dW.dtype is torch.bfloat16 else F32, w.data_ptr(), nb,
                                         _raw_stream(stream, dev)))
     return dX, dW
+
+
+@dataclasses.dataclass(frozen=True, eq=False)
+class KvCache:
+    """Key/value cache in 8 bits (see fp8q_kv_cache in include/fp8q.h): codes k, v [n_pages, n_kv_heads, page_size,
+    head_dim] and scales k_scale, v_scale [n_pages, n_kv_heads], all uint8 on one CUDA device.  Make one with
+    :meth:`allocate`, or over tensors of your own; which pages a sequence has is the caller's to keep."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+    fmt: int = E4M3
+    _struct: object = dataclasses.field(init=False, repr=False, compare=False)
+
+    def __post_init__(self):
+        if not isinstance(self.k, torch.Tensor) or self.k.ndim != 4:
+            raise ValueError("k must be a tensor [n_pages, n_kv_heads, page_size, head_dim]")
+        n, h, p, d = self.k.shape
+        for name, shape in (("k", (n, h, p, d)), ("v", (n, h, p, d)), ("k_scale", (n, h)), ("v_scale", (n, h))):
+            _need(name, getattr(self, name), torch.uint8, shape, self.k.get_device() if self.k.is_cuda else -2)
+        if p not in (16, 32, 64, 128):
+            raise ValueError(f"page_size {p}: 16, 32, 64 or 128")
+        if d not in (64, 96, 128):
+            raise ValueError(f"head_dim {d}: 64, 96 or 128")
+        if self.fmt not in (E4M3, E5M2):
+            raise ValueError(f"fmt {self.fmt}: E4M3 or E5M2")
+        if not 1 <= n < 1 << 31 or not 1 <= h <= 1024:
+            raise ValueError(f"{n} pages of {h} heads")
+        object.__setattr__(self, "_struct", FP8QKvCache(n, p, h, d, self.fmt))
+
+    def __reduce__(self):  # copies and pickles make their own structure
+        return KvCache, (self.k, self.v, self.k_scale, self.v_scale, self.fmt)
+
+    @staticmethod
+    def allocate(n_pages: int, n_kv_heads: int, head_dim: int = 128, page_size: int = 64, fmt: int = E4M3,
+                 device="cuda") -> "KvCache":
+        """n_pages of page_size tokens (16, 32, 64 or 128), all zero."""
+        z = lambda *shape: torch.zeros(shape, dtype=torch.uint8, device=device)
+        return KvCache(z(n_pages, n_kv_heads, page_size, head_dim), z(n_pages, n_kv_heads, page_size, head_dim),
+                       z(n_pages, n_kv_heads), z(n_pages, n_kv_heads), fmt)
+
+    @property
+    def n_pages(self) -> int:
+        return self._struct.n_pages
+
+    @property
+    def page_size(self) -> int:
+        return self._struct.page_size
+
+    @property
+    def n_kv_heads(self) -> int:
+        return self._struct.n_kv_heads
+
+    @property
+    def head_dim(self) -> int:
+        return self._struct.head_dim
+
+
+def _kv_call(cache, pages, lens, row_start, dev: int):
+    """Checks what the cache's entry points share; the C structure, n_seqs, max_pages and row_start's address."""
+    c = cache._struct
+    k, v, ks, vs = cache.k, cache.v, cache.k_scale, cache.v_scale
+    if k.get_device() != dev:
+        raise ValueError(f"the cache is on {k.device}, not on the current device cuda:{dev}")
+    # where the tensors are now: a program may have moved their storage
+    c.k, c.v, c.k_scale, c.v_scale = k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr()
+    shape = getattr(pages, "shape", ())
+    if len(shape) != 2:
+        raise ValueError("pages must be a CUDA tensor [n_seqs, max_pages]")
+    if not _fits(pages, torch.int32, shape, dev):
+        _refuse("pages", pages, torch.int32, shape, dev)
+    n = shape[0]
+    if not _fits(lens, torch.int32, (n,), dev):
+        _refuse("lens", lens, torch.int32, (n,), dev)
+    if row_start is None:
+        return c, n, shape[1], None
+    if not _fits(row_start, torch.int32, (n + 1,), dev):
+        _refuse("row_start", row_start, torch.int32, (n + 1,), dev)
+    return c, n, shape[1], row_start.data_ptr()
+
+
+def kv_cache_append(cache: KvCache, qkv: torch.Tensor, pages: torch.Tensor, lens: torch.Tensor, n_heads: int,
+                    row_start: torch.Tensor | None = None, stream=None):
+    """Writes the K and V heads of qkv [T, (n_heads + 2 n_kv_heads) head_dim] (bf16 or fp32; n_heads may be 0) into the
+    cache, as the last tokens of each sequence.  pages [n_seqs, max_pages] int32: each sequence's pages in the order of
+    its tokens; lens [n_seqs] int32: its tokens, these included; row_start [n_seqs + 1] int32: each sequence's first row
+    (default: T / n_seqs rows each).  See kv_cache_append in include/fp8q.h."""
+    (T, width), dev = _matrix("qkv", qkv)
+    if width != (n_heads + 2 * cache.n_kv_heads) * cache.head_dim:
+        raise ValueError(f"qkv has {width} columns, not ({n_heads} + 2 * {cache.n_kv_heads}) heads of {cache.head_dim}")
+    c, n, max_pages, start = _kv_call(cache, pages, lens, row_start, dev)
+    _check("kv_cache_append",
+           lib.kv_cache_append(c, pages.data_ptr(), n, max_pages, lens.data_ptr(), start, qkv.data_ptr(),
+                               BF16 if qkv.dtype is torch.bfloat16 else F32, T, n_heads, _raw_stream(stream, dev)))
+
+
+def kv_cache_read(cache: KvCache, pages: torch.Tensor, lens: torch.Tensor, T: int, row_start: torch.Tensor | None = None,
+                  dtype=torch.bfloat16, kv=None, stream=None):
+    """The values that the cache holds for the last tokens of each sequence: kv [T, 2 n_kv_heads head_dim] (bf16 or fp32; a
+    given kv decides its own type), row = [k heads | v heads]; T / n_seqs rows a sequence, or row_start's.  Rows behind the last sequence
+    are not written."""
+    dev, device = torch._C._cuda_getDevice(), cache.k.device
+    shape = (T, 2 * cache.n_kv_heads * cache.head_dim)
+    c, n, max_pages, start = _kv_call(cache, pages, lens, row_start, dev)
+    if kv is not None:
+        dtype = getattr(kv, "dtype", None)
+    if dtype not in _REAL:
+        raise TypeError(f"dtype {dtype}: bfloat16 or float32")
+    kv = _out("kv", kv, dtype, shape, dev, device, stream)
+    _check("kv_cache_read",
+           lib.kv_cache_read(c, pages.data_ptr(), n, max_pages, lens.data_ptr(), start, T, kv.data_ptr(),
+                             BF16 if dtype is torch.bfloat16 else F32, _raw_stream(stream, dev)))
+    return kv
+
+
+def attention_cached_workspace_size(cache: KvCache, T: int, n_seqs: int, n_heads: int) -> int:
+    return lib.attention_cached_workspace_size(cache._struct, T, n_seqs, n_heads)
+
+
+def attention_cached(cache: KvCache, qkv: torch.Tensor, pages: torch.Tensor, lens: torch.Tensor, n_heads: int,
+                     row_start: torch.Tensor | None = None, att=None, lse=None, ws=None, stream=None):
+    """Causal grouped-query attention of the q heads of qkv [T, (n_heads + 2 n_kv_heads) head_dim] (bf16) over the cache,
+    each row seeing its sequence's tokens up to its own (append them first); pages, lens, row_start as kv_cache_append.
+    Returns (att [T, n_heads head_dim] bf16, lse [n_heads, T] fp32); rows behind the last sequence are not written."""
+    (T, width), dev = _matrix("qkv", qkv, _HEAD)
+    device = qkv.device
+    if width != (n_heads + 2 * cache.n_kv_heads) * cache.head_dim:
+        raise ValueError(f"qkv has {width} columns, not ({n_heads} + 2 * {cache.n_kv_heads}) heads of {cache.head_dim}")
+    c, n, max_pages, start = _kv_call(cache, pages, lens, row_start, dev)
+    att = _out("att", att, torch.bfloat16, (T, n_heads * cache.head_dim), dev, device, stream)
+    lse = _out("lse", lse, torch.float32, (n_heads, T), dev, device, stream)
+    nb = lib.attention_cached_workspace_size(c, T, n, n_heads)
+    w = _scratch(nb, dev, device, ws, stream)
+    _check("attention_cached",
+           lib.attention_cached(c, pages.data_ptr(), n, max_pages, lens.data_ptr(), start, qkv.data_ptr(), T, n_heads,
+                                att.data_ptr(), lse.data_ptr(), w.data_ptr(), nb, _raw_stream(stream, dev)))
+    return att, lse
 
 
 # ---------------------------------------------------------------------------

@@ -29,6 +29,7 @@ enum Kind {
   kKGemmQkv, kKGemmOResidual, kKGemmODgrad, kKGemmOWgrad, kKGemmQkvDgrad, kKGemmQkvWgrad,
   kKGemmGateUpRecompute, kKRmsnormBf16, kKAttnFwd, kKAttnBwdDelta, kKAttnBwdDkdv, kKAttnBwdDq,
   kKMxQuant, kKPrologueStats, kKPrologueCast, kKLayernormFwd, kKLayernormBwd, kKRope, kKCeFwd, kKCeBwd,
+  kKKvAppend, kKKvRead, kKKvAttend,
   kKCount
 };
 const char* const kKindNames[kKCount] = {
@@ -37,7 +38,8 @@ const char* const kKindNames[kKCount] = {
     "gemm_down_wgrad", "gemm_gate_up_dgrad", "gemm_gate_up_wgrad", "gemm",
     "gemm_qkv", "gemm_o_residual", "gemm_o_dgrad", "gemm_o_wgrad", "gemm_qkv_dgrad", "gemm_qkv_wgrad",
     "gemm_gate_up_recompute", "rmsnorm_bf16", "attn_fwd", "attn_bwd_delta", "attn_bwd_dkdv", "attn_bwd_dq",
-    "mx_quant", "prologue_stats", "prologue_cast", "layernorm_fwd", "layernorm_bwd", "rope", "ce_fwd", "ce_bwd"};
+    "mx_quant", "prologue_stats", "prologue_cast", "layernorm_fwd", "layernorm_bwd", "rope", "ce_fwd", "ce_bwd",
+    "kv_append", "kv_read", "attn_cached"};
 
 struct Trace {
   bool on = false;
@@ -1503,6 +1505,92 @@ int rope_fwd(const void* qkv, fp8q_dtype dtype, int64_t T, int n_heads, int n_kv
 int rope_bwd(const void* d_out, fp8q_dtype dtype, int64_t T, int n_heads, int n_kv_heads, const fp8q_rope* rope,
              const int32_t* pos, void* dqkv, fp8q_stream stream) {
   return rope_run(d_out, dtype, T, n_heads, n_kv_heads, rope, pos, 1, dqkv, stream);
+}
+
+// ---------------------------------------------------------------------------
+// The 8-bit key/value cache
+// ---------------------------------------------------------------------------
+namespace {
+// The cache's own fields.
+int validate_cache(const fp8q_kv_cache* c) {
+  if (!c) return FP8Q_ERR_INVALID_ARG;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) return FP8Q_ERR_UNSUPPORTED;
+  if (c->head_dim != 64 && c->head_dim != 96 && c->head_dim != 128) return FP8Q_ERR_UNSUPPORTED;
+  if (c->fmt != FP8Q_E4M3 && c->fmt != FP8Q_E5M2) return FP8Q_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || c->n_pages > INT32_MAX || c->n_kv_heads < 1 || c->n_kv_heads > 1024) return FP8Q_ERR_INVALID_ARG;
+  return FP8Q_OK;
+}
+bool kv_sizes_ok(int64_t T, int64_t n_seqs) {
+  return T >= 1 && T <= ((int64_t)1 << 28) && n_seqs >= 1 && n_seqs <= ((int64_t)1 << 20);
+}
+bool kv_heads_ok(const fp8q_kv_cache* c, int n_heads) {
+  return n_heads >= 1 && n_heads <= 1024 && n_heads % c->n_kv_heads == 0;
+}
+int kv_args(KvArgs* a, const fp8q_kv_cache* c, const int32_t* pages, int64_t n_seqs, int64_t max_pages, const int32_t* lens,
+            const int32_t* row_start, int64_t T) {
+  int e = validate_cache(c);
+  if (e) return e;
+  if (!al16(c->k) || !al16(c->v) || !c->k_scale || !c->v_scale) return FP8Q_ERR_INVALID_ARG;
+  if (!kv_sizes_ok(T, n_seqs)) return FP8Q_ERR_INVALID_ARG;
+  if (max_pages < 1 || max_pages > INT32_MAX / c->page_size) return FP8Q_ERR_INVALID_ARG;
+  if (!al4(pages) || !al4(lens) || (row_start && !al4(row_start))) return FP8Q_ERR_INVALID_ARG;
+  if (!row_start && T % n_seqs) return FP8Q_ERR_INVALID_ARG;
+  int shift = 4;
+  while ((1 << shift) < c->page_size) ++shift;
+  *a = KvArgs{c->k, c->v, c->k_scale, c->v_scale, c->n_pages, shift, c->n_kv_heads, c->head_dim, (int)c->fmt, pages, max_pages,
+              lens, row_start, (int)n_seqs, row_start ? 0 : (int)(T / n_seqs), T, nullptr};
+  return FP8Q_OK;
+}
+}  // namespace
+
+int kv_cache_append(const fp8q_kv_cache* cache, const int32_t* pages, int64_t n_seqs, int64_t max_pages,
+                    const int32_t* lens, const int32_t* row_start, const void* qkv, fp8q_dtype dtype, int64_t T, int n_heads,
+                    fp8q_stream stream) {
+  KvArgs a;
+  int e = kv_args(&a, cache, pages, n_seqs, max_pages, lens, row_start, T);
+  if (e) return e;
+  if (dtype != FP8Q_BF16 && dtype != FP8Q_F32) return FP8Q_ERR_INVALID_ARG;
+  if (!al16(qkv) || (n_heads != 0 && !kv_heads_ok(cache, n_heads))) return FP8Q_ERR_INVALID_ARG;
+  Ctx c;
+  if ((e = make_ctx(&c, stream))) return e;
+  a.status = c.L.status;
+  FP8Q_STEP(kKKvAppend, launch_kv_append(a, qkv, dtype == FP8Q_F32, n_heads, c.L));
+  return finish(c);
+}
+
+int kv_cache_read(const fp8q_kv_cache* cache, const int32_t* pages, int64_t n_seqs, int64_t max_pages, const int32_t* lens,
+                  const int32_t* row_start, int64_t T, void* kv, fp8q_dtype dtype, fp8q_stream stream) {
+  KvArgs a;
+  int e = kv_args(&a, cache, pages, n_seqs, max_pages, lens, row_start, T);
+  if (e) return e;
+  if (dtype != FP8Q_BF16 && dtype != FP8Q_F32) return FP8Q_ERR_INVALID_ARG;
+  if (!al16(kv)) return FP8Q_ERR_INVALID_ARG;
+  Ctx c;
+  if ((e = make_ctx(&c, stream))) return e;
+  a.status = c.L.status;
+  FP8Q_STEP(kKKvRead, launch_kv_read(a, kv, dtype == FP8Q_F32, c.L));
+  return finish(c);
+}
+
+size_t attention_cached_workspace_size(const fp8q_kv_cache* cache, int64_t T, int64_t n_seqs, int n_heads) {
+  if (validate_cache(cache) || !kv_sizes_ok(T, n_seqs) || !kv_heads_ok(cache, n_heads)) return 0;
+  return round256(kv_attend_workspace_bytes(T, (int)n_seqs, n_heads, cache->n_kv_heads, cache->head_dim));
+}
+
+int attention_cached(const fp8q_kv_cache* cache, const int32_t* pages, int64_t n_seqs, int64_t max_pages,
+                     const int32_t* lens, const int32_t* row_start, const void* qkv, int64_t T, int n_heads, void* att,
+                     float* lse, void* ws, size_t ws_bytes, fp8q_stream stream) {
+  KvArgs a;
+  int e = kv_args(&a, cache, pages, n_seqs, max_pages, lens, row_start, T);
+  if (e) return e;
+  if (!kv_heads_ok(cache, n_heads) || !al16(qkv) || !al16(att) || !al4(lse)) return FP8Q_ERR_INVALID_ARG;
+  if ((e = check_ws(ws, ws_bytes, attention_cached_workspace_size(cache, T, n_seqs, n_heads)))) return e;
+  Ctx c;
+  if ((e = make_ctx(&c, stream))) return e;
+  a.status = c.L.status;
+  FP8Q_STEP(kKKvAttend, launch_kv_attend(a, static_cast<const uint16_t*>(qkv), n_heads, static_cast<uint16_t*>(att), lse, ws,
+                                         c.L));
+  return finish(c);
 }
 
 // ---------------------------------------------------------------------------

@@ -95,6 +95,27 @@ struct RopePlan {
 cudaError_t launch_rope(const void* in, int f32, const RopePlan& plan, const int32_t* pos, int64_t T, int n_heads,
                         int n_kv_heads, int inverse, void* out, const Launch& L);
 
+// The 8-bit key/value cache (codes and E8M0 scales by pages) and the rows of one call.
+constexpr unsigned kStatusBadCache = 0x8u;
+struct KvArgs {
+  uint8_t *k, *v, *k_scale, *v_scale;
+  int64_t n_pages;
+  int page_shift;            // log2 of the page's tokens
+  int hkv, dh, fmt;
+  const int32_t* pages;      // [n_seqs, max_pages]
+  int64_t max_pages;
+  const int32_t* lens;       // [n_seqs]
+  const int32_t* row_start;  // [n_seqs + 1] or null: `rows` each
+  int n_seqs, rows;
+  int64_t T;
+  unsigned* status;
+};
+cudaError_t launch_kv_append(const KvArgs& a, const void* qkv, int f32, int n_heads, const Launch& L);
+cudaError_t launch_kv_read(const KvArgs& a, void* kv, int f32, const Launch& L);
+size_t kv_attend_workspace_bytes(int64_t T, int n_seqs, int n_heads, int hkv, int dh);
+cudaError_t launch_kv_attend(const KvArgs& a, const uint16_t* qkv, int n_heads, uint16_t* att, float* lse, void* ws,
+                             const Launch& L);
+
 // Softmax cross entropy of the linear head z = x W^T (x [T, d], W [V, d] bf16).
 constexpr unsigned kStatusBadTarget = 0x4u;
 size_t ce_workspace_bytes(int64_t T, int64_t d, int64_t V, int bwd);

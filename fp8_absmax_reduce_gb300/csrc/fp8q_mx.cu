@@ -44,33 +44,6 @@ inline cudaError_t post_launch(const Launch& L) {
   return cudaGetLastError();
 }
 
-// The smallest X in [-127, 127] with a <= fmax * 2^X for a finite, non-negative a given by its
-// fp32 bits.  fmax = 1.75 * 2^EMAX (E4M3: 448, EMAX 8; E5M2: 57344, EMAX 15).  With a = M * 2^e,
-// M in [1, 2): a <= 1.75 * 2^(X + EMAX) exactly when X >= e - EMAX + (M > 1.75).
-template <int FMT>
-__device__ __forceinline__ int mx_exponent(uint32_t abits) {
-  constexpr int EMAX = FMT == 0 ? 8 : 15;
-  if (abits == 0) return -127;
-  int e;
-  bool above;
-  const uint32_t E = abits >> 23, m = abits & 0x7FFFFFu;
-  if (E != 0) {
-    e = (int)E - 127;
-    above = m > 0x600000u;  // M = 1 + m / 2^23 > 1.75
-  } else {                  // subnormal: a = m * 2^-149
-    const int p = 31 - __clz((int)m);
-    e = p - 149;
-    above = 4ull * m > 7ull << p;  // m / 2^p > 1.75
-  }
-  int X = e - EMAX + (above ? 1 : 0);
-  return X < -127 ? -127 : (X > 127 ? 127 : X);
-}
-
-// 2^-X as fp32 (X in [-127, 127]; 2^-127 is subnormal).
-__device__ __forceinline__ float pow2_neg(int X) {
-  return X == 127 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(127 - X) << 23);
-}
-
 // Byte offset of (operand row r, contraction index k) in the chunked scale layout.
 __device__ __forceinline__ int64_t sf_offset(int64_t r, int64_t k, int64_t n_kchunks) {
   return ((r >> 7) * n_kchunks + (k >> 7)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + ((k >> 5) & 3);

@@ -78,6 +78,7 @@ typedef void* fp8q_stream; /* cudaStream_t */
 #define FP8Q_STATUS_NONFINITE 0x1u
 #define FP8Q_STATUS_TIMEOUT 0x2u
 #define FP8Q_STATUS_BAD_TARGET 0x4u /* linear_cross_entropy_*: a target outside [0, V) that is not ignore_index */
+#define FP8Q_STATUS_BAD_CACHE 0x8u  /* kv_cache_*, attention_cached: a page, length or row range outside its bounds */
 
 /* ------------------------------------------------------------------------ */
 /* Per-tensor absmax quantization (LLMQ §1 dynamic tensor-level scaling;    */
@@ -527,6 +528,72 @@ FP8Q_API int rope_fwd(const void* qkv, fp8q_dtype dtype, int64_t T, int n_heads,
                       const fp8q_rope* rope, const int32_t* pos, void* out, fp8q_stream stream);
 FP8Q_API int rope_bwd(const void* d_out, fp8q_dtype dtype, int64_t T, int n_heads, int n_kv_heads,
                       const fp8q_rope* rope, const int32_t* pos, void* dqkv, fp8q_stream stream);
+
+/* ------------------------------------------------------------------------ */
+/* Key/value cache in 8 bits with a scale for each page and head, and the    */
+/* attention that reads it: running a sequence token by token.              */
+/* ------------------------------------------------------------------------ */
+/* A page holds page_size consecutive tokens of one sequence, for every K/V head.  K and V are codes of fmt, each worth
+ * decode(code) 2^X with one X for a page and head, stored as the E8M0 code X + 127 (0 .. 254).  Scale rule (mx_quantize's, per
+ * page and head): X is the smallest integer with amax <= fmt_max 2^X, clamped to [-127, 127] (-127 where all is zero); nothing
+ * is clipped.  The structure is host memory and is read during the call only; what it points to is the caller's. */
+typedef struct fp8q_kv_cache {
+  int64_t n_pages;    /* 1 .. 2^31 - 1 */
+  int page_size;      /* 16, 32, 64 or 128 tokens */
+  int n_kv_heads;     /* 1 .. 1024 */
+  int head_dim;       /* 64, 96 or 128 */
+  fp8q_fmt fmt;
+  uint8_t* k;         /* [n_pages, n_kv_heads, page_size, head_dim] codes */
+  uint8_t* v;
+  uint8_t* k_scale;   /* [n_pages, n_kv_heads] E8M0 codes */
+  uint8_t* v_scale;
+} fp8q_kv_cache;
+/* What the entry points below share:
+ *   pages [n_seqs, max_pages] int32: token t of sequence s lies in page pages[s][t / page_size], slot t % page_size; entries
+ *     behind a sequence's last page are not read.
+ *   lens [n_seqs] int32: the tokens of each sequence in the cache, those of this call included.
+ *   row_start [n_seqs + 1] int32, never decreasing, or NULL: rows row_start[s] .. row_start[s + 1] - 1 are those of sequence s, and rows from
+ *     row_start[n_seqs] on belong to none (a padded batch: they are neither read nor written).  NULL: T is a multiple of
+ *     n_seqs, and every sequence has T / n_seqs rows.
+ * Row j of the n rows of sequence s is its token lens[s] - n + j: the call's rows are a sequence's last tokens.  A row whose
+ * token would be negative is padding (a slot of a batch without a sequence has lens 0): it is not appended, reads as zero
+ * and attends to nothing.
+ * All three are device memory, read by the kernels.  A length outside [0, max_pages page_size] (taken as 0), rows outside
+ * [0, T] (taken as none) and a page outside [0, n_pages) (its tokens are not written, read as zero and not attended to)
+ * set FP8Q_STATUS_BAD_CACHE.  A row_start that decreases may go unreported, and leaves it open which sequence a row is taken
+ * for.  No access leaves its tensor, whatever they hold.
+ * Requirements: 1 <= T <= 2^28, 1 <= n_seqs <= 2^20, max_pages >= 1, max_pages page_size < 2^31, n_heads a multiple of n_kv_heads, at most 1024;
+ * k, v, qkv, kv and att 16-byte, pages, lens, row_start and lse 4-byte aligned; head_dim and page_size outside their lists are
+ * FP8Q_ERR_UNSUPPORTED. */
+
+/* Writes the K and V heads of qkv [T, (n_heads + 2 n_kv_heads) head_dim] (bf16 or fp32, row = [q heads | k heads | v heads] as
+ * attention_fwd and rope_fwd have it; n_heads may be 0) into the cache.  A page whose first token is among the call's starts
+ * anew, whatever it held; in a page that holds earlier tokens of its sequence X only grows, and where it does their codes
+ * move to the new scale: code' = rne(decode(code) 2^(X_old - X)), exact but for codes that become subnormal.
+ * code = fp8_rne_satfinite(v 2^-X).  A value that is NaN or Inf is stored as the NaN code 0x7F, does not count for X and sets
+ * FP8Q_STATUS_NONFINITE.  Slots behind the last token keep what they held.  Sequences may share pages that a call only reads;
+ * a page that a call writes must be in one place of `pages` only.  No workspace. */
+FP8Q_API int kv_cache_append(const fp8q_kv_cache* cache, const int32_t* pages, int64_t n_seqs, int64_t max_pages,
+                             const int32_t* lens, const int32_t* row_start, const void* qkv, fp8q_dtype dtype, int64_t T,
+                             int n_heads, fp8q_stream stream);
+/* kv [T, 2 n_kv_heads head_dim] (bf16 or fp32), row = [k heads | v heads]: what the cache holds for the rows' tokens (exact in fp32;
+ * bf16 is exact too but where decode(code) 2^X is subnormal or overflows).  No workspace. */
+FP8Q_API int kv_cache_read(const fp8q_kv_cache* cache, const int32_t* pages, int64_t n_seqs, int64_t max_pages,
+                           const int32_t* lens, const int32_t* row_start, int64_t T, void* kv, fp8q_dtype dtype,
+                           fp8q_stream stream);
+/* Causal attention of the call's rows over the cache (their own tokens appended before): the row of token t sees tokens
+ * 0 .. t of its sequence; query head h reads K/V head h / (n_heads / n_kv_heads); scale 1 / sqrt(head_dim).
+ *   qkv [T, (n_heads + 2 n_kv_heads) head_dim] bf16: the q heads are read.
+ *   att [T, n_heads head_dim] bf16, lse [n_heads, T] fp32 as attention_fwd writes them; a row that sees nothing has att 0 and
+ *   lse -Inf.
+ * Scores, maxima, sums and accumulators are fp32; codes and q enter the tensor cores without loss (fp16, q over a power
+ * of two of its row), the probabilities as fp16 relative to the row's maximum (2^-11 of each, at least 2^-39 of the
+ * maximum).  Slots behind a sequence's last token may hold anything.  Deterministic.
+ * Workspace: attention_cached_workspace_size bytes (0 for sizes outside the limits), 256-byte aligned. */
+FP8Q_API size_t attention_cached_workspace_size(const fp8q_kv_cache* cache, int64_t T, int64_t n_seqs, int n_heads);
+FP8Q_API int attention_cached(const fp8q_kv_cache* cache, const int32_t* pages, int64_t n_seqs, int64_t max_pages,
+                              const int32_t* lens, const int32_t* row_start, const void* qkv, int64_t T, int n_heads,
+                              void* att, float* lse, void* ws, size_t ws_bytes, fp8q_stream stream);
 
 /* ------------------------------------------------------------------------ */
 /* Layer norm, beside the RMSNorm entry points, for models that use it.     */

@@ -1,0 +1,527 @@
+"""The 8-bit key/value cache against its definition in 64 bits: writing, reading back, and attention over it.
+
+Codes, scales and values read back are equal to the definition's.  Attention: an output is off by at most
+  2^-8 |att|                                     its rounding to bf16,
+  (2^-11 + 2 e + (keys + 16) 2^-22) size         the probabilities as fp16 (half a step, 2^-11 of each); their exponents' errors e;
+                                                 fp32 sums over the keys,
+with size = sum p |v| / sum p and e = (dh + 16) 2^-23 max sum |q| |k| / sqrt(dh): a score is an fp32 sum of dh products that
+the tensor core may cut at 2^-23 of its terms, and its scaling, subtraction and 2^x each add a rounding of the same size.
+lse: e + (keys + 16) 2^-22 for the sum's logarithm, and 2^-22 |lse|."""
+
+import copy
+import pickle
+
+import numpy as np
+import pytest
+import torch
+
+import _kv_ref as ref
+import fp8_absmax_reduce_gb300 as fq
+from _gpu import fp8_table
+
+pytestmark = pytest.mark.gpu
+
+TABLE = [fp8_table(0), fp8_table(1)]
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+class World:
+    """A cache, sequences in it, and the same in the reference.  Slots that no token was written to hold NaN codes."""
+
+    def __init__(self, fmt=0, dh=128, P=64, hq=4, hkv=2, lens=(1,), rows=1, ragged=None, seed=0, extra=2, behind=0, wide=True):
+        self.fmt, self.dh, self.P, self.hq, self.hkv = fmt, dh, P, hq, hkv
+        self.rng = np.random.default_rng(seed)
+        need = [-(-n // P) for n in lens]
+        n_pages = sum(need) + extra
+        order = self.rng.permutation(n_pages)
+        width = max(1, max(need))
+        self.pages = np.full((len(lens), width), -1, np.int64)
+        at = 0
+        for s, k in enumerate(need):
+            self.pages[s, :k] = order[at:at + k]
+            at += k
+        self.lens = list(lens)
+        self.row_start = None
+        if ragged is not None:
+            self.row_start = [0]
+            for r in ragged:
+                self.row_start.append(self.row_start[-1] + r)
+        self.T = (len(lens) * rows if ragged is None else self.row_start[-1]) + behind
+        self.rows = ref.rows_of(len(lens), self.T, self.row_start)
+        self.cache = fq.KvCache.allocate(n_pages, hkv, dh, P, fmt)
+        self.cache.k.fill_(0x7F)
+        self.cache.v.fill_(0xFF)
+        self.ref = {n: np.full((n_pages, hkv, P, dh), np.nan) for n in "kv"} | {n: np.full((n_pages, hkv), -127) for n in ("kx", "vx")}
+        self.wide = np.where(self.rng.random(dh) < 0.05, 6.0, 1.0) if wide else np.ones(dh)
+
+    def args(self):
+        return i32(self.pages), i32(self.lens)
+
+    def start(self):
+        return None if self.row_start is None else i32(self.row_start)
+
+    def qkv(self, dtype=torch.bfloat16, std=1.0):
+        x = self.rng.standard_normal((self.T, self.hq + 2 * self.hkv, self.dh)) * std * np.exp2(self.rng.integers(-2, 3, (self.T, 1, 1)))
+        x[:, self.hq:self.hq + self.hkv] *= self.wide
+        t = torch.tensor(x, dtype=torch.float32).to(dtype).cuda()
+        return t.reshape(self.T, -1), t.double().cpu().numpy()
+
+    def fill(self):
+        """Every sequence's tokens before this call's, written by the framework and by the reference."""
+        before = [max(0, n - r) for n, (_, r) in zip(self.lens, self.rows)]
+        if not any(before):
+            return
+        start = np.concatenate([[0], np.cumsum(before)]).tolist()
+        rows = ref.rows_of(len(before), start[-1], start)
+        x = self.rng.standard_normal((start[-1], 2 * self.hkv, self.dh)) * np.exp2(self.rng.integers(-2, 3, (start[-1], 1, 1)))
+        x[:, :self.hkv] *= self.wide
+        t = torch.tensor(x, dtype=torch.float32).cuda()
+        fq.kv_cache_append(self.cache, t.reshape(start[-1], -1), i32(self.pages), i32(before), 0, row_start=i32(start))
+        ref.append(self.ref, self.fmt, self.P, self.pages, before, rows, t.double().cpu().numpy().reshape(-1, 2, self.hkv, self.dh))
+
+    def append(self, dtype=torch.bfloat16, **kw):
+        t, x = self.qkv(dtype)
+        fq.kv_cache_append(self.cache, t, *self.args(), self.hq, row_start=self.start(), **kw)
+        ref.append(self.ref, self.fmt, self.P, self.pages, self.lens, self.rows, x[:, self.hq:].reshape(-1, 2, self.hkv, self.dh))
+        return t, x
+
+    def check_cache(self):
+        torch.cuda.synchronize()
+        for n, c, x in (("k", self.cache.k, self.cache.k_scale), ("v", self.cache.v, self.cache.v_scale)):
+            got = TABLE[self.fmt][c.cpu().numpy()]
+            assert np.array_equal(np.isnan(got), np.isnan(self.ref[n])), n
+            assert np.array_equal(np.nan_to_num(got), np.nan_to_num(self.ref[n])), n
+            wrote = ~np.isnan(self.ref[n]).all(axis=(2, 3))
+            assert np.array_equal(x.cpu().numpy().astype(int)[wrote] - 127, self.ref[n + "x"][wrote]), n
+
+    def check_attention(self, att, lse, q):
+        torch.cuda.synchronize()
+        want, size, wlse, mag = ref.attend(self.ref, self.P, self.pages, self.lens, self.rows, q)
+        owned = ~np.isnan(wlse[0])
+        assert owned.any()
+        got, glse = att.double().cpu().numpy().reshape(want.shape), lse.double().cpu().numpy()
+        keys = max(1, max(self.lens))
+        e = (self.dh + 16) * 2.0 ** -23 * mag.T[:, :, None]
+        tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * e + (keys + 16) * 2.0 ** -22) * size
+        worst = np.max((np.abs(got - want) - tol)[owned])
+        assert worst <= 0, f"att off by {worst} more than allowed"
+        empty = np.isneginf(wlse)
+        assert np.array_equal(np.isneginf(glse)[:, owned], empty[:, owned])
+        seen = owned[None] & ~empty
+        glse, wlse = np.where(seen, glse, 0), np.where(seen, wlse, 0)
+        tol = e[:, :, 0].T + (keys + 16) * 2.0 ** -22 + 2.0 ** -22 * np.abs(wlse)
+        assert (np.abs(glse - wlse)[seen] <= tol[seen]).all()
+
+    def attend(self, t, x, **kw):
+        att, lse = fq.attention_cached(self.cache, t, *self.args(), self.hq, row_start=self.start(), **kw)
+        self.check_attention(att, lse, x[:, :self.hq])
+        return att, lse
+
+
+SHAPES = [  # dh, P, hq, hkv
+    (128, 64, 4, 2), (128, 128, 7, 1), (64, 16, 3, 3), (96, 32, 10, 2), (128, 16, 16, 1), (64, 128, 40, 2), (96, 64, 1, 1)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("dh,P,hq,hkv", SHAPES)
+def test_append_prompts_then_tokens(fmt, dtype, dh, P, hq, hkv):
+    """New sequences of one token to several pages, then one more token each, then a few; read back at each step."""
+    fq.get_status(clear=True)
+    lens = [1, P - 1, P, P + 1, 3 * P + 5]
+    w = World(fmt, dh, P, hq, hkv, [n + 8 for n in lens], seed=dh + P + fmt)
+    for n_rows, upto in ((lens, lens), ([1] * 5, [n + 1 for n in lens]), ([7, 0, 3, 7, 1], [n + k for n, k in zip(lens, (8, 1, 4, 8, 2))])):
+        w.lens, w.row_start = upto, np.concatenate([[0], np.cumsum(n_rows)]).tolist()
+        w.T = w.row_start[-1]
+        w.rows = ref.rows_of(5, w.T, w.row_start)
+        w.append(dtype)
+        w.check_cache()
+        for out in (torch.float32, torch.bfloat16):
+            # every token of every sequence
+            full = np.concatenate([[0], np.cumsum(upto)]).tolist()
+            got = fq.kv_cache_read(w.cache, *w.args(), full[-1], row_start=i32(full), dtype=out)
+            want = ref.read(w.ref, P, w.pages, upto, ref.rows_of(5, full[-1], full), full[-1])
+            assert np.array_equal(got.double().cpu().numpy(), want)
+    assert fq.get_status() == 0
+
+
+@pytest.mark.parametrize("n,rows", [(1, 1), (3, 2), (70, 1), (2, 130), (5, 33)])
+def test_append_of_equal_rows(n, rows):
+    w = World(0, 64, 32, 2, 2, [rows + (37 * s) % 101 for s in range(n)], rows=rows, seed=n)
+    w.fill()
+    w.append()
+    w.check_cache()
+    got = fq.kv_cache_read(w.cache, *w.args(), w.T, dtype=torch.float32)
+    assert np.array_equal(got.double().cpu().numpy(), ref.read(w.ref, w.P, w.pages, w.lens, w.rows, w.T))
+
+
+def test_append_of_many_ragged_sequences():
+    """Sequences with no rows between others, in blocks of rows that begin inside pages; a batch longer than a search of one step."""
+    rng = np.random.default_rng(4)
+    ragged = rng.integers(0, 6, 1100).tolist()
+    ragged[500] = 200
+    lens = [r + int(rng.integers(0, 40)) for r in ragged]
+    w = World(0, 64, 16, 1, 1, lens, ragged=ragged, seed=5, behind=9)
+    w.fill()
+    w.append()
+    w.check_cache()
+    kv = torch.full((w.T, 2 * 64), 7.0, device="cuda")
+    fq.kv_cache_read(w.cache, *w.args(), w.T, row_start=w.start(), kv=kv)
+    want = ref.read(w.ref, w.P, w.pages, w.lens, w.rows, w.T)
+    assert np.array_equal(kv.double().cpu().numpy(), np.where(np.isnan(want), 7.0, want))
+
+
+def test_scales_grow_and_small_values_follow():
+    """A page whose later tokens are larger by powers of two from 1 to 2^40, then by none."""
+    for fmt in (0, 1):
+        w = World(fmt, 64, 16, 0, 1, [16], seed=9)
+        for t, grow in enumerate([0, 1, 1, 3, 8, 8, 9, 17, 40, 40, 0, 2]):
+            w.lens = [t + 1]
+            x = w.rng.standard_normal((1, 2, 64)) * 2.0 ** grow
+            d = torch.tensor(x, dtype=torch.float32).cuda()
+            fq.kv_cache_append(w.cache, d.reshape(1, -1), i32(w.pages), i32(w.lens), 0)
+            ref.append(w.ref, fmt, 16, w.pages, w.lens, [(0, 1)], d.double().cpu().numpy().reshape(1, 2, 1, 64))
+            w.check_cache()
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_scale_rule_at_its_borders(fmt):
+    """amax on, just above and just below fmax 2^X, the largest and smallest fp32 values, zero."""
+    f = np.float32(ref.FMAX[fmt])
+    vals = [f, np.nextafter(f, np.float32(np.inf)), np.nextafter(f, np.float32(0)), f / 2, np.float32(1.75), np.float32(0),
+            np.finfo(np.float32).max, np.float32(2.0 ** -149), np.float32(2.0 ** -126), np.float32(3e-39), np.float32(1e-30)]
+    n = len(vals)
+    w = World(fmt, 64, 16, 0, 1, [1] * n, seed=1)
+    x = np.zeros((n, 2, 1, 64), np.float32)
+    x[:, 0, 0, 3], x[:, 1, 0, 60] = vals, [-v for v in vals]
+    fq.kv_cache_append(w.cache, torch.tensor(x).cuda().reshape(n, -1), i32(w.pages), i32(w.lens), 0)
+    ref.append(w.ref, fmt, 16, w.pages, w.lens, w.rows, x.astype(float))
+    w.check_cache()
+
+
+def test_values_that_are_not_finite_are_marked_and_spoil_no_other():
+    fq.get_status(clear=True)
+    w = World(0, 64, 16, 2, 2, [20, 5], rows=4, seed=3)
+    w.fill()
+    t, x = w.qkv()
+    t[1, 2 * 64 + 5] = float("inf")     # first K head, second row
+    t[2, 5 * 64 + 1] = float("nan")     # second V head, third row
+    t[5, 3 * 64:4 * 64] = float("nan")  # a whole K head of a row
+    fq.kv_cache_append(w.cache, t, *w.args(), 2)
+    x = t.double().cpu().numpy().reshape(8, 6, 64)
+    ref.append(w.ref, 0, 16, w.pages, w.lens, w.rows, x[:, 2:].reshape(-1, 2, 2, 64))
+    w.check_cache()
+    assert fq.get_status(clear=True) == fq.STATUS_NONFINITE
+    # rows before the NaN tokens, and heads without one, are what they were
+    att, lse = fq.attention_cached(w.cache, t, *w.args(), 2)
+    torch.cuda.synchronize()
+    a = att.float().view(8, 2, 64)
+    assert torch.isfinite(a[0]).all() and torch.isfinite(a[4]).all()
+    assert torch.isnan(a[1:4, 0]).all() and torch.isfinite(a[1, 1]).all()  # K head 0 holds a NaN in token 17
+    assert torch.isnan(a[2:4, 1, 1]).all() and torch.isfinite(a[2:4, 1, 2:]).all()  # V head 1: one column
+    assert torch.isnan(a[5:, 1]).all() and torch.isfinite(a[5:, 0]).all()
+
+
+ATTEND = [  # dh, P, hq, hkv, lens, rows, ragged
+    (128, 64, 4, 2, [1], 1, None),
+    (128, 64, 40, 8, [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 500], 1, None),
+    (128, 128, 28, 4, [1000, 1, 0, 257, 0], 1, None),
+    (64, 16, 12, 12, [5, 100, 17, 333], None, [3, 0, 1, 6]),
+    (96, 32, 10, 2, [40, 7, 200], 7, None),
+    (128, 16, 16, 1, [300, 3, 4], 4, None),          # 64 rows of a head; a sequence shorter than its rows
+    (64, 128, 40, 2, [70, 130], 3, None),            # 60 rows of a head
+    (128, 64, 5, 1, [260, 90], None, [150, 90]),     # a piece of a prompt, a whole prompt
+    (96, 64, 1, 1, [1030], 1, None),
+    (64, 32, 6, 6, [2100, 1, 900], None, [1, 1, 130]),
+    (128, 32, 33, 1, [129, 64], 2, None),
+]
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("case", range(len(ATTEND)))
+def test_attention_matches_its_definition(case, fmt):
+    dh, P, hq, hkv, lens, rows, ragged = ATTEND[case]
+    fq.get_status(clear=True)
+    w = World(fmt, dh, P, hq, hkv, lens, rows=rows, ragged=ragged, seed=case, behind=0 if ragged is None else 3)
+    w.fill()
+    t, x = w.append()
+    w.check_cache()
+    w.attend(t, x)
+    assert fq.get_status() == 0
+
+
+def test_rows_behind_the_last_sequence_are_left_as_they_were():
+    w = World(0, 128, 32, 6, 2, [50, 9], ragged=[3, 2], behind=4, seed=2)
+    w.fill()
+    t, x = w.append()
+    att = torch.full((w.T, 6 * 128), 3.0, device="cuda").bfloat16()
+    lse = torch.full((6, w.T), 5.0, device="cuda")
+    w.attend(t, x, att=att, lse=lse)
+    assert (att[5:] == 3).all() and (lse[:, 5:] == 5).all()
+
+
+def test_pages_of_very_different_sizes():
+    """V pages 2^20 apart, and K so that the probable keys are those of the small pages: each keeps its own precision."""
+    w = World(0, 64, 16, 2, 1, [200], rows=1, seed=11, wide=False)
+    before = 199
+    x = w.rng.standard_normal((before, 2, 1, 64))
+    size = np.exp2(np.repeat(w.rng.integers(-10, 11, 13), 16)[:before])
+    x[:, 1] *= size[:, None, None]
+    d = torch.tensor(x, dtype=torch.float32).cuda()
+    fq.kv_cache_append(w.cache, d.reshape(before, -1), i32(w.pages), i32([before]), 0)
+    ref.append(w.ref, 0, 16, w.pages, [before], [(0, before)], d.double().cpu().numpy())
+    t, q = w.append()
+    w.attend(t, q)
+
+
+def test_sharp_and_flat_probabilities():
+    """Scores of +-60 (one key takes all), and of zero (every key alike); many keys far below the largest."""
+    for std in (8.0, 0.0):
+        w = World(0, 128, 64, 4, 2, [700, 65], rows=1, seed=12)
+        w.fill()
+        w.append()
+        t, x = w.qkv(std=std)
+        w.attend(t, x)
+    # a first key 20 above 5000 equal ones
+    w = World(0, 64, 64, 1, 1, [5000], rows=1, seed=13)
+    k = np.zeros((5000, 2, 1, 64))
+    k[0, 0, 0, 0] = 20.0
+    k[:, 1] = w.rng.standard_normal((5000, 1, 64))
+    d = torch.tensor(k, dtype=torch.float32).cuda()
+    fq.kv_cache_append(w.cache, d.reshape(5000, -1), i32(w.pages), i32([5000]), 0)
+    ref.append(w.ref, 0, 64, w.pages, [5000], [(0, 5000)], d.double().cpu().numpy())
+    q = torch.zeros((1, 3 * 64), device="cuda").bfloat16()
+    for big in (8.0, 4.0):
+        q[0, 0] = big
+        w.attend(q, q.double().cpu().numpy().reshape(1, 3, 64))
+
+
+def test_q_of_any_size():
+    """q from the smallest to the largest magnitudes of bf16, with small elements beside large ones; K so that scores stay finite."""
+    for std in (2.0 ** -120, 2.0 ** -30, 2.0 ** 20, 2.0 ** 100):
+        w = World(0, 64, 16, 2, 1, [40], rows=1, seed=14, wide=False)
+        k = w.rng.standard_normal((40, 2, 1, 64))
+        k[:, 0] /= std
+        d = torch.tensor(k, dtype=torch.float32).cuda()
+        fq.kv_cache_append(w.cache, d.reshape(40, -1), i32(w.pages), i32([40]), 0)
+        ref.append(w.ref, 0, 16, w.pages, [40], [(0, 40)], d.double().cpu().numpy())
+        x = w.rng.standard_normal((1, 4, 64)) * np.exp2(w.rng.integers(-12, 1, (1, 4, 64)).astype(float)) * std
+        q = torch.tensor(x, dtype=torch.float64).to(torch.bfloat16).cuda()
+        w.attend(q.reshape(1, -1), q.double().cpu().numpy())
+
+
+@pytest.mark.parametrize("n,length,hkv,hq", [(1, 20000, 1, 5), (1, 4000, 8, 8), (40, 700, 2, 2), (300, 40, 1, 1)])
+def test_work_split_over_the_keys(n, length, hkv, hq):
+    """Long sequences cut over many blocks, and more sequences than blocks."""
+    w = World(0, 128, 64, hq, hkv, [max(1, length - 13 * s) for s in range(n)], rows=1, seed=n)
+    w.fill()
+    t, x = w.append()
+    a1 = w.attend(t, x)
+    a2 = fq.attention_cached(w.cache, t, *w.args(), hq)
+    assert all(torch.equal(a, b) for a, b in zip(a1, a2))
+
+
+def test_bad_pages_lengths_and_rows_are_reported_and_touch_nothing_else():
+    """Invalid tables are turned into the status bit by the kernels' own checks."""
+    w = World(0, 128, 32, 4, 2, [100, 70, 33], ragged=[2, 3, 1], seed=6)
+    w.fill()
+    t, x = w.append()
+    good = fq.attention_cached(w.cache, t, *w.args(), 4, row_start=w.start())
+    kv_good = fq.kv_cache_read(w.cache, *w.args(), w.T, row_start=w.start())
+    torch.cuda.synchronize()
+    keep = [c.clone() for c in (w.cache.k, w.cache.v, w.cache.k_scale, w.cache.v_scale)]
+    fq.get_status(clear=True)
+    for bad_page in (-5, w.cache.n_pages, 2 ** 31 - 1, -2 ** 31):
+        p = w.pages.copy()
+        p[0, 1] = bad_page                     # a page in the middle: its tokens are not seen
+        p[1, 2] = bad_page                     # the page of the second sequence's rows (tokens 67 .. 69)
+        fq.kv_cache_append(w.cache, t, i32(p), i32(w.lens), 4, row_start=w.start())
+        att, lse = fq.attention_cached(w.cache, t, i32(p), i32(w.lens), 4, row_start=w.start())
+        kv = fq.kv_cache_read(w.cache, i32(p), i32(w.lens), w.T, row_start=w.start())
+        torch.cuda.synchronize()
+        assert fq.get_status(clear=True) == fq.STATUS_BAD_CACHE
+        assert all(torch.equal(a, b) for a, b in zip(keep, (w.cache.k, w.cache.v, w.cache.k_scale, w.cache.v_scale)))
+        assert (kv[2:5] == 0).all() and torch.equal(kv[:2], kv_good[:2]) and torch.equal(kv[5:], kv_good[5:])
+        assert torch.equal(att[5:], good[0][5:])
+        saved, w.pages = w.pages, p
+        w.check_attention(att, lse, x[:, :4])
+        w.pages = saved
+    for lens in ([100, -1, 33], [100, 32 * w.pages.shape[1] + 1, 33], [100, 2 ** 31 - 1, 33], [100, -2 ** 31, 33]):
+        fq.kv_cache_append(w.cache, t, i32(w.pages), i32(lens), 4, row_start=w.start())
+        att, lse = fq.attention_cached(w.cache, t, i32(w.pages), i32(lens), 4, row_start=w.start())
+        kv = fq.kv_cache_read(w.cache, i32(w.pages), i32(lens), w.T, row_start=w.start())
+        torch.cuda.synchronize()
+        assert fq.get_status(clear=True) == fq.STATUS_BAD_CACHE
+        assert (att[2:5] == 0).all() and torch.isneginf(lse[:, 2:5]).all() and (kv[2:5] == 0).all()
+        assert torch.equal(att[:2], good[0][:2]) and torch.equal(att[5:], good[0][5:])
+        assert all(torch.equal(a, b) for a, b in zip(keep, (w.cache.k, w.cache.v, w.cache.k_scale, w.cache.v_scale)))
+    for start in ([0, 2, 9, 9], [-3, 2, 5, 6], [0, 2, 1, 6], [0, 2, 2 ** 31 - 1, -2 ** 31], [2 ** 31 - 1] * 4):
+        fq.attention_cached(w.cache, t, i32(w.pages), i32(w.lens), 4, row_start=i32(start))
+        fq.kv_cache_read(w.cache, i32(w.pages), i32(w.lens), w.T, row_start=i32(start))
+        scratch = fq.KvCache(w.cache.k.clone(), w.cache.v.clone(), w.cache.k_scale.clone(), w.cache.v_scale.clone())
+        fq.kv_cache_append(scratch, t, i32(w.pages), i32(w.lens), 4, row_start=i32(start))
+        torch.cuda.synchronize()
+        status = fq.get_status(clear=True)
+        if start == [0, 2, 1, 6] or start[0] == 2 ** 31 - 1:  # decreasing rows may go unreported; no row of the call is anyone's
+            assert status in (0, fq.STATUS_BAD_CACHE)
+        else:
+            assert status == fq.STATUS_BAD_CACHE
+
+
+def test_pages_past_32_bits():
+    """A cache of over 4 GB for K: the last pages are written, read and attended to."""
+    n_pages = (1 << 32) // (64 * 128 * 4) + 5
+    cache = fq.KvCache.allocate(n_pages, 4, 128, 64)
+    pages = i32([[n_pages - 1, 3, n_pages - 2]])
+    g = torch.Generator(device="cuda").manual_seed(1)
+    qkv = torch.randn((150, 12 * 128), generator=g, device="cuda").bfloat16()
+    fq.kv_cache_append(cache, qkv, pages, i32([150]), 4)
+    small = fq.KvCache.allocate(3, 4, 128, 64)
+    fq.kv_cache_append(small, qkv, i32([[0, 1, 2]]), i32([150]), 4)
+    for a, b in ((cache.k, small.k), (cache.v, small.v), (cache.k_scale, small.k_scale), (cache.v_scale, small.v_scale)):
+        assert torch.equal(a[pages[0].long()], b) and int(a[:3].count_nonzero()) == 0
+    a1, a2 = (fq.attention_cached(c, qkv, p, i32([150]), 4) for c, p in ((cache, pages), (small, i32([[0, 1, 2]]))))
+    assert torch.equal(a1[0], a2[0]) and torch.equal(a1[1], a2[1])
+    assert torch.equal(fq.kv_cache_read(cache, pages, i32([150]), 150), fq.kv_cache_read(small, i32([[0, 1, 2]]), i32([150]), 150))
+
+
+def test_sequences_may_share_pages_that_they_read():
+    w = World(0, 64, 16, 2, 1, [40], rows=1, seed=8)
+    w.fill()
+    t, x = w.append()
+    one = fq.attention_cached(w.cache, t, *w.args(), 2)
+    two = fq.attention_cached(w.cache, t.repeat(3, 1), i32(np.repeat(w.pages, 3, 0)), i32([40] * 3), 2)
+    assert all(torch.equal(two[0][i], one[0][0]) and torch.equal(two[1][:, i], one[1][:, 0]) for i in range(3))
+    back = fq.kv_cache_read(w.cache, i32(np.repeat(w.pages, 3, 0)), i32([40] * 3), 60)
+    assert torch.equal(back[:20], back[20:40]) and torch.equal(back[:20], back[40:])
+
+
+def test_a_step_taken_back_is_overwritten():
+    """Drafted tokens that were not accepted: the length goes back, the next tokens take their slots."""
+    w = World(0, 64, 16, 2, 1, [30], rows=6, seed=21)
+    w.fill()
+    w.append()
+    w.lens, w.T = [27], 2
+    w.rows = ref.rows_of(1, 2, None)
+    t, x = w.append()
+    w.check_cache()
+    w.attend(t, x)
+
+
+def test_entry_points_refuse():
+    c = fq.KvCache.allocate(4, 2, 64, 16)
+    q = torch.zeros((2, 8 * 64), device="cuda").bfloat16()
+    p, n = i32([[0, 1], [2, 3]]), i32([3, 4])
+    for call in (lambda **k: fq.kv_cache_append(**{**dict(cache=c, qkv=q, pages=p, lens=n, n_heads=4), **k}),
+                 lambda **k: fq.attention_cached(**{**dict(cache=c, qkv=q, pages=p, lens=n, n_heads=4), **k})):
+        call()
+        for bad in (dict(qkv=q[:, :64].contiguous()), dict(qkv=q.cpu()), dict(qkv=q[0]), dict(qkv=q.t()), dict(pages=p.long()),
+                    dict(pages=p[0]), dict(pages=p.t()), dict(lens=n.long()), dict(lens=n[:1]), dict(lens=[3, 4]),
+                    dict(row_start=n), dict(row_start=i32([0, 1, 2]).long()), dict(n_heads=3), dict(qkv=q.half()), dict(pages=None)):
+            with pytest.raises((ValueError, TypeError)):
+                call(**bad)
+        with pytest.raises(fq.Fp8qError):
+            call(qkv=torch.zeros((3, 8 * 64), device="cuda").bfloat16())  # 3 rows of 2 sequences
+    with pytest.raises(TypeError):
+        fq.attention_cached(c, q.float(), p, n, 4)
+    with pytest.raises(TypeError):
+        fq.kv_cache_read(c, p, n, 2, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        fq.kv_cache_read(c, p, n, 2, kv=torch.empty((2, 64), device="cuda"))
+    with pytest.raises(ValueError):
+        fq.attention_cached(c, q, p, n, 4, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        fq.attention_cached(c, q, p, n, 4, att=torch.empty((2, 64), device="cuda").bfloat16())
+    with pytest.raises(fq.Fp8qError):
+        fq.kv_cache_read(c, p, n, 0)
+    for bad in (dict(k=c.k[:, :, :8]), dict(k_scale=c.k_scale.int()), dict(v=c.v[:2]), dict(v=c.v.cpu()), dict(fmt=3)):
+        with pytest.raises((ValueError, TypeError)):
+            fq.KvCache(**{**dict(k=c.k, v=c.v, k_scale=c.k_scale, v_scale=c.v_scale), **bad})
+
+
+def test_copies_of_a_cache_are_their_own():
+    w = World(0, 64, 16, 2, 1, [20], rows=1, seed=15)
+    w.fill()
+    t, x = w.append()
+    want = fq.attention_cached(w.cache, t, *w.args(), 2)
+    other = copy.deepcopy(w.cache)
+    w.cache.k.zero_()
+    for c in (other, pickle.loads(pickle.dumps(other))):
+        got = fq.attention_cached(c, t, *w.args(), 2)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_calls_on_another_stream_and_in_graphs():
+    """stream=; a captured step replayed with new lengths; two graphs with workspaces of their own at once."""
+    w = World(0, 128, 64, 8, 2, [130, 64, 1], rows=1, seed=16, extra=4)
+    w.fill()
+    t, x = w.append()
+    args = w.args()
+    want = w.attend(t, x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = fq.attention_cached(w.cache, t, *args, 8, stream=side)
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    graphs, outs = [], []
+    with torch.cuda.stream(side):
+        fq.kv_cache_append(w.cache, t, *args, 8)
+    side.synchronize()
+    for _ in range(2):
+        ws = torch.empty(fq.attention_cached_workspace_size(w.cache, 3, 3, 8), dtype=torch.uint8, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(fq.attention_cached(w.cache, t, *args, 8, ws=ws) + (fq.kv_cache_read(w.cache, *args, 3), ws))
+        graphs.append(g)
+    for lens in ([130, 64, 1], [100, 3, 0]):
+        args[1].copy_(i32(lens))
+        torch.cuda.synchronize()
+        for g in graphs:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                g.replay()
+        torch.cuda.synchronize()
+        eager = fq.attention_cached(w.cache, t, *args, 8) + (fq.kv_cache_read(w.cache, *args, 3),)
+        for o in outs:
+            assert all(torch.equal(a, b) for a, b in zip(o, eager))
+
+
+def test_a_sequence_run_token_by_token():
+    """rope, append and attention as a program uses them: a prompt through attention_fwd and into the cache, then tokens one
+    at a time; each against attention over the values that the cache holds.  The prompt's last token is also attended to over the cache: it
+    differs from attention_fwd's by the codes' rounding.  V's is at most 2^-4 of each value, and as independent from value to value as
+    they are, so it moves the sum by at most 2^-4 of itself; K's moves a score by at most 2^-4 of its own spread (about 0.7^2), and the sum
+    by that much: together below 2 2^-4."""
+    S, hq, hkv, steps = 256, 8, 2, 20
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rope = fq.Rope.make()
+    w = World(0, 128, 64, hq, hkv, [S + steps] * 2, rows=1, seed=17)
+    qkv = (0.7 * torch.randn((2 * S, (hq + 2 * hkv) * 128), generator=g, device="cuda")).bfloat16()
+    pos = torch.arange(S, device="cuda").repeat(2).int()
+    qkv = fq.rope_fwd(qkv, pos, rope, hq, hkv, out=qkv)
+    att, _ = fq.attention_fwd(qkv, S, hq, hkv)
+    w.lens, w.T = [S, S], 2 * S
+    w.rows = ref.rows_of(2, 2 * S, None)
+    fq.kv_cache_append(w.cache, qkv, *w.args(), hq)
+    host = qkv.double().cpu().numpy().reshape(2 * S, -1, 128)
+    ref.append(w.ref, 0, 64, w.pages, w.lens, w.rows, host[:, hq:].reshape(-1, 2, hkv, 128))
+    w.check_cache()
+    last = qkv[[S - 1, 2 * S - 1]].contiguous()
+    cached, _ = fq.attention_cached(w.cache, last, *w.args(), hq)
+    off = (cached.float() - att[[S - 1, 2 * S - 1]].float()).norm() / att[[S - 1, 2 * S - 1]].float().norm()
+    assert float(off) < 2 * 2.0 ** -4
+    lens = i32([S, S])
+    for i in range(steps):
+        lens += 1
+        w.lens, w.T = [S + i + 1] * 2, 2
+        w.rows = ref.rows_of(2, 2, None)
+        t = (0.7 * torch.randn((2, (hq + 2 * hkv) * 128), generator=g, device="cuda")).bfloat16()
+        t = fq.rope_fwd(t, lens - 1, rope, hq, hkv)
+        x = t.double().cpu().numpy().reshape(2, -1, 128)
+        fq.kv_cache_append(w.cache, t, i32(w.pages), lens, hq)
+        ref.append(w.ref, 0, 64, w.pages, w.lens, w.rows, x[:, hq:].reshape(-1, 2, hkv, 128))
+        got = fq.attention_cached(w.cache, t, i32(w.pages), lens, hq)
+        w.check_attention(*got, x[:, :hq])
+    w.check_cache()
