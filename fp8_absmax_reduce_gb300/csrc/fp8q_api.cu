@@ -1573,7 +1573,8 @@ int kv_cache_read(const fp8q_kv_cache* cache, const int32_t* pages, int64_t n_se
 }
 
 size_t attention_cached_workspace_size(const fp8q_kv_cache* cache, int64_t T, int64_t n_seqs, int n_heads) {
-  if (validate_cache(cache) || !kv_sizes_ok(T, n_seqs) || !kv_heads_ok(cache, n_heads)) return 0;
+  if (validate_cache(cache) || !kv_sizes_ok(T, n_seqs) || !kv_heads_ok(cache, n_heads) || T * n_heads > INT32_MAX)
+    return 0;
   return round256(kv_attend_workspace_bytes(T, (int)n_seqs, n_heads, cache->n_kv_heads, cache->head_dim));
 }
 
@@ -1583,7 +1584,8 @@ int attention_cached(const fp8q_kv_cache* cache, const int32_t* pages, int64_t n
   KvArgs a;
   int e = kv_args(&a, cache, pages, n_seqs, max_pages, lens, row_start, T);
   if (e) return e;
-  if (!kv_heads_ok(cache, n_heads) || !al16(qkv) || !al16(att) || !al4(lse)) return FP8Q_ERR_INVALID_ARG;
+  if (!kv_heads_ok(cache, n_heads) || T * n_heads > INT32_MAX || !al16(qkv) || !al16(att) || !al4(lse))
+    return FP8Q_ERR_INVALID_ARG;
   if ((e = check_ws(ws, ws_bytes, attention_cached_workspace_size(cache, T, n_seqs, n_heads)))) return e;
   Ctx c;
   if ((e = make_ctx(&c, stream))) return e;

@@ -1,96 +1,647 @@
-// Causal attention of a few rows a sequence over the 8-bit key/value cache.
+// Causal attention of a call's last tokens over the 8-bit key/value cache.
+//
+// The cache is read once and each byte of it meets 16 rows or more (the query heads that share a K/V head, times the call's tokens), 32
+// operations a byte: bound by memory.  Tensor memory's accumulators of 128 rows would stand mostly empty, and their operands
+// would have to go through shared memory a second time as fp16; so the products are warp-level
+// m16n8k16 ones, whose operands are made in registers, and FP8 codes become fp16 (exactly) on the way from shared memory.
+//
+// A warp has 16 rows and 32 keys at a time.  Both products allow any order of their contraction, and of their
+// columns, as long as both operands share it, and that decides the layout:
+//   S = Q K^T: a thread's share of a key is head_dim / 4 consecutive bytes; word i of it is its operand of step i.
+//   O = P V: column c of tile t stands for element c head_dim / 8 + t, so a thread's share of a key is head_dim / 8 consecutive bytes, and
+//   its share of O is head_dim / 4 consecutive elements of two rows.
+// P leaves S's accumulators as the second product's operand, with no exchange between threads.
+//
+// Precision.  Scores are fp32 in the log2 domain.  q is divided by a power of two of its row and so is exact in fp16 (elements
+// below 2^-28 of the row's largest lose bits).  p = 2^(s - m) enters as fp16 times 2^15, so it has 11 bits down to 2^-29 of the
+// row's largest and vanishes below 2^-39.  V's scales are relative to the largest so far (xref), which moves like the
+// maximum does, and p times that ratio is what is rounded.
+//
+// Work.  The keys of all (sequence, row tile, K/V head) units form one line of blocks of 128 keys, cut into equal
+// parts, one a CTA; a unit that is cut leaves fp32 partial results, which the second kernel joins in order.
 #include <cuda_fp16.h>
 
+#include "fp8q_head.cuh"
 #include "fp8q_kv.cuh"
 
 namespace fp8q {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128, kWarps = 4, kBlockKeys = 128;
+constexpr int kCtasPerSm = 3, kMaxCtas = 152 * kCtasPerSm;
+constexpr int kNoPage = 0x1000;   // in place of a scale: the keys are not seen
+constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
 
-__device__ __forceinline__ float block_reduce(float v, float* red, bool is_max) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float w = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    v = is_max ? fmaxf(v, w) : v + w;
+// What CTA j leaves behind when it begins a unit and does not end it.
+struct Cut {
+  int64_t first, end;  // the unit's blocks on the line; first = end: nothing
+  int64_t total;       // of the line
+  int ctas;            // parts of the line
+  int head;            // K/V head
+  int row0, rows;      // first row of the call, and rows (tokens times heads) of the tile
+  int group_row;       // the tile's first (token, head) pair
+};
+
+struct AttendArgs {
+  KvArgs kv;
+  const uint16_t* qkv;
+  int n_heads;
+  float scale_log2;  // log2(e) / sqrt(head_dim)
+  uint16_t* att;
+  float* lse;
+  float* part_o;     // [2 kMaxCtas][R][DH]
+  float* part_lse;   // [2 kMaxCtas][R], log2
+  Cut* cuts;         // [kMaxCtas]
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// 16 bytes into shared memory; bytes = 0 writes zeros and reads nothing.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Offset of byte `b` (of a 16-byte piece) of a row in a tile of rows of DH codes.  Rows of 128: piece ^ row % 8; of 64: two rows to a
+// line of 128, piece ^ twice the line % 4; with these, and with rows of 96 as they are, the K reads of a
+// quarter of a warp, and the V reads of 128 and 64, touch every bank once.
+template <int DH>
+__device__ __forceinline__ uint32_t place(int row, int b) {
+  if (DH == 128) return (uint32_t)(row * 128 + ((((b >> 4) ^ row) & 7) << 4) + (b & 15));
+  if (DH == 64) {
+    const int line = row >> 1, piece = (row & 1) * 4 + (b >> 4);
+    return (uint32_t)(line * 128 + ((piece ^ ((line & 3) << 1)) << 4) + (b & 15));
   }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float r = red[0];
-  for (int i = 1; i < kThreads / 32; ++i) r = is_max ? fmaxf(r, red[i]) : r + red[i];
-  return r;
+  return (uint32_t)(row * 96 + b);
 }
 
-// One block: one row and one query head.  128 keys at a time: a key a thread for the scores, a column a thread for the sum.
+// N / 4 words of a row from byte b on.
+template <int DH, int N>
+__device__ __forceinline__ void take(const uint8_t* tile, int row, int b, uint32_t (&w)[N / 4]) {
+  if (N % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 16; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4*>(tile + place<DH>(row, b + 16 * i));
+      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+    }
+  } else if (N % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+      const uint2 v = *reinterpret_cast<const uint2*>(tile + place<DH>(row, b + 8 * i));
+      w[2 * i] = v.x; w[2 * i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(tile + place<DH>(row, b + 4 * i));
+  }
+}
+
+// Whether any of four codes is NaN or infinite.
 template <int FMT>
-__global__ void __launch_bounds__(kThreads) k_kv_attend_rows(const KvArgs a, const uint16_t* __restrict__ qkv, int n_heads,
-                                                             float scale, uint16_t* att, float* lse) {
-  __shared__ float q[128], p[kThreads], red[4];
-  __shared__ int ids[kThreads];
-  const int row = blockIdx.x, h = blockIdx.y, g = h / (n_heads / a.hkv), t = threadIdx.x;
-  const int s = kv_find(a, row);
-  if (s < 0) return;
-  const KvSeq sq = kv_seq(a, s);
-  if (row < sq.first || row >= sq.first + sq.n) return;
-  const int keys = max(0, sq.pos(row) + 1);
-  if (t < a.dh)
-    q[t] = __uint_as_float((uint32_t)qkv[(int64_t)row * (n_heads + 2 * a.hkv) * a.dh + h * a.dh + t] << 16);
-  float m = -INFINITY, l = 0.0f, o = 0.0f;
-  for (int k0 = 0; k0 < keys; k0 += kThreads) {
+__device__ __forceinline__ uint32_t nonfinite4(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + (FMT == 0 ? 0x01010101u : 0x04040404u)) & 0x80808080u;
+}
+
+template <int DH, int RW>
+struct Shape {
+  static constexpr int KW = kWarps / RW;      // groups of warps that share their keys
+  static constexpr int GK = 32 * RW;          // keys of a group at a time
+  static constexpr int R = 16 * RW;           // rows of the CTA
+  static constexpr int kTile = kBlockKeys * DH;
+  static constexpr int kRing = 2 * 2 * kTile; // two stages of K and V
+  static constexpr int kPitch = DH + 4;       // floats of a row of partial O
+  static constexpr int kJoin = KW * R * kPitch * 4;
+  static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+};
+
+// Where a CTA's part of the line begins: every CTA adds the line up by itself.
+struct Line {
+  int s;         // the sequence
+  int64_t base;  // its first block
+};
+template <int R>
+__device__ __forceinline__ int64_t seq_blocks(const AttendArgs& p, const KvSeq& q, int& units, int& nb) {
+  const int64_t pairs = (int64_t)q.n * (p.n_heads / p.kv.hkv);
+  units = (int)((pairs + R - 1) / R) * p.kv.hkv;
+  nb = max(1, (q.len + kBlockKeys - 1) / kBlockKeys);
+  return (int64_t)units * nb;
+}
+
+template <int FMT, int DH, int RW>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const AttendArgs p) {
+  using C = Shape<DH, RW>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t warp_sums[kWarps];
+  __shared__ Line line_s;
+  __shared__ int scales[2][kWarps][4];  // [stage][part of 32 keys][2 K, 2 V scales of 16 keys each]
+  __shared__ float row_m[kWarps][16], row_l[kWarps][16];
+  __shared__ int row_x[kWarps];
+  start_dependents();
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, c = lane & 3, g8 = lane >> 2;
+  const int kg = warp / RW, rw = warp % RW;
+  const int G = p.n_heads / p.kv.hkv;
+
+  // ---- the line, and this CTA's part of it
+  const int per = (p.kv.n_seqs + kThreads - 1) / kThreads;
+  int64_t total = 0, before = 0, own;  // the line; the blocks of the sequences before this thread's, and of its own
+  {
+    int64_t sum = 0;
+    for (int s = t * per; s < min((t + 1) * per, p.kv.n_seqs); ++s) {
+      int units, nb;
+      sum += seq_blocks<C::R>(p, kv_seq(p.kv, s), units, nb);
+    }
+    int64_t upto = sum;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, k);
+      if (lane >= k) upto += v;
+    }
+    if (lane == 31) warp_sums[warp] = upto;
     __syncthreads();
-    const int key = k0 + t;
-    float x = -INFINITY;
-    int id = -1;
-    if (key < keys) id = kv_page(a, s, key >> a.page_shift);
-    if (id >= 0) {
-      const int64_t ph = (int64_t)id * a.hkv + g;
-      const uint8_t* kp = a.k + ((ph << a.page_shift) + (key & ((1 << a.page_shift) - 1))) * a.dh;
-      x = 0.0f;
-      for (int c = 0; c < a.dh; c += 2) {
-        const uint32_t w = f16x2_of<FMT>(*reinterpret_cast<const uint16_t*>(kp + c));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-        x += f.x * q[c] + f.y * q[c + 1];
-      }
-      x *= e8m0(a.k_scale[ph]) * scale;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      before += w < warp ? warp_sums[w] : 0;
+      total += warp_sums[w];
     }
-    ids[t] = id;
-    const float mn = fmaxf(m, block_reduce(x, red, true));
-    const float ref = mn == -INFINITY ? 0.0f : mn;
-    const float w = expf(x - ref), fade = expf(m - ref);
-    p[t] = w;
-    l = l * fade + block_reduce(w, red, false);
-    o *= fade;
-    m = mn;
-    if (t < a.dh) {
-      for (int k = 0; k < kThreads; ++k) {
-        if (ids[k] < 0) continue;
-        const int64_t ph = (int64_t)ids[k] * a.hkv + g;
-        const uint32_t v = a.v[((ph << a.page_shift) + ((k0 + k) & ((1 << a.page_shift) - 1))) * a.dh + t];
-        const uint32_t f = f16x2_of<FMT>(v);
-        o += p[k] * __low2float(*reinterpret_cast<const __half2*>(&f)) * e8m0(a.v_scale[ph]);
+    before += upto - sum;
+    own = sum;
+  }
+  const int ctas = (int)min((int64_t)gridDim.x, total);
+  const int j = blockIdx.x;
+  if (t == 0) p.cuts[j].first = p.cuts[j].end = 0;
+  if (j >= ctas) return;
+  const int64_t begin = total * j / ctas, end = total * (j + 1) / ctas;
+  if (begin >= before && begin < before + own) {
+    int64_t base = before;
+    int s = t * per;
+    for (; s < p.kv.n_seqs - 1; ++s) {
+      int units, nb;
+      const int64_t n = seq_blocks<C::R>(p, kv_seq(p.kv, s), units, nb);
+      if (begin < base + n) break;
+      base += n;
+    }
+    line_s.s = s;
+    line_s.base = base;
+  }
+  __syncthreads();
+  int s = line_s.s;
+  int64_t base = line_s.base, at = begin;
+
+  while (at < end && s < p.kv.n_seqs) {
+    const KvSeq q = kv_seq(p.kv, s);
+    int units, nb;
+    const int64_t n_blocks = seq_blocks<C::R>(p, q, units, nb);
+    if (at >= base + n_blocks) {
+      base += n_blocks;
+      ++s;
+      continue;
+    }
+    // ---- one segment: blocks [b0, b1) of unit u
+    const int u = (int)((at - base) / nb), b0 = (int)((at - base) % nb);
+    const int b1 = (int)min((int64_t)nb, b0 + (end - at));
+    const int64_t unit0 = base + (int64_t)u * nb;
+    at += b1 - b0;
+    const int rt = u / p.kv.hkv, h = u % p.kv.hkv;
+    const int r0 = rt * C::R, pairs = q.n * G;
+    const int n_rows = min(C::R, pairs - r0);
+    // rows of this thread: limit = the keys that a row sees; rows that do not exist see all and are dropped
+    int limit[2], token[2], head[2];
+    float rscale[2];
+    uint32_t qa[DH / 16][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = rw * 16 + g8 + 8 * e, r = r0 + i;
+      const bool real = i < n_rows;
+      token[e] = real ? r / G : 0;
+      head[e] = real ? r - token[e] * G : 0;
+      limit[e] = real ? q.len - q.n + token[e] + 1 : 0x7FFFFFFF;
+    }
+    const int kmin = __reduce_min_sync(0xFFFFFFFFu, min(limit[0], limit[1]));
+    int kmax = max(limit[0] == 0x7FFFFFFF ? 0 : limit[0], limit[1] == 0x7FFFFFFF ? 0 : limit[1]);
+    kmax = __reduce_max_sync(0xFFFFFFFFu, kmax);                                   // of the warp
+    const int klim = max(0, q.len - q.n + (r0 + n_rows - 1) / G + 1);              // of the CTA
+    const int stop = min(b1, (klim + kBlockKeys - 1) / kBlockKeys);
+    int exq[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const bool real = rw * 16 + g8 + 8 * e < n_rows;
+      const uint16_t* src = p.qkv + (int64_t)(q.first + token[e]) * (p.n_heads + 2 * p.kv.hkv) * DH +
+                            (int64_t)(h * G + head[e]) * DH + c * (DH / 4);
+      uint32_t w[DH / 8];
+#pragma unroll
+      for (int i = 0; i < DH / 32; ++i) {
+        const uint4 v = real ? ld_nc_v4(src + 8 * i) : make_uint4(0, 0, 0, 0);
+        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+      }
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < DH / 8; ++i) m = max(m, absmax_bf16x2(w[i]));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      const int ex = max((int)(m >> 23) - 127, -110);  // the row's largest |q| < 2^(ex + 1)
+      const float f = pow2i(14 - ex);
+#pragma unroll
+      for (int i = 0; i < DH / 16; ++i) {
+        qa[i][e] = pack_half2(bf16_lo(w[2 * i]) * f, bf16_hi(w[2 * i]) * f);
+        qa[i][e + 2] = pack_half2(bf16_lo(w[2 * i + 1]) * f, bf16_hi(w[2 * i + 1]) * f);
+      }
+      exq[e] = ex - 14;
+      rscale[e] = p.scale_log2;
+    }
+    float o[DH / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    int xref = -1000;
+#pragma unroll
+    for (int i = 0; i < DH / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
+
+    // ---- the ring: this warp copies its part of 32 keys of its group's tile
+    const int64_t table = (int64_t)s * p.kv.max_pages;
+    const int my_keys = kg * C::GK + rw * 32;  // within a block
+    auto page_of = [&](int b, int sub) {       // the page of 16 keys: -1 none (behind the limit), -2 reported
+      const int key = b * kBlockKeys + my_keys + 16 * sub;
+      if (b >= stop || key >= klim) return -1;
+      const int id = p.kv.pages[table + (key >> p.kv.page_shift)];
+      if (id >= 0 && id < p.kv.n_pages) return id;
+      atomicOr(p.kv.status, kStatusBadCache);
+      return -1;
+    };
+    auto scale_of = [&](const int (&id)[2]) {  // lanes 0 .. 3: K of both, V of both
+      const int i = id[lane & 1];
+      if (i < 0 || lane >= 4) return kNoPage;
+      return (int)(lane & 2 ? p.kv.v_scale : p.kv.k_scale)[(int64_t)i * p.kv.hkv + h] - 127;
+    };
+    auto copy_tile = [&](int b, const int (&id)[2], int sc, int stage) {
+      const int key = b * kBlockKeys + my_keys;
+      if (lane < 4) scales[stage][warp][lane] = sc;
+      const int slot = key & ((1 << p.kv.page_shift) - 1);
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        const int sl = (slot + 16 * sub) & ((1 << p.kv.page_shift) - 1);
+        const int64_t off = id[sub] < 0 ? 0 : ((((int64_t)id[sub] * p.kv.hkv + h) << p.kv.page_shift) + sl) * DH;
+        const int rows = id[sub] < 0 ? 0 : min(16, klim - key - 16 * sub);
+#pragma unroll
+        for (int i = 0; i < DH / 32; ++i) {
+          const int lin = (i * 32 + lane) * 16, row = lin / DH, byte = lin - row * DH;
+          const int bytes = row < rows ? 16 : 0;
+          const uint32_t to = smem_addr(smem) + (uint32_t)(stage * 2 * C::kTile + kg * C::GK * DH) +
+                              place<DH>(rw * 32 + 16 * sub + row, byte);
+          copy16(to, p.kv.k + off + (bytes ? lin : 0), bytes);
+          copy16(to + C::kTile, p.kv.v + off + (bytes ? lin : 0), bytes);
+        }
+      }
+    };
+    auto group_sync = [&]() {
+      if (RW == 1) __syncwarp();
+      else asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(32 * RW) : "memory");
+    };
+
+    int id_a[2], id_b[2], sc_a;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) id_a[i] = page_of(b0, i);
+    sc_a = scale_of(id_a);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) id_b[i] = page_of(b0 + 1, i);
+    auto next = [&](int b) {  // copies block b's keys; a step ahead its successor's scales, two ahead the pages
+      if (b < stop) copy_tile(b, id_a, sc_a, (b - b0) & 1);
+      copies_commit();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) id_a[i] = id_b[i];
+      sc_a = scale_of(id_a);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) id_b[i] = page_of(b + 2, i);
+    };
+    next(b0);
+#pragma unroll 1
+    for (int b = b0; b < stop; ++b) {
+      next(b + 1);
+      copies_wait<1>();
+      group_sync();
+      const int stage = (b - b0) & 1;
+#pragma unroll 1
+      for (int part = 0; part < RW; ++part) {
+        const int key0 = b * kBlockKeys + kg * C::GK + part * 32;
+        if (key0 >= kmax) break;
+        const uint8_t* kt = smem + stage * 2 * C::kTile + kg * C::GK * DH;
+        const uint8_t* vt = kt + C::kTile;
+        const int row0 = part * 32;
+        const int* sc = scales[stage][kg * RW + part];
+        const int xk[2] = {sc[0], sc[1]}, xv[2] = {sc[2], sc[3]};
+        float z[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          uint32_t w[DH / 16];
+          take<DH, DH / 4>(kt, row0 + 8 * n + g8, c * (DH / 4), w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[n][e] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < DH / 16; ++i) mma16816(z[n], qa[i], f16x2_of<FMT>(w[i]), f16x2_of<FMT>(w[i] >> 16));
+        }
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+          const float f0 = rscale[0] * pow2i(exq[0] + xk[sub]), f1 = rscale[1] * pow2i(exq[1] + xk[sub]);
+#pragma unroll
+          for (int n = 2 * sub; n < 2 * sub + 2; ++n) {
+            z[n][0] *= f0; z[n][1] *= f0; z[n][2] *= f1; z[n][3] *= f1;
+          }
+        }
+        const bool edge = key0 + 32 > kmin || xk[0] == kNoPage || xk[1] == kNoPage;
+        if (edge) {
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + 8 * n + 2 * c + (e & 1);
+              if (key >= limit[e >> 1] || xk[n >> 1] == kNoPage) z[n][e] = -INFINITY;
+            }
+        }
+        float mn[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = m[e];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) x = fmaxf(x, fmaxf(z[n][2 * e], z[n][2 * e + 1]));
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
+          mn[e] = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+        }
+        const int xv0 = xv[0] == kNoPage ? -1000 : xv[0], xv1 = xv[1] == kNoPage ? -1000 : xv[1];
+        const int xnew = max(xref, max(xv0, xv1));
+        if (__any_sync(0xFFFFFFFFu, mn[0] != m[0] || mn[1] != m[1] || xnew != xref)) {
+          const float fx = pow2i(xref - xnew);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float fade = mn[e] == m[e] ? 1.0f : ex2(m[e] - mn[e]);
+            l[e] *= fade;
+            const float fo = fade * fx;
+#pragma unroll
+            for (int i = 0; i < DH / 8; ++i) {
+              o[i][2 * e] *= fo;
+              o[i][2 * e + 1] *= fo;
+            }
+            m[e] = mn[e];
+          }
+          xref = xnew;
+        }
+        const float ref0 = m[0] == -INFINITY ? 0.0f : m[0], ref1 = m[1] == -INFINITY ? 0.0f : m[1];
+        const float fv[2] = {pow2i(15 + xv0 - xref), pow2i(15 + xv1 - xref)};
+        uint32_t pa[2][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const float p0 = ex2(z[n][0] - ref0), p1 = ex2(z[n][1] - ref0), p2 = ex2(z[n][2] - ref1), p3 = ex2(z[n][3] - ref1);
+          l[0] += p0 + p1;
+          l[1] += p2 + p3;
+          const float f = fv[n >> 1];
+          pa[n >> 1][(n & 1) * 2] = pack_half2(p0 * f, p1 * f);
+          pa[n >> 1][(n & 1) * 2 + 1] = pack_half2(p2 * f, p3 * f);
+        }
+        // the keys of step ks: rows 2c, 2c + 1, 2c + 8, 2c + 9 of its 16
+        uint32_t odd = 0;
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t w[DH / 32];
+            take<DH, DH / 8>(vt, row0 + (i >> 2) * 16 + 2 * c + (i & 1) + (i & 2) * 4, g8 * (DH / 8), w);
+#pragma unroll
+            for (int k = 0; k < DH / 32; ++k) odd |= nonfinite4<FMT>(w[k]);
+          }
+          odd = __any_sync(0xFFFFFFFFu, odd != 0);
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          uint32_t w[4][DH / 32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            take<DH, DH / 8>(vt, row0 + ks * 16 + 2 * c + (i & 1) + (i >> 1) * 8, g8 * (DH / 8), w[i]);
+          if (!odd) {
+#pragma unroll
+            for (int k = 0; k < DH / 32; ++k) {
+              const uint32_t a0 = __byte_perm(w[0][k], w[1][k], 0x5140), a1 = __byte_perm(w[0][k], w[1][k], 0x7362);
+              const uint32_t e0 = __byte_perm(w[2][k], w[3][k], 0x5140), e1 = __byte_perm(w[2][k], w[3][k], 0x7362);
+              mma16816(o[4 * k], pa[ks], f16x2_of<FMT>(a0), f16x2_of<FMT>(e0));
+              mma16816(o[4 * k + 1], pa[ks], f16x2_of<FMT>(a0 >> 16), f16x2_of<FMT>(e0 >> 16));
+              mma16816(o[4 * k + 2], pa[ks], f16x2_of<FMT>(a1), f16x2_of<FMT>(e1));
+              mma16816(o[4 * k + 3], pa[ks], f16x2_of<FMT>(a1 >> 16), f16x2_of<FMT>(e1 >> 16));
+            }
+          } else {
+            // Some V is NaN or infinite, and some row does not see every key: a masked key's weight of 0 times it would be
+            // NaN.  Such values become 0, and a second product of ones finds the rows that do see one.
+            uint32_t ones[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + ks * 16 + 2 * c + (e >> 1) * 8;
+              const int lim = xk[ks] == kNoPage ? 0 : limit[e & 1];
+              ones[e] = (key < lim ? 0x3C00u : 0u) | (key + 1 < lim ? 0x3C000000u : 0u);
+            }
+#pragma unroll
+            for (int k = 0; k < DH / 32; ++k)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t b[2], n[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t v = f16x2_of<FMT>(__byte_perm(w[2 * e][k], w[2 * e + 1][k], (uint32_t)(i | (4 + i) << 4)));
+                  const uint32_t bad = (((v & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u) >> 15;
+                  b[e] = v & ~(bad * 0xFFFFu);
+                  n[e] = bad * 0x3C00u;
+                }
+                float seen[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                mma16816(seen, ones, n[0], n[1]);
+                mma16816(o[4 * k + i], pa[ks], b[0], b[1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (seen[e] != 0.0f) o[4 * k + i][e] = __uint_as_float(0x7FC00000u);
+              }
+          }
+        }
+      }
+      group_sync();
+    }
+    copies_wait<0>();
+
+    // ---- join the groups' results: through the ring's memory
+    __syncthreads();
+    float* join = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
+      if (c == 0) {
+        row_m[warp][g8 + 8 * e] = m[e];
+        row_l[warp][g8 + 8 * e] = l[e];
+      }
+      float* to = join + (kg * C::R + rw * 16 + g8 + 8 * e) * C::kPitch + c * (DH / 4);
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int i = 0; i < DH / 32; ++i)
+          *reinterpret_cast<float4*>(to + half * (DH / 8) + 4 * i) =
+              make_float4(o[4 * i][2 * e + half], o[4 * i + 1][2 * e + half], o[4 * i + 2][2 * e + half], o[4 * i + 3][2 * e + half]);
+    }
+    if (lane == 0) row_x[warp] = xref;
+    __syncthreads();
+    const bool whole = b0 == 0 && b1 == nb, starts = b0 == 0;
+    const int slot = 2 * j + (starts ? 1 : 0);
+    for (int i = t; i < n_rows * (DH / 4); i += kThreads) {
+      const int r = i / (DH / 4), col = (i - r * (DH / 4)) * 4;
+      float M = -INFINITY;
+      int X = -1000;
+#pragma unroll
+      for (int k = 0; k < C::KW; ++k) {
+        M = fmaxf(M, row_m[k * RW + r / 16][r & 15]);
+        X = max(X, row_x[k * RW + r / 16]);
+      }
+      float L = 0.0f, a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < C::KW; ++k) {
+        const int w = k * RW + r / 16;
+        const float mk = row_m[w][r & 15];
+        const float f = mk == M ? (M == -INFINITY ? 0.0f : 1.0f) : ex2(mk - M);
+        L += row_l[w][r & 15] * (row_l[w][r & 15] != row_l[w][r & 15] ? 1.0f : f);
+        const float fo = f * pow2i(row_x[w] - X);
+        const float4 v = *reinterpret_cast<const float4*>(join + (k * C::R + r) * C::kPitch + col);
+        a[0] += v.x * fo; a[1] += v.y * fo; a[2] += v.z * fo; a[3] += v.w * fo;
+      }
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L, fx = pow2i(X);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a[k] = L == 0.0f ? 0.0f : a[k] * 0x1p-15f * inv * fx;
+      const float lse2 = L == 0.0f ? -INFINITY : M + log2f(L);
+      if (whole) {
+        const int tok = (r0 + r) / G, hd = h * G + (r0 + r) - tok * G;
+        *reinterpret_cast<uint2*>(p.att + ((int64_t)(q.first + tok) * p.n_heads + hd) * DH + col) =
+            make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+        if (col == 0) p.lse[(int64_t)hd * p.kv.T + q.first + tok] = lse2 * kLn2;
+      } else {
+        *reinterpret_cast<float4*>(p.part_o + ((int64_t)slot * C::R + r) * DH + col) = make_float4(a[0], a[1], a[2], a[3]);
+        if (col == 0) p.part_lse[slot * C::R + r] = lse2;
       }
     }
+    if (t == 0 && starts && !whole)
+      p.cuts[j] = Cut{unit0, unit0 + nb, total, ctas, h, q.first, n_rows, r0};
+    __syncthreads();
   }
-  if (t < a.dh) {
-    const uint16_t bits = (uint16_t)pack_bf16x2(l == 0.0f ? 0.0f : o / l, 0.0f);
-    att[((int64_t)row * n_heads + h) * a.dh + t] = bits;
+}
+
+// Block (j, r): row r of the unit that CTA j began and did not end.  Its parts in order: CTA j's last, then the first of
+// those after it; a warp takes every fourth.
+template <int DH, int R>
+__global__ void __launch_bounds__(kThreads) k_kv_join(const AttendArgs p) {
+  __shared__ float acc_s[kWarps][DH], sum_s[kWarps];
+  wait_for_previous();
+  const int j = blockIdx.x, r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Cut cut = p.cuts[j];
+  if (cut.first == cut.end || r >= cut.rows) return;
+  // the last CTA of the unit: the one whose part holds block end - 1
+  int last = j + 1;
+  while (last + 1 < cut.ctas && cut.total * (last + 1) / cut.ctas < cut.end) ++last;
+  const int n = last - j + 1;
+  auto slot = [&](int i) { return i == 0 ? 2 * j + 1 : 2 * (j + i); };
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_lse[slot(i) * R + r]);
+#pragma unroll
+  for (int k = 16; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, k));
+  float acc[DH / 32], sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < DH / 32; ++k) acc[k] = 0.0f;
+#pragma unroll 4
+  for (int i = warp; i < n; i += kWarps) {
+    const float e = p.part_lse[slot(i) * R + r];
+    const float w = e == -INFINITY ? 0.0f : ex2(e - M);
+    const float* src = p.part_o + ((int64_t)slot(i) * R + r) * DH + lane;
+    sum += w;
+#pragma unroll
+    for (int k = 0; k < DH / 32; ++k) acc[k] += w * src[32 * k];
   }
-  if (t == 0) lse[(int64_t)h * a.T + row] = m + logf(l);
+#pragma unroll
+  for (int k = 0; k < DH / 32; ++k) acc_s[warp][lane + 32 * k] = acc[k];
+  if (lane == 0) sum_s[warp] = sum;
+  __syncthreads();
+  const int G = p.n_heads / p.kv.hkv, tok = (cut.group_row + r) / G, hd = cut.head * G + (cut.group_row + r) - tok * G;
+  const float total = sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3];
+  if (threadIdx.x < DH / 2) {
+    float v[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int col = 2 * threadIdx.x + k;
+      const float a = acc_s[0][col] + acc_s[1][col] + acc_s[2][col] + acc_s[3][col];
+      v[k] = total == 0.0f ? 0.0f : a / total;
+    }
+    *reinterpret_cast<uint32_t*>(p.att + ((int64_t)(cut.row0 + tok) * p.n_heads + hd) * DH + 2 * threadIdx.x) = pack_bf16x2(v[0], v[1]);
+  }
+  if (threadIdx.x == 0) p.lse[(int64_t)hd * p.kv.T + cut.row0 + tok] = total == 0.0f ? -INFINITY : (M + log2f(total)) * kLn2;
+}
+
+// Groups of 16 rows of a CTA: as many as a sequence's (token, head) pairs fill, four at most.
+int row_groups(int64_t T, int n_seqs, int n_heads, int hkv) {
+  const int64_t pairs = (T + n_seqs - 1) / n_seqs * (n_heads / hkv);
+  return pairs <= 16 ? 1 : pairs <= 32 ? 2 : 4;
+}
+struct Pieces {
+  size_t lse, cuts, all;
+};
+Pieces pieces(int rw, int dh) {
+  auto pad = [](size_t n) { return (n + 255) & ~size_t(255); };
+  Pieces w;
+  w.lse = pad((size_t)2 * kMaxCtas * 16 * rw * dh * 4);
+  w.cuts = w.lse + pad((size_t)2 * kMaxCtas * 16 * rw * 4);
+  w.all = w.cuts + pad(sizeof(Cut) * kMaxCtas);
+  return w;
+}
+
+template <int FMT, int DH, int RW>
+cudaError_t launch(const AttendArgs& p, int ctas, int join_rows, cudaStream_t s) {
+  using C = Shape<DH, RW>;
+  cudaError_t e = cudaFuncSetAttribute(k_kv_attend<FMT, DH, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  k_kv_attend<FMT, DH, RW><<<ctas, kThreads, C::kSmem, s>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_dependent(k_kv_join<DH, C::R>, dim3((unsigned)ctas, (unsigned)min(join_rows, C::R)), kThreads, 0, s, p);
+}
+template <int FMT, int DH>
+cudaError_t launch_rw(int rw, const AttendArgs& p, int ctas, int join_rows, cudaStream_t s) {
+  return rw == 1 ? launch<FMT, DH, 1>(p, ctas, join_rows, s)
+                 : rw == 2 ? launch<FMT, DH, 2>(p, ctas, join_rows, s) : launch<FMT, DH, 4>(p, ctas, join_rows, s);
 }
 
 }  // namespace
 
-size_t kv_attend_workspace_bytes(int64_t, int, int, int, int) { return 256; }
+size_t kv_attend_workspace_bytes(int64_t T, int n_seqs, int n_heads, int hkv, int dh) {
+  return pieces(row_groups(T, n_seqs, n_heads, hkv), dh).all;
+}
 
-cudaError_t launch_kv_attend(const KvArgs& a, const uint16_t* qkv, int n_heads, uint16_t* att, float* lse, void*,
+cudaError_t launch_kv_attend(const KvArgs& a, const uint16_t* qkv, int n_heads, uint16_t* att, float* lse, void* ws,
                              const Launch& L) {
-  const dim3 grid((unsigned)a.T, (unsigned)n_heads);
-  (a.fmt ? k_kv_attend_rows<1> : k_kv_attend_rows<0>)<<<grid, kThreads, 0, L.stream>>>(a, qkv, n_heads, 1.0f / sqrtf((float)a.dh),
-                                                                                      att, lse);
-  if (L.launches) ++*L.launches;
-  return cudaGetLastError();
+  const int rw = row_groups(a.T, a.n_seqs, n_heads, a.hkv);
+  const Pieces w = pieces(rw, a.dh);
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  AttendArgs p{a, qkv, n_heads, kLog2e / sqrtf((float)a.dh), att, lse, reinterpret_cast<float*>(b),
+               reinterpret_cast<float*>(b + w.lse), reinterpret_cast<Cut*>(b + w.cuts)};
+  const int ctas = min(kMaxCtas, L.num_sms * kCtasPerSm);
+  const int64_t pairs = a.row_start ? 1 << 20 : (int64_t)a.rows * (n_heads / a.hkv);
+  const int join_rows = (int)min(pairs, (int64_t)(16 * rw));
+  cudaError_t e;
+  if (a.dh == 128) e = a.fmt ? launch_rw<1, 128>(rw, p, ctas, join_rows, L.stream) : launch_rw<0, 128>(rw, p, ctas, join_rows, L.stream);
+  else if (a.dh == 96) e = a.fmt ? launch_rw<1, 96>(rw, p, ctas, join_rows, L.stream) : launch_rw<0, 96>(rw, p, ctas, join_rows, L.stream);
+  else e = a.fmt ? launch_rw<1, 64>(rw, p, ctas, join_rows, L.stream) : launch_rw<0, 64>(rw, p, ctas, join_rows, L.stream);
+  if (e != cudaSuccess) return e;
+  if (L.launches) *L.launches += 2;
+  return cudaSuccess;
 }
 
 }  // namespace fp8q

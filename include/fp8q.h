@@ -589,7 +589,8 @@ FP8Q_API int kv_cache_read(const fp8q_kv_cache* cache, const int32_t* pages, int
  * Scores, maxima, sums and accumulators are fp32; codes and q enter the tensor cores without loss (fp16, q over a power
  * of two of its row), the probabilities as fp16 relative to the row's maximum (2^-11 of each, at least 2^-39 of the
  * maximum).  Slots behind a sequence's last token may hold anything.  Deterministic.
- * Workspace: attention_cached_workspace_size bytes (0 for sizes outside the limits), 256-byte aligned. */
+ * Requirement besides those above: T n_heads < 2^31.  Workspace: attention_cached_workspace_size bytes (0 for sizes outside
+ * the limits), 256-byte aligned. */
 FP8Q_API size_t attention_cached_workspace_size(const fp8q_kv_cache* cache, int64_t T, int64_t n_seqs, int n_heads);
 FP8Q_API int attention_cached(const fp8q_kv_cache* cache, const int32_t* pages, int64_t n_seqs, int64_t max_pages,
                               const int32_t* lens, const int32_t* row_start, const void* qkv, int64_t T, int n_heads,
