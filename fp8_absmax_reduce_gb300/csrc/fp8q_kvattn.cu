@@ -17,8 +17,8 @@
 // row's largest and vanishes below 2^-39.  V's scales are relative to the largest so far (xref), which moves like the
 // maximum does, and p times that ratio is what is rounded.
 //
-// Work.  The keys of all (sequence, row tile, K/V head) units form one line of blocks of 128 keys, cut into equal
-// parts, one a CTA; a unit that is cut leaves fp32 partial results, which the second kernel joins in order.
+// Work.  The keys of all (sequence, row tile, K/V head) units form one line of blocks of 128 keys, each unit preceded by what it costs
+// besides; it is cut into equal parts, one a CTA.  A unit that is cut leaves fp32 partial results, which the second kernel joins in order.
 #include <cuda_fp16.h>
 
 #include "fp8q_head.cuh"
@@ -35,7 +35,7 @@ constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
 
 // What CTA j leaves behind when it begins a unit and does not end it.
 struct Cut {
-  int64_t first, end;  // the unit's blocks on the line; first = end: nothing
+  int64_t first, end;  // the unit on the line; first = end: nothing
   int64_t total;       // of the line
   int ctas;            // parts of the line
   int head;            // K/V head
@@ -74,6 +74,9 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 // 16 bytes into shared memory; bytes = 0 writes zeros and reads nothing.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -131,17 +134,21 @@ struct Shape {
   static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
 };
 
+// What a unit costs besides its keys, in blocks of keys: its rows, its first page, joining the warps.
+constexpr int kUnitCost = 3;
+
 // Where a CTA's part of the line begins: every CTA adds the line up by itself.
 struct Line {
   int s;         // the sequence
   int64_t base;  // its first block
 };
 template <int R>
-__device__ __forceinline__ int64_t seq_blocks(const AttendArgs& p, const KvSeq& q, int& units, int& nb) {
+__device__ __forceinline__ int64_t seq_cost(const AttendArgs& p, const KvSeq& q, int& units, int& nb, int& cost) {
   const int64_t pairs = (int64_t)q.n * (p.n_heads / p.kv.hkv);
   units = (int)((pairs + R - 1) / R) * p.kv.hkv;
-  nb = max(1, (q.len + kBlockKeys - 1) / kBlockKeys);
-  return (int64_t)units * nb;
+  nb = (q.len + kBlockKeys - 1) / kBlockKeys;
+  cost = nb ? nb + kUnitCost : 1;
+  return (int64_t)units * cost;
 }
 
 template <int FMT, int DH, int RW>
@@ -164,8 +171,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
   {
     int64_t sum = 0;
     for (int s = t * per; s < min((t + 1) * per, p.kv.n_seqs); ++s) {
-      int units, nb;
-      sum += seq_blocks<C::R>(p, kv_seq(p.kv, s), units, nb);
+      int units, nb, cost;
+      sum += seq_cost<C::R>(p, kv_seq(p.kv, s), units, nb, cost);
     }
     int64_t upto = sum;
 #pragma unroll
@@ -192,8 +199,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
     int64_t base = before;
     int s = t * per;
     for (; s < p.kv.n_seqs - 1; ++s) {
-      int units, nb;
-      const int64_t n = seq_blocks<C::R>(p, kv_seq(p.kv, s), units, nb);
+      int units, nb, cost;
+      const int64_t n = seq_cost<C::R>(p, kv_seq(p.kv, s), units, nb, cost);
       if (begin < base + n) break;
       base += n;
     }
@@ -206,24 +213,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
 
   while (at < end && s < p.kv.n_seqs) {
     const KvSeq q = kv_seq(p.kv, s);
-    int units, nb;
-    const int64_t n_blocks = seq_blocks<C::R>(p, q, units, nb);
-    if (at >= base + n_blocks) {
-      base += n_blocks;
+    int units, nb, cost;
+    const int64_t here = seq_cost<C::R>(p, q, units, nb, cost);
+    if (at >= base + here) {
+      base += here;
       ++s;
       continue;
     }
-    // ---- one segment: blocks [b0, b1) of unit u
-    const int u = (int)((at - base) / nb), b0 = (int)((at - base) % nb);
-    const int b1 = (int)min((int64_t)nb, b0 + (end - at));
-    const int64_t unit0 = base + (int64_t)u * nb;
-    at += b1 - b0;
+    // ---- one segment: blocks [b0, b1) of unit u, whose own cost comes before its blocks
+    const int u = (int)((at - base) / cost), v0 = (int)((at - base) - (int64_t)u * cost);
+    const int v1 = (int)min((int64_t)cost, v0 + (end - at));
+    const int64_t unit0 = base + (int64_t)u * cost;
+    at += v1 - v0;
+    const int b0 = max(0, v0 - kUnitCost), b1 = max(0, v1 - kUnitCost);
+    if (b0 == b1 && nb) continue;
     const int rt = u / p.kv.hkv, h = u % p.kv.hkv;
     const int r0 = rt * C::R, pairs = q.n * G;
     const int n_rows = min(C::R, pairs - r0);
+    if (nb == 0) {  // an empty slot of a batch
+      for (int i = t; i < n_rows * (DH / 4); i += kThreads) {
+        const int r = i / (DH / 4), tok = (r0 + r) / G, hd = h * G + (r0 + r) - tok * G;
+        *reinterpret_cast<uint2*>(p.att + ((int64_t)(q.first + tok) * p.n_heads + hd) * DH + (i - r * (DH / 4)) * 4) = make_uint2(0, 0);
+        if (i == r * (DH / 4)) p.lse[(int64_t)hd * p.kv.T + q.first + tok] = -INFINITY;
+      }
+      continue;
+    }
     // rows of this thread: limit = the keys that a row sees; rows that do not exist see all and are dropped
     int limit[2], token[2], head[2];
-    float rscale[2];
     uint32_t qa[DH / 16][4];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -238,32 +254,104 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
     kmax = __reduce_max_sync(0xFFFFFFFFu, kmax);                                   // of the warp
     const int klim = max(0, q.len - q.n + (r0 + n_rows - 1) / G + 1);              // of the CTA
     const int stop = min(b1, (klim + kBlockKeys - 1) / kBlockKeys);
+    // ---- the ring: this warp copies its part of 32 keys of its group's tile
+    const int32_t* table = p.kv.pages + (int64_t)s * p.kv.max_pages;
+    const int my_keys = kg * C::GK + rw * 32;  // within a block
+    const int page_mask = (1 << p.kv.page_shift) - 1;
+    const uint32_t ring = smem_addr(smem) + (uint32_t)(kg * C::GK * DH);
+    // Lane k: the page of keys 16 (k % 2) .. of this warp's part; -1 where it is none, or behind the limit.
+    auto page_of = [&](int b) {
+      const int key = b * kBlockKeys + my_keys + 16 * (lane & 1);
+      if (b >= stop || key >= klim) return -1;
+      const int id = table[key >> p.kv.page_shift];
+      if (id >= 0 && id < p.kv.n_pages) return id;
+      atomicOr(p.kv.status, kStatusBadCache);
+      return -1;
+    };
+    auto scale_of = [&](int id) {  // lanes 0 .. 3: K of both, V of both
+      if (id < 0 || lane >= 4) return kNoPage;
+      return (int)(lane & 2 ? p.kv.v_scale : p.kv.k_scale)[(int64_t)id * p.kv.hkv + h] - 127;
+    };
+    auto copy_tile = [&](int b, int id_lane, int sc, int stage) {
+      const int key = b * kBlockKeys + my_keys;
+      const uint32_t to = ring + (uint32_t)(stage * 2 * C::kTile);
+      const bool full = key + 32 <= klim;
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        const int id = __shfl_sync(0xFFFFFFFFu, id_lane, sub);
+        const int sl = (key + 16 * sub) & page_mask;
+        const int64_t off = ((((int64_t)max(id, 0) * p.kv.hkv + h) << p.kv.page_shift) + sl) * DH;
+        const uint8_t *ks = p.kv.k + off + lane * 16, *vs = p.kv.v + off + lane * 16;
+        if (full && id >= 0) {
+#pragma unroll
+          for (int i = 0; i < DH / 32; ++i) {
+            const int lin = (i * 32 + lane) * 16, row = lin / DH, byte = lin - row * DH;
+            const uint32_t d = to + place<DH>(rw * 32 + 16 * sub + row, byte);
+            copy16(d, ks + i * 512);
+            copy16(d + C::kTile, vs + i * 512);
+          }
+        } else {  // rows that no row of the CTA sees become zero, and are not read
+          const int rows = id < 0 ? 0 : min(16, klim - key - 16 * sub);
+#pragma unroll 1
+          for (int i = 0; i < DH / 32; ++i) {
+            const int lin = (i * 32 + lane) * 16, row = lin / DH, byte = lin - row * DH;
+            const uint32_t d = to + place<DH>(rw * 32 + 16 * sub + row, byte);
+            const int bytes = row < rows ? 16 : 0;
+            copy16(d, bytes ? ks + i * 512 : p.kv.k, bytes);
+            copy16(d + C::kTile, bytes ? vs + i * 512 : p.kv.v, bytes);
+          }
+        }
+      }
+      if (lane < 4) scales[stage][warp][lane] = sc;
+    };
+    auto group_sync = [&]() {
+      if (RW == 1) __syncwarp();
+      else asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(32 * RW) : "memory");
+    };
+
+    uint32_t qw[2][DH / 8];
+    auto load_q = [&]() {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const bool real = rw * 16 + g8 + 8 * e < n_rows;
+        const uint16_t* src = p.qkv + (int64_t)(q.first + token[e]) * (p.n_heads + 2 * p.kv.hkv) * DH +
+                              (int64_t)(h * G + head[e]) * DH + c * (DH / 4);
+#pragma unroll
+        for (int i = 0; i < DH / 32; ++i) {
+          const uint4 v = real ? ld_nc_v4(src + 8 * i) : make_uint4(0, 0, 0, 0);
+          qw[e][4 * i] = v.x; qw[e][4 * i + 1] = v.y; qw[e][4 * i + 2] = v.z; qw[e][4 * i + 3] = v.w;
+        }
+      }
+    };
+    // The chain that a segment begins with is a page's number, then its keys (and its scales, which are stored after
+    // the copies are on their way); q is fetched beside it and made ready while the first keys arrive.
+    int id_a = page_of(b0), id_b = page_of(b0 + 1);
+    load_q();
+    int sc_a = scale_of(id_a);
+    auto next = [&](int b) {  // copies block b's keys; a step ahead its successor's scales, two ahead the pages
+      if (b < stop) copy_tile(b, id_a, sc_a, (b - b0) & 1);
+      copies_commit();
+      id_a = id_b;
+      sc_a = scale_of(id_a);
+      id_b = page_of(b + 2);
+    };
+    next(b0);
     int exq[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const bool real = rw * 16 + g8 + 8 * e < n_rows;
-      const uint16_t* src = p.qkv + (int64_t)(q.first + token[e]) * (p.n_heads + 2 * p.kv.hkv) * DH +
-                            (int64_t)(h * G + head[e]) * DH + c * (DH / 4);
-      uint32_t w[DH / 8];
-#pragma unroll
-      for (int i = 0; i < DH / 32; ++i) {
-        const uint4 v = real ? ld_nc_v4(src + 8 * i) : make_uint4(0, 0, 0, 0);
-        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-      }
       uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < DH / 8; ++i) m = max(m, absmax_bf16x2(w[i]));
+      for (int i = 0; i < DH / 8; ++i) m = max(m, absmax_bf16x2(qw[e][i]));
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
       const int ex = max((int)(m >> 23) - 127, -110);  // the row's largest |q| < 2^(ex + 1)
       const float f = pow2i(14 - ex);
 #pragma unroll
       for (int i = 0; i < DH / 16; ++i) {
-        qa[i][e] = pack_half2(bf16_lo(w[2 * i]) * f, bf16_hi(w[2 * i]) * f);
-        qa[i][e + 2] = pack_half2(bf16_lo(w[2 * i + 1]) * f, bf16_hi(w[2 * i + 1]) * f);
+        qa[i][e] = pack_half2(bf16_lo(qw[e][2 * i]) * f, bf16_hi(qw[e][2 * i]) * f);
+        qa[i][e + 2] = pack_half2(bf16_lo(qw[e][2 * i + 1]) * f, bf16_hi(qw[e][2 * i + 1]) * f);
       }
       exq[e] = ex - 14;
-      rscale[e] = p.scale_log2;
     }
     float o[DH / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
     int xref = -1000;
@@ -272,63 +360,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
 
-    // ---- the ring: this warp copies its part of 32 keys of its group's tile
-    const int64_t table = (int64_t)s * p.kv.max_pages;
-    const int my_keys = kg * C::GK + rw * 32;  // within a block
-    auto page_of = [&](int b, int sub) {       // the page of 16 keys: -1 none (behind the limit), -2 reported
-      const int key = b * kBlockKeys + my_keys + 16 * sub;
-      if (b >= stop || key >= klim) return -1;
-      const int id = p.kv.pages[table + (key >> p.kv.page_shift)];
-      if (id >= 0 && id < p.kv.n_pages) return id;
-      atomicOr(p.kv.status, kStatusBadCache);
-      return -1;
-    };
-    auto scale_of = [&](const int (&id)[2]) {  // lanes 0 .. 3: K of both, V of both
-      const int i = id[lane & 1];
-      if (i < 0 || lane >= 4) return kNoPage;
-      return (int)(lane & 2 ? p.kv.v_scale : p.kv.k_scale)[(int64_t)i * p.kv.hkv + h] - 127;
-    };
-    auto copy_tile = [&](int b, const int (&id)[2], int sc, int stage) {
-      const int key = b * kBlockKeys + my_keys;
-      if (lane < 4) scales[stage][warp][lane] = sc;
-      const int slot = key & ((1 << p.kv.page_shift) - 1);
-#pragma unroll
-      for (int sub = 0; sub < 2; ++sub) {
-        const int sl = (slot + 16 * sub) & ((1 << p.kv.page_shift) - 1);
-        const int64_t off = id[sub] < 0 ? 0 : ((((int64_t)id[sub] * p.kv.hkv + h) << p.kv.page_shift) + sl) * DH;
-        const int rows = id[sub] < 0 ? 0 : min(16, klim - key - 16 * sub);
-#pragma unroll
-        for (int i = 0; i < DH / 32; ++i) {
-          const int lin = (i * 32 + lane) * 16, row = lin / DH, byte = lin - row * DH;
-          const int bytes = row < rows ? 16 : 0;
-          const uint32_t to = smem_addr(smem) + (uint32_t)(stage * 2 * C::kTile + kg * C::GK * DH) +
-                              place<DH>(rw * 32 + 16 * sub + row, byte);
-          copy16(to, p.kv.k + off + (bytes ? lin : 0), bytes);
-          copy16(to + C::kTile, p.kv.v + off + (bytes ? lin : 0), bytes);
-        }
-      }
-    };
-    auto group_sync = [&]() {
-      if (RW == 1) __syncwarp();
-      else asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(32 * RW) : "memory");
-    };
-
-    int id_a[2], id_b[2], sc_a;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) id_a[i] = page_of(b0, i);
-    sc_a = scale_of(id_a);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) id_b[i] = page_of(b0 + 1, i);
-    auto next = [&](int b) {  // copies block b's keys; a step ahead its successor's scales, two ahead the pages
-      if (b < stop) copy_tile(b, id_a, sc_a, (b - b0) & 1);
-      copies_commit();
-#pragma unroll
-      for (int i = 0; i < 2; ++i) id_a[i] = id_b[i];
-      sc_a = scale_of(id_a);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) id_b[i] = page_of(b + 2, i);
-    };
-    next(b0);
 #pragma unroll 1
     for (int b = b0; b < stop; ++b) {
       next(b + 1);
@@ -354,14 +385,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
 #pragma unroll
           for (int i = 0; i < DH / 16; ++i) mma16816(z[n], qa[i], f16x2_of<FMT>(w[i]), f16x2_of<FMT>(w[i] >> 16));
         }
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-          const float f0 = rscale[0] * pow2i(exq[0] + xk[sub]), f1 = rscale[1] * pow2i(exq[1] + xk[sub]);
-#pragma unroll
-          for (int n = 2 * sub; n < 2 * sub + 2; ++n) {
-            z[n][0] *= f0; z[n][1] *= f0; z[n][2] *= f1; z[n][3] *= f1;
-          }
-        }
         const bool edge = key0 + 32 > kmin || xk[0] == kNoPage || xk[1] == kNoPage;
         if (edge) {
 #pragma unroll
@@ -372,12 +395,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
               if (key >= limit[e >> 1] || xk[n >> 1] == kNoPage) z[n][e] = -INFINITY;
             }
         }
-        float mn[2];
+        // the row's maximum: a page's scale is positive, so it goes to the page's maximum alone
+        float f[2][2], mn[2];  // [page][row]
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float x = m[e];
 #pragma unroll
-          for (int n = 0; n < 4; ++n) x = fmaxf(x, fmaxf(z[n][2 * e], z[n][2 * e + 1]));
+          for (int sub = 0; sub < 2; ++sub) {
+            f[sub][e] = p.scale_log2 * pow2i(max(exq[e] + xk[sub], -100));
+            const float y = fmaxf(fmaxf(z[2 * sub][2 * e], z[2 * sub][2 * e + 1]), fmaxf(z[2 * sub + 1][2 * e], z[2 * sub + 1][2 * e + 1]));
+            x = fmaxf(x, y * f[sub][e]);
+          }
           x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
           mn[e] = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
         }
@@ -399,17 +427,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
           }
           xref = xnew;
         }
-        const float ref0 = m[0] == -INFINITY ? 0.0f : m[0], ref1 = m[1] == -INFINITY ? 0.0f : m[1];
-        const float fv[2] = {pow2i(15 + xv0 - xref), pow2i(15 + xv1 - xref)};
+        // 2^(s - m + 15 + dx), dx the exponent of the page's V over xref.  The sum takes 2^dx back, so it holds for pages of any V;
+        // below 2^-60 nothing is left of one in fp16.
+        const int dx[2] = {max(xv0 - xref, -60), max(xv1 - xref, -60)};
+        float back[2], ref[2][2];
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+          back[sub] = pow2i(-dx[sub]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) ref[sub][e] = (float)(15 + dx[sub]) - (m[e] == -INFINITY ? 0.0f : m[e]);
+        }
         uint32_t pa[2][4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          const float p0 = ex2(z[n][0] - ref0), p1 = ex2(z[n][1] - ref0), p2 = ex2(z[n][2] - ref1), p3 = ex2(z[n][3] - ref1);
-          l[0] += p0 + p1;
-          l[1] += p2 + p3;
-          const float f = fv[n >> 1];
-          pa[n >> 1][(n & 1) * 2] = pack_half2(p0 * f, p1 * f);
-          pa[n >> 1][(n & 1) * 2 + 1] = pack_half2(p2 * f, p3 * f);
+          const int sub = n >> 1;
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            w[e] = ex2(__fmaf_rn(z[n][e], f[sub][e >> 1], ref[sub][e >> 1]));
+            l[e >> 1] = __fmaf_rn(w[e], back[sub], l[e >> 1]);
+          }
+          pa[sub][(n & 1) * 2] = pack_half2(w[0], w[1]);
+          pa[sub][(n & 1) * 2 + 1] = pack_half2(w[2], w[3]);
         }
         // the keys of step ks: rows 2c, 2c + 1, 2c + 8, 2c + 9 of its 16
         uint32_t odd = 0;
@@ -520,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
       }
       const float inv = L == 0.0f ? 0.0f : 1.0f / L, fx = pow2i(X);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) a[k] = L == 0.0f ? 0.0f : a[k] * 0x1p-15f * inv * fx;
-      const float lse2 = L == 0.0f ? -INFINITY : M + log2f(L);
+      for (int k = 0; k < 4; ++k) a[k] = L == 0.0f ? 0.0f : a[k] * inv * fx;
+      const float lse2 = L == 0.0f ? -INFINITY : M + (log2f(L) - 15.0f);
       if (whole) {
         const int tok = (r0 + r) / G, hd = h * G + (r0 + r) - tok * G;
         *reinterpret_cast<uint2*>(p.att + ((int64_t)(q.first + tok) * p.n_heads + hd) * DH + col) =
@@ -533,58 +572,78 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
       }
     }
     if (t == 0 && starts && !whole)
-      p.cuts[j] = Cut{unit0, unit0 + nb, total, ctas, h, q.first, n_rows, r0};
+      p.cuts[j] = Cut{unit0, unit0 + cost, total, ctas, h, q.first, n_rows, r0};
     __syncthreads();
   }
 }
 
 // Block (j, r): row r of the unit that CTA j began and did not end.  Its parts in order: CTA j's last, then the first of
-// those after it; a warp takes every fourth.
+// those after it; a warp takes every eighth, eight at a time in flight.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 template <int DH, int R>
-__global__ void __launch_bounds__(kThreads) k_kv_join(const AttendArgs p) {
-  __shared__ float acc_s[kWarps][DH], sum_s[kWarps];
+__global__ void __launch_bounds__(kJoinThreads) k_kv_join(const AttendArgs p) {
+  __shared__ float weight[kMaxCtas + 8 * kJoinWarps], acc_s[kJoinWarps][DH], max_s[kJoinWarps], sum_s[kJoinWarps];
   wait_for_previous();
-  const int j = blockIdx.x, r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int j = blockIdx.x, r = blockIdx.y, t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const Cut cut = p.cuts[j];
   if (cut.first == cut.end || r >= cut.rows) return;
-  // the last CTA of the unit: the one whose part holds block end - 1
-  int last = j + 1;
-  while (last + 1 < cut.ctas && cut.total * (last + 1) / cut.ctas < cut.end) ++last;
-  const int n = last - j + 1;
+  // the last CTA of the unit is the last whose part of the line begins before the unit's end: total i / ctas < end
+  const int n = (int)((cut.end * cut.ctas + cut.total - 1) / cut.total) - j;
   auto slot = [&](int i) { return i == 0 ? 2 * j + 1 : 2 * (j + i); };
   float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_lse[slot(i) * R + r]);
+  for (int i = t; i < n; i += kJoinThreads) {
+    weight[i] = p.part_lse[slot(i) * R + r];
+    M = fmaxf(M, weight[i]);
+  }
 #pragma unroll
   for (int k = 16; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, k));
+  if (lane == 0) max_s[warp] = M;
+  __syncthreads();
+  M = max_s[0];
+#pragma unroll
+  for (int k = 1; k < kJoinWarps; ++k) M = fmaxf(M, max_s[k]);
   float acc[DH / 32], sum = 0.0f;
 #pragma unroll
   for (int k = 0; k < DH / 32; ++k) acc[k] = 0.0f;
-#pragma unroll 4
-  for (int i = warp; i < n; i += kWarps) {
-    const float e = p.part_lse[slot(i) * R + r];
-    const float w = e == -INFINITY ? 0.0f : ex2(e - M);
-    const float* src = p.part_o + ((int64_t)slot(i) * R + r) * DH + lane;
-    sum += w;
+  for (int i0 = warp; i0 < n; i0 += 8 * kJoinWarps) {
+    float v[8][DH / 32], w[8];
 #pragma unroll
-    for (int k = 0; k < DH / 32; ++k) acc[k] += w * src[32 * k];
+    for (int q = 0; q < 8; ++q) {
+      const int i = i0 + q * kJoinWarps;
+      const bool in = i < n;
+      const float e = in ? weight[i] : -INFINITY;
+      w[q] = e == -INFINITY ? 0.0f : ex2(e - M);
+      const float* src = p.part_o + ((int64_t)slot(in ? i : 0) * R + r) * DH + lane;
+#pragma unroll
+      for (int k = 0; k < DH / 32; ++k) v[q][k] = in ? src[32 * k] : 0.0f;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      sum += w[q];
+#pragma unroll
+      for (int k = 0; k < DH / 32; ++k) acc[k] += w[q] * v[q][k];
+    }
   }
 #pragma unroll
   for (int k = 0; k < DH / 32; ++k) acc_s[warp][lane + 32 * k] = acc[k];
   if (lane == 0) sum_s[warp] = sum;
   __syncthreads();
   const int G = p.n_heads / p.kv.hkv, tok = (cut.group_row + r) / G, hd = cut.head * G + (cut.group_row + r) - tok * G;
-  const float total = sum_s[0] + sum_s[1] + sum_s[2] + sum_s[3];
-  if (threadIdx.x < DH / 2) {
+  float total = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kJoinWarps; ++k) total += sum_s[k];
+  if (t < DH / 2) {
     float v[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int col = 2 * threadIdx.x + k;
-      const float a = acc_s[0][col] + acc_s[1][col] + acc_s[2][col] + acc_s[3][col];
+      float a = 0.0f;
+#pragma unroll
+      for (int q = 0; q < kJoinWarps; ++q) a += acc_s[q][2 * t + k];
       v[k] = total == 0.0f ? 0.0f : a / total;
     }
-    *reinterpret_cast<uint32_t*>(p.att + ((int64_t)(cut.row0 + tok) * p.n_heads + hd) * DH + 2 * threadIdx.x) = pack_bf16x2(v[0], v[1]);
+    *reinterpret_cast<uint32_t*>(p.att + ((int64_t)(cut.row0 + tok) * p.n_heads + hd) * DH + 2 * t) = pack_bf16x2(v[0], v[1]);
   }
-  if (threadIdx.x == 0) p.lse[(int64_t)hd * p.kv.T + cut.row0 + tok] = total == 0.0f ? -INFINITY : (M + log2f(total)) * kLn2;
+  if (t == 0) p.lse[(int64_t)hd * p.kv.T + cut.row0 + tok] = total == 0.0f ? -INFINITY : (M + log2f(total)) * kLn2;
 }
 
 // Groups of 16 rows of a CTA: as many as a sequence's (token, head) pairs fill, four at most.
@@ -611,7 +670,7 @@ cudaError_t launch(const AttendArgs& p, int ctas, int join_rows, cudaStream_t s)
   if (e != cudaSuccess) return e;
   k_kv_attend<FMT, DH, RW><<<ctas, kThreads, C::kSmem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_dependent(k_kv_join<DH, C::R>, dim3((unsigned)ctas, (unsigned)min(join_rows, C::R)), kThreads, 0, s, p);
+  return launch_dependent(k_kv_join<DH, C::R>, dim3((unsigned)ctas, (unsigned)min(join_rows, C::R)), kJoinThreads, 0, s, p);
 }
 template <int FMT, int DH>
 cudaError_t launch_rw(int rw, const AttendArgs& p, int ctas, int join_rows, cudaStream_t s) {
