@@ -5,12 +5,13 @@
 // would have to go through shared memory a second time as fp16; so the products are warp-level
 // m16n8k16 ones, whose operands are made in registers, and FP8 codes become fp16 (exactly) on the way from shared memory.
 //
-// A warp has 16 rows and 32 keys at a time.  Both products allow any order of their contraction, and of their
-// columns, as long as both operands share it, and that decides the layout:
-//   S = Q K^T: a thread's share of a key is head_dim / 4 consecutive bytes; word i of it is its operand of step i.
-//   O = P V: column c of tile t stands for element c head_dim / 8 + t, so a thread's share of a key is head_dim / 8 consecutive bytes, and
-//   its share of O is head_dim / 4 consecutive elements of two rows.
-// P leaves S's accumulators as the second product's operand, with no exchange between threads.
+// A warp takes 32 keys at a time for 8 rows, or 16.  Keys are the products' long side (M = 16), rows the short one (N = 8), so the
+// few rows of a token's query heads fill what they use.  Both products allow any order of their contraction, and the second of
+// its rows, as long as both operands share it, and that decides the layout:
+//   S^T = K Q^T: a thread's share of a key is head_dim / 4 consecutive bytes; word i of it is its operand of step i.
+//   O^T = V^T P^T: rows g and g + 8 of tile i stand for elements g head_dim / 8 + 2 i and the next, so a thread's share of a key is
+//   head_dim / 8 consecutive bytes, and so is its share of a row of O.
+// P goes from the first product's accumulators to the second's operand through four 8 x 8 transposes.
 //
 // Precision.  Scores are fp32 in the log2 domain.  q is divided by a power of two of its row and so is exact in fp16 (elements
 // below 2^-28 of the row's largest lose bits).  p = 2^(s - m) enters as fp16 times 2^15, so it has 11 bits down to 2^-29 of the
@@ -29,7 +30,7 @@ namespace fp8q {
 namespace {
 
 constexpr int kThreads = 128, kWarps = 4, kBlockKeys = 128;
-constexpr int kCtasPerSm = 3, kMaxCtas = 152 * kCtasPerSm;
+constexpr int kMaxCtas = 152 * 5;
 constexpr int kNoPage = 0x1000;   // in place of a scale: the keys are not seen
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
 
@@ -122,16 +123,19 @@ __device__ __forceinline__ uint32_t nonfinite4(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + (FMT == 0 ? 0x01010101u : 0x04040404u)) & 0x80808080u;
 }
 
-template <int DH, int RW>
+template <int DH, int NT, int RW>
 struct Shape {
   static constexpr int KW = kWarps / RW;      // groups of warps that share their keys
   static constexpr int GK = 32 * RW;          // keys of a group at a time
-  static constexpr int R = 16 * RW;           // rows of the CTA
+  static constexpr int RT = 8 * NT;           // rows of a warp
+  static constexpr int R = RT * RW;           // rows of the CTA
   static constexpr int kTile = kBlockKeys * DH;
   static constexpr int kRing = 2 * 2 * kTile; // two stages of K and V
   static constexpr int kPitch = DH + 4;       // floats of a row of partial O
   static constexpr int kJoin = KW * R * kPitch * 4;
   static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+  // as many as shared memory and the registers of their accumulators allow
+  static constexpr int kCtas = NT == 1 ? (DH == 128 ? 3 : DH == 96 ? 4 : 5) : (DH == 64 ? 4 : 3);
 };
 
 // What a unit costs besides its keys, in blocks of keys: its rows, its first page, joining the warps.
@@ -140,25 +144,37 @@ constexpr int kUnitCost = 3;
 // Where a CTA's part of the line begins: every CTA adds the line up by itself.
 struct Line {
   int s;         // the sequence
+  KvSeq q;
   int64_t base;  // its first block
 };
 template <int R>
 __device__ __forceinline__ int64_t seq_cost(const AttendArgs& p, const KvSeq& q, int& units, int& nb, int& cost) {
-  const int64_t pairs = (int64_t)q.n * (p.n_heads / p.kv.hkv);
-  units = (int)((pairs + R - 1) / R) * p.kv.hkv;
+  const int pairs = q.n * (p.n_heads / p.kv.hkv);  // below 2^31 with T n_heads
+  units = (int)((pairs + (int64_t)(R - 1)) / R) * p.kv.hkv;
   nb = (q.len + kBlockKeys - 1) / kBlockKeys;
   cost = nb ? nb + kUnitCost : 1;
   return (int64_t)units * cost;
 }
+// total j / ctas; a 64-bit division costs a third of a microsecond
+__device__ __forceinline__ int64_t part(int64_t total, int j, int ctas) {
+  return total < (1 << 21) ? (int64_t)((uint32_t)total * (uint32_t)j / (uint32_t)ctas) : total * j / ctas;
+}
 
-template <int FMT, int DH, int RW>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const AttendArgs p) {
-  using C = Shape<DH, RW>;
+// Transposes an 8 x 8 tile of 16-bit values over the warp: from (row lane / 4, columns 2 (lane % 4) and the next) to the same of its columns.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int FMT, int DH, int NT, int RW>
+__global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_attend(const AttendArgs p) {
+  using C = Shape<DH, NT, RW>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t warp_sums[kWarps];
   __shared__ Line line_s;
   __shared__ int scales[2][kWarps][4];  // [stage][part of 32 keys][2 K, 2 V scales of 16 keys each]
-  __shared__ float row_m[kWarps][16], row_l[kWarps][16];
+  __shared__ float row_m[kWarps][C::RT], row_l[kWarps][C::RT];
   __shared__ int row_x[kWarps];
   start_dependents();
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, c = lane & 3, g8 = lane >> 2;
@@ -167,14 +183,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
 
   // ---- the line, and this CTA's part of it
   const int per = (p.kv.n_seqs + kThreads - 1) / kThreads;
-  int64_t total = 0, before = 0, own;  // the line; the blocks of the sequences before this thread's, and of its own
+  int64_t total = 0, before = 0, own = 0;  // the line; the blocks of the sequences before this thread's, and of its own
+  KvSeq mine{0, 0, 0};                     // the last of them
+  for (int s = t * per; s < min((t + 1) * per, p.kv.n_seqs); ++s) {
+    int units, nb, cost;
+    mine = kv_seq(p.kv, s);
+    own += seq_cost<C::R>(p, mine, units, nb, cost);
+  }
   {
-    int64_t sum = 0;
-    for (int s = t * per; s < min((t + 1) * per, p.kv.n_seqs); ++s) {
-      int units, nb, cost;
-      sum += seq_cost<C::R>(p, kv_seq(p.kv, s), units, nb, cost);
-    }
-    int64_t upto = sum;
+    int64_t upto = own;
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) {
       const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, k);
@@ -187,49 +204,54 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
       before += w < warp ? warp_sums[w] : 0;
       total += warp_sums[w];
     }
-    before += upto - sum;
-    own = sum;
+    before += upto - own;
   }
   const int ctas = (int)min((int64_t)gridDim.x, total);
   const int j = blockIdx.x;
   if (t == 0) p.cuts[j].first = p.cuts[j].end = 0;
   if (j >= ctas) return;
-  const int64_t begin = total * j / ctas, end = total * (j + 1) / ctas;
+  const int64_t begin = part(total, j, ctas), end = part(total, j + 1, ctas);
   if (begin >= before && begin < before + own) {
     int64_t base = before;
     int s = t * per;
-    for (; s < p.kv.n_seqs - 1; ++s) {
-      int units, nb, cost;
-      const int64_t n = seq_cost<C::R>(p, kv_seq(p.kv, s), units, nb, cost);
-      if (begin < base + n) break;
-      base += n;
+    if (per > 1) {
+      mine = kv_seq(p.kv, s);
+      for (; s < p.kv.n_seqs - 1; ++s) {
+        int units, nb, cost;
+        const int64_t n = seq_cost<C::R>(p, mine, units, nb, cost);
+        if (begin < base + n) break;
+        base += n;
+        mine = kv_seq(p.kv, s + 1);
+      }
     }
     line_s.s = s;
+    line_s.q = mine;
     line_s.base = base;
   }
   __syncthreads();
   int s = line_s.s;
+  KvSeq q = line_s.q;
   int64_t base = line_s.base, at = begin;
 
-  while (at < end && s < p.kv.n_seqs) {
-    const KvSeq q = kv_seq(p.kv, s);
+  while (at < end) {
     int units, nb, cost;
     const int64_t here = seq_cost<C::R>(p, q, units, nb, cost);
     if (at >= base + here) {
       base += here;
-      ++s;
+      if (++s >= p.kv.n_seqs) break;
+      q = kv_seq(p.kv, s);
       continue;
     }
     // ---- one segment: blocks [b0, b1) of unit u, whose own cost comes before its blocks
-    const int u = (int)((at - base) / cost), v0 = (int)((at - base) - (int64_t)u * cost);
+    const int u = here < (int64_t)1 << 31 ? (int)((uint32_t)(at - base) / (uint32_t)cost) : (int)((at - base) / cost);
+    const int v0 = (int)((at - base) - (int64_t)u * cost);
     const int v1 = (int)min((int64_t)cost, v0 + (end - at));
     const int64_t unit0 = base + (int64_t)u * cost;
     at += v1 - v0;
     const int b0 = max(0, v0 - kUnitCost), b1 = max(0, v1 - kUnitCost);
     if (b0 == b1 && nb) continue;
-    const int rt = u / p.kv.hkv, h = u % p.kv.hkv;
-    const int r0 = rt * C::R, pairs = q.n * G;
-    const int n_rows = min(C::R, pairs - r0);
+    const int rt = u / p.kv.hkv, h = u - rt * p.kv.hkv;
+    const int r0 = rt * C::R, n_rows = min(C::R, q.n * G - r0);
     if (nb == 0) {  // an empty slot of a batch
       for (int i = t; i < n_rows * (DH / 4); i += kThreads) {
         const int r = i / (DH / 4), tok = (r0 + r) / G, hd = h * G + (r0 + r) - tok * G;
@@ -238,22 +260,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
       }
       continue;
     }
-    // rows of this thread: limit = the keys that a row sees; rows that do not exist see all and are dropped
-    int limit[2], token[2], head[2];
-    uint32_t qa[DH / 16][4];
+    // limit = the keys that a row sees; rows that do not exist see all and are dropped.  This thread's scores are of
+    // rows 8 n + 2 c and the next of its warp.
+    constexpr int kAll = 0x7FFFFFFF;
+    const int before_rows = q.len - q.n;  // tokens before the call's
+    int limit[NT][2], kmin = kAll, kmax = 0;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int i = rw * 16 + g8 + 8 * e, r = r0 + i;
-      const bool real = i < n_rows;
-      token[e] = real ? r / G : 0;
-      head[e] = real ? r - token[e] * G : 0;
-      limit[e] = real ? q.len - q.n + token[e] + 1 : 0x7FFFFFFF;
-    }
-    const int kmin = __reduce_min_sync(0xFFFFFFFFu, min(limit[0], limit[1]));
-    int kmax = max(limit[0] == 0x7FFFFFFF ? 0 : limit[0], limit[1] == 0x7FFFFFFF ? 0 : limit[1]);
-    kmax = __reduce_max_sync(0xFFFFFFFFu, kmax);                                   // of the warp
-    const int klim = max(0, q.len - q.n + (r0 + n_rows - 1) / G + 1);              // of the CTA
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = rw * C::RT + 8 * n + 2 * c + e;
+        limit[n][e] = r < n_rows ? before_rows + (r0 + r) / G + 1 : kAll;
+        kmin = min(kmin, limit[n][e]);
+        kmax = max(kmax, r < n_rows ? limit[n][e] : 0);
+      }
+    kmin = __reduce_min_sync(0xFFFFFFFFu, kmin);
+    kmax = __reduce_max_sync(0xFFFFFFFFu, kmax);                                // of the warp
+    const int klim = max(0, before_rows + (r0 + n_rows - 1) / G + 1);           // of the CTA
     const int stop = min(b1, (klim + kBlockKeys - 1) / kBlockKeys);
+
     // ---- the ring: this warp copies its part of 32 keys of its group's tile
     const int32_t* table = p.kv.pages + (int64_t)s * p.kv.max_pages;
     const int my_keys = kg * C::GK + rw * 32;  // within a block
@@ -309,24 +334,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
       else asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(32 * RW) : "memory");
     };
 
-    uint32_t qw[2][DH / 8];
-    auto load_q = [&]() {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const bool real = rw * 16 + g8 + 8 * e < n_rows;
-        const uint16_t* src = p.qkv + (int64_t)(q.first + token[e]) * (p.n_heads + 2 * p.kv.hkv) * DH +
-                              (int64_t)(h * G + head[e]) * DH + c * (DH / 4);
-#pragma unroll
-        for (int i = 0; i < DH / 32; ++i) {
-          const uint4 v = real ? ld_nc_v4(src + 8 * i) : make_uint4(0, 0, 0, 0);
-          qw[e][4 * i] = v.x; qw[e][4 * i + 1] = v.y; qw[e][4 * i + 2] = v.z; qw[e][4 * i + 3] = v.w;
-        }
-      }
-    };
     // The chain that a segment begins with is a page's number, then its keys (and its scales, which are stored after
     // the copies are on their way); q is fetched beside it and made ready while the first keys arrive.
     int id_a = page_of(b0), id_b = page_of(b0 + 1);
-    load_q();
+    uint32_t qw[NT][DH / 8];  // row 8 n + lane / 4, elements c DH / 4 ..
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = rw * C::RT + 8 * n + g8, tok = (r0 + r) / G;
+      const uint16_t* src = p.qkv + (int64_t)(q.first + tok) * (p.n_heads + 2 * p.kv.hkv) * DH +
+                            (int64_t)(h * G + (r0 + r) - tok * G) * DH + c * (DH / 4);
+#pragma unroll
+      for (int i = 0; i < DH / 32; ++i) {
+        const uint4 v = r < n_rows ? ld_nc_v4(src + 8 * i) : make_uint4(0, 0, 0, 0);
+        qw[n][4 * i] = v.x; qw[n][4 * i + 1] = v.y; qw[n][4 * i + 2] = v.z; qw[n][4 * i + 3] = v.w;
+      }
+    }
     int sc_a = scale_of(id_a);
     auto next = [&](int b) {  // copies block b's keys; a step ahead its successor's scales, two ahead the pages
       if (b < stop) copy_tile(b, id_a, sc_a, (b - b0) & 1);
@@ -336,29 +358,36 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
       id_b = page_of(b + 2);
     };
     next(b0);
-    int exq[2];
+    uint32_t qb[NT][DH / 16][2];
+    int exq[NT][2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int n = 0; n < NT; ++n) {
       uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < DH / 8; ++i) m = max(m, absmax_bf16x2(qw[e][i]));
+      for (int i = 0; i < DH / 8; ++i) m = max(m, absmax_bf16x2(qw[n][i]));
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
       const int ex = max((int)(m >> 23) - 127, -110);  // the row's largest |q| < 2^(ex + 1)
       const float f = pow2i(14 - ex);
 #pragma unroll
       for (int i = 0; i < DH / 16; ++i) {
-        qa[i][e] = pack_half2(bf16_lo(qw[e][2 * i]) * f, bf16_hi(qw[e][2 * i]) * f);
-        qa[i][e + 2] = pack_half2(bf16_lo(qw[e][2 * i + 1]) * f, bf16_hi(qw[e][2 * i + 1]) * f);
+        qb[n][i][0] = pack_half2(bf16_lo(qw[n][2 * i]) * f, bf16_hi(qw[n][2 * i]) * f);
+        qb[n][i][1] = pack_half2(bf16_lo(qw[n][2 * i + 1]) * f, bf16_hi(qw[n][2 * i + 1]) * f);
       }
-      exq[e] = ex - 14;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) exq[n][e] = __shfl_sync(0xFFFFFFFFu, ex - 14, (2 * c + e) * 4);
     }
-    float o[DH / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    float o[DH / 16][NT][4], m[NT][2], l[NT][2];
     int xref = -1000;
 #pragma unroll
-    for (int i = 0; i < DH / 8; ++i)
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
+      for (int i = 0; i < DH / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][n][e] = 0.0f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+    }
 
 #pragma unroll 1
     for (int b = b0; b < stop; ++b) {
@@ -367,90 +396,101 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
       group_sync();
       const int stage = (b - b0) & 1;
 #pragma unroll 1
-      for (int part = 0; part < RW; ++part) {
-        const int key0 = b * kBlockKeys + kg * C::GK + part * 32;
+      for (int sub = 0; sub < RW; ++sub) {
+        const int key0 = b * kBlockKeys + kg * C::GK + sub * 32;
         if (key0 >= kmax) break;
         const uint8_t* kt = smem + stage * 2 * C::kTile + kg * C::GK * DH;
         const uint8_t* vt = kt + C::kTile;
-        const int row0 = part * 32;
-        const int* sc = scales[stage][kg * RW + part];
+        const int row0 = sub * 32;
+        const int* sc = scales[stage][kg * RW + sub];
         const int xk[2] = {sc[0], sc[1]}, xv[2] = {sc[2], sc[3]};
-        float z[4][4];
+        // scores: [16 keys][8 rows][keys lane / 4 and 8 on, rows 2 c and the next]
+        float z[2][NT][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          uint32_t w[DH / 16];
-          take<DH, DH / 4>(kt, row0 + 8 * n + g8, c * (DH / 4), w);
+        for (int k = 0; k < 2; ++k) {
+          uint32_t wa[DH / 16], wb[DH / 16];
+          take<DH, DH / 4>(kt, row0 + 16 * k + g8, c * (DH / 4), wa);
+          take<DH, DH / 4>(kt, row0 + 16 * k + 8 + g8, c * (DH / 4), wb);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) z[n][e] = 0.0f;
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < DH / 16; ++i) mma16816(z[n], qa[i], f16x2_of<FMT>(w[i]), f16x2_of<FMT>(w[i] >> 16));
+            for (int e = 0; e < 4; ++e) z[k][n][e] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < DH / 16; ++i) {
+            const uint32_t a[4] = {f16x2_of<FMT>(wa[i]), f16x2_of<FMT>(wb[i]), f16x2_of<FMT>(wa[i] >> 16), f16x2_of<FMT>(wb[i] >> 16)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(z[k][n], a, qb[n][i][0], qb[n][i][1]);
+          }
         }
         const bool edge = key0 + 32 > kmin || xk[0] == kNoPage || xk[1] == kNoPage;
         if (edge) {
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = key0 + 8 * n + 2 * c + (e & 1);
-              if (key >= limit[e >> 1] || xk[n >> 1] == kNoPage) z[n][e] = -INFINITY;
-            }
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (key0 + 16 * k + g8 + 8 * (e >> 1) >= limit[n][e & 1] || xk[k] == kNoPage) z[k][n][e] = -INFINITY;
         }
         // the row's maximum: a page's scale is positive, so it goes to the page's maximum alone
-        float f[2][2], mn[2];  // [page][row]
+        float f[2][NT][2], mn[NT][2];
+        bool moved = false;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = m[e];
-#pragma unroll
-          for (int sub = 0; sub < 2; ++sub) {
-            f[sub][e] = p.scale_log2 * pow2i(max(exq[e] + xk[sub], -100));
-            const float y = fmaxf(fmaxf(z[2 * sub][2 * e], z[2 * sub][2 * e + 1]), fmaxf(z[2 * sub + 1][2 * e], z[2 * sub + 1][2 * e + 1]));
-            x = fmaxf(x, y * f[sub][e]);
-          }
-          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
-          mn[e] = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
-        }
-        const int xv0 = xv[0] == kNoPage ? -1000 : xv[0], xv1 = xv[1] == kNoPage ? -1000 : xv[1];
-        const int xnew = max(xref, max(xv0, xv1));
-        if (__any_sync(0xFFFFFFFFu, mn[0] != m[0] || mn[1] != m[1] || xnew != xref)) {
-          const float fx = pow2i(xref - xnew);
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float fade = mn[e] == m[e] ? 1.0f : ex2(m[e] - mn[e]);
-            l[e] *= fade;
-            const float fo = fade * fx;
+            float x = m[n][e];
 #pragma unroll
-            for (int i = 0; i < DH / 8; ++i) {
-              o[i][2 * e] *= fo;
-              o[i][2 * e + 1] *= fo;
+            for (int k = 0; k < 2; ++k) {
+              f[k][n][e] = p.scale_log2 * pow2i(max(exq[n][e] + xk[k], -100));
+              x = fmaxf(x, fmaxf(z[k][n][e], z[k][n][e + 2]) * f[k][n][e]);
             }
-            m[e] = mn[e];
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, w));
+            mn[n][e] = x;
+            moved |= x != m[n][e];
           }
+        const int xv0 = xv[0] == kNoPage ? -1000 : xv[0], xv1 = xv[1] == kNoPage ? -1000 : xv[1];
+        const int xnew = max(xref, max(xv0, xv1));
+        if (__any_sync(0xFFFFFFFFu, moved || xnew != xref)) {
+          const float fx = pow2i(xref - xnew);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float fade = mn[n][e] == m[n][e] ? 1.0f : ex2(m[n][e] - mn[n][e]);
+              l[n][e] *= fade;
+              const float fo = fade * fx;
+#pragma unroll
+              for (int i = 0; i < DH / 16; ++i) {
+                o[i][n][e] *= fo;
+                o[i][n][e + 2] *= fo;
+              }
+              m[n][e] = mn[n][e];
+            }
           xref = xnew;
         }
         // 2^(s - m + 15 + dx), dx the exponent of the page's V over xref.  The sum takes 2^dx back, so it holds for pages of any V;
         // below 2^-60 nothing is left of one in fp16.
-        const int dx[2] = {max(xv0 - xref, -60), max(xv1 - xref, -60)};
-        float back[2], ref[2][2];
+        uint32_t pb[2][NT][2];
 #pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-          back[sub] = pow2i(-dx[sub]);
+        for (int k = 0; k < 2; ++k) {
+          const int dx = max((k ? xv1 : xv0) - xref, -60);
+          const float back = pow2i(-dx);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) ref[sub][e] = (float)(15 + dx[sub]) - (m[e] == -INFINITY ? 0.0f : m[e]);
-        }
-        uint32_t pa[2][4];
+          for (int n = 0; n < NT; ++n) {
+            float w[4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int sub = n >> 1;
-          float w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            w[e] = ex2(__fmaf_rn(z[n][e], f[sub][e >> 1], ref[sub][e >> 1]));
-            l[e >> 1] = __fmaf_rn(w[e], back[sub], l[e >> 1]);
+            for (int e = 0; e < 4; ++e) {
+              const float mr = m[n][e & 1];
+              w[e] = ex2(__fmaf_rn(z[k][n][e], f[k][n][e & 1], (float)(15 + dx) - (mr == -INFINITY ? 0.0f : mr)));
+              l[n][e & 1] = __fmaf_rn(w[e], back, l[n][e & 1]);
+            }
+            pb[k][n][0] = transposed(pack_half2(w[0], w[1]));
+            pb[k][n][1] = transposed(pack_half2(w[2], w[3]));
           }
-          pa[sub][(n & 1) * 2] = pack_half2(w[0], w[1]);
-          pa[sub][(n & 1) * 2 + 1] = pack_half2(w[2], w[3]);
         }
-        // the keys of step ks: rows 2c, 2c + 1, 2c + 8, 2c + 9 of its 16
+        // the keys of step k: rows 2c, 2c + 1, 2c + 8, 2c + 9 of its 16
         uint32_t odd = 0;
         if (edge) {
 #pragma unroll
@@ -463,50 +503,48 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
           odd = __any_sync(0xFFFFFFFFu, odd != 0);
         }
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
+        for (int k = 0; k < 2; ++k) {
           uint32_t w[4][DH / 32];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            take<DH, DH / 8>(vt, row0 + ks * 16 + 2 * c + (i & 1) + (i >> 1) * 8, g8 * (DH / 8), w[i]);
-          if (!odd) {
+            take<DH, DH / 8>(vt, row0 + k * 16 + 2 * c + (i & 1) + (i >> 1) * 8, g8 * (DH / 8), w[i]);
+          uint32_t ones[NT][2];
+          if (odd) {
 #pragma unroll
-            for (int k = 0; k < DH / 32; ++k) {
-              const uint32_t a0 = __byte_perm(w[0][k], w[1][k], 0x5140), a1 = __byte_perm(w[0][k], w[1][k], 0x7362);
-              const uint32_t e0 = __byte_perm(w[2][k], w[3][k], 0x5140), e1 = __byte_perm(w[2][k], w[3][k], 0x7362);
-              mma16816(o[4 * k], pa[ks], f16x2_of<FMT>(a0), f16x2_of<FMT>(e0));
-              mma16816(o[4 * k + 1], pa[ks], f16x2_of<FMT>(a0 >> 16), f16x2_of<FMT>(e0 >> 16));
-              mma16816(o[4 * k + 2], pa[ks], f16x2_of<FMT>(a1), f16x2_of<FMT>(e1));
-              mma16816(o[4 * k + 3], pa[ks], f16x2_of<FMT>(a1 >> 16), f16x2_of<FMT>(e1 >> 16));
-            }
-          } else {
-            // Some V is NaN or infinite, and some row does not see every key: a masked key's weight of 0 times it would be
-            // NaN.  Such values become 0, and a second product of ones finds the rows that do see one.
-            uint32_t ones[4];
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int key = key0 + ks * 16 + 2 * c + (e >> 1) * 8;
-              const int lim = xk[ks] == kNoPage ? 0 : limit[e & 1];
-              ones[e] = (key < lim ? 0x3C00u : 0u) | (key + 1 < lim ? 0x3C000000u : 0u);
-            }
+              for (int e = 0; e < 2; ++e) {
+                const int key = key0 + 16 * k + g8 + 8 * e;
+                ones[n][e] = transposed(xk[k] == kNoPage ? 0u : (key < limit[n][0] ? 0x3C00u : 0u) | (key < limit[n][1] ? 0x3C000000u : 0u));
+              }
+          }
 #pragma unroll
-            for (int k = 0; k < DH / 32; ++k)
+          for (int i = 0; i < DH / 16; ++i) {
+            // bytes 2 i and 2 i + 1: the elements of rows lane / 4 and lane / 4 + 8 of tile i, for two pairs of keys
+            const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;
+            const uint32_t x = __byte_perm(w[0][i >> 1], w[1][i >> 1], sel), y = __byte_perm(w[2][i >> 1], w[3][i >> 1], sel);
+            uint32_t a[4] = {f16x2_of<FMT>(x), f16x2_of<FMT>(x >> 16), f16x2_of<FMT>(y), f16x2_of<FMT>(y >> 16)};
+            if (odd) {
+              // Some V is NaN or infinite, and some row does not see every key: a masked key's weight of 0 times it would be
+              // NaN.  Such values become 0, and a second product, of ones, finds the rows that do see one.
+              uint32_t bad[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t b[2], n[2];
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t high = (((a[e] & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u) >> 15;
+                a[e] &= ~(high * 0xFFFFu);
+                bad[e] = high * 0x3C00u;
+              }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const uint32_t v = f16x2_of<FMT>(__byte_perm(w[2 * e][k], w[2 * e + 1][k], (uint32_t)(i | (4 + i) << 4)));
-                  const uint32_t bad = (((v & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u) >> 15;
-                  b[e] = v & ~(bad * 0xFFFFu);
-                  n[e] = bad * 0x3C00u;
-                }
+              for (int n = 0; n < NT; ++n) {
                 float seen[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma16816(seen, ones, n[0], n[1]);
-                mma16816(o[4 * k + i], pa[ks], b[0], b[1]);
+                mma16816(seen, bad, ones[n][0], ones[n][1]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  if (seen[e] != 0.0f) o[4 * k + i][e] = __uint_as_float(0x7FC00000u);
+                  if (seen[e] != 0.0f) o[i][n][e] = __uint_as_float(0x7FC00000u);
               }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(o[i][n], a, pb[k][n][0], pb[k][n][1]);
           }
         }
       }
@@ -518,41 +556,43 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_kv_attend(const Attend
     __syncthreads();
     float* join = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
-      l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
-      if (c == 0) {
-        row_m[warp][g8 + 8 * e] = m[e];
-        row_l[warp][g8 + 8 * e] = l[e];
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * c + e;  // of the warp
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], w);
+        if (g8 == 0) {
+          row_m[warp][r] = m[n][e];
+          row_l[warp][r] = l[n][e];
+        }
+        if (rw * C::RT + r < n_rows) {
+          float* to = join + (kg * C::R + rw * C::RT + r) * C::kPitch + g8 * (DH / 8);
+#pragma unroll
+          for (int i = 0; i < DH / 32; ++i)
+            *reinterpret_cast<float4*>(to + 4 * i) = make_float4(o[2 * i][n][e], o[2 * i][n][e + 2], o[2 * i + 1][n][e], o[2 * i + 1][n][e + 2]);
+        }
       }
-      float* to = join + (kg * C::R + rw * 16 + g8 + 8 * e) * C::kPitch + c * (DH / 4);
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int i = 0; i < DH / 32; ++i)
-          *reinterpret_cast<float4*>(to + half * (DH / 8) + 4 * i) =
-              make_float4(o[4 * i][2 * e + half], o[4 * i + 1][2 * e + half], o[4 * i + 2][2 * e + half], o[4 * i + 3][2 * e + half]);
-    }
     if (lane == 0) row_x[warp] = xref;
     __syncthreads();
-    const bool whole = b0 == 0 && b1 == nb, starts = b0 == 0;
+    const bool starts = b0 == 0, whole = starts && b1 == nb;
     const int slot = 2 * j + (starts ? 1 : 0);
     for (int i = t; i < n_rows * (DH / 4); i += kThreads) {
-      const int r = i / (DH / 4), col = (i - r * (DH / 4)) * 4;
+      const int r = i / (DH / 4), col = (i - r * (DH / 4)) * 4, w0 = r / C::RT, wr = r - w0 * C::RT;
       float M = -INFINITY;
       int X = -1000;
 #pragma unroll
       for (int k = 0; k < C::KW; ++k) {
-        M = fmaxf(M, row_m[k * RW + r / 16][r & 15]);
-        X = max(X, row_x[k * RW + r / 16]);
+        M = fmaxf(M, row_m[k * RW + w0][wr]);
+        X = max(X, row_x[k * RW + w0]);
       }
       float L = 0.0f, a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int k = 0; k < C::KW; ++k) {
-        const int w = k * RW + r / 16;
-        const float mk = row_m[w][r & 15];
+        const int w = k * RW + w0;
+        const float mk = row_m[w][wr], lk = row_l[w][wr];
         const float f = mk == M ? (M == -INFINITY ? 0.0f : 1.0f) : ex2(mk - M);
-        L += row_l[w][r & 15] * (row_l[w][r & 15] != row_l[w][r & 15] ? 1.0f : f);
+        L += lk * (lk != lk ? 1.0f : f);
         const float fo = f * pow2i(row_x[w] - X);
         const float4 v = *reinterpret_cast<const float4*>(join + (k * C::R + r) * C::kPitch + col);
         a[0] += v.x * fo; a[1] += v.y * fo; a[2] += v.z * fo; a[3] += v.w * fo;
@@ -646,58 +686,67 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_join(const AttendArgs p) {
   if (t == 0) p.lse[(int64_t)hd * p.kv.T + cut.row0 + tok] = total == 0.0f ? -INFINITY : (M + log2f(total)) * kLn2;
 }
 
-// Groups of 16 rows of a CTA: as many as a sequence's (token, head) pairs fill, four at most.
-int row_groups(int64_t T, int n_seqs, int n_heads, int hkv) {
+// Rows of a CTA for the (token, head) pairs of a sequence and K/V head: 8 of one warp or 16; above, two or four warps share their keys
+// for 16 rows each.
+struct Rows {
+  int nt, rw;
+  int count() const { return 8 * nt * rw; }
+};
+Rows rows_of(int64_t T, int n_seqs, int n_heads, int hkv) {
   const int64_t pairs = (T + n_seqs - 1) / n_seqs * (n_heads / hkv);
-  return pairs <= 16 ? 1 : pairs <= 32 ? 2 : 4;
+  return pairs <= 8 ? Rows{1, 1} : pairs <= 16 ? Rows{2, 1} : pairs <= 32 ? Rows{2, 2} : Rows{2, 4};
 }
 struct Pieces {
   size_t lse, cuts, all;
 };
-Pieces pieces(int rw, int dh) {
+Pieces pieces(int rows, int dh) {
   auto pad = [](size_t n) { return (n + 255) & ~size_t(255); };
   Pieces w;
-  w.lse = pad((size_t)2 * kMaxCtas * 16 * rw * dh * 4);
-  w.cuts = w.lse + pad((size_t)2 * kMaxCtas * 16 * rw * 4);
+  w.lse = pad((size_t)2 * kMaxCtas * rows * dh * 4);
+  w.cuts = w.lse + pad((size_t)2 * kMaxCtas * rows * 4);
   w.all = w.cuts + pad(sizeof(Cut) * kMaxCtas);
   return w;
 }
 
-template <int FMT, int DH, int RW>
-cudaError_t launch(const AttendArgs& p, int ctas, int join_rows, cudaStream_t s) {
-  using C = Shape<DH, RW>;
-  cudaError_t e = cudaFuncSetAttribute(k_kv_attend<FMT, DH, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+template <int FMT, int DH, int NT, int RW>
+cudaError_t launch(const AttendArgs& p, int sms, int64_t pairs, cudaStream_t s) {
+  using C = Shape<DH, NT, RW>;
+  static_assert(C::kCtas * 152 <= kMaxCtas, "parts of the workspace");
+  const int ctas = min(kMaxCtas, sms * C::kCtas);
+  cudaError_t e = cudaFuncSetAttribute(k_kv_attend<FMT, DH, NT, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  k_kv_attend<FMT, DH, RW><<<ctas, kThreads, C::kSmem, s>>>(p);
+  k_kv_attend<FMT, DH, NT, RW><<<ctas, kThreads, C::kSmem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_dependent(k_kv_join<DH, C::R>, dim3((unsigned)ctas, (unsigned)min(join_rows, C::R)), kJoinThreads, 0, s, p);
+  return launch_dependent(k_kv_join<DH, C::R>, dim3((unsigned)ctas, (unsigned)min(pairs, (int64_t)C::R)), kJoinThreads, 0, s, p);
 }
 template <int FMT, int DH>
-cudaError_t launch_rw(int rw, const AttendArgs& p, int ctas, int join_rows, cudaStream_t s) {
-  return rw == 1 ? launch<FMT, DH, 1>(p, ctas, join_rows, s)
-                 : rw == 2 ? launch<FMT, DH, 2>(p, ctas, join_rows, s) : launch<FMT, DH, 4>(p, ctas, join_rows, s);
+cudaError_t launch_rows(Rows r, const AttendArgs& p, int sms, int64_t pairs, cudaStream_t s) {
+  if (r.nt == 1) return launch<FMT, DH, 1, 1>(p, sms, pairs, s);
+  return r.rw == 1 ? launch<FMT, DH, 2, 1>(p, sms, pairs, s)
+                   : r.rw == 2 ? launch<FMT, DH, 2, 2>(p, sms, pairs, s) : launch<FMT, DH, 2, 4>(p, sms, pairs, s);
+}
+template <int FMT>
+cudaError_t launch_dh(Rows r, const AttendArgs& p, int sms, int64_t pairs, cudaStream_t s) {
+  return p.kv.dh == 128 ? launch_rows<FMT, 128>(r, p, sms, pairs, s)
+                        : p.kv.dh == 96 ? launch_rows<FMT, 96>(r, p, sms, pairs, s) : launch_rows<FMT, 64>(r, p, sms, pairs, s);
 }
 
 }  // namespace
 
 size_t kv_attend_workspace_bytes(int64_t T, int n_seqs, int n_heads, int hkv, int dh) {
-  return pieces(row_groups(T, n_seqs, n_heads, hkv), dh).all;
+  return pieces(rows_of(T, n_seqs, n_heads, hkv).count(), dh).all;
 }
 
 cudaError_t launch_kv_attend(const KvArgs& a, const uint16_t* qkv, int n_heads, uint16_t* att, float* lse, void* ws,
                              const Launch& L) {
-  const int rw = row_groups(a.T, a.n_seqs, n_heads, a.hkv);
-  const Pieces w = pieces(rw, a.dh);
+  const Rows r = rows_of(a.T, a.n_seqs, n_heads, a.hkv);
+  const Pieces w = pieces(r.count(), a.dh);
   uint8_t* b = static_cast<uint8_t*>(ws);
   AttendArgs p{a, qkv, n_heads, kLog2e / sqrtf((float)a.dh), att, lse, reinterpret_cast<float*>(b),
                reinterpret_cast<float*>(b + w.lse), reinterpret_cast<Cut*>(b + w.cuts)};
-  const int ctas = min(kMaxCtas, L.num_sms * kCtasPerSm);
-  const int64_t pairs = a.row_start ? 1 << 20 : (int64_t)a.rows * (n_heads / a.hkv);
-  const int join_rows = (int)min(pairs, (int64_t)(16 * rw));
-  cudaError_t e;
-  if (a.dh == 128) e = a.fmt ? launch_rw<1, 128>(rw, p, ctas, join_rows, L.stream) : launch_rw<0, 128>(rw, p, ctas, join_rows, L.stream);
-  else if (a.dh == 96) e = a.fmt ? launch_rw<1, 96>(rw, p, ctas, join_rows, L.stream) : launch_rw<0, 96>(rw, p, ctas, join_rows, L.stream);
-  else e = a.fmt ? launch_rw<1, 64>(rw, p, ctas, join_rows, L.stream) : launch_rw<0, 64>(rw, p, ctas, join_rows, L.stream);
+  // rows of a unit at most, where the host knows them
+  const int64_t pairs = a.row_start ? (int64_t)1 << 20 : (int64_t)a.rows * (n_heads / a.hkv);
+  const cudaError_t e = a.fmt ? launch_dh<1>(r, p, L.num_sms, pairs, L.stream) : launch_dh<0>(r, p, L.num_sms, pairs, L.stream);
   if (e != cudaSuccess) return e;
   if (L.launches) *L.launches += 2;
   return cudaSuccess;
