@@ -14,8 +14,7 @@ namespace fp8q {
 
 namespace {
 
-constexpr int kAppendThreads = 128;
-constexpr int kHeld = 8;  // vectors of 8 elements that a thread keeps between the absmax and the codes
+constexpr int kHeld = 8;  // vectors of 8 elements that a thread keeps between the absmax and the codes: a page's, of one head
 
 template <int F32>
 struct In8 {
@@ -65,10 +64,10 @@ __device__ __forceinline__ uint32_t shift4(uint32_t codes, float s) {
 }
 
 // Block (c, h, kv) takes the pieces of pages that begin in rows [c rows_per_block, ...): a piece is what a call writes of one page,
-// and begins at a sequence's first row or at a page's first token.
-template <int F32, int FMT>
-__global__ void __launch_bounds__(kAppendThreads) k_kv_append(const KvArgs a, const void* __restrict__ qkv, int n_heads,
-                                                              int rows_per_block) {
+// and begins at a sequence's first row or at a page's first token.  Its values are read once and kept in registers.
+template <int F32, int FMT, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_kv_append(const KvArgs a, const void* __restrict__ qkv, int n_heads,
+                                                       int rows_per_block) {
   __shared__ uint32_t red[32];
   const int h = blockIdx.y, is_v = blockIdx.z, P = 1 << a.page_shift;
   const int vecs = a.dh >> 3;  // vectors of 8 of a token
@@ -79,13 +78,17 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(const KvArgs a, co
   const int64_t r0 = (int64_t)blockIdx.x * rows_per_block;
   const int end = (int)min(r0 + rows_per_block, a.T);
   bool nonfinite = false;
+  int s = -1;
+  KvSeq q{0, 0, 0};
   for (int row = (int)r0; row < end;) {
-    const int s = kv_find(a, row);
-    if (s < 0) { ++row; continue; }
-    const KvSeq q = kv_seq(a, s);
-    if (row < q.first || row >= q.first + q.n) {  // behind the last sequence, or rows that are not in order
-      ++row;
-      continue;
+    if (row < q.first || row >= q.first + q.n) {
+      s = kv_find_warp(a, row);
+      if (s < 0) { ++row; continue; }
+      q = kv_seq(a, s);
+      if (row < q.first || row >= q.first + q.n) {  // behind the last sequence, or rows that are not in order
+        ++row;
+        continue;
+      }
     }
     const int pos = q.pos(row);
     if (pos < 0) {  // padding
@@ -94,47 +97,48 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(const KvArgs a, co
     }
     const int slot = pos & (P - 1);
     const int m = min(P - slot, q.first + q.n - row);  // tokens of this page from here on
-    if (row != q.first && slot != 0) {  // the piece began in an earlier block
+    if (row != q.first && slot != 0) {                 // the piece began in an earlier block
       row += m;
       continue;
     }
-    const int id = kv_page(a, s, pos >> a.page_shift);
-    const int first = row;
+    const int first = row, n = m * vecs;
     row += m;
+    const int id = kv_page(a, s, pos >> a.page_shift);
+    In8<F32> held[kHeld];
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      const int i = threadIdx.x + k * THREADS, t = i / vecs;
+      if (i < n) held[k].load(qkv, (int64_t)(first + t) * width + col + (i - t * vecs) * 8);
+    }
     if (id < 0) continue;
     const int64_t ph = (int64_t)id * a.hkv + h;
     const int was = slot ? (int)scales[ph] - 127 : 0;
     uint8_t* page = codes + (ph << a.page_shift) * a.dh;
-    const int n = m * vecs;
-    In8<F32> held[kHeld];
     uint32_t amax = 0;
-    for (int i = threadIdx.x, k = 0; i < n; i += kAppendThreads, ++k) {
-      const int t = i / vecs;
-      In8<F32> x;
-      x.load(qkv, (int64_t)(first + t) * width + col + (i - t * vecs) * 8);
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
       float v[8];
-      x.get(v);
-      amax = max(amax, absmax8(v, nonfinite));
+      held[k].get(v);
+      if ((int)threadIdx.x + k * THREADS < n) amax = max(amax, absmax8(v, nonfinite));
     }
-    (void)held;
     amax = block_max_u32(amax, red);
     int X = mx_exponent<FMT>(amax);
     if (slot) X = max(X, was);
     const float scale = pow2_neg(X);
-    for (int i = threadIdx.x; i < n; i += kAppendThreads) {
-      const int t = i / vecs;
-      In8<F32> x;
-      x.load(qkv, (int64_t)(first + t) * width + col + (i - t * vecs) * 8);
-      float v[8];
-      x.get(v);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = abs_bits(v[k]) >= kInf ? __uint_as_float(0x7FC00000u) : __fmul_rn(v[k], scale);
-      *reinterpret_cast<uint2*>(page + (int64_t)slot * a.dh + i * 8) =
-          make_uint2(cvt_fp8x4<FMT>(v[0], v[1], v[2], v[3]), cvt_fp8x4<FMT>(v[4], v[5], v[6], v[7]));
+    for (int k = 0; k < kHeld; ++k) {
+      const int i = threadIdx.x + k * THREADS;
+      float v[8];
+      held[k].get(v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = abs_bits(v[e]) >= kInf ? __uint_as_float(0x7FC00000u) : __fmul_rn(v[e], scale);
+      if (i < n)
+        *reinterpret_cast<uint2*>(page + slot * a.dh + i * 8) =
+            make_uint2(cvt_fp8x4<FMT>(v[0], v[1], v[2], v[3]), cvt_fp8x4<FMT>(v[4], v[5], v[6], v[7]));
     }
     if (slot && X > was) {  // the tokens that were there, to the new scale
       const float down = pow2_down(was - X);
-      for (int i = threadIdx.x; i < slot * vecs; i += kAppendThreads) {
+      for (int i = threadIdx.x; i < slot * vecs; i += THREADS) {
         uint2* p = reinterpret_cast<uint2*>(page + i * 8);
         const uint2 w = *p;
         *p = make_uint2(shift4<FMT>(w.x, down), shift4<FMT>(w.y, down));
@@ -145,65 +149,101 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(const KvArgs a, co
   if (nonfinite) atomicOr(a.status, kStatusNonfinite);
 }
 
-// One thread: 8 codes of one row.
-template <int F32, int FMT>
-__global__ void __launch_bounds__(256) k_kv_read(const KvArgs a, void* __restrict__ kv) {
-  const int vecs = 2 * a.hkv * a.dh / 8;
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= a.T * vecs) return;
-  const int row = (int)(i / vecs), e = (int)(i - (int64_t)row * vecs) * 8;
-  const int s = kv_find(a, row);
-  if (s < 0) return;
-  const KvSeq q = kv_seq(a, s);
-  if (row < q.first || row >= q.first + q.n) return;
-  const int pos = q.pos(row);
-  uint2 w = make_uint2(0u, 0u);
-  float scale = 1.0f;
-  if (pos >= 0) {
-    const int id = kv_page(a, s, pos >> a.page_shift);
-    if (id >= 0) {
-      const int head = e / a.dh, is_v = head >= a.hkv;
-      const int64_t ph = (int64_t)id * a.hkv + head - is_v * a.hkv;
-      scale = e8m0((is_v ? a.v_scale : a.k_scale)[ph]);
-      const int slot = pos & ((1 << a.page_shift) - 1);
-      w = *reinterpret_cast<const uint2*>((is_v ? a.v : a.k) + ((ph << a.page_shift) + slot) * a.dh + e - head * a.dh);
+// A warp takes rows_per_warp rows, 16 bytes of output a lane and step, kReads steps in flight.
+constexpr int kReadThreads = 256, kReads = 8;
+template <int F32, int FMT, int DH>
+__global__ void __launch_bounds__(kReadThreads) k_kv_read(const KvArgs a, void* __restrict__ kv, int rows_per_warp) {
+  constexpr int N = F32 ? 4 : 8;  // codes of 16 bytes of output
+  const int lane = threadIdx.x & 31, P = 1 << a.page_shift;
+  const int vecs = 2 * a.hkv * DH / N;
+  const int64_t r0 = ((int64_t)blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5)) * rows_per_warp;
+  const int end = (int)min(r0 + rows_per_warp, a.T);
+  int s = -1;
+  KvSeq q{0, 0, 0};
+  for (int row = (int)r0; row < end; ++row) {
+    if (row < q.first || row >= q.first + q.n) {
+      s = kv_find_warp(a, row);
+      if (s < 0) continue;
+      q = kv_seq(a, s);
+      if (row < q.first || row >= q.first + q.n) continue;
+    }
+    const int pos = q.pos(row);
+    const int id = pos < 0 ? -1 : kv_page(a, s, pos >> a.page_shift);
+    const int64_t ph0 = (int64_t)id * a.hkv;
+    const int slot = pos & (P - 1);
+    uint4* out = reinterpret_cast<uint4*>(kv) + (int64_t)row * vecs;
+    for (int i0 = lane; i0 < vecs; i0 += 32 * kReads) {
+      uint32_t w[kReads][N / 4];
+      uint32_t x[kReads];
+#pragma unroll
+      for (int k = 0; k < kReads; ++k) {
+        const int i = i0 + 32 * k, e = i * N, head = e / DH, is_v = head >= a.hkv;
+        const int64_t ph = ph0 + head - is_v * a.hkv;
+        const bool in = i < vecs && id >= 0;
+        const uint8_t* src = (is_v ? a.v : a.k) + ((ph << a.page_shift) + slot) * DH + e - head * DH;
+        x[k] = in ? (is_v ? a.v_scale : a.k_scale)[ph] : 127u;
+        if (N == 8) {
+          const uint2 u = in ? *reinterpret_cast<const uint2*>(src) : make_uint2(0, 0);
+          w[k][0] = u.x;
+          w[k][N / 4 - 1] = u.y;
+        } else {
+          w[k][0] = in ? *reinterpret_cast<const uint32_t*>(src) : 0u;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kReads; ++k) {
+        const float scale = e8m0(x[k]);
+        float v[N];
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+          const uint32_t h2 = f16x2_of<FMT>(w[k][j >> 1] >> (16 * (j & 1)));
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+          v[2 * j] = f.x * scale;
+          v[2 * j + 1] = f.y * scale;
+        }
+        uint4 o;
+        if (F32) o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        else o = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4 % N], v[5 % N]), pack_bf16x2(v[6 % N], v[7 % N]));
+        if (i0 + 32 * k < vecs) out[i0 + 32 * k] = o;
+      }
     }
   }
-  float v[8];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t h2 = f16x2_of<FMT>((k < 2 ? w.x : w.y) >> (16 * (k & 1)));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-    v[2 * k] = f.x * scale;
-    v[2 * k + 1] = f.y * scale;
-  }
-  const int64_t o = (int64_t)row * (vecs * 8) + e;
-  if (F32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(kv) + o);
-    p[0] = make_float4(v[0], v[1], v[2], v[3]);
-    p[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(kv) + o) =
-        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-  }
+}
+
+template <int F32, int FMT>
+void read_dh(const KvArgs& a, void* kv, unsigned grid, int rows, cudaStream_t s) {
+  auto* k = a.dh == 128 ? k_kv_read<F32, FMT, 128> : a.dh == 96 ? k_kv_read<F32, FMT, 96> : k_kv_read<F32, FMT, 64>;
+  k<<<grid, kReadThreads, 0, s>>>(a, kv, rows);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(const KvArgs& a, const void* qkv, int f32, int n_heads, const Launch& L) {
-  const int rows = 1 << a.page_shift;
+  // Rows of a block: a page's where that fills the GPU (T = 8680, 8 heads of 128: 10 us); for fewer, down to one, until
+  // there are about eight blocks an SM, so that a block seldom writes more than one sequence's token.
+  const int64_t per = a.T * 2 * a.hkv / (8 * L.num_sms);
+  const int rows = (int)(per < 1 ? 1 : per < (1 << a.page_shift) ? per : 1 << a.page_shift);
   const dim3 grid((unsigned)((a.T + rows - 1) / rows), (unsigned)a.hkv, 2);
-  auto* k = f32 ? (a.fmt ? k_kv_append<1, 1> : k_kv_append<1, 0>) : (a.fmt ? k_kv_append<0, 1> : k_kv_append<0, 0>);
-  k<<<grid, kAppendThreads, 0, L.stream>>>(a, qkv, n_heads, rows);
+  // kHeld vectors a thread hold the largest piece
+  if ((a.dh << a.page_shift) <= 8 * kHeld * 128) {
+    auto* k = f32 ? (a.fmt ? k_kv_append<1, 1, 128> : k_kv_append<1, 0, 128>) : (a.fmt ? k_kv_append<0, 1, 128> : k_kv_append<0, 0, 128>);
+    k<<<grid, 128, 0, L.stream>>>(a, qkv, n_heads, rows);
+  } else {
+    auto* k = f32 ? (a.fmt ? k_kv_append<1, 1, 256> : k_kv_append<1, 0, 256>) : (a.fmt ? k_kv_append<0, 1, 256> : k_kv_append<0, 0, 256>);
+    k<<<grid, 256, 0, L.stream>>>(a, qkv, n_heads, rows);
+  }
   if (L.launches) ++*L.launches;
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv_read(const KvArgs& a, void* kv, int f32, const Launch& L) {
-  const int64_t n = a.T * (2 * a.hkv * a.dh / 8);
-  const unsigned grid = (unsigned)((n + 255) / 256);
-  auto* k = f32 ? (a.fmt ? k_kv_read<1, 1> : k_kv_read<1, 0>) : (a.fmt ? k_kv_read<0, 1> : k_kv_read<0, 0>);
-  k<<<grid, 256, 0, L.stream>>>(a, kv);
+  // four rows a warp where that still gives every SM its 64 warps
+  const int warps = kReadThreads / 32;
+  const int64_t per = a.T / (64 * (int64_t)L.num_sms);
+  const int rows = (int)(per < 1 ? 1 : per > 4 ? 4 : per);
+  const unsigned grid = (unsigned)((a.T + (int64_t)rows * warps - 1) / ((int64_t)rows * warps));
+  if (f32) a.fmt ? read_dh<1, 1>(a, kv, grid, rows, L.stream) : read_dh<1, 0>(a, kv, grid, rows, L.stream);
+  else a.fmt ? read_dh<0, 1>(a, kv, grid, rows, L.stream) : read_dh<0, 0>(a, kv, grid, rows, L.stream);
   if (L.launches) ++*L.launches;
   return cudaGetLastError();
 }

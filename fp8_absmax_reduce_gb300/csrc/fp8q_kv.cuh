@@ -44,6 +44,21 @@ __device__ __forceinline__ int kv_find(const KvArgs& a, int row) {
   return lo;
 }
 
+// The same by a whole warp: 32 starts at a time, two steps for 1000 sequences instead of ten.
+__device__ __forceinline__ int kv_find_warp(const KvArgs& a, int row) {
+  if (!a.row_start) return row / a.rows;
+  const int lane = threadIdx.x & 31;
+  int lo = -1, hi = a.n_seqs;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 32) / 33, at = lo + (lane + 1) * step;
+    const unsigned le = __ballot_sync(0xFFFFFFFFu, at < hi && a.row_start[at < hi ? at : 0] <= row);
+    const int n = __ffs(~le) ? __ffs(~le) - 1 : 32;  // starts that are not behind the row
+    lo += n * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
 // Page p of sequence s; -1, and reported, where the table names none.
 __device__ __forceinline__ int kv_page(const KvArgs& a, int s, int p) {
   const int id = a.pages[s * a.max_pages + p];
