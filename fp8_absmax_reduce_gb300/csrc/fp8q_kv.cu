@@ -40,13 +40,21 @@ struct In8 {
 
 constexpr uint32_t kInf = 0x7F800000u;
 
-// Bits of the largest finite |v|; values that are not finite are noted.
-__device__ __forceinline__ uint32_t absmax8(const float (&v)[8], bool& nonfinite) {
+// The largest |v| of 8 as fp32 bits (a NaN's are above infinity's); bf16 values by twos.
+template <int F32>
+__device__ __forceinline__ uint32_t absmax8(const In8<F32>& x) {
+  const uint32_t* u = reinterpret_cast<const uint32_t*>(x.w);
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < (F32 ? 8 : 4); ++k) m = F32 ? max(m, u[k] & 0x7FFFFFFFu) : __vmaxu2(m, u[k] & 0x7FFF7FFFu);
+  return F32 ? m : max(m << 16, m & 0xFFFF0000u);
+}
+// The same over what is finite.
+__device__ __forceinline__ uint32_t finite_absmax8(const float (&v)[8]) {
   uint32_t m = 0;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const uint32_t b = abs_bits(v[k]);
-    nonfinite |= b >= kInf;
     m = max(m, b >= kInf ? 0u : b);
   }
   return m;
@@ -63,24 +71,28 @@ __device__ __forceinline__ uint32_t shift4(uint32_t codes, float s) {
   return cvt_fp8x4<FMT>(a.x * s, a.y * s, b.x * s, b.y * s);
 }
 
-// Block (c, h, kv) takes the pieces of pages that begin in rows [c rows_per_block, ...): a piece is what a call writes of one page,
-// and begins at a sequence's first row or at a page's first token.  Its values are read once and kept in registers.
-template <int F32, int FMT, int THREADS>
-__global__ void __launch_bounds__(THREADS) k_kv_append(const KvArgs a, const void* __restrict__ qkv, int n_heads,
-                                                       int rows_per_block) {
+// Group x of THREADS threads (a warp, or a block), head y, K or V z: the pieces of pages that begin in rows [x rows_per_group, ...).  A
+// piece is what a call writes of one page; it begins at a sequence's first row or at a page's first token.  Its values are
+// read once and kept in registers, where kHeld vectors a thread hold them.
+constexpr int kAppendThreads = 128;  // of a block, at least
+template <int F32, int FMT, int DH, int THREADS>
+__global__ void __launch_bounds__(THREADS < kAppendThreads ? kAppendThreads : THREADS)
+    k_kv_append(const KvArgs a, const void* __restrict__ qkv, int n_heads, int rows_per_group) {
+  constexpr int kGroups = THREADS < kAppendThreads ? kAppendThreads / THREADS : 1;
   __shared__ uint32_t red[32];
-  const int h = blockIdx.y, is_v = blockIdx.z, P = 1 << a.page_shift;
-  const int vecs = a.dh >> 3;  // vectors of 8 of a token
-  const int64_t width = (int64_t)(n_heads + 2 * a.hkv) * a.dh;
-  const int64_t col = (int64_t)(n_heads + is_v * a.hkv + h) * a.dh;
+  const int h = blockIdx.y, is_v = blockIdx.z, P = 1 << a.page_shift, tid = threadIdx.x % THREADS;
+  constexpr int vecs = DH / 8;  // vectors of 8 of a token
+  const int64_t width = (int64_t)(n_heads + 2 * a.hkv) * DH;
+  const int64_t col = (int64_t)(n_heads + is_v * a.hkv + h) * DH;
   uint8_t* codes = is_v ? a.v : a.k;
   uint8_t* scales = is_v ? a.v_scale : a.k_scale;
-  const int64_t r0 = (int64_t)blockIdx.x * rows_per_block;
-  const int end = (int)min(r0 + rows_per_block, a.T);
+  const int64_t r0 = ((int64_t)blockIdx.x * kGroups + threadIdx.x / THREADS) * rows_per_group;
+  const int end = (int)min(r0 + rows_per_group, a.T);
+  auto group_max = [&](uint32_t v) { return THREADS == 32 ? warp_max_u32(v) : block_max_u32(v, red); };
   bool nonfinite = false;
   int s = -1;
   KvSeq q{0, 0, 0};
-  for (int row = (int)r0; row < end;) {
+  for (int row = (int)min(r0, a.T); row < end;) {
     if (row < q.first || row >= q.first + q.n) {
       s = kv_find_warp(a, row);
       if (s < 0) { ++row; continue; }
@@ -97,54 +109,87 @@ __global__ void __launch_bounds__(THREADS) k_kv_append(const KvArgs a, const voi
     }
     const int slot = pos & (P - 1);
     const int m = min(P - slot, q.first + q.n - row);  // tokens of this page from here on
-    if (row != q.first && slot != 0) {                 // the piece began in an earlier block
+    if (row != q.first && slot != 0) {                 // the piece began before this group's rows
       row += m;
       continue;
     }
     const int first = row, n = m * vecs;
     row += m;
     const int id = kv_page(a, s, pos >> a.page_shift);
+    const bool fits = THREADS > 32 || n <= kHeld * THREADS;  // a block's registers hold any piece
+    auto load = [&](In8<F32>& x, int i) {
+      const int t = i / vecs;
+      x.load(qkv, (int64_t)(first + t) * width + col + (i - t * vecs) * 8);
+    };
     In8<F32> held[kHeld];
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-      const int i = threadIdx.x + k * THREADS, t = i / vecs;
-      if (i < n) held[k].load(qkv, (int64_t)(first + t) * width + col + (i - t * vecs) * 8);
-    }
+    for (int k = 0; k < kHeld; ++k)
+      if (tid + k * THREADS < n) load(held[k], tid + k * THREADS);
     if (id < 0) continue;
     const int64_t ph = (int64_t)id * a.hkv + h;
     const int was = slot ? (int)scales[ph] - 127 : 0;
-    uint8_t* page = codes + (ph << a.page_shift) * a.dh;
+    uint8_t* page = codes + (ph << a.page_shift) * DH;
     uint32_t amax = 0;
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-      float v[8];
-      held[k].get(v);
-      if ((int)threadIdx.x + k * THREADS < n) amax = max(amax, absmax8(v, nonfinite));
+    for (int k = 0; k < kHeld; ++k)
+      if (tid + k * THREADS < n) amax = max(amax, absmax8(held[k]));
+    if (!fits)
+#pragma unroll 1
+      for (int i = tid + kHeld * THREADS; i < n; i += THREADS) {
+        In8<F32> x;
+        load(x, i);
+        amax = max(amax, absmax8(x));
+      }
+    amax = group_max(amax);
+    const bool odd = amax >= kInf;  // a value is NaN or infinite: those do not count, and become NaN codes
+    if (odd) {
+      amax = 0;
+#pragma unroll 1
+      for (int i = tid; i < n; i += THREADS) {
+        In8<F32> x;
+        load(x, i);
+        float v[8];
+        x.get(v);
+        amax = max(amax, finite_absmax8(v));
+      }
+      amax = group_max(amax);
+      nonfinite = true;
     }
-    amax = block_max_u32(amax, red);
     int X = mx_exponent<FMT>(amax);
     if (slot) X = max(X, was);
     const float scale = pow2_neg(X);
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-      const int i = threadIdx.x + k * THREADS;
+    auto store = [&](const In8<F32>& x, int i) {
       float v[8];
-      held[k].get(v);
+      x.get(v);
+      if (odd) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = abs_bits(v[e]) >= kInf ? __uint_as_float(0x7FC00000u) : __fmul_rn(v[e], scale);
-      if (i < n)
-        *reinterpret_cast<uint2*>(page + slot * a.dh + i * 8) =
-            make_uint2(cvt_fp8x4<FMT>(v[0], v[1], v[2], v[3]), cvt_fp8x4<FMT>(v[4], v[5], v[6], v[7]));
-    }
+        for (int e = 0; e < 8; ++e) v[e] = abs_bits(v[e]) >= kInf ? __uint_as_float(0x7FC00000u) : v[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], scale);
+      *reinterpret_cast<uint2*>(page + slot * DH + i * 8) =
+          make_uint2(cvt_fp8x4<FMT>(v[0], v[1], v[2], v[3]), cvt_fp8x4<FMT>(v[4], v[5], v[6], v[7]));
+    };
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (tid + k * THREADS < n) store(held[k], tid + k * THREADS);
+    if (!fits)
+#pragma unroll 1
+      for (int i = tid + kHeld * THREADS; i < n; i += THREADS) {
+        In8<F32> x;
+        load(x, i);
+        store(x, i);
+      }
     if (slot && X > was) {  // the tokens that were there, to the new scale
       const float down = pow2_down(was - X);
-      for (int i = threadIdx.x; i < slot * vecs; i += THREADS) {
+      for (int i = tid; i < slot * vecs; i += THREADS) {
         uint2* p = reinterpret_cast<uint2*>(page + i * 8);
         const uint2 w = *p;
         *p = make_uint2(shift4<FMT>(w.x, down), shift4<FMT>(w.y, down));
       }
     }
-    if (threadIdx.x == 0 && (!slot || X != was)) scales[ph] = (uint8_t)(X + 127);
+    if (tid == 0 && (!slot || X != was)) scales[ph] = (uint8_t)(X + 127);
+    if (THREADS == 32) __syncwarp();  // every lane has read the scale before a later piece's
   }
   if (nonfinite) atomicOr(a.status, kStatusNonfinite);
 }
@@ -210,6 +255,29 @@ __global__ void __launch_bounds__(kReadThreads) k_kv_read(const KvArgs a, void* 
   }
 }
 
+template <int F32, int FMT, int DH>
+void append_threads(const KvArgs& a, const void* qkv, int n_heads, int sms, cudaStream_t s) {
+  // A piece has a sequence's rows, or a page's tokens.  Where that is 16 at most (or what a warp's registers hold), a warp
+  // takes it alone: nothing waits for a block, and four times as many pieces' loads are in flight.  A group of threads gets a page's tokens of rows, or fewer, down to one,
+  // until there are about as many groups as fit the GPU.
+  const int P = 1 << a.page_shift;
+  const int64_t piece = (a.T + a.n_seqs - 1) / a.n_seqs;
+  const bool warp = (piece < P ? piece : P) <= 16 || P * DH <= 8 * kHeld * 32;
+  const int64_t per = a.T * 2 * a.hkv / ((warp ? 64 : 8) * sms);
+  const int rows = (int)(per < 1 ? 1 : 2 * per < P ? per : P);
+  const int64_t groups = (a.T + rows - 1) / rows;
+  const dim3 grid((unsigned)(warp ? (groups + 3) / 4 : groups), (unsigned)a.hkv, 2);
+  if (warp) k_kv_append<F32, FMT, DH, 32><<<grid, kAppendThreads, 0, s>>>(a, qkv, n_heads, rows);
+  else if (P * DH <= 8 * kHeld * 128) k_kv_append<F32, FMT, DH, 128><<<grid, 128, 0, s>>>(a, qkv, n_heads, rows);
+  else k_kv_append<F32, FMT, DH, 256><<<grid, 256, 0, s>>>(a, qkv, n_heads, rows);
+}
+template <int F32, int FMT>
+void append_dh(const KvArgs& a, const void* qkv, int n_heads, int sms, cudaStream_t s) {
+  if (a.dh == 128) append_threads<F32, FMT, 128>(a, qkv, n_heads, sms, s);
+  else if (a.dh == 96) append_threads<F32, FMT, 96>(a, qkv, n_heads, sms, s);
+  else append_threads<F32, FMT, 64>(a, qkv, n_heads, sms, s);
+}
+
 template <int F32, int FMT>
 void read_dh(const KvArgs& a, void* kv, unsigned grid, int rows, cudaStream_t s) {
   auto* k = a.dh == 128 ? k_kv_read<F32, FMT, 128> : a.dh == 96 ? k_kv_read<F32, FMT, 96> : k_kv_read<F32, FMT, 64>;
@@ -219,19 +287,8 @@ void read_dh(const KvArgs& a, void* kv, unsigned grid, int rows, cudaStream_t s)
 }  // namespace
 
 cudaError_t launch_kv_append(const KvArgs& a, const void* qkv, int f32, int n_heads, const Launch& L) {
-  // Rows of a block: a page's where that fills the GPU (T = 8680, 8 heads of 128: 10 us); for fewer, down to one, until
-  // there are about eight blocks an SM, so that a block seldom writes more than one sequence's token.
-  const int64_t per = a.T * 2 * a.hkv / (8 * L.num_sms);
-  const int rows = (int)(per < 1 ? 1 : per < (1 << a.page_shift) ? per : 1 << a.page_shift);
-  const dim3 grid((unsigned)((a.T + rows - 1) / rows), (unsigned)a.hkv, 2);
-  // kHeld vectors a thread hold the largest piece
-  if ((a.dh << a.page_shift) <= 8 * kHeld * 128) {
-    auto* k = f32 ? (a.fmt ? k_kv_append<1, 1, 128> : k_kv_append<1, 0, 128>) : (a.fmt ? k_kv_append<0, 1, 128> : k_kv_append<0, 0, 128>);
-    k<<<grid, 128, 0, L.stream>>>(a, qkv, n_heads, rows);
-  } else {
-    auto* k = f32 ? (a.fmt ? k_kv_append<1, 1, 256> : k_kv_append<1, 0, 256>) : (a.fmt ? k_kv_append<0, 1, 256> : k_kv_append<0, 0, 256>);
-    k<<<grid, 256, 0, L.stream>>>(a, qkv, n_heads, rows);
-  }
+  if (f32) a.fmt ? append_dh<1, 1>(a, qkv, n_heads, L.num_sms, L.stream) : append_dh<1, 0>(a, qkv, n_heads, L.num_sms, L.stream);
+  else a.fmt ? append_dh<0, 1>(a, qkv, n_heads, L.num_sms, L.stream) : append_dh<0, 0>(a, qkv, n_heads, L.num_sms, L.stream);
   if (L.launches) ++*L.launches;
   return cudaGetLastError();
 }
