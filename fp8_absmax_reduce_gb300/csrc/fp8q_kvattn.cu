@@ -20,57 +20,20 @@
 //
 // Work.  The keys of all (sequence, row tile, K/V head) units form one line of blocks of 128 keys, each unit preceded by what it costs
 // besides; it is cut into equal parts, one a CTA.  A unit that is cut leaves fp32 partial results, which the second kernel joins in order.
-#include <cuda_fp16.h>
+#include <atomic>
 
-#include "fp8q_head.cuh"
-#include "fp8q_kv.cuh"
+#include "fp8q_kvline.cuh"
 
 namespace fp8q {
 
 namespace {
 
-constexpr int kThreads = 128, kWarps = 4, kBlockKeys = 128;
-constexpr int kMaxCtas = 152 * 5;
-constexpr int kNoPage = 0x1000;   // in place of a scale: the keys are not seen
-constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
-
-// What CTA j leaves behind when it begins a unit and does not end it.
-struct Cut {
-  int64_t first, end;  // the unit on the line; first = end: nothing
-  int64_t total;       // of the line
-  int ctas;            // parts of the line
-  int head;            // K/V head
-  int row0, rows;      // first row of the call, and rows (tokens times heads) of the tile
-  int group_row;       // the tile's first (token, head) pair
-};
-
-struct AttendArgs {
-  KvArgs kv;
-  const uint16_t* qkv;
-  int n_heads;
-  float scale_log2;  // log2(e) / sqrt(head_dim)
-  uint16_t* att;
-  float* lse;
-  float* part_o;     // [2 kMaxCtas][R][DH]
-  float* part_lse;   // [2 kMaxCtas][R], log2
-  Cut* cuts;         // [kMaxCtas]
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
+constexpr int kThreads = 128, kWarps = 4;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 // 16 bytes into shared memory; bytes = 0 writes zeros and reads nothing.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
@@ -117,12 +80,6 @@ __device__ __forceinline__ void take(const uint8_t* tile, int row, int b, uint32
   }
 }
 
-// Whether any of four codes is NaN or infinite.
-template <int FMT>
-__device__ __forceinline__ uint32_t nonfinite4(uint32_t w) {
-  return ((w & 0x7F7F7F7Fu) + (FMT == 0 ? 0x01010101u : 0x04040404u)) & 0x80808080u;
-}
-
 template <int DH, int NT, int RW>
 struct Shape {
   static constexpr int KW = kWarps / RW;      // groups of warps that share their keys
@@ -141,12 +98,6 @@ struct Shape {
 // What a unit costs besides its keys, in blocks of keys: its rows, its first page, joining the warps.
 constexpr int kUnitCost = 3;
 
-// Where a CTA's part of the line begins: every CTA adds the line up by itself.
-struct Line {
-  int s;         // the sequence
-  KvSeq q;
-  int64_t base;  // its first block
-};
 template <int R>
 __device__ __forceinline__ int64_t seq_cost(const AttendArgs& p, const KvSeq& q, int& units, int& nb, int& cost) {
   const int pairs = q.n * (p.n_heads / p.kv.hkv);  // below 2^31 with T n_heads
@@ -155,11 +106,6 @@ __device__ __forceinline__ int64_t seq_cost(const AttendArgs& p, const KvSeq& q,
   cost = nb ? nb + kUnitCost : 1;
   return (int64_t)units * cost;
 }
-// total j / ctas; a 64-bit division costs a third of a microsecond
-__device__ __forceinline__ int64_t part(int64_t total, int j, int ctas) {
-  return total < (1 << 21) ? (int64_t)((uint32_t)total * (uint32_t)j / (uint32_t)ctas) : total * j / ctas;
-}
-
 // Transposes an 8 x 8 tile of 16-bit values over the warp: from (row lane / 4, columns 2 (lane % 4) and the next) to the same of its columns.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t y;
@@ -687,24 +633,28 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_join(const AttendArgs p) {
 }
 
 // Rows of a CTA for the (token, head) pairs of a sequence and K/V head: 8 of one warp or 16; above, two or four warps share their keys
-// for 16 rows each.
+// for 16 rows each; and from kManyPairs on the kernel on tensor memory.
+constexpr int kManyPairs = 65;
 struct Rows {
   int nt, rw;
-  int count() const { return 8 * nt * rw; }
+  bool many() const { return nt == 0; }
+  int count() const { return many() ? kv_attend_many_rows() : 8 * nt * rw; }
+  int ctas() const { return many() ? 152 : kMaxCtas; }
 };
 Rows rows_of(int64_t T, int n_seqs, int n_heads, int hkv) {
   const int64_t pairs = (T + n_seqs - 1) / n_seqs * (n_heads / hkv);
-  return pairs <= 8 ? Rows{1, 1} : pairs <= 16 ? Rows{2, 1} : pairs <= 32 ? Rows{2, 2} : Rows{2, 4};
+  return pairs <= 8 ? Rows{1, 1} : pairs <= 16 ? Rows{2, 1} : pairs <= 32 ? Rows{2, 2} : pairs < kManyPairs ? Rows{2, 4} : Rows{0, 0};
 }
 struct Pieces {
   size_t lse, cuts, all;
 };
-Pieces pieces(int rows, int dh) {
+Pieces pieces(Rows r, int dh) {
   auto pad = [](size_t n) { return (n + 255) & ~size_t(255); };
+  const size_t parts = 2 * (size_t)r.ctas();
   Pieces w;
-  w.lse = pad((size_t)2 * kMaxCtas * rows * dh * 4);
-  w.cuts = w.lse + pad((size_t)2 * kMaxCtas * rows * 4);
-  w.all = w.cuts + pad(sizeof(Cut) * kMaxCtas);
+  w.lse = pad(parts * r.count() * dh * 4);
+  w.cuts = w.lse + pad(parts * r.count() * 4);
+  w.all = w.cuts + pad(sizeof(Cut) * r.ctas());
   return w;
 }
 
@@ -713,7 +663,8 @@ cudaError_t launch(const AttendArgs& p, int sms, int64_t pairs, cudaStream_t s) 
   using C = Shape<DH, NT, RW>;
   static_assert(C::kCtas * 152 <= kMaxCtas, "parts of the workspace");
   const int ctas = min(kMaxCtas, sms * C::kCtas);
-  cudaError_t e = cudaFuncSetAttribute(k_kv_attend<FMT, DH, NT, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = kv_smem(k_kv_attend<FMT, DH, NT, RW>, C::kSmem, configured);
   if (e != cudaSuccess) return e;
   k_kv_attend<FMT, DH, NT, RW><<<ctas, kThreads, C::kSmem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -734,19 +685,20 @@ cudaError_t launch_dh(Rows r, const AttendArgs& p, int sms, int64_t pairs, cudaS
 }  // namespace
 
 size_t kv_attend_workspace_bytes(int64_t T, int n_seqs, int n_heads, int hkv, int dh) {
-  return pieces(rows_of(T, n_seqs, n_heads, hkv).count(), dh).all;
+  return pieces(rows_of(T, n_seqs, n_heads, hkv), dh).all;
 }
 
 cudaError_t launch_kv_attend(const KvArgs& a, const uint16_t* qkv, int n_heads, uint16_t* att, float* lse, void* ws,
                              const Launch& L) {
   const Rows r = rows_of(a.T, a.n_seqs, n_heads, a.hkv);
-  const Pieces w = pieces(r.count(), a.dh);
+  const Pieces w = pieces(r, a.dh);
   uint8_t* b = static_cast<uint8_t*>(ws);
   AttendArgs p{a, qkv, n_heads, kLog2e / sqrtf((float)a.dh), att, lse, reinterpret_cast<float*>(b),
                reinterpret_cast<float*>(b + w.lse), reinterpret_cast<Cut*>(b + w.cuts)};
   // rows of a unit at most, where the host knows them
   const int64_t pairs = a.row_start ? (int64_t)1 << 20 : (int64_t)a.rows * (n_heads / a.hkv);
-  const cudaError_t e = a.fmt ? launch_dh<1>(r, p, L.num_sms, pairs, L.stream) : launch_dh<0>(r, p, L.num_sms, pairs, L.stream);
+  const cudaError_t e = r.many() ? launch_kv_attend_many(p, min(r.ctas(), L.num_sms), L.stream)
+                        : a.fmt ? launch_dh<1>(r, p, L.num_sms, pairs, L.stream) : launch_dh<0>(r, p, L.num_sms, pairs, L.stream);
   if (e != cudaSuccess) return e;
   if (L.launches) *L.launches += 2;
   return cudaSuccess;

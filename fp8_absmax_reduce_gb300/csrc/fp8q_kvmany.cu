@@ -1,0 +1,668 @@
+// Causal attention over the 8-bit key/value cache for many rows a sequence (pieces of prompts): on the 5th-generation tensor
+// cores, bound by them and by the exponentials.
+//
+// The products are tcgen05 kind::f16 ones, fp16 operands and fp32 accumulators in tensor memory: FP8 codes are fp16 numbers, and q is
+// one over a power of two of its row, so the scores lose nothing.  (FP8 operands would need q and P in several 4-bit parts.)
+// A CTA has 256 rows of one K/V head, two tiles of 128 (token, query head) pairs, A and B, which share what is
+// made of each block of 128 keys; its 384 threads (with a thirteenth warp each thread would have 128 registers, not 168):
+//   warps 0-2    codes of K and V from the cache's pages, a block ahead in registers, into swizzled fp16 tiles (K two, V one), and
+//                the block's scales;
+//   warp 3       the products, one thread: S_A = Q_A K^T, O_A += P_A V of the block before, then B's;
+//   warps 4-11   a row a thread (A, then B): q into shared memory; per block the row's maximum from S, P = 2^(s - m) as fp16
+//                into shared memory, and at the end O over the sum.
+// P's window is that of the few rows' kernel: p 2^11 in fp16, the reference maximum moving when it is exceeded by 2^4.
+// The keys of all (sequence, row tile, K/V head) units are cut into equal parts, one a CTA, as there.
+//
+// Every mbarrier wait is bounded; on expiry the CTA records FP8Q_STATUS_TIMEOUT, stops issuing, waits for the products that it
+// issued, frees tensor memory and exits.
+#include "fp8q_kvline.cuh"
+
+namespace fp8q {
+
+namespace {
+
+constexpr int kLoaders = 96, kMmaWarp = 3, kFirstRowWarp = 4, kThreads = 384;
+constexpr int kTileRows = 128, kRows = 2 * kTileRows;
+constexpr int kAtom = 16384;       // 128 rows x 128 bytes: 64 fp16 columns of a swizzled tile
+constexpr int kTile = 2 * kAtom;   // a tile of 128 columns
+constexpr int kQ = 0;              // [2 tiles]
+constexpr int kK = kQ + 2 * kTile; // [2 stages]
+constexpr int kV = kK + 2 * kTile;
+constexpr int kP = kV + kTile;     // [2 tiles]
+constexpr int kBars = kP + 2 * kTile;
+constexpr int kMisc = kBars + 256;
+constexpr float kOffset = 11.0f, kSlack = 4.0f;
+constexpr int kAll = 0x7FFFFFFF;
+// What a unit costs besides its keys, in blocks: q, the first pages, the results.
+constexpr int kUnitCost = 2;
+
+// A block's scales as the rows need them, 16 keys each: 2^X of K; kOffset + dx and 2^-dx of V, dx its exponent over the segment's largest.
+struct BlockScales {
+  float k[8], dx[8], back[8];
+  int none[4];  // [0]: bit g: keys 16 g .. have no page
+};
+struct Misc {
+  BlockScales scales[2];  // by K's stage
+  int xref[2];            // by segment: the largest exponent of V
+  int odd;                // some V was NaN or infinite, and is 0 in its tile
+  uint32_t tmem;
+  int abort;
+};
+constexpr int kSmem = kMisc + (int)sizeof(Misc) + 1024;
+static_assert(kSmem <= 232448 - 64, "shared memory per CTA");
+
+__host__ __device__ constexpr uint32_t idesc_f16(int n, int b_mn) {
+  return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+// S = Q K^T over DH: both K-major tiles of 128 rows.
+template <int DH>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
+#pragma unroll
+  for (int i = 0; i < DH / 16; ++i) {
+    const uint32_t off = (uint32_t)((i >> 2) * kAtom + (i & 3) * 32);
+    umma_bf16(d, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + off, 16, 1024), idesc_f16(128, 0), i ? 1u : 0u);
+  }
+}
+// O (+)= P V over 128 keys: P K-major, V MN-major (a row a key), N = 64 or 128 columns.
+template <int N>
+__device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t off = (uint32_t)((i >> 2) * kAtom + (i & 3) * 32);
+    umma_bf16(d, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + i * 2048, kAtom, 1024), idesc_f16(N, 1),
+              (accumulate || i) ? 1u : 0u);
+  }
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort)) != 0;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// 16-byte piece j (8 fp16) of row r of a swizzled tile.
+__device__ __forceinline__ uint32_t piece(uint32_t tile, int r, int j) {
+  return tile + (uint32_t)((j >> 3) * kAtom + r * 128 + (((j ^ r) & 7) << 4));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// A sequence's units: row tile by row tile, each for every K/V head.
+struct Tiles {
+  int pairs, before, G;  // (token, head) pairs; tokens before the call's; query heads of a K/V head
+  __device__ __forceinline__ int count() const { return (int)((pairs + (int64_t)(kRows - 1)) / kRows); }
+  __device__ __forceinline__ int rows(int rt) const { return min(kRows, pairs - rt * kRows); }
+  // the keys that pair r sees
+  __device__ __forceinline__ int limit(int r) const { return max(0, before + r / G + 1); }
+  __device__ __forceinline__ int blocks(int rt) const { return (limit(rt * kRows + rows(rt) - 1) + kBlockKeys - 1) / kBlockKeys; }
+  __device__ __forceinline__ int cost(int rt) const {
+    const int nb = blocks(rt);
+    return nb ? nb + kUnitCost : 1;
+  }
+};
+__device__ __forceinline__ Tiles tiles_of(const AttendArgs& p, const KvSeq& q) {
+  const int G = p.n_heads / p.kv.hkv;
+  return Tiles{q.n * G, q.len - q.n, G};
+}
+__device__ __forceinline__ int64_t seq_cost(const AttendArgs& p, const KvSeq& q) {
+  const Tiles t = tiles_of(p, q);
+  int64_t sum = 0;
+  for (int rt = 0; rt < t.count(); ++rt) sum += t.cost(rt);
+  return sum * p.kv.hkv;
+}
+
+// One part of the line after the other: what all roles walk through alike.
+struct Walk {
+  const AttendArgs& p;
+  int s, rt;       // sequence, row tile
+  KvSeq q;
+  Tiles t;
+  int64_t base;    // first block of the row tile's units
+  int64_t at, end;
+  // of the segment
+  int h, r0, n_rows, nb, b0, b1;
+  int64_t unit0, cost;
+  __device__ __forceinline__ Walk(const AttendArgs& args, const Line& l, int64_t begin, int64_t stop)
+      : p(args), s(l.s), rt(0), q(l.q), t(tiles_of(args, l.q)), base(l.base), at(begin), end(stop) {}
+  __device__ __forceinline__ bool next() {
+    while (at < end) {
+      if (rt >= t.count()) {
+        if (++s >= p.kv.n_seqs) return false;
+        q = kv_seq(p.kv, s);
+        t = tiles_of(p, q);
+        rt = 0;
+        continue;
+      }
+      const int c = t.cost(rt);
+      const int64_t here = (int64_t)c * p.kv.hkv;
+      if (at >= base + here) {
+        base += here;
+        ++rt;
+        continue;
+      }
+      h = here < (int64_t)1 << 32 ? (int)((uint32_t)(at - base) / (uint32_t)c) : (int)((at - base) / c);
+      const int v0 = (int)((at - base) - (int64_t)h * c), v1 = (int)min((int64_t)c, v0 + (end - at));
+      unit0 = base + (int64_t)h * c;
+      cost = c;
+      nb = t.blocks(rt);
+      at += v1 - v0;
+      b0 = max(0, v0 - kUnitCost);
+      b1 = min(nb, max(0, v1 - kUnitCost));
+      if (b0 == b1 && nb) continue;
+      r0 = rt * kRows;
+      n_rows = t.rows(rt);
+      return true;
+    }
+    return false;
+  }
+  // blocks of this segment that tile `side` sees
+  __device__ __forceinline__ int blocks_of(int side) const {
+    const int rows = min(kTileRows, n_rows - side * kTileRows);
+    if (rows <= 0) return 0;
+    return max(0, min(b1, (t.limit(r0 + side * kTileRows + rows - 1) + kBlockKeys - 1) / kBlockKeys) - b0);
+  }
+};
+
+template <int FMT, int DH>
+__global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs p) {
+  constexpr int N = DH == 64 ? 64 : 128;  // columns of V's tile and of O: 96 are filled up with zeros
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBars);
+  uint64_t* q_full = bars + 0;    // [2] per tile, once a segment
+  uint64_t* k_full = bars + 2;    // [2] per stage
+  uint64_t* k_empty = bars + 4;   // [2] both S of the block are computed
+  uint64_t* v_full = bars + 6;
+  uint64_t* v_empty = bars + 7;   // both P V of the block are computed
+  uint64_t* s_full = bars + 8;    // [2] per tile
+  uint64_t* s_free = bars + 10;   // [2] the rows have read S
+  uint64_t* p_full = bars + 12;   // [2]
+  uint64_t* p_free = bars + 14;   // [2] P V has read P, and O holds every product so far
+  uint64_t* drain = bars + 16;
+  Misc& misc = *reinterpret_cast<Misc*>(smem + kMisc);
+  volatile int* abort_flag = &misc.abort;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  start_dependents();
+
+  // ---- the line, and this CTA's part of it (the sums lie where Q will)
+  int64_t* warp_sums = reinterpret_cast<int64_t*>(smem);
+  Line* line_s = reinterpret_cast<Line*>(smem + 256);
+  const int per = (p.kv.n_seqs + kThreads - 1) / kThreads;
+  int64_t total = 0, before = 0, own = 0;
+  for (int s = t * per; s < min((t + 1) * per, p.kv.n_seqs); ++s) own += seq_cost(p, kv_seq(p.kv, s));
+  {
+    int64_t upto = own;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, k);
+      if (lane >= k) upto += v;
+    }
+    if (lane == 31) warp_sums[warp] = upto;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) {
+      before += w < warp ? warp_sums[w] : 0;
+      total += warp_sums[w];
+    }
+    before += upto - own;
+  }
+  const int ctas = (int)min((int64_t)gridDim.x, total);
+  const int j = blockIdx.x;
+  if (t == 0) p.cuts[j].first = p.cuts[j].end = 0;
+  if (j >= ctas) return;
+  const int64_t begin = part(total, j, ctas), end = part(total, j + 1, ctas);
+  if (begin >= before && begin < before + own) {
+    int64_t base = before;
+    int s = t * per;
+    KvSeq q = kv_seq(p.kv, s);
+    for (; s < p.kv.n_seqs - 1; ++s) {
+      const int64_t n = seq_cost(p, q);
+      if (begin < base + n) break;
+      base += n;
+      q = kv_seq(p.kv, s + 1);
+    }
+    line_s->s = s;
+    line_s->q = q;
+    line_s->base = base;
+  }
+  if (t == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], kTileRows);
+      mbar_init(&k_full[i], kLoaders);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], kTileRows);
+      mbar_init(&p_full[i], kTileRows);
+      mbar_init(&p_free[i], 1);
+    }
+    mbar_init(v_full, kLoaders);
+    mbar_init(v_empty, 1);
+    mbar_init(drain, 1);
+    misc.abort = misc.odd = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) { tmem_alloc(&misc.tmem, 512); tmem_relinquish(); }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc.tmem;
+  const Line line = *line_s;
+  __syncthreads();  // Q may be written
+  const uint32_t sbase = smem_addr(smem);
+  if (DH == 96) {
+    for (int i = t; i < 128 * 4; i += kThreads) st_shared_v4(piece(sbase + kV, i >> 2, 12 + (i & 3)), make_uint4(0, 0, 0, 0));
+    __syncthreads();
+  }
+  Walk w(p, line, begin, end);
+  int tile = 0, seg = 0;  // blocks and segments so far
+  bool ok = true;
+
+  if (warp < kLoaders / 32) {
+    // ---------------- codes to fp16 ----------------
+    constexpr int kPieces = DH / 16;  // of 16 codes, of a key
+    constexpr int kMine = (kBlockKeys * kPieces + kLoaders - 1) / kLoaders;  // of a thread, of a block
+    while (ok && w.next()) {
+      const int n_blocks = max(w.blocks_of(0), w.blocks_of(1));
+      if (n_blocks == 0) { ++seg; continue; }
+      const int klim = w.t.limit(w.r0 + w.n_rows - 1), stop = w.b0 + n_blocks;
+      const int32_t* table = p.kv.pages + (int64_t)w.s * p.kv.max_pages;
+      const int mask = (1 << p.kv.page_shift) - 1;
+      // lanes 0 .. 7: the page of keys 16 lane .. of block b; -1: none
+      auto page_of = [&](int b) {
+        const int key = b * kBlockKeys + 16 * lane;
+        if (lane >= 8 || b >= stop || key >= klim) return -1;
+        const int id = table[key >> p.kv.page_shift];
+        if (id >= 0 && id < p.kv.n_pages) return id;
+        atomicOr(p.kv.status, kStatusBadCache);
+        return -1;
+      };
+      uint4 kw[kMine], vw[kMine];
+      auto load = [&](const uint8_t* codes, int b, int ids, uint4 (&x)[kMine]) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int idx = i * kLoaders + t, row = idx / kPieces, col = (idx - row * kPieces) * 16, key = b * kBlockKeys + row;
+          const int id = __shfl_sync(0xFFFFFFFFu, ids, (row >> 4) & 7);
+          const int64_t at = ((((int64_t)id * p.kv.hkv + w.h) << p.kv.page_shift) + (key & mask)) * DH + col;
+          x[i] = id >= 0 && row < kBlockKeys && key < klim ? ld_nc_v4(codes + at) : make_uint4(0, 0, 0, 0);
+        }
+      };
+      int ids = page_of(w.b0), ids_next = page_of(w.b0 + 1);
+      load(p.kv.k, w.b0, ids, kw);
+      load(p.kv.v, w.b0, ids, vw);
+      // the segment's largest exponent of V (every warp by itself: no wait among them)
+      int xref = -1000;
+      for (int pg = (w.b0 * kBlockKeys >> p.kv.page_shift) + lane; (int64_t)pg << p.kv.page_shift < min((int64_t)klim, (int64_t)stop * kBlockKeys);
+           pg += 32) {
+        const int id = table[pg];
+        if (id >= 0 && id < p.kv.n_pages) xref = max(xref, (int)p.kv.v_scale[(int64_t)id * p.kv.hkv + w.h] - 127);
+      }
+      xref = __reduce_max_sync(0xFFFFFFFFu, xref);
+      if (t == 0) misc.xref[seg & 1] = xref;
+      auto convert = [&](uint32_t dst, const uint4& x, int row, int ch) {
+        const uint4 lo = make_uint4(f16x2_of<FMT>(x.x), f16x2_of<FMT>(x.x >> 16), f16x2_of<FMT>(x.y), f16x2_of<FMT>(x.y >> 16));
+        const uint4 hi = make_uint4(f16x2_of<FMT>(x.z), f16x2_of<FMT>(x.z >> 16), f16x2_of<FMT>(x.w), f16x2_of<FMT>(x.w >> 16));
+        // the pieces of the second 64 columns in the other order: eight lanes then write to all banks
+        const bool swap = DH == 128 && ch >= 4;
+        st_shared_v4(piece(dst, row, 2 * ch + swap), swap ? hi : lo);
+        st_shared_v4(piece(dst, row, 2 * ch + !swap), swap ? lo : hi);
+      };
+      for (int b = w.b0; b < stop && ok; ++b, ++tile) {
+        const int st = tile & 1;
+        const uint32_t u = (uint32_t)(tile >> 1) & 1u;
+        // scales of this block, lanes 0 .. 7 of warp 0 K's, of warp 1 V's
+        int x = kNoPage;
+        if (warp < 2 && ids >= 0) x = (int)(warp ? p.kv.v_scale : p.kv.k_scale)[(int64_t)ids * p.kv.hkv + w.h] - 127;
+        if (!warp_wait(&k_empty[st], u ^ 1u, abort_flag)) { ok = false; break; }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int idx = i * kLoaders + t, row = idx / kPieces;
+          if (row < kBlockKeys) convert(sbase + kK + st * kTile, kw[i], row, idx - row * kPieces);
+        }
+        BlockScales& sc = misc.scales[st];
+        if (warp == 0) {
+          const unsigned none = __ballot_sync(0xFFFFFFFFu, x == kNoPage) & 0xFFu;
+          if (lane < 8) sc.k[lane] = pow2i(x == kNoPage ? 0 : x);
+          if (lane == 0) sc.none[0] = (int)none;
+        } else if (warp == 1 && lane < 8) {
+          const int dx = max(x == kNoPage ? -60 : x - xref, -60);
+          sc.dx[lane] = kOffset + (float)dx;
+          sc.back[lane] = pow2i(-dx);
+        }
+        fence_async_shared();
+        mbar_arrive(&k_full[st]);
+        ids = ids_next;
+        ids_next = page_of(b + 2);
+        load(p.kv.k, b + 1, ids, kw);
+        if (!warp_wait(v_empty, ((uint32_t)tile & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int idx = i * kLoaders + t, row = idx / kPieces, ch = idx - row * kPieces;
+          uint32_t v[4] = {vw[i].x, vw[i].y, vw[i].z, vw[i].w};
+          if (nonfinite4<FMT>(v[0]) | nonfinite4<FMT>(v[1]) | nonfinite4<FMT>(v[2]) | nonfinite4<FMT>(v[3])) {
+            // a weight of 0 times it would be NaN in rows that do not see it: 0 here, and the rows look for themselves
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] &= ~((nonfinite4<FMT>(v[k]) >> 7) * 0xFFu);
+            misc.odd = 1;
+          }
+          if (row < kBlockKeys) convert(sbase + kV, make_uint4(v[0], v[1], v[2], v[3]), row, ch);
+        }
+        fence_async_shared();
+        mbar_arrive(v_full);
+        load(p.kv.v, b + 1, ids, vw);
+      }
+      ++seg;
+    }
+    if (!ok) {
+      atomicOr(p.kv.status, kStatusTimeout);
+      *abort_flag = 1;
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      // ---------------- the products ----------------
+      uint32_t nq[2] = {0, 0}, ns[2] = {0, 0};  // segments and blocks of each tile so far
+      while (ok && w.next()) {
+        const int na = w.blocks_of(0), nb = w.blocks_of(1), n = max(na, nb);
+        const int nx[2] = {na, nb};
+        if (n == 0) continue;
+        for (int side = 0; side < 2 && ok; ++side)
+          if (nx[side]) {
+            ok = mbar_wait(&q_full[side], nq[side] & 1u, abort_flag);
+            ++nq[side];
+          }
+        for (int b = 0; b <= n && ok; ++b) {
+          const int st = (tile + b) & 1;
+          if (b < n && !mbar_wait(&k_full[st], (uint32_t)((tile + b) >> 1) & 1u, abort_flag)) { ok = false; break; }
+          if (b > 0 && !mbar_wait(v_full, (uint32_t)(tile + b - 1) & 1u, abort_flag)) { ok = false; break; }
+          for (int side = 0; side < 2; ++side) {
+            if (b < nx[side]) {
+              if (!mbar_wait(&s_free[side], ((ns[side] + (uint32_t)b) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+              tc_fence_after();
+              mma_scores<DH>(tmem + side * 128, sbase + kQ + side * kTile, sbase + kK + st * kTile);
+              umma_commit(&s_full[side]);
+            }
+            if (side == 1 && b < n) umma_commit(&k_empty[st]);
+            if (b > 0 && b - 1 < nx[side]) {
+              if (!mbar_wait(&p_full[side], (ns[side] + (uint32_t)(b - 1)) & 1u, abort_flag)) { ok = false; break; }
+              tc_fence_after();
+              mma_values<N>(tmem + 256 + side * 128, sbase + kP + side * kTile, sbase + kV, b > 1);
+              umma_commit(&p_free[side]);
+            }
+          }
+          if (ok && b > 0) umma_commit(v_empty);
+        }
+        tile += n;
+        ns[0] += (uint32_t)na;
+        ns[1] += (uint32_t)nb;
+      }
+      if (!ok) {
+        atomicOr(p.kv.status, kStatusTimeout);
+        *abort_flag = 1;
+      }
+      umma_commit(drain);
+      int dummy = 0;
+      mbar_wait(drain, 0, &dummy);
+    }
+  } else {
+    // ---------------- a row a thread ----------------
+    const int side = (warp - kFirstRowWarp) >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + (uint32_t)(side * 128) + lane_off, tO = tS + 256;
+    const uint32_t qtile = sbase + kQ + side * kTile, ptile = sbase + kP + side * kTile;
+    uint32_t done = 0;  // blocks of this tile so far
+    while (ok && w.next()) {
+      const int nx = w.blocks_of(side), n = max(w.blocks_of(0), w.blocks_of(1));
+      const int i = side * kTileRows + r, pair = w.r0 + i;
+      const bool real = i < w.n_rows;
+      const int G = w.t.G, tok = pair / G, hd = w.h * G + pair - tok * G;
+      const int64_t row = w.q.first + tok;
+      const int limit = real ? w.t.limit(pair) : kAll;
+      const int kmin = __reduce_min_sync(0xFFFFFFFFu, limit);
+      float m = -INFINITY, l = 0.0f;
+      int xref = 0;
+      if (nx) {
+        // q over a power of two of its row, as fp16
+        uint32_t x[DH / 2];
+        const uint16_t* src = p.qkv + row * (p.n_heads + 2 * p.kv.hkv) * DH + (int64_t)hd * DH;
+        uint32_t big = 0;
+#pragma unroll
+        for (int k = 0; k < DH / 8; ++k) {
+          const uint4 v = real ? ld_nc_v4(src + 8 * k) : make_uint4(0, 0, 0, 0);
+          x[4 * k] = v.x; x[4 * k + 1] = v.y; x[4 * k + 2] = v.z; x[4 * k + 3] = v.w;
+        }
+#pragma unroll
+        for (int k = 0; k < DH / 2; ++k) big = max(big, absmax_bf16x2(x[k]));
+        const int ex = max((int)(big >> 23) - 127, -110);
+        const float fq = pow2i(14 - ex), rowf = p.scale_log2 * pow2i(ex - 14);
+#pragma unroll
+        for (int k = 0; k < DH / 8; ++k) {
+          uint32_t y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = pack_half2(bf16_lo(x[4 * k + e]) * fq, bf16_hi(x[4 * k + e]) * fq);
+          st_shared_v4(piece(qtile, r, k), make_uint4(y[0], y[1], y[2], y[3]));
+        }
+        fence_async_shared();
+        mbar_arrive(&q_full[side]);
+
+        for (int b = 0; b < nx && ok; ++b, ++done) {
+          const int kt = tile + b, st = kt & 1;
+          if (!warp_wait(&s_full[side], done & 1u, abort_flag)) { ok = false; break; }
+          // the block's scales, from their writers (long arrived: S is made of that block)
+          if (!warp_wait(&k_full[st], (uint32_t)(kt >> 1) & 1u, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const BlockScales& sc = misc.scales[st];
+          xref = misc.xref[seg & 1];
+          const int key0 = (w.b0 + b) * kBlockKeys, none = sc.none[0];
+          const bool edge = key0 + kBlockKeys > kmin || none;
+          float f[8];
+#pragma unroll
+          for (int g = 0; g < 8; ++g) f[g] = fminf(fmaxf(rowf * sc.k[g], 0x1p-100f), 0x1p126f);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t z[32];
+            tmem_ld32(tS + c * 32, z);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              float y[2] = {-INFINITY, -INFINITY};
+              if (edge) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  const bool out = key0 + c * 32 + g * 16 + k >= limit || (none >> (2 * c + g) & 1);
+                  y[k & 1] = fmaxf(y[k & 1], out ? -INFINITY : __uint_as_float(z[g * 16 + k]));
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) y[k & 1] = fmaxf(y[k & 1], __uint_as_float(z[g * 16 + k]));
+              }
+              mx = fmaxf(mx, fmaxf(y[0], y[1]) * f[2 * c + g]);
+            }
+          }
+          // P V of the block before has read P, and O holds every product up to it
+          if (!warp_wait(&p_free[side], (done & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          if (__any_sync(0xFFFFFFFFu, mx > m + kSlack)) {
+            const float mn = fmaxf(m, mx), alpha = mn == m ? 1.0f : ex2(m - mn);
+            if (b > 0) {
+#pragma unroll 1
+              for (int c = 0; c < N / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tO + c * 32, o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                tmem_st32(tO + c * 32, o);
+              }
+            }
+            l *= alpha;
+            m = mn;
+          }
+          const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t z[32], y[16];
+            tmem_ld32(tS + c * 32, z);
+            if (c == 3) {
+              tc_fence_before();
+              mbar_arrive(&s_free[side]);
+            }
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const float2 fg = make_float2(f[2 * c + g], f[2 * c + g]);
+              const float cg = sc.dx[2 * c + g] - ref;
+              const float2 c2 = make_float2(cg, cg);
+              float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int col = g * 16 + 2 * k;
+                const float2 e = __ffma2_rn(make_float2(__uint_as_float(z[col]), __uint_as_float(z[col + 1])), fg, c2);
+                float p0 = ex2(e.x), p1 = ex2(e.y);
+                if (edge) {
+                  const int key = key0 + c * 32 + col;
+                  if (key >= limit || (none >> (2 * c + g) & 1)) p0 = 0.0f;
+                  if (key + 1 >= limit || (none >> (2 * c + g) & 1)) p1 = 0.0f;
+                }
+                sum = __fadd2_rn(sum, make_float2(p0, p1));
+                y[g * 8 + k] = pack_half2(p0, p1);
+              }
+              l = __fmaf_rn(sum.x + sum.y, sc.back[2 * c + g], l);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) st_shared_v4(piece(ptile, r, 4 * c + k), make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]));
+          }
+          tc_fence_before();
+          fence_async_shared();
+          mbar_arrive(&p_full[side]);
+        }
+        // the last product
+        if (ok && !warp_wait(&p_free[side], (done & 1u) ^ 1u, abort_flag)) ok = false;
+        if (!ok) break;
+        tc_fence_after();
+      }
+      // ---- the row's result: O over the sum
+      const bool starts = w.b0 == 0, whole = starts && w.b1 == w.nb;
+      const int slot = 2 * j + (starts ? 1 : 0);
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l, fx = pow2i(xref);
+      const float lse2 = l == 0.0f ? -INFINITY : m + (log2f(l) - kOffset);
+      // Where V held NaN or infinite values: each column's first key with one, into this warp's rows of P, which is read out.
+      const bool odd = nx && *(volatile int*)&misc.odd;
+      int* bad = reinterpret_cast<int*>(smem + kP + side * kTile + (warp & 3) * 4096);
+      if (odd) {
+        for (int k = lane; k < DH; k += 32) bad[k] = kAll;
+        __syncwarp();
+        const int last = min((w.b0 + nx) * kBlockKeys, w.t.limit(w.r0 + min(w.n_rows, (side + 1) * kTileRows) - 1));
+        for (int key = w.b0 * kBlockKeys + lane; key < last; key += 32) {
+          const int id = p.kv.pages[(int64_t)w.s * p.kv.max_pages + (key >> p.kv.page_shift)];
+          if (id < 0 || id >= p.kv.n_pages) continue;
+          const uint8_t* codes = p.kv.v + ((((int64_t)id * p.kv.hkv + w.h) << p.kv.page_shift) + (key & ((1 << p.kv.page_shift) - 1))) * DH;
+          for (int k = 0; k < DH; ++k)
+            if (nonfinite4<FMT>(codes[k]) & 0x80u) atomicMin(&bad[k], key);
+        }
+        __syncwarp();
+      }
+#pragma unroll 1
+      for (int c = 0; c < DH / 32; ++c) {
+        uint32_t o[32];
+        __syncwarp();
+        if (nx) tmem_ld32(tO + c * 32, o);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          float v = l == 0.0f ? 0.0f : __uint_as_float(nx ? o[k] : 0u) * inv * fx;
+          if (odd && bad[c * 32 + k] < limit) v = __uint_as_float(0x7FC00000u);
+          o[k] = __float_as_uint(v);
+        }
+        if (!real) {  // no row of the call
+        } else if (whole) {
+          uint4* to = reinterpret_cast<uint4*>(p.att + (row * p.n_heads + hd) * DH + c * 32);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            to[k] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * k]), __uint_as_float(o[8 * k + 1])),
+                               pack_bf16x2(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3])),
+                               pack_bf16x2(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5])),
+                               pack_bf16x2(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7])));
+        } else {
+          uint4* to = reinterpret_cast<uint4*>(p.part_o + ((int64_t)slot * kRows + i) * DH + c * 32);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) to[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+      }
+      if (real) {
+        if (whole) p.lse[(int64_t)hd * p.kv.T + row] = lse2 * kLn2;
+        else p.part_lse[slot * kRows + i] = lse2;
+      }
+      if (t == 32 * kFirstRowWarp && starts && !whole)
+        p.cuts[j] = Cut{w.unit0, w.unit0 + w.cost, total, ctas, w.h, w.q.first, w.n_rows, w.r0};
+      tc_fence_before();
+      tile += n;
+      ++seg;
+    }
+    if (!ok) {
+      atomicOr(p.kv.status, kStatusTimeout);
+      *abort_flag = 1;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Block (j, y): rows 8 y .. of the unit that CTA j began and did not end, a row a warp; its parts in order.
+constexpr int kJoinRows = 8;
+template <int DH>
+__global__ void __launch_bounds__(32 * kJoinRows) k_kv_join_many(const AttendArgs p) {
+  wait_for_previous();
+  const int j = blockIdx.x, r = blockIdx.y * kJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const Cut cut = p.cuts[j];
+  if (cut.first == cut.end || r >= cut.rows) return;
+  const int n = (int)((cut.end * cut.ctas + cut.total - 1) / cut.total) - j;
+  auto slot = [&](int i) { return i == 0 ? 2 * j + 1 : 2 * (j + i); };
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_lse[slot(i) * kRows + r]);
+#pragma unroll
+  for (int k = 16; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, k));
+  float acc[DH / 32], sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < DH / 32; ++k) acc[k] = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float e = p.part_lse[slot(i) * kRows + r];
+    const float wgt = e == -INFINITY ? 0.0f : ex2(e - M);
+    const float* src = p.part_o + ((int64_t)slot(i) * kRows + r) * DH + lane;
+    sum += wgt;
+#pragma unroll
+    for (int k = 0; k < DH / 32; ++k) acc[k] += wgt * src[32 * k];
+  }
+  const int G = p.n_heads / p.kv.hkv, tok = (cut.group_row + r) / G, hd = cut.head * G + (cut.group_row + r) - tok * G;
+  __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(p.att) + ((int64_t)(cut.row0 + tok) * p.n_heads + hd) * DH + lane;
+#pragma unroll
+  for (int k = 0; k < DH / 32; ++k) to[32 * k] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : acc[k] / sum);
+  if (lane == 0) p.lse[(int64_t)hd * p.kv.T + cut.row0 + tok] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kLn2;
+}
+
+template <int FMT, int DH>
+cudaError_t launch(const AttendArgs& p, int ctas, cudaStream_t s) {
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = kv_smem(k_kv_attend_many<FMT, DH>, kSmem, configured);
+  if (e != cudaSuccess) return e;
+  k_kv_attend_many<FMT, DH><<<ctas, kThreads, kSmem, s>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_dependent(k_kv_join_many<DH>, dim3((unsigned)ctas, kRows / kJoinRows), 32 * kJoinRows, 0, s, p);
+}
+
+}  // namespace
+
+int kv_attend_many_rows() { return kRows; }
+
+cudaError_t launch_kv_attend_many(const AttendArgs& p, int ctas, cudaStream_t s) {
+  if (p.kv.fmt)
+    return p.kv.dh == 128 ? launch<1, 128>(p, ctas, s) : p.kv.dh == 96 ? launch<1, 96>(p, ctas, s) : launch<1, 64>(p, ctas, s);
+  return p.kv.dh == 128 ? launch<0, 128>(p, ctas, s) : p.kv.dh == 96 ? launch<0, 96>(p, ctas, s) : launch<0, 64>(p, ctas, s);
+}
+
+}  // namespace fp8q

@@ -253,6 +253,62 @@ def test_attention_matches_its_definition(case, fmt):
     assert fq.get_status() == 0
 
 
+MANY = [  # more than 64 (token, query head) pairs of a K/V head: the kernel on tensor memory
+    (128, 64, 5, 1, [700, 512, 130], 130, None),
+    (96, 16, 10, 2, [300, 0, 45], 40, None),
+    (64, 128, 6, 6, [1000, 90], None, [90, 90]),
+    (128, 16, 8, 1, [257, 1024, 33], None, [257, 64, 1]),
+    (96, 128, 3, 1, [2000], None, [100]),
+    (128, 32, 70, 1, [5, 300], 1, None),             # 70 heads of one token
+    (64, 64, 2, 2, [400] * 5, None, [399, 1, 0, 257, 128]),
+    (128, 128, 4, 4, [129] * 40, 128, None),         # more units than SMs
+    (128, 64, 1, 1, [9000], 300, None),              # a unit cut over many CTAs
+]
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_attention_of_many_rows_matches_its_definition(case, fmt):
+    dh, P, hq, hkv, lens, rows, ragged = MANY[case]
+    fq.get_status(clear=True)
+    w = World(fmt, dh, P, hq, hkv, lens, rows=rows, ragged=ragged, seed=100 + case, behind=0 if ragged is None else 2)
+    w.fill()
+    t, x = w.append()
+    first = w.attend(t, x)
+    again = fq.attention_cached(w.cache, t, *w.args(), hq, row_start=w.start())
+    torch.cuda.synchronize()
+    n = w.T if w.row_start is None else w.row_start[-1]
+    assert torch.equal(first[0][:n], again[0][:n]) and torch.equal(first[1][:, :n], again[1][:, :n])
+    assert fq.get_status() == 0
+
+
+def test_many_rows_see_values_that_are_not_finite_only_behind_them():
+    w = World(0, 64, 32, 2, 2, [300, 300], rows=200, seed=30)
+    w.fill()
+    t, _ = w.qkv()
+    t[120, 2 * 64 + 5] = float("inf")   # K head 0 of the first sequence's token 220
+    t[150, 5 * 64 + 7] = float("nan")   # V head 1, column 7, of its token 250
+    fq.kv_cache_append(w.cache, t, *w.args(), 2)
+    x = t.double().cpu().numpy().reshape(400, 6, 64)
+    ref.append(w.ref, 0, 32, w.pages, w.lens, w.rows, x[:, 2:].reshape(-1, 2, 2, 64))
+    w.check_cache()
+    att, lse = fq.attention_cached(w.cache, t, *w.args(), 2)
+    torch.cuda.synchronize()
+    a = att.float().view(400, 2, 64)
+    assert torch.isnan(a[120:200, 0]).all() and torch.isfinite(a[:120, 0]).all() and torch.isfinite(a[200:]).all()
+    assert torch.isnan(a[150:200, 1, 7]).all()
+    a[150:200, 1, 7] = 0
+    assert torch.isfinite(a[:, 1]).all()
+    # what is finite is what it was: rows before, and the other columns
+    fine = {k: np.nan_to_num(v) if k in "kv" else v for k, v in w.ref.items()}
+    want, size, _, _ = ref.attend(fine, 32, w.pages, w.lens, w.rows, x[:, :2])
+    got = att.double().cpu().numpy().reshape(400, 2, 64)
+    rows = [r for r in range(400) if not 120 <= r < 200]
+    assert np.abs(got[rows, 0] - want[rows, 0]).max() < 0.02 * size.max()
+    others = [c for c in range(64) if c != 7]
+    assert np.abs(got[:, 1][:, others] - want[:, 1][:, others]).max() < 0.02 * size.max()
+
+
 def test_rows_behind_the_last_sequence_are_left_as_they_were():
     w = World(0, 128, 32, 6, 2, [50, 9], ragged=[3, 2], behind=4, seed=2)
     w.fill()
