@@ -4,11 +4,11 @@
 // The products are tcgen05 kind::f16 ones, fp16 operands and fp32 accumulators in tensor memory: FP8 codes are fp16 numbers, and q is
 // one over a power of two of its row, so the scores lose nothing.  (FP8 operands would need q and P in several 4-bit parts.)
 // A CTA has 256 rows of one K/V head, two tiles of 128 (token, query head) pairs, A and B, which share what is
-// made of each block of 128 keys; its 384 threads (with a thirteenth warp each thread would have 128 registers, not 168):
-//   warps 0-2    codes of K and V from the cache's pages, a block ahead in registers, into swizzled fp16 tiles (K two, V one), and
-//                the block's scales;
-//   warp 3       the products, one thread: S_A = Q_A K^T, O_A += P_A V of the block before, then B's;
-//   warps 4-11   a row a thread (A, then B): q into shared memory; per block the row's maximum from S, P = 2^(s - m) as fp16
+// made of each block of 128 keys; its 16 warps (two of them idle: rows' warps stand at their quarter of tensor memory):
+//   warp 5       pages, bulk copies of a block's codes of K and V into shared memory, and its scales, a block ahead;
+//   warps 0-3    the codes into swizzled fp16 tiles, one for K and one for V;
+//   warp 4       the products, one thread: S_A = Q_A K^T, O_A += P_A V of the block before, then B's;
+//   warps 8-15   a row a thread (A, then B): q into shared memory; per block the row's maximum from S, P = 2^(s - m) as fp16
 //                into shared memory, and at the end O over the sum.
 // P's window is that of the few rows' kernel: p 2^11 in fp16, the reference maximum moving when it is exceeded by 2^4.
 // The keys of all (sequence, row tile, K/V head) units are cut into equal parts, one a CTA, as there.
@@ -21,15 +21,16 @@ namespace fp8q {
 
 namespace {
 
-constexpr int kLoaders = 96, kMmaWarp = 3, kFirstRowWarp = 4, kThreads = 384;
+constexpr int kLoaders = 128, kMmaWarp = 4, kCopyWarp = 5, kFirstRowWarp = 8, kThreads = 512;
 constexpr int kTileRows = 128, kRows = 2 * kTileRows;
 constexpr int kAtom = 16384;       // 128 rows x 128 bytes: 64 fp16 columns of a swizzled tile
 constexpr int kTile = 2 * kAtom;   // a tile of 128 columns
 constexpr int kQ = 0;              // [2 tiles]
-constexpr int kK = kQ + 2 * kTile; // [2 stages]
-constexpr int kV = kK + 2 * kTile;
-constexpr int kP = kV + kTile;     // [2 tiles]
-constexpr int kBars = kP + 2 * kTile;
+constexpr int kK = kQ + 2 * kTile;
+constexpr int kV = kK + kTile;
+constexpr int kP = kV + kTile;         // [2 tiles]
+constexpr int kCodes = kP + 2 * kTile; // the next block's codes: K, V
+constexpr int kBars = kCodes + kTile;
 constexpr int kMisc = kBars + 256;
 constexpr float kOffset = 11.0f, kSlack = 4.0f;
 constexpr int kAll = 0x7FFFFFFF;
@@ -41,9 +42,16 @@ struct BlockScales {
   float k[8], dx[8], back[8];
   int none[4];  // [0]: bit g: keys 16 g .. have no page
 };
+// What is to be seen of a block's codes.
+struct BlockKeys {
+  int rows;   // keys that some row sees: 128 but in the last block
+  int have;   // bit g: keys 16 g .. have a page
+  int check;  // some row does not see all of them: V is looked at for what is not finite
+};
 struct Misc {
-  BlockScales scales[2];  // by K's stage
-  int xref[2];            // by segment: the largest exponent of V
+  BlockScales scales[2];  // by block
+  BlockKeys keys[2];
+  int xref[4];            // by segment: the largest exponent of V
   int odd;                // some V was NaN or infinite, and is 0 in its tile
   uint32_t tmem;
   int abort;
@@ -74,7 +82,12 @@ __device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint32_t b, b
   }
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort)) != 0;
+  return __all_sync(0xFFFFFFFFu, mbar_wait_held(bar, parity, abort)) != 0;
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
 }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -179,8 +192,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBars);
   uint64_t* q_full = bars + 0;    // [2] per tile, once a segment
-  uint64_t* k_full = bars + 2;    // [2] per stage
-  uint64_t* k_empty = bars + 4;   // [2] both S of the block are computed
+  uint64_t* k_full = bars + 2;
+  uint64_t* k_empty = bars + 3;   // both S of the block are computed
+  uint64_t* sc_full = bars + 4;   // [2] a block's scales (every other block's: a row may still read the one before)
   uint64_t* v_full = bars + 6;
   uint64_t* v_empty = bars + 7;   // both P V of the block are computed
   uint64_t* s_full = bars + 8;    // [2] per tile
@@ -188,6 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
   uint64_t* p_full = bars + 12;   // [2]
   uint64_t* p_free = bars + 14;   // [2] P V has read P, and O holds every product so far
   uint64_t* drain = bars + 16;
+  uint64_t* code_full = bars + 17;   // K's, V's codes of the next block
+  uint64_t* code_free = bars + 19;   // [2] they have been read
   Misc& misc = *reinterpret_cast<Misc*>(smem + kMisc);
   volatile int* abort_flag = &misc.abort;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -236,16 +252,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
   if (t == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], kTileRows);
-      mbar_init(&k_full[i], kLoaders);
-      mbar_init(&k_empty[i], 1);
+      mbar_init(&sc_full[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&s_free[i], kTileRows);
       mbar_init(&p_full[i], kTileRows);
       mbar_init(&p_free[i], 1);
     }
+    mbar_init(k_full, kLoaders);
+    mbar_init(k_empty, 1);
     mbar_init(v_full, kLoaders);
     mbar_init(v_empty, 1);
     mbar_init(drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&code_full[i], 1);
+      mbar_init(&code_free[i], kLoaders);
+    }
     misc.abort = misc.odd = 0;
     fence_mbar_init();
   }
@@ -267,14 +288,93 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
 
   if (warp < kLoaders / 32) {
     // ---------------- codes to fp16 ----------------
-    constexpr int kPieces = DH / 16;  // of 16 codes, of a key
-    constexpr int kMine = (kBlockKeys * kPieces + kLoaders - 1) / kLoaders;  // of a thread, of a block
+    constexpr int kPieces = DH / 16;  // of 16 codes, of a key: and of a thread, of a block
+    // Piece i of this thread: codes 16 ch .. of key row `row`.  Rows of 128: eight neighbouring threads take the first half of a row
+    // and the second of the next, so that what they read, and the two 16-byte pieces that each writes, touch every bank once; i moves
+    // the row by 16, so neither offset depends on it.
+    auto place = [&](int i, int& row, int& ch) {
+      const int idx = i * kLoaders + t;
+      if (DH == 128) {
+        row = i * 16 + (((t >> 4) << 1) | ((t >> 2) & 1));
+        ch = (t & 3) | (((t >> 2) ^ (t >> 3)) & 1) << 2;
+      } else {
+        row = idx / kPieces;
+        ch = idx - row * kPieces;
+      }
+    };
+    // Four pieces are read before the first is written: a write holds the reads behind it back.
+    auto convert = [&](uint32_t dst, uint32_t from, bool values, const BlockKeys& keys) {
+      constexpr int kBatch = DH == 96 ? 3 : 4;
+      const int rows = keys.rows, have = keys.have, check = keys.check && values;
+      const bool whole = rows == kBlockKeys && have == 0xFF;
+#pragma unroll 1
+      for (int i0 = 0; i0 < kPieces; i0 += kBatch) {
+        uint4 x[kBatch];
+        int row[kBatch], ch[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          place(i0 + k, row[k], ch[k]);
+          x[k] = ld_shared_v4(from + (uint32_t)(row[k] * DH + ch[k] * 16));
+        }
+        if (!whole) {
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k)
+            if (row[k] >= rows || !(have >> (row[k] >> 4) & 1)) x[k] = make_uint4(0, 0, 0, 0);
+        }
+        if (check) {
+          uint32_t odd = 0;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) odd |= nonfinite4<FMT>(x[k].x) | nonfinite4<FMT>(x[k].y) | nonfinite4<FMT>(x[k].z) | nonfinite4<FMT>(x[k].w);
+          if (odd) {  // a weight of 0 times it would be NaN in rows that do not see it: 0 here, and the rows look for themselves
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              x[k].x &= ~((nonfinite4<FMT>(x[k].x) >> 7) * 0xFFu);
+              x[k].y &= ~((nonfinite4<FMT>(x[k].y) >> 7) * 0xFFu);
+              x[k].z &= ~((nonfinite4<FMT>(x[k].z) >> 7) * 0xFFu);
+              x[k].w &= ~((nonfinite4<FMT>(x[k].w) >> 7) * 0xFFu);
+            }
+            misc.odd = 1;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const uint4 v = x[k];
+          st_shared_v4(piece(dst, row[k], 2 * ch[k]),
+                       make_uint4(f16x2_of<FMT>(v.x), f16x2_of<FMT>(v.x >> 16), f16x2_of<FMT>(v.y), f16x2_of<FMT>(v.y >> 16)));
+          st_shared_v4(piece(dst, row[k], 2 * ch[k] + 1),
+                       make_uint4(f16x2_of<FMT>(v.z), f16x2_of<FMT>(v.z >> 16), f16x2_of<FMT>(v.w), f16x2_of<FMT>(v.w >> 16)));
+        }
+      }
+    };
     while (ok && w.next()) {
-      const int n_blocks = max(w.blocks_of(0), w.blocks_of(1));
-      if (n_blocks == 0) { ++seg; continue; }
-      const int klim = w.t.limit(w.r0 + w.n_rows - 1), stop = w.b0 + n_blocks;
+      const int n = max(w.blocks_of(0), w.blocks_of(1));
+      for (int b = 0; b < n; ++b, ++tile) {
+        const uint32_t par = (uint32_t)tile & 1u;
+        if (!warp_wait(k_empty, par ^ 1u, abort_flag) || !warp_wait(&code_full[0], par, abort_flag)) { ok = false; break; }
+        convert(sbase + kK, sbase + kCodes, false, misc.keys[par]);
+        mbar_arrive(&code_free[0]);
+        fence_async_shared();
+        mbar_arrive(k_full);
+        if (!warp_wait(v_empty, par ^ 1u, abort_flag) || !warp_wait(&code_full[1], par, abort_flag)) { ok = false; break; }
+        convert(sbase + kV, sbase + kCodes + kAtom, true, misc.keys[par]);
+        mbar_arrive(&code_free[1]);
+        fence_async_shared();
+        mbar_arrive(v_full);
+      }
+    }
+    if (!ok) {
+      atomicOr(p.kv.status, kStatusTimeout);
+      *abort_flag = 1;
+    }
+  } else if (warp == kCopyWarp) {
+    // ---------------- pages, copies, scales ----------------
+    uint32_t fetched[2] = {0, 0};  // blocks whose codes were asked for
+    while (ok && w.next()) {
+      const int n = max(w.blocks_of(0), w.blocks_of(1));
+      if (n == 0) { ++seg; continue; }
+      const int first = w.t.limit(w.r0), klim = w.t.limit(w.r0 + w.n_rows - 1), stop = w.b0 + n;
       const int32_t* table = p.kv.pages + (int64_t)w.s * p.kv.max_pages;
-      const int mask = (1 << p.kv.page_shift) - 1;
+      const int mask = (1 << p.kv.page_shift) - 1, step = min(1 << p.kv.page_shift, kBlockKeys) >> 4;  // groups of 16 keys of a copy
       // lanes 0 .. 7: the page of keys 16 lane .. of block b; -1: none
       auto page_of = [&](int b) {
         const int key = b * kBlockKeys + 16 * lane;
@@ -284,20 +384,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
         atomicOr(p.kv.status, kStatusBadCache);
         return -1;
       };
-      uint4 kw[kMine], vw[kMine];
-      auto load = [&](const uint8_t* codes, int b, int ids, uint4 (&x)[kMine]) {
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const int idx = i * kLoaders + t, row = idx / kPieces, col = (idx - row * kPieces) * 16, key = b * kBlockKeys + row;
-          const int id = __shfl_sync(0xFFFFFFFFu, ids, (row >> 4) & 7);
-          const int64_t at = ((((int64_t)id * p.kv.hkv + w.h) << p.kv.page_shift) + (key & mask)) * DH + col;
-          x[i] = id >= 0 && row < kBlockKeys && key < klim ? ld_nc_v4(codes + at) : make_uint4(0, 0, 0, 0);
+      // Lanes 0 .. 7 copy block b's codes of K (0) or V (1), a page (or 128 keys) each.  Slots behind the last key come along.
+      auto fetch = [&](int which, int b, int id, unsigned have) {
+        ++fetched[which];
+        const bool mine = lane < 8 && lane % step == 0 && id >= 0;
+        const uint32_t bytes = (uint32_t)(step * 16 * DH);
+        const unsigned copies = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+        if (lane == 0) {
+          if (copies) mbar_arrive_expect_tx(&code_full[which], copies * bytes);
+          else mbar_arrive(&code_full[which]);
         }
+        __syncwarp();
+        if (mine) {
+          const int64_t at = ((((int64_t)id * p.kv.hkv + w.h) << p.kv.page_shift) + ((b * kBlockKeys + 16 * lane) & mask)) * DH;
+          bulk_load(smem + kCodes + which * kAtom + lane * 16 * DH, (which ? p.kv.v : p.kv.k) + at, bytes, &code_full[which]);
+        }
+        __syncwarp();
       };
       int ids = page_of(w.b0), ids_next = page_of(w.b0 + 1);
-      load(p.kv.k, w.b0, ids, kw);
-      load(p.kv.v, w.b0, ids, vw);
-      // the segment's largest exponent of V (every warp by itself: no wait among them)
+      // the segment's largest exponent of V
       int xref = -1000;
       for (int pg = (w.b0 * kBlockKeys >> p.kv.page_shift) + lane; (int64_t)pg << p.kv.page_shift < min((int64_t)klim, (int64_t)stop * kBlockKeys);
            pg += 32) {
@@ -305,64 +410,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
         if (id >= 0 && id < p.kv.n_pages) xref = max(xref, (int)p.kv.v_scale[(int64_t)id * p.kv.hkv + w.h] - 127);
       }
       xref = __reduce_max_sync(0xFFFFFFFFu, xref);
-      if (t == 0) misc.xref[seg & 1] = xref;
-      auto convert = [&](uint32_t dst, const uint4& x, int row, int ch) {
-        const uint4 lo = make_uint4(f16x2_of<FMT>(x.x), f16x2_of<FMT>(x.x >> 16), f16x2_of<FMT>(x.y), f16x2_of<FMT>(x.y >> 16));
-        const uint4 hi = make_uint4(f16x2_of<FMT>(x.z), f16x2_of<FMT>(x.z >> 16), f16x2_of<FMT>(x.w), f16x2_of<FMT>(x.w >> 16));
-        // the pieces of the second 64 columns in the other order: eight lanes then write to all banks
-        const bool swap = DH == 128 && ch >= 4;
-        st_shared_v4(piece(dst, row, 2 * ch + swap), swap ? hi : lo);
-        st_shared_v4(piece(dst, row, 2 * ch + !swap), swap ? lo : hi);
-      };
-      for (int b = w.b0; b < stop && ok; ++b, ++tile) {
-        const int st = tile & 1;
-        const uint32_t u = (uint32_t)(tile >> 1) & 1u;
-        // scales of this block, lanes 0 .. 7 of warp 0 K's, of warp 1 V's
-        int x = kNoPage;
-        if (warp < 2 && ids >= 0) x = (int)(warp ? p.kv.v_scale : p.kv.k_scale)[(int64_t)ids * p.kv.hkv + w.h] - 127;
-        if (!warp_wait(&k_empty[st], u ^ 1u, abort_flag)) { ok = false; break; }
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const int idx = i * kLoaders + t, row = idx / kPieces;
-          if (row < kBlockKeys) convert(sbase + kK + st * kTile, kw[i], row, idx - row * kPieces);
-        }
-        BlockScales& sc = misc.scales[st];
-        if (warp == 0) {
-          const unsigned none = __ballot_sync(0xFFFFFFFFu, x == kNoPage) & 0xFFu;
-          if (lane < 8) sc.k[lane] = pow2i(x == kNoPage ? 0 : x);
-          if (lane == 0) sc.none[0] = (int)none;
-        } else if (warp == 1 && lane < 8) {
-          const int dx = max(x == kNoPage ? -60 : x - xref, -60);
+      if (lane == 0) misc.xref[seg & 3] = xref;
+      for (int b = w.b0; b < stop; ++b, ++tile) {
+        const uint32_t par = (uint32_t)tile & 1u;
+        const int none = kNoPage;
+        const int xk = ids >= 0 ? (int)p.kv.k_scale[(int64_t)ids * p.kv.hkv + w.h] - 127 : none;
+        const int xv = ids >= 0 ? (int)p.kv.v_scale[(int64_t)ids * p.kv.hkv + w.h] - 127 : none;
+        const unsigned have = __ballot_sync(0xFFFFFFFFu, ids >= 0) & 0xFFu;
+        const int here = ids;
+        ids = ids_next;
+        ids_next = page_of(b + 2);
+        // K's codes of the block before have been read
+        if (!warp_wait(&code_free[0], par ^ 1u, abort_flag)) { ok = false; break; }
+        if (lane == 0) misc.keys[par] = BlockKeys{min(kBlockKeys, klim - b * kBlockKeys), (int)have, (b + 1) * kBlockKeys > first};
+        __syncwarp();
+        fetch(0, b, here, have);
+        // V's too, which were written when P V of the one before that was done: its scales have been read
+        if (!warp_wait(&code_free[1], par ^ 1u, abort_flag)) { ok = false; break; }
+        fetch(1, b, here, have);
+        BlockScales& sc = misc.scales[par];
+        if (lane < 8) {
+          const int dx = max(xv == none ? -60 : xv - xref, -60);
+          sc.k[lane] = pow2i(xk == none ? 0 : xk);
           sc.dx[lane] = kOffset + (float)dx;
           sc.back[lane] = pow2i(-dx);
         }
-        fence_async_shared();
-        mbar_arrive(&k_full[st]);
-        ids = ids_next;
-        ids_next = page_of(b + 2);
-        load(p.kv.k, b + 1, ids, kw);
-        if (!warp_wait(v_empty, ((uint32_t)tile & 1u) ^ 1u, abort_flag)) { ok = false; break; }
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const int idx = i * kLoaders + t, row = idx / kPieces, ch = idx - row * kPieces;
-          uint32_t v[4] = {vw[i].x, vw[i].y, vw[i].z, vw[i].w};
-          if (nonfinite4<FMT>(v[0]) | nonfinite4<FMT>(v[1]) | nonfinite4<FMT>(v[2]) | nonfinite4<FMT>(v[3])) {
-            // a weight of 0 times it would be NaN in rows that do not see it: 0 here, and the rows look for themselves
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] &= ~((nonfinite4<FMT>(v[k]) >> 7) * 0xFFu);
-            misc.odd = 1;
-          }
-          if (row < kBlockKeys) convert(sbase + kV, make_uint4(v[0], v[1], v[2], v[3]), row, ch);
-        }
-        fence_async_shared();
-        mbar_arrive(v_full);
-        load(p.kv.v, b + 1, ids, vw);
+        if (lane == 0) sc.none[0] = (int)(~have & 0xFFu);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_full[par]);
       }
       ++seg;
     }
     if (!ok) {
       atomicOr(p.kv.status, kStatusTimeout);
       *abort_flag = 1;
+      int never = 0;  // the copies in flight, before the memory is given back
+      for (int i = 0; i < 2; ++i)
+        if (fetched[i]) warp_wait(&code_full[i], (fetched[i] - 1) & 1u, &never);
     }
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
@@ -374,23 +458,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
         if (n == 0) continue;
         for (int side = 0; side < 2 && ok; ++side)
           if (nx[side]) {
-            ok = mbar_wait(&q_full[side], nq[side] & 1u, abort_flag);
+            ok = mbar_wait_held(&q_full[side], nq[side] & 1u, abort_flag);
             ++nq[side];
           }
         for (int b = 0; b <= n && ok; ++b) {
-          const int st = (tile + b) & 1;
-          if (b < n && !mbar_wait(&k_full[st], (uint32_t)((tile + b) >> 1) & 1u, abort_flag)) { ok = false; break; }
-          if (b > 0 && !mbar_wait(v_full, (uint32_t)(tile + b - 1) & 1u, abort_flag)) { ok = false; break; }
+          if (b < n && !mbar_wait_held(k_full, (uint32_t)(tile + b) & 1u, abort_flag)) { ok = false; break; }
+          if (b > 0 && !mbar_wait_held(v_full, (uint32_t)(tile + b - 1) & 1u, abort_flag)) { ok = false; break; }
           for (int side = 0; side < 2; ++side) {
             if (b < nx[side]) {
-              if (!mbar_wait(&s_free[side], ((ns[side] + (uint32_t)b) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+              if (!mbar_wait_held(&s_free[side], ((ns[side] + (uint32_t)b) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
               tc_fence_after();
-              mma_scores<DH>(tmem + side * 128, sbase + kQ + side * kTile, sbase + kK + st * kTile);
+              mma_scores<DH>(tmem + side * 128, sbase + kQ + side * kTile, sbase + kK);
               umma_commit(&s_full[side]);
             }
-            if (side == 1 && b < n) umma_commit(&k_empty[st]);
+            if (side == 1 && b < n) umma_commit(k_empty);
             if (b > 0 && b - 1 < nx[side]) {
-              if (!mbar_wait(&p_full[side], (ns[side] + (uint32_t)(b - 1)) & 1u, abort_flag)) { ok = false; break; }
+              if (!mbar_wait_held(&p_full[side], (ns[side] + (uint32_t)(b - 1)) & 1u, abort_flag)) { ok = false; break; }
               tc_fence_after();
               mma_values<N>(tmem + 256 + side * 128, sbase + kP + side * kTile, sbase + kV, b > 1);
               umma_commit(&p_free[side]);
@@ -410,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
       int dummy = 0;
       mbar_wait(drain, 0, &dummy);
     }
-  } else {
+  } else if (warp >= kFirstRowWarp) {
     // ---------------- a row a thread ----------------
     const int side = (warp - kFirstRowWarp) >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -452,37 +535,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
         mbar_arrive(&q_full[side]);
 
         for (int b = 0; b < nx && ok; ++b, ++done) {
-          const int kt = tile + b, st = kt & 1;
+          const int kpar = (tile + b) & 1;
           if (!warp_wait(&s_full[side], done & 1u, abort_flag)) { ok = false; break; }
-          // the block's scales, from their writers (long arrived: S is made of that block)
-          if (!warp_wait(&k_full[st], (uint32_t)(kt >> 1) & 1u, abort_flag)) { ok = false; break; }
+          if (!warp_wait(&sc_full[kpar], (uint32_t)((tile + b) >> 1) & 1u, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const BlockScales& sc = misc.scales[st];
-          xref = misc.xref[seg & 1];
+          const BlockScales& sc = misc.scales[kpar];
+          xref = misc.xref[seg & 3];
           const int key0 = (w.b0 + b) * kBlockKeys, none = sc.none[0];
           const bool edge = key0 + kBlockKeys > kmin || none;
-          float f[8];
-#pragma unroll
-          for (int g = 0; g < 8; ++g) f[g] = fminf(fmaxf(rowf * sc.k[g], 0x1p-100f), 0x1p126f);
+          auto factor = [&](int g) { return fminf(fmaxf(rowf * sc.k[g], 0x1p-100f), 0x1p126f); };
+          auto hidden = [&](int col) { return key0 + col >= limit || (none >> (col >> 4) & 1); };
           float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t z[32];
             tmem_ld32(tS + c * 32, z);
+            if (edge) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (hidden(c * 32 + k)) z[k] = 0xFF800000u;
+            }
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-              float y[2] = {-INFINITY, -INFINITY};
-              if (edge) {
+              float y[4];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                  const bool out = key0 + c * 32 + g * 16 + k >= limit || (none >> (2 * c + g) & 1);
-                  y[k & 1] = fmaxf(y[k & 1], out ? -INFINITY : __uint_as_float(z[g * 16 + k]));
-                }
-              } else {
+              for (int k = 0; k < 4; ++k) y[k] = __uint_as_float(z[g * 16 + k]);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) y[k & 1] = fmaxf(y[k & 1], __uint_as_float(z[g * 16 + k]));
-              }
-              mx = fmaxf(mx, fmaxf(y[0], y[1]) * f[2 * c + g]);
+              for (int k = 4; k < 16; ++k) y[k & 3] = fmaxf(y[k & 3], __uint_as_float(z[g * 16 + k]));
+              mx = fmaxf(mx, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * factor(2 * c + g));
             }
           }
           // P V of the block before has read P, and O holds every product up to it
@@ -504,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
             m = mn;
           }
           const float ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t z[32], y[16];
             tmem_ld32(tS + c * 32, z);
@@ -512,26 +592,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
               tc_fence_before();
               mbar_arrive(&s_free[side]);
             }
+            if (edge) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (hidden(c * 32 + k)) z[k] = 0xFF800000u;
+            }
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-              const float2 fg = make_float2(f[2 * c + g], f[2 * c + g]);
-              const float cg = sc.dx[2 * c + g] - ref;
-              const float2 c2 = make_float2(cg, cg);
-              float2 sum = make_float2(0.0f, 0.0f);
+              const float fg = factor(2 * c + g), cg = sc.dx[2 * c + g] - ref;
+              const float2 f2 = make_float2(fg, fg), c2 = make_float2(cg, cg);
+              float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 const int col = g * 16 + 2 * k;
-                const float2 e = __ffma2_rn(make_float2(__uint_as_float(z[col]), __uint_as_float(z[col + 1])), fg, c2);
-                float p0 = ex2(e.x), p1 = ex2(e.y);
-                if (edge) {
-                  const int key = key0 + c * 32 + col;
-                  if (key >= limit || (none >> (2 * c + g) & 1)) p0 = 0.0f;
-                  if (key + 1 >= limit || (none >> (2 * c + g) & 1)) p1 = 0.0f;
-                }
-                sum = __fadd2_rn(sum, make_float2(p0, p1));
-                y[g * 8 + k] = pack_half2(p0, p1);
+                const float2 e = __ffma2_rn(make_float2(__uint_as_float(z[col]), __uint_as_float(z[col + 1])), f2, c2);
+                const float2 pr = make_float2(ex2(e.x), ex2(e.y));
+                sum[k & 1] = __fadd2_rn(sum[k & 1], pr);
+                y[g * 8 + k] = pack_half2(pr.x, pr.y);
               }
-              l = __fmaf_rn(sum.x + sum.y, sc.back[2 * c + g], l);
+              sum[0] = __fadd2_rn(sum[0], sum[1]);
+              l = __fmaf_rn(sum[0].x + sum[0].y, sc.back[2 * c + g], l);
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) st_shared_v4(piece(ptile, r, 4 * c + k), make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]));
