@@ -6,7 +6,7 @@
 // A CTA has 256 rows of one K/V head, two tiles of 128 (token, query head) pairs, A and B, which share what is
 // made of each block of 128 keys; its 16 warps (two of them idle: rows' warps stand at their quarter of tensor memory):
 //   warp 5       pages, bulk copies of a block's codes of K and V into shared memory, and its scales, a block ahead;
-//   warps 0-3    the codes into swizzled fp16 tiles, one for K and one for V;
+//   warps 0-3    the codes into swizzled fp16 tiles, two for K's and two for V's (whose tiles are free at different times);
 //   warp 4       the products, one thread: S_A = Q_A K^T, O_A += P_A V of the block before, then B's;
 //   warps 8-15   a row a thread (A, then B): q into shared memory; per block the row's maximum from S, P = 2^(s - m) as fp16
 //                into shared memory, and at the end O over the sum.
@@ -21,7 +21,7 @@ namespace fp8q {
 
 namespace {
 
-constexpr int kLoaders = 128, kMmaWarp = 4, kCopyWarp = 5, kFirstRowWarp = 8, kThreads = 512;
+constexpr int kLoaders = 64 /* of K, of V */, kMmaWarp = 4, kCopyWarp = 5, kFirstRowWarp = 8, kThreads = 512;
 constexpr int kTileRows = 128, kRows = 2 * kTileRows;
 constexpr int kAtom = 16384;       // 128 rows x 128 bytes: 64 fp16 columns of a swizzled tile
 constexpr int kTile = 2 * kAtom;   // a tile of 128 columns
@@ -50,7 +50,7 @@ struct BlockKeys {
 };
 struct Misc {
   BlockScales scales[2];  // by block
-  BlockKeys keys[2];
+  BlockKeys keys[4];      // by block
   int xref[4];            // by segment: the largest exponent of V
   int odd;                // some V was NaN or infinite, and is 0 in its tile
   uint32_t tmem;
@@ -82,7 +82,7 @@ __device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint32_t b, b
   }
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait_held(bar, parity, abort)) != 0;
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort)) != 0;
 }
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
@@ -286,17 +286,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
   int tile = 0, seg = 0;  // blocks and segments so far
   bool ok = true;
 
-  if (warp < kLoaders / 32) {
+  if (warp < 2 * kLoaders / 32) {
     // ---------------- codes to fp16 ----------------
-    constexpr int kPieces = DH / 16;  // of 16 codes, of a key: and of a thread, of a block
+    constexpr int kPieces = DH / 16;                            // of 16 codes, of a key
+    constexpr int kMine = kBlockKeys * kPieces / kLoaders;      // of a thread, of a block
+    const int is_v = warp >> 1, lt = t & (kLoaders - 1);
     // Piece i of this thread: codes 16 ch .. of key row `row`.  Rows of 128: eight neighbouring threads take the first half of a row
     // and the second of the next, so that what they read, and the two 16-byte pieces that each writes, touch every bank once; i moves
-    // the row by 16, so neither offset depends on it.
+    // the row by 8, so neither offset depends on it.
     auto place = [&](int i, int& row, int& ch) {
-      const int idx = i * kLoaders + t;
+      const int idx = i * kLoaders + lt;
       if (DH == 128) {
-        row = i * 16 + (((t >> 4) << 1) | ((t >> 2) & 1));
-        ch = (t & 3) | (((t >> 2) ^ (t >> 3)) & 1) << 2;
+        row = i * 8 + (((lt >> 4) << 1) | ((lt >> 2) & 1));
+        ch = (lt & 3) | (((lt >> 2) ^ (lt >> 3)) & 1) << 2;
       } else {
         row = idx / kPieces;
         ch = idx - row * kPieces;
@@ -304,11 +306,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
     };
     // Four pieces are read before the first is written: a write holds the reads behind it back.
     auto convert = [&](uint32_t dst, uint32_t from, bool values, const BlockKeys& keys) {
-      constexpr int kBatch = DH == 96 ? 3 : 4;
+      constexpr int kBatch = 4;
       const int rows = keys.rows, have = keys.have, check = keys.check && values;
       const bool whole = rows == kBlockKeys && have == 0xFF;
 #pragma unroll 1
-      for (int i0 = 0; i0 < kPieces; i0 += kBatch) {
+      for (int i0 = 0; i0 < kMine; i0 += kBatch) {
         uint4 x[kBatch];
         int row[kBatch], ch[kBatch];
 #pragma unroll
@@ -346,20 +348,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
         }
       }
     };
+    uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
     while (ok && w.next()) {
       const int n = max(w.blocks_of(0), w.blocks_of(1));
       for (int b = 0; b < n; ++b, ++tile) {
         const uint32_t par = (uint32_t)tile & 1u;
-        if (!warp_wait(k_empty, par ^ 1u, abort_flag) || !warp_wait(&code_full[0], par, abort_flag)) { ok = false; break; }
-        convert(sbase + kK, sbase + kCodes, false, misc.keys[par]);
-        mbar_arrive(&code_free[0]);
+        if (!warp_wait(empty, par ^ 1u, abort_flag) || !warp_wait(&code_full[is_v], par, abort_flag)) { ok = false; break; }
+        convert(sbase + (is_v ? kV : kK), sbase + kCodes + is_v * kAtom, is_v, misc.keys[tile & 3]);
+        mbar_arrive(&code_free[is_v]);
         fence_async_shared();
-        mbar_arrive(k_full);
-        if (!warp_wait(v_empty, par ^ 1u, abort_flag) || !warp_wait(&code_full[1], par, abort_flag)) { ok = false; break; }
-        convert(sbase + kV, sbase + kCodes + kAtom, true, misc.keys[par]);
-        mbar_arrive(&code_free[1]);
-        fence_async_shared();
-        mbar_arrive(v_full);
+        mbar_arrive(full);
       }
     }
     if (!ok) {
@@ -422,10 +420,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
         ids_next = page_of(b + 2);
         // K's codes of the block before have been read
         if (!warp_wait(&code_free[0], par ^ 1u, abort_flag)) { ok = false; break; }
-        if (lane == 0) misc.keys[par] = BlockKeys{min(kBlockKeys, klim - b * kBlockKeys), (int)have, (b + 1) * kBlockKeys > first};
+        if (lane == 0) misc.keys[tile & 3] = BlockKeys{min(kBlockKeys, klim - b * kBlockKeys), (int)have, (b + 1) * kBlockKeys > first};
         __syncwarp();
         fetch(0, b, here, have);
-        // V's too, which were written when P V of the one before that was done: its scales have been read
+        // V's too, whose tile was written when P V of the one before it was done: that one's scales have been read
         if (!warp_wait(&code_free[1], par ^ 1u, abort_flag)) { ok = false; break; }
         fetch(1, b, here, have);
         BlockScales& sc = misc.scales[par];
@@ -458,22 +456,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
         if (n == 0) continue;
         for (int side = 0; side < 2 && ok; ++side)
           if (nx[side]) {
-            ok = mbar_wait_held(&q_full[side], nq[side] & 1u, abort_flag);
+            ok = mbar_wait(&q_full[side], nq[side] & 1u, abort_flag);
             ++nq[side];
           }
         for (int b = 0; b <= n && ok; ++b) {
-          if (b < n && !mbar_wait_held(k_full, (uint32_t)(tile + b) & 1u, abort_flag)) { ok = false; break; }
-          if (b > 0 && !mbar_wait_held(v_full, (uint32_t)(tile + b - 1) & 1u, abort_flag)) { ok = false; break; }
+          if (b < n && !mbar_wait(k_full, (uint32_t)(tile + b) & 1u, abort_flag)) { ok = false; break; }
+          if (b > 0 && !mbar_wait(v_full, (uint32_t)(tile + b - 1) & 1u, abort_flag)) { ok = false; break; }
           for (int side = 0; side < 2; ++side) {
             if (b < nx[side]) {
-              if (!mbar_wait_held(&s_free[side], ((ns[side] + (uint32_t)b) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+              if (!mbar_wait(&s_free[side], ((ns[side] + (uint32_t)b) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
               tc_fence_after();
               mma_scores<DH>(tmem + side * 128, sbase + kQ + side * kTile, sbase + kK);
               umma_commit(&s_full[side]);
             }
             if (side == 1 && b < n) umma_commit(k_empty);
             if (b > 0 && b - 1 < nx[side]) {
-              if (!mbar_wait_held(&p_full[side], (ns[side] + (uint32_t)(b - 1)) & 1u, abort_flag)) { ok = false; break; }
+              if (!mbar_wait(&p_full[side], (ns[side] + (uint32_t)(b - 1)) & 1u, abort_flag)) { ok = false; break; }
               tc_fence_after();
               mma_values<N>(tmem + 256 + side * 128, sbase + kP + side * kTile, sbase + kV, b > 1);
               umma_commit(&p_free[side]);
