@@ -4,9 +4,10 @@
 // The products are tcgen05 kind::f16 ones, fp16 operands and fp32 accumulators in tensor memory: FP8 codes are fp16 numbers, and q is
 // one over a power of two of its row, so the scores lose nothing.  (FP8 operands would need q and P in several 4-bit parts.)
 // A CTA has 256 rows of one K/V head, two tiles of 128 (token, query head) pairs, A and B, which share what is
-// made of each block of 128 keys; its 16 warps (two of them idle: rows' warps stand at their quarter of tensor memory):
+// made of each block of 128 keys; its 16 warps:
 //   warp 5       pages, bulk copies of a block's codes of K and V into shared memory, and its scales, a block ahead;
-//   warps 0-3    the codes into swizzled fp16 tiles, two for K's and two for V's (whose tiles are free at different times);
+//   warps 0-3    K's codes into a swizzled fp16 tile (each block's first product waits for it);
+//   warps 6, 7   V's;
 //   warp 4       the products, one thread: S_A = Q_A K^T, O_A += P_A V of the block before, then B's;
 //   warps 8-15   a row a thread (A, then B): q into shared memory; per block the row's maximum from S, P = 2^(s - m) as fp16
 //                into shared memory, and at the end O over the sum.
@@ -15,13 +16,15 @@
 //
 // Every mbarrier wait is bounded; on expiry the CTA records FP8Q_STATUS_TIMEOUT, stops issuing, waits for the products that it
 // issued, frees tensor memory and exits.
+#include <type_traits>
+
 #include "fp8q_kvline.cuh"
 
 namespace fp8q {
 
 namespace {
 
-constexpr int kLoaders = 64 /* of K, of V */, kMmaWarp = 4, kCopyWarp = 5, kFirstRowWarp = 8, kThreads = 512;
+constexpr int kKThreads = 128, kVThreads = 64, kMmaWarp = 4, kCopyWarp = 5, kFirstRowWarp = 8, kThreads = 512;
 constexpr int kTileRows = 128, kRows = 2 * kTileRows;
 constexpr int kAtom = 16384;       // 128 rows x 128 bytes: 64 fp16 columns of a swizzled tile
 constexpr int kTile = 2 * kAtom;   // a tile of 128 columns
@@ -258,14 +261,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
       mbar_init(&p_full[i], kTileRows);
       mbar_init(&p_free[i], 1);
     }
-    mbar_init(k_full, kLoaders);
+    mbar_init(k_full, kKThreads);
     mbar_init(k_empty, 1);
-    mbar_init(v_full, kLoaders);
+    mbar_init(v_full, kVThreads);
     mbar_init(v_empty, 1);
     mbar_init(drain, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&code_full[i], 1);
-      mbar_init(&code_free[i], kLoaders);
+      mbar_init(&code_free[i], i ? kVThreads : kKThreads);
     }
     misc.abort = misc.odd = 0;
     fence_mbar_init();
@@ -286,75 +289,72 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
   int tile = 0, seg = 0;  // blocks and segments so far
   bool ok = true;
 
-  if (warp < 2 * kLoaders / 32) {
-    // ---------------- codes to fp16 ----------------
-    constexpr int kPieces = DH / 16;                            // of 16 codes, of a key
-    constexpr int kMine = kBlockKeys * kPieces / kLoaders;      // of a thread, of a block
-    const int is_v = warp >> 1, lt = t & (kLoaders - 1);
+  // ---------------- codes to fp16: THREADS threads, `lt` this one's number ----------------
+  constexpr int kPieces = DH / 16;  // of 16 codes, of a key
+  auto convert = [&](auto threads, int lt, uint32_t dst, uint32_t from, bool values, const BlockKeys& keys) {
+    constexpr int kN = decltype(threads)::value, kMine = kBlockKeys * kPieces / kN, kBatch = kMine % 4 ? 3 : 4;
     // Piece i of this thread: codes 16 ch .. of key row `row`.  Rows of 128: eight neighbouring threads take the first half of a row
     // and the second of the next, so that what they read, and the two 16-byte pieces that each writes, touch every bank once; i moves
-    // the row by 8, so neither offset depends on it.
+    // the row by a multiple of 8, so neither offset depends on it.
     auto place = [&](int i, int& row, int& ch) {
-      const int idx = i * kLoaders + lt;
       if (DH == 128) {
-        row = i * 8 + (((lt >> 4) << 1) | ((lt >> 2) & 1));
+        row = i * (kN / 8) + (((lt >> 4) << 1) | ((lt >> 2) & 1));
         ch = (lt & 3) | (((lt >> 2) ^ (lt >> 3)) & 1) << 2;
       } else {
+        const int idx = i * kN + lt;
         row = idx / kPieces;
         ch = idx - row * kPieces;
       }
     };
-    // Four pieces are read before the first is written: a write holds the reads behind it back.
-    auto convert = [&](uint32_t dst, uint32_t from, bool values, const BlockKeys& keys) {
-      constexpr int kBatch = 4;
-      const int rows = keys.rows, have = keys.have, check = keys.check && values;
-      const bool whole = rows == kBlockKeys && have == 0xFF;
+    const int rows = keys.rows, have = keys.have, check = keys.check && values;
+    const bool whole = rows == kBlockKeys && have == 0xFF;
+    // A batch is read before its first piece is written: a write holds the reads behind it back.
 #pragma unroll 1
-      for (int i0 = 0; i0 < kMine; i0 += kBatch) {
-        uint4 x[kBatch];
-        int row[kBatch], ch[kBatch];
+    for (int i0 = 0; i0 < kMine; i0 += kBatch) {
+      uint4 x[kBatch];
+      int row[kBatch], ch[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          place(i0 + k, row[k], ch[k]);
-          x[k] = ld_shared_v4(from + (uint32_t)(row[k] * DH + ch[k] * 16));
-        }
-        if (!whole) {
+      for (int k = 0; k < kBatch; ++k) {
+        place(i0 + k, row[k], ch[k]);
+        x[k] = ld_shared_v4(from + (uint32_t)(row[k] * DH + ch[k] * 16));
+      }
+      if (!whole) {
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k)
-            if (row[k] >= rows || !(have >> (row[k] >> 4) & 1)) x[k] = make_uint4(0, 0, 0, 0);
-        }
-        if (check) {
-          uint32_t odd = 0;
+        for (int k = 0; k < kBatch; ++k)
+          if (row[k] >= rows || !(have >> (row[k] >> 4) & 1)) x[k] = make_uint4(0, 0, 0, 0);
+      }
+      if (check) {
+        uint32_t odd = 0;
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k) odd |= nonfinite4<FMT>(x[k].x) | nonfinite4<FMT>(x[k].y) | nonfinite4<FMT>(x[k].z) | nonfinite4<FMT>(x[k].w);
-          if (odd) {  // a weight of 0 times it would be NaN in rows that do not see it: 0 here, and the rows look for themselves
+        for (int k = 0; k < kBatch; ++k) odd |= nonfinite4<FMT>(x[k].x) | nonfinite4<FMT>(x[k].y) | nonfinite4<FMT>(x[k].z) | nonfinite4<FMT>(x[k].w);
+        if (odd) {  // a weight of 0 times it would be NaN in rows that do not see it: 0 here, and the rows look for themselves
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-              x[k].x &= ~((nonfinite4<FMT>(x[k].x) >> 7) * 0xFFu);
-              x[k].y &= ~((nonfinite4<FMT>(x[k].y) >> 7) * 0xFFu);
-              x[k].z &= ~((nonfinite4<FMT>(x[k].z) >> 7) * 0xFFu);
-              x[k].w &= ~((nonfinite4<FMT>(x[k].w) >> 7) * 0xFFu);
-            }
-            misc.odd = 1;
+          for (int k = 0; k < kBatch; ++k) {
+            x[k].x &= ~((nonfinite4<FMT>(x[k].x) >> 7) * 0xFFu);
+            x[k].y &= ~((nonfinite4<FMT>(x[k].y) >> 7) * 0xFFu);
+            x[k].z &= ~((nonfinite4<FMT>(x[k].z) >> 7) * 0xFFu);
+            x[k].w &= ~((nonfinite4<FMT>(x[k].w) >> 7) * 0xFFu);
           }
-        }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const uint4 v = x[k];
-          st_shared_v4(piece(dst, row[k], 2 * ch[k]),
-                       make_uint4(f16x2_of<FMT>(v.x), f16x2_of<FMT>(v.x >> 16), f16x2_of<FMT>(v.y), f16x2_of<FMT>(v.y >> 16)));
-          st_shared_v4(piece(dst, row[k], 2 * ch[k] + 1),
-                       make_uint4(f16x2_of<FMT>(v.z), f16x2_of<FMT>(v.z >> 16), f16x2_of<FMT>(v.w), f16x2_of<FMT>(v.w >> 16)));
+          misc.odd = 1;
         }
       }
-    };
-    uint64_t *full = is_v ? v_full : k_full, *empty = is_v ? v_empty : k_empty;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const uint4 v = x[k];
+        st_shared_v4(piece(dst, row[k], 2 * ch[k]),
+                     make_uint4(f16x2_of<FMT>(v.x), f16x2_of<FMT>(v.x >> 16), f16x2_of<FMT>(v.y), f16x2_of<FMT>(v.y >> 16)));
+        st_shared_v4(piece(dst, row[k], 2 * ch[k] + 1),
+                     make_uint4(f16x2_of<FMT>(v.z), f16x2_of<FMT>(v.z >> 16), f16x2_of<FMT>(v.w), f16x2_of<FMT>(v.w >> 16)));
+      }
+    }
+  };
+  auto convert_blocks = [&](auto threads, int lt, int is_v, uint64_t* full, uint64_t* empty) {
     while (ok && w.next()) {
       const int n = max(w.blocks_of(0), w.blocks_of(1));
       for (int b = 0; b < n; ++b, ++tile) {
         const uint32_t par = (uint32_t)tile & 1u;
         if (!warp_wait(empty, par ^ 1u, abort_flag) || !warp_wait(&code_full[is_v], par, abort_flag)) { ok = false; break; }
-        convert(sbase + (is_v ? kV : kK), sbase + kCodes + is_v * kAtom, is_v, misc.keys[tile & 3]);
+        convert(threads, lt, sbase + (is_v ? kV : kK), sbase + kCodes + is_v * kAtom, is_v, misc.keys[tile & 3]);
         mbar_arrive(&code_free[is_v]);
         fence_async_shared();
         mbar_arrive(full);
@@ -364,6 +364,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
       atomicOr(p.kv.status, kStatusTimeout);
       *abort_flag = 1;
     }
+  };
+
+  if (t < kKThreads) {
+    convert_blocks(std::integral_constant<int, kKThreads>{}, t, 0, k_full, k_empty);
+  } else if (warp == 6 || warp == 7) {
+    convert_blocks(std::integral_constant<int, kVThreads>{}, t - 192, 1, v_full, v_empty);
   } else if (warp == kCopyWarp) {
     // ---------------- pages, copies, scales ----------------
     uint32_t fetched[2] = {0, 0};  // blocks whose codes were asked for
@@ -461,7 +467,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
           }
         for (int b = 0; b <= n && ok; ++b) {
           if (b < n && !mbar_wait(k_full, (uint32_t)(tile + b) & 1u, abort_flag)) { ok = false; break; }
-          if (b > 0 && !mbar_wait(v_full, (uint32_t)(tile + b - 1) & 1u, abort_flag)) { ok = false; break; }
           for (int side = 0; side < 2; ++side) {
             if (b < nx[side]) {
               if (!mbar_wait(&s_free[side], ((ns[side] + (uint32_t)b) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
@@ -471,7 +476,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
             }
             if (side == 1 && b < n) umma_commit(k_empty);
             if (b > 0 && b - 1 < nx[side]) {
-              if (!mbar_wait(&p_full[side], (ns[side] + (uint32_t)(b - 1)) & 1u, abort_flag)) { ok = false; break; }
+              if (!mbar_wait(v_full, (uint32_t)(tile + b - 1) & 1u, abort_flag) ||
+                  !mbar_wait(&p_full[side], (ns[side] + (uint32_t)(b - 1)) & 1u, abort_flag)) { ok = false; break; }
               tc_fence_after();
               mma_values<N>(tmem + 256 + side * 128, sbase + kP + side * kTile, sbase + kV, b > 1);
               umma_commit(&p_free[side]);
@@ -584,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
           const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            uint32_t z[32], y[16];
+            uint32_t z[32];
             tmem_ld32(tS + c * 32, z);
             if (c == 3) {
               tc_fence_before();
@@ -600,19 +606,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
               const float fg = factor(2 * c + g), cg = sc.dx[2 * c + g] - ref;
               const float2 f2 = make_float2(fg, fg), c2 = make_float2(cg, cg);
               float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+              uint32_t y[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 const int col = g * 16 + 2 * k;
                 const float2 e = __ffma2_rn(make_float2(__uint_as_float(z[col]), __uint_as_float(z[col + 1])), f2, c2);
                 const float2 pr = make_float2(ex2(e.x), ex2(e.y));
                 sum[k & 1] = __fadd2_rn(sum[k & 1], pr);
-                y[g * 8 + k] = pack_half2(pr.x, pr.y);
+                y[k] = pack_half2(pr.x, pr.y);
               }
               sum[0] = __fadd2_rn(sum[0], sum[1]);
               l = __fmaf_rn(sum[0].x + sum[0].y, sc.back[2 * c + g], l);
-            }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) st_shared_v4(piece(ptile, r, 4 * c + k), make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]));
+              for (int k = 0; k < 2; ++k)
+                st_shared_v4(piece(ptile, r, 2 * (2 * c + g) + k), make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]));
+            }
           }
           tc_fence_before();
           fence_async_shared();
