@@ -136,9 +136,10 @@ __device__ __forceinline__ int64_t seq_cost(const AttendArgs& p, const KvSeq& q)
   return sum * p.kv.hkv;
 }
 
-// One part of the line after the other: what all roles walk through alike.
+// One part of the line after the other: what all roles walk through alike.  next() is a function of its own, and a Walk lies in
+// local memory: inlined into every role, its code and its registers were in the way of the loops over the blocks.
 struct Walk {
-  const AttendArgs& p;
+  const AttendArgs* p;
   int s, rt;       // sequence, row tile
   KvSeq q;
   Tiles t;
@@ -147,19 +148,18 @@ struct Walk {
   // of the segment
   int h, r0, n_rows, nb, b0, b1;
   int64_t unit0, cost;
-  __device__ __forceinline__ Walk(const AttendArgs& args, const Line& l, int64_t begin, int64_t stop)
-      : p(args), s(l.s), rt(0), q(l.q), t(tiles_of(args, l.q)), base(l.base), at(begin), end(stop) {}
-  __device__ __forceinline__ bool next() {
+  __device__ __noinline__ bool next() {
+    const KvArgs& kv = p->kv;
     while (at < end) {
       if (rt >= t.count()) {
-        if (++s >= p.kv.n_seqs) return false;
-        q = kv_seq(p.kv, s);
-        t = tiles_of(p, q);
+        if (++s >= kv.n_seqs) return false;
+        q = kv_seq(kv, s);
+        t = tiles_of(*p, q);
         rt = 0;
         continue;
       }
       const int c = t.cost(rt);
-      const int64_t here = (int64_t)c * p.kv.hkv;
+      const int64_t here = (int64_t)c * kv.hkv;
       if (at >= base + here) {
         base += here;
         ++rt;
@@ -189,7 +189,7 @@ struct Walk {
 };
 
 template <int FMT, int DH>
-__global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs p) {
+__global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_constant__ AttendArgs p) {
   constexpr int N = DH == 64 ? 64 : 128;  // columns of V's tile and of O: 96 are filled up with zeros
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -285,7 +285,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
     for (int i = t; i < 128 * 4; i += kThreads) st_shared_v4(piece(sbase + kV, i >> 2, 12 + (i & 3)), make_uint4(0, 0, 0, 0));
     __syncthreads();
   }
-  Walk w(p, line, begin, end);
+  Walk w;
+  w.p = &p;
+  w.s = line.s;
+  w.rt = 0;
+  w.q = line.q;
+  w.t = tiles_of(p, line.q);
+  w.base = line.base;
+  w.at = begin;
+  w.end = end;
   int tile = 0, seg = 0;  // blocks and segments so far
   bool ok = true;
 
@@ -379,15 +387,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
       const int first = w.t.limit(w.r0), klim = w.t.limit(w.r0 + w.n_rows - 1), stop = w.b0 + n;
       const int32_t* table = p.kv.pages + (int64_t)w.s * p.kv.max_pages;
       const int mask = (1 << p.kv.page_shift) - 1, step = min(1 << p.kv.page_shift, kBlockKeys) >> 4;  // groups of 16 keys of a copy
-      // lanes 0 .. 7: the page of keys 16 lane .. of block b; -1: none
-      auto page_of = [&](int b) {
-        const int key = b * kBlockKeys + 16 * lane;
-        if (lane >= 8 || b >= stop || key >= klim) return -1;
-        const int id = table[key >> p.kv.page_shift];
+      // Lanes 0 .. 7: the page of keys 16 lane .. of block b.  Read a block before it is looked at, and its scales a block before
+      // they are: a load under a condition, or looked at at once, would hold this warp for its latency.
+      auto seen = [&](int b) { return lane < 8 && b < stop && b * kBlockKeys + 16 * lane < klim; };
+      auto read_page = [&](int b) { return table[seen(b) ? (b * kBlockKeys + 16 * lane) >> p.kv.page_shift : 0]; };
+      auto page_of = [&](int b, int id) {  // -1: none
+        if (!seen(b)) return -1;
         if (id >= 0 && id < p.kv.n_pages) return id;
         atomicOr(p.kv.status, kStatusBadCache);
         return -1;
       };
+      auto read_scale = [&](const uint8_t* scales, int id) { return (int)scales[(int64_t)max(id, 0) * p.kv.hkv + w.h]; };
       // Lanes 0 .. 7 copy block b's codes of K (0) or V (1), a page (or 128 keys) each.  Slots behind the last key come along.
       auto fetch = [&](int which, int b, int id, unsigned have) {
         ++fetched[which];
@@ -405,7 +415,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
         }
         __syncwarp();
       };
-      int ids = page_of(w.b0), ids_next = page_of(w.b0 + 1);
+      int here = read_page(w.b0), next = read_page(w.b0 + 1);
+      here = page_of(w.b0, here);
+      int xk = read_scale(p.kv.k_scale, here), xv = read_scale(p.kv.v_scale, here);
       // the segment's largest exponent of V
       int xref = -1000;
       for (int pg = (w.b0 * kBlockKeys >> p.kv.page_shift) + lane; (int64_t)pg << p.kv.page_shift < min((int64_t)klim, (int64_t)stop * kBlockKeys);
@@ -417,13 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
       if (lane == 0) misc.xref[seg & 3] = xref;
       for (int b = w.b0; b < stop; ++b, ++tile) {
         const uint32_t par = (uint32_t)tile & 1u;
-        const int none = kNoPage;
-        const int xk = ids >= 0 ? (int)p.kv.k_scale[(int64_t)ids * p.kv.hkv + w.h] - 127 : none;
-        const int xv = ids >= 0 ? (int)p.kv.v_scale[(int64_t)ids * p.kv.hkv + w.h] - 127 : none;
-        const unsigned have = __ballot_sync(0xFFFFFFFFu, ids >= 0) & 0xFFu;
-        const int here = ids;
-        ids = ids_next;
-        ids_next = page_of(b + 2);
+        const unsigned have = __ballot_sync(0xFFFFFFFFu, here >= 0) & 0xFFu;
         // K's codes of the block before have been read
         if (!warp_wait(&code_free[0], par ^ 1u, abort_flag)) { ok = false; break; }
         if (lane == 0) misc.keys[tile & 3] = BlockKeys{min(kBlockKeys, klim - b * kBlockKeys), (int)have, (b + 1) * kBlockKeys > first};
@@ -434,14 +440,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const AttendArgs
         fetch(1, b, here, have);
         BlockScales& sc = misc.scales[par];
         if (lane < 8) {
-          const int dx = max(xv == none ? -60 : xv - xref, -60);
-          sc.k[lane] = pow2i(xk == none ? 0 : xk);
+          const int dx = max(here < 0 ? -60 : xv - 127 - xref, -60);
+          sc.k[lane] = pow2i(here < 0 ? 0 : xk - 127);
           sc.dx[lane] = kOffset + (float)dx;
           sc.back[lane] = pow2i(-dx);
         }
         if (lane == 0) sc.none[0] = (int)(~have & 0xFFu);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sc_full[par]);
+        here = page_of(b + 1, next);
+        next = read_page(b + 2);
+        xk = read_scale(p.kv.k_scale, here);
+        xv = read_scale(p.kv.v_scale, here);
       }
       ++seg;
     }
