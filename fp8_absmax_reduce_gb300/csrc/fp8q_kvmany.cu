@@ -115,10 +115,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 // A sequence's units: row tile by row tile, each for every K/V head.
 struct Tiles {
   int pairs, before, G;  // (token, head) pairs; tokens before the call's; query heads of a K/V head
+  uint32_t inv;          // 2^32 / G, rounded up: r inv / 2^32 is r / G for r below 2^22 (G at most 1024)
+  __device__ __forceinline__ int token(int r) const { return G == 1 ? r : r < 1 << 22 ? (int)__umulhi((uint32_t)r, inv) : r / G; }
   __device__ __forceinline__ int count() const { return (int)((pairs + (int64_t)(kRows - 1)) / kRows); }
   __device__ __forceinline__ int rows(int rt) const { return min(kRows, pairs - rt * kRows); }
   // the keys that pair r sees
-  __device__ __forceinline__ int limit(int r) const { return max(0, before + r / G + 1); }
+  __device__ __forceinline__ int limit(int r) const { return max(0, before + token(r) + 1); }
   __device__ __forceinline__ int blocks(int rt) const { return (limit(rt * kRows + rows(rt) - 1) + kBlockKeys - 1) / kBlockKeys; }
   __device__ __forceinline__ int cost(int rt) const {
     const int nb = blocks(rt);
@@ -127,7 +129,7 @@ struct Tiles {
 };
 __device__ __forceinline__ Tiles tiles_of(const AttendArgs& p, const KvSeq& q) {
   const int G = p.n_heads / p.kv.hkv;
-  return Tiles{q.n * G, q.len - q.n, G};
+  return Tiles{q.n * G, q.len - q.n, G, 0xFFFFFFFFu / (uint32_t)G + 1u};
 }
 __device__ __forceinline__ int64_t seq_cost(const AttendArgs& p, const KvSeq& q) {
   const Tiles t = tiles_of(p, q);
@@ -217,7 +219,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
   Line* line_s = reinterpret_cast<Line*>(smem + 256);
   const int per = (p.kv.n_seqs + kThreads - 1) / kThreads;
   int64_t total = 0, before = 0, own = 0;
-  for (int s = t * per; s < min((t + 1) * per, p.kv.n_seqs); ++s) own += seq_cost(p, kv_seq(p.kv, s));
+  KvSeq mine{0, 0, 0};  // the last of this thread's sequences
+  for (int s = t * per; s < min((t + 1) * per, p.kv.n_seqs); ++s) {
+    mine = kv_seq(p.kv, s);
+    own += seq_cost(p, mine);
+  }
   {
     int64_t upto = own;
 #pragma unroll
@@ -241,15 +247,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
   if (begin >= before && begin < before + own) {
     int64_t base = before;
     int s = t * per;
-    KvSeq q = kv_seq(p.kv, s);
-    for (; s < p.kv.n_seqs - 1; ++s) {
-      const int64_t n = seq_cost(p, q);
-      if (begin < base + n) break;
-      base += n;
-      q = kv_seq(p.kv, s + 1);
+    if (per > 1) {
+      mine = kv_seq(p.kv, s);
+      for (; s < p.kv.n_seqs - 1; ++s) {
+        const int64_t n = seq_cost(p, mine);
+        if (begin < base + n) break;
+        base += n;
+        mine = kv_seq(p.kv, s + 1);
+      }
     }
     line_s->s = s;
-    line_s->q = q;
+    line_s->q = mine;
     line_s->base = base;
   }
   if (t == 0) {
@@ -518,33 +526,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       const int nx = w.blocks_of(side), n = max(w.blocks_of(0), w.blocks_of(1));
       const int i = side * kTileRows + r, pair = w.r0 + i;
       const bool real = i < w.n_rows;
-      const int G = w.t.G, tok = pair / G, hd = w.h * G + pair - tok * G;
+      const int G = w.t.G, tok = w.t.token(real ? pair : w.r0), hd = w.h * G + (real ? pair : w.r0) - tok * G;
       const int64_t row = w.q.first + tok;
       const int limit = real ? w.t.limit(pair) : kAll;
       const int kmin = __reduce_min_sync(0xFFFFFFFFu, limit);
       float m = -INFINITY, l = 0.0f;
       int xref = 0;
       if (nx) {
-        // q over a power of two of its row, as fp16
-        uint32_t x[DH / 2];
-        const uint16_t* src = p.qkv + row * (p.n_heads + 2 * p.kv.hkv) * DH + (int64_t)hd * DH;
-        uint32_t big = 0;
+        // q over a power of two of its row, as fp16: a warp takes its 32 rows a few at a time, 16 bytes a lane (a thread that read its own
+        // row took 15000 cycles for it).  A row that does not exist reads the unit's first.
+        constexpr int kLanes = DH == 64 ? 8 : 16, kStep = 32 / kLanes, kBatch = 4;
+        const int sub = lane / kLanes, col = lane % kLanes;
+        int ex = -110;
+#pragma unroll 1
+        for (int k0 = 0; k0 < 32 / kStep; k0 += kBatch) {
+          uint4 v[kBatch];
 #pragma unroll
-        for (int k = 0; k < DH / 8; ++k) {
-          const uint4 v = real ? ld_nc_v4(src + 8 * k) : make_uint4(0, 0, 0, 0);
-          x[4 * k] = v.x; x[4 * k + 1] = v.y; x[4 * k + 2] = v.z; x[4 * k + 3] = v.w;
+          for (int k = 0; k < kBatch; ++k) {
+            const int other = w.r0 + i - lane + (k0 + k) * kStep + sub;
+            const int pr = other - w.r0 < w.n_rows ? other : w.r0, tk = w.t.token(pr);
+            const uint16_t* src = p.qkv + ((int64_t)(w.q.first + tk) * (p.n_heads + 2 * p.kv.hkv) + w.h * G + pr - tk * G) * DH;
+            v[k] = ld_nc_v4(src + (col * 8 < DH ? col * 8 : 0));
+          }
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            uint32_t big = max(max(absmax_bf16x2(v[k].x), absmax_bf16x2(v[k].y)), max(absmax_bf16x2(v[k].z), absmax_bf16x2(v[k].w)));
+#pragma unroll
+            for (int m = 1; m < kLanes; m <<= 1) big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, m));
+            const int e = max((int)(big >> 23) - 127, -110);
+            const float fq = pow2i(14 - e);
+            if (col * 8 < DH)
+              st_shared_v4(piece(qtile, (warp & 3) * 32 + (k0 + k) * kStep + sub, col),
+                           make_uint4(pack_half2(bf16_lo(v[k].x) * fq, bf16_hi(v[k].x) * fq), pack_half2(bf16_lo(v[k].y) * fq, bf16_hi(v[k].y) * fq),
+                                      pack_half2(bf16_lo(v[k].z) * fq, bf16_hi(v[k].z) * fq), pack_half2(bf16_lo(v[k].w) * fq, bf16_hi(v[k].w) * fq)));
+            const int mine = __shfl_sync(0xFFFFFFFFu, e, (lane % kStep) * kLanes);
+            if (lane / kStep == k0 + k) ex = mine;
+          }
         }
-#pragma unroll
-        for (int k = 0; k < DH / 2; ++k) big = max(big, absmax_bf16x2(x[k]));
-        const int ex = max((int)(big >> 23) - 127, -110);
-        const float fq = pow2i(14 - ex), rowf = p.scale_log2 * pow2i(ex - 14);
-#pragma unroll
-        for (int k = 0; k < DH / 8; ++k) {
-          uint32_t y[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] = pack_half2(bf16_lo(x[4 * k + e]) * fq, bf16_hi(x[4 * k + e]) * fq);
-          st_shared_v4(piece(qtile, r, k), make_uint4(y[0], y[1], y[2], y[3]));
-        }
+        const float rowf = p.scale_log2 * pow2i(ex - 14);
         fence_async_shared();
         mbar_arrive(&q_full[side]);
 
@@ -662,6 +681,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
         }
         __syncwarp();
       }
+      // Through this warp's rows of P (4 KB of its own after `bad`), so that neighbouring lanes write a row's neighbouring bytes.
+      const uint32_t stage = ptile + (uint32_t)((warp & 3) * 4096) + kAtom;
+      const int64_t to_att = (row * p.n_heads + hd) * DH, to_part = ((int64_t)slot * kRows + i) * DH;
 #pragma unroll 1
       for (int c = 0; c < DH / 32; ++c) {
         uint32_t o[32];
@@ -673,19 +695,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
           if (odd && bad[c * 32 + k] < limit) v = __uint_as_float(0x7FC00000u);
           o[k] = __float_as_uint(v);
         }
-        if (!real) {  // no row of the call
-        } else if (whole) {
-          uint4* to = reinterpret_cast<uint4*>(p.att + (row * p.n_heads + hd) * DH + c * 32);
+        if (whole) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            to[k] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * k]), __uint_as_float(o[8 * k + 1])),
-                               pack_bf16x2(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3])),
-                               pack_bf16x2(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5])),
-                               pack_bf16x2(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7])));
+            st_shared_v4(stage + lane * 64 + ((k ^ (lane >> 1)) & 3) * 16,
+                         make_uint4(pack_bf16x2(__uint_as_float(o[8 * k]), __uint_as_float(o[8 * k + 1])),
+                                    pack_bf16x2(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3])),
+                                    pack_bf16x2(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5])),
+                                    pack_bf16x2(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7]))));
         } else {
-          uint4* to = reinterpret_cast<uint4*>(p.part_o + ((int64_t)slot * kRows + i) * DH + c * 32);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) to[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          for (int k = 0; k < 8; ++k)
+            st_shared_v4(stage + lane * 128 + ((k ^ lane) & 7) * 16, make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
+        }
+        __syncwarp();
+        const int step = whole ? 8 : 4, lanes = 32 / step;  // rows at a time; lanes of a row
+#pragma unroll 4
+        for (int k = 0; k < 32 / step; ++k) {
+          const int from = k * step + lane / lanes, col = lane % lanes;
+          const int64_t at = __shfl_sync(0xFFFFFFFFu, whole ? to_att : to_part, from);
+          if (!__shfl_sync(0xFFFFFFFFu, (int)real, from)) continue;
+          if (whole)
+            *reinterpret_cast<uint4*>(p.att + at + c * 32 + col * 8) = ld_shared_v4(stage + from * 64 + ((col ^ (from >> 1)) & 3) * 16);
+          else
+            *reinterpret_cast<uint4*>(p.part_o + at + c * 32 + col * 4) = ld_shared_v4(stage + from * 128 + ((col ^ from) & 7) * 16);
         }
       }
       if (real) {
@@ -708,37 +741,55 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// Block (j, y): rows 8 y .. of the unit that CTA j began and did not end, a row a warp; its parts in order.
-constexpr int kJoinRows = 8;
+// Block (j, y): rows 32 y .. of the unit that CTA j began and did not end, four a warp at a time; its parts in order.
+constexpr int kJoinWarps = 8, kJoinRows = 4;
 template <int DH>
-__global__ void __launch_bounds__(32 * kJoinRows) k_kv_join_many(const AttendArgs p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join_many(const AttendArgs p) {
   wait_for_previous();
-  const int j = blockIdx.x, r = blockIdx.y * kJoinRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int j = blockIdx.x, r0 = (blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * kJoinRows, lane = threadIdx.x & 31;
   const Cut cut = p.cuts[j];
-  if (cut.first == cut.end || r >= cut.rows) return;
+  if (cut.first == cut.end || r0 >= cut.rows) return;
   const int n = (int)((cut.end * cut.ctas + cut.total - 1) / cut.total) - j;
   auto slot = [&](int i) { return i == 0 ? 2 * j + 1 : 2 * (j + i); };
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_lse[slot(i) * kRows + r]);
+  float M[kJoinRows], sum[kJoinRows], acc[kJoinRows][DH / 32];
 #pragma unroll
-  for (int k = 16; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, k));
-  float acc[DH / 32], sum = 0.0f;
+  for (int q = 0; q < kJoinRows; ++q) {
+    M[q] = -INFINITY;
+    sum[q] = 0.0f;
 #pragma unroll
-  for (int k = 0; k < DH / 32; ++k) acc[k] = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float e = p.part_lse[slot(i) * kRows + r];
-    const float wgt = e == -INFINITY ? 0.0f : ex2(e - M);
-    const float* src = p.part_o + ((int64_t)slot(i) * kRows + r) * DH + lane;
-    sum += wgt;
-#pragma unroll
-    for (int k = 0; k < DH / 32; ++k) acc[k] += wgt * src[32 * k];
+    for (int k = 0; k < DH / 32; ++k) acc[q][k] = 0.0f;
   }
-  const int G = p.n_heads / p.kv.hkv, tok = (cut.group_row + r) / G, hd = cut.head * G + (cut.group_row + r) - tok * G;
-  __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(p.att) + ((int64_t)(cut.row0 + tok) * p.n_heads + hd) * DH + lane;
+  // (rows behind the tile's last hold what an earlier call left; they are not written)
+  for (int i = 0; i < n; ++i) {
+    float e[kJoinRows], v[kJoinRows][DH / 32];
 #pragma unroll
-  for (int k = 0; k < DH / 32; ++k) to[32 * k] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : acc[k] / sum);
-  if (lane == 0) p.lse[(int64_t)hd * p.kv.T + cut.row0 + tok] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kLn2;
+    for (int q = 0; q < kJoinRows; ++q) {
+      e[q] = p.part_lse[slot(i) * kRows + r0 + q];
+      const float* src = p.part_o + ((int64_t)slot(i) * kRows + r0 + q) * DH + lane;
+#pragma unroll
+      for (int k = 0; k < DH / 32; ++k) v[q][k] = src[32 * k];
+    }
+#pragma unroll
+    for (int q = 0; q < kJoinRows; ++q) {
+      const float mn = fmaxf(M[q], e[q]);
+      const float fade = mn == M[q] ? 1.0f : ex2(M[q] - mn), wgt = e[q] == -INFINITY ? 0.0f : e[q] == mn ? 1.0f : ex2(e[q] - mn);
+      sum[q] = sum[q] * fade + wgt;
+#pragma unroll
+      for (int k = 0; k < DH / 32; ++k) acc[q][k] = acc[q][k] * fade + (e[q] == -INFINITY ? 0.0f : wgt * v[q][k]);
+      M[q] = mn;
+    }
+  }
+  const int G = p.n_heads / p.kv.hkv;
+#pragma unroll
+  for (int q = 0; q < kJoinRows; ++q) {
+    const int r = r0 + q;
+    if (r >= cut.rows) break;
+    const int tok = (cut.group_row + r) / G, hd = cut.head * G + (cut.group_row + r) - tok * G;
+    __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(p.att) + ((int64_t)(cut.row0 + tok) * p.n_heads + hd) * DH + lane;
+#pragma unroll
+    for (int k = 0; k < DH / 32; ++k) to[32 * k] = __float2bfloat16_rn(sum[q] == 0.0f ? 0.0f : acc[q][k] / sum[q]);
+    if (lane == 0) p.lse[(int64_t)hd * p.kv.T + cut.row0 + tok] = sum[q] == 0.0f ? -INFINITY : (M[q] + log2f(sum[q])) * kLn2;
+  }
 }
 
 template <int FMT, int DH>
@@ -748,7 +799,7 @@ cudaError_t launch(const AttendArgs& p, int ctas, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   k_kv_attend_many<FMT, DH><<<ctas, kThreads, kSmem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_dependent(k_kv_join_many<DH>, dim3((unsigned)ctas, kRows / kJoinRows), 32 * kJoinRows, 0, s, p);
+  return launch_dependent(k_kv_join_many<DH>, dim3((unsigned)ctas, kRows / (kJoinRows * kJoinWarps)), 32 * kJoinWarps, 0, s, p);
 }
 
 }  // namespace
