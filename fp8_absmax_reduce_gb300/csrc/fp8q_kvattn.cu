@@ -230,19 +230,18 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
     const int my_keys = kg * C::GK + rw * 32;  // within a block
     const int page_mask = (1 << p.kv.page_shift) - 1;
     const uint32_t ring = smem_addr(smem) + (uint32_t)(kg * C::GK * DH);
-    // Lane k: the page of keys 16 (k % 2) .. of this warp's part; -1 where it is none, or behind the limit.
-    auto page_of = [&](int b) {
-      const int key = b * kBlockKeys + my_keys + 16 * (lane & 1);
-      if (b >= stop || key >= klim) return -1;
-      const int id = table[key >> p.kv.page_shift];
+    // Lane k: the page of keys 16 (k % 2) .. of this warp's part of block b, and lanes 0 .. 3 its scales (K of both, V of both).  Read
+    // a step before they are looked at: a load under a condition, or looked at at once, holds the warp for its latency.
+    auto seen = [&](int b) { return b < stop && b * kBlockKeys + my_keys + 16 * (lane & 1) < klim; };
+    auto read_page = [&](int b) { return table[seen(b) ? (b * kBlockKeys + my_keys + 16 * (lane & 1)) >> p.kv.page_shift : 0]; };
+    auto page_of = [&](int b, int id) {  // -1: none, or behind the limit
+      if (!seen(b)) return -1;
       if (id >= 0 && id < p.kv.n_pages) return id;
       atomicOr(p.kv.status, kStatusBadCache);
       return -1;
     };
-    auto scale_of = [&](int id) {  // lanes 0 .. 3: K of both, V of both
-      if (id < 0 || lane >= 4) return kNoPage;
-      return (int)(lane & 2 ? p.kv.v_scale : p.kv.k_scale)[(int64_t)id * p.kv.hkv + h] - 127;
-    };
+    const uint8_t* scale_base = (lane & 2 ? p.kv.v_scale : p.kv.k_scale) + h;
+    auto read_scale = [&](int id) { return (int)scale_base[(int64_t)max(id, 0) * p.kv.hkv]; };
     auto copy_tile = [&](int b, int id_lane, int sc, int stage) {
       const int key = b * kBlockKeys + my_keys;
       const uint32_t to = ring + (uint32_t)(stage * 2 * C::kTile);
@@ -273,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
           }
         }
       }
-      if (lane < 4) scales[stage][warp][lane] = sc;
+      if (lane < 4) scales[stage][warp][lane] = id_lane < 0 ? kNoPage : sc - 127;
     };
     auto group_sync = [&]() {
       if (RW == 1) __syncwarp();
@@ -282,26 +281,28 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
 
     // The chain that a segment begins with is a page's number, then its keys (and its scales, which are stored after
     // the copies are on their way); q is fetched beside it and made ready while the first keys arrive.
-    int id_a = page_of(b0), id_b = page_of(b0 + 1);
+    int id_a = read_page(b0), id_b = read_page(b0 + 1);
     uint32_t qw[NT][DH / 8];  // row 8 n + lane / 4, elements c DH / 4 ..
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int r = rw * C::RT + 8 * n + g8, tok = (r0 + r) / G;
+      // a row that does not exist reads the unit's first
+      const int r = rw * C::RT + 8 * n + g8, pair = r0 + (r < n_rows ? r : 0), tok = pair / G;
       const uint16_t* src = p.qkv + (int64_t)(q.first + tok) * (p.n_heads + 2 * p.kv.hkv) * DH +
-                            (int64_t)(h * G + (r0 + r) - tok * G) * DH + c * (DH / 4);
+                            (int64_t)(h * G + pair - tok * G) * DH + c * (DH / 4);
 #pragma unroll
       for (int i = 0; i < DH / 32; ++i) {
-        const uint4 v = r < n_rows ? ld_nc_v4(src + 8 * i) : make_uint4(0, 0, 0, 0);
+        const uint4 v = ld_nc_v4(src + 8 * i);
         qw[n][4 * i] = v.x; qw[n][4 * i + 1] = v.y; qw[n][4 * i + 2] = v.z; qw[n][4 * i + 3] = v.w;
       }
     }
-    int sc_a = scale_of(id_a);
+    id_a = page_of(b0, id_a);
+    int sc_a = read_scale(id_a);
     auto next = [&](int b) {  // copies block b's keys; a step ahead its successor's scales, two ahead the pages
       if (b < stop) copy_tile(b, id_a, sc_a, (b - b0) & 1);
       copies_commit();
-      id_a = id_b;
-      sc_a = scale_of(id_a);
-      id_b = page_of(b + 2);
+      id_a = page_of(b + 1, id_b);
+      sc_a = read_scale(id_a);
+      id_b = read_page(b + 2);
     };
     next(b0);
     uint32_t qb[NT][DH / 16][2];
