@@ -103,6 +103,7 @@ def _load() -> ctypes.CDLL:
     L.attention_cached_workspace_size.restype = sz
     L.attention_cached_workspace_size.argtypes = [cache_p, i64, i64, i32]
     L.attention_cached.argtypes = [cache_p, vp, i64, i64, vp, vp, vp, i64, i32, vp, vp, vp, sz, vp]
+    L.fp8q_selftest_attention_cached_wait_limit.argtypes = L.attention_cached.argtypes[:-1] + [i64, vp]
     L.fp8q_trace_start.argtypes = [i32]
     L.fp8q_trace_read.argtypes = [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int), i32]
     L.fp8q_kernel_name.restype = ctypes.c_char_p
@@ -688,6 +689,7 @@ class KvCache:
     v_scale: torch.Tensor
     fmt: int = E4M3
     _struct: object = dataclasses.field(init=False, repr=False, compare=False)
+    _last: list = dataclasses.field(init=False, repr=False, compare=False)  # ((T, n_seqs, n_heads), workspace bytes)
 
     def __post_init__(self):
         if not isinstance(self.k, torch.Tensor) or self.k.ndim != 4:
@@ -704,6 +706,7 @@ class KvCache:
         if not 1 <= n < 1 << 31 or not 1 <= h <= 1024:
             raise ValueError(f"{n} pages of {h} heads")
         object.__setattr__(self, "_struct", FP8QKvCache(n, p, h, d, self.fmt))
+        object.__setattr__(self, "_last", [(None, 0)])
 
     def __reduce__(self):  # copies and pickles make their own structure
         return KvCache, (self.k, self.v, self.k_scale, self.v_scale, self.fmt)
@@ -794,11 +797,7 @@ def attention_cached_workspace_size(cache: KvCache, T: int, n_seqs: int, n_heads
     return lib.attention_cached_workspace_size(cache._struct, T, n_seqs, n_heads)
 
 
-def attention_cached(cache: KvCache, qkv: torch.Tensor, pages: torch.Tensor, lens: torch.Tensor, n_heads: int,
-                     row_start: torch.Tensor | None = None, att=None, lse=None, ws=None, stream=None):
-    """Causal grouped-query attention of the q heads of qkv [T, (n_heads + 2 n_kv_heads) head_dim] (bf16) over the cache,
-    each row seeing its sequence's tokens up to its own (append them first); pages, lens, row_start as kv_cache_append.
-    Returns (att [T, n_heads head_dim] bf16, lse [n_heads, T] fp32); rows behind the last sequence are not written."""
+def _attention_cached(name, fn, cache, qkv, pages, lens, n_heads, row_start, att, lse, ws, stream, *limit):
     (T, width), dev = _matrix("qkv", qkv, _HEAD)
     device = qkv.device
     if width != (n_heads + 2 * cache.n_kv_heads) * cache.head_dim:
@@ -806,12 +805,34 @@ def attention_cached(cache: KvCache, qkv: torch.Tensor, pages: torch.Tensor, len
     c, n, max_pages, start = _kv_call(cache, pages, lens, row_start, dev)
     att = _out("att", att, torch.bfloat16, (T, n_heads * cache.head_dim), dev, device, stream)
     lse = _out("lse", lse, torch.float32, (n_heads, T), dev, device, stream)
-    nb = lib.attention_cached_workspace_size(c, T, n, n_heads)
+    # the size of the last call's workspace: a program's next call is mostly of the same sizes
+    last = cache._last[0]
+    if last[0] == (T, n, n_heads):
+        nb = last[1]
+    else:
+        nb = lib.attention_cached_workspace_size(c, T, n, n_heads)
+        cache._last[0] = ((T, n, n_heads), nb)
     w = _scratch(nb, dev, device, ws, stream)
-    _check("attention_cached",
-           lib.attention_cached(c, pages.data_ptr(), n, max_pages, lens.data_ptr(), start, qkv.data_ptr(), T, n_heads,
-                                att.data_ptr(), lse.data_ptr(), w.data_ptr(), nb, _raw_stream(stream, dev)))
+    _check(name, fn(c, pages.data_ptr(), n, max_pages, lens.data_ptr(), start, qkv.data_ptr(), T, n_heads, att.data_ptr(),
+                    lse.data_ptr(), w.data_ptr(), nb, *limit, _raw_stream(stream, dev)))
     return att, lse
+
+
+def attention_cached(cache: KvCache, qkv: torch.Tensor, pages: torch.Tensor, lens: torch.Tensor, n_heads: int,
+                     row_start: torch.Tensor | None = None, att=None, lse=None, ws=None, stream=None):
+    """Causal grouped-query attention of the q heads of qkv [T, (n_heads + 2 n_kv_heads) head_dim] (bf16) over the cache,
+    each row seeing its sequence's tokens up to its own (append them first); pages, lens, row_start as kv_cache_append.
+    Returns (att [T, n_heads head_dim] bf16, lse [n_heads, T] fp32); rows behind the last sequence are not written."""
+    return _attention_cached("attention_cached", lib.attention_cached, cache, qkv, pages, lens, n_heads, row_start, att, lse, ws,
+                             stream)
+
+
+def selftest_attention_cached_wait_limit(cache: KvCache, qkv: torch.Tensor, pages: torch.Tensor, lens: torch.Tensor,
+                                         n_heads: int, limit_s: float, row_start=None, stream=None):
+    """attention_cached with the pipeline waits of its kernel for many rows limited to limit_s
+    (fp8q_selftest_attention_cached_wait_limit in include/fp8q.h).  Returns (att, lse), incomplete on a time-out."""
+    return _attention_cached("fp8q_selftest_attention_cached_wait_limit", lib.fp8q_selftest_attention_cached_wait_limit, cache, qkv,
+                             pages, lens, n_heads, row_start, None, None, None, stream, max(1, int(limit_s * 1e9)))
 
 
 # ---------------------------------------------------------------------------

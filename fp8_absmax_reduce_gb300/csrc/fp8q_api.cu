@@ -1578,9 +1578,10 @@ size_t attention_cached_workspace_size(const fp8q_kv_cache* cache, int64_t T, in
   return round256(kv_attend_workspace_bytes(T, (int)n_seqs, n_heads, cache->n_kv_heads, cache->head_dim));
 }
 
-int attention_cached(const fp8q_kv_cache* cache, const int32_t* pages, int64_t n_seqs, int64_t max_pages,
-                     const int32_t* lens, const int32_t* row_start, const void* qkv, int64_t T, int n_heads, void* att,
-                     float* lse, void* ws, size_t ws_bytes, fp8q_stream stream) {
+namespace {
+int attention_cached_run(const fp8q_kv_cache* cache, const int32_t* pages, int64_t n_seqs, int64_t max_pages, const int32_t* lens,
+                         const int32_t* row_start, const void* qkv, int64_t T, int n_heads, void* att, float* lse, void* ws,
+                         size_t ws_bytes, fp8q_stream stream, uint64_t wait_ns) {
   KvArgs a;
   int e = kv_args(&a, cache, pages, n_seqs, max_pages, lens, row_start, T);
   if (e) return e;
@@ -1590,9 +1591,27 @@ int attention_cached(const fp8q_kv_cache* cache, const int32_t* pages, int64_t n
   Ctx c;
   if ((e = make_ctx(&c, stream))) return e;
   a.status = c.L.status;
+  c.L.wait_ns = wait_ns;
   FP8Q_STEP(kKKvAttend, launch_kv_attend(a, static_cast<const uint16_t*>(qkv), n_heads, static_cast<uint16_t*>(att), lse, ws,
                                          c.L));
   return finish(c);
+}
+}  // namespace
+
+int attention_cached(const fp8q_kv_cache* cache, const int32_t* pages, int64_t n_seqs, int64_t max_pages,
+                     const int32_t* lens, const int32_t* row_start, const void* qkv, int64_t T, int n_heads, void* att,
+                     float* lse, void* ws, size_t ws_bytes, fp8q_stream stream) {
+  return attention_cached_run(cache, pages, n_seqs, max_pages, lens, row_start, qkv, T, n_heads, att, lse, ws, ws_bytes, stream, 0);
+}
+
+int fp8q_selftest_attention_cached_wait_limit(const fp8q_kv_cache* cache, const int32_t* pages, int64_t n_seqs,
+                                              int64_t max_pages, const int32_t* lens, const int32_t* row_start, const void* qkv,
+                                              int64_t T, int n_heads, void* att, float* lse, void* ws, size_t ws_bytes,
+                                              int64_t limit_ns, fp8q_stream stream) {
+  if (limit_ns < 1 || limit_ns > 10000000000ll || !cache) return FP8Q_ERR_INVALID_ARG;
+  if (cache->fmt != FP8Q_E4M3 || cache->head_dim != 128) return FP8Q_ERR_UNSUPPORTED;
+  return attention_cached_run(cache, pages, n_seqs, max_pages, lens, row_start, qkv, T, n_heads, att, lse, ws, ws_bytes, stream,
+                              (uint64_t)limit_ns);
 }
 
 // ---------------------------------------------------------------------------

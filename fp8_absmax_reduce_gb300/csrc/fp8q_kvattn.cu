@@ -695,7 +695,7 @@ cudaError_t launch_kv_attend(const KvArgs& a, const uint16_t* qkv, int n_heads, 
   const Pieces w = pieces(r, a.dh);
   uint8_t* b = static_cast<uint8_t*>(ws);
   AttendArgs p{a, qkv, n_heads, kLog2e / sqrtf((float)a.dh), att, lse, reinterpret_cast<float*>(b),
-               reinterpret_cast<float*>(b + w.lse), reinterpret_cast<Cut*>(b + w.cuts)};
+               reinterpret_cast<float*>(b + w.lse), reinterpret_cast<Cut*>(b + w.cuts), L.wait_ns};
   // rows of a unit at most, where the host knows them
   const int64_t pairs = a.row_start ? (int64_t)1 << 20 : (int64_t)a.rows * (n_heads / a.hkv);
   const cudaError_t e = r.many() ? launch_kv_attend_many(p, min(r.ctas(), L.num_sms), L.stream)

@@ -36,6 +36,7 @@ struct AttendArgs {
   float* part_o;     // [2 per CTA][R][DH]
   float* part_lse;   // [2 per CTA][R], log2
   Cut* cuts;         // [CTAs]
+  uint64_t wait_ns;  // limit of the waits of the kernel for many rows (0: 2 s)
 };
 
 __device__ __forceinline__ float ex2(float x) {

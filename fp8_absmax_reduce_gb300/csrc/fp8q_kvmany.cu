@@ -37,8 +37,9 @@ constexpr int kBars = kCodes + kTile;
 constexpr int kMisc = kBars + 256;
 constexpr float kOffset = 11.0f, kSlack = 4.0f;
 constexpr int kAll = 0x7FFFFFFF;
-// What a unit costs besides its keys, in blocks: q, the first pages, the results.
-constexpr int kUnitCost = 2;
+// What a unit costs besides its keys, in blocks: q, the first pages, the results.  (2 x 512 tokens of 40 heads over 8192: 207, 200, 194,
+// 194 and 192 us with 2, 4, 7, 10 and 14; 16 x 16 over 4096: 91, 82, 79, 78, 85.)
+constexpr int kUnitCost = 7;
 
 // A block's scales as the rows need them, 16 keys each: 2^X of K; kOffset + dx and 2^-dx of V, dx its exponent over the segment's largest.
 struct BlockScales {
@@ -84,8 +85,14 @@ __device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint32_t b, b
               (accumulate || i) ? 1u : 0u);
   }
 }
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort)) != 0;
+// SHORT: the self-test's waits, which poll and give up after limit_ns (a kernel of its own: the choice at every wait cost a tenth).
+template <bool SHORT>
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  return SHORT ? mbar_poll(bar, parity, abort, limit_ns) : mbar_wait(bar, parity, abort);
+}
+template <bool SHORT>
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  return __all_sync(0xFFFFFFFFu, wait<SHORT>(bar, parity, abort, limit_ns)) != 0;
 }
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
@@ -190,7 +197,7 @@ struct Walk {
   }
 };
 
-template <int FMT, int DH>
+template <int FMT, int DH, bool SHORT>
 __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_constant__ AttendArgs p) {
   constexpr int N = DH == 64 ? 64 : 128;  // columns of V's tile and of O: 96 are filled up with zeros
   extern __shared__ uint8_t smem_raw[];
@@ -369,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       const int n = max(w.blocks_of(0), w.blocks_of(1));
       for (int b = 0; b < n; ++b, ++tile) {
         const uint32_t par = (uint32_t)tile & 1u;
-        if (!warp_wait(empty, par ^ 1u, abort_flag) || !warp_wait(&code_full[is_v], par, abort_flag)) { ok = false; break; }
+        if (!warp_wait<SHORT>(empty, par ^ 1u, abort_flag, p.wait_ns) || !warp_wait<SHORT>(&code_full[is_v], par, abort_flag, p.wait_ns)) { ok = false; break; }
         convert(threads, lt, sbase + (is_v ? kV : kK), sbase + kCodes + is_v * kAtom, is_v, misc.keys[tile & 3]);
         mbar_arrive(&code_free[is_v]);
         fence_async_shared();
@@ -439,12 +446,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
         const uint32_t par = (uint32_t)tile & 1u;
         const unsigned have = __ballot_sync(0xFFFFFFFFu, here >= 0) & 0xFFu;
         // K's codes of the block before have been read
-        if (!warp_wait(&code_free[0], par ^ 1u, abort_flag)) { ok = false; break; }
+        if (!warp_wait<SHORT>(&code_free[0], par ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
         if (lane == 0) misc.keys[tile & 3] = BlockKeys{min(kBlockKeys, klim - b * kBlockKeys), (int)have, (b + 1) * kBlockKeys > first};
         __syncwarp();
         fetch(0, b, here, have);
         // V's too, whose tile was written when P V of the one before it was done: that one's scales have been read
-        if (!warp_wait(&code_free[1], par ^ 1u, abort_flag)) { ok = false; break; }
+        if (!warp_wait<SHORT>(&code_free[1], par ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
         fetch(1, b, here, have);
         BlockScales& sc = misc.scales[par];
         if (lane < 8) {
@@ -468,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       *abort_flag = 1;
       int never = 0;  // the copies in flight, before the memory is given back
       for (int i = 0; i < 2; ++i)
-        if (fetched[i]) warp_wait(&code_full[i], (fetched[i] - 1) & 1u, &never);
+        if (fetched[i]) warp_wait<false>(&code_full[i], (fetched[i] - 1) & 1u, &never, 0);
     }
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
@@ -480,22 +487,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
         if (n == 0) continue;
         for (int side = 0; side < 2 && ok; ++side)
           if (nx[side]) {
-            ok = mbar_wait(&q_full[side], nq[side] & 1u, abort_flag);
+            ok = wait<SHORT>(&q_full[side], nq[side] & 1u, abort_flag, p.wait_ns);
             ++nq[side];
           }
         for (int b = 0; b <= n && ok; ++b) {
-          if (b < n && !mbar_wait(k_full, (uint32_t)(tile + b) & 1u, abort_flag)) { ok = false; break; }
+          if (b < n && !wait<SHORT>(k_full, (uint32_t)(tile + b) & 1u, abort_flag, p.wait_ns)) { ok = false; break; }
           for (int side = 0; side < 2; ++side) {
             if (b < nx[side]) {
-              if (!mbar_wait(&s_free[side], ((ns[side] + (uint32_t)b) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+              if (!wait<SHORT>(&s_free[side], ((ns[side] + (uint32_t)b) & 1u) ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
               tc_fence_after();
               mma_scores<DH>(tmem + side * 128, sbase + kQ + side * kTile, sbase + kK);
               umma_commit(&s_full[side]);
             }
             if (side == 1 && b < n) umma_commit(k_empty);
             if (b > 0 && b - 1 < nx[side]) {
-              if (!mbar_wait(v_full, (uint32_t)(tile + b - 1) & 1u, abort_flag) ||
-                  !mbar_wait(&p_full[side], (ns[side] + (uint32_t)(b - 1)) & 1u, abort_flag)) { ok = false; break; }
+              if (!wait<SHORT>(v_full, (uint32_t)(tile + b - 1) & 1u, abort_flag, p.wait_ns) ||
+                  !wait<SHORT>(&p_full[side], (ns[side] + (uint32_t)(b - 1)) & 1u, abort_flag, p.wait_ns)) { ok = false; break; }
               tc_fence_after();
               mma_values<N>(tmem + 256 + side * 128, sbase + kP + side * kTile, sbase + kV, b > 1);
               umma_commit(&p_free[side]);
@@ -535,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       if (nx) {
         // q over a power of two of its row, as fp16: a warp takes its 32 rows a few at a time, 16 bytes a lane (a thread that read its own
         // row took 15000 cycles for it).  A row that does not exist reads the unit's first.
-        constexpr int kLanes = DH == 64 ? 8 : 16, kStep = 32 / kLanes, kBatch = 4;
+        constexpr int kLanes = DH == 64 ? 8 : 16, kStep = 32 / kLanes, kBatch = 8;
         const int sub = lane / kLanes, col = lane % kLanes;
         int ex = -110;
 #pragma unroll 1
@@ -569,8 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
 
         for (int b = 0; b < nx && ok; ++b, ++done) {
           const int kpar = (tile + b) & 1;
-          if (!warp_wait(&s_full[side], done & 1u, abort_flag)) { ok = false; break; }
-          if (!warp_wait(&sc_full[kpar], (uint32_t)((tile + b) >> 1) & 1u, abort_flag)) { ok = false; break; }
+          if (!warp_wait<SHORT>(&s_full[side], done & 1u, abort_flag, p.wait_ns)) { ok = false; break; }
+          if (!warp_wait<SHORT>(&sc_full[kpar], (uint32_t)((tile + b) >> 1) & 1u, abort_flag, p.wait_ns)) { ok = false; break; }
           tc_fence_after();
           const BlockScales& sc = misc.scales[kpar];
           xref = misc.xref[seg & 3];
@@ -599,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
             }
           }
           // P V of the block before has read P, and O holds every product up to it
-          if (!warp_wait(&p_free[side], (done & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+          if (!warp_wait<SHORT>(&p_free[side], (done & 1u) ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
           tc_fence_after();
           if (__any_sync(0xFFFFFFFFu, mx > m + kSlack)) {
             const float mn = fmaxf(m, mx), alpha = mn == m ? 1.0f : ex2(m - mn);
@@ -656,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
           mbar_arrive(&p_full[side]);
         }
         // the last product
-        if (ok && !warp_wait(&p_free[side], (done & 1u) ^ 1u, abort_flag)) ok = false;
+        if (ok && !warp_wait<SHORT>(&p_free[side], (done & 1u) ^ 1u, abort_flag, p.wait_ns)) ok = false;
         if (!ok) break;
         tc_fence_after();
       }
@@ -792,12 +799,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join_many(const AttendAr
   }
 }
 
-template <int FMT, int DH>
+template <int FMT, int DH, bool SHORT = false>
 cudaError_t launch(const AttendArgs& p, int ctas, cudaStream_t s) {
   static std::atomic<uint64_t> configured{0};
-  cudaError_t e = kv_smem(k_kv_attend_many<FMT, DH>, kSmem, configured);
+  cudaError_t e = kv_smem(k_kv_attend_many<FMT, DH, SHORT>, kSmem, configured);
   if (e != cudaSuccess) return e;
-  k_kv_attend_many<FMT, DH><<<ctas, kThreads, kSmem, s>>>(p);
+  k_kv_attend_many<FMT, DH, SHORT><<<ctas, kThreads, kSmem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_dependent(k_kv_join_many<DH>, dim3((unsigned)ctas, kRows / (kJoinRows * kJoinWarps)), 32 * kJoinWarps, 0, s, p);
 }
@@ -807,6 +814,7 @@ cudaError_t launch(const AttendArgs& p, int ctas, cudaStream_t s) {
 int kv_attend_many_rows() { return kRows; }
 
 cudaError_t launch_kv_attend_many(const AttendArgs& p, int ctas, cudaStream_t s) {
+  if (p.wait_ns && p.kv.fmt == 0 && p.kv.dh == 128) return launch<0, 128, true>(p, ctas, s);
   if (p.kv.fmt)
     return p.kv.dh == 128 ? launch<1, 128>(p, ctas, s) : p.kv.dh == 96 ? launch<1, 96>(p, ctas, s) : launch<1, 64>(p, ctas, s);
   return p.kv.dh == 128 ? launch<0, 128>(p, ctas, s) : p.kv.dh == 96 ? launch<0, 96>(p, ctas, s) : launch<0, 64>(p, ctas, s);

@@ -719,6 +719,17 @@ FP8Q_API int fp8q_selftest_linear_cross_entropy_wait_limit(int backward, const v
                                                            float* lse, void* dX, void* dW, fp8q_dtype dw_dtype, void* ws,
                                                            size_t ws_bytes, int64_t limit_ns, fp8q_stream stream);
 
+/* Diagnostics for the abort sequence of attention_cached's kernel for many rows (no page counterpart): attention_cached,
+ * except that, where a sequence has more than 64 (row, query head) pairs of a K/V head on average, the waits of its pipeline poll
+ * and give up after limit_ns (1 ns .. 10 s) instead of 2 s.  E4M3 and head_dim 128 only (else FP8Q_ERR_UNSUPPORTED).  With a limit of nanoseconds ordinary waits run out: the CTA records
+ * FP8Q_STATUS_TIMEOUT, stops issuing, waits (with the full 2 s limit) for its products and copies, frees its tensor memory
+ * and exits; att and lse are then incomplete and the context stays usable.  Returns FP8Q_OK once enqueued (synchronous
+ * errors as attention_cached). */
+FP8Q_API int fp8q_selftest_attention_cached_wait_limit(const fp8q_kv_cache* cache, const int32_t* pages, int64_t n_seqs,
+                                                       int64_t max_pages, const int32_t* lens, const int32_t* row_start,
+                                                       const void* qkv, int64_t T, int n_heads, void* att, float* lse,
+                                                       void* ws, size_t ws_bytes, int64_t limit_ns, fp8q_stream stream);
+
 /* Kernel-level timing for benchmarks.  While tracing is on for the calling
  * host thread, each kernel step the library enqueues is bracketed by two CUDA
  * events recorded on the stream it is launched on (host-side CUDA objects; no

@@ -581,3 +581,108 @@ def test_a_sequence_run_token_by_token():
         got = fq.attention_cached(w.cache, t, i32(w.pages), lens, hq)
         w.check_attention(*got, x[:, :hq])
     w.check_cache()
+
+
+@pytest.mark.parametrize("lens,rows", [([900, 300], 100), ([2000] * 40, 40)])
+def test_waits_that_run_out_end_the_call_and_nothing_else(lens, rows):
+    """Every wait of the kernel for many rows gives up at once: the status says so, the call returns, and the next call is right."""
+    w = World(0, 128, 64, 4, 2, lens, rows=rows, seed=40)
+    w.fill()
+    t, x = w.append()
+    want = fq.attention_cached(w.cache, t, *w.args(), 4)
+    torch.cuda.synchronize()
+    fq.get_status(clear=True)
+    for _ in range(3):
+        fq.selftest_attention_cached_wait_limit(w.cache, t, *w.args(), 4, 1e-9)
+        torch.cuda.synchronize()
+        assert fq.get_status(clear=True) == fq.STATUS_TIMEOUT
+    got = fq.attention_cached(w.cache, t, *w.args(), 4)
+    torch.cuda.synchronize()
+    assert fq.get_status() == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def _on_a_stream():
+    w = World(0, 128, 64, 8, 2, [130, 64, 1], rows=1, seed=41)
+    w.fill()
+    t, _ = w.append()
+    m = World(0, 64, 32, 4, 1, [300, 90], rows=60, seed=42)
+    m.fill()
+    s, _ = m.append()
+    args, margs = w.args(), m.args()
+    return {"attention_cached": (lambda **k: fq.attention_cached(w.cache, t, *args, 8, **k), fq.attention_cached_workspace_size(w.cache, 3, 3, 8)),
+            "attention_cached_many": (lambda **k: fq.attention_cached(m.cache, s, *margs, 4, **k), fq.attention_cached_workspace_size(m.cache, 120, 2, 4)),
+            "kv_cache_read": (lambda **k: (fq.kv_cache_read(m.cache, *margs, 120, **k),), 0)}
+
+
+@pytest.mark.parametrize("name", ["attention_cached", "attention_cached_many", "kv_cache_read"])
+def test_memory_of_calls_on_another_stream(name):
+    """What a call allocates on a busy stream is that stream's: neither its workspace nor its outputs are handed out meanwhile."""
+    call, ws = _on_a_stream()[name]
+    want = [t.clone() for t in call()]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    out = call(stream=s)
+    junk = [torch.full((max(ws, 1),), 0xA5, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(bool((j == 0xA5).all()) for j in junk) and all(torch.equal(a, b) for a, b in zip(out, want))
+    torch.cuda.current_stream().wait_stream(s)
+    out = call(stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda._sleep(20_000_000)
+    copies, sizes = [t.clone() for t in out], [t.nbytes for t in out]
+    del out
+    with torch.cuda.stream(s):
+        junk = [torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda") for n in sizes]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(copies, want)) and len(junk) == len(want)
+
+
+def test_appends_on_another_stream_and_captured():
+    """kv_cache_append with stream=, and replayed from a graph over a length that the program moves on."""
+    w = World(0, 64, 16, 2, 1, [20, 33], rows=1, seed=43)
+    w.fill()
+    lens = i32([19, 32])
+    t = torch.zeros((2, 4 * 64), device="cuda").bfloat16()
+    pages = i32(w.pages)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        lens += 1
+        fq.kv_cache_append(w.cache, t, pages, lens, 2)
+    w.lens = [20, 33]
+    v, x = w.qkv()
+    t.copy_(v)
+    lens.copy_(i32([19, 32]))
+    torch.cuda.synchronize()
+    graph.replay()
+    ref.append(w.ref, 0, 16, w.pages, w.lens, w.rows, x[:, 2:].reshape(-1, 2, 1, 64))
+    w.check_cache()
+    v, x = w.qkv()  # the same tokens again, larger: the scales grow
+    v *= 64
+    torch.cuda.synchronize()
+    fq.kv_cache_append(w.cache, v, pages, i32(w.lens), 2, stream=side)
+    side.synchronize()
+    ref.append(w.ref, 0, 16, w.pages, w.lens, w.rows, 64 * x[:, 2:].reshape(-1, 2, 1, 64))
+    w.check_cache()
+
+
+def test_launches_are_traced_and_counted():
+    import ctypes
+    w = World(0, 64, 16, 2, 1, [20], rows=1, seed=44)
+    w.fill()
+    t, _ = w.qkv()
+    assert fq.lib.fp8q_trace_start(16) == 0
+    counts = []
+    for call in (lambda: fq.kv_cache_append(w.cache, t, *w.args(), 2), lambda: fq.kv_cache_read(w.cache, *w.args(), 1),
+                 lambda: fq.attention_cached(w.cache, t, *w.args(), 2)):
+        call()
+        counts.append(fq.last_launch_count())
+    fq.lib.fp8q_trace_stop()
+    torch.cuda.synchronize()
+    ms, kinds = (ctypes.c_float * 16)(), (ctypes.c_int * 16)()
+    n = fq.lib.fp8q_trace_read(ms, kinds, 16)
+    assert [fq.lib.fp8q_kernel_name(kinds[k]).decode() for k in range(n)] == ["kv_append", "kv_read", "attn_cached"]
+    assert counts == [1, 1, 2] and all(ms[k] > 0 for k in range(n))

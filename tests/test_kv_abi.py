@@ -97,3 +97,13 @@ def test_cache_struct_matches_the_header(fq, tmp_path):
     subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(tmp_path / "layout")], check=True)
     got = subprocess.run([str(tmp_path / "layout")], check=True, capture_output=True, text=True).stdout.split()
     assert [int(v) for v in got] == [ctypes.sizeof(fq.FP8QKvCache)] + [getattr(fq.FP8QKvCache, n).offset for n in names]
+
+
+def test_wait_limit_is_validated(fq):
+    need = fq.lib.attention_cached_workspace_size(cache(fq), 4, 2, 4)
+
+    def call(limit, ws=FAKE, **kw):
+        return fq.lib.fp8q_selftest_attention_cached_wait_limit(cache(fq, **kw), FAKE, 2, 3, FAKE, None, FAKE, 4, 4, FAKE, FAKE, ws, need, limit, None)
+    for limit in (0, -1, 10 ** 10 + 1):
+        assert call(limit) == INVALID
+    assert call(1, ws=None) == WORKSPACE and call(1, fmt=1) == UNSUPPORTED and call(1, head_dim=64) == UNSUPPORTED
