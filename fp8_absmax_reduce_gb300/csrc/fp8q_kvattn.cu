@@ -564,12 +564,12 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
   }
 }
 
-// Block (j, r): row r of the unit that CTA j began and did not end.  Its parts in order: CTA j's last, then the first of
-// those after it; a warp takes every eighth, eight at a time in flight.
+// Block (j, r): row r of the unit that CTA j began and did not end.  Its parts: CTA j's last, then the first of those after it; a warp
+// takes every eighth, eight at a time in flight, and the warps' sums are added in order.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 template <int DH, int R>
 __global__ void __launch_bounds__(kJoinThreads) k_kv_join(const AttendArgs p) {
-  __shared__ float weight[kMaxCtas + 8 * kJoinWarps], acc_s[kJoinWarps][DH], max_s[kJoinWarps], sum_s[kJoinWarps];
+  __shared__ float acc_s[kJoinWarps][DH], max_s[kJoinWarps], sum_s[kJoinWarps];
   wait_for_previous();
   const int j = blockIdx.x, r = blockIdx.y, t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const Cut cut = p.cuts[j];
@@ -577,59 +577,59 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_join(const AttendArgs p) {
   // the last CTA of the unit is the last whose part of the line begins before the unit's end: total i / ctas < end
   const int n = (int)((cut.end * cut.ctas + cut.total - 1) / cut.total) - j;
   auto slot = [&](int i) { return i == 0 ? 2 * j + 1 : 2 * (j + i); };
-  float M = -INFINITY;
-  for (int i = t; i < n; i += kJoinThreads) {
-    weight[i] = p.part_lse[slot(i) * R + r];
-    M = fmaxf(M, weight[i]);
-  }
-#pragma unroll
-  for (int k = 16; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, k));
-  if (lane == 0) max_s[warp] = M;
-  __syncthreads();
-  M = max_s[0];
-#pragma unroll
-  for (int k = 1; k < kJoinWarps; ++k) M = fmaxf(M, max_s[k]);
-  float acc[DH / 32], sum = 0.0f;
+  float acc[DH / 32], sum = 0.0f, M = -INFINITY;
 #pragma unroll
   for (int k = 0; k < DH / 32; ++k) acc[k] = 0.0f;
   for (int i0 = warp; i0 < n; i0 += 8 * kJoinWarps) {
-    float v[8][DH / 32], w[8];
+    float v[8][DH / 32], e[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int i = i0 + q * kJoinWarps;
-      const bool in = i < n;
-      const float e = in ? weight[i] : -INFINITY;
-      w[q] = e == -INFINITY ? 0.0f : ex2(e - M);
-      const float* src = p.part_o + ((int64_t)slot(in ? i : 0) * R + r) * DH + lane;
+    for (int q = 0; q < 8; ++q) {  // a part that does not exist is the warp's first, with no weight
+      const int i = i0 + q * kJoinWarps, s = slot(i < n ? i : i0);
+      e[q] = p.part_lse[s * R + r];
+      const float* src = p.part_o + ((int64_t)s * R + r) * DH + lane;
 #pragma unroll
-      for (int k = 0; k < DH / 32; ++k) v[q][k] = in ? src[32 * k] : 0.0f;
+      for (int k = 0; k < DH / 32; ++k) v[q][k] = src[32 * k];
+      if (i >= n) e[q] = -INFINITY;
     }
+    float mn = M;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) mn = fmaxf(mn, e[q]);
+    const float fade = mn == M ? 1.0f : ex2(M - mn);
+    sum *= fade;
+#pragma unroll
+    for (int k = 0; k < DH / 32; ++k) acc[k] *= fade;
+    M = mn;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      sum += w[q];
+      const float w = e[q] == -INFINITY ? 0.0f : ex2(e[q] - M);
+      sum += w;
 #pragma unroll
-      for (int k = 0; k < DH / 32; ++k) acc[k] += w[q] * v[q][k];
+      for (int k = 0; k < DH / 32; ++k) acc[k] += e[q] == -INFINITY ? 0.0f : w * v[q][k];
     }
   }
 #pragma unroll
   for (int k = 0; k < DH / 32; ++k) acc_s[warp][lane + 32 * k] = acc[k];
-  if (lane == 0) sum_s[warp] = sum;
-  __syncthreads();
-  const int G = p.n_heads / p.kv.hkv, tok = (cut.group_row + r) / G, hd = cut.head * G + (cut.group_row + r) - tok * G;
-  float total = 0.0f;
-#pragma unroll
-  for (int k = 0; k < kJoinWarps; ++k) total += sum_s[k];
-  if (t < DH / 2) {
-    float v[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      float a = 0.0f;
-#pragma unroll
-      for (int q = 0; q < kJoinWarps; ++q) a += acc_s[q][2 * t + k];
-      v[k] = total == 0.0f ? 0.0f : a / total;
-    }
-    *reinterpret_cast<uint32_t*>(p.att + ((int64_t)(cut.row0 + tok) * p.n_heads + hd) * DH + 2 * t) = pack_bf16x2(v[0], v[1]);
+  if (lane == 0) {
+    max_s[warp] = M;
+    sum_s[warp] = sum;
   }
+  __syncthreads();
+  if (t >= DH / 2) return;
+  M = max_s[0];
+#pragma unroll
+  for (int k = 1; k < kJoinWarps; ++k) M = fmaxf(M, max_s[k]);
+  float total = 0.0f, v[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int k = 0; k < kJoinWarps; ++k) {  // (a warp whose rows are NaN has no maximum, and its sum is NaN)
+    const float f = max_s[k] == M ? 1.0f : max_s[k] == -INFINITY ? (sum_s[k] == 0.0f ? 0.0f : 1.0f) : ex2(max_s[k] - M);
+    total += f * sum_s[k];
+    v[0] += f * acc_s[k][2 * t];
+    v[1] += f * acc_s[k][2 * t + 1];
+  }
+  const int G = p.n_heads / p.kv.hkv, tok = (cut.group_row + r) / G, hd = cut.head * G + (cut.group_row + r) - tok * G;
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  *reinterpret_cast<uint32_t*>(p.att + ((int64_t)(cut.row0 + tok) * p.n_heads + hd) * DH + 2 * t) =
+      total == 0.0f ? 0u : pack_bf16x2(v[0] * inv, v[1] * inv);
   if (t == 0) p.lse[(int64_t)hd * p.kv.T + cut.row0 + tok] = total == 0.0f ? -INFINITY : (M + log2f(total)) * kLn2;
 }
 
