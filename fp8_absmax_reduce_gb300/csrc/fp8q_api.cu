@@ -1532,7 +1532,7 @@ int kv_args(KvArgs* a, const fp8q_kv_cache* c, const int32_t* pages, int64_t n_s
   if (e) return e;
   if (!al16(c->k) || !al16(c->v) || !c->k_scale || !c->v_scale) return FP8Q_ERR_INVALID_ARG;
   if (!kv_sizes_ok(T, n_seqs)) return FP8Q_ERR_INVALID_ARG;
-  if (max_pages < 1 || max_pages > INT32_MAX / c->page_size) return FP8Q_ERR_INVALID_ARG;
+  if (max_pages < 1 || max_pages > ((int64_t)1 << 30) / c->page_size) return FP8Q_ERR_INVALID_ARG;
   if (!al4(pages) || !al4(lens) || (row_start && !al4(row_start))) return FP8Q_ERR_INVALID_ARG;
   if (!row_start && T % n_seqs) return FP8Q_ERR_INVALID_ARG;
   int shift = 4;

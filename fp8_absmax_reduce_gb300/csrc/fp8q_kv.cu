@@ -217,22 +217,25 @@ __global__ void __launch_bounds__(kReadThreads) k_kv_read(const KvArgs a, void* 
     const int64_t ph0 = (int64_t)id * a.hkv;
     const int slot = pos & (P - 1);
     uint4* out = reinterpret_cast<uint4*>(kv) + (int64_t)row * vecs;
+    if (id < 0) {  // padding, or no page
+      for (int i = lane; i < vecs; i += 32) out[i] = make_uint4(0, 0, 0, 0);
+      continue;
+    }
     for (int i0 = lane; i0 < vecs; i0 += 32 * kReads) {
       uint32_t w[kReads][N / 4];
       uint32_t x[kReads];
 #pragma unroll
-      for (int k = 0; k < kReads; ++k) {
-        const int i = i0 + 32 * k, e = i * N, head = e / DH, is_v = head >= a.hkv;
+      for (int k = 0; k < kReads; ++k) {  // (behind the row's end its last piece again, which is not written)
+        const int e = min(i0 + 32 * k, vecs - 1) * N, head = e / DH, is_v = head >= a.hkv;
         const int64_t ph = ph0 + head - is_v * a.hkv;
-        const bool in = i < vecs && id >= 0;
         const uint8_t* src = (is_v ? a.v : a.k) + ((ph << a.page_shift) + slot) * DH + e - head * DH;
-        x[k] = in ? (is_v ? a.v_scale : a.k_scale)[ph] : 127u;
+        x[k] = (is_v ? a.v_scale : a.k_scale)[ph];
         if (N == 8) {
-          const uint2 u = in ? *reinterpret_cast<const uint2*>(src) : make_uint2(0, 0);
+          const uint2 u = *reinterpret_cast<const uint2*>(src);
           w[k][0] = u.x;
           w[k][N / 4 - 1] = u.y;
         } else {
-          w[k][0] = in ? *reinterpret_cast<const uint32_t*>(src) : 0u;
+          w[k][0] = *reinterpret_cast<const uint32_t*>(src);
         }
       }
 #pragma unroll

@@ -562,7 +562,7 @@ typedef struct fp8q_kv_cache {
  * [0, T] (taken as none) and a page outside [0, n_pages) (its tokens are not written, read as zero and not attended to)
  * set FP8Q_STATUS_BAD_CACHE.  A row_start that decreases may go unreported, and leaves it open which sequence a row is taken
  * for.  No access leaves its tensor, whatever they hold.
- * Requirements: 1 <= T <= 2^28, 1 <= n_seqs <= 2^20, max_pages >= 1, max_pages page_size < 2^31, n_heads a multiple of n_kv_heads, at most 1024;
+ * Requirements: 1 <= T <= 2^28, 1 <= n_seqs <= 2^20, max_pages >= 1, max_pages page_size <= 2^30, n_heads a multiple of n_kv_heads, at most 1024;
  * k, v, qkv, kv and att 16-byte, pages, lens, row_start and lse 4-byte aligned; head_dim and page_size outside their lists are
  * FP8Q_ERR_UNSUPPORTED. */
 
@@ -587,8 +587,12 @@ FP8Q_API int kv_cache_read(const fp8q_kv_cache* cache, const int32_t* pages, int
  *   att [T, n_heads head_dim] bf16, lse [n_heads, T] fp32 as attention_fwd writes them; a row that sees nothing has att 0 and
  *   lse -Inf.
  * Scores, maxima, sums and accumulators are fp32; codes and q enter the tensor cores without loss (fp16, q over a power
- * of two of its row), the probabilities as fp16 relative to the row's maximum (2^-11 of each, at least 2^-39 of the
- * maximum).  Slots behind a sequence's last token may hold anything.  Deterministic.
+ * of two of its row: elements below 2^-28 of the row's largest lose bits).  The probabilities multiply V as fp16, relative to the row's
+ * maximum and to the page's scale of V over the largest of the sequence: 2^-11 of each while their product is above 2^-25 of
+ * the largest, and nothing is left of one below 2^-36.  The sum that divides is fp32 of the unrounded ones.
+ * Slots behind a sequence's last token may hold anything, and so may tokens that a row does not see.  att and lse must
+ * not overlap the inputs.  Deterministic.  A call is two launches; up to 64 (row, query head) pairs of a sequence and K/V
+ * head (T / n_seqs rows taken for each) take warp-level products, more take tensor memory.
  * Requirement besides those above: T n_heads < 2^31.  Workspace: attention_cached_workspace_size bytes (0 for sizes outside
  * the limits), 256-byte aligned. */
 FP8Q_API size_t attention_cached_workspace_size(const fp8q_kv_cache* cache, int64_t T, int64_t n_seqs, int n_heads);

@@ -53,7 +53,7 @@ def test_what_they_share_is_refused(fq):
                     dict(head_dim=256), dict(head_dim=0), dict(page_size=-64)):
             assert f(cache(fq, **bad)) == UNSUPPORTED, bad
         for bad in (dict(pages=None), dict(pages=ODD), dict(lens=None), dict(lens=ODD), dict(start=ODD), dict(n=0), dict(n=(1 << 20) + 1),
-                    dict(n=3), dict(most=0), dict(most=-1), dict(most=(1 << 31) // 64), dict(T=0), dict(T=(1 << 28) + 1), dict(T=-4)):
+                    dict(n=3), dict(most=0), dict(most=-1), dict(most=(1 << 30) // 64 + 1), dict(T=0), dict(T=(1 << 28) + 1), dict(T=-4)):
             assert f(cache(fq), **bad) == INVALID, bad
 
 
