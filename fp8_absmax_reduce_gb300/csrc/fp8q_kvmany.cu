@@ -55,7 +55,7 @@ struct BlockKeys {
 struct Misc {
   BlockScales scales[2];  // by block
   BlockKeys keys[4];      // by block
-  int xref[4];            // by segment: the largest exponent of V
+  int xref[4];            // by segment that has blocks: the largest exponent of V
   int odd;                // some V was NaN or infinite, and is 0 in its tile
   uint32_t tmem;
   int abort;
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
   w.base = line.base;
   w.at = begin;
   w.end = end;
-  int tile = 0, seg = 0;  // blocks and segments so far
+  int tile = 0, seg = 0;  // blocks so far, and segments that had some: what a role is ahead by in blocks bounds it in these, not in empty ones
   bool ok = true;
 
   // ---------------- codes to fp16: THREADS threads, `lt` this one's number ----------------
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
     uint32_t fetched[2] = {0, 0};  // blocks whose codes were asked for
     while (ok && w.next()) {
       const int n = max(w.blocks_of(0), w.blocks_of(1));
-      if (n == 0) { ++seg; continue; }
+      if (n == 0) continue;
       const int first = w.t.limit(w.r0), klim = w.t.limit(w.r0 + w.n_rows - 1), stop = w.b0 + n;
       const int32_t* table = p.kv.pages + (int64_t)w.s * p.kv.max_pages;
       const int mask = (1 << p.kv.page_shift) - 1, step = min(1 << p.kv.page_shift, kBlockKeys) >> 4;  // groups of 16 keys of a copy
@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
         p.cuts[j] = Cut{w.unit0, w.unit0 + w.cost, total, ctas, w.h, w.q.first, w.n_rows, w.r0};
       tc_fence_before();
       tile += n;
-      ++seg;
+      seg += n > 0;
     }
     if (!ok) {
       atomicOr(p.kv.status, kStatusTimeout);

@@ -97,7 +97,7 @@ class World:
             wrote = ~np.isnan(self.ref[n]).all(axis=(2, 3))
             assert np.array_equal(x.cpu().numpy().astype(int)[wrote] - 127, self.ref[n + "x"][wrote]), n
 
-    def check_attention(self, att, lse, q):
+    def check_attention(self, att, lse, q, below=0.0):
         torch.cuda.synchronize()
         want, size, wlse, mag = ref.attend(self.ref, self.P, self.pages, self.lens, self.rows, q)
         owned = ~np.isnan(wlse[0])
@@ -105,7 +105,7 @@ class World:
         got, glse = att.double().cpu().numpy().reshape(want.shape), lse.double().cpu().numpy()
         keys = max(1, max(self.lens))
         e = (self.dh + 16) * 2.0 ** -23 * mag.T[:, :, None]
-        tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * e + (keys + 16) * 2.0 ** -22) * size
+        tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * e + (keys + 16) * 2.0 ** -22) * size + below
         worst = np.max((np.abs(got - want) - tol)[owned])
         assert worst <= 0, f"att off by {worst} more than allowed"
         empty = np.isneginf(wlse)
@@ -280,6 +280,31 @@ def test_attention_of_many_rows_matches_its_definition(case, fmt):
     n = w.T if w.row_start is None else w.row_start[-1]
     assert torch.equal(first[0][:n], again[0][:n]) and torch.equal(first[1][:, :n], again[1][:, :n])
     assert fq.get_status() == 0
+
+
+@pytest.mark.parametrize("idle", [1, 2, 3, 7])
+def test_many_rows_with_idle_slots_between_sequences_of_different_sizes(idle):
+    """Sequences of one or two blocks, V 2^20 apart, with empty slots between them: a CTA has many of both."""
+    n = 1500
+    lens = [(200 if s % 8 else 120) if s % (idle + 1) == 0 else 0 for s in range(n)]
+    w = World(0, 64, 64, 9, 1, lens, rows=8, seed=40 + idle, wide=False)
+    before = [max(0, k - 8) for k in lens]
+    start = np.concatenate([[0], np.cumsum(before)]).tolist()
+    x = w.rng.standard_normal((start[-1], 2, 1, 64))
+    x[:, 1] *= np.repeat(np.exp2(w.rng.integers(-10, 11, n)), before)[:, None, None]
+    d = torch.tensor(x, dtype=torch.float32).cuda()
+    fq.kv_cache_append(w.cache, d.reshape(start[-1], -1), i32(w.pages), i32(before), 0, row_start=i32(start))
+    ref.append(w.ref, 0, 64, w.pages, before, ref.rows_of(n, start[-1], start), d.double().cpu().numpy())
+    t, x = w.append()
+    # A weight in a small page is p 2^dx 2^11 in fp16, dx the page's exponent below the sequence's largest page: where that is subnormal
+    # it is off by up to 2^-25, which multiplies a code of up to 448 in units of the largest page's 2^X <= 2 max |v| / 448.  A sum of
+    # weights is 1 at least, so an output is off by keys 2^-25 2^-11 2 max |v| besides.
+    below = np.zeros((w.T, 1, 1))
+    for s, (first, m) in enumerate(w.rows):
+        v, _ = ref.held(w.ref, 64, w.pages, s, lens[s], "v")
+        below[first:first + m] = lens[s] * 2.0 ** -35 * np.abs(v).max(initial=0.0)
+    att, lse = fq.attention_cached(w.cache, t, *w.args(), 9)
+    w.check_attention(att, lse, x[:, :9], below)
 
 
 def test_many_rows_see_values_that_are_not_finite_only_behind_them():
