@@ -24,7 +24,8 @@
 // Measured (both kernels, out of a graph, caches cold): 64 sequences of up to 8192 tokens, 40 + 8 heads of 128, 372 MB of cache: 70 us, 5.3
 // TB/s; 48 of 32768: 221 us, 6.3 TB/s; one of 250007, 28 + 4 heads: 54 us, 4.8 TB/s; 24 of 3000 with 6 rows each, 12 + 12 heads of 64: 21 us.
 // About 3 us go before the first byte of the cache arrives (the line, the pages), 3 to 4 for the second launch, a tenth for CTAs
-// that end before the last.  Inside, shared memory and the issue slots of the conversions are each some two thirds busy.
+// that end before the last.  Inside, with 12 warps an SM (their registers fill it) the
+// issue slots are 43 % taken and shared memory 25 %: what holds the rest is the latency of a warp's own chain of instructions.
 #include <atomic>
 
 #include "fp8q_kvline.cuh"
@@ -642,7 +643,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_join(const AttendArgs p) {
 
 // Rows of a CTA for the (token, head) pairs of a sequence and K/V head: 8 of one warp or 16; above, two or four warps share their keys
 // for 16 rows each; and from kManyPairs on the kernel on tensor memory.  (2 sequences of 8192, 16 of 4096 and 64 of 1000, 40 + 8 heads of
-// 128: 50 pairs 43, 82 and 100 us here and 50, 79, 129 there; 80 pairs 55, 140, 149 and 48, 93, 136.)
+// 128: 35 pairs 35, 74 and 83 us here and 40, 71, 102 there; 50 pairs 41, 78, 95 and 39, 63, 109; 80 pairs 55, 140, 149 and 40, 75, 110.)
 constexpr int kManyPairs = 65;
 struct Rows {
   int nt, rw;

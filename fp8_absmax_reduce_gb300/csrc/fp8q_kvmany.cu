@@ -8,9 +8,13 @@
 //   warp 5       pages, bulk copies of a block's codes of K and V into shared memory, and its scales, a block ahead;
 //   warps 0-3    K's codes into a swizzled fp16 tile (each block's first product waits for it);
 //   warps 6, 7   V's;
-//   warp 4       the products, one thread: S_A = Q_A K^T, O_A += P_A V of the block before, then B's;
+//   warp 4       the products, one thread: O_A += P_A V of the block before, S_A = Q_A K^T, then B's;
 //   warps 8-15   a row a thread (A, then B): q into shared memory; per block the row's maximum from S, P = 2^(s - m) as fp16
-//                into shared memory, and at the end O over the sum.
+//                over S in tensor memory, and at the end O over the sum.
+// S, P and O fill tensor memory, so a tile's S waits for its P V; meanwhile the other tile's rows work.  P in shared memory, and S a
+// block ahead, was slower (195 us against 185 for 2 x 512 tokens over 8192): shared memory carries the products' operands (Q and K alone
+// its full width while S is made), the codes and what is made of them.  That the next S may be issued on top of P right behind the
+// product that reads it rests on one thread's products of one CTA running in the order of issue.
 // P's window is that of the few rows' kernel: p 2^11 in fp16, the reference maximum moving when it is exceeded by 2^4.
 // The keys of all (sequence, row tile, K/V head) units are cut into equal parts, one a CTA, as there.
 //
@@ -31,14 +35,13 @@ constexpr int kTile = 2 * kAtom;   // a tile of 128 columns
 constexpr int kQ = 0;              // [2 tiles]
 constexpr int kK = kQ + 2 * kTile;
 constexpr int kV = kK + kTile;
-constexpr int kP = kV + kTile;         // [2 tiles]
-constexpr int kCodes = kP + 2 * kTile; // the next block's codes: K, V
+constexpr int kCodes = kV + kTile; // the next block's codes: K, V
 constexpr int kBars = kCodes + kTile;
 constexpr int kMisc = kBars + 256;
 constexpr float kOffset = 11.0f, kSlack = 4.0f;
 constexpr int kAll = 0x7FFFFFFF;
-// What a unit costs besides its keys, in blocks: q, the first pages, the results.  (2 x 512 tokens of 40 heads over 8192: 207, 200, 194,
-// 194 and 192 us with 2, 4, 7, 10 and 14; 16 x 16 over 4096: 91, 82, 79, 78, 85.)
+// What a unit costs besides its keys, in blocks: q, the first pages, the results.  (With P in shared memory, 2 x 512 tokens of 40 heads over 8192: 207,
+// 200, 194, 194 and 192 us with 2, 4, 7, 10 and 14; 16 x 16 over 4096: 91, 82, 79, 78, 85.)
 constexpr int kUnitCost = 7;
 
 // A block's scales as the rows need them, 16 keys each: 2^X of K; kOffset + dx and 2^-dx of V, dx its exponent over the segment's largest.
@@ -61,10 +64,19 @@ struct Misc {
   int abort;
 };
 constexpr int kSmem = kMisc + (int)sizeof(Misc) + 1024;
-static_assert(kSmem <= 232448 - 64, "shared memory per CTA");
+static_assert(kSmem <= 232448, "shared memory per CTA");
 
 __host__ __device__ constexpr uint32_t idesc_f16(int n, int b_mn) {
   return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+// D[tmem] (+)= A[tmem] B[shared], fp16 operands.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 // S = Q K^T over DH: both K-major tiles of 128 rows.
 template <int DH>
@@ -75,15 +87,12 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
     umma_bf16(d, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + off, 16, 1024), idesc_f16(128, 0), i ? 1u : 0u);
   }
 }
-// O (+)= P V over 128 keys: P K-major, V MN-major (a row a key), N = 64 or 128 columns.
+// O (+)= P V over 128 keys: P in tensor memory, over S, V MN-major (a row a key), N = 64 or 128 columns.
 template <int N>
 __device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t off = (uint32_t)((i >> 2) * kAtom + (i & 3) * 32);
-    umma_bf16(d, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + i * 2048, kAtom, 1024), idesc_f16(N, 1),
-              (accumulate || i) ? 1u : 0u);
-  }
+  for (int i = 0; i < 8; ++i)
+    umma_f16_ts(d, a + i * 8, smem_desc_sw128(b + i * 2048, kAtom, 1024), idesc_f16(N, 1), (accumulate || i) ? 1u : 0u);
 }
 // SHORT: the self-test's waits, which poll and give up after limit_ns (a kernel of its own: the choice at every wait cost a tenth).
 template <bool SHORT>
@@ -118,6 +127,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // A sequence's units: row tile by row tile, each for every K/V head.
 struct Tiles {
@@ -209,10 +227,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
   uint64_t* sc_full = bars + 4;   // [2] a block's scales (every other block's: a row may still read the one before)
   uint64_t* v_full = bars + 6;
   uint64_t* v_empty = bars + 7;   // both P V of the block are computed
-  uint64_t* s_full = bars + 8;    // [2] per tile
-  uint64_t* s_free = bars + 10;   // [2] the rows have read S
+  uint64_t* s_full = bars + 8;    // [2] per tile; O holds every product before it
+  uint64_t* o_full = bars + 10;   // [2] O is complete
   uint64_t* p_full = bars + 12;   // [2]
-  uint64_t* p_free = bars + 14;   // [2] P V has read P, and O holds every product so far
   uint64_t* drain = bars + 16;
   uint64_t* code_full = bars + 17;   // K's, V's codes of the next block
   uint64_t* code_free = bars + 19;   // [2] they have been read
@@ -272,9 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       mbar_init(&q_full[i], kTileRows);
       mbar_init(&sc_full[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], kTileRows);
+      mbar_init(&o_full[i], 1);
       mbar_init(&p_full[i], kTileRows);
-      mbar_init(&p_free[i], 1);
     }
     mbar_init(k_full, kKThreads);
     mbar_init(k_empty, 1);
@@ -491,24 +507,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
             ++nq[side];
           }
         for (int b = 0; b <= n && ok; ++b) {
-          if (b < n && !wait<SHORT>(k_full, (uint32_t)(tile + b) & 1u, abort_flag, p.wait_ns)) { ok = false; break; }
           for (int side = 0; side < 2; ++side) {
-            if (b < nx[side]) {
-              if (!wait<SHORT>(&s_free[side], ((ns[side] + (uint32_t)b) & 1u) ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
-              tc_fence_after();
-              mma_scores<DH>(tmem + side * 128, sbase + kQ + side * kTile, sbase + kK);
-              umma_commit(&s_full[side]);
-            }
-            if (side == 1 && b < n) umma_commit(k_empty);
             if (b > 0 && b - 1 < nx[side]) {
               if (!wait<SHORT>(v_full, (uint32_t)(tile + b - 1) & 1u, abort_flag, p.wait_ns) ||
                   !wait<SHORT>(&p_full[side], (ns[side] + (uint32_t)(b - 1)) & 1u, abort_flag, p.wait_ns)) { ok = false; break; }
               tc_fence_after();
-              mma_values<N>(tmem + 256 + side * 128, sbase + kP + side * kTile, sbase + kV, b > 1);
-              umma_commit(&p_free[side]);
+              mma_values<N>(tmem + 256 + side * 128, tmem + side * 128, sbase + kV, b > 1);
+              if (b == nx[side]) umma_commit(&o_full[side]);
+            }
+            if (side == 1 && b > 0) umma_commit(v_empty);
+            if (b < nx[side]) {
+              if (!wait<SHORT>(k_full, (uint32_t)(tile + b) & 1u, abort_flag, p.wait_ns)) { ok = false; break; }
+              tc_fence_after();
+              mma_scores<DH>(tmem + side * 128, sbase + kQ + side * kTile, sbase + kK);
+              umma_commit(&s_full[side]);
             }
           }
-          if (ok && b > 0) umma_commit(v_empty);
+          if (ok && b < n) umma_commit(k_empty);
         }
         tile += n;
         ns[0] += (uint32_t)na;
@@ -527,8 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
     const int side = (warp - kFirstRowWarp) >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + (uint32_t)(side * 128) + lane_off, tO = tS + 256;
-    const uint32_t qtile = sbase + kQ + side * kTile, ptile = sbase + kP + side * kTile;
-    uint32_t done = 0;  // blocks of this tile so far
+    const uint32_t qtile = sbase + kQ + side * kTile;
+    uint32_t done = 0, n_segs = 0;  // blocks of this tile so far, and segments that had some
     while (ok && w.next()) {
       const int nx = w.blocks_of(side), n = max(w.blocks_of(0), w.blocks_of(1));
       const int i = side * kTileRows + r, pair = w.r0 + i;
@@ -605,9 +620,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
               mx = fmaxf(mx, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * factor(2 * c + g));
             }
           }
-          // P V of the block before has read P, and O holds every product up to it
-          if (!warp_wait<SHORT>(&p_free[side], (done & 1u) ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
-          tc_fence_after();
           if (__any_sync(0xFFFFFFFFu, mx > m + kSlack)) {
             const float mn = fmaxf(m, mx), alpha = mn == m ? 1.0f : ex2(m - mn);
             if (b > 0) {
@@ -628,21 +640,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
           for (int c = 0; c < 4; ++c) {
             uint32_t z[32];
             tmem_ld32(tS + c * 32, z);
-            if (c == 3) {
-              tc_fence_before();
-              mbar_arrive(&s_free[side]);
-            }
             if (edge) {
 #pragma unroll
               for (int k = 0; k < 32; ++k)
                 if (hidden(c * 32 + k)) z[k] = 0xFF800000u;
             }
+            uint32_t yy[16];
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
+              uint32_t* y = yy + 8 * g;
               const float fg = factor(2 * c + g), cg = sc.dx[2 * c + g] - ref;
               const float2 f2 = make_float2(fg, fg), c2 = make_float2(cg, cg);
               float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-              uint32_t y[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 const int col = g * 16 + 2 * k;
@@ -653,17 +662,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
               }
               sum[0] = __fadd2_rn(sum[0], sum[1]);
               l = __fmaf_rn(sum[0].x + sum[0].y, sc.back[2 * c + g], l);
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-                st_shared_v4(piece(ptile, r, 2 * (2 * c + g) + k), make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]));
             }
+            tmem_st16(tS + c * 16, yy);
           }
+          tmem_wait_st();
           tc_fence_before();
-          fence_async_shared();
           mbar_arrive(&p_full[side]);
         }
         // the last product
-        if (ok && !warp_wait<SHORT>(&p_free[side], (done & 1u) ^ 1u, abort_flag, p.wait_ns)) ok = false;
+        if (ok && !warp_wait<SHORT>(&o_full[side], n_segs++ & 1u, abort_flag, p.wait_ns)) ok = false;
         if (!ok) break;
         tc_fence_after();
       }
@@ -672,9 +679,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       const int slot = 2 * j + (starts ? 1 : 0);
       const float inv = l == 0.0f ? 0.0f : 1.0f / l, fx = pow2i(xref);
       const float lse2 = l == 0.0f ? -INFINITY : m + (log2f(l) - kOffset);
-      // Where V held NaN or infinite values: each column's first key with one, into this warp's rows of P, which is read out.
+      // Where V held NaN or infinite values: each column's first key with one, into this warp's rows of Q, which the last S has read.
       const bool odd = nx && *(volatile int*)&misc.odd;
-      int* bad = reinterpret_cast<int*>(smem + kP + side * kTile + (warp & 3) * 4096);
+      int* bad = reinterpret_cast<int*>(smem + kQ + side * kTile + (warp & 3) * 4096);
       if (odd) {
         for (int k = lane; k < DH; k += 32) bad[k] = kAll;
         __syncwarp();
@@ -688,8 +695,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
         }
         __syncwarp();
       }
-      // Through this warp's rows of P (4 KB of its own after `bad`), so that neighbouring lanes write a row's neighbouring bytes.
-      const uint32_t stage = ptile + (uint32_t)((warp & 3) * 4096) + kAtom;
+      // Through this warp's rows of Q's second half (4 KB of its own behind `bad`), so that neighbouring lanes write a row's neighbouring bytes.
+      const uint32_t stage = qtile + (uint32_t)((warp & 3) * 4096) + kAtom;
       const int64_t to_att = (row * p.n_heads + hd) * DH, to_part = ((int64_t)slot * kRows + i) * DH;
 #pragma unroll 1
       for (int c = 0; c < DH / 32; ++c) {
