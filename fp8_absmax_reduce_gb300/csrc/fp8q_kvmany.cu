@@ -5,10 +5,10 @@
 // The products are tcgen05 kind::f16 ones, fp16 operands and fp32 accumulators in tensor memory: FP8 codes are fp16 numbers, and q is
 // one over a power of two of its row, so the scores lose nothing.  (FP8 operands would need q and P in several 4-bit parts.)
 // A CTA has 256 rows of one K/V head, two tiles of 128 (token, query head) pairs, A and B, which share what is
-// made of each block of 128 keys; its 16 warps:
+// made of each block of 128 keys; its 16 warps (two have no work: a quarter of tensor memory's lanes is a warp's by its number modulo 4):
 //   warp 5       pages, bulk copies of a block's codes of K and V into shared memory, and its scales, a block ahead;
-//   warps 0-3    K's codes into a swizzled fp16 tile (each block's first product waits for it);
-//   warps 6, 7   V's;
+//   warps 0-3    K's codes into a swizzled fp16 tile, then V's.  (V's by two warps of its own made two of an SM's four schedulers, and
+//                the rows that run there, the last: 2 x 512 tokens over 8192 take 184 us either way, 64 x 104 over 1000 325 and 301);
 //   warp 4       the products, one thread: O_A += P_A V of the block before, S_A = Q_A K^T, then B's;
 //   warps 8-15   a row a thread (A, then B): q into shared memory; per block the row's maximum from S, P = 2^(s - m) as fp16
 //                over S in tensor memory, and at the end O over the sum.
@@ -29,7 +29,7 @@ namespace fp8q {
 
 namespace {
 
-constexpr int kKThreads = 128, kVThreads = 64, kMmaWarp = 4, kCopyWarp = 5, kFirstRowWarp = 8, kThreads = 512;
+constexpr int kConvertThreads = 128, kMmaWarp = 4, kCopyWarp = 5, kFirstRowWarp = 8, kThreads = 512;
 constexpr int kTileRows = 128, kRows = 2 * kTileRows;
 constexpr int kAtom = 16384;       // 128 rows x 128 bytes: 64 fp16 columns of a swizzled tile
 constexpr int kTile = 2 * kAtom;   // a tile of 128 columns
@@ -293,14 +293,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       mbar_init(&o_full[i], 1);
       mbar_init(&p_full[i], kTileRows);
     }
-    mbar_init(k_full, kKThreads);
+    mbar_init(k_full, kConvertThreads);
     mbar_init(k_empty, 1);
-    mbar_init(v_full, kVThreads);
+    mbar_init(v_full, kConvertThreads);
     mbar_init(v_empty, 1);
     mbar_init(drain, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&code_full[i], 1);
-      mbar_init(&code_free[i], i ? kVThreads : kKThreads);
+      mbar_init(&code_free[i], kConvertThreads);
     }
     misc.abort = misc.odd = 0;
     fence_mbar_init();
@@ -388,28 +388,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       }
     }
   };
-  auto convert_blocks = [&](auto threads, int lt, int is_v, uint64_t* full, uint64_t* empty) {
+  if (t < kConvertThreads) {
     while (ok && w.next()) {
       const int n = max(w.blocks_of(0), w.blocks_of(1));
-      for (int b = 0; b < n; ++b, ++tile) {
+      for (int b = 0; b < n && ok; ++b, ++tile) {
         const uint32_t par = (uint32_t)tile & 1u;
-        if (!warp_wait<SHORT>(empty, par ^ 1u, abort_flag, p.wait_ns) || !warp_wait<SHORT>(&code_full[is_v], par, abort_flag, p.wait_ns)) { ok = false; break; }
-        convert(threads, lt, sbase + (is_v ? kV : kK), sbase + kCodes + is_v * kAtom, is_v, misc.keys[tile & 3]);
-        mbar_arrive(&code_free[is_v]);
-        fence_async_shared();
-        mbar_arrive(full);
+#pragma unroll 1
+        for (int is_v = 0; is_v < 2; ++is_v) {
+          if (!warp_wait<SHORT>(is_v ? v_empty : k_empty, par ^ 1u, abort_flag, p.wait_ns) ||
+              !warp_wait<SHORT>(&code_full[is_v], par, abort_flag, p.wait_ns)) { ok = false; break; }
+          convert(std::integral_constant<int, kConvertThreads>{}, t, sbase + (is_v ? kV : kK), sbase + kCodes + is_v * kAtom, is_v, misc.keys[tile & 3]);
+          mbar_arrive(&code_free[is_v]);
+          fence_async_shared();
+          mbar_arrive(is_v ? v_full : k_full);
+        }
       }
     }
     if (!ok) {
       atomicOr(p.kv.status, kStatusTimeout);
       *abort_flag = 1;
     }
-  };
-
-  if (t < kKThreads) {
-    convert_blocks(std::integral_constant<int, kKThreads>{}, t, 0, k_full, k_empty);
-  } else if (warp == 6 || warp == 7) {
-    convert_blocks(std::integral_constant<int, kVThreads>{}, t - 192, 1, v_full, v_empty);
   } else if (warp == kCopyWarp) {
     // ---------------- pages, copies, scales ----------------
     uint32_t fetched[2] = {0, 0};  // blocks whose codes were asked for
