@@ -554,35 +554,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       float m = -INFINITY, l = 0.0f;
       int xref = 0;
       if (nx) {
-        // q over a power of two of its row, as fp16: a warp takes its 32 rows a few at a time, 16 bytes a lane (a thread that read its own
+        // q over a power of two of its row, as fp16: a warp reads its 32 rows at once, 16 bytes a lane and row (a thread that read its own
         // row took 15000 cycles for it).  A row that does not exist reads the unit's first.
-        constexpr int kLanes = DH == 64 ? 8 : 16, kStep = 32 / kLanes, kBatch = 8;
-        const int sub = lane / kLanes, col = lane % kLanes;
+        constexpr int kLanes = DH == 64 ? 8 : 16, kStep = 32 / kLanes, kSteps = 32 / kStep;
+        const int sub = lane / kLanes, col = lane % kLanes, r0 = w.r0, first = w.q.first, n_rows = w.n_rows, head0 = w.h * G;
+        const int64_t width = (int64_t)(p.n_heads + 2 * p.kv.hkv) * DH;
+        const uint16_t* base = p.qkv + (col * 8 < DH ? col * 8 : 0);
         int ex = -110;
-#pragma unroll 1
-        for (int k0 = 0; k0 < 32 / kStep; k0 += kBatch) {
-          uint4 v[kBatch];
+        uint4 v[kSteps];
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int other = w.r0 + i - lane + (k0 + k) * kStep + sub;
-            const int pr = other - w.r0 < w.n_rows ? other : w.r0, tk = w.t.token(pr);
-            const uint16_t* src = p.qkv + ((int64_t)(w.q.first + tk) * (p.n_heads + 2 * p.kv.hkv) + w.h * G + pr - tk * G) * DH;
-            v[k] = ld_nc_v4(src + (col * 8 < DH ? col * 8 : 0));
-          }
+        for (int k = 0; k < kSteps; ++k) {
+          const int other = i - lane + k * kStep + sub, pr = r0 + (other < n_rows ? other : 0), tk = w.t.token(pr);
+          v[k] = ld_nc_v4(base + (first + tk) * width + (head0 + pr - tk * G) * DH);
+        }
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            uint32_t big = max(max(absmax_bf16x2(v[k].x), absmax_bf16x2(v[k].y)), max(absmax_bf16x2(v[k].z), absmax_bf16x2(v[k].w)));
+        for (int k = 0; k < kSteps; ++k) {
+          uint32_t big = max(max(absmax_bf16x2(v[k].x), absmax_bf16x2(v[k].y)), max(absmax_bf16x2(v[k].z), absmax_bf16x2(v[k].w)));
 #pragma unroll
-            for (int m = 1; m < kLanes; m <<= 1) big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, m));
-            const int e = max((int)(big >> 23) - 127, -110);
-            const float fq = pow2i(14 - e);
-            if (col * 8 < DH)
-              st_shared_v4(piece(qtile, (warp & 3) * 32 + (k0 + k) * kStep + sub, col),
-                           make_uint4(pack_half2(bf16_lo(v[k].x) * fq, bf16_hi(v[k].x) * fq), pack_half2(bf16_lo(v[k].y) * fq, bf16_hi(v[k].y) * fq),
-                                      pack_half2(bf16_lo(v[k].z) * fq, bf16_hi(v[k].z) * fq), pack_half2(bf16_lo(v[k].w) * fq, bf16_hi(v[k].w) * fq)));
-            const int mine = __shfl_sync(0xFFFFFFFFu, e, (lane % kStep) * kLanes);
-            if (lane / kStep == k0 + k) ex = mine;
-          }
+          for (int m = 1; m < kLanes; m <<= 1) big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, m));
+          const int e = max((int)(big >> 23) - 127, -110);
+          const float fq = pow2i(14 - e);
+          if (col * 8 < DH)
+            st_shared_v4(piece(qtile, (warp & 3) * 32 + k * kStep + sub, col),
+                         make_uint4(pack_half2(bf16_lo(v[k].x) * fq, bf16_hi(v[k].x) * fq), pack_half2(bf16_lo(v[k].y) * fq, bf16_hi(v[k].y) * fq),
+                                    pack_half2(bf16_lo(v[k].z) * fq, bf16_hi(v[k].z) * fq), pack_half2(bf16_lo(v[k].w) * fq, bf16_hi(v[k].w) * fq)));
+          const int mine = __shfl_sync(0xFFFFFFFFu, e, (lane % kStep) * kLanes);
+          if (lane / kStep == k) ex = mine;
         }
         const float rowf = p.scale_log2 * pow2i(ex - 14);
         fence_async_shared();
@@ -697,7 +694,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       }
       // Through this warp's rows of Q's second half (4 KB of its own behind `bad`), so that neighbouring lanes write a row's neighbouring bytes.
       const uint32_t stage = qtile + (uint32_t)((warp & 3) * 4096) + kAtom;
-      const int64_t to_att = (row * p.n_heads + hd) * DH, to_part = ((int64_t)slot * kRows + i) * DH;
+      const int to = real ? (int)(row * p.n_heads + hd) : -1;  // below 2^31
+      const int64_t to_part = ((int64_t)slot * kRows + i - lane) * DH;
+      const int there = w.n_rows - (i - lane);  // rows of this warp
 #pragma unroll 1
       for (int c = 0; c < DH / 32; ++c) {
         uint32_t o[32];
@@ -709,7 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
           if (odd && bad[c * 32 + k] < limit) v = __uint_as_float(0x7FC00000u);
           o[k] = __float_as_uint(v);
         }
-        if (whole) {
+        if (whole) {  // four lanes a row
+          const int col = lane & 3;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             st_shared_v4(stage + lane * 64 + ((k ^ (lane >> 1)) & 3) * 16,
@@ -717,22 +717,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
                                     pack_bf16x2(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3])),
                                     pack_bf16x2(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5])),
                                     pack_bf16x2(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7]))));
-        } else {
+          __syncwarp();
+          uint4 x[4];
+          int at[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int from = k * 8 + (lane >> 2);
+            x[k] = ld_shared_v4(stage + from * 64 + ((col ^ (from >> 1)) & 3) * 16);
+            at[k] = __shfl_sync(0xFFFFFFFFu, to, from);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (at[k] >= 0) *reinterpret_cast<uint4*>(p.att + (int64_t)at[k] * DH + c * 32 + col * 8) = x[k];
+        } else {  // eight lanes a row
+          const int col = lane & 7;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             st_shared_v4(stage + lane * 128 + ((k ^ lane) & 7) * 16, make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
-        }
-        __syncwarp();
-        const int step = whole ? 8 : 4, lanes = 32 / step;  // rows at a time; lanes of a row
-#pragma unroll 4
-        for (int k = 0; k < 32 / step; ++k) {
-          const int from = k * step + lane / lanes, col = lane % lanes;
-          const int64_t at = __shfl_sync(0xFFFFFFFFu, whole ? to_att : to_part, from);
-          if (!__shfl_sync(0xFFFFFFFFu, (int)real, from)) continue;
-          if (whole)
-            *reinterpret_cast<uint4*>(p.att + at + c * 32 + col * 8) = ld_shared_v4(stage + from * 64 + ((col ^ (from >> 1)) & 3) * 16);
-          else
-            *reinterpret_cast<uint4*>(p.part_o + at + c * 32 + col * 4) = ld_shared_v4(stage + from * 128 + ((col ^ from) & 7) * 16);
+          __syncwarp();
+          uint4 x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int from = k * 4 + (lane >> 3);
+            x[k] = ld_shared_v4(stage + from * 128 + ((col ^ from) & 7) * 16);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int from = k * 4 + (lane >> 3);
+            if (from < there) *reinterpret_cast<uint4*>(p.part_o + to_part + from * DH + c * 32 + col * 4) = x[k];
+          }
         }
       }
       if (real) {
