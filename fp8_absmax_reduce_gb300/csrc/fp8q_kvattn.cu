@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_join(const AttendArgs p) {
 
 // Rows of a CTA for the (token, head) pairs of a sequence and K/V head: 8 of one warp or 16; above, two or four warps share their keys
 // for 16 rows each; and from kManyPairs on the kernel on tensor memory.  (2 sequences of 8192, 16 of 4096 and 64 of 1000, 40 + 8 heads of
-// 128: 35 pairs 35, 74 and 83 us here and 40, 71, 102 there; 50 pairs 41, 78, 95 and 39, 63, 109; 80 pairs 55, 140, 149 and 39, 73, 106.)
+// 128: 35 pairs 35, 74 and 83 us here and 40, 71, 102 there; 50 pairs 41, 78, 95 and 39, 63, 109; 80 pairs 55, 140, 149 and 38, 70, 100.)
 constexpr int kManyPairs = 65;
 struct Rows {
   int nt, rw;

@@ -1,11 +1,11 @@
 // Causal attention over the 8-bit key/value cache for many rows a sequence (pieces of prompts): on the 5th-generation tensor
-// cores, bound by them, by the exponentials, and by the shared memory between.  2 x 512 tokens of 40 + 8 heads of 128 over 8192: 184 us with
-// the join, 807 TFLOP/s; the tensor pipe is active for a third of it.
+// cores, bound by the chain of a tile's products and exponentials.  2 x 512 tokens of 40 + 8 heads of 128 over 8192: 183 us with the
+// join, 811 TFLOP/s; the tensor pipe is active for 37 % of it, a block of 128 keys takes 4200 cycles.
 //
 // The products are tcgen05 kind::f16 ones, fp16 operands and fp32 accumulators in tensor memory: FP8 codes are fp16 numbers, and q is
 // one over a power of two of its row, so the scores lose nothing.  (FP8 operands would need q and P in several 4-bit parts.)
 // A CTA has 256 rows of one K/V head, two tiles of 128 (token, query head) pairs, A and B, which share what is
-// made of each block of 128 keys; its 16 warps (two have no work: a quarter of tensor memory's lanes is a warp's by its number modulo 4):
+// made of each block of 128 keys; its 16 warps (two have no work: a warp's number modulo 4 says which quarter of tensor memory's lanes it reads):
 //   warp 5       pages, bulk copies of a block's codes of K and V into shared memory, and its scales, a block ahead;
 //   warps 0-3    K's codes into a swizzled fp16 tile, then V's.  (V's by two warps of its own made two of an SM's four schedulers, and
 //                the rows that run there, the last: 2 x 512 tokens over 8192 take 184 us either way, 64 x 104 over 1000 325 and 301);
@@ -41,8 +41,8 @@ constexpr int kBars = kCodes + kTile;
 constexpr int kMisc = kBars + 256;
 constexpr float kOffset = 11.0f, kSlack = 4.0f;
 constexpr int kAll = 0x7FFFFFFF;
-// What a unit costs besides its keys, in blocks: q, the first pages, the results.  (With P in shared memory, 2 x 512 tokens of 40 heads over 8192: 207,
-// 200, 194, 194 and 192 us with 2, 4, 7, 10 and 14; 16 x 16 over 4096: 91, 82, 79, 78, 85.)
+// What a unit costs besides its keys, in blocks: q, the first pages, the results.  (2 x 512 tokens of 40 heads over 8192: 189, 185, 183, 183
+// and 182 us with 3, 5, 7, 10 and 14; 16 x 104 over 4096: 208, 202, 184, 185, 192; 16 x 16: 73, 69, 70, 74, 82.)
 constexpr int kUnitCost = 7;
 
 // A block's scales as the rows need them, 16 keys each: 2^X of K; kOffset + dx and 2^-dx of V, dx its exponent over the segment's largest.
