@@ -19,8 +19,8 @@
 // P's window is that of the few rows' kernel: p 2^11 in fp16, the reference maximum moving when it is exceeded by 2^4.
 // The keys of all (sequence, row tile, K/V head) units are cut into equal parts, one a CTA, as there.
 //
-// Every mbarrier wait is bounded; on expiry the CTA records FP8Q_STATUS_TIMEOUT, stops issuing, waits for the products that it
-// issued, frees tensor memory and exits.
+// Every mbarrier wait is bounded; on expiry the CTA records FP8Q_STATUS_TIMEOUT, stops issuing, waits for the products and copies that it
+// issued, whichever role gave up, frees tensor memory and exits.
 #include <type_traits>
 
 #include "fp8q_kvline.cuh"
@@ -488,10 +488,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
     if (!ok) {
       atomicOr(p.kv.status, kStatusTimeout);
       *abort_flag = 1;
-      int never = 0;  // the copies in flight, before the memory is given back
-      for (int i = 0; i < 2; ++i)
-        if (fetched[i]) warp_wait<false>(&code_full[i], (fetched[i] - 1) & 1u, &never, 0);
     }
+    // The copies in flight, before the memory is given back.  This warp may have asked for its last block and left its loop in order
+    // where another role gives up and nobody waits for the block any more; when none did, they have landed.
+    int never = 0;
+    for (int i = 0; i < 2; ++i)
+      if (fetched[i]) warp_wait<false>(&code_full[i], (fetched[i] - 1) & 1u, &never, 0);
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
       // ---------------- the products ----------------

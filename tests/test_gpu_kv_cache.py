@@ -626,6 +626,26 @@ def test_waits_that_run_out_end_the_call_and_nothing_else(lens, rows):
     assert fq.get_status() == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("lens,rows", [([900, 300], 100), ([128], 100), ([250] * 5, 60)])
+def test_waits_that_run_out_after_the_last_copy_leave_none_in_flight(lens, rows):
+    """A CTA of one or two blocks has asked for all of its copies when the roles that wait for them give up.  It stays until they have
+    landed, so the kernels that follow at once have its shared memory to themselves and are right."""
+    w = World(0, 128, 64, 4, 2, lens, rows=rows, seed=45)
+    w.fill()
+    t, x = w.append()
+    want = fq.attention_cached(w.cache, t, *w.args(), 4)
+    args = w.args()
+    torch.cuda.synchronize()
+    fq.get_status(clear=True)
+    outs = []
+    for _ in range(20):
+        fq.selftest_attention_cached_wait_limit(w.cache, t, *args, 4, 1e-9)
+        outs.append(fq.attention_cached(w.cache, t, *args, 4))
+    torch.cuda.synchronize()
+    assert fq.get_status(clear=True) == fq.STATUS_TIMEOUT
+    assert all(torch.equal(a, b) for o in outs for a, b in zip(o, want))
+
+
 def _on_a_stream():
     w = World(0, 128, 64, 8, 2, [130, 64, 1], rows=1, seed=41)
     w.fill()
