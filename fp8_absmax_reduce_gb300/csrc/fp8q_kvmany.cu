@@ -11,11 +11,12 @@
 //                the rows that run there, the last: 2 x 512 tokens over 8192 take 184 us either way, 64 x 104 over 1000 325 and 301);
 //   warp 4       the products, one thread: O_A += P_A V of the block before, S_A = Q_A K^T, then B's;
 //   warps 8-15   a row a thread (A, then B): q into shared memory; per block the row's maximum from S, P = 2^(s - m) as fp16
-//                over S in tensor memory, and at the end O over the sum.
-// S, P and O fill tensor memory, so a tile's S waits for its P V; meanwhile the other tile's rows work.  P in shared memory, and S a
+//                in tensor memory, and at the end O over the sum.
+// P lies over S: S and O fill tensor memory, so a tile's S waits for its P V; meanwhile the other tile's rows work.  P in shared memory, and S a
 // block ahead, was slower (195 us against 185 for 2 x 512 tokens over 8192): shared memory carries the products' operands (Q and K alone
-// its full width while S is made), the codes and what is made of them.  That the next S may be issued on top of P right behind the
-// product that reads it rests on one thread's products of one CTA running in the order of issue.
+// its full width while S is made), the codes and what is made of them.  Products with different accumulators may run in another order than
+they were issued in, so S over P waits for the product that reads P (1 to 2 % at head_dim 96 and 128); at head_dim 64 P lies beside O, which
+has half of its columns to spare, and nothing waits (1 % faster than over S).
 // P's window is that of the few rows' kernel: p 2^11 in fp16, the reference maximum moving when it is exceeded by 2^4.
 // The keys of all (sequence, row tile, K/V head) units are cut into equal parts, one a CTA, as there.
 //
@@ -88,7 +89,7 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
     umma_bf16(d, smem_desc_sw128(a + off, 16, 1024), smem_desc_sw128(b + off, 16, 1024), idesc_f16(128, 0), i ? 1u : 0u);
   }
 }
-// O (+)= P V over 128 keys: P in tensor memory, over S, V MN-major (a row a key), N = 64 or 128 columns.
+// O (+)= P V over 128 keys: P in tensor memory, V MN-major (a row a key), N = 64 or 128 columns.
 template <int N>
 __device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
 #pragma unroll
@@ -219,6 +220,7 @@ struct Walk {
 template <int FMT, int DH, bool SHORT>
 __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_constant__ AttendArgs p) {
   constexpr int N = DH == 64 ? 64 : 128;  // columns of V's tile and of O: 96 are filled up with zeros
+  constexpr int kP = DH == 64 ? 256 + 64 : 0;  // columns from S to P: beside O where that leaves room
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBars);
@@ -231,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
   uint64_t* s_full = bars + 8;    // [2] per tile; O holds every product before it
   uint64_t* o_full = bars + 10;   // [2] O is complete
   uint64_t* p_full = bars + 12;   // [2]
+  uint64_t* pv_done = bars + 14;  // [2] P V has read P, and S may be written over it
   uint64_t* drain = bars + 16;
   uint64_t* code_full = bars + 17;   // K's, V's codes of the next block
   uint64_t* code_free = bars + 19;   // [2] they have been read
@@ -292,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       mbar_init(&s_full[i], 1);
       mbar_init(&o_full[i], 1);
       mbar_init(&p_full[i], kTileRows);
+      mbar_init(&pv_done[i], 1);
     }
     mbar_init(k_full, kConvertThreads);
     mbar_init(k_empty, 1);
@@ -497,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
       // ---------------- the products ----------------
-      uint32_t nq[2] = {0, 0}, ns[2] = {0, 0};  // segments and blocks of each tile so far
+      uint32_t nq[2] = {0, 0}, ns[2] = {0, 0}, np[2] = {0, 0};  // segments, blocks and waits for P V of each tile so far
       while (ok && w.next()) {
         const int na = w.blocks_of(0), nb = w.blocks_of(1), n = max(na, nb);
         const int nx[2] = {na, nb};
@@ -513,12 +517,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
               if (!wait<SHORT>(v_full, (uint32_t)(tile + b - 1) & 1u, abort_flag, p.wait_ns) ||
                   !wait<SHORT>(&p_full[side], (ns[side] + (uint32_t)(b - 1)) & 1u, abort_flag, p.wait_ns)) { ok = false; break; }
               tc_fence_after();
-              mma_values<N>(tmem + 256 + side * 128, tmem + side * 128, sbase + kV, b > 1);
+              mma_values<N>(tmem + 256 + side * 128, tmem + side * 128 + kP, sbase + kV, b > 1);
               if (b == nx[side]) umma_commit(&o_full[side]);
+              else if (kP == 0) umma_commit(&pv_done[side]);
             }
             if (side == 1 && b > 0) umma_commit(v_empty);
             if (b < nx[side]) {
               if (!wait<SHORT>(k_full, (uint32_t)(tile + b) & 1u, abort_flag, p.wait_ns)) { ok = false; break; }
+              if (kP == 0 && b > 0 && !wait<SHORT>(&pv_done[side], np[side]++ & 1u, abort_flag, p.wait_ns)) { ok = false; break; }
               tc_fence_after();
               mma_scores<DH>(tmem + side * 128, sbase + kQ + side * kTile, sbase + kK);
               umma_commit(&s_full[side]);
@@ -661,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
               sum[0] = __fadd2_rn(sum[0], sum[1]);
               l = __fmaf_rn(sum[0].x + sum[0].y, sc.back[2 * c + g], l);
             }
-            tmem_st16(tS + c * 16, yy);
+            tmem_st16(tS + kP + c * 16, yy);
           }
           tmem_wait_st();
           tc_fence_before();
