@@ -15,8 +15,8 @@
 // P lies over S: S and O fill tensor memory, so a tile's S waits for its P V; meanwhile the other tile's rows work.  P in shared memory, and S a
 // block ahead, was slower (195 us against 185 for 2 x 512 tokens over 8192): shared memory carries the products' operands (Q and K alone
 // its full width while S is made), the codes and what is made of them.  Products with different accumulators may run in another order than
-they were issued in, so S over P waits for the product that reads P (1 to 2 % at head_dim 96 and 128); at head_dim 64 P lies beside O, which
-has half of its columns to spare, and nothing waits (1 % faster than over S).
+// they were issued in, so S over P waits for the product that reads P (1 to 2 % at head_dim 96 and 128); at head_dim 64 P lies beside O, which
+// has half of its columns to spare, and nothing waits (1 % faster than over S).
 // P's window is that of the few rows' kernel: p 2^11 in fp16, the reference maximum moving when it is exceeded by 2^4.
 // The keys of all (sequence, row tile, K/V head) units are cut into equal parts, one a CTA, as there.
 //
