@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
         const int xv0 = xv[0] == kNoPage ? -1000 : xv[0], xv1 = xv[1] == kNoPage ? -1000 : xv[1];
         const int xnew = max(xref, max(xv0, xv1));
         if (__any_sync(0xFFFFFFFFu, moved || xnew != xref)) {
-          const float fx = pow2i(xref - xnew);
+          const float fx = pow2(xref - xnew);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -548,11 +548,11 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
         const float mk = row_m[w][wr], lk = row_l[w][wr];
         const float f = mk == M ? (M == -INFINITY ? 0.0f : 1.0f) : ex2(mk - M);
         L += lk * (lk != lk ? 1.0f : f);
-        const float fo = f * pow2i(row_x[w] - X);
+        const float fo = f * pow2(row_x[w] - X);
         const float4 v = *reinterpret_cast<const float4*>(join + (k * C::R + r) * C::kPitch + col);
         a[0] += v.x * fo; a[1] += v.y * fo; a[2] += v.z * fo; a[3] += v.w * fo;
       }
-      const float inv = L == 0.0f ? 0.0f : 1.0f / L, fx = pow2i(X);
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L, fx = pow2(X);
 #pragma unroll
       for (int k = 0; k < 4; ++k) a[k] = L == 0.0f ? 0.0f : a[k] * inv * fx;
       const float lse2 = L == 0.0f ? -INFINITY : M + (log2f(L) - 15.0f);

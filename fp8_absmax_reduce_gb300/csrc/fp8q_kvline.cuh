@@ -44,7 +44,12 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// 2^e, e between -126 and 127 or taken as the nearer of them: where what is below vanishes.
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(min(max(e, -126), 127) + 127) << 23); }
+// 2^e down to the smallest subnormal number, and 0 below: a page's scale goes to 2^-127, the ratio of two to 2^-254.
+__device__ __forceinline__ float pow2(int e) {
+  return __uint_as_float(e >= -126 ? (uint32_t)(min(e, 127) + 127) << 23 : e < -149 ? 0u : 1u << (e + 149));
+}
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);

@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
         BlockScales& sc = misc.scales[par];
         if (lane < 8) {
           const int dx = max(here < 0 ? -60 : xv - 127 - xref, -60);
-          sc.k[lane] = pow2i(here < 0 ? 0 : xk - 127);
+          sc.k[lane] = pow2(here < 0 ? 0 : xk - 127);
           sc.dx[lane] = kOffset + (float)dx;
           sc.back[lane] = pow2i(-dx);
         }
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       // ---- the row's result: O over the sum
       const bool starts = w.b0 == 0, whole = starts && w.b1 == w.nb;
       const int slot = 2 * j + (starts ? 1 : 0);
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l, fx = pow2i(xref);
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l, fx = pow2(xref);
       const float lse2 = l == 0.0f ? -INFINITY : m + (log2f(l) - kOffset);
       // Where V held NaN or infinite values: each column's first key with one, into this warp's rows of Q, which the last S has read.
       const bool odd = nx && *(volatile int*)&misc.odd;

@@ -394,6 +394,24 @@ def test_q_of_any_size():
         w.attend(q.reshape(1, -1), q.double().cpu().numpy())
 
 
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("dh,rows", [(64, 1), (128, 1), (96, 9), (64, 130), (128, 130)])
+def test_pages_of_the_smallest_scale(dh, rows, fmt):
+    """K and V below fmax 2^-127, so that their scale has code 0, and q so that scores are of unit size; every kernel, units cut and whole.
+    Outputs are near bf16's subnormal numbers, half a step of which (2^-134) is allowed besides, and as much for fp32's."""
+    w = World(fmt, dh, 32, 4, 2, [1000, 150, 130], rows=rows, seed=50 + dh)
+    start = np.concatenate([[0], np.cumsum(w.lens)]).tolist()
+    x = w.rng.uniform(-1, 1, (start[-1], 4, dh)) * 2.0 ** -119
+    d = torch.tensor(x, dtype=torch.float32).cuda()
+    fq.kv_cache_append(w.cache, d.reshape(start[-1], -1), i32(w.pages), i32(w.lens), 0, row_start=i32(start))
+    ref.append(w.ref, fmt, 32, w.pages, w.lens, ref.rows_of(3, start[-1], start), d.double().cpu().numpy().reshape(-1, 2, 2, dh))
+    w.check_cache()
+    assert (w.ref["kx"][w.pages[0]] == -127).all() and (w.ref["vx"][w.pages[0]] == -127).all()
+    q, x = w.qkv(std=2.0 ** 117)
+    att, lse = fq.attention_cached(w.cache, q, *w.args(), 4)
+    w.check_attention(att, lse, x[:, :4], below=2.0 ** -133)
+
+
 @pytest.mark.parametrize("n,length,hkv,hq", [(1, 20000, 1, 5), (1, 4000, 8, 8), (40, 700, 2, 2), (300, 40, 1, 1)])
 def test_work_split_over_the_keys(n, length, hkv, hq):
     """Long sequences cut over many blocks, and more sequences than blocks."""
