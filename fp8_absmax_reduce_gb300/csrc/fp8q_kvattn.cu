@@ -15,8 +15,8 @@
 //
 // Precision.  Scores are fp32 in the log2 domain.  q is divided by a power of two of its row and so is exact in fp16 (elements
 // below 2^-28 of the row's largest lose bits).  p = 2^(s - m) enters as fp16 times 2^15, so it has 11 bits down to 2^-29 of the
-// row's largest and vanishes below 2^-39.  V's scales are relative to the largest so far (xref), which moves like the
-// maximum does, and p times that ratio is what is rounded.
+// row's largest and vanishes below 2^-39.  V's scales are relative to the largest that the row has seen so far (xr), which moves like the
+// maximum does, and p times that ratio is what is rounded.  Both are a row's own: what it does not see does not move a bit of it.
 //
 // Work.  The keys of all (sequence, row tile, K/V head) units form one line of blocks of 128 keys, each unit preceded by what it costs
 // besides; it is cut into equal parts, one a CTA.  A unit that is cut leaves fp32 partial results, which the second kernel joins in order.
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
   __shared__ Line line_s;
   __shared__ int scales[2][kWarps][4];  // [stage][part of 32 keys][2 K, 2 V scales of 16 keys each]
   __shared__ float row_m[kWarps][C::RT], row_l[kWarps][C::RT];
-  __shared__ int row_x[kWarps];
+  __shared__ int row_x[kWarps][C::RT];
   start_dependents();
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, c = lane & 3, g8 = lane >> 2;
   const int kg = warp / RW, rw = warp % RW;
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
       for (int e = 0; e < 2; ++e) exq[n][e] = __shfl_sync(0xFFFFFFFFu, ex - 14, (2 * c + e) * 4);
     }
     float o[DH / 16][NT][4], m[NT][2], l[NT][2];
-    int xref = -1000;
+    int xr[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -342,6 +342,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
         for (int e = 0; e < 4; ++e) o[i][n][e] = 0.0f;
       m[n][0] = m[n][1] = -INFINITY;
       l[n][0] = l[n][1] = 0.0f;
+      xr[n][0] = xr[n][1] = -1000;
     }
 
 #pragma unroll 1
@@ -390,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
         // the row's maximum: a page's scale is positive, so it goes to the page's maximum alone
         float f[2][NT][2], mn[NT][2];
         bool moved = false;
+        const int xv0 = xv[0] == kNoPage ? -1000 : xv[0], xv1 = xv[1] == kNoPage ? -1000 : xv[1];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -405,41 +407,68 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
             mn[n][e] = x;
             moved |= x != m[n][e];
           }
-        const int xv0 = xv[0] == kNoPage ? -1000 : xv[0], xv1 = xv[1] == kNoPage ? -1000 : xv[1];
-        const int xnew = max(xref, max(xv0, xv1));
-        if (__any_sync(0xFFFFFFFFu, moved || xnew != xref)) {
-          const float fx = pow2(xref - xnew);
+        if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float fade = mn[n][e] == m[n][e] ? 1.0f : ex2(m[n][e] - mn[n][e]);
               l[n][e] *= fade;
-              const float fo = fade * fx;
 #pragma unroll
               for (int i = 0; i < DH / 16; ++i) {
-                o[i][n][e] *= fo;
-                o[i][n][e + 2] *= fo;
+                o[i][n][e] *= fade;
+                o[i][n][e + 2] *= fade;
               }
               m[n][e] = mn[n][e];
             }
-          xref = xnew;
         }
-        // 2^(s - m + 15 + dx), dx the exponent of the page's V over xref.  The sum takes 2^dx back, so it holds for pages of any V;
-        // below 2^-60 nothing is left of one in fp16.
+        // The largest scale of V that each row has seen.  Rows' differ only from the first step on that not all see, and what follows is such a
+        // step; there a row may see one of the two groups of 16 keys, or none.
+        auto largest = [&](int n, int e) {
+          return max(xr[n][e], edge ? max(key0 < limit[n][e] ? xv0 : -1000, key0 + 16 < limit[n][e] ? xv1 : -1000) : max(xv0, xv1));
+        };
+        bool grew = false;
+        if (edge) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) grew |= largest(n, e) != xr[n][e];
+          grew = __any_sync(0xFFFFFFFFu, grew);
+        } else {
+          grew = largest(0, 0) != xr[0][0];
+        }
+        if (grew) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int x = largest(n, e);
+              const float fx = pow2(xr[n][e] - x);
+#pragma unroll
+              for (int i = 0; i < DH / 16; ++i) {
+                o[i][n][e] *= fx;
+                o[i][n][e + 2] *= fx;
+              }
+              xr[n][e] = x;
+            }
+        }
+        // 2^(s - m + 15 + dx), dx the exponent of the page's V over xr.  The sum takes 2^dx back, so it holds for pages of any V;
+        // below 2^-60 nothing is left of one in fp16.  (A page that the row does not see may be above xr.)
         uint32_t pb[2][NT][2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int dx = max((k ? xv1 : xv0) - xref, -60);
-          const float back = pow2i(-dx);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float mr = m[n][e & 1];
-              w[e] = ex2(__fmaf_rn(z[k][n][e], f[k][n][e & 1], (float)(15 + dx) - (mr == -INFINITY ? 0.0f : mr)));
-              l[n][e & 1] = __fmaf_rn(w[e], back, l[n][e & 1]);
+            for (int e = 0; e < 2; ++e) {
+              const int dx = max(min((k ? xv1 : xv0) - xr[n][e], 0), -60);
+              const float add = (float)(15 + dx) - (m[n][e] == -INFINITY ? 0.0f : m[n][e]), back = pow2i(-dx);
+#pragma unroll
+              for (int i = e; i < 4; i += 2) {
+                w[i] = ex2(__fmaf_rn(z[k][n][i], f[k][n][e], add));
+                l[n][e] = __fmaf_rn(w[i], back, l[n][e]);
+              }
             }
             pb[k][n][0] = transposed(pack_half2(w[0], w[1]));
             pb[k][n][1] = transposed(pack_half2(w[2], w[3]));
@@ -520,6 +549,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
         if (g8 == 0) {
           row_m[warp][r] = m[n][e];
           row_l[warp][r] = l[n][e];
+          row_x[warp][r] = xr[n][e];
         }
         if (rw * C::RT + r < n_rows) {
           float* to = join + (kg * C::R + rw * C::RT + r) * C::kPitch + g8 * (DH / 8);
@@ -528,7 +558,6 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
             *reinterpret_cast<float4*>(to + 4 * i) = make_float4(o[2 * i][n][e], o[2 * i][n][e + 2], o[2 * i + 1][n][e], o[2 * i + 1][n][e + 2]);
         }
       }
-    if (lane == 0) row_x[warp] = xref;
     __syncthreads();
     const bool starts = b0 == 0, whole = starts && b1 == nb;
     const int slot = 2 * j + (starts ? 1 : 0);
@@ -539,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
 #pragma unroll
       for (int k = 0; k < C::KW; ++k) {
         M = fmaxf(M, row_m[k * RW + w0][wr]);
-        X = max(X, row_x[k * RW + w0]);
+        X = max(X, row_x[k * RW + w0][wr]);
       }
       float L = 0.0f, a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -548,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
         const float mk = row_m[w][wr], lk = row_l[w][wr];
         const float f = mk == M ? (M == -INFINITY ? 0.0f : 1.0f) : ex2(mk - M);
         L += lk * (lk != lk ? 1.0f : f);
-        const float fo = f * pow2(row_x[w] - X);
+        const float fo = f * pow2(row_x[w][wr] - X);
         const float4 v = *reinterpret_cast<const float4*>(join + (k * C::R + r) * C::kPitch + col);
         a[0] += v.x * fo; a[1] += v.y * fo; a[2] += v.z * fo; a[3] += v.w * fo;
       }

@@ -17,7 +17,8 @@
 // its full width while S is made), the codes and what is made of them.  Products with different accumulators may run in another order than
 // they were issued in, so S over P waits for the product that reads P (1 to 2 % at head_dim 96 and 128); at head_dim 64 P lies beside O, which
 // has half of its columns to spare, and nothing waits (1 % faster than over S).
-// P's window is that of the few rows' kernel: p 2^11 in fp16, the reference maximum moving when it is exceeded by 2^4.
+// P's window is that of the few rows' kernel: p 2^11 in fp16, the reference maximum moving when it is exceeded by 2^4, and V's scales
+// relative to the largest that the row has seen so far.  Both are a row's own: what it does not see does not move a bit of it.
 // The keys of all (sequence, row tile, K/V head) units are cut into equal parts, one a CTA, as there.
 //
 // Every mbarrier wait is bounded; on expiry the CTA records FP8Q_STATUS_TIMEOUT, stops issuing, waits for the products and copies that it
@@ -41,15 +42,18 @@ constexpr int kCodes = kV + kTile; // the next block's codes: K, V
 constexpr int kBars = kCodes + kTile;
 constexpr int kMisc = kBars + 256;
 constexpr float kOffset = 11.0f, kSlack = 4.0f;
+constexpr int kNothing = -45;      // V's exponent over the reference, at least: nothing is left of 2^(11 + 4 - 45) in fp16
 constexpr int kAll = 0x7FFFFFFF;
 // What a unit costs besides its keys, in blocks: q, the first pages, the results.  (2 x 512 tokens of 40 heads over 8192: 189, 185, 183, 183
 // and 182 us with 3, 5, 7, 10 and 14; 16 x 104 over 4096: 208, 202, 184, 185, 192; 16 x 16: 73, 69, 70, 74, 82.)
 constexpr int kUnitCost = 7;
 
-// A block's scales as the rows need them, 16 keys each: 2^X of K; kOffset + dx and 2^-dx of V, dx its exponent over the segment's largest.
+// A block's scales as the rows need them, 16 keys each: 2^X of K; X of V, and dx, 2^-dx, its exponent over the block's largest.
 struct BlockScales {
   float k[8], dx[8], back[8];
-  int none[4];  // [0]: bit g: keys 16 g .. have no page
+  int v[8];  // -1000: no page
+  int none;  // bit g: keys 16 g .. have no page
+  int vmax;  // the largest of v
 };
 // What is to be seen of a block's codes.
 struct BlockKeys {
@@ -60,7 +64,6 @@ struct BlockKeys {
 struct Misc {
   BlockScales scales[2];  // by block
   BlockKeys keys[4];      // by block
-  int xref[4];            // by segment that has blocks: the largest exponent of V
   int odd;                // some V was NaN or infinite, and is 0 in its tile
   uint32_t tmem;
   int abort;
@@ -330,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
   w.base = line.base;
   w.at = begin;
   w.end = end;
-  int tile = 0, seg = 0;  // blocks so far, and segments that had some: what a role is ahead by in blocks bounds it in these, not in empty ones
+  int tile = 0;  // blocks so far
   bool ok = true;
 
   // ---------------- codes to fp16: THREADS threads, `lt` this one's number ----------------
@@ -452,15 +455,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       int here = read_page(w.b0), next = read_page(w.b0 + 1);
       here = page_of(w.b0, here);
       int xk = read_scale(p.kv.k_scale, here), xv = read_scale(p.kv.v_scale, here);
-      // the segment's largest exponent of V
-      int xref = -1000;
-      for (int pg = (w.b0 * kBlockKeys >> p.kv.page_shift) + lane; (int64_t)pg << p.kv.page_shift < min((int64_t)klim, (int64_t)stop * kBlockKeys);
-           pg += 32) {
-        const int id = table[pg];
-        if (id >= 0 && id < p.kv.n_pages) xref = max(xref, (int)p.kv.v_scale[(int64_t)id * p.kv.hkv + w.h] - 127);
-      }
-      xref = __reduce_max_sync(0xFFFFFFFFu, xref);
-      if (lane == 0) misc.xref[seg & 3] = xref;
       for (int b = w.b0; b < stop; ++b, ++tile) {
         const uint32_t par = (uint32_t)tile & 1u;
         const unsigned have = __ballot_sync(0xFFFFFFFFu, here >= 0) & 0xFFu;
@@ -474,12 +468,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
         fetch(1, b, here, have);
         BlockScales& sc = misc.scales[par];
         if (lane < 8) {
-          const int dx = max(here < 0 ? -60 : xv - 127 - xref, -60);
           sc.k[lane] = pow2(here < 0 ? 0 : xk - 127);
-          sc.dx[lane] = kOffset + (float)dx;
+        }
+        const int v = here < 0 ? -1000 : xv - 127, vmax = __reduce_max_sync(0xFFFFFFFFu, v);  // (lanes from 8 on have none)
+        if (lane < 8) {
+          const int dx = max(v - vmax, kNothing);
+          sc.v[lane] = v;
+          sc.dx[lane] = (float)dx;
           sc.back[lane] = pow2i(-dx);
         }
-        if (lane == 0) sc.none[0] = (int)(~have & 0xFFu);
+        if (lane == 0) {
+          sc.none = (int)(~have & 0xFFu);
+          sc.vmax = vmax;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sc_full[par]);
         here = page_of(b + 1, next);
@@ -487,7 +488,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
         xk = read_scale(p.kv.k_scale, here);
         xv = read_scale(p.kv.v_scale, here);
       }
-      ++seg;
     }
     if (!ok) {
       atomicOr(p.kv.status, kStatusTimeout);
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       const int limit = real ? w.t.limit(pair) : kAll;
       const int kmin = __reduce_min_sync(0xFFFFFFFFu, limit);
       float m = -INFINITY, l = 0.0f;
-      int xref = 0;
+      int xr = -1000;
       if (nx) {
         // q over a power of two of its row, as fp16: a warp reads its 32 rows at once, 16 bytes a lane and row (a thread that read its own
         // row took 15000 cycles for it).  A row that does not exist reads the unit's first.
@@ -599,12 +599,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
           if (!warp_wait<SHORT>(&sc_full[kpar], (uint32_t)((tile + b) >> 1) & 1u, abort_flag, p.wait_ns)) { ok = false; break; }
           tc_fence_after();
           const BlockScales& sc = misc.scales[kpar];
-          xref = misc.xref[seg & 3];
-          const int key0 = (w.b0 + b) * kBlockKeys, none = sc.none[0];
+          const int key0 = (w.b0 + b) * kBlockKeys, none = sc.none;
           const bool edge = key0 + kBlockKeys > kmin || none;
           auto factor = [&](int g) { return fminf(fmaxf(rowf * sc.k[g], 0x1p-100f), 0x1p126f); };
           auto hidden = [&](int col) { return key0 + col >= limit || (none >> (col >> 4) & 1); };
           float mx = -INFINITY;
+          int xnew = max(xr, sc.vmax);
+          if (edge) {
+            xnew = xr;
+            for (int g = 0; g < 8; ++g)
+              if (!hidden(16 * g)) xnew = max(xnew, sc.v[g]);
+          }
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t z[32];
@@ -624,37 +629,52 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
               mx = fmaxf(mx, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * factor(2 * c + g));
             }
           }
-          if (__any_sync(0xFFFFFFFFu, mx > m + kSlack)) {
-            const float mn = fmaxf(m, mx), alpha = mn == m ? 1.0f : ex2(m - mn);
+          bool up = mx - m > kSlack;
+          if (__any_sync(0xFFFFFFFFu, up || xnew != xr)) {
+            up |= !edge && mx > m;  // (what rows do not all see moves only those that see it)
+            const float alpha = up ? ex2(m - mx) : 1.0f, fo = alpha * pow2(xr - xnew);
             if (b > 0) {
 #pragma unroll 1
               for (int c = 0; c < N / 32; ++c) {
                 uint32_t o[32];
                 tmem_ld32(tO + c * 32, o);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fo);
                 tmem_st32(tO + c * 32, o);
               }
             }
             l *= alpha;
-            m = mn;
+            if (up) m = mx;
+            xr = xnew;
           }
           const float ref = m == -INFINITY ? 0.0f : m;
+          // 2^(s - m + 11 + dx), dx the exponent of the page's V over xr; the sum takes 2^dx back, so it holds for pages of any V.  Where all
+          // rows see the block dx is the block's own and one shift a row; elsewhere a page that the row does not see may be above xr.
+          const int shift = max(sc.vmax - xr, kNothing);
+          const float off = kOffset + (float)shift - ref;
+          float sum_b = 0.0f;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t z[32];
             tmem_ld32(tS + c * 32, z);
+            float add[2] = {sc.dx[2 * c] + off, sc.dx[2 * c + 1] + off}, back[2] = {sc.back[2 * c], sc.back[2 * c + 1]};
             if (edge) {
 #pragma unroll
               for (int k = 0; k < 32; ++k)
                 if (hidden(c * 32 + k)) z[k] = 0xFF800000u;
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                const int dx = max(min(sc.v[2 * c + g] - xr, 0), kNothing);
+                add[g] = kOffset + (float)dx - ref;
+                back[g] = pow2i(-dx);
+              }
             }
             uint32_t yy[16];
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
               uint32_t* y = yy + 8 * g;
-              const float fg = factor(2 * c + g), cg = sc.dx[2 * c + g] - ref;
-              const float2 f2 = make_float2(fg, fg), c2 = make_float2(cg, cg);
+              const float fg = factor(2 * c + g);
+              const float2 f2 = make_float2(fg, fg), c2 = make_float2(add[g], add[g]);
               float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
@@ -665,13 +685,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
                 y[k] = pack_half2(pr.x, pr.y);
               }
               sum[0] = __fadd2_rn(sum[0], sum[1]);
-              l = __fmaf_rn(sum[0].x + sum[0].y, sc.back[2 * c + g], l);
+              sum_b = __fmaf_rn(sum[0].x + sum[0].y, back[g], sum_b);
             }
             tmem_st16(tS + kP + c * 16, yy);
           }
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&p_full[side]);
+          l = __fmaf_rn(sum_b, edge ? 1.0f : pow2i(-shift), l);
         }
         // the last product
         if (ok && !warp_wait<SHORT>(&o_full[side], n_segs++ & 1u, abort_flag, p.wait_ns)) ok = false;
@@ -681,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       // ---- the row's result: O over the sum
       const bool starts = w.b0 == 0, whole = starts && w.b1 == w.nb;
       const int slot = 2 * j + (starts ? 1 : 0);
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l, fx = pow2(xref);
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l, fx = pow2(xr);
       const float lse2 = l == 0.0f ? -INFINITY : m + (log2f(l) - kOffset);
       // Where V held NaN or infinite values: each column's first key with one, into this warp's rows of Q, which the last S has read.
       const bool odd = nx && *(volatile int*)&misc.odd;
@@ -764,7 +785,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
         p.cuts[j] = Cut{w.unit0, w.unit0 + w.cost, total, ctas, w.h, w.q.first, w.n_rows, w.r0};
       tc_fence_before();
       tile += n;
-      seg += n > 0;
     }
     if (!ok) {
       atomicOr(p.kv.status, kStatusTimeout);

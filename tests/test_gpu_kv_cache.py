@@ -395,6 +395,35 @@ def test_q_of_any_size():
 
 
 @pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("dh,hq,rows,before", [(128, 2, 4, 45), (64, 4, 8, 60), (96, 8, 8, 1004), (128, 4, 30, 20), (64, 4, 130, 30), (96, 2, 200, 700),
+                                               (128, 6, 150, 0), (128, 4, 300, 5000)])
+def test_rows_do_not_depend_on_values_that_they_do_not_see(dh, hq, rows, before, fmt):
+    """V of the pages of the call's later tokens from unit size to 2^100 of it: rows before those pages keep their bits, and are right; rows
+    that see them lose at most what vanishes beside them, keys 2^-36 of the largest scale, which is at most twice max |v| over fmax, times fmax."""
+    n, P = before + rows, 16
+    border = -(-(before + rows // 2) // P) * P  # a page's first token, inside the call's
+    outs = []
+    for up in (0, 30, 40, 100):
+        w = World(fmt, dh, P, hq, 2, [n], rows=rows, seed=60 + dh, wide=False)
+        w.fill()
+        q, x = w.qkv()
+        v = q.view(rows, hq + 4, dh)[:, hq + 2:]
+        v[max(0, border - before):] *= 2.0 ** up
+        x = q.double().cpu().numpy().reshape(rows, hq + 4, dh)
+        fq.kv_cache_append(w.cache, q, *w.args(), hq)
+        ref.append(w.ref, fmt, P, w.pages, w.lens, w.rows, x[:, hq:].reshape(-1, 2, 2, dh))
+        w.check_cache()
+        att, lse = fq.attention_cached(w.cache, q, *w.args(), hq)
+        seen = before + np.arange(rows) >= border
+        big, _ = ref.held(w.ref, P, w.pages, 0, n, "v")
+        w.check_attention(att, lse, x[:, :hq], below=(seen * n * 2.0 ** -35 * np.abs(big).max())[:, None, None])
+        outs.append((att[:border - before], lse[:, :border - before]))
+    assert 0 < border - before < rows
+    for att, lse in outs[1:]:
+        assert torch.equal(att, outs[0][0]) and torch.equal(lse, outs[0][1])
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
 @pytest.mark.parametrize("dh,rows", [(64, 1), (128, 1), (96, 9), (64, 130), (128, 130)])
 def test_pages_of_the_smallest_scale(dh, rows, fmt):
     """K and V below fmax 2^-127, so that their scale has code 0, and q so that scores are of unit size; every kernel, units cut and whole.
