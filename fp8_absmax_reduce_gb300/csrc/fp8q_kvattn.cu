@@ -344,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
       l[n][0] = l[n][1] = 0.0f;
       xr[n][0] = xr[n][1] = -1000;
     }
+    bool large = false;  // some row's maximum is above kLarge
 
 #pragma unroll 1
     for (int b = b0; b < stop; ++b) {
@@ -408,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
             moved |= x != m[n][e];
           }
         if (__any_sync(0xFFFFFFFFu, moved)) {
+          large = false;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -420,7 +422,20 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
                 o[i][n][e + 2] *= fade;
               }
               m[n][e] = mn[n][e];
+              large |= m[n][e] != -INFINITY && fabsf(m[n][e]) >= kLarge;
             }
+          large = __any_sync(0xFFFFFFFFu, large);
+        }
+        if (large) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {  // the difference, over what it is multiplied by below
+                const float mr = m[n][e & 1] == -INFINITY ? 0.0f : m[n][e & 1];
+                z[k][n][e] = __fsub_rn(__fmul_rn(z[k][n][e], f[k][n][e & 1]), mr) * rcp(f[k][n][e & 1]);
+              }
         }
         // The largest scale of V that each row has seen.  Rows' differ only from the first step on that not all see, and what follows is such a
         // step; there a row may see one of the two groups of 16 keys, or none.
@@ -463,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int dx = max(min((k ? xv1 : xv0) - xr[n][e], 0), -60);
-              const float add = (float)(15 + dx) - (m[n][e] == -INFINITY ? 0.0f : m[n][e]), back = pow2i(-dx);
+              const float add = (float)(15 + dx) - (large || m[n][e] == -INFINITY ? 0.0f : m[n][e]), back = pow2i(-dx);
 #pragma unroll
               for (int i = e; i < 4; i += 2) {
                 w[i] = ex2(__fmaf_rn(z[k][n][i], f[k][n][e], add));
@@ -592,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
         if (col == 0) p.lse[(int64_t)hd * p.kv.T + q.first + tok] = lse2 * kLn2;
       } else {
         *reinterpret_cast<float4*>(p.part_o + ((int64_t)slot * C::R + r) * DH + col) = make_float4(a[0], a[1], a[2], a[3]);
-        if (col == 0) p.part_lse[slot * C::R + r] = lse2;
+        if (col == 0) p.part_sum[slot * C::R + r] = make_float2(M, L * 0x1p-15f);
       }
     }
     if (t == 0 && starts && !whole)
@@ -602,10 +617,11 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
 }
 
 // Block (j, r): row r of the unit that CTA j began and did not end.  Its parts: CTA j's last, then the first of those after it; a warp
-// takes every eighth, eight at a time in flight, and the warps' sums are added in order.
+// takes every eighth, eight at a time in flight, and the warps' sums are added in order.  Most blocks have nothing to do, so what counts is how
+// many an SM holds (16 x 5 rows over 4096: 48 us with five, 54 with three; 24 x 6 rows of heads of 64: 21.5 with six, 22.1 with five).
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 template <int DH, int R>
-__global__ void __launch_bounds__(kJoinThreads) k_kv_join(const AttendArgs p) {
+__global__ void __launch_bounds__(kJoinThreads, DH == 64 ? 6 : 5) k_kv_join(const AttendArgs p) {
   __shared__ float acc_s[kJoinWarps][DH], max_s[kJoinWarps], sum_s[kJoinWarps];
   wait_for_previous();
   const int j = blockIdx.x, r = blockIdx.y, t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -618,19 +634,20 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_join(const AttendArgs p) {
 #pragma unroll
   for (int k = 0; k < DH / 32; ++k) acc[k] = 0.0f;
   for (int i0 = warp; i0 < n; i0 += 8 * kJoinWarps) {
-    float v[8][DH / 32], e[8];
+    float v[8][DH / 32];
+    float2 e[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {  // a part that does not exist is the warp's first, with no weight
       const int i = i0 + q * kJoinWarps, s = slot(i < n ? i : i0);
-      e[q] = p.part_lse[s * R + r];
+      e[q] = p.part_sum[s * R + r];
       const float* src = p.part_o + ((int64_t)s * R + r) * DH + lane;
 #pragma unroll
       for (int k = 0; k < DH / 32; ++k) v[q][k] = src[32 * k];
-      if (i >= n) e[q] = -INFINITY;
+      if (i >= n) e[q] = make_float2(-INFINITY, 0.0f);
     }
     float mn = M;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) mn = fmaxf(mn, e[q]);
+    for (int q = 0; q < 8; ++q) mn = fmaxf(mn, e[q].x);
     const float fade = mn == M ? 1.0f : ex2(M - mn);
     sum *= fade;
 #pragma unroll
@@ -638,10 +655,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv_join(const AttendArgs p) {
     M = mn;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const float w = e[q] == -INFINITY ? 0.0f : ex2(e[q] - M);
+      const float w = e[q].y * (e[q].x == M ? 1.0f : ex2(e[q].x - M));  // (the sum of a part that saw nothing is 0)
       sum += w;
 #pragma unroll
-      for (int k = 0; k < DH / 32; ++k) acc[k] += e[q] == -INFINITY ? 0.0f : w * v[q][k];
+      for (int k = 0; k < DH / 32; ++k) acc[k] += e[q].y == 0.0f ? 0.0f : w * v[q][k];
     }
   }
 #pragma unroll
@@ -685,14 +702,14 @@ Rows rows_of(int64_t T, int n_seqs, int n_heads, int hkv) {
   return pairs <= 8 ? Rows{1, 1} : pairs <= 16 ? Rows{2, 1} : pairs <= 32 ? Rows{2, 2} : pairs < kManyPairs ? Rows{2, 4} : Rows{0, 0};
 }
 struct Pieces {
-  size_t lse, cuts, all;
+  size_t sum, cuts, all;
 };
 Pieces pieces(Rows r, int dh) {
   auto pad = [](size_t n) { return (n + 255) & ~size_t(255); };
   const size_t parts = 2 * (size_t)r.ctas();
   Pieces w;
-  w.lse = pad(parts * r.count() * dh * 4);
-  w.cuts = w.lse + pad(parts * r.count() * 4);
+  w.sum = pad(parts * r.count() * dh * 4);
+  w.cuts = w.sum + pad(parts * r.count() * sizeof(float2));
   w.all = w.cuts + pad(sizeof(Cut) * r.ctas());
   return w;
 }
@@ -733,7 +750,7 @@ cudaError_t launch_kv_attend(const KvArgs& a, const uint16_t* qkv, int n_heads, 
   const Pieces w = pieces(r, a.dh);
   uint8_t* b = static_cast<uint8_t*>(ws);
   AttendArgs p{a, qkv, n_heads, kLog2e / sqrtf((float)a.dh), att, lse, reinterpret_cast<float*>(b),
-               reinterpret_cast<float*>(b + w.lse), reinterpret_cast<Cut*>(b + w.cuts), L.wait_ns};
+               reinterpret_cast<float2*>(b + w.sum), reinterpret_cast<Cut*>(b + w.cuts), L.wait_ns};
   // rows of a unit at most, where the host knows them
   const int64_t pairs = a.row_start ? (int64_t)1 << 20 : (int64_t)a.rows * (n_heads / a.hkv);
   const cudaError_t e = r.many() ? launch_kv_attend_many(p, min(r.ctas(), L.num_sms), L.stream)

@@ -14,6 +14,10 @@ namespace fp8q {
 constexpr int kBlockKeys = 128;
 constexpr int kMaxCtas = 152 * 5;
 constexpr int kNoPage = 0x1000;   // in place of a scale: the keys are not seen
+// A reference maximum (log2) from which on scores are rounded before it is taken from them.  One step, z f + (offset - m), rounds the offset
+// away where m is large (half a unit of 2^-14 below 2^10), and leaves the maximum's own rounding in the exponent: from 2^24 on it
+// would leave fp16's range upwards, or all weights would vanish.
+constexpr float kLarge = 1024.0f;
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
 
 // What CTA j leaves behind when it begins a unit and does not end it.
@@ -34,7 +38,7 @@ struct AttendArgs {
   uint16_t* att;
   float* lse;
   float* part_o;     // [2 per CTA][R][DH]
-  float* part_lse;   // [2 per CTA][R], log2
+  float2* part_sum;  // [2 per CTA][R]: the maximum (log2), and the sum over it; apart, as one would vanish in the other's rounding
   Cut* cuts;         // [CTAs]
   uint64_t wait_ns;  // limit of the waits of the kernel for many rows (0: 2 s)
 };
@@ -42,6 +46,11 @@ struct AttendArgs {
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {  // to a unit in the last place
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 // 2^e, e between -126 and 127 or taken as the nearer of them: where what is below vanishes.

@@ -220,6 +220,25 @@ struct Walk {
   }
 };
 
+// What a row's scores of keys 16 g .. of a block are multiplied by.
+__device__ __forceinline__ float factor_of(float rowf, const BlockScales& sc, int g) {
+  return fminf(fmaxf(rowf * sc.k[g], 0x1p-100f), 0x1p126f);
+}
+// Where scores are large: this thread's row of S becomes the differences from its reference, over what they are multiplied by later.
+__device__ __noinline__ void take_reference(uint32_t tS, const BlockScales& sc, float rowf, float ref) {
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t z[32];
+    tmem_ld32(tS + c * 32, z);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float f = factor_of(rowf, sc, 2 * c + (k >> 4));
+      z[k] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(z[k]), f), ref) * rcp(f));
+    }
+    tmem_st32(tS + c * 32, z);
+  }
+}
+
 template <int FMT, int DH, bool SHORT>
 __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_constant__ AttendArgs p) {
   constexpr int N = DH == 64 ? 64 : 128;  // columns of V's tile and of O: 96 are filled up with zeros
@@ -561,6 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       const int kmin = __reduce_min_sync(0xFFFFFFFFu, limit);
       float m = -INFINITY, l = 0.0f;
       int xr = -1000;
+      bool large = false;  // some row's reference is above kLarge
       if (nx) {
         // q over a power of two of its row, as fp16: a warp reads its 32 rows at once, 16 bytes a lane and row (a thread that read its own
         // row took 15000 cycles for it).  A row that does not exist reads the unit's first.
@@ -601,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
           const BlockScales& sc = misc.scales[kpar];
           const int key0 = (w.b0 + b) * kBlockKeys, none = sc.none;
           const bool edge = key0 + kBlockKeys > kmin || none;
-          auto factor = [&](int g) { return fminf(fmaxf(rowf * sc.k[g], 0x1p-100f), 0x1p126f); };
+          auto factor = [&](int g) { return factor_of(rowf, sc, g); };
           auto hidden = [&](int col) { return key0 + col >= limit || (none >> (col >> 4) & 1); };
           float mx = -INFINITY;
           int xnew = max(xr, sc.vmax);
@@ -646,12 +666,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
             l *= alpha;
             if (up) m = mx;
             xr = xnew;
+            large = __any_sync(0xFFFFFFFFu, m != -INFINITY && fabsf(m) >= kLarge);
           }
           const float ref = m == -INFINITY ? 0.0f : m;
           // 2^(s - m + 11 + dx), dx the exponent of the page's V over xr; the sum takes 2^dx back, so it holds for pages of any V.  Where all
           // rows see the block dx is the block's own and one shift a row; elsewhere a page that the row does not see may be above xr.
           const int shift = max(sc.vmax - xr, kNothing);
-          const float off = kOffset + (float)shift - ref;
+          const float taken = large ? 0.0f : ref, off = kOffset + (float)shift - taken;
+          if (large) take_reference(tS, sc, rowf, ref);
           float sum_b = 0.0f;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -665,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
 #pragma unroll
               for (int g = 0; g < 2; ++g) {
                 const int dx = max(min(sc.v[2 * c + g] - xr, 0), kNothing);
-                add[g] = kOffset + (float)dx - ref;
+                add[g] = kOffset + (float)dx - taken;
                 back[g] = pow2i(-dx);
               }
             }
@@ -779,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       }
       if (real) {
         if (whole) p.lse[(int64_t)hd * p.kv.T + row] = lse2 * kLn2;
-        else p.part_lse[slot * kRows + i] = lse2;
+        else p.part_sum[slot * kRows + i] = make_float2(m, l * 0x1p-11f);
       }
       if (t == 32 * kFirstRowWarp && starts && !whole)
         p.cuts[j] = Cut{w.unit0, w.unit0 + w.cost, total, ctas, w.h, w.q.first, w.n_rows, w.r0};
@@ -816,21 +838,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_kv_join_many(const AttendAr
   }
   // (rows behind the tile's last hold what an earlier call left; they are not written)
   for (int i = 0; i < n; ++i) {
-    float e[kJoinRows], v[kJoinRows][DH / 32];
+    float2 e[kJoinRows];
+    float v[kJoinRows][DH / 32];
 #pragma unroll
     for (int q = 0; q < kJoinRows; ++q) {
-      e[q] = p.part_lse[slot(i) * kRows + r0 + q];
+      e[q] = p.part_sum[slot(i) * kRows + r0 + q];
       const float* src = p.part_o + ((int64_t)slot(i) * kRows + r0 + q) * DH + lane;
 #pragma unroll
       for (int k = 0; k < DH / 32; ++k) v[q][k] = src[32 * k];
     }
 #pragma unroll
     for (int q = 0; q < kJoinRows; ++q) {
-      const float mn = fmaxf(M[q], e[q]);
-      const float fade = mn == M[q] ? 1.0f : ex2(M[q] - mn), wgt = e[q] == -INFINITY ? 0.0f : e[q] == mn ? 1.0f : ex2(e[q] - mn);
+      const float mn = fmaxf(M[q], e[q].x), fade = mn == M[q] ? 1.0f : ex2(M[q] - mn);
+      const float wgt = e[q].y * (e[q].x == mn ? 1.0f : ex2(e[q].x - mn));  // (the sum of a part that saw nothing is 0)
       sum[q] = sum[q] * fade + wgt;
 #pragma unroll
-      for (int k = 0; k < DH / 32; ++k) acc[q][k] = acc[q][k] * fade + (e[q] == -INFINITY ? 0.0f : wgt * v[q][k]);
+      for (int k = 0; k < DH / 32; ++k) acc[q][k] = acc[q][k] * fade + (e[q].y == 0.0f ? 0.0f : wgt * v[q][k]);
       M[q] = mn;
     }
   }

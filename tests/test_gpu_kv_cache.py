@@ -395,6 +395,38 @@ def test_q_of_any_size():
 
 
 @pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("dh,hq,rows", [(64, 8, 1), (128, 7, 1), (96, 12, 1), (128, 5, 6), (64, 4, 130), (128, 3, 140)])
+def test_scores_of_any_size(dh, hq, rows, fmt):
+    """Scores from 2^7 to 2^117, either sign, of which one is largest or many are alike, to the last bit; the others are further below than any
+    weight reaches.  Then only the weights' rounding, the sums' and the output's are left: a score's own error is the same for all that count, but
+    for the window's offset, which may go into a reference below 2^10, rounded to half a unit of 2^-14 there.
+    lse: five roundings of the score (scale, product, sum, ln 2 and its product)."""
+    n = 300
+    for a in (10, 18, 22, 24, 25, 27, 31, 40, 90, 120):
+        w = World(fmt, dh, 32, hq, 1, [n, n - 111], rows=rows, seed=a, wide=False)
+        start = np.concatenate([[0], np.cumsum(w.lens)]).tolist()
+        kv = w.rng.standard_normal((start[-1], 2, 1, dh))
+        kv[:, 0] = 0
+        kv[:, 0, 0, 3] = 0.5
+        for s in range(2):
+            kv[start[s] + 101, 0, 0, 3] = 1.0
+        d = torch.tensor(kv, dtype=torch.float32).cuda()
+        fq.kv_cache_append(w.cache, d.reshape(start[-1], -1), i32(w.pages), i32(w.lens), 0, row_start=i32(start))
+        ref.append(w.ref, fmt, 32, w.pages, w.lens, ref.rows_of(2, start[-1], start), d.double().cpu().numpy())
+        x = np.zeros((w.T, hq + 2, dh))
+        x[:, :hq, 3] = w.rng.choice([-1, 1], (w.T, hq)) * w.rng.integers(128, 256, (w.T, hq)) * 2.0 ** (a - 7)
+        q = torch.tensor(x).to(torch.bfloat16).cuda()
+        att, lse = fq.attention_cached(w.cache, q.reshape(w.T, -1), *w.args(), hq)
+        torch.cuda.synchronize()
+        want, size, wlse, _ = ref.attend(w.ref, 32, w.pages, w.lens, w.rows, x[:, :hq])
+        got, glse = att.double().cpu().numpy().reshape(want.shape), lse.double().cpu().numpy()
+        assert np.isfinite(got).all() and np.isfinite(glse).all(), a
+        off = np.abs(got - want) - (2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -15 + (n + 16) * 2.0 ** -22) * size)
+        assert off.max() <= 0, (a, off.max())
+        assert (np.abs(glse - wlse) <= 5 * 2.0 ** -24 * (1 + 2.0 ** -10) * np.abs(wlse) + (n + 16) * 2.0 ** -22).all(), a
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
 @pytest.mark.parametrize("dh,hq,rows,before", [(128, 2, 4, 45), (64, 4, 8, 60), (96, 8, 8, 1004), (128, 4, 30, 20), (64, 4, 130, 30), (96, 2, 200, 700),
                                                (128, 6, 150, 0), (128, 4, 300, 5000)])
 def test_rows_do_not_depend_on_values_that_they_do_not_see(dh, hq, rows, before, fmt):
