@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
                 o[i][n][e + 2] *= fade;
               }
               m[n][e] = mn[n][e];
-              large |= m[n][e] != -INFINITY && fabsf(m[n][e]) >= kLarge;
+              large |= is_large(m[n][e]);
             }
           large = __any_sync(0xFFFFFFFFu, large);
         }
@@ -432,10 +432,8 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {  // the difference, over what it is multiplied by below
-                const float mr = m[n][e & 1] == -INFINITY ? 0.0f : m[n][e & 1];
-                z[k][n][e] = __fsub_rn(__fmul_rn(z[k][n][e], f[k][n][e & 1]), mr) * rcp(f[k][n][e & 1]);
-              }
+              for (int e = 0; e < 4; ++e)  // the difference, over what it is multiplied by below
+                if (is_large(m[n][e & 1])) z[k][n][e] = __fsub_rn(__fmul_rn(z[k][n][e], f[k][n][e & 1]), m[n][e & 1]) * rcp(f[k][n][e & 1]);
         }
         // The largest scale of V that each row has seen.  Rows' differ only from the first step on that not all see, and what follows is such a
         // step; there a row may see one of the two groups of 16 keys, or none.
@@ -478,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DH, NT, RW>::kCtas) k_kv_atten
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int dx = max(min((k ? xv1 : xv0) - xr[n][e], 0), -60);
-              const float add = (float)(15 + dx) - (large || m[n][e] == -INFINITY ? 0.0f : m[n][e]), back = pow2i(-dx);
+              const float add = (float)(15 + dx) - (fabsf(m[n][e]) >= kLarge ? 0.0f : m[n][e]), back = pow2i(-dx);
 #pragma unroll
               for (int i = e; i < 4; i += 2) {
                 w[i] = ex2(__fmaf_rn(z[k][n][i], f[k][n][e], add));

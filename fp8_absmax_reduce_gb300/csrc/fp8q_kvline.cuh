@@ -18,6 +18,7 @@ constexpr int kNoPage = 0x1000;   // in place of a scale: the keys are not seen
 // away where m is large (half a unit of 2^-14 below 2^10), and leaves the maximum's own rounding in the exponent: from 2^24 on it
 // would leave fp16's range upwards, or all weights would vanish.
 constexpr float kLarge = 1024.0f;
+__device__ __forceinline__ bool is_large(float m) { return fabsf(m) >= kLarge && m != -INFINITY; }
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
 
 // What CTA j leaves behind when it begins a unit and does not end it.

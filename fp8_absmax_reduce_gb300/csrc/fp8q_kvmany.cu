@@ -224,8 +224,8 @@ struct Walk {
 __device__ __forceinline__ float factor_of(float rowf, const BlockScales& sc, int g) {
   return fminf(fmaxf(rowf * sc.k[g], 0x1p-100f), 0x1p126f);
 }
-// Where scores are large: this thread's row of S becomes the differences from its reference, over what they are multiplied by later.
-__device__ __noinline__ void take_reference(uint32_t tS, const BlockScales& sc, float rowf, float ref) {
+// Where a row's scores are large: this thread's row of S becomes the differences from its reference m, over what they are multiplied by later.
+__device__ __noinline__ void take_reference(uint32_t tS, const BlockScales& sc, float rowf, float m) {
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t z[32];
@@ -233,7 +233,7 @@ __device__ __noinline__ void take_reference(uint32_t tS, const BlockScales& sc, 
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
       const float f = factor_of(rowf, sc, 2 * c + (k >> 4));
-      z[k] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(z[k]), f), ref) * rcp(f));
+      if (is_large(m)) z[k] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(z[k]), f), m) * rcp(f));
     }
     tmem_st32(tS + c * 32, z);
   }
@@ -666,14 +666,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
             l *= alpha;
             if (up) m = mx;
             xr = xnew;
-            large = __any_sync(0xFFFFFFFFu, m != -INFINITY && fabsf(m) >= kLarge);
+            large = __any_sync(0xFFFFFFFFu, is_large(m));
           }
-          const float ref = m == -INFINITY ? 0.0f : m;
+          const float ref = fabsf(m) >= kLarge ? 0.0f : m;  // (a large one is taken before; a row that has seen nothing has none)
           // 2^(s - m + 11 + dx), dx the exponent of the page's V over xr; the sum takes 2^dx back, so it holds for pages of any V.  Where all
           // rows see the block dx is the block's own and one shift a row; elsewhere a page that the row does not see may be above xr.
           const int shift = max(sc.vmax - xr, kNothing);
-          const float taken = large ? 0.0f : ref, off = kOffset + (float)shift - taken;
-          if (large) take_reference(tS, sc, rowf, ref);
+          const float off = kOffset + (float)shift - ref;
+          if (large) take_reference(tS, sc, rowf, m);
           float sum_b = 0.0f;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
 #pragma unroll
               for (int g = 0; g < 2; ++g) {
                 const int dx = max(min(sc.v[2 * c + g] - xr, 0), kNothing);
-                add[g] = kOffset + (float)dx - taken;
+                add[g] = kOffset + (float)dx - ref;
                 back[g] = pow2i(-dx);
               }
             }

@@ -456,6 +456,32 @@ def test_rows_do_not_depend_on_values_that_they_do_not_see(dh, hq, rows, before,
 
 
 @pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("dh,hq,rows,before", [(128, 2, 4, 45), (64, 4, 8, 60), (96, 8, 8, 1004), (128, 4, 30, 20), (64, 4, 130, 30), (96, 2, 200, 700),
+                                               (128, 6, 150, 0)])
+def test_rows_keep_their_bits_whatever_keys_they_do_not_see(dh, hq, rows, before, fmt):
+    """K of the pages of the call's later tokens of unit size, 2^20 and 2^60 of it (scores that are taken another way), and not finite, V too."""
+    n, P = before + rows, 16
+    border = -(-(before + rows // 2) // P) * P
+    outs = []
+    for up in (1.0, 2.0 ** 20, 2.0 ** 60, float("nan")):
+        w = World(fmt, dh, P, hq, 2, [n], rows=rows, seed=70 + dh, wide=False)
+        w.fill()
+        q, _ = w.qkv()
+        kv = q.view(rows, hq + 4, dh)[:, hq:]
+        kv[border - before:, :2] *= up
+        if up != up:
+            kv[border - before:] = up
+        fq.kv_cache_append(w.cache, q, *w.args(), hq)
+        att, lse = fq.attention_cached(w.cache, q, *w.args(), hq)
+        outs.append((att[:border - before], lse[:, :border - before]))
+    torch.cuda.synchronize()
+    fq.get_status(clear=True)
+    assert 0 < border - before < rows and torch.isfinite(outs[0][0]).all() and torch.isfinite(outs[0][1]).all()
+    for att, lse in outs[1:]:
+        assert torch.equal(att, outs[0][0]) and torch.equal(lse, outs[0][1])
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
 @pytest.mark.parametrize("dh,rows", [(64, 1), (128, 1), (96, 9), (64, 130), (128, 130)])
 def test_pages_of_the_smallest_scale(dh, rows, fmt):
     """K and V below fmax 2^-127, so that their scale has code 0, and q so that scores are of unit size; every kernel, units cut and whole.
