@@ -32,23 +32,12 @@ __device__ __forceinline__ KvSeq kv_seq(const KvArgs& a, int s) {
   return q;
 }
 
-// The last sequence that starts at or before `row` (with rows never decreasing, the one that owns it); -1 if none does.
-__device__ __forceinline__ int kv_find(const KvArgs& a, int row) {
-  if (!a.row_start) return row / a.rows;
-  int lo = -1, hi = a.n_seqs;  // row_start[lo] <= row < row_start[hi]
-  while (hi - lo > 1) {
-    const int m = (lo + hi) >> 1;
-    if (a.row_start[m] <= row) lo = m;
-    else hi = m;
-  }
-  return lo;
-}
-
-// The same by a whole warp: 32 starts at a time, two steps for 1000 sequences instead of ten.
+// The last sequence that starts at or before `row` (with rows never decreasing, the one that owns it); -1 if none does.  By a whole
+// warp: 32 starts at a time, two steps for 1000 sequences instead of ten.
 __device__ __forceinline__ int kv_find_warp(const KvArgs& a, int row) {
   if (!a.row_start) return row / a.rows;
   const int lane = threadIdx.x & 31;
-  int lo = -1, hi = a.n_seqs;
+  int lo = -1, hi = a.n_seqs;  // row_start[lo] <= row < row_start[hi]
   while (hi - lo > 1) {
     const int step = (hi - lo + 32) / 33, at = lo + (lane + 1) * step;
     const unsigned le = __ballot_sync(0xFFFFFFFFu, at < hi && a.row_start[at < hi ? at : 0] <= row);

@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
       };
       auto read_scale = [&](const uint8_t* scales, int id) { return (int)scales[(int64_t)max(id, 0) * p.kv.hkv + w.h]; };
       // Lanes 0 .. 7 copy block b's codes of K (0) or V (1), a page (or 128 keys) each.  Slots behind the last key come along.
-      auto fetch = [&](int which, int b, int id, unsigned have) {
+      auto fetch = [&](int which, int b, int id) {
         ++fetched[which];
         const bool mine = lane < 8 && lane % step == 0 && id >= 0;
         const uint32_t bytes = (uint32_t)(step * 16 * DH);
@@ -481,10 +481,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_attend_many(const __grid_con
         if (!warp_wait<SHORT>(&code_free[0], par ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
         if (lane == 0) misc.keys[tile & 3] = BlockKeys{min(kBlockKeys, klim - b * kBlockKeys), (int)have, (b + 1) * kBlockKeys > first};
         __syncwarp();
-        fetch(0, b, here, have);
+        fetch(0, b, here);
         // V's too, whose tile was written when P V of the one before it was done: that one's scales have been read
         if (!warp_wait<SHORT>(&code_free[1], par ^ 1u, abort_flag, p.wait_ns)) { ok = false; break; }
-        fetch(1, b, here, have);
+        fetch(1, b, here);
         BlockScales& sc = misc.scales[par];
         if (lane < 8) {
           sc.k[lane] = pow2(here < 0 ? 0 : xk - 127);
