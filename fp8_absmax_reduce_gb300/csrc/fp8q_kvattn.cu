@@ -1,7 +1,7 @@
 // Causal attention of a call's last tokens over the 8-bit key/value cache.
 //
-// The cache is read once and each byte of it meets 16 rows or more (the query heads that share a K/V head, times the call's tokens), 32
-// operations a byte: bound by memory.  Tensor memory's accumulators of 128 rows would stand mostly empty, and their operands
+// The cache is read once, and each byte of it meets the rows of its K/V head: the query heads that share it, times the call's tokens, 1 to 64 of
+// them, two operations each: bound by memory.  Tensor memory's accumulators of 128 rows would stand mostly empty, and their operands
 // would have to go through shared memory a second time as fp16; so the products are warp-level
 // m16n8k16 ones, whose operands are made in registers, and FP8 codes become fp16 (exactly) on the way from shared memory.
 //
@@ -21,11 +21,13 @@
 // Work.  The keys of all (sequence, row tile, K/V head) units form one line of blocks of 128 keys, each unit preceded by what it costs
 // besides; it is cut into equal parts, one a CTA.  A unit that is cut leaves fp32 partial results, which the second kernel joins in order.
 //
-// Measured (both kernels, out of a graph, caches cold): 64 sequences of up to 8192 tokens, 40 + 8 heads of 128, 372 MB of cache: 70 us, 5.3
-// TB/s; 48 of 32768: 221 us, 6.3 TB/s; one of 250007, 28 + 4 heads: 54 us, 4.8 TB/s; 24 of 3000 with 6 rows each, 12 + 12 heads of 64: 21 us.
+// Measured (both kernels, out of a graph; lengths of batches differ, and sizes here are the largest): 64 sequences of up to 8192 tokens, 40 + 8
+// heads of 128, 372 MB of cache: 69 us, 5.4 TB/s; 48 of up to 32768, 1.4 GB: 219 us, 6.4 TB/s; one of 250007, 28 + 4 heads: 54 us, 4.8
+// TB/s; 24 of up to 3000 with up to 6 rows (83 in all), 12 + 12 heads of 64: 21.5 us.  A reference of V's scales for each row costs tiles of
+// more than 8 rows 3 to 5 % (16 of up to 4096 with 5 rows: 45 us with one for a warp, 48 with its own for each).
 // About 3 us go before the first byte of the cache arrives (the line, the pages), 3 to 4 for the second launch, a tenth for CTAs
 // that end before the last.  Inside, with 12 warps an SM (their registers fill it) the
-// issue slots are 43 % taken and shared memory 25 %: what holds the rest is the latency of a warp's own chain of instructions.
+// issue slots are 45 % taken and shared memory 24 %: what holds the rest is the latency of a warp's own chain of instructions.
 #include <atomic>
 
 #include "fp8q_kvline.cuh"
@@ -102,8 +104,8 @@ struct Shape {
 };
 
 // What a unit costs besides its keys, in blocks of keys: its rows, its first page, joining the warps.  (64 sequences of up to 8192 tokens:
-// 70.9, 69.9, 70.9, 70.9 and 71.4 us with 1, 2, 3, 4 and 6; 24 of 3000 with 6 rows: 20.8, 21.3, 21.1, 22.1, 23.1; 64 of 1000: 29.5, 28.2,
-// 27.7, 27.0, 26.9.)
+// 71.4, 69.3, 68.8, 69.5 and 72.3 us with 1, 2, 3, 4 and 6; 24 of up to 3000 with up to 6 rows: 21.2, 21.5, 21.5, 22.2, 23.3; 64 of up to
+// 1000: 27.3, 26.1, 26.2, 25.6, 25.3.)
 constexpr int kUnitCost = 3;
 
 template <int R>
@@ -686,8 +688,10 @@ __global__ void __launch_bounds__(kJoinThreads, DH == 64 ? 6 : 5) k_kv_join(cons
 }
 
 // Rows of a CTA for the (token, head) pairs of a sequence and K/V head: 8 of one warp or 16; above, two or four warps share their keys
-// for 16 rows each; and from kManyPairs on the kernel on tensor memory.  (2 sequences of 8192, 16 of 4096 and 64 of 1000, 40 + 8 heads of
-// 128: 35 pairs 35, 74 and 83 us here and 40, 71, 102 there; 50 pairs 41, 78, 95 and 39, 63, 109; 80 pairs 55, 140, 149 and 38, 70, 100.)
+// for 16 rows each; and from kManyPairs on the kernel on tensor memory.  (2 sequences of up to 8192, 16 of up to 4096 and 64 of up to 1000,
+// 40 + 8 heads of 128: 35 pairs 37, 74 and 84 us here and 51, 70, 98 there; 50 pairs 42, 78, 96 and 51, 63, 100; 80 pairs 54, 139, 149 and
+// 52, 74, 103.)  Pairs are T / n_seqs rows times the heads, as the host does not know more: a batch that mixes a long piece of a prompt with single
+// tokens is better split into two calls.
 constexpr int kManyPairs = 65;
 struct Rows {
   int nt, rw;

@@ -1,6 +1,8 @@
 // Causal attention over the 8-bit key/value cache for many rows a sequence (pieces of prompts): on the 5th-generation tensor
-// cores, bound by the chain of a tile's products and exponentials.  2 x 512 tokens of 40 + 8 heads of 128 over 8192: 183 us with the
-// join, 811 TFLOP/s; the tensor pipe is active for 37 % of it, a block of 128 keys takes 4200 cycles.
+// cores, bound by the chain of a tile's products and exponentials.  Two pieces of 512 tokens of 40 + 8 heads of 128 over 8192 and 6471: 192 us
+// with the join, 771 TFLOP/s; the tensor pipe is active for 35 % of it, a block of 128 keys takes about 4500 cycles, whether the tiles' rows exist or
+// not.  (Below: "2 x 512 over 8192"; other sizes are the largest of a batch, too.  Times of variants that were tried are beside that of the
+// kernel as it then was.)
 //
 // The products are tcgen05 kind::f16 ones, fp16 operands and fp32 accumulators in tensor memory: FP8 codes are fp16 numbers, and q is
 // one over a power of two of its row, so the scores lose nothing.  (FP8 operands would need q and P in several 4-bit parts.)
@@ -18,7 +20,8 @@
 // they were issued in, so S over P waits for the product that reads P (1 to 2 % at head_dim 96 and 128); at head_dim 64 P lies beside O, which
 // has half of its columns to spare, and nothing waits (1 % faster than over S).
 // P's window is that of the few rows' kernel: p 2^11 in fp16, the reference maximum moving when it is exceeded by 2^4, and V's scales
-// relative to the largest that the row has seen so far.  Both are a row's own: what it does not see does not move a bit of it.
+// relative to the largest that the row has seen so far.  Both are a row's own: what it does not see does not move a bit of it.  (One reference for
+// all rows of a unit's part, known before its first block, took 186 us where this takes 189, and scores of any size 191.)
 // The keys of all (sequence, row tile, K/V head) units are cut into equal parts, one a CTA, as there.
 //
 // Every mbarrier wait is bounded; on expiry the CTA records FP8Q_STATUS_TIMEOUT, stops issuing, waits for the products and copies that it
@@ -44,8 +47,8 @@ constexpr int kMisc = kBars + 256;
 constexpr float kOffset = 11.0f, kSlack = 4.0f;
 constexpr int kNothing = -45;      // V's exponent over the reference, at least: nothing is left of 2^(11 + 4 - 45) in fp16
 constexpr int kAll = 0x7FFFFFFF;
-// What a unit costs besides its keys, in blocks: q, the first pages, the results.  (2 x 512 tokens of 40 heads over 8192: 189, 185, 183, 183
-// and 182 us with 3, 5, 7, 10 and 14; 16 x 104 over 4096: 208, 202, 184, 185, 192; 16 x 16: 73, 69, 70, 74, 82.)
+// What a unit costs besides its keys, in blocks: q, the first pages, the results.  (2 x 512 tokens of 40 heads over 8192: 197, 195, 193, 192
+// and 193 us with 3, 5, 7, 10 and 14; 16 x 104 over 4096: 217, 209, 193, 195, 199; 16 x 16: 77, 73, 74, 78, 85.)
 constexpr int kUnitCost = 7;
 
 // A block's scales as the rows need them, 16 keys each: 2^X of K; X of V, and dx, 2^-dx, its exponent over the block's largest.

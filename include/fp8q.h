@@ -591,7 +591,8 @@ FP8Q_API int kv_cache_read(const fp8q_kv_cache* cache, const int32_t* pages, int
  * maximum and to the page's scale of V over the largest that the row sees: 2^-11 of each while their product is above 2^-25 of
  * the largest, and nothing is left of one below 2^-36.  The sum that divides is fp32 of the unrounded ones.  K and V that a row does
  * not see do not change a bit of its results.
- * Slots behind a sequence's last token may hold anything, and so may tokens that a row does not see.  att and lse must
+ * Slots behind a sequence's last token may hold anything, and so may tokens that a row does not see; a V that is not finite makes
+ * its column not finite in the rows that see it.  att and lse must
  * not overlap the inputs.  Deterministic.  A call is two launches; up to 64 (row, query head) pairs of a sequence and K/V
  * head (T / n_seqs rows taken for each) take warp-level products, more take tensor memory.
  * Requirement besides those above: T n_heads < 2^31.  Workspace: attention_cached_workspace_size bytes (0 for sizes outside
