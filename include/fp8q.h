@@ -590,7 +590,7 @@ FP8Q_API int kv_cache_read(const fp8q_kv_cache* cache, const int32_t* pages, int
  * of two of its row: elements below 2^-28 of the row's largest lose bits).  The probabilities multiply V as fp16, relative to the row's
  * maximum and to the page's scale of V over the largest that the row sees: 2^-11 of each while their product is above 2^-25 of
  * the largest, and nothing is left of one below 2^-36.  The sum that divides is fp32 of the unrounded ones.  K and V that a row does
- * not see do not change a bit of its results.
+ * not see do not change a bit of its results, but through the scale of a page that they share with what it sees.
  * Slots behind a sequence's last token may hold anything, and so may tokens that a row does not see; a V that is not finite makes
  * its column not finite in the rows that see it.  att and lse must
  * not overlap the inputs.  Deterministic.  A call is two launches; up to 64 (row, query head) pairs of a sequence and K/V
